@@ -229,7 +229,8 @@ typedef struct {
  * Errors: INVALID_ARG (bad descriptor, null/misaligned kv_dev), CUDA. */
 int leyline_pool_create(const leyline_pool_desc_t* desc, void* kv_dev, leyline_pool_t** out);
 
-/* Wait for the pool's enqueued work and free what the library allocated (never kv_dev). */
+/* Wait for the pool's enqueued work and free what the library allocated (never kv_dev).
+ * Errors: INVALID_ARG (null pool, or batches of it are still alive). */
 int leyline_pool_destroy(leyline_pool_t* pool);
 
 /* Take n pages off the free-page list, for the caller's initial fill or prefill.
@@ -272,10 +273,11 @@ int64_t leyline_free_page_count(const leyline_pool_t* pool);
  *     have been overwritten): the splices since the checkpoint took more pages
  *     than were free at the checkpoint;
  *   - stored rope bands were turned in place since the checkpoint (a re-index
- *     splice of an eager pool, or leyline_materialize), unless flags holds
+ *     splice of an eager pool, or leyline_materialize) or stored rows were written
+ *     again (leyline_batch_plan), unless flags holds
  *     LEYLINE_ROLLBACK_ACCEPT_TURNED: the accounting is then restored but those
- *     bands stay turned (benchmark repeats, where the work and not the values
- *     matters).
+ *     bands stay turned and those rows as written (benchmark repeats, where the
+ *     work and not the values matters).
  * Both refuse a `stream` under graph capture (INVALID_ARG): the ring positions
  * they save and restore are host state at enqueue time.
  * Errors: INVALID_ARG, CUDA. */
@@ -381,6 +383,137 @@ int leyline_materialize_requests(leyline_pool_t* pool, const leyline_block_table
  * at page * block_size + t % block_size, page = table[t / block_size]).  Owned by
  * the pool; NULL for other pools. */
 int32_t* leyline_pending_ptr(leyline_pool_t* pool);
+
+/* ------------------------------------------- new tokens: batches of chunks ----
+ *
+ * Section 2.3 leaves prefill to the caller: the rows of R are written "into new
+ * slots", and the requests go on decoding over the edited cache.  A batch is the
+ * pool's side of such a step.  It takes one chunk of new tokens per request (one
+ * token when a request decodes, more for a prompt, for the rows of an R after its
+ * splice, or for drafted tokens) through every layer of a model:
+ *
+ *     leyline_batch_plan(batch, &bt, chunks, n, stream);       once a step
+ *     for each layer:
+ *         leyline_append(batch, layer, rows, ...);             norm, turn, write rows
+ *         leyline_rotate(batch, &q, &q, ...);                  norm and turn query heads
+ *         leyline_attention(batch, layer, &q_latent, &q, ...); attend through the table
+ *
+ * The tokens of a batch are numbered through its chunks in order: chunk 0's
+ * tokens first.  Token tensors have one entry per token.
+ *
+ * Chunk i covers the rows [start, start + n) of its request.  Rows below the
+ * request's length are written again (the rows of an R just spliced in); rows
+ * from it on extend the request, and the plan takes their pages off the free
+ * list, installs them in the table and advances the length.  The rows of a chunk
+ * hold nothing defined from the plan on until every layer has been appended.
+ * rope_start is the rotary position of the chunk's first token: start, unless
+ * EVICT directives left the request's survivors at other positions.
+ *
+ * CUDA graphs.  leyline_batch_plan runs on the host for the lengths as they stand
+ * and refuses a stream under capture.  leyline_append, leyline_rotate and
+ * leyline_attention can be captured: they read the plan from the batch's device
+ * memory, at addresses that do not change, so a graph of a step's layers can be
+ * replayed after each new plan.  Their token tensors must then have room for the
+ * tokens of every plan the graph is replayed with (at most max_tokens).  The
+ * library does not see replays: order them after the plan and before later work
+ * on the pool (the same stream does), and do not replay two graphs of one batch
+ * at once, since a batch has one workspace. */
+typedef struct leyline_batch leyline_batch_t; /* opaque, owned by the library */
+
+typedef struct {
+    int32_t req;
+    int32_t n;          /* new tokens, >= 0 */
+    int64_t start;      /* row of the first one, 0 <= start <= length of the request */
+    int64_t rope_start; /* rotary position of the first one, >= 0 (normally start) */
+} leyline_chunk_t;
+
+/* bf16 heads [token][head][dim] with the innermost axis contiguous.  Strides are in
+ * elements and multiples of 8, ptr is 16-byte aligned device memory of the pool's GPU. */
+typedef struct {
+    void* ptr;
+    int64_t token_stride;
+    int64_t head_stride;
+} leyline_heads_t;
+
+/* Create a batch for plans of at most max_chunks chunks and max_tokens tokens, for
+ * q_heads query heads (a multiple of rope_heads).  Allocates the plan's device
+ * buffers (8 + 4 * rope_dim bytes per token), pinned staging for plans, and the
+ * attention workspace (partial outputs of row tiles whose rows are split over
+ * several CTAs: some 40 MiB for MLA rows).  Synchronous.  The pool cannot be
+ * destroyed while it has batches.
+ * Errors: INVALID_ARG (null argument, sizes out of range, q_heads not a multiple
+ * of rope_heads, or a pool whose rows leyline_attention does not take: latent_dim
+ * not a multiple of 8 * rope_heads, zero or above 1024, rope_dim above 256), CUDA. */
+int leyline_batch_create(leyline_pool_t* pool, int32_t max_chunks, int32_t max_tokens, int32_t q_heads,
+                         leyline_batch_t** out);
+
+/* Wait for the pool's enqueued work and free the batch. */
+int leyline_batch_destroy(leyline_batch_t* batch);
+
+/* Plan a step: validate the chunks against seq_lens_host, take pages for rows past
+ * a request's length, and enqueue one kernel that installs them (table, seq_lens_dev),
+ * clears the pending counts of the chunks' rows in a LAZY pool and stores the plan
+ * (slots, cos and sin of the rotary positions, split of the attention's work).
+ * seq_lens_host is updated at enqueue time.  Several chunks may name one request:
+ * in the order given each starts at or below the length that the ones before it
+ * leave, and their rows do not overlap.
+ * Writing rows that existed at a leyline_pool_checkpoint counts as changing stored
+ * rows in place: leyline_pool_rollback then asks for LEYLINE_ROLLBACK_ACCEPT_TURNED.
+ * Errors (nothing is enqueued or changed): INVALID_ARG (null argument, a bad chunk
+ * field, more chunks or tokens than the batch holds, overlapping chunks, `stream`
+ * under graph capture), CAPACITY (a length above max_blocks * block_size),
+ * NO_PAGES.  CUDA: a launch failed after validation. */
+int leyline_batch_plan(leyline_batch_t* batch, leyline_block_table_t* bt, const leyline_chunk_t* chunks, int32_t n,
+                       void* stream);
+
+/* Write the batch's rows of one layer through the block table: rows is bf16
+ * [tokens][row] (row as in the pool: latent | rope bands), not yet turned, with
+ * row_stride elements from one token's row to the next (a multiple of 8, at least
+ * the row).  With latent_norm (bf16 [latent_dim]) the latent is x * w /
+ * sqrt(mean(x^2) + eps) of the given one; with key_norm (bf16 [rope_dim]) so is
+ * each rope band, before its turn.  Each band is then turned by its token's rotary
+ * position.  Everything is computed in fp32 and rounded once to bf16 (with
+ * LEYLINE_ROTATE_BF16_NAIVE the turn rounds as a splice's does, after a norm that is
+ * rounded to bf16); without norms the latent is copied bit for bit.  Enqueues one kernel; rows may lie in pinned
+ * host memory.  Every row must be finite for a norm to be.
+ * Errors: INVALID_ARG, CUDA. */
+int leyline_append(leyline_batch_t* batch, int32_t layer, const void* rows, int64_t row_stride,
+                   const void* latent_norm, const void* key_norm, float eps, void* stream);
+
+/* Turn the query bands q [tokens][q_heads][rope_dim] by their tokens' rotary
+ * positions into out (same shape; may be q itself, but may not overlap it
+ * otherwise), each first normed with `norm` (bf16 [rope_dim]) if it is not NULL, as
+ * leyline_append norms keys; same arithmetic.  Enqueues one kernel.
+ * Errors: INVALID_ARG, CUDA. */
+int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyline_heads_t* out, const void* norm,
+                   float eps, void* stream);
+
+/* Attention of the batch's tokens over the rows of their requests, read in place
+ * through the block table (section 3).  Token t, the i-th of its chunk, attends to
+ * the rows [0, start + i] (its own last), or with LEYLINE_ATTENTION_PREFIX to the
+ * rows [0, start) before its chunk (a caller that has the chunk's keys at hand
+ * merges the two by lse).  Per head h, with x_s = scale * <query, key_s>:
+ *     out = sum_s exp(x_s) value_s / sum_s exp(x_s),   lse = ln sum_s exp(x_s).
+ * rope_heads <= 1 (MLA): every head's key is the whole row, its value the latent;
+ * the query of a head is q_latent [tokens][q_heads][latent_dim] beside q_rope
+ * [tokens][q_heads][rope_dim], already turned (leyline_rotate), and out is
+ * [tokens][q_heads][latent_dim].  rope_heads > 1 (GQA/MHA): head h uses key band
+ * and value slice h / (q_heads / rope_heads) of latent_dim / rope_heads values;
+ * q_latent must be NULL and out is [tokens][q_heads][latent_dim / rope_heads].
+ * In a LAZY pool each key band is turned by its row's pending count as
+ * leyline_gather turns it.  lse (fp32 [tokens][q_heads], contiguous) may be NULL.
+ * A token without rows (PREFIX, start 0) gets zeros and lse -inf.  Rows past the last
+ * one that a token of the chunk attends to are not read, whatever they hold; a value
+ * that is not finite in one of the chunk's own rows reaches its earlier tokens too.
+ * Scores and sums are fp32; the weights exp(x - max) are rounded to bf16 for
+ * the product with the values.  Enqueues one kernel, and a second one that joins the
+ * partial results of split row tiles.  Two calls on the same inputs and plan give
+ * the same bits.
+ * Errors: INVALID_ARG, CUDA. */
+#define LEYLINE_ATTENTION_PREFIX 1
+int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads_t* q_latent,
+                      const leyline_heads_t* q_rope, const leyline_heads_t* out, float* lse, float scale,
+                      int32_t flags, void* stream);
 
 /* ----------------------------------------------------------- checking ---- */
 

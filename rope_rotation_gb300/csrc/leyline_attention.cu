@@ -1,0 +1,292 @@
+// leyline_attention.cu -- attention of a batch's tokens over the paged cache (sm_103a): the
+// kernel for any row shape, and the join of split row tiles.
+//
+// Per query row (token, head), with x_s = scale * <q, k_s> over the rows s it attends to:
+//   m = max x_s,  l = sum exp(x_s - m),  out = sum exp(x_s - m) v_s / l,  lse = m + ln l.
+// One pass over the rows keeps m, l and the unscaled output, multiplying l and the output by
+// exp(m_old - m_new) when a tile raises m.
+#include "leyline_batch.h"
+#include "leyline_device.cuh"
+
+namespace leyline {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+// Slot of cache row `row` of a table row; -1 (with the status bit) when its page is bad.
+__device__ __forceinline__ long long row_slot(const int32_t* table_row, const Geometry& g, long long row,
+                                              int32_t* status)
+{
+    const long long blk = row / g.block_size;
+    const int page = table_row[blk];
+    if (page < 0 || page >= g.num_pages) {
+        raise_status(status, ST_BAD_PAGE);
+        return -1;
+    }
+    return (long long)page * g.block_size + (row - blk * g.block_size);
+}
+
+// ------------------------------------------------------------- any row shape --
+// A CTA takes its items' query rows 16 at a time and the cache rows 16 at a time through
+// shared memory; one thread per (query row, cache row) score, the output in shared memory.
+constexpr int kAnyThreads = 256;
+constexpr int kAnyTile = 16;
+
+struct AnyShape {
+    int key_vecs, value_vecs, stage_vecs;  // 16-byte vectors of a key, a value and a staged row
+    int q_pitch, s_pitch;                  // padded pitches (vectors) of the query and cache rows
+    size_t q_off, s_off, o_off, bytes;
+};
+
+__host__ __device__ inline AnyShape any_shape(const Geometry& g)
+{
+    AnyShape s;
+    const bool mla = g.rope_heads <= 1;
+    s.value_vecs = g.latent_vecs / (mla ? 1 : g.rope_heads);
+    s.key_vecs = g.head_vecs + (mla ? g.latent_vecs : 0);
+    s.stage_vecs = s.value_vecs + g.head_vecs;  // [value | key band]; MLA: the whole row is the key
+    s.q_pitch = s.key_vecs + 1;
+    s.s_pitch = s.stage_vecs + 1;
+    s.q_off = 0;
+    s.s_off = s.q_off + (size_t)16 * kAnyTile * s.q_pitch;
+    s.o_off = s.s_off + (size_t)16 * kAnyTile * s.s_pitch;
+    s.bytes = s.o_off + sizeof(float) * kAnyTile * s.value_vecs * 8;
+    return s;
+}
+
+__global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_constant__ AttnArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float p_s[kAnyTile][kAnyTile + 1];
+    __shared__ float m_s[kAnyTile], l_s[kAnyTile], corr_s[kAnyTile];
+    __shared__ long long slot_s[kAnyTile];
+    const Geometry& g = a.g;
+    const AnyShape sh = any_shape(g);
+    uint4* q_s = reinterpret_cast<uint4*>(smem + sh.q_off);
+    uint4* kv_s = reinterpret_cast<uint4*>(smem + sh.s_off);
+    float* o_s = reinterpret_cast<float*>(smem + sh.o_off);
+    const int tid = threadIdx.x;
+    const int qi = tid / kAnyTile, ki = tid % kAnyTile;
+    const bool mla = g.rope_heads <= 1;
+    const int group = a.q_heads / (mla ? 1 : g.rope_heads);
+    const int vdim = sh.value_vecs * 8;
+    const bool bf16 = g.precision == LEYLINE_ROTATE_BF16_NAIVE;
+    const float scale2 = a.scale * kLog2e;
+    wait_for_previous_grid();
+    allow_next_grid();
+    for (int it = a.cta_begin[blockIdx.x]; it < a.cta_begin[blockIdx.x + 1]; ++it) {
+        const AttnItem item = a.items[it];
+        const ChunkDev ch = a.chunks[item.chunk];
+        const int32_t* table_row = a.header->table + (long long)ch.req * a.header->max_blocks;
+        for (int r0 = 0; r0 < item.rows; r0 += kAnyTile) {
+            const int rows = min(kAnyTile, item.rows - r0);
+            __syncthreads();
+            for (int i = tid; i < rows * sh.key_vecs; i += kAnyThreads) {
+                const int r = i / sh.key_vecs, c = i - r * sh.key_vecs;
+                const int row = item.row0 + r0 + r;
+                const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
+                const int lat = sh.key_vecs - g.head_vecs;
+                const HeadsView& v = c < lat ? a.q_latent : a.q_rope;
+                q_s[r * sh.q_pitch + c] =
+                    static_cast<const uint4*>(v.ptr)[(tok * v.token_stride + head * v.head_stride) / 8 +
+                                                     (c < lat ? c : c - lat)];
+            }
+            for (int i = tid; i < kAnyTile * vdim; i += kAnyThreads) o_s[i] = 0.f;
+            if (tid < kAnyTile) {
+                m_s[tid] = -INFINITY;
+                l_s[tid] = 0.f;
+            }
+            const int my_tok = (item.row0 + r0 + min(qi, rows - 1)) / group;
+            const long long my_end = a.prefix ? ch.start : ch.start + my_tok + 1;  // rows [0, my_end)
+            const int last_tok = (item.row0 + r0 + rows - 1) / group;
+            const long long end = min((long long)item.key1, (long long)(a.prefix ? ch.start : ch.start + last_tok + 1));
+            for (long long s0 = item.key0; s0 < end; s0 += kAnyTile) {
+                const int keys = (int)min((long long)kAnyTile, end - s0);
+                __syncthreads();
+                if (tid < kAnyTile) slot_s[tid] = tid < keys ? row_slot(table_row, g, s0 + tid, a.status) : -1;
+                __syncthreads();
+                for (int i = tid; i < kAnyTile * sh.stage_vecs; i += kAnyThreads) {
+                    const int r = i / sh.stage_vecs, c = i - r * sh.stage_vecs;
+                    const long long slot = slot_s[r];
+                    uint4 v = {};
+                    if (slot >= 0)
+                        v = c < sh.value_vecs ? a.kv[lat_off(g, a.layer, slot) + item.band * sh.value_vecs + c]
+                                              : a.kv[band_off(g, a.layer, slot) + item.band * g.head_vecs +
+                                                     (c - sh.value_vecs)];
+                    kv_s[r * sh.s_pitch + c] = v;
+                }
+                __syncthreads();
+                if (a.pending) {  // turn the bands by their rows' pending counts, as a gather does
+                    const int pairs8 = g.head_vecs / 2, half = g.rope_dim / 2;
+                    for (int i = tid; i < kAnyTile * pairs8; i += kAnyThreads) {
+                        const int r = i / pairs8, q = i - r * pairs8;
+                        const int pend = slot_s[r] >= 0 ? a.pending[slot_s[r]] : 0;
+                        if (pend == 0) continue;
+                        float c[8], s[8];
+                        for (int w = 0; w < 8; ++w) pending_trig(pend, a.turn, half, 8 * q + w, bf16, c[w], s[w]);
+                        uint4* band = kv_s + r * sh.s_pitch + sh.value_vecs;
+                        if (g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT) {
+                            if (bf16) rotate_half_split<true>(band[q], band[q + pairs8], c, s);
+                            else rotate_half_split<false>(band[q], band[q + pairs8], c, s);
+                        } else {
+                            if (bf16) {
+                                rotate_interleaved<true>(band[2 * q], c, s);
+                                rotate_interleaved<true>(band[2 * q + 1], c + 4, s + 4);
+                            } else {
+                                rotate_interleaved<false>(band[2 * q], c, s);
+                                rotate_interleaved<false>(band[2 * q + 1], c + 4, s + 4);
+                            }
+                        }
+                    }
+                    __syncthreads();
+                }
+                float x = -INFINITY;
+                if (qi < rows && s0 + ki < my_end && ki < keys && slot_s[ki] >= 0) {
+                    const uint4* qv = q_s + qi * sh.q_pitch;
+                    const uint4* kvv = kv_s + ki * sh.s_pitch + (sh.stage_vecs - sh.key_vecs);
+                    float acc = 0.f;
+                    for (int c = 0; c < sh.key_vecs; ++c) {
+                        const uint4 u = qv[c], w = kvv[c];
+                        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = bf2(uw[e]), h = bf2(ww[e]);
+                            acc = fmaf(f.x, h.x, acc);
+                            acc = fmaf(f.y, h.y, acc);
+                        }
+                    }
+                    x = acc * scale2;
+                }
+                // the 16 lanes of a query row
+                float top = x;
+                for (int m = kAnyTile / 2; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const float m_old = m_s[qi];
+                const float m_new = fmaxf(m_old, top);
+                const float p = x == -INFINITY ? 0.f : exp2f(x - m_new);  // a NaN score stays NaN
+                float sum = p;
+                for (int m = kAnyTile / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                p_s[qi][ki] = p;
+                __syncwarp();
+                if (ki == 0) {
+                    const float corr = m_new == -INFINITY ? 1.f : exp2f(m_old - m_new);
+                    corr_s[qi] = corr;
+                    m_s[qi] = m_new;
+                    l_s[qi] = l_s[qi] * corr + sum;
+                }
+                __syncthreads();
+                const __nv_bfloat16* val = reinterpret_cast<const __nv_bfloat16*>(kv_s);
+                for (int d = tid; d < vdim; d += kAnyThreads) {
+                    float v[kAnyTile];
+#pragma unroll
+                    for (int k = 0; k < kAnyTile; ++k) v[k] = __bfloat162float(val[k * sh.s_pitch * 8 + d]);
+                    for (int r = 0; r < rows; ++r) {
+                        float o = o_s[r * vdim + d] * corr_s[r];
+#pragma unroll
+                        for (int k = 0; k < kAnyTile; ++k) o = fmaf(p_s[r][k], v[k], o);
+                        o_s[r * vdim + d] = o;
+                    }
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < rows * vdim; i += kAnyThreads) {
+                const int r = i / vdim, d = i - r * vdim;
+                const float l = l_s[r];
+                const float o = l > 0.f ? o_s[i] / l : (l == 0.f ? 0.f : l);
+                const int row = item.row0 + r0 + r;
+                if (item.part >= 0) {
+                    a.part_out[((long long)item.part * kAttnRows + r0 + r) * vdim + d] = o;
+                } else {
+                    const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
+                    static_cast<__nv_bfloat16*>(a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + d] =
+                        __float2bfloat16_rn(o);
+                }
+            }
+            if (tid < rows) {
+                const int row = item.row0 + r0 + tid;
+                const float lse = l_s[tid] == 0.f ? -INFINITY : (m_s[tid] + log2f(l_s[tid])) * kLn2;
+                if (item.part >= 0) {
+                    a.part_lse[(long long)item.part * kAttnRows + r0 + tid] = lse;
+                } else if (a.lse) {
+                    const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
+                    a.lse[tok * a.q_heads + head] = lse;
+                }
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------------- join --
+// Partial results k of a row: out = sum w_k out_k / sum w_k with w_k = exp(lse_k - max),
+// lse = max + ln sum w_k.  One CTA per query row; the parts are added in order, so the result
+// does not depend on which CTA finished first.
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a)
+{
+    wait_for_previous_grid();
+    allow_next_grid();
+    const int j = blockIdx.x / kAttnRows, r = blockIdx.x % kAttnRows;
+    if (j >= a.header->n_joins) return;
+    const AttnJoin jn = a.joins[j];
+    if (r >= jn.rows) return;
+    const Geometry& g = a.g;
+    const bool mla = g.rope_heads <= 1;
+    const int group = a.q_heads / (mla ? 1 : g.rope_heads);
+    const int vdim = g.latent_dim / (mla ? 1 : g.rope_heads);
+    const float* lse = a.part_lse + (long long)jn.part0 * kAttnRows + r;
+    float top = -INFINITY;
+    for (int k = 0; k < jn.parts; ++k) top = fmaxf(top, lse[(long long)k * kAttnRows]);
+    const ChunkDev ch = a.chunks[jn.chunk];
+    const int row = jn.row0 + r;
+    const long long tok = ch.tok0 + row / group, head = jn.band * group + row % group;
+    __nv_bfloat16* out =
+        static_cast<__nv_bfloat16*>(a.out.ptr) + tok * a.out.token_stride + head * a.out.head_stride;
+    float total = 0.f;
+    for (int k = 0; k < jn.parts; ++k) {
+        const float x = lse[(long long)k * kAttnRows];
+        if (x != -INFINITY) total += exp2f((x - top) * kLog2e);
+    }
+    const float inv = total > 0.f ? 1.f / total : total;
+    for (int d = threadIdx.x * 4; d < vdim; d += kJoinThreads * 4) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < jn.parts; ++k) {
+            const float x = lse[(long long)k * kAttnRows];
+            if (x == -INFINITY) continue;
+            const float w = exp2f((x - top) * kLog2e) * inv;
+            const float4 v = *reinterpret_cast<const float4*>(
+                a.part_out + ((long long)(jn.part0 + k) * kAttnRows + r) * vdim + d);
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+        uint2 packed = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        *reinterpret_cast<uint2*>(out + d) = packed;
+    }
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[tok * a.q_heads + head] = total > 0.f ? top + log2f(total) * kLn2 : (total == 0.f ? -INFINITY : total);
+}
+
+}  // namespace
+
+int attention_prepare(const Geometry& g)
+{
+    return (int)cudaFuncSetAttribute(attend_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)any_shape(g).bytes);
+}
+
+int launch_attention(const AttnArgs& a, int ctas, void* stream)
+{
+    return (int)launch_dependent_smem(attend_any_kernel, ctas, kAnyThreads, any_shape(a.g).bytes,
+                                      (cudaStream_t)stream, a);
+}
+
+int launch_join(const AttnArgs& a, int joins, void* stream)
+{
+    return (int)launch_dependent(join_kernel, joins * kAttnRows, kJoinThreads, (cudaStream_t)stream, a);
+}
+
+}  // namespace leyline

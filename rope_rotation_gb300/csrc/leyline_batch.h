@@ -1,0 +1,197 @@
+// leyline_batch.h -- batches of new tokens: what the host plan hands to the kernels that
+// append rows (leyline_append.cu) and attend over them (leyline_attention.cu).
+//
+// A plan lives in the batch's own device memory, at addresses that never change, so that
+// captured graphs of a step's layers can be replayed after each new plan.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <utility>
+#include <vector>
+
+#include "leyline_internal.h"
+
+namespace leyline {
+
+constexpr int kAttnRows = 64;  // query rows (token, head) of a row tile
+constexpr int kAttnKeys = 64;  // cache rows of a key tile
+
+// The plan's header, first in the plan's device buffer.
+struct BatchHeader {
+    const int32_t* table;  // block table the plan was made for
+    int32_t max_blocks;
+    int32_t n_tokens;
+    int32_t n_joins;
+    int32_t pad[3];
+};
+
+// One chunk, as attention sees it.
+struct ChunkDev {
+    int32_t req;
+    int32_t n;       // tokens
+    int32_t tok0;    // first token of the batch
+    int32_t pad;
+    int64_t start;   // row of the first token
+};
+
+// One piece of attention work: a tile of up to kAttnRows query rows of one chunk and key
+// band, over the cache rows [key0, key1).  Row r is token r / group, head band * group +
+// r % group of the chunk (group = query heads per key band).  part < 0: the piece is all of
+// the tile's work and writes the result; else it writes partial result `part`.
+struct AttnItem {
+    int32_t chunk;
+    int32_t band;
+    int32_t row0;
+    int32_t rows;
+    int32_t key0;
+    int32_t key1;
+    int32_t part;
+    int32_t pad;
+};
+
+// A row tile whose work was split into pieces part0 .. part0 + parts - 1.
+struct AttnJoin {
+    int32_t chunk;
+    int32_t band;
+    int32_t row0;
+    int32_t rows;
+    int32_t part0;
+    int32_t parts;
+    int32_t pad[2];
+};
+
+// A run of up to kPlanRun tokens of one chunk, as the plan's install kernel sees it.
+constexpr int kPlanRun = 32;
+struct PlanRun {
+    int32_t req;
+    int32_t n;
+    int32_t tok0;
+    int32_t old_blocks;  // blocks the request had before the plan
+    int64_t start;       // row of the run's first token
+    int64_t rope_start;  // its rotary position
+    int64_t pop;         // ring position of the page of block old_blocks
+    int64_t new_len;     // >= 0: the length to store (the request's last run), else -1
+};
+
+// Where the parts of the plan lie in the batch's device buffer (bytes).
+struct BatchLayout {
+    size_t chunks, items, cta_begin, joins, bytes;
+};
+
+// Validated chunks of a plan and the pages they take.
+struct ChunkPlan {
+    std::vector<ChunkDev> chunks;
+    std::vector<PlanRun> runs;
+    std::vector<std::pair<int32_t, int64_t>> new_len;  // (request, length) of extended requests
+    int64_t tokens = 0;
+    int64_t pages = 0;
+    bool rewrites = false;  // rows that existed before are written again
+};
+// Validate a plan's chunks against the table's lengths and lay out their runs; pop_base is the
+// ring position of the first page the plan takes.  Returns LEYLINE_OK or an error code (the
+// message is set); changes nothing but *out.
+int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyline_chunk_t* chunks, int32_t n,
+                 int64_t max_tokens, int64_t free_pages, int64_t pop_base, ChunkPlan* out);
+
+// What the split of the attention's work goes by.
+struct WorkShape {
+    int32_t bands;  // key bands attention works on (1: MLA)
+    int32_t group;  // query heads per band
+    int32_t ctas;
+};
+// Where the split is written: items[row tiles + ctas], cta_begin[ctas + 1], joins[ctas].
+struct Split {
+    AttnItem* items;
+    int32_t* cta_begin;
+    AttnJoin* joins;
+    int32_t n_items = 0;
+    int32_t n_joins = 0;
+    int32_t n_parts = 0;
+};
+void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out);
+
+struct HeadsView {
+    void* ptr;
+    int64_t token_stride;  // in elements
+    int64_t head_stride;
+};
+
+struct InstallArgs {
+    const uint4* staged;   // pinned plan, copied to plan
+    uint4* plan;
+    const PlanRun* runs;   // pinned
+    int64_t plan_vecs;
+    int32_t n_runs;
+    int32_t max_blocks;
+    int32_t* table;
+    int32_t* seq_lens_dev;
+    const int32_t* free_q;
+    int64_t q_cap;
+    int32_t* pending;      // lazy pools, else nullptr
+    const double* theta;   // theta_j, rope_dim / 2 values
+    int64_t* slot;         // [tokens]
+    float2* trig;          // [tokens][rope_dim / 2]
+    int32_t* status;
+    Geometry g;
+};
+
+struct AppendArgs {
+    uint4* kv;
+    const uint4* rows;
+    int64_t row_stride;    // in 16-byte vectors
+    const uint4* latent_norm;
+    const uint4* key_norm;
+    float eps;
+    int32_t layer;
+    const BatchHeader* header;
+    const int64_t* slot;
+    const float2* trig;
+    Geometry g;
+};
+
+struct RotateArgs {
+    HeadsView q, out;
+    const uint4* norm;
+    float eps;
+    int32_t q_heads;
+    const BatchHeader* header;
+    const float2* trig;
+    Geometry g;
+};
+
+struct AttnArgs {
+    const uint4* kv;
+    HeadsView q_latent, q_rope, out;  // q_latent.ptr nullptr for grouped rows
+    float* lse;
+    float scale;
+    int32_t layer;
+    int32_t prefix;        // attend to the rows before the chunk only
+    int32_t q_heads;
+    const BatchHeader* header;
+    const ChunkDev* chunks;
+    const AttnItem* items;
+    const int32_t* cta_begin;  // [CTAs + 1]: each CTA's items
+    const AttnJoin* joins;
+    float* part_out;       // [parts][kAttnRows][value dim]
+    float* part_lse;       // [parts][kAttnRows], natural log
+    const int32_t* pending;
+    const double* turn;    // lazy pools' turn table
+    int32_t* status;
+    Geometry g;
+};
+
+// Widest rows attention takes (leyline_batch_create checks them).
+constexpr int kAttnMaxValue = 1024;
+constexpr int kAttnMaxRope = 256;
+
+int launch_install(const InstallArgs& a, void* stream);
+int launch_append(const AppendArgs& a, int64_t tokens, int sm_count, void* stream);
+int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* stream);
+// `ctas` is the number of CTAs the plan's work was split over.
+int attention_prepare(const Geometry& g);
+int launch_attention(const AttnArgs& a, int ctas, void* stream);
+int launch_join(const AttnArgs& a, int joins, void* stream);
+
+}  // namespace leyline

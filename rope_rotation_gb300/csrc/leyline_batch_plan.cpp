@@ -1,0 +1,185 @@
+// leyline_batch_plan.cpp -- host planning of a batch of new tokens: the chunks' validation, the
+// pages they take, and the split of the attention's work over the CTAs.  Touches no device.
+#include <algorithm>
+#include <climits>
+#include <cstdio>
+
+#include "leyline_batch.h"
+
+namespace leyline {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int bad(const char* msg) { return set_error(LEYLINE_ERR_INVALID_ARG, msg); }
+
+}  // namespace
+
+int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyline_chunk_t* chunks, int32_t n,
+                 int64_t max_tokens, int64_t free_pages, int64_t pop_base, ChunkPlan* out)
+{
+    char msg[192];
+    const int64_t cap = (int64_t)bt.max_blocks * g.block_size;
+    struct Req {
+        int64_t old_len, len, pop, last_run;
+    };
+    std::vector<int32_t> order(n);
+    std::vector<int32_t> req_of;  // requests of the plan, sorted
+    for (int32_t k = 0; k < n; ++k) {
+        const leyline_chunk_t& c = chunks[k];
+        order[k] = k;
+        if (c.req < 0 || c.req >= bt.num_reqs || c.n < 0 || c.start < 0 || c.rope_start < 0 ||
+            c.rope_start > ((int64_t)1 << 40)) {
+            snprintf(msg, sizeof msg, "chunk %d: request, n, start or rope_start out of range", k);
+            return bad(msg);
+        }
+        out->tokens += c.n;
+        if (out->tokens > max_tokens) return bad("more tokens than the batch holds");
+        req_of.push_back(c.req);
+    }
+    std::sort(req_of.begin(), req_of.end());
+    req_of.erase(std::unique(req_of.begin(), req_of.end()), req_of.end());
+    std::vector<Req> reqs(req_of.size());
+    auto find = [&](int32_t req) -> Req& {
+        return reqs[std::lower_bound(req_of.begin(), req_of.end(), req) - req_of.begin()];
+    };
+    for (size_t i = 0; i < reqs.size(); ++i) {
+        const int64_t len = bt.seq_lens_host[req_of[i]];
+        if (len < 0 || len > cap) return bad("seq_lens_host entry outside [0, max_blocks * block_size]");
+        reqs[i] = Req{len, len, -1, -1};
+    }
+    for (int32_t k = 0; k < n; ++k) {
+        const leyline_chunk_t& c = chunks[k];
+        Req& r = find(c.req);
+        if (c.start > r.len) {
+            snprintf(msg, sizeof msg, "chunk %d: start %lld is past the request's length %lld", k, (long long)c.start,
+                     (long long)r.len);
+            return bad(msg);
+        }
+        if (c.start + c.n > cap)
+            return set_error(LEYLINE_ERR_CAPACITY, "a chunk ends past max_blocks * block_size");
+        if (c.start + c.n > INT32_MAX - kAttnKeys) return set_error(LEYLINE_ERR_CAPACITY, "a length above 2^31 - 65");
+        if (c.n > 0 && c.start < r.old_len) out->rewrites = true;
+        r.len = std::max(r.len, c.start + c.n);
+    }
+    // rows of one request's chunks may not overlap
+    std::sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
+        const leyline_chunk_t &a = chunks[x], &c = chunks[y];
+        return a.req != c.req ? a.req < c.req : a.start != c.start ? a.start < c.start : a.n < c.n;
+    });
+    int32_t before = -1;  // the last chunk with rows
+    for (int32_t k : order) {
+        const leyline_chunk_t& c = chunks[k];
+        if (c.n == 0) continue;
+        if (before >= 0 && chunks[before].req == c.req && c.start < chunks[before].start + chunks[before].n) {
+            snprintf(msg, sizeof msg, "chunks %d and %d share rows of request %d", before, k, c.req);
+            return bad(msg);
+        }
+        before = k;
+    }
+    for (size_t i = 0; i < reqs.size(); ++i) {
+        Req& r = reqs[i];
+        r.pop = pop_base + out->pages;
+        out->pages += ceil_div(r.len, g.block_size) - ceil_div(r.old_len, g.block_size);
+        if (r.len != r.old_len) out->new_len.emplace_back(req_of[i], r.len);
+    }
+    if (out->pages > free_pages) return set_error(LEYLINE_ERR_NO_PAGES, "not enough free pages for the chunks' rows");
+    int32_t tok = 0;
+    for (int32_t k = 0; k < n; ++k) {
+        const leyline_chunk_t& c = chunks[k];
+        Req& r = find(c.req);
+        out->chunks.push_back(ChunkDev{c.req, c.n, tok, 0, c.start});
+        for (int32_t t = 0; t < c.n; t += kPlanRun) {
+            r.last_run = (int64_t)out->runs.size();
+            out->runs.push_back(PlanRun{c.req, std::min(kPlanRun, c.n - t), tok + t,
+                                        (int32_t)ceil_div(r.old_len, g.block_size), c.start + t, c.rope_start + t,
+                                        r.pop, -1});
+        }
+        tok += c.n;
+    }
+    for (const Req& r : reqs)
+        if (r.last_run >= 0 && r.len != r.old_len) out->runs[r.last_run].new_len = r.len;
+    return LEYLINE_OK;
+}
+
+// The split of the attention's work over the CTAs.  A row tile costs its key tiles plus a fixed
+// share for its queries and its output; the tiles form one list, which the CTAs take in
+// contiguous runs of equal cost, so a tile may end in one CTA and go on in the next.  A CTA never
+// starts or leaves less than kMinKeyTiles of a tile that has more.  split_by cuts by a given share
+// and returns the last CTA's cost.
+constexpr int64_t kTileCost = 2;
+constexpr int64_t kMinKeyTiles = 2;
+static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks, int64_t quota, Split* out)
+{
+    int64_t used = 0;  // of the current CTA's quota
+    int32_t cta = 0;
+    out->cta_begin[0] = 0;
+    auto next_cta = [&] {
+        if (cta + 1 < w.ctas) {
+            out->cta_begin[++cta] = out->n_items;
+            used = 0;
+        }
+    };
+    for (size_t k = 0; k < chunks.size(); ++k) {
+        const ChunkDev& c = chunks[k];
+        const int64_t rows = (int64_t)c.n * w.group;
+        for (int32_t band = 0; band < w.bands; ++band)
+            for (int64_t r0 = 0; r0 < rows; r0 += kAttnRows) {
+                const int32_t n_rows = (int32_t)std::min<int64_t>(kAttnRows, rows - r0);
+                const int64_t end = c.start + (r0 + n_rows - 1) / w.group + 1;
+                const int64_t tiles = ceil_div(end, kAttnKeys);
+                int64_t done = 0;
+                int32_t first_item = out->n_items;
+                while (done < tiles) {
+                    const bool last_cta = cta + 1 == w.ctas;
+                    const int64_t left = tiles - done;
+                    int64_t take = last_cta ? left : std::min(left, quota - used - kTileCost);
+                    if (take < left && (take < kMinKeyTiles || left - take < kMinKeyTiles)) {
+                        // too little room here, or too little left over: all of it or none
+                        if (used > 0 && take < kMinKeyTiles) {
+                            next_cta();
+                            continue;
+                        }
+                        take = std::min(left, std::max(take, kMinKeyTiles));
+                        if (left - take < kMinKeyTiles) take = left;
+                    }
+                    AttnItem& it = out->items[out->n_items++];
+                    it = AttnItem{(int32_t)k, band, (int32_t)r0, n_rows, (int32_t)(done * kAttnKeys),
+                                  (int32_t)std::min(end, (done + take) * kAttnKeys), -1, 0};
+                    done += take;
+                    used += take + kTileCost;
+                    if (used + kTileCost >= quota) next_cta();
+                }
+                const int32_t parts = out->n_items - first_item;
+                if (parts > 1) {
+                    out->joins[out->n_joins++] =
+                        AttnJoin{(int32_t)k, band, (int32_t)r0, n_rows, out->n_parts, parts, {0, 0}};
+                    for (int32_t i = first_item; i < out->n_items; ++i) out->items[i].part = out->n_parts++;
+                }
+            }
+    }
+    while (cta < w.ctas) out->cta_begin[++cta] = out->n_items;
+    return used;
+}
+
+void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out)
+{
+    int64_t total = 0, pieces = 0;
+    for (const ChunkDev& c : chunks) {
+        const int64_t rows = (int64_t)c.n * w.group;
+        for (int64_t r0 = 0; r0 < rows; r0 += kAttnRows) {
+            const int64_t last = (std::min(r0 + kAttnRows, rows) - 1) / w.group;
+            total += w.bands * ceil_div(c.start + last + 1, kAttnKeys);
+            pieces += w.bands;
+        }
+    }
+    // Cutting tiles adds pieces, and borders leave some of a CTA's share unused: the last CTA takes
+    // what is left, so the share grows until that is no more than a share.
+    const Split empty = *out;
+    int64_t quota = ceil_div(total + kTileCost * pieces, w.ctas) + 1;
+    while (split_by(w, chunks, quota, out) > quota) {
+        *out = empty;
+        quota += std::max<int64_t>(1, quota / 64);
+    }
+}
+
+}  // namespace leyline

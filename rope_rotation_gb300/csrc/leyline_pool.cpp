@@ -43,18 +43,11 @@ constexpr size_t kPlanSlotBytes = 64 << 10;  // pinned plan staging per slot (gr
 // Timing event pairs created when kernel timing is switched on (more are made on demand).
 constexpr size_t kTimingEventsUpFront = 256;
 
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
-    }
-    ~DeviceGuard()
-    {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+}  // namespace
+
+namespace leyline {
 
 int cuda_error(cudaError_t e, const char* what)
 {
@@ -62,8 +55,6 @@ int cuda_error(cudaError_t e, const char* what)
     snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString(e));
     return set_error(LEYLINE_ERR_CUDA, msg);
 }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int wait_pool(leyline_pool_t* p)
 {
@@ -115,10 +106,6 @@ int mark_done(leyline_pool_t* p, cudaStream_t stream)
     p->last_stream = stream;
     return LEYLINE_OK;
 }
-
-}  // namespace
-
-namespace leyline {
 
 int resolve_access(const void* ptr, int device, const char* what, void** alias, bool* is_host)
 {
@@ -285,6 +272,7 @@ int leyline_pool_create(const leyline_pool_desc_t* desc, void* kv_dev, leyline_p
 int leyline_pool_destroy(leyline_pool_t* p)
 {
     if (!p) return set_error(LEYLINE_ERR_INVALID_ARG, "null pool");
+    if (p->batches > 0) return set_error(LEYLINE_ERR_INVALID_ARG, "the pool still has batches: destroy them first");
     DeviceGuard guard(p->device);
     if (p->has_work) cudaEventSynchronize(p->done);
     for (auto& ev : p->tev) {

@@ -1,5 +1,5 @@
 // leyline_pool_state.h -- host-side state of a pool (the opaque leyline_pool_t).
-// Shared by the C ABI translation units (leyline_pool.cpp, leyline_noalloc.cu);
+// Shared by the C ABI translation units (leyline_pool.cpp, leyline_noalloc.cu, leyline_batch.cpp);
 // no kernel reads it.
 #pragma once
 
@@ -21,6 +21,19 @@ struct NvtxRange {
     ~NvtxRange() { nvtxRangePop(); }
     NvtxRange(const NvtxRange&) = delete;
     NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = false;
+    explicit DeviceGuard(int dev)
+    {
+        if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
+    }
+    ~DeviceGuard()
+    {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
 };
 }  // namespace leyline
 
@@ -87,5 +100,19 @@ struct leyline_pool {
     bool has_ckpt = false;
     int64_t ckpt_head = 0;
     int64_t ckpt_tail = 0;
-    bool ckpt_turned = false;  // stored bands were turned in place since the checkpoint
+    bool ckpt_turned = false;  // stored rows were changed in place since the checkpoint
+    int batches = 0;           // live batches (leyline_batch_create)
 };
+
+namespace leyline {
+// Shared by the entry points (leyline_pool.cpp).
+int cuda_error(cudaError_t e, const char* what);
+// Wait for the pool's last enqueued work.
+int wait_pool(leyline_pool* p);
+// Refuse (INVALID_ARG) a stream under graph capture.
+int refuse_capture(cudaStream_t stream, const char* what);
+// Make `stream` wait for the pool's previous work when it came from another stream.
+int order_after_previous(leyline_pool* p, cudaStream_t stream);
+// Record the pool's last enqueued work.
+int mark_done(leyline_pool* p, cudaStream_t stream);
+}  // namespace leyline

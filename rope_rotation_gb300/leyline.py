@@ -83,6 +83,13 @@ class Stats(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+LEYLINE_ATTENTION_PREFIX = 1
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _SIGNATURES = {
     "leyline_pool_create": (ctypes.c_int, [ctypes.POINTER(PoolDesc), _vp, ctypes.POINTER(_vp)]),
@@ -106,6 +113,15 @@ _SIGNATURES = {
     "leyline_materialize_requests": (ctypes.c_int, [_vp, ctypes.POINTER(BlockTable), ctypes.POINTER(ctypes.c_int32),
                                                     ctypes.c_int32, _vp]),
     "leyline_pending_ptr": (ctypes.c_void_p, [_vp]),
+    "leyline_batch_create": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                            ctypes.POINTER(_vp)]),
+    "leyline_batch_destroy": (ctypes.c_int, [_vp]),
+    # the chunks go in as a plain address: the data of a CHUNK_DTYPE array
+    "leyline_batch_plan": (ctypes.c_int, [_vp, ctypes.POINTER(BlockTable), _vp, ctypes.c_int32, _vp]),
+    "leyline_append": (ctypes.c_int, [_vp, ctypes.c_int32, _vp, ctypes.c_int64, _vp, _vp, ctypes.c_float, _vp]),
+    "leyline_rotate": (ctypes.c_int, [_vp, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _vp, ctypes.c_float, _vp]),
+    "leyline_attention": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.POINTER(Heads), ctypes.POINTER(Heads),
+                                         ctypes.POINTER(Heads), _vp, ctypes.c_float, ctypes.c_int32, _vp]),
     "leyline_sync_status": (ctypes.c_int, [_vp]),
     "leyline_kernel_timing_enable": (ctypes.c_int, [_vp, ctypes.c_int32]),
     "leyline_kernel_timing_read": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_double),
@@ -354,6 +370,87 @@ def leyline_materialize_requests(pool, tables: Tables, reqs, stream=None) -> Non
 def leyline_pending_ptr(pool) -> int:
     """Device address of the pending counts (0 when the pool is not lazy)."""
     return load().leyline_pending_ptr(pool) or 0
+
+
+# --------------------------------------------------------------- batches ----
+
+# leyline_chunk_t as a numpy record: a structured array of it is a C array of chunks.
+CHUNK_DTYPE = np.dtype([("req", "<i4"), ("n", "<i4"), ("start", "<i8"), ("rope_start", "<i8")], align=True)
+
+
+def chunk_batch(chunks) -> np.ndarray:
+    """chunks: (req, start, n) or (req, start, n, rope_start) of each chunk (rope_start: start),
+    or a CHUNK_DTYPE array, which is taken as it is."""
+    if isinstance(chunks, np.ndarray) and chunks.dtype == CHUNK_DTYPE:
+        if chunks.ndim != 1 or not chunks.flags.c_contiguous:
+            raise ValueError("chunk arrays must be 1-D and contiguous")
+        return chunks
+    chunks = [tuple(c) for c in chunks]
+    if any(len(c) not in (3, 4) for c in chunks):
+        raise ValueError("a chunk is (req, start, n) or (req, start, n, rope_start)")
+    return np.array([(c[0], c[2], c[1], c[3] if len(c) == 4 else c[1]) for c in chunks], dtype=CHUNK_DTYPE)
+
+
+def leyline_batch_create(pool, max_chunks: int, max_tokens: int, q_heads: int) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    _check(load().leyline_batch_create(pool, max_chunks, max_tokens, q_heads, ctypes.byref(h)))
+    return h
+
+
+def leyline_batch_destroy(batch) -> None:
+    _check(load().leyline_batch_destroy(batch))
+
+
+def leyline_batch_plan(batch, tables: Tables, chunks, stream=None) -> None:
+    """chunks: as chunk_batch() takes them."""
+    a = chunk_batch(chunks)
+    _check(load().leyline_batch_plan(batch, ctypes.byref(tables.bt), a.ctypes.data, a.size, _stream_ptr(stream)))
+
+
+def heads(t, what: str, tokens: int, n_heads: int, dim: int) -> Heads:
+    """A view of a bf16 tensor [>= tokens][n_heads][dim] whose last axis is contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or t.shape[0] < tokens or t.shape[1] != n_heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [>= {tokens}][{n_heads}][{dim}]")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+    if n_heads == 1:  # the stride of an axis of one entry says nothing
+        hs = dim
+    if t.shape[0] == 1:
+        ts = n_heads * hs
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps: float = 1e-6, stream=None) -> None:
+    """rows: bf16 [tokens][row] whose last axis is contiguous, on the pool's GPU or in pinned host
+    memory; latent_norm, key_norm: contiguous bf16 weights or None."""
+    import torch
+    if rows.dtype != torch.bfloat16:
+        raise ValueError(f"rows: dtype {rows.dtype}, expected torch.bfloat16")
+    if rows.dim() != 2 or rows.stride(1) != 1:
+        raise ValueError("rows: expected [tokens][row] with a contiguous last axis")
+    stride = rows.stride(0) if rows.shape[0] > 1 else rows.shape[1]
+    _check(load().leyline_append(batch, layer, rows.data_ptr(), stride,
+                                 None if latent_norm is None else _rows_ptr(latent_norm, "latent_norm"),
+                                 None if key_norm is None else _rows_ptr(key_norm, "key_norm"), eps,
+                                 _stream_ptr(stream)))
+
+
+def leyline_rotate(batch, q: Heads, out: Heads, norm=None, eps: float = 1e-6, stream=None) -> None:
+    """q, out: heads(); norm: contiguous bf16 weights or None."""
+    _check(load().leyline_rotate(batch, ctypes.byref(q), ctypes.byref(out),
+                                 None if norm is None else _rows_ptr(norm, "norm"), eps, _stream_ptr(stream)))
+
+
+def leyline_attention(batch, layer: int, q_latent: Optional[Heads], q_rope: Heads, out: Heads, lse, scale: float,
+                      flags: int = 0, stream=None) -> None:
+    """q_latent (None for rows of several bands), q_rope, out: heads(); lse: contiguous fp32 or None."""
+    _check(load().leyline_attention(batch, layer, None if q_latent is None else ctypes.byref(q_latent),
+                                    ctypes.byref(q_rope), ctypes.byref(out),
+                                    None if lse is None else lse.data_ptr(), scale, flags, _stream_ptr(stream)))
 
 
 def leyline_sync_status(pool) -> None:

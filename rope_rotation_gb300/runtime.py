@@ -9,6 +9,7 @@ nothing itself.
 """
 from __future__ import annotations
 
+import weakref
 from typing import Sequence
 
 import numpy as np
@@ -48,6 +49,7 @@ class PagedCache:
         self.table = torch.full((max_reqs, max_blocks), -1, dtype=torch.int32, device=self.device)
         self.seq_lens_dev = torch.zeros(max_reqs, dtype=torch.int32, device=self.device)
         self.tables = leyline.Tables(self.table, self.seq_lens_dev, np.zeros(max_reqs, dtype=np.int64))
+        self._batches = weakref.WeakSet()
 
     # ------------------------------------------------------------------
     @property
@@ -134,6 +136,12 @@ class PagedCache:
         """materialize several distinct requests in one launch per 64 of them."""
         leyline.leyline_materialize_requests(self.pool, self.tables, reqs, stream)
 
+    def batch(self, max_chunks: int, max_tokens: int, q_heads: int) -> "Batch":
+        """A batch for steps of at most max_tokens new tokens in max_chunks chunks (see Batch)."""
+        b = Batch(self, max_chunks, max_tokens, q_heads)
+        self._batches.add(b)
+        return b
+
     def pending(self):
         """Pending counts [num_pages][block_size] of a lazy pool, as a torch view (None otherwise)."""
         addr = leyline.leyline_pending_ptr(self.pool)
@@ -154,8 +162,100 @@ class PagedCache:
 
     def close(self) -> None:
         if self.pool is not None:
+            for b in list(self._batches):  # a pool outlives its batches
+                b.close()
             leyline.leyline_pool_destroy(self.pool)
             self.pool = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Batch:
+    """New tokens of a step: rows appended to the cache, queries turned, attention over the cache.
+
+    plan() takes one chunk of new tokens per request, once a step; append(), rotate() and
+    attention() then serve each layer, on tensors whose first axis is the plan's tokens, chunk after
+    chunk.  The last three can be captured into a CUDA graph and replayed after each new plan,
+    on tensors with room for max_tokens.
+    """
+
+    def __init__(self, cache: PagedCache, max_chunks: int, max_tokens: int, q_heads: int):
+        self.cache = cache
+        self.max_chunks = max_chunks
+        self.max_tokens = max_tokens
+        self.q_heads = q_heads
+        self.bands = cache.rope_heads
+        self.value_dim = cache.latent_dim // self.bands
+        self.tokens = 0
+        self.handle = None
+        self.handle = leyline.leyline_batch_create(cache.pool, max_chunks, max_tokens, q_heads)
+
+    def plan(self, chunks, stream=None) -> None:
+        """chunks: (req, start, n) or (req, start, n, rope_start) of each: the n tokens at rows
+        [start, start + n) of request req.  Rows past the request's length take pages."""
+        a = leyline.chunk_batch(chunks)
+        leyline.leyline_batch_plan(self.handle, self.cache.tables, a, stream)
+        self.tokens = int(a["n"].sum())
+
+    def _device(self, t, what: str):
+        if t.device != self.cache.kv.device:
+            raise ValueError(f"{what}: on {t.device}, the cache is on {self.cache.kv.device}")
+        return t
+
+    def _weights(self, t, what: str, n: int):
+        if t is not None and tuple(t.shape) != (n,):
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({n},)")
+        return t if t is None else self._device(t, what)
+
+    def _heads(self, t, what: str, dim: int) -> leyline.Heads:
+        return leyline.heads(self._device(t, what), what, self.tokens, self.q_heads, dim)
+
+    def append(self, layer: int, rows, latent_norm=None, key_norm=None, eps: float = 1e-6, stream=None) -> None:
+        """Write rows [tokens][row] of one layer, normed and turned by their positions."""
+        if rows.dim() != 2 or rows.shape[0] < self.tokens or rows.shape[1] != self.cache.row:
+            raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [>= {self.tokens}][{self.cache.row}]")
+        leyline.leyline_append(self.handle, layer, rows,
+                               self._weights(latent_norm, "latent_norm", self.cache.latent_dim),
+                               self._weights(key_norm, "key_norm", self.cache.rope_dim), eps, stream)
+
+    def rotate(self, q, out=None, norm=None, eps: float = 1e-6, stream=None):
+        """Norm and turn query bands [tokens][q_heads][rope_dim] into out (default: a new tensor; q itself is fine)."""
+        if out is None:
+            out = self.cache.torch.empty_like(q)
+        dim = self.cache.rope_dim
+        leyline.leyline_rotate(self.handle, self._heads(q, "q", dim), self._heads(out, "out", dim),
+                               self._weights(norm, "norm", dim), eps, stream)
+        return out
+
+    def attention(self, layer: int, q_latent, q_rope, scale: float, out=None, lse=None, prefix: bool = False,
+                  stream=None):
+        """(out [tokens][q_heads][value], lse [tokens][q_heads]) of the turned queries over the rows up to
+        their own (prefix: the rows before their chunk).  q_latent is None for rows of several bands."""
+        torch = self.cache.torch
+        if out is None:
+            out = torch.empty((q_rope.shape[0], self.q_heads, self.value_dim), dtype=torch.bfloat16,
+                              device=self.cache.kv.device)
+        if lse is None:
+            lse = torch.empty((q_rope.shape[0], self.q_heads), dtype=torch.float32, device=self.cache.kv.device)
+        elif (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < self.tokens
+              or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
+            raise ValueError(f"lse: expected contiguous fp32 [>= {self.tokens}][{self.q_heads}]")
+        if (q_latent is None) != (self.bands > 1):
+            raise ValueError("q_latent goes with rows of one band (MLA), and only with those")
+        leyline.leyline_attention(
+            self.handle, layer, None if q_latent is None else self._heads(q_latent, "q_latent", self.cache.latent_dim),
+            self._heads(q_rope, "q_rope", self.cache.rope_dim), self._heads(out, "out", self.value_dim),
+            self._device(lse, "lse"), scale, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0, stream)
+        return out, lse
+
+    def close(self) -> None:
+        if self.handle is not None:
+            leyline.leyline_batch_destroy(self.handle)
+            self.handle = None
 
     def __del__(self):
         try:
