@@ -436,14 +436,14 @@ typedef struct {
 } leyline_heads_t;
 
 /* Create a batch for plans of at most max_chunks chunks and max_tokens tokens, for
- * q_heads query heads (a multiple of rope_heads).  Allocates the plan's device
+ * q_heads query heads (leyline_attention needs a multiple of rope_heads).  Allocates the plan's device
  * buffers (8 + 4 * rope_dim bytes per token), pinned staging for plans, and the
  * attention workspace (partial outputs of row tiles whose rows are split over
  * several CTAs: some 40 MiB for MLA rows).  Synchronous.  The pool cannot be
  * destroyed while it has batches.
- * Errors: INVALID_ARG (null argument, sizes out of range, q_heads not a multiple
- * of rope_heads, or a pool whose rows leyline_attention does not take: latent_dim
- * not a multiple of 8 * rope_heads, zero or above 1024, rope_dim above 256), CUDA. */
+ * Errors: INVALID_ARG (null argument, sizes out of range, or a pool whose rows
+ * leyline_attention does not take: latent_dim not a multiple of 8 * rope_heads,
+ * zero or above 1024, rope_dim above 256), CUDA. */
 int leyline_batch_create(leyline_pool_t* pool, int32_t max_chunks, int32_t max_tokens, int32_t q_heads,
                          leyline_batch_t** out);
 
@@ -500,8 +500,9 @@ int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyli
  * [tokens][q_heads][latent_dim].  rope_heads > 1 (GQA/MHA): head h uses key band
  * and value slice h / (q_heads / rope_heads) of latent_dim / rope_heads values;
  * q_latent must be NULL and out is [tokens][q_heads][latent_dim / rope_heads].
- * In a LAZY pool each key band is turned by its row's pending count as
- * leyline_gather turns it.  lse (fp32 [tokens][q_heads], contiguous) may be NULL.
+ * In a LAZY pool each key band is turned by its row's pending count, as
+ * leyline_gather turns it but for the rounding: the scores take the turned band
+ * to 2^-17 of its size (LEYLINE_ROTATE_BF16_NAIVE: as gathered).  lse (fp32 [tokens][q_heads], contiguous) may be NULL.
  * A token without rows (PREFIX, start 0) gets zeros and lse -inf.  Rows past the last
  * one that a token of the chunk attends to are not read, whatever they hold; a value
  * that is not finite in one of the chunk's own rows reaches its earlier tokens too.
@@ -519,8 +520,9 @@ int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads
 
 /* Wait for the pool's enqueued work and read its device status word.  Returns
  * LEYLINE_OK, LEYLINE_ERR_DEVICE_CHECK if a kernel met a page id or position
- * outside the pool or table (it then skipped that row; the status is cleared by
- * this call), or LEYLINE_ERR_CUDA. */
+ * outside the pool or table (it then skipped that row, or in attention took it as
+ * zeros) or gave up a wait inside a kernel after a second (its output is then not
+ * valid); the status is cleared by this call.  LEYLINE_ERR_CUDA otherwise. */
 int leyline_sync_status(leyline_pool_t* pool);
 
 /* Kernel timing for benchmarks.  While enabled, each splice records CUDA events

@@ -49,7 +49,8 @@ __host__ __device__ inline AnyShape any_shape(const Geometry& g)
     s.key_vecs = g.head_vecs + (mla ? g.latent_vecs : 0);
     s.stage_vecs = s.value_vecs + g.head_vecs;  // [value | key band]; MLA: the whole row is the key
     s.q_pitch = s.key_vecs + 1;
-    s.s_pitch = s.stage_vecs + 1;
+    // lazy pools: and the low part of the turned band, which bf16 alone would round away
+    s.s_pitch = s.stage_vecs + ((g.flags & LEYLINE_POOL_LAZY) ? g.head_vecs : 0) + 1;
     s.q_off = 0;
     s.s_off = s.q_off + (size_t)16 * kAnyTile * s.q_pitch;
     s.o_off = s.s_off + (size_t)16 * kAnyTile * s.s_pitch;
@@ -119,37 +120,40 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                     kv_s[r * sh.s_pitch + c] = v;
                 }
                 __syncthreads();
-                if (a.pending) {  // turn the bands by their rows' pending counts, as a gather does
-                    const int pairs8 = g.head_vecs / 2, half = g.rope_dim / 2;
-                    for (int i = tid; i < kAnyTile * pairs8; i += kAnyThreads) {
-                        const int r = i / pairs8, q = i - r * pairs8;
+                if (a.pending) {  // turn the bands by their rows' pending counts, into high and low parts
+                    const int half = g.rope_dim / 2;
+                    for (int i = tid; i < kAnyTile * half; i += kAnyThreads) {
+                        const int r = i / half, j = i - r * half;
                         const int pend = slot_s[r] >= 0 ? a.pending[slot_s[r]] : 0;
-                        if (pend == 0) continue;
-                        float c[8], s[8];
-                        for (int w = 0; w < 8; ++w) pending_trig(pend, a.turn, half, 8 * q + w, bf16, c[w], s[w]);
-                        uint4* band = kv_s + r * sh.s_pitch + sh.value_vecs;
-                        if (g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT) {
-                            if (bf16) rotate_half_split<true>(band[q], band[q + pairs8], c, s);
-                            else rotate_half_split<false>(band[q], band[q + pairs8], c, s);
-                        } else {
-                            if (bf16) {
-                                rotate_interleaved<true>(band[2 * q], c, s);
-                                rotate_interleaved<true>(band[2 * q + 1], c + 4, s + 4);
-                            } else {
-                                rotate_interleaved<false>(band[2 * q], c, s);
-                                rotate_interleaved<false>(band[2 * q + 1], c + 4, s + 4);
-                            }
+                        __nv_bfloat16* band = reinterpret_cast<__nv_bfloat16*>(kv_s + r * sh.s_pitch + sh.value_vecs);
+                        __nv_bfloat16* low = band + g.rope_dim;
+                        const bool split = g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
+                        const int e0 = split ? j : 2 * j, e1 = split ? j + half : 2 * j + 1;
+                        const float x0 = __bfloat162float(band[e0]), x1 = __bfloat162float(band[e1]);
+                        float y0 = x0, y1 = x1;
+                        if (pend != 0) {
+                            float c, s;
+                            pending_trig(pend, a.turn, half, j, bf16, c, s);
+                            if (bf16) turn_bf16(x0, x1, c, s, y0, y1);
+                            else turn_fp32(x0, x1, c, s, y0, y1);
                         }
+                        band[e0] = __float2bfloat16_rn(y0);
+                        band[e1] = __float2bfloat16_rn(y1);
+                        // the naive arm's result is the rounded one
+                        low[e0] = __float2bfloat16_rn(bf16 ? 0.f : y0 - __bfloat162float(band[e0]));
+                        low[e1] = __float2bfloat16_rn(bf16 ? 0.f : y1 - __bfloat162float(band[e1]));
                     }
                     __syncthreads();
                 }
                 float x = -INFINITY;
-                if (qi < rows && s0 + ki < my_end && ki < keys && slot_s[ki] >= 0) {
+                if (qi < rows && s0 + ki < my_end && ki < keys) {  // a bad page's row counts as zeros
                     const uint4* qv = q_s + qi * sh.q_pitch;
                     const uint4* kvv = kv_s + ki * sh.s_pitch + (sh.stage_vecs - sh.key_vecs);
                     float acc = 0.f;
-                    for (int c = 0; c < sh.key_vecs; ++c) {
-                        const uint4 u = qv[c], w = kvv[c];
+                    const int low_vecs = a.pending ? g.head_vecs : 0;
+                    for (int c = 0; c < sh.key_vecs + low_vecs; ++c) {
+                        // the query's band meets the low part too
+                        const uint4 u = qv[c < sh.key_vecs ? c : c - g.head_vecs], w = kvv[c];
                         const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -274,12 +278,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 int attention_prepare(const Geometry& g)
 {
+    if (mla_shape(g)) return attention_mla_prepare();
     return (int)cudaFuncSetAttribute(attend_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)any_shape(g).bytes);
 }
 
 int launch_attention(const AttnArgs& a, int ctas, void* stream)
 {
+    if (mla_shape(a.g)) return launch_attention_mla(a, ctas, stream);
     return (int)launch_dependent_smem(attend_any_kernel, ctas, kAnyThreads, any_shape(a.g).bytes,
                                       (cudaStream_t)stream, a);
 }

@@ -169,8 +169,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     const int32_t bands = std::max(g.rope_heads, 1);
     if (max_chunks < 1 || max_chunks > (1 << 16)) return bad("max_chunks must be in [1, 65536]");
     if (max_tokens < 1 || max_tokens > (1 << 22)) return bad("max_tokens must be in [1, 4194304]");
-    if (q_heads < 1 || q_heads > 1024 || q_heads % bands != 0)
-        return bad("q_heads must be in [1, 1024] and a multiple of rope_heads");
+    if (q_heads < 1 || q_heads > 1024) return bad("q_heads must be in [1, 1024]");
     if (g.latent_dim < 8 || g.latent_dim > kAttnMaxValue || g.latent_dim % (8 * bands) != 0)
         return bad("attention needs a latent_dim in [8, 1024], a multiple of 8 * rope_heads");
     if (g.rope_dim > kAttnMaxRope) return bad("attention needs rope_dim <= 256");
@@ -182,7 +181,8 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     b->max_tokens = max_tokens;
     b->q_heads = q_heads;
     b->value_dim = g.latent_dim / bands;
-    b->shape = WorkShape{bands, q_heads / bands, p->sm_count};
+    // a head count that does not go over the key bands does for append and rotate alone
+    b->shape = WorkShape{bands, q_heads % bands == 0 ? q_heads / bands : 0, p->sm_count};
     // every chunk's rows are cut into tiles of their own
     b->max_tiles = (ceil_div((int64_t)max_tokens * b->shape.group, kAttnRows) + max_chunks) * bands;
     if (b->max_tiles > INT32_MAX / 4) {
@@ -413,6 +413,7 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     const bool mla = g.rope_heads <= 1;
     if (layer < 0 || layer >= g.num_layers) return bad("layer out of range");
     if (!b->planned) return bad("the batch has no plan");
+    if (b->shape.group == 0) return bad("attention needs q_heads to be a multiple of rope_heads");
     if ((flags & ~LEYLINE_ATTENTION_PREFIX) != 0) return bad("unknown flags");
     if (!std::isfinite(scale)) return bad("scale must be finite");
     if (!mla && q_latent) return bad("q_latent must be NULL for rows of several bands");

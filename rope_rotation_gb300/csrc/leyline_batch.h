@@ -192,6 +192,9 @@ int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* strea
 // `ctas` is the number of CTAs the plan's work was split over.
 int attention_prepare(const Geometry& g);
 int launch_attention(const AttnArgs& a, int ctas, void* stream);
+// Rows of latent 512 and one 64-wide band (leyline_attention_mla.cu).
+int attention_mla_prepare();
+int launch_attention_mla(const AttnArgs& a, int ctas, void* stream);
 int launch_join(const AttnArgs& a, int joins, void* stream);
 
 }  // namespace leyline

@@ -105,7 +105,8 @@ def attention64(cache, layer, chunks, q_latent, q_rope, scale, prefix=False, pai
     """(out, lse, tol_out, tol_lse) in fp64; the tolerances follow from the arithmetic:
 
     a score's error dx: an fp32 sum of d products is off by at most d * 2^-24 of the sum of their magnitudes
-    (taken twice, for any order inside the matrix unit), a lazily turned key by half a bf16 step of its pair;
+    (taken twice, for any order inside the matrix unit), a lazily turned key by an fp32 error of the turn (2^-20 of its
+    pair) and by what two bf16 values leave of it (2^-17);
     the weights exp(x - m) by dx and 2^-21, and by half a bf16 step in the product with the values; their sum by
     2^-23 for each of n / 64 + 64 additions in a row.  So out is off by
     (HALF + 2 dx + ...) * sum p |v| / l and the final rounding, lse by dx and the sum's error."""
@@ -137,7 +138,7 @@ def attention64(cache, layer, chunks, q_latent, q_rope, scale, prefix=False, pai
                 q = q_rope[t0:t0 + n, h].double()
                 x = q @ k.T
                 mag = q.abs() @ k.abs().T
-                lazy = q.abs() @ pair_norm(k, pair_layout).T * HALF if turned is not None else 0.0
+                lazy = q.abs() @ pair_norm(k, pair_layout).T * (2.0 ** -17 + 2.0 ** -20) if turned is not None else 0.0
                 d = k.shape[1]
                 if G == 1:
                     ql = q_latent[t0:t0 + n, h].double()

@@ -137,8 +137,12 @@ def test_refusals_of_the_calls():
     with pytest.raises(LeylineError):  # pageable host rows
         b.append(0, rows.cpu())
     grouped = BH.make_cache([4], B=16, latent=256, rope=64, bands=4)
+    uneven = grouped.batch(1, 1, 6)  # heads that do not go over the bands: for append and rotate alone
+    uneven.plan([(0, 3, 1)])
+    uneven.append(0, BH.bf16(1, 512))
+    uneven.rotate(BH.bf16(1, 6, 64))
     with pytest.raises(LeylineError):
-        grouped.batch(1, 1, 6)  # not a multiple of the bands
+        uneven.attention(0, None, BH.bf16(1, 6, 64), 1.0)
     gb = grouped.batch(1, 4, 8)
     gb.plan([(0, 0, 4)])
     with pytest.raises(LeylineError):
@@ -366,12 +370,15 @@ def test_attention_interleaved_lazy():
     _attend([900], [(0, 900, 20)], 16, flags=LAZY, pairs=1, B=1)
 
 
-def test_lazy_attention_equals_attention_over_gathered_rows():
-    """A lazy pool's bands are turned on the way as leyline_gather turns them: the same bits as over a pool that
-    holds the gathered rows."""
+@pytest.mark.parametrize("shape", ["mla", "grouped"])
+def test_lazy_naive_pool_attends_to_the_gathered_rows(shape):
+    """With the naive rounding a turned band is a bf16 value: attention over a lazy pool gives the same bits as over
+    an eager pool that holds what leyline_gather returns."""
+    lat, rope, bands = SHAPES[shape]
     lens = [1234, 77]
-    lazy = BH.make_cache(lens, extra=8, B=16, flags=LAZY)
-    eager = BH.make_cache(lens, extra=8, B=16)
+    kw = dict(extra=8, B=16, precision=1, latent=lat, rope=rope, bands=bands)
+    lazy = BH.make_cache(lens, flags=LAZY, **kw)
+    eager = BH.make_cache(lens, **kw)
     for r, n in enumerate(lens):
         flat = torch.from_numpy(lazy.slot_index(r, np.arange(n))).cuda()
         turns = torch.from_numpy(np.random.default_rng(r).integers(-9000, 9000, n // 10 + 1).astype(np.int32)).cuda()
@@ -380,8 +387,8 @@ def test_lazy_attention_equals_attention_over_gathered_rows():
         for layer in range(2):
             eager.write_layer_rows(layer, flat_e, lazy.gather(r, layer, 0, n))
     chunks = [(0, 1234, 3), (1, 77, 1)]
-    ql, q = BH.bf16(4, 16, 512), BH.bf16(4, 16, 64, seed=1)
-    rows = BH.bf16(4, 576, seed=2)
+    ql, q = BH.bf16(4, 16, 512) if bands == 1 else None, BH.bf16(4, 16, rope, seed=1)
+    rows = BH.bf16(4, lazy.row, seed=2)
     got = []
     for cache in (lazy, eager):
         b = cache.batch(2, 4, 16)
