@@ -11,13 +11,20 @@
 //
 // One persistent CTA per SM takes the contiguous run of items the plan gave it.  Roles:
 //   warps 0-3  softmax: S from TMEM, running maximum and sum (fp32), P to shared memory, output
-//   warp 4     one thread issues every MMA
-//   warps 5-8  copy queries and cache rows to shared memory (16-byte cp.async through the block
-//              table), into a ring of 18 column chunks of 64 rows x 64 columns, two tiles' worth,
-//              each with barriers of its own
+//   warp 4     issues the MMAs (one lane)
+//   warp 5     loads cache tiles through the block table (TMA, 8 rows of a page at a time)
+//   warps 6-9  copy the queries (cp.async: any strides), the cache tiles that TMA does not take (block
+//              sizes that 8 does not divide; tiles that end inside, whose other rows are zeroed, since
+//              they meet weights of 0 in the product with V), and in a lazy pool turn the bands
 // In a lazy pool the band of each row is turned by its pending count on the way, in fp32, and goes
-// to shared memory as the sum of two bf16 values (a chunk for each): the scores then carry the turn
-// to 2^-17, not to the 2^-9 of one bf16 rounding, which the other rows do not have either.
+// to shared memory as the sum of two bf16 values: the scores then carry the turn to 2^-17, not to the
+// 2^-9 of one bf16 rounding, which the other rows do not have either.
+//
+// A cache tile in shared memory is 8 groups of 8 rows; a group holds the rows' 64-wide column chunks one
+// after another (latent 0..7, band, lazy pools: the band's low part), 8 rows x 128 bytes each, swizzled.
+// That is what one three-dimensional TMA box of 8 rows writes, and its strides serve both operands:
+// smaller boxes, a chunk of 16 rows at a time, took 100 cycles of issue each, 36 a tile, and bound
+// the kernel.
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
 #include "leyline_batch.h"
@@ -31,25 +38,33 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps;
+constexpr int kLoadWarp = kMmaWarp + 1;
 constexpr int kCopyWarps = 4;
 constexpr int kCopyThreads = 32 * kCopyWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 2 + kCopyWarps);
 
-constexpr int kChunks = 9;                           // 64-wide column chunks of a row: latent 0..7, band 8
 constexpr int kLatentChunks = 8;
-constexpr int kChunkBytes = kAttnKeys * 128;         // 64 rows x 128 bytes
-// The ring: a tile takes its band's chunk (lazy pools: high and low part), then the latent's.  18 is
-// even and so are a lazy tile's 10, and 9 + 9 fill it: the two chunks of a block of O^T (2 x 64 value
-// dimensions) always lie side by side.
-constexpr int kSlots = 18;
-constexpr int kQOff = 0;
-constexpr int kRingOff = kQOff + kChunks * kChunkBytes;
-constexpr int kPOff = kRingOff + kSlots * kChunkBytes;
-constexpr int kMiscOff = kPOff + kChunkBytes;
+constexpr int kAtomBytes = 1024;                     // 8 rows x 128 bytes
+constexpr int kStages = 2;
+constexpr int kSteps = kAttnKeys / 16;               // steps of 16 cache rows, in which PV frees a stage
+
+// Shared memory of a pool kind: query rows of a tile, column chunks of a cache row.
+template <bool kLazy>
+struct Smem {
+    static constexpr int rows = kLazy ? kAttnRowsLazy : kAttnRows;
+    static constexpr int chunks = kLazy ? 10 : 9;
+    static constexpr int group_bytes = chunks * kAtomBytes;
+    static constexpr int stage_bytes = kAttnKeys / 8 * group_bytes;
+    static constexpr int q_chunk_bytes = rows * 128;  // queries: 9 chunks of `rows` rows
+    static constexpr int q = 0;
+    static constexpr int stage = q + 9 * q_chunk_bytes;
+    static constexpr int p = stage + kStages * stage_bytes;
+    static constexpr int misc = p + rows * 128;
+};
 
 struct Misc {
-    unsigned long long full[kSlots];
-    unsigned long long empty[kSlots];
+    unsigned long long full[kStages];
+    unsigned long long empty[kStages][kSteps];
     unsigned long long q_full, q_empty;
     unsigned long long s_full[2];
     unsigned long long p_ready, pv_done, drained;
@@ -58,14 +73,16 @@ struct Misc {
     float factor[kAttnRows];              // rescale, then 1 / l
     float2 trig[kCopyWarps][32];          // lazy pools: cos, sin of the last pending count
 };
-constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;  // and room to align the start
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+template <bool kLazy>
+constexpr int kSmemBytes = Smem<kLazy>::misc + (int)sizeof(Misc) + 1024;  // and room to align the start
+static_assert(kSmemBytes<false> <= 232448 && kSmemBytes<true> <= 232448, "shared memory of a CTA");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;    // 4 blocks of 64 columns
 constexpr uint32_t kTmemS = 256;  // 2 buffers of 64 columns
 
 constexpr float kRaise = 8.f;
+constexpr unsigned long long kDrainTime = 1000000ull;  // 1 ms: longer than any copy in flight takes
 
 // The item as every role sees it.
 struct Work {
@@ -87,33 +104,129 @@ __device__ __forceinline__ Work load_work(const AttnArgs& a, int i)
 
 __device__ __forceinline__ int padded_rows(int rows) { return (rows + 15) & ~15; }
 
+// -------------------------------------------------------------------- loads --
+// The stages in turn, and the parity of their current use.
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ void advance()
+    {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// A cache row's page (as the table has it) and its row in the page; nothing is loaded past `end`.
+struct PageOf {
+    int page, off;
+    bool in;
+};
+
+__device__ __forceinline__ PageOf page_of(const AttnArgs& a, const Work& w, const int32_t* table_row, long long pos)
+{
+    const unsigned blk = (unsigned)pos / (unsigned)a.g.block_size;
+    PageOf p{-1, (int)((unsigned)pos - blk * (unsigned)a.g.block_size), pos < w.end};
+    if (p.in) p.page = table_row[blk];
+    return p;
+}
+
+// Its row in the tensor maps (of all layers' rows); -8 (a box there holds no row of the tensor and loads
+// zeros) past the end and for a bad page.
+__device__ __forceinline__ int map_row(const AttnArgs& a, const PageOf& p)
+{
+    if (p.page >= 0 && p.page < a.g.num_pages)
+        return (int)(((long long)a.layer * a.g.num_pages + p.page) * a.g.block_size + p.off);
+    if (p.in) raise_status(a.status, ST_BAD_PAGE);
+    return -8;
+}
+
+// False (for the whole warp) when the CTA has given up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Misc* m, int32_t* status)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &m->quit, status));
+}
+
+// Whether TMA takes the tile at `key` (of its latents, in a lazy pool).
+__device__ __forceinline__ bool by_box(const MlaMaps& maps, const Work& w, long long key)
+{
+    return maps.boxes && key + kAttnKeys <= w.end;
+}
+
+template <bool kLazy>
+__device__ __forceinline__ void load_tiles(const AttnArgs& a, const MlaMaps& maps, Misc* m, uint32_t smem)
+{
+    using S = Smem<kLazy>;
+    const int lane = threadIdx.x & 31;
+    const bool split = (a.g.flags & LEYLINE_POOL_SPLIT_ROPE) != 0;
+    Ring ring;
+    bool go = true;
+    for (int i = a.cta_begin[blockIdx.x]; go && i < a.cta_begin[blockIdx.x + 1]; ++i) {
+        const Work w = load_work(a, i);
+        const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        PageOf next{};
+        if (w.tiles > 0) next = page_of(a, w, table_row, w.it.key0 + 8 * (lane & 7));
+        for (int t = 0; go && t < w.tiles; ++t) {
+            const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            const bool box = by_box(maps, w, key);
+            const int my_y = box ? map_row(a, next) : 0;
+            if (t + 1 < w.tiles) next = page_of(a, w, table_row, key + kAttnKeys + 8 * (lane & 7));  // in flight meanwhile
+            const uint32_t full = smem_addr(&m->full[ring.stage]);
+            const uint32_t dst = smem + S::stage + ring.stage * S::stage_bytes;
+            if (!box) {  // the copy warps' tile: only this warp's arrival
+                go = warp_wait(smem_addr(&m->empty[ring.stage][kSteps - 1]), ring.phase ^ 1, m, a.status);
+                if (go && lane == 0) mbar_arrive(full);
+                ring.advance();
+                continue;
+            }
+            int y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, my_y, k);
+#pragma unroll
+            for (int step = 0; step < kSteps; ++step) {
+                go = go && warp_wait(smem_addr(&m->empty[ring.stage][step]), ring.phase ^ 1, m, a.status);
+                if (!go) break;
+                if (elect_lane()) {
+                    if (step == 0) mbar_expect_tx(full, 8 * (kLazy ? 8 : 9) * kAtomBytes);
+#pragma unroll
+                    for (int k = 2 * step; k < 2 * step + 2; ++k) {
+                        tma_box3(dst + k * S::group_bytes, &maps.rows, y[k], full);
+                        if (split && !kLazy) tma_box2(dst + k * S::group_bytes + 8 * kAtomBytes, &maps.bands, y[k], full);
+                    }
+                }
+                __syncwarp();
+            }
+            ring.advance();
+        }
+    }
+    if (go) return;  // every load has been waited for by the MMAs
+    // The CTA gives up: what is still in flight must land before it ends.  A stage's barrier may lack the copy
+    // warps' arrivals, so the loads are waited for by time: none takes as long as the limit.
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < kDrainTime) {
+    }
+}
+
 // ------------------------------------------------------------------- copies --
+__device__ __forceinline__ void store(uint32_t at, const uint4& y)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+}
+
+template <bool kLazy>
 struct Copier {
+    using S = Smem<kLazy>;
     const AttnArgs& a;
+    const MlaMaps& maps;
     Misc* m;
     uint32_t smem;
     int tid, v, r0;  // 16-byte chunk of a 128-byte row segment, first row
     int trig_count;  // pending count whose cos / sin this warp's slice holds
     bool trig_valid;
 
-    // False (for the whole warp) when the CTA has given up.
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
-    {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, &m->quit, a.status));
-    }
-
-    // Slots of this thread's rows (r0 + 16 i) of the tile at `key`; -1: not loaded.
-    __device__ __forceinline__ void slots(const Work& w, long long key, int (&page)[4], int (&off)[4])
-    {
-        const int32_t* row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned pos = (unsigned)(key + r0 + 16 * i);
-            const unsigned blk = pos / (unsigned)a.g.block_size;
-            off[i] = (int)(pos - blk * (unsigned)a.g.block_size);
-            page[i] = pos < (unsigned long long)w.end ? row[blk] : -1;
-        }
-    }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, m, a.status); }
 
     // This lane's 8 values of a row's band, turned by the row's pending count, as hi + lo (all 32 lanes; the 8
     // lanes of a row share `pend`).
@@ -170,39 +283,31 @@ struct Copier {
         }
     }
 
-    __device__ __forceinline__ uint32_t place(uint32_t chunk_base, int row) const
+    // This thread's 16 bytes of query row `row` / cache row `row` in a chunk.
+    __device__ __forceinline__ uint32_t q_place(int chunk, int row) const
     {
-        return chunk_base + row * 128 + ((v ^ (row & 7)) << 4);
+        return smem + S::q + chunk * S::q_chunk_bytes + row * 128 + ((v ^ (row & 7)) << 4);
+    }
+    __device__ __forceinline__ uint32_t place(int stage, int chunk, int row) const
+    {
+        return smem + S::stage + stage * S::stage_bytes + (row / 8) * S::group_bytes + chunk * kAtomBytes + (row & 7) * 128 +
+               ((v ^ (row & 7)) << 4);
     }
 
     __device__ __forceinline__ void run()
     {
-        const uint4* kv = a.kv;
         const Geometry& g = a.g;
         const int group = a.q_heads;
-        int slot_at = 0;     // next slot of the ring
-        uint32_t phase = 0;  // of its use
+        Ring ring;
         uint32_t q_phase = 0;
         trig_valid = false;
-        auto next_slot = [&] {
-            if (++slot_at == kSlots) {
-                slot_at = 0;
-                phase ^= 1;
-            }
-        };
-        auto store = [&](int slot, int r, const uint4& y) {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place(smem + kRingOff + slot * kChunkBytes, r)),
-                         "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                         : "memory");
-        };
         for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i) {
             const Work w = load_work(a, i);
             if (w.tiles == 0) continue;
             if (!wait(smem_addr(&m->q_empty), q_phase ^ 1)) return;
             q_phase ^= 1;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int r = r0 + 16 * k;
+            for (int r = r0; r < padded_rows(w.it.rows); r += 16) {
                 const bool on = r < w.it.rows;
                 const int row = w.it.row0 + (on ? r : 0);
                 const long long tok = w.ch.tok0 + row / group, head = row % group;
@@ -211,70 +316,73 @@ struct Copier {
                 const uint4* band =
                     static_cast<const uint4*>(a.q_rope.ptr) + (tok * a.q_rope.token_stride + head * a.q_rope.head_stride) / 8;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    cp_async16(place(smem + kQOff + c * kChunkBytes, r), c < 8 ? lat + 8 * c + v : band + v, on);
+                for (int c = 0; c <= kLatentChunks; ++c)
+                    cp_async16(q_place(c, r), c < kLatentChunks ? lat + 8 * c + v : band + v, on);
             }
             cp_async_arrive(smem_addr(&m->q_full));
-            int page[4], off[4];
-            slots(w, w.it.key0, page, off);
+            const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
             for (int t = 0; t < w.tiles; ++t) {
                 const long long key = w.it.key0 + (long long)t * kAttnKeys;
-                const uint4 *lat[4], *band[4];
-                bool on[4];
-                int pend[4];
+                const bool box = by_box(maps, w, key);
+                const uint32_t full = smem_addr(&m->full[ring.stage]);
+                if (box && !kLazy) {  // the load warp's tile: only these warps' arrivals
+                    if (!wait(smem_addr(&m->empty[ring.stage][kSteps - 1]), ring.phase ^ 1)) return;
+                    if (tid % 32 == 0) mbar_arrive_n(full, 32);
+                    ring.advance();
+                    continue;
+                }
+                long long slot[4];  // of rows r0 + 16 k: < 0, not loaded
+                const uint4* band[4];
+                uint4 hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    on[k] = page[k] >= 0 && page[k] < g.num_pages;
-                    if (!on[k] && key + r0 + 16 * k < w.end) raise_status(a.status, ST_BAD_PAGE);
-                    const long long slot = on[k] ? (long long)page[k] * g.block_size + off[k] : 0;
-                    lat[k] = kv + lat_off(g, a.layer, slot) + v;
-                    band[k] = kv + band_off(g, a.layer, slot) + v;
-                    pend[k] = a.pending && on[k] ? a.pending[slot] : 0;
+                    const int row = map_row(a, page_of(a, w, table_row, key + r0 + 16 * k));
+                    slot[k] = row < 0 ? -1 : row - (long long)a.layer * g.num_pages * g.block_size;
+                    band[k] = a.kv + band_off(g, a.layer, max(slot[k], 0ll)) + v;
                 }
-                if (t + 1 < w.tiles) slots(w, key + kAttnKeys, page, off);  // in flight while this tile is copied
-                // the band first: its slot is free again as soon as S is done
-                if (!wait(smem_addr(&m->empty[slot_at]), phase ^ 1)) return;
-                if (a.pending) {
-                    uint4 hi[4], lo[4];
+                if (kLazy) {
+                    int pend[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) hi[k] = on[k] ? ld_stream(band[k]) : make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 4; ++k) {
+                        pend[k] = slot[k] >= 0 ? a.pending[slot[k]] : 0;
+                        hi[k] = slot[k] >= 0 ? ld_stream(band[k]) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint4 x = hi[k];
                         turned(x, pend[k], hi[k], lo[k]);
-                        store(slot_at, r0 + 16 * k, hi[k]);
                     }
-                    fence_async_smem();
-                    mbar_arrive(smem_addr(&m->full[slot_at]));
-                    next_slot();
-                    if (!wait(smem_addr(&m->empty[slot_at]), phase ^ 1)) return;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) store(slot_at, r0 + 16 * k, lo[k]);
-                    fence_async_smem();
-                    mbar_arrive(smem_addr(&m->full[slot_at]));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        cp_async16(place(smem + kRingOff + slot_at * kChunkBytes, r0 + 16 * k), band[k], on[k]);
-                    cp_async_arrive(smem_addr(&m->full[slot_at]));
                 }
-                next_slot();
-#pragma unroll 2
-                for (int c = 0; c < kLatentChunks; ++c) {
-                    if (!wait(smem_addr(&m->empty[slot_at]), phase ^ 1)) return;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        cp_async16(place(smem + kRingOff + slot_at * kChunkBytes, r0 + 16 * k), lat[k] + 8 * c, on[k]);
-                    cp_async_arrive(smem_addr(&m->full[slot_at]));
-                    next_slot();
+                for (int k = 0; k < 4; ++k) {  // rows r0 + 16 k are freed by PV's step k
+                    const int r = r0 + 16 * k;
+                    if (!wait(smem_addr(&m->empty[ring.stage][k]), ring.phase ^ 1)) return;
+                    if (kLazy) {
+                        store(place(ring.stage, 8, r), hi[k]);
+                        store(place(ring.stage, 9, r), lo[k]);
+                    } else {
+                        cp_async16(place(ring.stage, 8, r), band[k], slot[k] >= 0);
+                    }
+                    if (!box) {
+                        const uint4* lat = a.kv + lat_off(g, a.layer, max(slot[k], 0ll)) + v;
+#pragma unroll
+                        for (int c = 0; c < kLatentChunks; ++c)
+                            cp_async16(place(ring.stage, c, r), lat + 8 * c, slot[k] >= 0);
+                    }
                 }
+                if (kLazy) {
+                    fence_async_smem();
+                    mbar_arrive(full);
+                }
+                cp_async_arrive(full);  // when the copies have landed
+                ring.advance();
             }
         }
     }
 };
 
 // --------------------------------------------------------------------- MMAs --
-// The tiles of the CTA's items in order, as the issuing thread walks them.
+// The tiles of the CTA's items in order, as the issuing warp walks them.
 struct TileCursor {
     int item, end_item;
     int tile, tiles, n;  // n: columns of O^T (query rows, padded)
@@ -309,79 +417,77 @@ struct TileCursor {
     }
 };
 
+template <bool kLazy>
 __device__ __forceinline__ void issue_mmas(const AttnArgs& a, Misc* m, uint32_t smem, uint32_t tmem)
 {
+    using S = Smem<kLazy>;
     constexpr uint32_t kDescS = mma_desc(kAttnRows, kAttnKeys, false, false);
-    const int band_chunks = a.pending ? 2 : 1;
-    const int tile_chunks = band_chunks + kLatentChunks;
+    constexpr uint32_t kStage = S::stage_bytes / 16, kGroup = S::group_bytes / 16, kQChunk = S::q_chunk_bytes / 16;
+    const uint64_t q_mat = smem_matrix(smem + S::q, 16, 1024);
+    const uint64_t k_mat = smem_matrix(smem + S::stage, 16, S::group_bytes);
+    const uint64_t v_mat = smem_matrix(smem + S::stage, kAtomBytes, S::group_bytes);
+    const uint64_t p_mat = smem_matrix(smem + S::p, 16, 1024);
+    // The whole warp walks the tiles, so that what the MMAs are given stays uniform; one lane issues.
+    auto test = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
     TileCursor s, pv;
     s.start(a);
     pv.start(a);
-    int chunk = 0;            // next chunk of S
-    int s_slot = 0, pv_slot = 0;  // first slots of the two cursors' tiles
-    uint32_t s_phase = 0;     // of slot s_slot + chunk
     uint32_t q_phase = 0;
-    unsigned long long t0 = global_ns();
+    uint32_t idle = 0;
+    unsigned long long t0 = 0;
     while (!pv.done()) {
         bool moved = false;
         // S of a tile may run one tile ahead of its product with V: there are two S buffers
-        if (!s.done() && s.index <= pv.index + 1) {
-            const int at = s_slot + chunk < kSlots ? s_slot + chunk : s_slot + chunk - kSlots;
-            bool ready = chunk > 0 || s.tile > 0 || mbar_test(smem_addr(&m->q_full), q_phase);
-            ready = ready && mbar_test(smem_addr(&m->full[at]), s_phase);
-            if (ready) {
-                fence_async_smem();
-                tcgen05_after_sync();
-                const uint32_t k_at = smem + kRingOff + at * kChunkBytes;
-                const uint32_t q_at = smem + kQOff + (chunk < band_chunks ? kLatentChunks : chunk - band_chunks) * kChunkBytes;
-                const uint32_t d = tmem + kTmemS + (s.index & 1) * 64;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(d, smem_matrix(q_at + k * 32, 16, 1024), smem_matrix(k_at + k * 32, 16, 1024), kDescS,
-                             chunk > 0 || k > 0);
-                if (at + 1 == kSlots) s_phase ^= 1;
-                if (++chunk == tile_chunks) {
-                    chunk = 0;
-                    mma_commit(smem_addr(&m->s_full[s.index & 1]));
-                    for (int c = 0; c < band_chunks; ++c) mma_commit(smem_addr(&m->empty[s_slot + c]));
-                    s_slot += tile_chunks;
-                    if (s_slot >= kSlots) s_slot -= kSlots;
-                    if (s.tile == 0) q_phase ^= 1;
-                    if (s.tile + 1 == s.tiles) mma_commit(smem_addr(&m->q_empty));
-                    s.next(a);
-                }
-                moved = true;
-            }
-        }
-        if (pv.index < s.index && mbar_test(smem_addr(&m->p_ready), pv.index & 1)) {
+        if (!s.done() && s.index <= pv.index + 1 && test(smem_addr(&m->full[s.index % kStages]), (s.index / kStages) & 1) &&
+            (s.tile > 0 || test(smem_addr(&m->q_full), q_phase))) {
+            fence_async_smem();
             tcgen05_after_sync();
-            const uint32_t desc = mma_desc(128, pv.n, true, false);
-            for (int b = 0; b < 4; ++b) {
-                int at = pv_slot + band_chunks + 2 * b;
-                if (at >= kSlots) at -= kSlots;
-                const uint32_t v_at = smem + kRingOff + at * kChunkBytes;
+            if (elect_lane()) {
+                const uint32_t d = tmem + kTmemS + (s.index & 1) * 64;
+                const uint64_t k_at = k_mat + (uint64_t)(s.index % kStages * kStage);
 #pragma unroll
-                for (int k = 0; k < kAttnKeys / 16; ++k)
-                    mma_bf16(tmem + kTmemO + b * 64, smem_matrix(v_at + k * 2048, kChunkBytes, 1024),
-                             smem_matrix(smem + kPOff + k * 32, 16, 1024), desc, pv.tile > 0 || k > 0);
-                mma_commit(smem_addr(&m->empty[at]));
-                mma_commit(smem_addr(&m->empty[at + 1]));
+                for (int c = 0; c < S::chunks; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // the band's low part meets the query's band too
+                        mma_bf16(d, q_mat + (uint64_t)(min(c, 8) * kQChunk + 2 * k),
+                                 k_at + (uint64_t)(c * (kAtomBytes / 16) + 2 * k), kDescS, c > 0 || k > 0);
+                mma_commit(smem_addr(&m->s_full[s.index & 1]));
+                if (s.tile + 1 == s.tiles) mma_commit(smem_addr(&m->q_empty));
             }
-            mma_commit(smem_addr(&m->pv_done));
-            pv_slot += tile_chunks;
-            if (pv_slot >= kSlots) pv_slot -= kSlots;
+            __syncwarp();
+            if (s.tile == 0) q_phase ^= 1;
+            s.next(a);
+            moved = true;
+        }
+        if (pv.index < s.index && test(smem_addr(&m->p_ready), pv.index & 1)) {
+            tcgen05_after_sync();
+            if (elect_lane()) {
+                const uint32_t desc = mma_desc(128, pv.n, true, false);
+                const uint64_t v_at = v_mat + (uint64_t)(pv.index % kStages * kStage);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        mma_bf16(tmem + kTmemO + b * 64, v_at + (uint64_t)(2 * k * kGroup + 2 * b * (kAtomBytes / 16)),
+                                 p_mat + 2 * k, desc, pv.tile > 0 || k > 0);
+                    mma_commit(smem_addr(&m->empty[pv.index % kStages][k]));
+                }
+                mma_commit(smem_addr(&m->pv_done));
+            }
+            __syncwarp();
             pv.next(a);
             moved = true;
         }
         if (moved) {
-            t0 = global_ns();
-        } else {
-            if (*(volatile int*)&m->quit) break;
-            if (global_ns() - t0 > kWaitLimit) {
+            idle = 0;
+        } else if ((++idle & 1023) == 0) {  // the clock is read now and then only: reading it is slow
+            if (idle == 1024) t0 = global_ns();
+            const bool late = global_ns() - t0 > kWaitLimit;
+            if (late) {
                 *(volatile int*)&m->quit = 1;
                 raise_status(a.status, ST_TIMEOUT);
-                break;
             }
+            if (__any_sync(0xffffffffu, late || *(volatile int*)&m->quit)) break;
         }
     }
 }
@@ -432,8 +538,10 @@ __device__ __forceinline__ void scale_output(Misc* m, uint32_t tmem_o, int n)
     tmem_wait_st();
 }
 
+template <bool kLazy>
 __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t smem, uint32_t tmem)
 {
+    using S = Smem<kLazy>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t tmem_o = tmem + kTmemO + lanes;
@@ -511,11 +619,13 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
                 scale_output(m, tmem_o, n);
                 softmax_sync();  // before the next rescale's factors
             }
+            if (16 * warp < n) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {  // value k: columns 8 (k / 2) + 2 (lane % 4), + 1 of row[k & 1]
-                const int r = row[k & 1];
-                const uint32_t at = smem + kPOff + r * 128 + (((k / 2) ^ (r & 7)) << 4) + 4 * (lane % 4);
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(p[k]) : "memory");
+                for (int k = 0; k < 16; ++k) {  // value k: columns 8 (k / 2) + 2 (lane % 4), + 1 of row[k & 1]
+                    const int r = row[k & 1];
+                    const uint32_t at = smem + S::p + r * 128 + (((k / 2) ^ (r & 7)) << 4) + 4 * (lane % 4);
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(p[k]) : "memory");
+                }
             }
             fence_async_smem();
             tcgen05_before_sync();
@@ -570,16 +680,19 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) attend_mla_kernel(const __grid_constant__ AttnArgs a)
+template <bool kLazy>
+__global__ void __launch_bounds__(kThreads, 1) attend_mla_kernel(const __grid_constant__ AttnArgs a,
+                                                              const __grid_constant__ MlaMaps maps)
 {
     extern __shared__ unsigned char raw[];
     const uint32_t smem = (smem_addr(raw) + 1023) & ~1023u;
-    Misc* m = reinterpret_cast<Misc*>(raw + (smem - smem_addr(raw)) + kMiscOff);
+    Misc* m = reinterpret_cast<Misc*>(raw + (smem - smem_addr(raw)) + Smem<kLazy>::misc);
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_addr(&m->full[s]), kCopyThreads);
-            mbar_init(smem_addr(&m->empty[s]), 1);
+        for (int s = 0; s < kStages; ++s) {
+            // the load warp and every copy thread (lazy pools: and again for the turned bands)
+            mbar_init(smem_addr(&m->full[s]), 1 + (kLazy ? 2 : 1) * kCopyThreads);
+            for (int k = 0; k < kSteps; ++k) mbar_init(smem_addr(&m->empty[s][k]), 1);
         }
         mbar_init(smem_addr(&m->q_full), kCopyThreads);
         mbar_init(smem_addr(&m->q_empty), 1);
@@ -599,20 +712,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_mla_kernel(const __grid_co
     wait_for_previous_grid();
     allow_next_grid();
     if (warp < kSoftmaxWarps) {
-        run_softmax(a, m, smem, tmem);
+        run_softmax<kLazy>(a, m, smem, tmem);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
-        if ((threadIdx.x & 31) == 0) {
-            issue_mmas(a, m, smem, tmem);
-            // nothing is in flight when TMEM is freed
-            mma_commit(smem_addr(&m->drained));
-            const unsigned long long t0 = global_ns();
-            while (!mbar_try(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
-            }
+        issue_mmas<kLazy>(a, m, smem, tmem);
+        // nothing is in flight when TMEM is freed
+        if (elect_lane()) mma_commit(smem_addr(&m->drained));
+        __syncwarp();
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
         }
+    } else if (warp == kLoadWarp) {
+        load_tiles<kLazy>(a, maps, m, smem);
     } else {
-        const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
-        Copier c{a, m, smem, tid, tid % 8, tid / 8, 0, false};
+        const int tid = threadIdx.x - 32 * (kLoadWarp + 1);
+        Copier<kLazy> c{a, maps, m, smem, tid, tid % 8, tid / 8, 0, false};
         c.run();
         cp_async_wait_all();
     }
@@ -623,16 +737,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_mla_kernel(const __grid_co
     }
 }
 
-}  // namespace
 
-int attention_mla_prepare()
+// The driver's encoder of tensor maps, looked up at run time (the library links no driver library).
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled()
 {
-    return (int)cudaFuncSetAttribute(attend_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
 }
 
-int launch_attention_mla(const AttnArgs& a, int ctas, void* stream)
+// Map of `rows` rows of row_vecs 16-byte vectors at `base`, as planes of 64 columns: boxes of 8 rows of `planes`.
+bool make_map(EncodeTiled encode, CUtensorMap* map, const uint4* base, int64_t rows, int row_vecs, int planes)
 {
-    return (int)launch_dependent_smem(attend_mla_kernel, ctas, kThreads, kSmemBytes, (cudaStream_t)stream, a);
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_vecs * 16, 128};
+    const cuuint32_t box[3] = {64, 8, (cuuint32_t)planes}, steps[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 1 ? 3 : 2, const_cast<uint4*>(base), dims, strides, box,
+                  steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int attention_mla_prepare(const Geometry& g, const void* kv, MlaMaps* maps)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return (int)cudaErrorNotSupported;
+    const uint4* base = static_cast<const uint4*>(kv);
+    // rows of every layer follow one another, in whole rows and in the arrays of a split-rope pool alike
+    const int64_t rows = g.num_pages * g.block_size * g.num_layers;
+    const bool whole = !(g.flags & (LEYLINE_POOL_SPLIT_ROPE | LEYLINE_POOL_LAZY));
+    maps->boxes = g.block_size % 8 == 0 && rows <= INT32_MAX;
+    if (!make_map(encode, &maps->rows, base, rows, g.lat_row_vecs, whole ? 9 : 8) ||
+        !make_map(encode, &maps->bands, base + g.rope_base_vecs, rows, g.rope_row_vecs, 1))
+        return (int)cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attend_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemBytes<false>);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_mla_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<true>);
+    return (int)e;
+}
+
+int launch_attention_mla(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream)
+{
+    return (int)(a.pending ? launch_dependent_smem(attend_mla_kernel<true>, ctas, kThreads, kSmemBytes<true>,
+                                                   (cudaStream_t)stream, a, maps)
+                           : launch_dependent_smem(attend_mla_kernel<false>, ctas, kThreads, kSmemBytes<false>,
+                                                   (cudaStream_t)stream, a, maps));
 }
 
 }  // namespace leyline

@@ -28,6 +28,7 @@ struct leyline_batch {
     WorkShape shape{};
     int64_t max_tiles = 0;
     BatchLayout layout{};
+    MlaMaps maps{};
     size_t stage_bytes = 0;  // plan + runs
     char* d_plan = nullptr;
     int64_t* d_slot = nullptr;
@@ -182,9 +183,10 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     b->q_heads = q_heads;
     b->value_dim = g.latent_dim / bands;
     // a head count that does not go over the key bands does for append and rotate alone
-    b->shape = WorkShape{bands, q_heads % bands == 0 ? q_heads / bands : 0, p->sm_count};
+    b->shape = WorkShape{bands, q_heads % bands == 0 ? q_heads / bands : 0, p->sm_count,
+                         attention_takes_mla(g) && p->d_pending ? kAttnRowsLazy : kAttnRows};
     // every chunk's rows are cut into tiles of their own
-    b->max_tiles = (ceil_div((int64_t)max_tokens * b->shape.group, kAttnRows) + max_chunks) * bands;
+    b->max_tiles = (ceil_div((int64_t)max_tokens * b->shape.group, b->shape.rows) + max_chunks) * bands;
     if (b->max_tiles > INT32_MAX / 4) {
         free_batch(b);
         return bad("max_tokens * q_heads is too large");
@@ -208,7 +210,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
         e = cudaEventCreateWithFlags(&b->installed[i], cudaEventDisableTiming);
         if (e == cudaSuccess) e = cudaHostAlloc((void**)&b->h_stage[i], b->stage_bytes, cudaHostAllocDefault);
     }
-    if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g);
+    if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g, p->kv, &b->maps);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         free_batch(b);
@@ -449,7 +451,7 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     a.turn = p->d_theta_j;
     a.status = p->d_status;
     a.g = g;
-    int err = launch_attention(a, b->shape.ctas, stream);
+    int err = launch_attention(a, b->maps, b->shape.ctas, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the attention kernel");
     // a captured call may be replayed with plans that split more tiles
     const int joins = captured ? b->shape.ctas : b->n_joins;

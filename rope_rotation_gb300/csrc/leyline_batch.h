@@ -5,6 +5,7 @@
 // captured graphs of a step's layers can be replayed after each new plan.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -16,6 +17,8 @@
 namespace leyline {
 
 constexpr int kAttnRows = 64;  // query rows (token, head) of a row tile
+// Lazy pools of MLA rows: 48, since a turned band takes a chunk more of shared memory.
+constexpr int kAttnRowsLazy = 48;
 constexpr int kAttnKeys = 64;  // cache rows of a key tile
 
 // The plan's header, first in the plan's device buffer.
@@ -37,7 +40,7 @@ struct ChunkDev {
 };
 
 // One piece of attention work: a tile of up to kAttnRows query rows of one chunk and key
-// band, over the cache rows [key0, key1).  Row r is token r / group, head band * group +
+// band (WorkShape::rows), over the cache rows [key0, key1).  Row r is token r / group, head band * group +
 // r % group of the chunk (group = query heads per key band).  part < 0: the piece is all of
 // the tile's work and writes the result; else it writes partial result `part`.
 struct AttnItem {
@@ -100,6 +103,7 @@ struct WorkShape {
     int32_t bands;  // key bands attention works on (1: MLA)
     int32_t group;  // query heads per band
     int32_t ctas;
+    int32_t rows;   // query rows of a tile, at most kAttnRows
 };
 // Where the split is written: items[row tiles + ctas], cta_begin[ctas + 1], joins[ctas].
 struct Split {
@@ -186,15 +190,27 @@ struct AttnArgs {
 constexpr int kAttnMaxValue = 1024;
 constexpr int kAttnMaxRope = 256;
 
+// Tensor maps of an MLA pool's rows, all layers', for boxes of 8 rows: whole rows (their latents, in split-rope and
+// lazy pools), and the bands of split-rope pools.
+struct MlaMaps {
+    CUtensorMap rows, bands;
+    int boxes;  // whether pages hold whole boxes
+};
+
 int launch_install(const InstallArgs& a, void* stream);
 int launch_append(const AppendArgs& a, int64_t tokens, int sm_count, void* stream);
 int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* stream);
+// Whether the row shape takes the MLA kernel (latent 512, one 64-wide band).
+inline bool attention_takes_mla(const Geometry& g)
+{
+    return g.latent_vecs == 64 && g.rope_vecs == 8 && g.rope_heads == 1;
+}
+// Fills *maps for MLA rows at kv.
+int attention_prepare(const Geometry& g, const void* kv, MlaMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
-int attention_prepare(const Geometry& g);
-int launch_attention(const AttnArgs& a, int ctas, void* stream);
-// Rows of latent 512 and one 64-wide band (leyline_attention_mla.cu).
-int attention_mla_prepare();
-int launch_attention_mla(const AttnArgs& a, int ctas, void* stream);
+int launch_attention(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream);
+int attention_mla_prepare(const Geometry& g, const void* kv, MlaMaps* maps);  // leyline_attention_mla.cu
+int launch_attention_mla(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream);
 int launch_join(const AttnArgs& a, int joins, void* stream);
 
 }  // namespace leyline

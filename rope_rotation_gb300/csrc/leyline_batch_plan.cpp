@@ -123,8 +123,8 @@ static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks,
         const ChunkDev& c = chunks[k];
         const int64_t rows = (int64_t)c.n * w.group;
         for (int32_t band = 0; band < w.bands; ++band)
-            for (int64_t r0 = 0; r0 < rows; r0 += kAttnRows) {
-                const int32_t n_rows = (int32_t)std::min<int64_t>(kAttnRows, rows - r0);
+            for (int64_t r0 = 0; r0 < rows; r0 += w.rows) {
+                const int32_t n_rows = (int32_t)std::min<int64_t>(w.rows, rows - r0);
                 const int64_t end = c.start + (r0 + n_rows - 1) / w.group + 1;
                 const int64_t tiles = ceil_div(end, kAttnKeys);
                 int64_t done = 0;
@@ -166,8 +166,8 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
     int64_t total = 0, pieces = 0;
     for (const ChunkDev& c : chunks) {
         const int64_t rows = (int64_t)c.n * w.group;
-        for (int64_t r0 = 0; r0 < rows; r0 += kAttnRows) {
-            const int64_t last = (std::min(r0 + kAttnRows, rows) - 1) / w.group;
+        for (int64_t r0 = 0; r0 < rows; r0 += w.rows) {
+            const int64_t last = (std::min(r0 + w.rows, rows) - 1) / w.group;
             total += w.bands * ceil_div(c.start + last + 1, kAttnKeys);
             pieces += w.bands;
         }

@@ -32,6 +32,11 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -62,9 +67,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit, int32_t* status)
 {
     if (mbar_try(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try(bar, parity)) {
+    unsigned long long t0 = 0;
+    for (uint32_t spins = 1; !mbar_try(bar, parity); ++spins) {
+        if (spins % 64 != 0) continue;  // reading the clock is slow
         if (*quit) return false;
+        if (t0 == 0) t0 = global_ns();
         if (global_ns() - t0 > kWaitLimit) {
             *quit = 1;
             raise_status(status, ST_TIMEOUT);
@@ -74,7 +81,32 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // ------------------------------------------------------- asynchronous copies --
+// A box of a two- or three-dimensional tensor map at row y (columns and planes from 0); rows outside the
+// tensor arrive as zeros.
+__device__ __forceinline__ void tma_box2(uint32_t dst, const void* map, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(0), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(0), "r"(y), "r"(0), "r"(bar)
+        : "memory");
+}
+
 // 16 bytes to shared memory; zeros when !valid (nothing is read then).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid)
 {
@@ -162,6 +194,18 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn, bool b_
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)

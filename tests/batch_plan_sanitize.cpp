@@ -143,9 +143,10 @@ int main(int argc, char** argv)
             check((len[r] != lens[r]) == (stored.count(r) != 0) && (!stored.count(r) || stored[r] == len[r]),
                   "stored length");
 
-        WorkShape w{(int32_t)uniform(1, 4), (int32_t)uniform(1, 64), (int32_t)(chance(50) ? 152 : uniform(1, 200))};
+        WorkShape w{(int32_t)uniform(1, 4), (int32_t)uniform(1, 64), (int32_t)(chance(50) ? 152 : uniform(1, 200)),
+                    chance(70) ? kAttnRows : kAttnRowsLazy};
         int64_t tiles = 0, work = 0;
-        for (const ChunkDev& c : plan.chunks) tiles += w.bands * ceil_div((int64_t)c.n * w.group, kAttnRows);
+        for (const ChunkDev& c : plan.chunks) tiles += w.bands * ceil_div((int64_t)c.n * w.group, w.rows);
         // exact sizes, so that the sanitizer sees any entry too many
         std::vector<AttnItem> items((size_t)(tiles + w.ctas));
         std::vector<int32_t> begin(w.ctas + 1);
@@ -166,9 +167,9 @@ int main(int argc, char** argv)
         int32_t at = 0, join = 0, part = 0;
         for (int32_t k = 0; k < n; ++k)
             for (int32_t band = 0; band < w.bands; ++band)
-                for (int64_t r0 = 0; r0 < (int64_t)plan.chunks[k].n * w.group; r0 += kAttnRows) {
+                for (int64_t r0 = 0; r0 < (int64_t)plan.chunks[k].n * w.group; r0 += w.rows) {
                     const int64_t left = (int64_t)plan.chunks[k].n * w.group - r0;
-                    const int32_t n_rows = (int32_t)std::min<int64_t>(kAttnRows, left);
+                    const int32_t n_rows = (int32_t)std::min<int64_t>(w.rows, left);
                     const int64_t end = plan.chunks[k].start + (r0 + n_rows - 1) / w.group + 1;
                     int64_t key = 0;
                     const int32_t first = at;
