@@ -12,7 +12,7 @@
 // One persistent CTA per SM takes the contiguous run of items the plan gave it.  Roles:
 //   warps 0-3  softmax: S from TMEM, running maximum and sum (fp32), P to shared memory, output
 //   warp 4     issues the MMAs (one lane)
-//   warp 5     loads cache tiles through the block table (TMA, 8 rows of a page at a time)
+//   warp 5     loads cache tiles through the block table (TMA, 16 or 8 rows of a page at a time)
 //   warps 6-9  copy the queries (cp.async: any strides), the cache tiles that TMA does not take (block
 //              sizes that 8 does not divide; tiles that end inside, whose other rows are zeroed, since
 //              they meet weights of 0 in the product with V), and in a lazy pool turn the bands
@@ -22,9 +22,9 @@
 //
 // A cache tile in shared memory is 8 groups of 8 rows; a group holds the rows' 64-wide column chunks one
 // after another (latent 0..7, band, lazy pools: the band's low part), 8 rows x 128 bytes each, swizzled.
-// That is what one three-dimensional TMA box of 8 rows writes, and its strides serve both operands:
-// smaller boxes, a chunk of 16 rows at a time, took 100 cycles of issue each, 36 a tile, and bound
-// the kernel.
+// That is what one TMA box of whole rows writes (columns, rows of a group, chunks, groups), and its
+// strides serve both operands.  Smaller boxes, a chunk of 16 rows at a time, took 100 cycles of issue each, 36
+// a tile, and bound the kernel.
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
 #include "leyline_batch.h"
@@ -125,10 +125,12 @@ struct PageOf {
     bool in;
 };
 
-__device__ __forceinline__ PageOf page_of(const AttnArgs& a, const Work& w, const int32_t* table_row, long long pos)
+__device__ __forceinline__ PageOf page_of(const AttnArgs& a, const MlaMaps& maps, const Work& w, const int32_t* table_row,
+                                          long long pos)
 {
-    const unsigned blk = (unsigned)pos / (unsigned)a.g.block_size;
-    PageOf p{-1, (int)((unsigned)pos - blk * (unsigned)a.g.block_size), pos < w.end};
+    const unsigned u = (unsigned)pos, B = (unsigned)a.g.block_size;
+    const unsigned blk = maps.shift >= 0 ? u >> maps.shift : u / B;
+    PageOf p{-1, (int)(u - blk * B), pos < w.end};
     if (p.in) p.page = table_row[blk];
     return p;
 }
@@ -152,7 +154,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Misc* m
 // Whether TMA takes the tile at `key` (of its latents, in a lazy pool).
 __device__ __forceinline__ bool by_box(const MlaMaps& maps, const Work& w, long long key)
 {
-    return maps.boxes && key + kAttnKeys <= w.end;
+    return maps.box > 0 && key + kAttnKeys <= w.end;
 }
 
 template <bool kLazy>
@@ -161,43 +163,65 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, const MlaMaps& map
     using S = Smem<kLazy>;
     const int lane = threadIdx.x & 31;
     const bool split = (a.g.flags & LEYLINE_POOL_SPLIT_ROPE) != 0;
+    const bool wide = maps.box == 16;  // lanes 0..3: the tile's boxes of 16 rows; else lanes 0..7: of 8
+    const int my_row = wide ? 16 * (lane & 3) : 8 * (lane & 7);
     Ring ring;
     bool go = true;
     for (int i = a.cta_begin[blockIdx.x]; go && i < a.cta_begin[blockIdx.x + 1]; ++i) {
         const Work w = load_work(a, i);
         const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        const bool paged = maps.box > 0;
+        // the tile's boxes as indices of groups of 8 rows, found while the tile before is loaded
+        int y[8];
         PageOf next{};
-        if (w.tiles > 0) next = page_of(a, w, table_row, w.it.key0 + 8 * (lane & 7));
+        auto resolve = [&] {
+            const int mine = map_row(a, next) >> 3;  // a box that is not loaded: -1, or -2 where it has two groups
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, mine < 0 && wide ? -2 : mine, k);
+        };
+        if (paged && by_box(maps, w, w.it.key0)) {
+            next = page_of(a, maps, w, table_row, w.it.key0 + my_row);
+            resolve();
+        }
         for (int t = 0; go && t < w.tiles; ++t) {
             const long long key = w.it.key0 + (long long)t * kAttnKeys;
-            const bool box = by_box(maps, w, key);
-            const int my_y = box ? map_row(a, next) : 0;
-            if (t + 1 < w.tiles) next = page_of(a, w, table_row, key + kAttnKeys + 8 * (lane & 7));  // in flight meanwhile
             const uint32_t full = smem_addr(&m->full[ring.stage]);
             const uint32_t dst = smem + S::stage + ring.stage * S::stage_bytes;
-            if (!box) {  // the copy warps' tile: only this warp's arrival
+            const bool more = paged && t + 1 < w.tiles && by_box(maps, w, key + kAttnKeys);
+            if (more) next = page_of(a, maps, w, table_row, key + kAttnKeys + my_row);  // in flight meanwhile
+            if (!by_box(maps, w, key)) {  // the copy warps' tile: only this warp's arrival
                 go = warp_wait(smem_addr(&m->empty[ring.stage][kSteps - 1]), ring.phase ^ 1, m, a.status);
                 if (go && lane == 0) mbar_arrive(full);
                 ring.advance();
                 continue;
             }
-            int y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, my_y, k);
 #pragma unroll
             for (int step = 0; step < kSteps; ++step) {
                 go = go && warp_wait(smem_addr(&m->empty[ring.stage][step]), ring.phase ^ 1, m, a.status);
                 if (!go) break;
                 if (elect_lane()) {
                     if (step == 0) mbar_expect_tx(full, 8 * (kLazy ? 8 : 9) * kAtomBytes);
-#pragma unroll
-                    for (int k = 2 * step; k < 2 * step + 2; ++k) {
-                        tma_box3(dst + k * S::group_bytes, &maps.rows, y[k], full);
-                        if (split && !kLazy) tma_box2(dst + k * S::group_bytes + 8 * kAtomBytes, &maps.bands, y[k], full);
+                    const uint32_t at = dst + 2 * step * S::group_bytes;
+                    if (wide && !split && !kLazy) {
+                        tma_box4(at, &maps.rows, y[step], full);
+                    } else if (wide) {
+                        // a group's chunks are fewer than its room: a box for each group
+                        for (int k = 0; k < 2; ++k) {
+                            tma_box4(at + k * S::group_bytes, &maps.rows, y[step] + k, full);
+                            if (split && !kLazy)
+                                tma_box3(at + k * S::group_bytes + 8 * kAtomBytes, &maps.bands, y[step] + k, full);
+                        }
+                    } else {
+                        for (int k = 0; k < 2; ++k) {
+                            tma_box4(at + k * S::group_bytes, &maps.rows, y[2 * step + k], full);
+                            if (split && !kLazy)
+                                tma_box3(at + k * S::group_bytes + 8 * kAtomBytes, &maps.bands, y[2 * step + k], full);
+                        }
                     }
                 }
                 __syncwarp();
             }
+            if (more) resolve();
             ring.advance();
         }
     }
@@ -336,7 +360,7 @@ struct Copier {
                 uint4 hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int row = map_row(a, page_of(a, w, table_row, key + r0 + 16 * k));
+                    const int row = map_row(a, page_of(a, maps, w, table_row, key + r0 + 16 * k));
                     slot[k] = row < 0 ? -1 : row - (long long)a.layer * g.num_pages * g.block_size;
                     band[k] = a.kv + band_off(g, a.layer, max(slot[k], 0ll)) + v;
                 }
@@ -437,7 +461,6 @@ __device__ __forceinline__ void issue_mmas(const AttnArgs& a, Misc* m, uint32_t 
     unsigned long long t0 = 0;
     while (!pv.done()) {
         bool moved = false;
-        // S of a tile may run one tile ahead of its product with V: there are two S buffers
         if (!s.done() && s.index <= pv.index + 1 && test(smem_addr(&m->full[s.index % kStages]), (s.index / kStages) & 1) &&
             (s.tile > 0 || test(smem_addr(&m->q_full), q_phase))) {
             fence_async_smem();
@@ -603,7 +626,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int h = k & 1;
-                const float e0 = exp2f(x[2 * k] - base[h]), e1 = exp2f(x[2 * k + 1] - base[h]);
+                const float e0 = exp2_approx(x[2 * k] - base[h]), e1 = exp2_approx(x[2 * k + 1] - base[h]);
                 sum[h] += e0 + e1;
                 p[k] = pack_bf16x2(e0, e1);
             }
@@ -751,14 +774,16 @@ EncodeTiled encode_tiled()
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// Map of `rows` rows of row_vecs 16-byte vectors at `base`, as planes of 64 columns: boxes of 8 rows of `planes`.
-bool make_map(EncodeTiled encode, CUtensorMap* map, const uint4* base, int64_t rows, int row_vecs, int planes)
+// Map of `rows` rows of row_vecs 16-byte vectors at `base`: 64 columns, 8 rows of a group, `planes` planes of 64
+// columns (none: three dimensions), groups; boxes of `groups` groups.
+bool make_map(EncodeTiled encode, CUtensorMap* map, const uint4* base, int64_t rows, int row_vecs, int planes, int groups)
 {
-    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)row_vecs * 16, 128};
-    const cuuint32_t box[3] = {64, 8, (cuuint32_t)planes}, steps[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 1 ? 3 : 2, const_cast<uint4*>(base), dims, strides, box,
-                  steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t row = (cuuint64_t)row_vecs * 16, n = (cuuint64_t)(rows / 8);
+    const cuuint64_t dims[4] = {64, 8, planes ? (cuuint64_t)planes : n, n};
+    const cuuint64_t strides[3] = {row, planes ? 128 : 8 * row, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(planes ? planes : groups), (cuuint32_t)groups}, steps[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 4 : 3, const_cast<uint4*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -772,9 +797,14 @@ int attention_mla_prepare(const Geometry& g, const void* kv, MlaMaps* maps)
     // rows of every layer follow one another, in whole rows and in the arrays of a split-rope pool alike
     const int64_t rows = g.num_pages * g.block_size * g.num_layers;
     const bool whole = !(g.flags & (LEYLINE_POOL_SPLIT_ROPE | LEYLINE_POOL_LAZY));
-    maps->boxes = g.block_size % 8 == 0 && rows <= INT32_MAX;
-    if (!make_map(encode, &maps->rows, base, rows, g.lat_row_vecs, whole ? 9 : 8) ||
-        !make_map(encode, &maps->bands, base + g.rope_base_vecs, rows, g.rope_row_vecs, 1))
+    maps->box = g.block_size % 16 == 0 ? 16 : g.block_size % 8 == 0 ? 8 : 0;
+    if (rows > INT32_MAX) return (int)cudaErrorInvalidValue;
+    maps->shift = -1;
+    for (int k = 0; k < 31; ++k)
+        if (g.block_size == 1 << k) maps->shift = k;
+    // a box holds two groups where their chunks follow one another
+    if (maps->box && (!make_map(encode, &maps->rows, base, rows, g.lat_row_vecs, whole ? 9 : 8, whole && maps->box == 16 ? 2 : 1) ||
+                      !make_map(encode, &maps->bands, base + g.rope_base_vecs, rows, g.rope_row_vecs, 0, 1)))
         return (int)cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(attend_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes<false>);

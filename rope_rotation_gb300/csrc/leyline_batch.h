@@ -190,11 +190,12 @@ struct AttnArgs {
 constexpr int kAttnMaxValue = 1024;
 constexpr int kAttnMaxRope = 256;
 
-// Tensor maps of an MLA pool's rows, all layers', for boxes of 8 rows: whole rows (their latents, in split-rope and
+// Tensor maps of an MLA pool's rows, all layers', in groups of 8 rows: whole rows (their latents, in split-rope and
 // lazy pools), and the bands of split-rope pools.
 struct MlaMaps {
     CUtensorMap rows, bands;
-    int boxes;  // whether pages hold whole boxes
+    int box;    // rows of a box, 8 or 16; 0: the block size is no multiple of 8
+    int shift;  // log2 of the block size; -1: no power of two
 };
 
 int launch_install(const InstallArgs& a, void* stream);

@@ -87,24 +87,31 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 }
 
 // ------------------------------------------------------- asynchronous copies --
-// A box of a two- or three-dimensional tensor map at row y (columns and planes from 0); rows outside the
-// tensor arrive as zeros.
-__device__ __forceinline__ void tma_box2(uint32_t dst, const void* map, int y, uint32_t bar)
+// A box of a three- or four-dimensional tensor map at index y of its outermost axis (the others from 0);
+// what lies outside the tensor arrives as zeros.
+__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int y, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(
             dst),
         "l"(map), "r"(0), "r"(y), "r"(bar)
         : "memory");
 }
 
-__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int y, uint32_t bar)
+__device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int y, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(
             dst),
-        "l"(map), "r"(0), "r"(y), "r"(0), "r"(bar)
+        "l"(map), "r"(0), "r"(y), "r"(bar)
         : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // 16 bytes to shared memory; zeros when !valid (nothing is read then).
