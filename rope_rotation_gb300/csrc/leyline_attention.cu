@@ -291,16 +291,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 }  // namespace
 
-int attention_prepare(const Geometry& g, const void* kv, MlaMaps* maps)
+int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps)
 {
-    if (attention_takes_mla(g)) return attention_mla_prepare(g, kv, maps);
+    if (attention_takes_tiles(g)) return attention_tile_prepare(g, kv, maps);
     return (int)cudaFuncSetAttribute(attend_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)any_shape(g).bytes);
 }
 
-int launch_attention(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream)
+int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream)
 {
-    if (attention_takes_mla(a.g)) return launch_attention_mla(a, maps, ctas, stream);
+    if (attention_takes_tiles(a.g)) return launch_attention_tile(a, maps, ctas, stream);
     return (int)launch_dependent_smem(attend_any_kernel, ctas, kAnyThreads, any_shape(a.g).bytes,
                                       (cudaStream_t)stream, a);
 }

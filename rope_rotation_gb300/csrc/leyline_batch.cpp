@@ -28,7 +28,7 @@ struct leyline_batch {
     WorkShape shape{};
     int64_t max_tiles = 0;
     BatchLayout layout{};
-    MlaMaps maps{};
+    TileMaps maps{};
     size_t stage_bytes = 0;  // plan + runs
     char* d_plan = nullptr;
     int64_t* d_slot = nullptr;
@@ -184,7 +184,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     b->value_dim = g.latent_dim / bands;
     // a head count that does not go over the key bands does for append and rotate alone
     b->shape = WorkShape{bands, q_heads % bands == 0 ? q_heads / bands : 0, p->sm_count,
-                         attention_takes_mla(g) && p->d_pending ? kAttnRowsLazy : kAttnRows};
+                         bands == 1 && attention_takes_tiles(g) && p->d_pending ? kAttnRowsLazy : kAttnRows};
     // every chunk's rows are cut into tiles of their own
     b->max_tiles = (ceil_div((int64_t)max_tokens * b->shape.group, b->shape.rows) + max_chunks) * bands;
     if (b->max_tiles > INT32_MAX / 4) {

@@ -190,28 +190,28 @@ struct AttnArgs {
 constexpr int kAttnMaxValue = 1024;
 constexpr int kAttnMaxRope = 256;
 
-// Tensor maps of an MLA pool's rows, all layers', in groups of 8 rows: whole rows (their latents, in split-rope and
-// lazy pools), and the bands of split-rope pools.
-struct MlaMaps {
+// Tensor maps of a pool's rows, all layers', in groups of 8 rows and planes of 64 columns, for leyline_attention_tile.cu:
+// the values (whole MLA rows: with their band), and the bands.
+struct TileMaps {
     CUtensorMap rows, bands;
-    int box;    // rows of a box, 8 or 16; 0: the block size is no multiple of 8
-    int shift;  // log2 of the block size; -1: no power of two
+    int box;     // rows of a box, 8 or 16; 0: the block size is no multiple of 8
+    int shift;   // log2 of the block size; -1: no power of two
+    int values;  // planes of a band's values
+    int whole;   // the band comes with the values
+    int stages;  // cache tiles in shared memory
 };
 
 int launch_install(const InstallArgs& a, void* stream);
 int launch_append(const AppendArgs& a, int64_t tokens, int sm_count, void* stream);
 int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* stream);
-// Whether the row shape takes the MLA kernel (latent 512, one 64-wide band).
-inline bool attention_takes_mla(const Geometry& g)
-{
-    return g.latent_vecs == 64 && g.rope_vecs == 8 && g.rope_heads == 1;
-}
-// Fills *maps for MLA rows at kv.
-int attention_prepare(const Geometry& g, const void* kv, MlaMaps* maps);
+// Whether the rows go to the tensor-core kernel (leyline_attention_tile.cu).
+bool attention_takes_tiles(const Geometry& g);
+int attention_tile_prepare(const Geometry& g, const void* kv, TileMaps* maps);
+int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
+// Fills *maps for the rows at kv and readies their kernel.
+int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
-int launch_attention(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream);
-int attention_mla_prepare(const Geometry& g, const void* kv, MlaMaps* maps);  // leyline_attention_mla.cu
-int launch_attention_mla(const AttnArgs& a, const MlaMaps& maps, int ctas, void* stream);
+int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
 int launch_join(const AttnArgs& a, int joins, void* stream);
 
 }  // namespace leyline

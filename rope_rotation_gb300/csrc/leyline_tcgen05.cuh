@@ -87,23 +87,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 }
 
 // ------------------------------------------------------- asynchronous copies --
-// A box of a three- or four-dimensional tensor map at index y of its outermost axis (the others from 0);
+// A box of a four-dimensional tensor map at index z of its third axis and y of its outermost (the others from 0);
 // what lies outside the tensor arrives as zeros.
-__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int y, uint32_t bar)
+__device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int z, int y, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(
             dst),
-        "l"(map), "r"(0), "r"(y), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(map), "r"(0), "r"(y), "r"(bar)
+        "l"(map), "r"(0), "r"(z), "r"(y), "r"(bar)
         : "memory");
 }
 
@@ -128,6 +119,15 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
 }
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Four 8 x 8 matrices of 16-bit values from the fragments of a warp: thread t holds of matrix i the elements
+// 2 (t % 4), + 1 of row t / 4 in vi; lane 8 i + r gives the address of row r of matrix i.
+__device__ __forceinline__ void store_matrices(uint32_t at, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v0), "r"(v1), "r"(v2),
+                 "r"(v3)
+                 : "memory");
+}
 
 // Order generic-proxy accesses to shared memory with those of the async proxy (the tensor core).
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

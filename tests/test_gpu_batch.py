@@ -158,6 +158,9 @@ def test_refusals_of_the_calls():
 SHAPES = {  # latent, rope, bands
     "mla": (512, 64, 1),
     "grouped": (512, 128, 4),
+    "grouped-64": (256, 64, 4),
+    "grouped-256": (512, 256, 2),
+    "grouped-192": (384, 64, 2),  # values of 192
     "odd": (40, 48, 1),
     "odd-grouped": (72, 16, 3),
     "wide": (1024, 256, 2),
@@ -329,10 +332,11 @@ def test_attention_decode(ctx, heads):
     _attend([ctx - 1], [(0, ctx - 1, 1)], heads, seed=ctx)
 
 
-@pytest.mark.parametrize("B", [1, 3, 5, 16, 64, 100])
+@pytest.mark.parametrize("B", [1, 3, 5, 8, 16, 24, 64, 100])
 @pytest.mark.parametrize("flags", [0, LAZY, SPLIT, LAZY | SPLIT])
-def test_attention_blocks_and_pools(B, flags):
-    _attend([700, 0, 129, 64], [(0, 700, 1), (1, 0, 70), (2, 100, 29), (3, 64, 3)], 16, B=B, flags=flags, seed=B)
+@pytest.mark.parametrize("shape", ["mla", "grouped"])
+def test_attention_blocks_and_pools(B, flags, shape):
+    _attend([700, 0, 129, 64], [(0, 700, 1), (1, 0, 70), (2, 100, 29), (3, 64, 3)], 16, shape, B=B, flags=flags, seed=B)
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 17, 64, 100, 257])
@@ -342,8 +346,8 @@ def test_attention_chunks(n, heads):
     _attend([0, 333, 400], [(0, 0, n), (1, 333, n), (2, 20, n)], heads, seed=n)
 
 
-@pytest.mark.parametrize("shape", ["grouped", "odd", "odd-grouped", "wide"])
-@pytest.mark.parametrize("flags,pairs", [(0, 0), (LAZY, 1), (SPLIT, 0)])
+@pytest.mark.parametrize("shape", ["grouped", "grouped-64", "grouped-256", "grouped-192", "odd", "odd-grouped", "wide"])
+@pytest.mark.parametrize("flags,pairs", [(0, 0), (LAZY, 0), (LAZY, 1), (SPLIT, 0)])
 @pytest.mark.parametrize("per", [1, 4, 7])
 def test_attention_row_shapes(shape, flags, pairs, per):
     heads = per * SHAPES[shape][2]
@@ -370,7 +374,7 @@ def test_attention_interleaved_lazy():
     _attend([900], [(0, 900, 20)], 16, flags=LAZY, pairs=1, B=1)
 
 
-@pytest.mark.parametrize("shape", ["mla", "grouped"])
+@pytest.mark.parametrize("shape", ["mla", "grouped", "grouped-64", "grouped-256", "odd"])
 def test_lazy_naive_pool_attends_to_the_gathered_rows(shape):
     """With the naive rounding a turned band is a bf16 value: attention over a lazy pool gives the same bits as over
     an eager pool that holds what leyline_gather returns."""
@@ -387,7 +391,7 @@ def test_lazy_naive_pool_attends_to_the_gathered_rows(shape):
         for layer in range(2):
             eager.write_layer_rows(layer, flat_e, lazy.gather(r, layer, 0, n))
     chunks = [(0, 1234, 3), (1, 77, 1)]
-    ql, q = BH.bf16(4, 16, 512) if bands == 1 else None, BH.bf16(4, 16, rope, seed=1)
+    ql, q = BH.bf16(4, 16, lat) if bands == 1 else None, BH.bf16(4, 16, rope, seed=1)
     rows = BH.bf16(4, lazy.row, seed=2)
     got = []
     for cache in (lazy, eager):
