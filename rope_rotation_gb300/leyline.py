@@ -160,6 +160,25 @@ def _check(rc: int) -> None:
         raise LeylineError(rc, msg)
 
 
+def _raw_stream():
+    """A function of a device index: its current stream's address.  torch.cuda.current_stream builds a Stream object for
+    it (3 us of a call's host time); the raw query is what it wraps."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
+
+
+_current_raw_stream = None
+
+
+def current_stream_ptr(device: int) -> int:
+    """Address of the current stream of CUDA device `device`."""
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        _current_raw_stream = _raw_stream()
+    return _current_raw_stream(device)
+
+
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -409,19 +428,24 @@ def leyline_batch_plan(batch, tables: Tables, chunks, stream=None) -> None:
 
 def heads(t, what: str, tokens: int, n_heads: int, dim: int) -> Heads:
     """A view of a bf16 tensor [>= tokens][n_heads][dim] whose last axis is contiguous."""
-    import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _bf16():
         raise ValueError(f"{what}: dtype {t.dtype}, expected torch.bfloat16")
-    if t.dim() != 3 or t.shape[0] < tokens or t.shape[1] != n_heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [>= {tokens}][{n_heads}][{dim}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < tokens or shape[1] != n_heads or shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [>= {tokens}][{n_heads}][{dim}]")
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError(f"{what}: the last axis must be contiguous")
     if n_heads == 1:  # the stride of an axis of one entry says nothing
         hs = dim
-    if t.shape[0] == 1:
+    if shape[0] == 1:
         ts = n_heads * hs
     return Heads(t.data_ptr(), ts, hs)
+
+
+def _bf16():
+    import torch
+    return torch.bfloat16
 
 
 def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps: float = 1e-6, stream=None) -> None:

@@ -191,6 +191,7 @@ class Batch:
         self.bands = cache.rope_heads
         self.value_dim = cache.latent_dim // self.bands
         self.tokens = 0
+        self.device_index = cache.kv.device.index
         self.handle = None
         self.handle = leyline.leyline_batch_create(cache.pool, max_chunks, max_tokens, q_heads)
 
@@ -198,8 +199,12 @@ class Batch:
         """chunks: (req, start, n) or (req, start, n, rope_start) of each: the n tokens at rows
         [start, start + n) of request req.  Rows past the request's length take pages."""
         a = leyline.chunk_batch(chunks)
-        leyline.leyline_batch_plan(self.handle, self.cache.tables, a, stream)
+        leyline.leyline_batch_plan(self.handle, self.cache.tables, a, self._stream(stream))
         self.tokens = int(a["n"].sum())
+
+    def _stream(self, stream):
+        """The stream of a call: the one given, else the current one of the cache's device."""
+        return leyline.current_stream_ptr(self.device_index) if stream is None else stream
 
     def _device(self, t, what: str):
         if t.device != self.cache.kv.device:
@@ -220,7 +225,7 @@ class Batch:
             raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [>= {self.tokens}][{self.cache.row}]")
         leyline.leyline_append(self.handle, layer, rows,
                                self._weights(latent_norm, "latent_norm", self.cache.latent_dim),
-                               self._weights(key_norm, "key_norm", self.cache.rope_dim), eps, stream)
+                               self._weights(key_norm, "key_norm", self.cache.rope_dim), eps, self._stream(stream))
 
     def rotate(self, q, out=None, norm=None, eps: float = 1e-6, stream=None):
         """Norm and turn query bands [tokens][q_heads][rope_dim] into out (default: a new tensor; q itself is fine)."""
@@ -228,7 +233,7 @@ class Batch:
             out = self.cache.torch.empty_like(q)
         dim = self.cache.rope_dim
         leyline.leyline_rotate(self.handle, self._heads(q, "q", dim), self._heads(out, "out", dim),
-                               self._weights(norm, "norm", dim), eps, stream)
+                               self._weights(norm, "norm", dim), eps, self._stream(stream))
         return out
 
     def attention(self, layer: int, q_latent, q_rope, scale: float, out=None, lse=None, prefix: bool = False,
@@ -249,7 +254,7 @@ class Batch:
         leyline.leyline_attention(
             self.handle, layer, None if q_latent is None else self._heads(q_latent, "q_latent", self.cache.latent_dim),
             self._heads(q_rope, "q_rope", self.cache.rope_dim), self._heads(out, "out", self.value_dim),
-            self._device(lse, "lse"), scale, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0, stream)
+            self._device(lse, "lse"), scale, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0, self._stream(stream))
         return out, lse
 
     def close(self) -> None:
