@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libleyline.so")
 SOURCES = ["leyline_move.cu", "leyline_reindex.cu", "leyline_read.cu", "leyline_planner.cpp", "leyline_pool.cpp",
            "leyline_noalloc.cu", "leyline_append.cu", "leyline_attention.cu",
-           "leyline_attention_tile.cu", "leyline_batch.cpp",
+           "leyline_attention_tile.cu", "leyline_attention_pair.cu", "leyline_batch.cpp",
            "leyline_batch_plan.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

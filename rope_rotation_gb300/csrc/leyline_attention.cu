@@ -58,6 +58,8 @@ __host__ __device__ inline AnyShape any_shape(const Geometry& g)
     return s;
 }
 
+// kRedo: only the items that the pair kernel marked, whose tiles have kPairRows query rows.
+template <bool kRedo>
 __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_constant__ AttnArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -78,7 +80,10 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
     const float scale2 = a.scale * kLog2e;
     wait_for_previous_grid();
     allow_next_grid();
+    if (kRedo && a.header->pairs == 0) return;
+    constexpr int kPitch = kRedo ? kPairRows : kAttnRows;
     for (int it = a.cta_begin[blockIdx.x]; it < a.cta_begin[blockIdx.x + 1]; ++it) {
+        if (kRedo && a.redo[2 * it] == 0 && a.redo[2 * it + 1] == 0) continue;
         const AttnItem item = a.items[it];
         const ChunkDev ch = a.chunks[item.chunk];
         const int32_t* table_row = a.header->table + (long long)ch.req * a.header->max_blocks;
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                 const float o = l > 0.f ? o_s[i] / l : (l == 0.f ? 0.f : l);
                 const int row = item.row0 + r0 + r;
                 if (item.part >= 0) {
-                    a.part_out[((long long)item.part * kAttnRows + r0 + r) * vdim + d] = o;
+                    a.part_out[((long long)item.part * kPitch + r0 + r) * vdim + d] = o;
                 } else {
                     const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
                     static_cast<__nv_bfloat16*>(a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + d] =
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                 const int row = item.row0 + r0 + tid;
                 const float lse = l_s[tid] == 0.f ? -INFINITY : (m_s[tid] + log2f(l_s[tid])) * kLn2;
                 if (item.part >= 0) {
-                    a.part_lse[(long long)item.part * kAttnRows + r0 + tid] = lse;
+                    a.part_lse[(long long)item.part * kPitch + r0 + tid] = lse;
                 } else if (a.lse) {
                     const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
                     a.lse[tok * a.q_heads + head] = lse;
@@ -231,40 +236,41 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
 // depend on which CTA finished first.
 constexpr int kJoinThreads = 128;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int slices)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int slices, int rows)
 {
     wait_for_previous_grid();
     // the next kernel is not let in early: its CTAs, one per SM, would crowd onto the SMs that are free first
     const long long unit = blockIdx.x * (long long)(kJoinThreads / 32) + threadIdx.x / 32;
     const int slice = (int)(unit % slices);
-    const int j = (int)(unit / slices / kAttnRows), r = (int)(unit / slices % kAttnRows);
+    const int j = (int)(unit / slices / rows), r = (int)(unit / slices % rows);
     if (j >= a.header->n_joins) return;
     const AttnJoin jn = a.joins[j];
     if (r >= jn.rows) return;
+    const int pitch = a.header->pairs ? kPairRows : kAttnRows;
     const Geometry& g = a.g;
     const bool mla = g.rope_heads <= 1;
     const int group = a.q_heads / (mla ? 1 : g.rope_heads);
     const int vdim = g.latent_dim / (mla ? 1 : g.rope_heads);
     const int lane = threadIdx.x & 31;
-    const float* lse = a.part_lse + (long long)jn.part0 * kAttnRows + r;
+    const float* lse = a.part_lse + (long long)jn.part0 * pitch + r;
     float top = -INFINITY;
-    for (int k = lane; k < jn.parts; k += 32) top = fmaxf(top, lse[(long long)k * kAttnRows]);
+    for (int k = lane; k < jn.parts; k += 32) top = fmaxf(top, lse[(long long)k * pitch]);
     for (int m = 16; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     const int d = 128 * slice + 4 * lane;
     const bool on = d < vdim;
-    const float* part = a.part_out + ((long long)jn.part0 * kAttnRows + r) * vdim + (on ? d : 0);
+    const float* part = a.part_out + ((long long)jn.part0 * pitch + r) * vdim + (on ? d : 0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
     for (int k0 = 0; k0 < jn.parts; k0 += 32) {
         const int n = min(32, jn.parts - k0);
-        const float x = lane < n ? lse[(long long)(k0 + lane) * kAttnRows] : -INFINITY;
+        const float x = lane < n ? lse[(long long)(k0 + lane) * pitch] : -INFINITY;
         const float mine = x == -INFINITY ? 0.f : exp2f((x - top) * kLog2e);
         total += mine;
         for (int k = 0; k < n; k += 8) {
             float4 v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                v[u] = k + u < n ? __ldcg(reinterpret_cast<const float4*>(part + (long long)(k0 + k + u) * kAttnRows * vdim))
+                v[u] = k + u < n ? __ldcg(reinterpret_cast<const float4*>(part + (long long)(k0 + k + u) * pitch * vdim))
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -293,24 +299,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps)
 {
-    if (attention_takes_tiles(g)) return attention_tile_prepare(g, kv, maps);
-    return (int)cudaFuncSetAttribute(attend_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (attention_takes_tiles(g)) {
+        // the kernel that computes marked items again
+        cudaError_t e = cudaFuncSetAttribute(attend_any_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)any_shape(g).bytes);
+        return e != cudaSuccess ? (int)e : attention_tile_prepare(g, kv, maps);
+    }
+    return (int)cudaFuncSetAttribute(attend_any_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)any_shape(g).bytes);
+}
+
+int launch_attention_redo(const AttnArgs& a, int pairs, void* stream)
+{
+    return (int)launch_dependent_smem(attend_any_kernel<true>, pairs, kAnyThreads, any_shape(a.g).bytes,
+                                      (cudaStream_t)stream, a);
 }
 
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream)
 {
     if (attention_takes_tiles(a.g)) return launch_attention_tile(a, maps, ctas, stream);
-    return (int)launch_dependent_smem(attend_any_kernel, ctas, kAnyThreads, any_shape(a.g).bytes,
+    return (int)launch_dependent_smem(attend_any_kernel<false>, ctas, kAnyThreads, any_shape(a.g).bytes,
                                       (cudaStream_t)stream, a);
 }
 
-int launch_join(const AttnArgs& a, int joins, void* stream)
+int launch_join(const AttnArgs& a, int joins, int rows, void* stream)
 {
     const int vdim = a.g.latent_dim / std::max(a.g.rope_heads, 1);
     const int slices = (vdim + 127) / 128;
-    const int grid = (int)(((long long)joins * kAttnRows * slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    return (int)launch_dependent(join_kernel, grid, kJoinThreads, (cudaStream_t)stream, a, slices);
+    const int grid = (int)(((long long)joins * rows * slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    return (int)launch_dependent(join_kernel, grid, kJoinThreads, (cudaStream_t)stream, a, slices, rows);
 }
 
 }  // namespace leyline

@@ -1,0 +1,587 @@
+// leyline_attention_pair.cu -- attention over MLA rows by pairs of CTAs (sm_103a): the kernel for many query rows
+// (prompt chunks, many heads), where the tensor cores and shared memory bound the work.
+//
+// As leyline_attention_tile.cu, per tile of 64 cache rows, but two CTAs on neighbouring SMs work on 128 query rows
+// with products that span both (cta_group::2):
+//   S   = Q K^T    [128 x 64]: a CTA holds 64 query rows and 32 cache rows;
+//   O^T = V^T P^T  [512 x 128]: a CTA holds 256 value dimensions of all 64 cache rows, and P of its own 64 query rows.
+// Each CTA thus reads half of the operands of both products (S takes 24 cycles of shared memory a product instead of
+// 32 at half the tensor rate, O^T 48 for twice the work), and K and V lie in buffers of their own: K is free for the
+// next but one tile as soon as S is done, before the softmax.
+//
+// The reference maximum of a row is that of its item's first tile and stays: weights are exp2(x - m0), in bf16 and
+// fp32 as exact relative to their size as any.  A later score above m0 by more than 2^80 could leave fp32's range
+// in the sums; the item is then marked, and a kernel that follows computes it again (leyline_attention.cu).  So O
+// never has to be rescaled, which would take both CTAs to agree in the middle of every tile.
+//
+// Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
+// K and 7-10 V (TMA, one lane each: a thread issues a TMA instruction in 100 to 170 cycles, whatever its size, and a
+// thread alone bound the kernel), warps 11-14 copy the queries and the tiles that end inside.
+#include "leyline_attention.cuh"
+
+namespace leyline {
+namespace {
+
+constexpr int kSoftmaxWarps = 4;
+constexpr int kMmaWarp = 4, kKeyWarp = 5, kValueWarp = 7, kCopyWarp = 11;
+constexpr int kKeyWarps = 2, kCopyWarps = 4;
+constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
+
+constexpr int kRows = 64;               // query rows of a CTA
+constexpr int kHalfKeys = kAttnKeys / 2;  // cache rows whose keys a CTA holds
+constexpr int kStages = 2;
+constexpr int kSteps = kAttnKeys / 16;
+constexpr int kChunkBytes = kRows * 128;  // queries: 9 chunks
+constexpr int kKeyBytes = kHalfKeys / 8 * 9 * kAtomBytes;      // whole rows: [group][9 chunks]; else 8, and the band's region
+constexpr int kBandOff = kHalfKeys / 8 * 8 * kAtomBytes;
+constexpr int kValueGroup = 4 * kAtomBytes;                    // chunks 2 r, 2 r + 1, 4 + 2 r, 5 + 2 r of CTA r
+constexpr int kValueBytes = kAttnKeys / 8 * kValueGroup;
+constexpr int kKeyOff = 9 * kChunkBytes;
+constexpr int kValueOff = kKeyOff + kStages * kKeyBytes;
+constexpr int kPOff = kValueOff + kStages * kValueBytes;       // two buffers
+constexpr int kMiscOff = kPOff + 2 * kChunkBytes;
+
+// Barriers marked (first) are used in the first CTA alone; the others in both.
+struct Misc {
+    unsigned long long k_full[kStages], v_full[kStages];  // (first)
+    unsigned long long k_empty[kStages], v_empty[kStages][kSteps];
+    unsigned long long q_full;                            // (first)
+    unsigned long long q_empty;
+    unsigned long long tail_k[kStages], tail_v[kStages];  // the stage is free for a tile that ends inside
+    unsigned long long s_full[2];
+    unsigned long long p_ready[2];                        // (first)
+    unsigned long long pv_done[2];
+    unsigned long long x_ready;                           // both CTAs' factors are there
+    unsigned long long drained;
+    uint32_t tmem;
+    int quit;
+    int redo;                    // a score left the range of its row's reference
+    float half[2][kRows];        // a row's maximum, then sum, over either half of a tile's columns
+    float factor[2 * kRows];     // 1 / l of both CTAs' rows
+};
+constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0;    // 2 blocks of 128 columns: 128 of the CTA's dimensions x both CTAs' rows
+constexpr uint32_t kTmemS = 256;  // 2 buffers of 32 columns
+
+constexpr float kRange = 80.f;
+
+__device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, Misc* m, int32_t* status)
+{
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, &m->quit, status));
+}
+
+// -------------------------------------------------------------------- loads --
+// One lane of a warp each.  Keys (kValues false): loader `part` of two takes 16 of this CTA's 32 rows of a tile, whole;
+// values: loader `part` of four takes this CTA's four chunks of 16 of the tile's 64 rows, those of PV's step `part`.
+template <bool kValues>
+__device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& maps, Misc* m, uint32_t smem, uint32_t rank,
+                                           int part)
+{
+    const int pair = blockIdx.x / 2;
+    const bool wide = maps.box == 16;
+    const int boxes = wide ? 1 : 2;  // of two groups of 8 rows, or one each
+    const int first = (kValues ? 0 : (int)rank * kHalfKeys) + 16 * part;
+    const int layer_groups = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
+    const int chunks = maps.whole ? 9 : 8;
+    Ring ring;
+    for (int i = a.cta_begin[pair]; i < a.cta_begin[pair + 1]; ++i) {
+        const Work w = load_work(a, i);
+        const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        PageOf at[2];
+        auto look_up = [&](long long key) {
+            if (!by_box(maps, w, key)) return;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (k < boxes) at[k] = page_of(a, maps, w, table_row, key + first + 8 * k);
+        };
+        look_up(w.it.key0);
+        for (int t = 0; t < w.tiles; ++t) {
+            const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            const bool box = by_box(maps, w, key);
+            int y[2] = {-2, -2};
+            if (box) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (k < boxes) {
+                        const long long slot = slot_of(a, at[k]);
+                        if (slot >= 0) y[k] = layer_groups + (int)(slot >> 3);
+                    }
+            }
+            if (t + 1 < w.tiles) look_up(key + kAttnKeys);
+            const uint32_t empty = smem_addr(kValues ? &m->v_empty[ring.stage][part] : &m->k_empty[ring.stage]);
+            if (!mbar_wait_cluster(empty, ring.phase ^ 1, &m->quit, a.status)) return;
+            if (!box) {  // the copy warps' tile.  They do not follow the stages' uses, which a parity could not tell apart
+                mbar_arrive(smem_addr(kValues ? &m->tail_v[ring.stage] : &m->tail_k[ring.stage]));
+            } else {
+                // Both CTAs' bytes are counted in the first, whose loader alone arrives, for all that are expected: an
+                // arrival from the other CTA is a release at cluster scope, which took 1000 to 1600 cycles here
+                const uint32_t bar = smem_addr(kValues ? &m->v_full[ring.stage] : &m->k_full[ring.stage]);
+                const uint32_t full = cluster_addr(bar, 0);
+                if (rank == 0) {
+                    mbar_expect_tx(bar, 2 * (kValues ? kValueBytes / kSteps : kKeyBytes / kKeyWarps));
+                    mbar_arrive_n(bar, 2 * kCopyWarps / (kValues ? kSteps : kKeyWarps) - 1);
+                }
+                if (!kValues) {
+                    const uint32_t dst = smem + kKeyOff + ring.stage * kKeyBytes;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (k < boxes) {
+                            const int group = 2 * part + k;
+                            pair_box4(dst + group * chunks * kAtomBytes, &maps.pair_keys, 0, y[k], full);
+                            if (!maps.whole) pair_box4(dst + kBandOff + group * kAtomBytes, &maps.bands, 0, y[k], full);
+                        }
+                } else {
+                    const uint32_t dst = smem + kValueOff + ring.stage * kValueBytes;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (k < boxes)
+                            pair_box5(dst + (2 * part + k) * kValueGroup, &maps.pair_values, 2 * (int)rank, y[k], full);
+                }
+            }
+            ring.advance(kStages);
+        }
+    }
+}
+
+// Queries of this CTA's rows, and tiles that end inside: 16-byte copies, zeros for rows past the end.
+__device__ __forceinline__ void copy_tiles(const AttnArgs& a, const TileMaps& maps, Misc* m, uint32_t smem, uint32_t rank)
+{
+    const Geometry& g = a.g;
+    const int pair = blockIdx.x / 2, group = a.q_heads;
+    const int tid = threadIdx.x - 32 * kCopyWarp, v = tid % 8, r0 = tid / 8;
+    const int chunks = maps.whole ? 9 : 8;
+    // the copies of all four warps have landed when each has arrived
+    auto arrive = [&](unsigned long long* bar) {
+        cp_async_wait_all();
+        fence_async_smem();
+        __syncwarp();
+        if (tid % 32 == 0) cluster_arrive(cluster_addr(smem_addr(bar), 0), 1);
+    };
+    int ring_tiles = 0;  // of the items before
+    uint32_t q_phase = 0, tail_phase = 0;  // (a bit for each stage)
+    for (int i = a.cta_begin[pair]; i < a.cta_begin[pair + 1]; ++i) {
+        const Work w = load_work(a, i);
+        if (w.tiles == 0) continue;
+        if (!pair_warp_wait(smem_addr(&m->q_empty), q_phase ^ 1, m, a.status)) return;
+        q_phase ^= 1;
+#pragma unroll 1
+        for (int r = r0; r < kRows; r += 16) {
+            const bool on = (int)rank * kRows + r < w.it.rows;
+            const int row = w.it.row0 + (on ? (int)rank * kRows + r : 0);
+            const long long tok = w.ch.tok0 + row / group, head = row % group;
+            const uint4* lat = static_cast<const uint4*>(a.q_latent.ptr) +
+                               (tok * a.q_latent.token_stride + head * a.q_latent.head_stride) / 8 + v;
+            const uint4* band =
+                static_cast<const uint4*>(a.q_rope.ptr) + (tok * a.q_rope.token_stride + head * a.q_rope.head_stride) / 8 + v;
+            const uint32_t to = smem + r * 128 + ((v ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 9; ++c) cp_async16(to + c * kChunkBytes, c < 8 ? lat + 8 * c : band, on);
+        }
+        arrive(&m->q_full);
+        const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        // the last tile, where it ends inside
+        const int stage = (ring_tiles + w.tiles - 1) % kStages;
+        ring_tiles += w.tiles;
+        const long long key = w.it.key0 + (long long)(w.tiles - 1) * kAttnKeys;
+        if (by_box(maps, w, key)) continue;
+        if (!pair_warp_wait(smem_addr(&m->tail_k[stage]), tail_phase >> stage & 1, m, a.status)) return;
+        const uint32_t keys = smem + kKeyOff + stage * kKeyBytes, values = smem + kValueOff + stage * kValueBytes;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 16 * k;
+            const long long slot = slot_of(a, page_of(a, maps, w, table_row, key + rank * kHalfKeys + r));
+            const uint4* lat = a.kv + lat_off(g, a.layer, max(slot, 0ll)) + v;
+            const uint4* band = a.kv + band_off(g, a.layer, max(slot, 0ll)) + v;
+            const uint32_t in = (r & 7) * 128 + ((v ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) cp_async16(keys + ((r / 8) * chunks + c) * kAtomBytes + in, lat + 8 * c, slot >= 0);
+            cp_async16(keys + (maps.whole ? ((r / 8) * 9 + 8) * kAtomBytes : kBandOff + (r / 8) * kAtomBytes) + in, band,
+                       slot >= 0);
+        }
+        arrive(&m->k_full[stage]);
+        if (!pair_warp_wait(smem_addr(&m->tail_v[stage]), tail_phase >> stage & 1, m, a.status)) return;
+        tail_phase ^= 1u << stage;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = r0 + 16 * k;
+            const long long slot = slot_of(a, page_of(a, maps, w, table_row, key + r));
+            const uint4* lat = a.kv + lat_off(g, a.layer, max(slot, 0ll)) + v;
+            const uint32_t in = (r / 8) * kValueGroup + (r & 7) * 128 + ((v ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                cp_async16(values + c * kAtomBytes + in, lat + 8 * (4 * (c / 2) + 2 * (int)rank + c % 2), slot >= 0);
+        }
+        arrive(&m->v_full[stage]);
+    }
+}
+
+// --------------------------------------------------------------------- MMAs --
+struct TileCursor {
+    int item, end_item;
+    int tile, tiles;
+    int index;  // tiles before this one
+    Ring ring;
+
+    __device__ __forceinline__ void settle(const AttnArgs& a)
+    {
+        while (item < end_item) {
+            tiles = load_work(a, item).tiles;
+            tile = 0;
+            if (tiles > 0) return;
+            ++item;
+        }
+    }
+    __device__ __forceinline__ void start(const AttnArgs& a)
+    {
+        item = a.cta_begin[blockIdx.x / 2];
+        end_item = a.cta_begin[blockIdx.x / 2 + 1];
+        index = 0;
+        settle(a);
+    }
+    __device__ __forceinline__ bool done() const { return item >= end_item; }
+    __device__ __forceinline__ void next(const AttnArgs& a)
+    {
+        ++index;
+        ring.advance(kStages);
+        if (++tile == tiles) {
+            ++item;
+            settle(a);
+        }
+    }
+};
+
+__device__ __forceinline__ void issue_mmas(const AttnArgs& a, const TileMaps& maps, Misc* m, uint32_t smem, uint32_t tmem)
+{
+    constexpr uint32_t kDescS = mma_desc(2 * kRows, kAttnKeys, false, false);
+    constexpr uint32_t kDescO = mma_desc(256, 2 * kRows, true, false);
+    constexpr int kAtom = kAtomBytes / 16;
+    const int chunks = maps.whole ? 9 : 8;
+    const uint64_t q_mat = smem_matrix(smem, 16, 1024);
+    const uint64_t k_mat = smem_matrix(smem + kKeyOff, 16, chunks * kAtomBytes);
+    const uint64_t band_mat = smem_matrix(smem + kKeyOff + (maps.whole ? 8 * kAtomBytes : kBandOff), 16,
+                                          (maps.whole ? 9 : 1) * kAtomBytes);
+    const uint64_t v_mat = smem_matrix(smem + kValueOff, kAtomBytes, kValueGroup);
+    const uint64_t p_mat = smem_matrix(smem + kPOff, 16, 1024);
+    auto test = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_cluster(bar, parity)); };
+    TileCursor s, pv;
+    s.start(a);
+    pv.start(a);
+    uint32_t q_phase = 0;
+    uint32_t idle = 0;
+    unsigned long long t0 = 0;
+    while (!pv.done()) {
+        bool moved = false;
+        if (!s.done() && s.index <= pv.index + 1 && test(smem_addr(&m->k_full[s.ring.stage]), s.ring.phase) &&
+            (s.tile > 0 || test(smem_addr(&m->q_full), q_phase))) {
+            tcgen05_after_sync();
+            if (elect_lane()) {
+                const uint32_t d = tmem + kTmemS + (s.index & 1) * 32;
+                const uint32_t at = s.ring.stage * (kKeyBytes / 16);
+#pragma unroll
+                for (int c = 0; c < 9; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        pair_mma_bf16(d, q_mat + (uint64_t)(c * (kChunkBytes / 16) + 2 * k),
+                                      (c < 8 ? k_mat + (uint64_t)(at + c * kAtom + 2 * k) : band_mat + (uint64_t)(at + 2 * k)),
+                                      kDescS, c > 0 || k > 0);
+                pair_commit(smem_addr(&m->s_full[s.index & 1]));
+                pair_commit(smem_addr(&m->k_empty[s.ring.stage]));
+                if (s.tile + 1 == s.tiles) pair_commit(smem_addr(&m->q_empty));
+            }
+            __syncwarp();
+            if (s.tile == 0) q_phase ^= 1;
+            s.next(a);
+            moved = true;
+        }
+        if (pv.index < s.index && test(smem_addr(&m->p_ready[pv.index & 1]), (pv.index >> 1) & 1) &&
+            test(smem_addr(&m->v_full[pv.ring.stage]), pv.ring.phase)) {
+            tcgen05_after_sync();
+            if (elect_lane()) {
+                const uint32_t at = pv.ring.stage * (kValueBytes / 16);
+                const uint64_t p_at = p_mat + (uint64_t)((pv.index & 1) * (kChunkBytes / 16));
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        pair_mma_bf16(tmem + kTmemO + b * 128,
+                                      v_mat + (uint64_t)(at + k * (2 * kValueGroup / 16) + 2 * b * kAtom), p_at + 2 * k, kDescO,
+                                      pv.tile > 0 || k > 0);
+                    pair_commit(smem_addr(&m->v_empty[pv.ring.stage][k]));
+                }
+                pair_commit(smem_addr(&m->pv_done[pv.index & 1]));
+            }
+            __syncwarp();
+            pv.next(a);
+            moved = true;
+        }
+        if (moved) {
+            idle = 0;
+        } else if ((++idle & 1023) == 0) {
+            if (idle == 1024) t0 = global_ns();
+            const bool late = global_ns() - t0 > kWaitLimit;
+            if (late) {
+                *(volatile int*)&m->quit = 1;
+                raise_status(a.status, ST_TIMEOUT);
+            }
+            if (__any_sync(0xffffffffu, late || *(volatile int*)&m->quit)) break;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ softmax --
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// A thread has one query row (TMEM lanes 0..63 and again 64..127) and one half of a tile's columns.  The warps meet at
+// named barriers, so when the CTA gives up they go on without waiting; the status word says the output is not valid.
+__device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t smem, uint32_t tmem, uint32_t rank)
+{
+    const int pair = blockIdx.x / 2;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const int r = 32 * (warp & 1) + lane, half = warp >> 1;
+    const float scale2 = a.scale * kLog2e;
+    const int group = a.q_heads;
+    int index = 0;
+    uint32_t x_phase = 0;
+    for (int i = a.cta_begin[pair]; i < a.cta_begin[pair + 1]; ++i) {
+        const Work w = load_work(a, i);
+        const int rows = min(max(w.it.rows - (int)rank * kRows, 0), kRows);  // of this CTA
+        const int row0 = w.it.row0 + (int)rank * kRows;
+        const long long limit =
+            r < rows ? (a.prefix ? w.ch.start : w.ch.start + (row0 + r) / group + 1) : 0;  // this row's: [0, limit)
+        const long long open = a.prefix ? w.ch.start : w.ch.start + row0 / group + 1;      // every row attends below this
+        float top = -INFINITY, sum = 0.f;
+        bool redo = false;
+        for (int t = 0; t < w.tiles; ++t, ++index) {
+            const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            mbar_wait_cluster(smem_addr(&m->s_full[index & 1]), (index >> 1) & 1, &m->quit, a.status);
+            tcgen05_after_sync();
+            uint32_t v[32];
+            tmem_ld32(tmem + kTmemS + lanes + (index & 1) * 32, v);
+            tmem_wait_ld();
+            float x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * scale2;
+            if (key + kAttnKeys > open || rows < kRows) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (key + 32 * half + k >= limit) x[k] = -INFINITY;
+            }
+            float most = x[0];
+#pragma unroll
+            for (int k = 1; k < 32; ++k) most = fmaxf(most, x[k]);
+            if (t == 0) {
+                m->half[half][r] = most;
+                softmax_sync();
+                top = fmaxf(m->half[0][r], m->half[1][r]);
+            } else {
+                redo |= most > top + kRange;
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float e0 = exp2_approx(x[2 * k] - base), e1 = exp2_approx(x[2 * k + 1] - base);
+                sum += e0 + e1;
+                p[k] = pack_bf16x2(e0, e1);
+            }
+            if (index > 1) mbar_wait_cluster(smem_addr(&m->pv_done[index & 1]), ((index - 2) >> 1) & 1, &m->quit, a.status);
+            const uint32_t at = smem + kPOff + (index & 1) * kChunkBytes + r * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((4 * half + k) ^ (r & 7)) << 4)),
+                             "r"(p[4 * k]), "r"(p[4 * k + 1]), "r"(p[4 * k + 2]), "r"(p[4 * k + 3])
+                             : "memory");
+            fence_async_smem();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->p_ready[index & 1]), 0));
+        }
+        // the rows' sums, and 1 / l of both CTAs' rows in both
+        softmax_sync();  // the maxima have been read
+        m->half[half][r] = sum;
+        if (__any_sync(0xffffffffu, redo) && lane == 0) m->redo = 1;
+        softmax_sync();
+        if (threadIdx.x == 0) {
+            a.redo[2 * i + rank] = m->redo;
+            m->redo = 0;
+        }
+        if (half == 0) {
+            const float l = m->half[0][r] + m->half[1][r];
+            if (r < rows) {
+                const float lse = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+                if (w.it.part >= 0) {
+                    a.part_lse[(long long)w.it.part * kPairRows + rank * kRows + r] = lse;
+                } else if (a.lse) {
+                    const int q = row0 + r;
+                    a.lse[(long long)(w.ch.tok0 + q / group) * a.q_heads + q % group] = lse;
+                }
+            }
+            if (w.tiles > 0) {
+                const float f = l == 0.f ? 0.f : 1.f / l;
+                const uint32_t to = smem_addr(&m->factor[rank * kRows + r]);
+                cluster_store(cluster_addr(to, 0), f);
+                cluster_store(cluster_addr(to, 1), f);
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 0), 1);
+                    cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 1), 1);
+                }
+            }
+        }
+        if (w.tiles > 0) {
+            mbar_wait_cluster(smem_addr(&m->x_ready), x_phase, &m->quit, a.status);
+            x_phase ^= 1;
+            mbar_wait_cluster(smem_addr(&m->pv_done[(index - 1) & 1]), ((index - 1) >> 1) & 1, &m->quit, a.status);
+            tcgen05_after_sync();
+        }
+        for (int b = 0; b < 2; ++b) {
+            const int dim = 256 * b + 128 * (int)rank + 32 * warp + lane;
+            for (int c = 0; c < w.it.rows; c += 16) {
+                uint32_t v[16] = {};
+                if (w.tiles > 0) {
+                    tmem_ld16(tmem + kTmemO + lanes + b * 128 + c, v);
+                    tmem_wait_ld();
+                }
+                for (int k = 0; k < 16; ++k) {
+                    const int q = c + k;
+                    if (q >= w.it.rows) break;
+                    const float o = w.tiles > 0 ? __uint_as_float(v[k]) * m->factor[q] : 0.f;
+                    if (w.it.part >= 0) {
+                        a.part_out[((long long)w.it.part * kPairRows + q) * 512 + dim] = o;
+                    } else {
+                        const long long tok = w.ch.tok0 + (w.it.row0 + q) / group, head = (w.it.row0 + q) % group;
+                        static_cast<__nv_bfloat16*>(
+                            a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + dim] = __float2bfloat16_rn(o);
+                    }
+                }
+            }
+        }
+        tcgen05_before_sync();
+        softmax_sync();  // before the next item's maxima
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_constant__ AttnArgs a,
+                                                               const __grid_constant__ TileMaps maps)
+{
+    extern __shared__ unsigned char raw[];
+    const uint32_t smem = (smem_addr(raw) + 1023) & ~1023u;
+    Misc* m = reinterpret_cast<Misc*>(raw + (smem - smem_addr(raw)) + kMiscOff);
+    const int warp = threadIdx.x / 32;
+    const uint32_t rank = cluster_rank();
+    wait_for_previous_grid();
+    allow_next_grid();
+    if (a.header->pairs == 0) return;  // the plan is for the other kernel (both CTAs see the same)
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_addr(&m->k_full[s]), 2 * kCopyWarps);  // both CTAs' copy warps, or the loaders for as many
+            mbar_init(smem_addr(&m->v_full[s]), 2 * kCopyWarps);
+            mbar_init(smem_addr(&m->k_empty[s]), 1);
+            mbar_init(smem_addr(&m->tail_k[s]), kKeyWarps);
+            mbar_init(smem_addr(&m->tail_v[s]), kSteps);
+            for (int k = 0; k < kSteps; ++k) mbar_init(smem_addr(&m->v_empty[s][k]), 1);
+        }
+        mbar_init(smem_addr(&m->q_full), 2 * kCopyWarps);
+        mbar_init(smem_addr(&m->q_empty), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&m->s_full[b]), 1);
+            mbar_init(smem_addr(&m->p_ready[b]), 2 * kSoftmaxWarps);
+            mbar_init(smem_addr(&m->pv_done[b]), 1);
+        }
+        mbar_init(smem_addr(&m->x_ready), 4);  // the two warps of each CTA that hold the sums
+        mbar_init(smem_addr(&m->drained), 1);
+        m->quit = 0;
+        m->redo = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);
+    tcgen05_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_after_sync();
+    const uint32_t tmem = m->tmem;
+    if (warp < kSoftmaxWarps) {
+        run_softmax(a, m, smem, tmem, rank);
+        tcgen05_before_sync();
+    } else if (warp == kMmaWarp) {
+        if (rank == 0) {
+            issue_mmas(a, maps, m, smem, tmem);
+            // nothing is in flight when TMEM is freed
+            if (elect_lane()) pair_commit(smem_addr(&m->drained));
+            __syncwarp();
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_cluster(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
+            }
+        }
+    } else if (warp < kValueWarp) {
+        if (elect_lane()) load_tiles<false>(a, maps, m, smem, rank, warp - kKeyWarp);
+        __syncwarp();
+    } else if (warp < kCopyWarp) {
+        if (elect_lane()) load_tiles<true>(a, maps, m, smem, rank, warp - kValueWarp);
+        __syncwarp();
+    } else {
+        copy_tiles(a, maps, m, smem, rank);
+        cp_async_wait_all();
+    }
+    __syncthreads();
+    let_loads_land(&m->quit);
+    // neither CTA leaves while the other may still reach its shared memory, or a product its TMEM
+    cluster_sync();
+    if (warp == kMmaWarp) {
+        tcgen05_after_sync();
+        pair_tmem_free(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return (int)cudaErrorNotSupported;
+    uint4* base = static_cast<uint4*>(const_cast<void*>(kv));
+    const int64_t rows = g.num_pages * g.block_size * g.num_layers;
+    const cuuint64_t row = (cuuint64_t)g.lat_row_vecs * 16, n = (cuuint64_t)(rows / 8);
+    const cuuint32_t groups = (cuuint32_t)(maps->box / 8), ones[5] = {1, 1, 1, 1, 1};
+    const cuuint32_t planes = maps->whole ? 9 : 8;
+    // keys: 64 columns, 8 rows of a group, the row's planes, groups
+    const cuuint64_t k_dims[4] = {64, 8, planes, n}, k_strides[3] = {row, 128, 8 * row};
+    const cuuint32_t k_box[4] = {64, 8, planes, groups};
+    // values: 64 columns, 8 rows, planes of a half of the latent, halves, groups; a box takes two planes of both halves
+    const cuuint64_t v_dims[5] = {64, 8, 4, 2, n}, v_strides[4] = {row, 128, 512, 8 * row};
+    const cuuint32_t v_box[5] = {64, 8, 2, 2, groups};
+    if (encode(&maps->pair_keys, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, k_dims, k_strides, k_box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        encode(&maps->pair_values, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, v_dims, v_strides, v_box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return (int)cudaErrorInvalidValue;
+    return (int)cudaFuncSetAttribute(attend_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, void* stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return (int)cudaLaunchKernelEx(&cfg, attend_pair_kernel, a, maps);
+}
+
+}  // namespace leyline

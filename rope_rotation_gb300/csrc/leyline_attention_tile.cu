@@ -13,8 +13,9 @@
 // One persistent CTA per SM takes the contiguous run of items the plan gave it.  Roles:
 //   warps 0-3  softmax: S from TMEM, running maximum and sum (fp32), P to shared memory, output
 //   warp 4     issues the MMAs (one lane)
-//   warp 5     loads cache tiles through the block table (one lane: TMA, 16 or 8 rows of a page at a time)
-//   warps 6-9  copy the queries (cp.async: any strides), the cache tiles that TMA does not take (block
+//   warps 5-8  load cache tiles through the block table, 16 rows of a tile each (TMA, one lane: a thread issues a
+//              TMA instruction in 100 to 170 cycles, whatever its size, and a thread alone bound the kernel)
+//   warps 9-12 copy the queries (cp.async: any strides), the cache tiles that TMA does not take (block
 //              sizes that 8 does not divide; tiles that end inside, whose other rows are zeroed, since
 //              they meet weights of 0 in the product with V), and in a lazy pool turn the bands
 // In a lazy pool the band of each row is turned by its pending count on the way, in fp32, and goes
@@ -29,23 +30,19 @@
 //
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
-#include "leyline_batch.h"
-#include "leyline_tcgen05.cuh"
+#include "leyline_attention.cuh"
 
 namespace leyline {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 constexpr int kSoftmaxWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kLoadWarps = 4;  // one for each of PV's steps
 constexpr int kCopyWarps = 4;
 constexpr int kCopyThreads = 32 * kCopyWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2 + kCopyWarps);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kLoadWarps + kCopyWarps);
 
-constexpr int kAtomBytes = 1024;        // 8 rows x 128 bytes
 constexpr int kRegionChunk = kAttnKeys / 8 * kAtomBytes;  // a chunk of a tile's 64 rows
 constexpr int kSteps = kAttnKeys / 16;  // steps of 16 cache rows, in which PV frees a stage
 constexpr int kMaxStages = 6;
@@ -106,146 +103,65 @@ constexpr uint32_t kTmemO = 0;    // up to 4 blocks of 64 columns
 constexpr uint32_t kTmemS = 256;  // 2 buffers of 64 columns
 
 constexpr float kRaise = 8.f;
-constexpr unsigned long long kDrainTime = 1000000ull;  // 1 ms: longer than any load in flight takes
-
-// The item as every role sees it.
-struct Work {
-    AttnItem it;
-    ChunkDev ch;
-    int tiles;      // cache tiles
-    long long end;  // cache rows [key0, end) are loaded
-};
-
-__device__ __forceinline__ Work load_work(const AttnArgs& a, int i)
-{
-    Work w;
-    w.it = a.items[i];
-    w.ch = a.chunks[w.it.chunk];
-    w.end = min((long long)w.it.key1, a.prefix ? (long long)w.ch.start : (long long)w.it.key1);
-    w.tiles = w.end > w.it.key0 ? (int)((w.end - w.it.key0 + kAttnKeys - 1) / kAttnKeys) : 0;
-    return w;
-}
 
 __device__ __forceinline__ int padded_rows(int rows) { return (rows + 15) & ~15; }
 
-// The stages in turn, and the parity of their current use.
-struct Ring {
-    int stage = 0;
-    uint32_t phase = 0;
-
-    __device__ __forceinline__ void advance(int stages)
-    {
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-};
-
-// False (for the whole warp) when the CTA has given up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Misc* m, int32_t* status)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &m->quit, status));
-}
-
 // -------------------------------------------------------------------- loads --
-// A cache row's page (as the table has it) and its row in the page; nothing is loaded past `end`.
-struct PageOf {
-    int page, off;
-    bool in;
-};
-
-__device__ __forceinline__ PageOf page_of(const AttnArgs& a, const TileMaps& maps, const Work& w, const int32_t* table_row,
-                                          long long pos)
-{
-    const unsigned u = (unsigned)pos, B = (unsigned)a.g.block_size;
-    const unsigned blk = maps.shift >= 0 ? u >> maps.shift : u / B;
-    PageOf p{-1, (int)(u - blk * B), pos < w.end};
-    if (p.in) p.page = table_row[blk];
-    return p;
-}
-
-// Its slot; -1 past the end and for a bad page.
-__device__ __forceinline__ long long slot_of(const AttnArgs& a, const PageOf& p)
-{
-    if (p.page >= 0 && p.page < a.g.num_pages) return (long long)p.page * a.g.block_size + p.off;
-    if (p.in) raise_status(a.status, ST_BAD_PAGE);
-    return -1;
-}
-
-// Whether TMA takes the tile at `key` (its values, in a lazy pool).
-__device__ __forceinline__ bool by_box(const TileMaps& maps, const Work& w, long long key)
-{
-    return maps.box > 0 && key + kAttnKeys <= w.end;
-}
-
-// One lane runs all of it: per tile a wait for each freed step and its boxes, the next tile's table entries
-// in flight meanwhile.
+// One lane of each load warp: the boxes of the 16 rows of PV's step `step`, the next tile's table entries in flight
+// meanwhile.
 template <bool kMla, bool kLazy, int kKeys>
-__device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& maps, const Layout& l, Misc* m, uint32_t smem)
+__device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& maps, const Layout& l, Misc* m, uint32_t smem,
+                                           int step)
 {
     const bool wide = maps.box == 16;
-    const int boxes = wide ? 4 : 8;  // of a tile
+    const int boxes = wide ? 1 : 2;  // of two groups of 8 rows, or one each
     const bool bands = !kLazy && !maps.whole;
-    const uint32_t bytes = (l.row_chunks + (bands ? kKeys : 0)) * kRegionChunk;
+    const uint32_t bytes = (l.row_chunks + (bands ? kKeys : 0)) * (kRegionChunk / kSteps);
     const int layer_groups = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
     Ring ring;
     for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i) {
         const Work w = load_work(a, i);
         const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
         const int value_plane = kMla ? 0 : w.it.band * l.values, key_plane = kMla ? 0 : w.it.band * kKeys;
-        PageOf at[8];
+        PageOf at[2];
         auto look_up = [&](long long key) {
             if (!by_box(maps, w, key)) return;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < boxes) at[k] = page_of(a, maps, w, table_row, key + k * maps.box);
+            for (int k = 0; k < 2; ++k)
+                if (k < boxes) at[k] = page_of(a, maps, w, table_row, key + 16 * step + 8 * k);
         };
         look_up(w.it.key0);
         for (int t = 0; t < w.tiles; ++t) {
             const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            const bool box = by_box(maps, w, key);
+            int y[2] = {-2, -2};  // the boxes as indices of groups of 8 rows; one that is not loaded lies before the first
+            if (box) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (k < boxes) {
+                        const long long slot = slot_of(a, at[k]);
+                        if (slot >= 0) y[k] = layer_groups + (int)(slot >> 3);
+                    }
+            }
+            if (t + 1 < w.tiles) look_up(key + kAttnKeys);
             const uint32_t full = smem_addr(&m->full[ring.stage]);
-            const uint32_t dst = smem + l.stage + ring.stage * l.stage_bytes;
-            if (!by_box(maps, w, key)) {  // the copy warps' tile: only this lane's arrival
-                if (!mbar_wait(smem_addr(&m->empty[ring.stage][kSteps - 1]), ring.phase ^ 1, &m->quit, a.status)) return;
+            if (!mbar_wait(smem_addr(&m->empty[ring.stage][step]), ring.phase ^ 1, &m->quit, a.status)) return;
+            if (!box) {  // the copy warps' tile: only this lane's arrival
                 mbar_arrive(full);
-                look_up(key + kAttnKeys);
                 ring.advance(l.stages);
                 continue;
             }
-            int y[8];  // the boxes as indices of groups of 8 rows; one that is not loaded lies before the first
+            mbar_expect_tx(full, bytes);
+            const uint32_t dst = smem + l.stage + ring.stage * l.stage_bytes;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 2; ++k)
                 if (k < boxes) {
-                    const long long slot = slot_of(a, at[k]);
-                    y[k] = slot >= 0 ? layer_groups + (int)(slot >> 3) : -2;
-                }
-            if (t + 1 < w.tiles) look_up(key + kAttnKeys);
-#pragma unroll
-            for (int step = 0; step < kSteps; ++step) {
-                if (!mbar_wait(smem_addr(&m->empty[ring.stage][step]), ring.phase ^ 1, &m->quit, a.status)) return;
-                if (step == 0) mbar_expect_tx(full, bytes);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {  // a box of two groups, or one of each
-                    if (wide && k == 1) break;
                     const int group = 2 * step + k;
-                    const int at_group = wide ? y[step] : y[group];
-                    tma_box4(dst + group * l.row_chunks * kAtomBytes, &maps.rows, value_plane, at_group, full);
-                    if (bands) tma_box4(dst + l.band + group * kKeys * kAtomBytes, &maps.bands, key_plane, at_group, full);
+                    tma_box4(dst + group * l.row_chunks * kAtomBytes, &maps.rows, value_plane, y[k], full);
+                    if (bands) tma_box4(dst + l.band + group * kKeys * kAtomBytes, &maps.bands, key_plane, y[k], full);
                 }
-            }
             ring.advance(l.stages);
         }
-    }
-}
-
-// Where the CTA gives up, what is still in flight must land before it ends.  A stage's barrier may lack arrivals then,
-// so the loads are waited for by time.
-__device__ __forceinline__ void let_loads_land(Misc* m)
-{
-    if (!*(volatile int*)&m->quit) return;  // every load has been waited for by the MMAs
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < kDrainTime) {
     }
 }
 
@@ -267,7 +183,7 @@ struct Copier {
     int trig_count;  // pending count whose cos / sin this warp's slice holds
     bool trig_valid;
 
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, m, a.status); }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, &m->quit, a.status); }
 
     // This lane's 8 values of each chunk of a row's band, turned by the row's pending count, as hi + lo (all 32
     // lanes; the 8 lanes of a row share `pend`).
@@ -795,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            // the load warp and every copy thread (lazy pools: and again for the turned bands)
-            mbar_init(smem_addr(&m->full[s]), 1 + (kLazy ? 2 : 1) * kCopyThreads);
+            // the load warps and every copy thread (lazy pools: and again for the turned bands)
+            mbar_init(smem_addr(&m->full[s]), kLoadWarps + (kLazy ? 2 : 1) * kCopyThreads);
             for (int k = 0; k < kSteps; ++k) mbar_init(smem_addr(&m->empty[s][k]), 1);
         }
         mbar_init(smem_addr(&m->q_full), kCopyThreads);
@@ -816,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     const uint32_t tmem = m->tmem;
     wait_for_previous_grid();
     allow_next_grid();
-    if (warp < kSoftmaxWarps) {
+    if (a.header->pairs) {  // the plan is for the other kernel
+    } else if (warp < kSoftmaxWarps) {
         run_softmax<kMla>(a, l, m, smem, tmem);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
@@ -827,35 +744,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         const unsigned long long t0 = global_ns();
         while (!mbar_try(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
         }
-    } else if (warp == kLoadWarp) {
-        if (elect_lane()) load_tiles<kMla, kLazy, kKeys>(a, maps, l, m, smem);
+    } else if (warp < kLoadWarp + kLoadWarps) {
+        if (elect_lane()) load_tiles<kMla, kLazy, kKeys>(a, maps, l, m, smem, warp - kLoadWarp);
         __syncwarp();
     } else {
-        const int tid = threadIdx.x - 32 * (kLoadWarp + 1);
+        const int tid = threadIdx.x - 32 * (kLoadWarp + kLoadWarps);
         float2* trig = reinterpret_cast<float2*>(raw + (smem - smem_addr(raw)) + l.trig) + tid / 32 * 32 * kKeys;
         Copier<kMla, kLazy, kKeys> c{a, maps, l, m, smem, trig, tid, tid % 8, tid / 8, 0, false};
         c.run();
         cp_async_wait_all();
     }
     __syncthreads();
-    let_loads_land(m);
+    let_loads_land(&m->quit);
     if (warp == kMmaWarp) {
         tcgen05_after_sync();
         tmem_free(tmem, kTmemCols);
     }
-}
-
-// The driver's encoder of tensor maps, looked up at run time (the library links no driver library).
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-EncodeTiled encode_tiled()
-{
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
 }
 
 // Map of `rows` rows of row_vecs 16-byte vectors at `base`: 64 columns, 8 rows of a group, planes of 64 columns, groups;

@@ -26,6 +26,7 @@ struct leyline_batch {
     int32_t q_heads = 0;
     int32_t value_dim = 0;
     WorkShape shape{};
+    WorkShape pair_shape{};  // ctas 0: the pool's rows are not for pairs
     int64_t max_tiles = 0;
     BatchLayout layout{};
     TileMaps maps{};
@@ -36,6 +37,7 @@ struct leyline_batch {
     double* d_theta = nullptr;
     float* d_part_out = nullptr;
     float* d_part_lse = nullptr;
+    int32_t* d_redo = nullptr;
     // pinned staging, used in turn: the host rewrites a slot once the install that read it is done
     static constexpr int kSlots = 4;
     char* h_stage[kSlots] = {};
@@ -45,6 +47,7 @@ struct leyline_batch {
     bool planned = false;
     int32_t n_tokens = 0;
     int32_t n_joins = 0;
+    bool pairs = false;  // the plan is for pairs
 };
 
 namespace {
@@ -161,6 +164,7 @@ void free_batch(leyline_batch* b)
     if (b->d_theta) cudaFree(b->d_theta);
     if (b->d_part_out) cudaFree(b->d_part_out);
     if (b->d_part_lse) cudaFree(b->d_part_lse);
+    if (b->d_redo) cudaFree(b->d_redo);
     delete b;
 }
 
@@ -211,6 +215,11 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
         if (e == cudaSuccess) e = cudaHostAlloc((void**)&b->h_stage[i], b->stage_bytes, cudaHostAllocDefault);
     }
     if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g, p->kv, &b->maps);
+    if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending && b->maps.box > 0) {
+        b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows};
+        e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
+        if (e == cudaSuccess) e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
+    }
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         free_batch(b);
@@ -247,12 +256,14 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     if (!cp.chunks.empty()) memcpy(h + l.chunks, cp.chunks.data(), sizeof(ChunkDev) * cp.chunks.size());
     Split split{reinterpret_cast<AttnItem*>(h + l.items), reinterpret_cast<int32_t*>(h + l.cta_begin),
                 reinterpret_cast<AttnJoin*>(h + l.joins)};
-    split_work(b->shape, cp.chunks, &split);
+    const bool pairs = b->pair_shape.ctas > 0 && pairs_are_faster(b->shape, cp.chunks);
+    split_work(pairs ? b->pair_shape : b->shape, cp.chunks, &split);
     BatchHeader hd{};
     hd.table = bt->table;
     hd.max_blocks = bt->max_blocks;
     hd.n_tokens = (int32_t)cp.tokens;
     hd.n_joins = split.n_joins;
+    hd.pairs = pairs ? 1 : 0;
     memcpy(h, &hd, sizeof hd);
     if (!cp.runs.empty()) memcpy(h + l.bytes, cp.runs.data(), sizeof(PlanRun) * cp.runs.size());
 
@@ -290,6 +301,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->planned = true;
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
+    b->pairs = pairs;
     return LEYLINE_OK;
 }
 
@@ -447,16 +459,25 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     a.joins = reinterpret_cast<const AttnJoin*>(b->d_plan + b->layout.joins);
     a.part_out = b->d_part_out;
     a.part_lse = b->d_part_lse;
+    a.redo = b->d_redo;
     a.pending = p->d_pending;
     a.turn = p->d_theta_j;
     a.status = p->d_status;
     a.g = g;
-    int err = launch_attention(a, b->maps, b->shape.ctas, stream);
+    // a captured call may be replayed with plans for either kernel: both are launched, and the one the plan is not for
+    // ends at once
+    int err = 0;
+    if (captured || !b->pairs) err = launch_attention(a, b->maps, b->shape.ctas, stream);
+    if (err == 0 && b->pair_shape.ctas > 0 && (captured || b->pairs)) {
+        err = launch_attention_pair(a, b->maps, b->pair_shape.ctas, stream);
+        if (err == 0) err = launch_attention_redo(a, b->pair_shape.ctas, stream);
+    }
     if (err != 0) return cuda_error((cudaError_t)err, "launching the attention kernel");
-    // a captured call may be replayed with plans that split more tiles
+    // and with plans that split more tiles
     const int joins = captured ? b->shape.ctas : b->n_joins;
+    const int rows = captured ? (b->pair_shape.ctas > 0 ? kPairRows : kAttnRows) : b->pairs ? kPairRows : kAttnRows;
     if (joins > 0) {
-        err = launch_join(a, joins, stream);
+        err = launch_join(a, joins, rows, stream);
         if (err != 0) return cuda_error((cudaError_t)err, "launching the join kernel");
     }
     return leave(b, stream, captured);

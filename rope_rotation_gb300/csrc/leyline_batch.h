@@ -19,6 +19,8 @@ namespace leyline {
 constexpr int kAttnRows = 64;  // query rows (token, head) of a row tile
 // Lazy pools of MLA rows: 48, since a turned band takes a chunk more of shared memory.
 constexpr int kAttnRowsLazy = 48;
+// Pairs of CTAs (leyline_attention_pair.cu): 64 of each.
+constexpr int kPairRows = 128;
 constexpr int kAttnKeys = 64;  // cache rows of a key tile
 
 // The plan's header, first in the plan's device buffer.
@@ -27,7 +29,8 @@ struct BatchHeader {
     int32_t max_blocks;
     int32_t n_tokens;
     int32_t n_joins;
-    int32_t pad[3];
+    int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
+    int32_t pad[2];
 };
 
 // One chunk, as attention sees it.
@@ -103,7 +106,7 @@ struct WorkShape {
     int32_t bands;  // key bands attention works on (1: MLA)
     int32_t group;  // query heads per band
     int32_t ctas;
-    int32_t rows;   // query rows of a tile, at most kAttnRows
+    int32_t rows;   // query rows of a tile, at most kAttnRows, by pairs kPairRows (and ctas pairs)
 };
 // Where the split is written: items[row tiles + ctas], cta_begin[ctas + 1], joins[ctas].
 struct Split {
@@ -115,6 +118,7 @@ struct Split {
     int32_t n_parts = 0;
 };
 void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out);
+bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks);
 
 struct HeadsView {
     void* ptr;
@@ -178,8 +182,9 @@ struct AttnArgs {
     const AttnItem* items;
     const int32_t* cta_begin;  // [CTAs + 1]: each CTA's items
     const AttnJoin* joins;
-    float* part_out;       // [parts][kAttnRows][value dim]
-    float* part_lse;       // [parts][kAttnRows], natural log
+    float* part_out;       // [parts][kAttnRows, by pairs kPairRows][value dim]
+    float* part_lse;       // [parts][the same], natural log
+    int32_t* redo;         // by pairs: [items][2], set where the item is to be computed again
     const int32_t* pending;
     const double* turn;    // lazy pools' turn table
     int32_t* status;
@@ -194,6 +199,7 @@ constexpr int kAttnMaxRope = 256;
 // the values (whole MLA rows: with their band), and the bands.
 struct TileMaps {
     CUtensorMap rows, bands;
+    CUtensorMap pair_keys, pair_values;  // leyline_attention_pair.cu
     int box;     // rows of a box, 8 or 16; 0: the block size is no multiple of 8
     int shift;   // log2 of the block size; -1: no power of two
     int values;  // planes of a band's values
@@ -208,10 +214,16 @@ int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* strea
 bool attention_takes_tiles(const Geometry& g);
 int attention_tile_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
+// Attention by pairs of CTAs (leyline_attention_pair.cu), for MLA rows whose tiles come by TMA; after
+// attention_tile_prepare.  redo_attention computes again the items that it marked.
+int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps);
+int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, void* stream);
+int launch_attention_redo(const AttnArgs& a, int pairs, void* stream);
 // Fills *maps for the rows at kv and readies their kernel.
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
-int launch_join(const AttnArgs& a, int joins, void* stream);
+// joins: of tiles of `rows` query rows.
+int launch_join(const AttnArgs& a, int joins, int rows, void* stream);
 
 }  // namespace leyline

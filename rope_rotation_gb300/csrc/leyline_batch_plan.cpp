@@ -108,6 +108,10 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
 // and returns the last CTA's cost.
 constexpr int64_t kTileCost = 2;
 constexpr int64_t kMinKeyTiles = 2;
+
+// Cycles of a cache tile in the two kernels of MLA rows (2 * kPairCycles: a pair holds two SMs).
+constexpr int64_t kTileCycles = 3400;
+constexpr int64_t kPairCycles = 1800;
 static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks, int64_t quota, Split* out)
 {
     int64_t used = 0;  // of the current CTA's quota
@@ -180,6 +184,18 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
         *out = empty;
         quota += std::max<int64_t>(1, quota / 64);
     }
+}
+
+// Whether the work goes to pairs of CTAs: by the tiles that either kernel would take, times what a tile takes it.
+bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks)
+{
+    int64_t single = 0, pair = 0;
+    for (const ChunkDev& c : chunks) {
+        const int64_t rows = (int64_t)c.n * w.group, tiles = ceil_div(c.start + c.n, kAttnKeys);
+        single += ceil_div(rows, kAttnRows) * tiles;
+        pair += ceil_div(rows, kPairRows) * tiles;
+    }
+    return single * kTileCycles > pair * 2 * kPairCycles;
 }
 
 }  // namespace leyline

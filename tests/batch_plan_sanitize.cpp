@@ -144,7 +144,8 @@ int main(int argc, char** argv)
                   "stored length");
 
         WorkShape w{(int32_t)uniform(1, 4), (int32_t)uniform(1, 64), (int32_t)(chance(50) ? 152 : uniform(1, 200)),
-                    chance(70) ? kAttnRows : kAttnRowsLazy};
+                    chance(50) ? kAttnRows : chance(50) ? kAttnRowsLazy : kPairRows};
+        (void)pairs_are_faster(w, plan.chunks);
         int64_t tiles = 0, work = 0;
         for (const ChunkDev& c : plan.chunks) tiles += w.bands * ceil_div((int64_t)c.n * w.group, w.rows);
         // exact sizes, so that the sanitizer sees any entry too many
