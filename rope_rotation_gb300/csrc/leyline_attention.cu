@@ -229,20 +229,26 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
 
 // -------------------------------------------------------------------- join --
 // Partial results k of a row: out = sum w_k out_k / sum w_k with w_k = exp(lse_k - max),
-// lse = max + ln sum w_k.  A warp per query row and 128 value dimensions, with no barrier: its lanes form the
-// weights of 32 parts at a time, then read the parts with nothing between the loads (a row split over 128
-// CTAs took 73 us with one dependent load after another; a CTA per row with the weights in shared memory, 67
-// against 18 us on 9,280 rows of two or three parts).  The parts are added in order, so the result does not
-// depend on which CTA finished first.
+// lse = max + ln sum w_k.  A warp per query row and 128 value dimensions: its lanes form the weights of 32 parts at a
+// time, then read the parts eight loads at a time (a row split over 128 CTAs took 73 us with one dependent load after
+// another).  Where a plan splits tiles into many parts, kSplit = 4 warps share a row's: 12 -> 6 us for that row; with
+// two or three parts a row the other three would have nothing to do.  The parts are added in a fixed order, so
+// the result does not depend on which CTA finished first.
 constexpr int kJoinThreads = 128;
 
+template <int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int slices, int rows)
 {
+    __shared__ float4 sum_s[kJoinThreads];
+    __shared__ float total_s[kJoinThreads / 32];
     wait_for_previous_grid();
     // the next kernel is not let in early: its CTAs, one per SM, would crowd onto the SMs that are free first
-    const long long unit = blockIdx.x * (long long)(kJoinThreads / 32) + threadIdx.x / 32;
+    constexpr int kUnits = kJoinThreads / 32 / kSplit;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = warp % kSplit;
+    const long long unit = blockIdx.x * (long long)kUnits + warp / kSplit;
     const int slice = (int)(unit % slices);
     const int j = (int)(unit / slices / rows), r = (int)(unit / slices % rows);
+    // (with kSplit > 1 a CTA has one unit, so it leaves as a whole)
     if (j >= a.header->n_joins) return;
     const AttnJoin jn = a.joins[j];
     if (r >= jn.rows) return;
@@ -251,7 +257,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const bool mla = g.rope_heads <= 1;
     const int group = a.q_heads / (mla ? 1 : g.rope_heads);
     const int vdim = g.latent_dim / (mla ? 1 : g.rope_heads);
-    const int lane = threadIdx.x & 31;
     const float* lse = a.part_lse + (long long)jn.part0 * pitch + r;
     float top = -INFINITY;
     for (int k = lane; k < jn.parts; k += 32) top = fmaxf(top, lse[(long long)k * pitch]);
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const float* part = a.part_out + ((long long)jn.part0 * pitch + r) * vdim + (on ? d : 0);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
-    for (int k0 = 0; k0 < jn.parts; k0 += 32) {
+    for (int k0 = 32 * sub; k0 < jn.parts; k0 += 32 * kSplit) {
         const int n = min(32, jn.parts - k0);
         const float x = lane < n ? lse[(long long)(k0 + lane) * pitch] : -INFINITY;
         const float mine = x == -INFINITY ? 0.f : exp2f((x - top) * kLog2e);
@@ -283,6 +288,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
     }
     for (int m = 16; m > 0; m /= 2) total += __shfl_xor_sync(0xffffffffu, total, m);
+    if (kSplit > 1) {
+        sum_s[threadIdx.x] = o;
+        if (lane == 0) total_s[warp] = total;
+        __syncthreads();
+        if (sub != 0) return;
+        for (int k = 1; k < kSplit; ++k) {
+            const float4 v = sum_s[threadIdx.x + 32 * k];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+            total += total_s[warp + k];
+        }
+    }
     const float inv = total > 0.f ? 1.f / total : total;
     const ChunkDev ch = a.chunks[jn.chunk];
     const int row = jn.row0 + r;
@@ -322,12 +341,14 @@ int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* st
                                       (cudaStream_t)stream, a);
 }
 
-int launch_join(const AttnArgs& a, int joins, int rows, void* stream)
+int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream)
 {
     const int vdim = a.g.latent_dim / std::max(a.g.rope_heads, 1);
     const int slices = (vdim + 127) / 128;
-    const int grid = (int)(((long long)joins * rows * slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    return (int)launch_dependent(join_kernel, grid, kJoinThreads, (cudaStream_t)stream, a, slices, rows);
+    const long long units = (long long)joins * rows * slices;
+    cudaStream_t s = (cudaStream_t)stream;
+    return (int)(many_parts ? launch_dependent(join_kernel<4>, (int)units, kJoinThreads, s, a, slices, rows)
+                            : launch_dependent(join_kernel<1>, (int)((units + 3) / 4), kJoinThreads, s, a, slices, rows));
 }
 
 }  // namespace leyline

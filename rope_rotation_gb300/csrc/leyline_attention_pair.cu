@@ -31,6 +31,7 @@ constexpr int kRows = 64;               // query rows of a CTA
 constexpr int kHalfKeys = kAttnKeys / 2;  // cache rows whose keys a CTA holds
 constexpr int kStages = 2;
 constexpr int kSteps = kAttnKeys / 16;
+constexpr int kScores = 4;              // S buffers: S runs up to that many tiles ahead of O
 constexpr int kChunkBytes = kRows * 128;  // queries: 9 chunks
 constexpr int kKeyBytes = kHalfKeys / 8 * 9 * kAtomBytes;      // whole rows: [group][9 chunks]; else 8, and the band's region
 constexpr int kBandOff = kHalfKeys / 8 * 8 * kAtomBytes;
@@ -48,7 +49,7 @@ struct Misc {
     unsigned long long q_full;                            // (first)
     unsigned long long q_empty;
     unsigned long long tail_k[kStages], tail_v[kStages];  // the stage is free for a tile that ends inside
-    unsigned long long s_full[2];
+    unsigned long long s_full[kScores];
     unsigned long long p_ready[2];                        // (first)
     unsigned long long pv_done[2];
     unsigned long long x_ready;                           // both CTAs' factors are there
@@ -64,7 +65,7 @@ static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;    // 2 blocks of 128 columns: 128 of the CTA's dimensions x both CTAs' rows
-constexpr uint32_t kTmemS = 256;  // 2 buffers of 32 columns
+constexpr uint32_t kTmemS = 256;  // kScores buffers of 32 columns
 
 constexpr float kRange = 80.f;
 
@@ -274,11 +275,11 @@ __device__ __forceinline__ void issue_mmas(const AttnArgs& a, const TileMaps& ma
     unsigned long long t0 = 0;
     while (!pv.done()) {
         bool moved = false;
-        if (!s.done() && s.index <= pv.index + 1 && test(smem_addr(&m->k_full[s.ring.stage]), s.ring.phase) &&
+        if (!s.done() && s.index < pv.index + kScores && test(smem_addr(&m->k_full[s.ring.stage]), s.ring.phase) &&
             (s.tile > 0 || test(smem_addr(&m->q_full), q_phase))) {
             tcgen05_after_sync();
             if (elect_lane()) {
-                const uint32_t d = tmem + kTmemS + (s.index & 1) * 32;
+                const uint32_t d = tmem + kTmemS + (s.index % kScores) * 32;
                 const uint32_t at = s.ring.stage * (kKeyBytes / 16);
 #pragma unroll
                 for (int c = 0; c < 9; ++c)
@@ -287,7 +288,7 @@ __device__ __forceinline__ void issue_mmas(const AttnArgs& a, const TileMaps& ma
                         pair_mma_bf16(d, q_mat + (uint64_t)(c * (kChunkBytes / 16) + 2 * k),
                                       (c < 8 ? k_mat + (uint64_t)(at + c * kAtom + 2 * k) : band_mat + (uint64_t)(at + 2 * k)),
                                       kDescS, c > 0 || k > 0);
-                pair_commit(smem_addr(&m->s_full[s.index & 1]));
+                pair_commit(smem_addr(&m->s_full[s.index % kScores]));
                 pair_commit(smem_addr(&m->k_empty[s.ring.stage]));
                 if (s.tile + 1 == s.tiles) pair_commit(smem_addr(&m->q_empty));
             }
@@ -357,10 +358,10 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
         bool redo = false;
         for (int t = 0; t < w.tiles; ++t, ++index) {
             const long long key = w.it.key0 + (long long)t * kAttnKeys;
-            mbar_wait_cluster(smem_addr(&m->s_full[index & 1]), (index >> 1) & 1, &m->quit, a.status);
+            mbar_wait(smem_addr(&m->s_full[index % kScores]), (index / kScores) & 1, &m->quit, a.status);
             tcgen05_after_sync();
             uint32_t v[32];
-            tmem_ld32(tmem + kTmemS + lanes + (index & 1) * 32, v);
+            tmem_ld32(tmem + kTmemS + lanes + (index % kScores) * 32, v);
             tmem_wait_ld();
             float x[32];
 #pragma unroll
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
     const int warp = threadIdx.x / 32;
     const uint32_t rank = cluster_rank();
     wait_for_previous_grid();
-    allow_next_grid();
+    // (the next kernel is let in by this one's end: let in before, the join's waiting CTAs cost 15 us of a call of 26)
     if (a.header->pairs == 0) return;  // the plan is for the other kernel (both CTAs see the same)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -488,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
         }
         mbar_init(smem_addr(&m->q_full), 2 * kCopyWarps);
         mbar_init(smem_addr(&m->q_empty), 1);
+        for (int b = 0; b < kScores; ++b) mbar_init(smem_addr(&m->s_full[b]), 1);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&m->s_full[b]), 1);
             mbar_init(smem_addr(&m->p_ready[b]), 2 * kSoftmaxWarps);
             mbar_init(smem_addr(&m->pv_done[b]), 1);
         }

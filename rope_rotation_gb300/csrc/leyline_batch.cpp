@@ -48,6 +48,7 @@ struct leyline_batch {
     int32_t n_tokens = 0;
     int32_t n_joins = 0;
     bool pairs = false;  // the plan is for pairs
+    bool many_parts = false;  // it splits a tile into more than kFewParts
 };
 
 namespace {
@@ -302,6 +303,8 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
+    b->many_parts = false;
+    for (int32_t j = 0; j < split.n_joins; ++j) b->many_parts |= split.joins[j].parts > kFewParts;
     return LEYLINE_OK;
 }
 
@@ -477,7 +480,7 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     const int joins = captured ? b->shape.ctas : b->n_joins;
     const int rows = captured ? (b->pair_shape.ctas > 0 ? kPairRows : kAttnRows) : b->pairs ? kPairRows : kAttnRows;
     if (joins > 0) {
-        err = launch_join(a, joins, rows, stream);
+        err = launch_join(a, joins, rows, captured || b->many_parts, stream);
         if (err != 0) return cuda_error((cudaError_t)err, "launching the join kernel");
     }
     return leave(b, stream, captured);

@@ -223,7 +223,8 @@ int launch_attention_redo(const AttnArgs& a, int pairs, void* stream);
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
-// joins: of tiles of `rows` query rows.
-int launch_join(const AttnArgs& a, int joins, int rows, void* stream);
+// joins: of tiles of `rows` query rows; many_parts: some of them of more than kFewParts.
+constexpr int kFewParts = 16;
+int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream);
 
 }  // namespace leyline
