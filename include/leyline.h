@@ -405,7 +405,8 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * request's length are written again (the rows of an R just spliced in); rows
  * from it on extend the request, and the plan takes their pages off the free
  * list, installs them in the table and advances the length.  The rows of a chunk
- * hold nothing defined from the plan on until every layer has been appended.
+ * hold nothing defined from the plan on until every layer has been appended.  A plan
+ * holds until a splice, a rollback or a freed page changes one of its requests.
  * rope_start is the rotary position of the chunk's first token: start, unless
  * EVICT directives left the request's survivors at other positions.
  *
@@ -503,13 +504,16 @@ int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyli
  * In a LAZY pool each key band is turned by its row's pending count, as
  * leyline_gather turns it but for the rounding: the scores take the turned band
  * to 2^-17 of its size (LEYLINE_ROTATE_BF16_NAIVE: as gathered).  lse (fp32 [tokens][q_heads], contiguous) may be NULL.
- * A token without rows (PREFIX, start 0) gets zeros and lse -inf.  Rows past the last
- * one that a token of the chunk attends to are not read, whatever they hold; a value
- * that is not finite in one of the chunk's own rows reaches its earlier tokens too.
+ * A token without rows (PREFIX, start 0) gets zeros and lse -inf.  Rows that a token
+ * does not attend to do not reach its output, whatever they hold.  out may not
+ * overlap the queries.
  * Scores and sums are fp32; the weights exp(x - max) are rounded to bf16 for
- * the product with the values.  Enqueues one kernel, and a second one that joins the
- * partial results of split row tiles.  Two calls on the same inputs and plan give
- * the same bits.
+ * the product with the values (values above 2^100 may take its fp32 sums to infinity
+ * in chunks of one token).  Enqueues one kernel; for chunks of several tokens a
+ * second one that computes row tiles again whose output is not finite, or whose
+ * scores rise by more than 55 over those of the tile's first 64 rows (a slow path);
+ * and one that joins the partial results of split row tiles.  Two calls on the same
+ * inputs and plan give the same bits.
  * Errors: INVALID_ARG, CUDA. */
 #define LEYLINE_ATTENTION_PREFIX 1
 int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads_t* q_latent,

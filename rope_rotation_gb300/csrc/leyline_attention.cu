@@ -3,7 +3,7 @@
 //
 // Per query row (token, head), with x_s = scale * <q, k_s> over the rows s it attends to:
 //   m = max x_s,  l = sum exp(x_s - m),  out = sum exp(x_s - m) v_s / l,  lse = m + ln l.
-// One pass over the rows keeps m, l and the unscaled output, multiplying l and the output by
+// One pass over the rows keeps m, l and the output, multiplying l and the output by
 // exp(m_old - m_new) when a tile raises m.
 #include "leyline_batch.h"
 #include "leyline_device.cuh"
@@ -31,7 +31,8 @@ __device__ __forceinline__ long long row_slot(const int32_t* table_row, const Ge
 
 // ------------------------------------------------------------- any row shape --
 // A CTA takes its items' query rows 16 at a time and the cache rows 16 at a time through
-// shared memory; one thread per (query row, cache row) score, the output in shared memory.
+// shared memory; one thread per (query row, cache row) score, the output in shared memory.  The output is kept as the
+// mean by the weights so far, which is finite wherever the values are.
 constexpr int kAnyThreads = 256;
 constexpr int kAnyTile = 16;
 
@@ -58,7 +59,9 @@ __host__ __device__ inline AnyShape any_shape(const Geometry& g)
     return s;
 }
 
-// kRedo: only the items that the pair kernel marked, whose tiles have kPairRows query rows.
+// kRedo: only the items that a tensor-core kernel marked.  It marks those whose output is not finite, since a weight of
+// 0 does not keep an infinity or a NaN of a masked row out of a matrix product, and (by pairs) those whose scores left
+// its range.  Here a weight of 0 leaves its row out.
 template <bool kRedo>
 __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_constant__ AttnArgs a)
 {
@@ -80,9 +83,11 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
     const float scale2 = a.scale * kLog2e;
     wait_for_previous_grid();
     allow_next_grid();
-    if (kRedo && a.header->pairs == 0) return;
-    constexpr int kPitch = kRedo ? kPairRows : kAttnRows;
-    for (int it = a.cta_begin[blockIdx.x]; it < a.cta_begin[blockIdx.x + 1]; ++it) {
+    const int pitch = a.header->pairs ? kPairRows : kAttnRows;
+    // the CTA's items of the plan, or all items in turn
+    const int it0 = kRedo ? blockIdx.x : a.cta_begin[blockIdx.x];
+    const int it1 = kRedo ? a.header->n_items : a.cta_begin[blockIdx.x + 1];
+    for (int it = it0; it < it1; it += kRedo ? gridDim.x : 1) {
         if (kRedo && a.redo[2 * it] == 0 && a.redo[2 * it + 1] == 0) continue;
         const AttnItem item = a.items[it];
         const ChunkDev ch = a.chunks[item.chunk];
@@ -177,13 +182,14 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                 const float p = x == -INFINITY ? 0.f : exp2f(x - m_new);  // a NaN score stays NaN
                 float sum = p;
                 for (int m = kAnyTile / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                p_s[qi][ki] = p;
+                const float l_old = m_new == -INFINITY ? 0.f : l_s[qi] * exp2f(m_old - m_new);
+                const float l_new = l_old + sum;
+                p_s[qi][ki] = l_new == 0.f ? 0.f : p / l_new;
                 __syncwarp();
                 if (ki == 0) {
-                    const float corr = m_new == -INFINITY ? 1.f : exp2f(m_old - m_new);
-                    corr_s[qi] = corr;
+                    corr_s[qi] = l_new == 0.f ? 0.f : l_old / l_new;
                     m_s[qi] = m_new;
-                    l_s[qi] = l_s[qi] * corr + sum;
+                    l_s[qi] = l_new;
                 }
                 __syncthreads();
                 const __nv_bfloat16* val = reinterpret_cast<const __nv_bfloat16*>(kv_s);
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                     for (int r = 0; r < rows; ++r) {
                         float o = o_s[r * vdim + d] * corr_s[r];
 #pragma unroll
-                        for (int k = 0; k < kAnyTile; ++k) o = fmaf(p_s[r][k], v[k], o);
+                        for (int k = 0; k < kAnyTile; ++k) o = p_s[r][k] == 0.f ? o : fmaf(p_s[r][k], v[k], o);
                         o_s[r * vdim + d] = o;
                     }
                 }
@@ -202,11 +208,10 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
             __syncthreads();
             for (int i = tid; i < rows * vdim; i += kAnyThreads) {
                 const int r = i / vdim, d = i - r * vdim;
-                const float l = l_s[r];
-                const float o = l > 0.f ? o_s[i] / l : (l == 0.f ? 0.f : l);
+                const float o = o_s[i];
                 const int row = item.row0 + r0 + r;
                 if (item.part >= 0) {
-                    a.part_out[((long long)item.part * kPitch + r0 + r) * vdim + d] = o;
+                    a.part_out[((long long)item.part * pitch + r0 + r) * vdim + d] = o;
                 } else {
                     const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
                     static_cast<__nv_bfloat16*>(a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + d] =
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
                 const int row = item.row0 + r0 + tid;
                 const float lse = l_s[tid] == 0.f ? -INFINITY : (m_s[tid] + log2f(l_s[tid])) * kLn2;
                 if (item.part >= 0) {
-                    a.part_lse[(long long)item.part * kPitch + r0 + tid] = lse;
+                    a.part_lse[(long long)item.part * pitch + r0 + tid] = lse;
                 } else if (a.lse) {
                     const long long tok = ch.tok0 + row / group, head = item.band * group + row % group;
                     a.lse[tok * a.q_heads + head] = lse;
@@ -328,9 +333,9 @@ int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps)
                                      (int)any_shape(g).bytes);
 }
 
-int launch_attention_redo(const AttnArgs& a, int pairs, void* stream)
+int launch_attention_redo(const AttnArgs& a, int ctas, void* stream)
 {
-    return (int)launch_dependent_smem(attend_any_kernel<true>, pairs, kAnyThreads, any_shape(a.g).bytes,
+    return (int)launch_dependent_smem(attend_any_kernel<true>, ctas, kAnyThreads, any_shape(a.g).bytes,
                                       (cudaStream_t)stream, a);
 }
 

@@ -92,6 +92,23 @@ __device__ __forceinline__ void let_loads_land(int* quit)
     }
 }
 
+// Named barriers of the four softmax warps.
+__device__ __forceinline__ bool any_of_softmax(bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
 // The driver's encoder of tensor maps, looked up at run time (the library links no driver library).
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 

@@ -10,9 +10,10 @@
 // next but one tile as soon as S is done, before the softmax.
 //
 // The reference maximum of a row is that of its item's first tile and stays: weights are exp2(x - m0), in bf16 and
-// fp32 as exact relative to their size as any.  A later score above m0 by more than 2^80 could leave fp32's range
-// in the sums; the item is then marked, and a kernel that follows computes it again (leyline_attention.cu).  So O
-// never has to be rescaled, which would take both CTAs to agree in the middle of every tile.
+// fp32 as exact relative to their size as any.  A later score above m0 by more than 80 (as a power of 2) could leave
+// fp32's range in the sums; the item is then marked, as is one whose output is not finite, and a kernel that follows
+// computes it again (leyline_attention.cu).  So O never has to be rescaled, which would take both CTAs to agree in the
+// middle of every tile.
 //
 // Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
 // K and 7-10 V (TMA, one lane each: a thread issues a TMA instruction in 100 to 170 cycles, whatever its size, and a
@@ -56,7 +57,6 @@ struct Misc {
     unsigned long long drained;
     uint32_t tmem;
     int quit;
-    int redo;                    // a score left the range of its row's reference
     float half[2][kRows];        // a row's maximum, then sum, over either half of a tile's columns
     float factor[2 * kRows];     // 1 / l of both CTAs' rows
 };
@@ -333,7 +333,6 @@ __device__ __forceinline__ void issue_mmas(const AttnArgs& a, const TileMaps& ma
 }
 
 // ------------------------------------------------------------------ softmax --
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
 // A thread has one query row (TMEM lanes 0..63 and again 64..127) and one half of a tile's columns.  The warps meet at
 // named barriers, so when the CTA gives up they go on without waiting; the status word says the output is not valid.
@@ -404,12 +403,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
         // the rows' sums, and 1 / l of both CTAs' rows in both
         softmax_sync();  // the maxima have been read
         m->half[half][r] = sum;
-        if (__any_sync(0xffffffffu, redo) && lane == 0) m->redo = 1;
         softmax_sync();
-        if (threadIdx.x == 0) {
-            a.redo[2 * i + rank] = m->redo;
-            m->redo = 0;
-        }
         if (half == 0) {
             const float l = m->half[0][r] + m->half[1][r];
             if (r < rows) {
@@ -452,6 +446,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
                     const int q = c + k;
                     if (q >= w.it.rows) break;
                     const float o = w.tiles > 0 ? __uint_as_float(v[k]) * m->factor[q] : 0.f;
+                    redo |= !isfinite(o);
                     if (w.it.part >= 0) {
                         a.part_out[((long long)w.it.part * kPairRows + q) * 512 + dim] = o;
                     } else {
@@ -463,7 +458,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             }
         }
         tcgen05_before_sync();
-        softmax_sync();  // before the next item's maxima
+        redo = any_of_softmax(redo);  // and before the next item's maxima
+        if (threadIdx.x == 0) a.redo[2 * i + rank] = redo;
     }
 }
 
@@ -497,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
         mbar_init(smem_addr(&m->x_ready), 4);  // the two warps of each CTA that hold the sums
         mbar_init(smem_addr(&m->drained), 1);
         m->quit = 0;
-        m->redo = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);

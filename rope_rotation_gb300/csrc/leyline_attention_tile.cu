@@ -30,6 +30,8 @@
 //
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
+// An output that is not finite marks its item, which a kernel that follows computes again: a weight of 0 keeps a masked
+// row's infinity or NaN out of the sum there, not in a matrix product.
 #include "leyline_attention.cuh"
 
 namespace leyline {
@@ -506,22 +508,6 @@ __device__ __forceinline__ void issue_mmas(const AttnArgs& a, const TileMaps& ma
 }
 
 // ------------------------------------------------------------------ softmax --
-__device__ __forceinline__ bool any_of_softmax(bool x)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x)
-        : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
 __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -671,6 +657,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
             mbar_wait(smem_addr(&m->pv_done), (index - 1) & 1, &m->quit, a.status);
             tcgen05_after_sync();
         }
+        bool redo = false;
         for (int b = 0; b < blocks; ++b)
             for (int c = 0; c < n; c += 16) {
                 uint32_t v[16] = {};
@@ -684,6 +671,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                     const int r = c + k;
                     if (r >= w.it.rows) break;
                     const float o = __uint_as_float(v[k]) * m->factor[r];
+                    redo |= !isfinite(o);
                     if (w.it.part >= 0) {
                         a.part_out[((long long)w.it.part * kAttnRows + r) * vdim + dim] = o;
                     } else {
@@ -695,7 +683,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                 }
             }
         tcgen05_before_sync();
-        softmax_sync();  // before the next item's factors
+        redo = any_of_softmax(redo);  // and before the next item's factors
+        if (threadIdx.x == 0) *reinterpret_cast<int2*>(a.redo + 2 * i) = make_int2(redo, 0);
     }
 }
 

@@ -49,6 +49,7 @@ struct leyline_batch {
     int32_t n_joins = 0;
     bool pairs = false;  // the plan is for pairs
     bool many_parts = false;  // it splits a tile into more than kFewParts
+    bool masks = false;       // it has chunks of several tokens
 };
 
 namespace {
@@ -106,13 +107,13 @@ int check_norm(const void** w, int device, const char* what)
     return rc;
 }
 
-// Head axes written to must hold distinct places.
-int check_written(const HeadsView& v, int64_t heads, int64_t dim, const char* what)
+// Head axes written to must hold distinct places, for the plan's tokens.
+int check_written(const HeadsView& v, int64_t tokens, int64_t heads, int64_t dim, const char* what)
 {
     char msg[128];
     const int64_t lo = std::min(v.token_stride, v.head_stride), hi = std::max(v.token_stride, v.head_stride);
-    const bool head_inner = v.head_stride <= v.token_stride;
-    if ((heads > 1 && (lo < dim || (head_inner && hi < heads * lo))) || (heads == 1 && v.token_stride < dim)) {
+    const int64_t inner = v.head_stride <= v.token_stride ? heads : tokens;
+    if ((heads > 1 && (lo < dim || hi < inner * lo)) || (heads == 1 && v.token_stride < dim)) {
         snprintf(msg, sizeof msg, "%s: its strides let heads or tokens overlap", what);
         return bad(msg);
     }
@@ -216,10 +217,11 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
         if (e == cudaSuccess) e = cudaHostAlloc((void**)&b->h_stage[i], b->stage_bytes, cudaHostAllocDefault);
     }
     if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g, p->kv, &b->maps);
+    if (e == cudaSuccess && attention_takes_tiles(g))
+        e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
     if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending && b->maps.box > 0) {
         b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows};
         e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
-        if (e == cudaSuccess) e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
     }
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
@@ -265,6 +267,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     hd.n_tokens = (int32_t)cp.tokens;
     hd.n_joins = split.n_joins;
     hd.pairs = pairs ? 1 : 0;
+    hd.n_items = split.n_items;
     memcpy(h, &hd, sizeof hd);
     if (!cp.runs.empty()) memcpy(h + l.bytes, cp.runs.data(), sizeof(PlanRun) * cp.runs.size());
 
@@ -303,7 +306,8 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
-    b->many_parts = false;
+    b->many_parts = b->masks = false;
+    for (const ChunkDev& c : cp.chunks) b->masks |= c.n > 1;
     for (int32_t j = 0; j < split.n_joins; ++j) b->many_parts |= split.joins[j].parts > kFewParts;
     return LEYLINE_OK;
 }
@@ -355,18 +359,19 @@ int leyline_append(leyline_batch_t* b, int32_t layer, const void* rows, int64_t 
     if (row_stride % 8 != 0 || row_stride < g.row_elems) return bad("row_stride must be a multiple of 8, at least a row");
     if (latent_norm && g.rope_heads > 1) return bad("latent_norm is for rows with one band (MLA)");
     if (!(eps >= 0.f)) return bad("eps must not be negative");
-    if (!rows || (reinterpret_cast<uintptr_t>(rows) & 15) != 0) return bad("rows must be a 16-byte aligned pointer");
     cudaStream_t stream = (cudaStream_t)stream_v;
     DeviceGuard guard(p->device);
     if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
     bool host = false, captured = false;
     void* alias = nullptr;
-    int rc = resolve_access(rows, p->device, "rows", &alias, &host);
-    if (rc == LEYLINE_OK) rc = check_norm(&latent_norm, p->device, "latent_norm");
-    if (rc == LEYLINE_OK) rc = check_norm(&key_norm, p->device, "key_norm");
-    if (rc == LEYLINE_OK) rc = enter(b, stream, &captured);
+    int rc = enter(b, stream, &captured);
     if (rc != LEYLINE_OK) return rc;
     if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
+    if (!rows || (reinterpret_cast<uintptr_t>(rows) & 15) != 0) return bad("rows must be a 16-byte aligned pointer");
+    rc = resolve_access(rows, p->device, "rows", &alias, &host);
+    if (rc == LEYLINE_OK) rc = check_norm(&latent_norm, p->device, "latent_norm");
+    if (rc == LEYLINE_OK) rc = check_norm(&key_norm, p->device, "key_norm");
+    if (rc != LEYLINE_OK) return rc;
     AppendArgs a{};
     a.kv = static_cast<uint4*>(p->kv);
     a.rows = static_cast<const uint4*>(alias);
@@ -398,16 +403,17 @@ int leyline_rotate(leyline_batch_t* b, const leyline_heads_t* q, const leyline_h
     if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
     RotateArgs a{};
     bool captured = false;
-    int rc = check_heads(q, p->device, "q", &a.q);
+    int rc = enter(b, stream, &captured);
+    if (rc != LEYLINE_OK) return rc;
+    if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
+    rc = check_heads(q, p->device, "q", &a.q);
     if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
-    if (rc == LEYLINE_OK) rc = check_written(a.out, b->q_heads, p->g.rope_dim, "out");
+    if (rc == LEYLINE_OK) rc = check_written(a.out, b->n_tokens, b->q_heads, p->g.rope_dim, "out");
     if (rc == LEYLINE_OK && q->ptr == out->ptr &&
         (q->token_stride != out->token_stride || q->head_stride != out->head_stride))
         rc = bad("q and out start at one address with different strides");
     if (rc == LEYLINE_OK) rc = check_norm(&norm, p->device, "norm");
-    if (rc == LEYLINE_OK) rc = enter(b, stream, &captured);
     if (rc != LEYLINE_OK) return rc;
-    if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
     a.norm = static_cast<const uint4*>(norm);
     a.eps = eps;
     a.q_heads = b->q_heads;
@@ -440,15 +446,18 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
     AttnArgs a{};
     bool captured = false, host = false;
-    int rc = check_heads(q_rope, p->device, "q_rope", &a.q_rope);
-    if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
-    if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
-    if (rc == LEYLINE_OK) rc = check_written(a.out, b->q_heads, b->value_dim, "out");
-    void* lse_alias = lse;
-    if (rc == LEYLINE_OK && lse) rc = resolve_access(lse, p->device, "lse", &lse_alias, &host);
-    if (rc == LEYLINE_OK) rc = enter(b, stream, &captured);
+    int rc = enter(b, stream, &captured);
     if (rc != LEYLINE_OK) return rc;
     if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
+    rc = check_heads(q_rope, p->device, "q_rope", &a.q_rope);
+    if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
+    if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
+    if (rc == LEYLINE_OK) rc = check_written(a.out, b->n_tokens, b->q_heads, b->value_dim, "out");
+    // (an item may be computed again from its queries)
+    if (rc == LEYLINE_OK && (a.out.ptr == a.q_rope.ptr || a.out.ptr == a.q_latent.ptr)) rc = bad("out must not lie over the queries");
+    void* lse_alias = lse;
+    if (rc == LEYLINE_OK && lse) rc = resolve_access(lse, p->device, "lse", &lse_alias, &host);
+    if (rc != LEYLINE_OK) return rc;
     a.kv = static_cast<const uint4*>(p->kv);
     a.lse = static_cast<float*>(lse_alias);
     a.scale = scale;
@@ -471,10 +480,11 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     // ends at once
     int err = 0;
     if (captured || !b->pairs) err = launch_attention(a, b->maps, b->shape.ctas, stream);
-    if (err == 0 && b->pair_shape.ctas > 0 && (captured || b->pairs)) {
+    if (err == 0 && b->pair_shape.ctas > 0 && (captured || b->pairs))
         err = launch_attention_pair(a, b->maps, b->pair_shape.ctas, stream);
-        if (err == 0) err = launch_attention_redo(a, b->pair_shape.ctas, stream);
-    }
+    // the tokens of a decode batch's chunks attend to all that is loaded for them: nothing is masked
+    if (err == 0 && b->d_redo && (captured || b->pairs || (b->masks && !a.prefix)))
+        err = launch_attention_redo(a, b->shape.ctas, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the attention kernel");
     // and with plans that split more tiles
     const int joins = captured ? b->shape.ctas : b->n_joins;

@@ -30,7 +30,8 @@ struct BatchHeader {
     int32_t n_tokens;
     int32_t n_joins;
     int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
-    int32_t pad[2];
+    int32_t n_items;
+    int32_t pad;
 };
 
 // One chunk, as attention sees it.
@@ -184,7 +185,7 @@ struct AttnArgs {
     const AttnJoin* joins;
     float* part_out;       // [parts][kAttnRows, by pairs kPairRows][value dim]
     float* part_lse;       // [parts][the same], natural log
-    int32_t* redo;         // by pairs: [items][2], set where the item is to be computed again
+    int32_t* redo;         // [items][2], set where a tensor-core kernel's item is to be computed again
     const int32_t* pending;
     const double* turn;    // lazy pools' turn table
     int32_t* status;
@@ -215,10 +216,11 @@ bool attention_takes_tiles(const Geometry& g);
 int attention_tile_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
 // Attention by pairs of CTAs (leyline_attention_pair.cu), for MLA rows whose tiles come by TMA; after
-// attention_tile_prepare.  redo_attention computes again the items that it marked.
+// attention_tile_prepare.
 int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, void* stream);
-int launch_attention_redo(const AttnArgs& a, int pairs, void* stream);
+// Computes again, one cache row at a time, the items that either of the two marked.
+int launch_attention_redo(const AttnArgs& a, int ctas, void* stream);
 // Fills *maps for the rows at kv and readies their kernel.
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
