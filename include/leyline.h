@@ -508,12 +508,11 @@ int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyli
  * does not attend to do not reach its output, whatever they hold.  out may not
  * overlap the queries.
  * Scores and sums are fp32; the weights exp(x - max) are rounded to bf16 for
- * the product with the values (values above 2^100 may take its fp32 sums to infinity
- * in chunks of one token).  Enqueues one kernel; for chunks of several tokens a
- * second one that computes row tiles again whose output is not finite, or whose
- * scores rise by more than 55 over those of the tile's first 64 rows (a slow path);
- * and one that joins the partial results of split row tiles.  Two calls on the same
- * inputs and plan give the same bits.
+ * the product with the values.  A row tile whose output is not finite, or whose scores
+ * rise by more than 55 over those of the tile's first 64 rows, is computed again one
+ * row at a time (a slow path).  Enqueues one kernel, and a second one that joins the
+ * partial results of split row tiles.  Two calls on the same inputs and plan give
+ * the same bits.
  * Errors: INVALID_ARG, CUDA. */
 #define LEYLINE_ATTENTION_PREFIX 1
 int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads_t* q_latent,

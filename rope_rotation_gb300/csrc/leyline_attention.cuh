@@ -2,14 +2,11 @@
 // leyline_attention_pair.cu).
 #pragma once
 
-#include "leyline_batch.h"
+#include "leyline_attention_any.cuh"
 #include "leyline_tcgen05.cuh"
 
 namespace leyline {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kAtomBytes = 1024;  // 8 rows x 128 bytes
 constexpr unsigned long long kDrainTime = 1000000ull;  // 1 ms: longer than any load in flight takes

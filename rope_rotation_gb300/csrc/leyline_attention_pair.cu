@@ -11,8 +11,8 @@
 //
 // The reference maximum of a row is that of its item's first tile and stays: weights are exp2(x - m0), in bf16 and
 // fp32 as exact relative to their size as any.  A later score above m0 by more than 80 (as a power of 2) could leave
-// fp32's range in the sums; the item is then marked, as is one whose output is not finite, and a kernel that follows
-// computes it again (leyline_attention.cu).  So O never has to be rescaled, which would take both CTAs to agree in the
+// fp32's range in the sums; the item is then marked, as is one whose output is not finite, and computed
+// again at the end without the tensor cores (leyline_attention_any.cuh).  So O never has to be rescaled, which would take both CTAs to agree in the
 // middle of every tile.
 //
 // Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
@@ -58,6 +58,7 @@ struct Misc {
     uint32_t tmem;
     int quit;
     float half[2][kRows];        // a row's maximum, then sum, over either half of a tile's columns
+    float redo;                  // not 0: some item is to be computed again
     float factor[2 * kRows];     // 1 / l of both CTAs' rows
 };
 constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
@@ -459,14 +460,21 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
         }
         tcgen05_before_sync();
         redo = any_of_softmax(redo);  // and before the next item's maxima
-        if (threadIdx.x == 0) a.redo[2 * i + rank] = redo;
+        if (threadIdx.x == 0) {
+            a.redo[2 * i + rank] = redo;
+            if (redo) {
+                const uint32_t to = smem_addr(&m->redo);
+                cluster_store(cluster_addr(to, 0), 1.f);
+                cluster_store(cluster_addr(to, 1), 1.f);
+            }
+        }
     }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_constant__ AttnArgs a,
                                                                const __grid_constant__ TileMaps maps)
 {
-    extern __shared__ unsigned char raw[];
+    extern __shared__ __align__(16) unsigned char raw[];
     const uint32_t smem = (smem_addr(raw) + 1023) & ~1023u;
     Misc* m = reinterpret_cast<Misc*>(raw + (smem - smem_addr(raw)) + kMiscOff);
     const int warp = threadIdx.x / 32;
@@ -493,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
         mbar_init(smem_addr(&m->x_ready), 4);  // the two warps of each CTA that hold the sums
         mbar_init(smem_addr(&m->drained), 1);
         m->quit = 0;
+        m->redo = 0.f;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);
@@ -531,6 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
     if (warp == kMmaWarp) {
         tcgen05_after_sync();
         pair_tmem_free(tmem, kTmemCols);
+    }
+    const bool redo = m->redo != 0.f && !m->quit;
+    __syncthreads();  // before shared memory is written again
+    if (redo) {       // marked by either CTA: each computes its own rows again
+        for (int i = a.cta_begin[blockIdx.x / 2]; i < a.cta_begin[blockIdx.x / 2 + 1]; ++i) {
+            if (__ldcg(a.redo + 2 * i) == 0 && __ldcg(a.redo + 2 * i + 1) == 0) continue;
+            const AttnItem item = a.items[i];
+            attend_rows<kThreads>(a, item, min((int)rank * kRows, item.rows), min((int)(rank + 1) * kRows, item.rows), kPairRows,
+                                  raw);
+        }
     }
 }
 

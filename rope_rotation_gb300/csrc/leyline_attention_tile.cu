@@ -30,8 +30,8 @@
 //
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
-// An output that is not finite marks its item, which a kernel that follows computes again: a weight of 0 keeps a masked
-// row's infinity or NaN out of the sum there, not in a matrix product.
+// An item whose output is not finite is computed again, without the tensor cores: there a weight of 0 keeps a masked
+// row's infinity or NaN out of the sum, in a matrix product it does not.
 #include "leyline_attention.cuh"
 
 namespace leyline {
@@ -57,6 +57,7 @@ struct Misc {
     unsigned long long p_ready, pv_done, drained;
     uint32_t tmem;
     int quit;
+    int redo;  // some item is to be computed again
     float factor[kAttnRows];  // rescale, then 1 / l
 };
 
@@ -684,7 +685,10 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
             }
         tcgen05_before_sync();
         redo = any_of_softmax(redo);  // and before the next item's factors
-        if (threadIdx.x == 0) *reinterpret_cast<int2*>(a.redo + 2 * i) = make_int2(redo, 0);
+        if (threadIdx.x == 0) {
+            a.redo[2 * i] = redo;
+            if (redo) m->redo = 1;
+        }
     }
 }
 
@@ -692,7 +696,7 @@ template <bool kMla, bool kLazy, int kKeys>
 __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ AttnArgs a,
                                                                const __grid_constant__ TileMaps maps)
 {
-    extern __shared__ unsigned char raw[];
+    extern __shared__ __align__(16) unsigned char raw[];
     const Layout l = kMla ? make_layout(true, kLazy, kLazy ? false : maps.whole != 0, 1, 8, 2)
                           : make_layout(false, kLazy, false, kKeys, maps.values, maps.stages);
     const uint32_t smem = (smem_addr(raw) + 1023) & ~1023u;
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         mbar_init(smem_addr(&m->p_ready), kSoftmaxWarps);
         mbar_init(smem_addr(&m->pv_done), 1);
         mbar_init(smem_addr(&m->drained), 1);
-        m->quit = 0;
+        m->quit = m->redo = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&m->tmem), kTmemCols);
@@ -749,6 +753,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         tcgen05_after_sync();
         tmem_free(tmem, kTmemCols);
     }
+    const bool redo = m->redo && !m->quit;
+    __syncthreads();  // before shared memory is written again
+    if (redo) {
+        for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i)
+            if (a.redo[2 * i]) attend_rows<kThreads>(a, a.items[i], 0, a.items[i].rows, kAttnRows, raw);
+    }
 }
 
 // Map of `rows` rows of row_vecs 16-byte vectors at `base`: 64 columns, 8 rows of a group, planes of 64 columns, groups;
@@ -782,6 +792,12 @@ Layout layout_of(const Geometry& g, const TileMaps& maps)
 {
     return make_layout(g.rope_heads <= 1, (g.flags & LEYLINE_POOL_LAZY) != 0, maps.whole != 0, g.rope_dim / 64, maps.values,
                        maps.stages);
+}
+
+// The tiles' shared memory, or what attend_rows needs.
+int smem_of(const Geometry& g, const TileMaps& maps)
+{
+    return std::max(layout_of(g, maps).bytes, (int)any_shape(g).bytes);
 }
 
 }  // namespace
@@ -818,13 +834,12 @@ int attention_tile_prepare(const Geometry& g, const void* kv, TileMaps* maps)
                       !make_map(encode, &maps->bands, base + g.rope_base_vecs, rows, g.rope_row_vecs,
                                 keys * std::max(g.rope_heads, 1), keys, groups)))
         return (int)cudaErrorInvalidValue;
-    return (int)cudaFuncSetAttribute(kernel_of(g), cudaFuncAttributeMaxDynamicSharedMemorySize, layout_of(g, *maps).bytes);
+    return (int)cudaFuncSetAttribute(kernel_of(g), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(g, *maps));
 }
 
 int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream)
 {
-    return (int)launch_dependent_smem(kernel_of(a.g), ctas, kThreads, layout_of(a.g, maps).bytes, (cudaStream_t)stream, a,
-                                      maps);
+    return (int)launch_dependent_smem(kernel_of(a.g), ctas, kThreads, smem_of(a.g, maps), (cudaStream_t)stream, a, maps);
 }
 
 }  // namespace leyline

@@ -49,7 +49,6 @@ struct leyline_batch {
     int32_t n_joins = 0;
     bool pairs = false;  // the plan is for pairs
     bool many_parts = false;  // it splits a tile into more than kFewParts
-    bool masks = false;       // it has chunks of several tokens
 };
 
 namespace {
@@ -267,7 +266,6 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     hd.n_tokens = (int32_t)cp.tokens;
     hd.n_joins = split.n_joins;
     hd.pairs = pairs ? 1 : 0;
-    hd.n_items = split.n_items;
     memcpy(h, &hd, sizeof hd);
     if (!cp.runs.empty()) memcpy(h + l.bytes, cp.runs.data(), sizeof(PlanRun) * cp.runs.size());
 
@@ -306,8 +304,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
-    b->many_parts = b->masks = false;
-    for (const ChunkDev& c : cp.chunks) b->masks |= c.n > 1;
+    b->many_parts = false;
     for (int32_t j = 0; j < split.n_joins; ++j) b->many_parts |= split.joins[j].parts > kFewParts;
     return LEYLINE_OK;
 }
@@ -482,9 +479,6 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     if (captured || !b->pairs) err = launch_attention(a, b->maps, b->shape.ctas, stream);
     if (err == 0 && b->pair_shape.ctas > 0 && (captured || b->pairs))
         err = launch_attention_pair(a, b->maps, b->pair_shape.ctas, stream);
-    // the tokens of a decode batch's chunks attend to all that is loaded for them: nothing is masked
-    if (err == 0 && b->d_redo && (captured || b->pairs || (b->masks && !a.prefix)))
-        err = launch_attention_redo(a, b->shape.ctas, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the attention kernel");
     // and with plans that split more tiles
     const int joins = captured ? b->shape.ctas : b->n_joins;

@@ -16,6 +16,9 @@
 
 namespace leyline {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
 constexpr int kAttnRows = 64;  // query rows (token, head) of a row tile
 // Lazy pools of MLA rows: 48, since a turned band takes a chunk more of shared memory.
 constexpr int kAttnRowsLazy = 48;
@@ -30,8 +33,7 @@ struct BatchHeader {
     int32_t n_tokens;
     int32_t n_joins;
     int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
-    int32_t n_items;
-    int32_t pad;
+    int32_t pad[2];
 };
 
 // One chunk, as attention sees it.
@@ -185,7 +187,7 @@ struct AttnArgs {
     const AttnJoin* joins;
     float* part_out;       // [parts][kAttnRows, by pairs kPairRows][value dim]
     float* part_lse;       // [parts][the same], natural log
-    int32_t* redo;         // [items][2], set where a tensor-core kernel's item is to be computed again
+    int32_t* redo;         // [items][2], set where a CTA's part of a tensor-core kernel's item has to be computed again
     const int32_t* pending;
     const double* turn;    // lazy pools' turn table
     int32_t* status;
@@ -219,8 +221,6 @@ int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, voi
 // attention_tile_prepare.
 int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, void* stream);
-// Computes again, one cache row at a time, the items that either of the two marked.
-int launch_attention_redo(const AttnArgs& a, int ctas, void* stream);
 // Fills *maps for the rows at kv and readies their kernel.
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
