@@ -236,6 +236,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ rotate --
+// A lane has two bands in flight: 32 KB on each SM with one, too little for the latency of memory (4096 tokens of 128
+// bands of 64: 28 us with one, 25 with two at the same 32 warps per SM, 28 with four; 26 with one at 64 warps).
+constexpr int kAtOnce = 2;
+
 template <int kLayout>
 __global__ void __launch_bounds__(kAppendThreads) rotate_kernel(const __grid_constant__ RotateArgs a)
 {
@@ -252,31 +256,42 @@ __global__ void __launch_bounds__(kAppendThreads) rotate_kernel(const __grid_con
     const long long bands = (long long)a.header->n_tokens * a.q_heads;
     const long long per = 32 / width;  // bands of a warp at a time
     const long long warps = (long long)gridDim.x * (kAppendThreads / 32);
-    for (long long b0 = (blockIdx.x * (long long)(kAppendThreads / 32) + threadIdx.x / 32) * per; b0 < bands;
-         b0 += warps * per) {
-        const long long b = b0 + lane / width;
-        const bool on = b < bands && q < hv / 2;
-        const long long t = b / a.q_heads, h = b - t * a.q_heads;
-        uint4 x = {}, y = {}, w0 = {}, w1 = {};
-        const uint4* src = static_cast<const uint4*>(a.q.ptr) + (t * a.q.token_stride + h * a.q.head_stride) / 8;
-        if (on) {
-            x = src[v0];
-            y = src[v1];
-        }
-        float inv = 0.f;
-        if (a.norm) {
-            const float s = group_sum(sum_squares(x) + sum_squares(y), width);
-            inv = rsqrtf(s / (float)g.rope_dim + a.eps);
-            if (on) {
-                w0 = a.norm[v0];
-                w1 = a.norm[v1];
+    for (long long b0 = (blockIdx.x * (long long)(kAppendThreads / 32) + threadIdx.x / 32) * per * kAtOnce; b0 < bands;
+         b0 += warps * per * kAtOnce) {
+        uint4 x[kAtOnce], y[kAtOnce];
+        long long t[kAtOnce], h[kAtOnce];
+        bool on[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const long long b = b0 + k * per + lane / width;
+            on[k] = b < bands && q < hv / 2;
+            t[k] = (unsigned)b / (unsigned)a.q_heads;  // bands <= 2^32
+            h[k] = b - t[k] * a.q_heads;
+            const uint4* src = static_cast<const uint4*>(a.q.ptr) + (t[k] * a.q.token_stride + h[k] * a.q.head_stride) / 8;
+            x[k] = y[k] = make_uint4(0, 0, 0, 0);
+            if (on[k]) {
+                x[k] = src[v0];
+                y[k] = src[v1];
             }
         }
-        if (on) {
-            uint4* dst = static_cast<uint4*>(a.out.ptr) + (t * a.out.token_stride + h * a.out.head_stride) / 8;
-            encode_pairs<kLayout>(x, y, a.norm != nullptr, inv, w0, w1, a.trig + t * half + 8 * q, bf16);
-            dst[v0] = x;
-            dst[v1] = y;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            uint4 w0 = {}, w1 = {};
+            float inv = 0.f;
+            if (a.norm) {
+                const float s = group_sum(sum_squares(x[k]) + sum_squares(y[k]), width);
+                inv = rsqrtf(s / (float)g.rope_dim + a.eps);
+                if (on[k]) {
+                    w0 = a.norm[v0];
+                    w1 = a.norm[v1];
+                }
+            }
+            if (on[k]) {
+                uint4* dst = static_cast<uint4*>(a.out.ptr) + (t[k] * a.out.token_stride + h[k] * a.out.head_stride) / 8;
+                encode_pairs<kLayout>(x[k], y[k], a.norm != nullptr, inv, w0, w1, a.trig + t[k] * half + 8 * q, bf16);
+                dst[v0] = x[k];
+                dst[v1] = y[k];
+            }
         }
     }
 }
@@ -299,7 +314,7 @@ int launch_append(const AppendArgs& a, int64_t tokens, int sm_count, void* strea
 
 int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* stream)
 {
-    const int grid = grid_for(tokens * a.q_heads * (a.g.rope_dim / 16), kAppendThreads, sm_count * 8);
+    const int grid = grid_for((tokens * a.q_heads * (a.g.rope_dim / 16) + kAtOnce - 1) / kAtOnce, kAppendThreads, sm_count * 8);
     return (int)(a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT
                      ? launch_dependent(rotate_kernel<0>, grid, kAppendThreads, (cudaStream_t)stream, a)
                      : launch_dependent(rotate_kernel<1>, grid, kAppendThreads, (cudaStream_t)stream, a));

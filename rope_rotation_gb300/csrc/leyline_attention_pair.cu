@@ -59,8 +59,10 @@ struct Misc {
     int quit;
     float half[2][kRows];        // a row's maximum, then sum, over either half of a tile's columns
     float redo;                  // not 0: some item is to be computed again
-    float factor[2 * kRows];     // 1 / l of both CTAs' rows
+    // 1 / l of both CTAs' rows, for items in turn: one CTA may be an item ahead of the other's last step
+    alignas(16) float factor[2][2 * kRows];
 };
+static_assert(offsetof(Misc, factor) % 16 == 0 && kMiscOff % 16 == 0, "read in vectors");
 constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
@@ -416,48 +418,26 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
                     a.lse[(long long)(w.ch.tok0 + q / group) * a.q_heads + q % group] = lse;
                 }
             }
-            if (w.tiles > 0) {
-                const float f = l == 0.f ? 0.f : 1.f / l;
-                const uint32_t to = smem_addr(&m->factor[rank * kRows + r]);
-                cluster_store(cluster_addr(to, 0), f);
-                cluster_store(cluster_addr(to, 1), f);
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 0), 1);
-                    cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 1), 1);
-                }
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            const uint32_t to = smem_addr(&m->factor[x_phase][rank * kRows + r]);
+            cluster_store(cluster_addr(to, 0), f);
+            cluster_store(cluster_addr(to, 1), f);
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 0), 1);
+                cluster_arrive(cluster_addr(smem_addr(&m->x_ready), 1), 1);
             }
         }
+        mbar_wait_cluster(smem_addr(&m->x_ready), x_phase, &m->quit, a.status);
         if (w.tiles > 0) {
-            mbar_wait_cluster(smem_addr(&m->x_ready), x_phase, &m->quit, a.status);
-            x_phase ^= 1;
             mbar_wait_cluster(smem_addr(&m->pv_done[(index - 1) & 1]), ((index - 1) >> 1) & 1, &m->quit, a.status);
             tcgen05_after_sync();
         }
-        for (int b = 0; b < 2; ++b) {
-            const int dim = 256 * b + 128 * (int)rank + 32 * warp + lane;
-            for (int c = 0; c < w.it.rows; c += 16) {
-                uint32_t v[16] = {};
-                if (w.tiles > 0) {
-                    tmem_ld16(tmem + kTmemO + lanes + b * 128 + c, v);
-                    tmem_wait_ld();
-                }
-                for (int k = 0; k < 16; ++k) {
-                    const int q = c + k;
-                    if (q >= w.it.rows) break;
-                    const float o = w.tiles > 0 ? __uint_as_float(v[k]) * m->factor[q] : 0.f;
-                    redo |= !isfinite(o);
-                    if (w.it.part >= 0) {
-                        a.part_out[((long long)w.it.part * kPairRows + q) * 512 + dim] = o;
-                    } else {
-                        const long long tok = w.ch.tok0 + (w.it.row0 + q) / group, head = (w.it.row0 + q) % group;
-                        static_cast<__nv_bfloat16*>(
-                            a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + dim] = __float2bfloat16_rn(o);
-                    }
-                }
-            }
-        }
+        for (int c = 0; c < w.it.rows; c += 16)  // (P is free)
+            redo |= put_rows<kPairRows>(a, w, group, 512, c, 128 * (int)rank + 32 * warp, 256, 2, tmem + kTmemO + lanes + c,
+                                        128, m->factor[x_phase] + c, smem + kPOff + warp * 1024);
+        x_phase ^= 1;
         tcgen05_before_sync();
         redo = any_of_softmax(redo);  // and before the next item's maxima
         if (threadIdx.x == 0) {

@@ -58,8 +58,9 @@ struct Misc {
     uint32_t tmem;
     int quit;
     int redo;  // some item is to be computed again
-    float factor[kAttnRows];  // rescale, then 1 / l
+    alignas(16) float factor[kAttnRows];  // rescale, then 1 / l
 };
+static_assert(offsetof(Misc, factor) % 16 == 0 && sizeof(Misc) % 16 == 0, "read in vectors");
 
 // Shared memory of a kind of rows (bytes, from a 1024-byte aligned start).
 struct Layout {
@@ -642,8 +643,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
         if (lane % 4 == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (row[h] >= w.it.rows) continue;
                 m->factor[row[h]] = sums[h] == 0.f ? 0.f : 1.f / sums[h];
+                if (row[h] >= w.it.rows) continue;
                 const float lse = sums[h] == 0.f ? -INFINITY : (top[h] + log2f(sums[h])) * kLn2;
                 if (w.it.part >= 0) {
                     a.part_lse[(long long)w.it.part * kAttnRows + row[h]] = lse;
@@ -659,30 +660,9 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
             tcgen05_after_sync();
         }
         bool redo = false;
-        for (int b = 0; b < blocks; ++b)
-            for (int c = 0; c < n; c += 16) {
-                uint32_t v[16] = {};
-                if (w.tiles > 0) {
-                    tmem_ld16(tmem_o + b * 64 + c, v);
-                    tmem_wait_ld();
-                }
-                const int dim = 128 * b + 32 * warp + lane;
-                if (dim >= vdim) continue;
-                for (int k = 0; k < 16; ++k) {
-                    const int r = c + k;
-                    if (r >= w.it.rows) break;
-                    const float o = __uint_as_float(v[k]) * m->factor[r];
-                    redo |= !isfinite(o);
-                    if (w.it.part >= 0) {
-                        a.part_out[((long long)w.it.part * kAttnRows + r) * vdim + dim] = o;
-                    } else {
-                        const int q = w.it.row0 + r;
-                        const long long tok = w.ch.tok0 + q / group, head = w.it.band * group + q % group;
-                        static_cast<__nv_bfloat16*>(
-                            a.out.ptr)[tok * a.out.token_stride + head * a.out.head_stride + dim] = __float2bfloat16_rn(o);
-                    }
-                }
-            }
+        for (int c = 0; c < n; c += 16)  // (P is free)
+            redo |= put_rows<kAttnRows>(a, w, group, vdim, c, 32 * warp, 128, blocks, tmem_o + c, 64, m->factor + c,
+                                        smem + l.p + warp * 1024);
         tcgen05_before_sync();
         redo = any_of_softmax(redo);  // and before the next item's factors
         if (threadIdx.x == 0) {

@@ -164,3 +164,25 @@ def test_outputs_that_overlap_are_refused():
     b.attention(0, ql, q, 0.07, out=flat.as_strided((3, 4, 512), (512, 1536, 1)))  # heads outermost
     cache.check_status()
     cache.close()
+
+
+@pytest.mark.parametrize("heads,reqs", [(128, 100), (20, 300)])
+def test_many_short_tiles(heads, reqs):
+    """Row tiles of one or two cache tiles (with a prefix: of none) one after another on a CTA."""
+    rng = np.random.default_rng(heads)
+    lens = rng.integers(0, 130, size=reqs)
+    lens[:8] = 0
+    chunks = [(r, int(n), int(rng.integers(1, 9))) for r, n in enumerate(lens)]
+    cache = BH.make_cache(lens.tolist(), extra=8, layers=1)
+    b = cache.batch(reqs, 8 * reqs, heads)
+    b.plan(chunks)
+    T = b.tokens
+    b.append(0, BH.bf16(T, 576, seed=1))
+    ql, q = BH.bf16(T, heads, 512, seed=2), BH.bf16(T, heads, 64, seed=3)
+    for prefix in (False, True):
+        first = BH.check_attention(cache, b, 0, chunks, ql, q, 0.07, "short tiles", prefix=prefix)
+        for _ in range(20):
+            out, lse = b.attention(0, ql, q, 0.07, prefix=prefix)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    cache.check_status()
+    cache.close()
