@@ -78,6 +78,22 @@ __device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, Mi
 }
 
 // -------------------------------------------------------------------- loads --
+// The keys' loaders ask for the next tile's rows in L2 before they wait for a free stage: two tiles in shared memory are
+// too few bytes in flight for HBM's latency.  For chunks of few row tiles alone: the rows of a long chunk are in L2
+// already, and asking costs the loaders time (16 decodes of 128 heads, one tile each: 135 us without, 124 with; ragged
+// chunks of 8 tiles: 165, 163; a prompt chunk of 512 tiles: 747, 772).
+constexpr int kPrefetchTiles = 8;
+
+// `n` rows at a page's row, whole.
+__device__ __forceinline__ void prefetch_rows(const AttnArgs& a, const PageOf& p, int n)
+{
+    if (p.page < 0 || p.page >= a.g.num_pages) return;
+    const Geometry& g = a.g;
+    const long long slot = (long long)p.page * g.block_size + p.off;
+    prefetch_l2(a.kv + lat_off(g, a.layer, slot), (uint32_t)(n * g.lat_row_vecs * 16));
+    if (g.lat_row_vecs != g.row_vecs) prefetch_l2(a.kv + band_off(g, a.layer, slot), (uint32_t)(n * g.rope_row_vecs * 16));
+}
+
 // One lane of a warp each.  Keys (kValues false): loader `part` of two takes 16 of this CTA's 32 rows of a tile, whole;
 // values: loader `part` of four takes this CTA's four chunks of 16 of the tile's 64 rows, those of PV's step `part`.
 template <bool kValues>
@@ -94,6 +110,7 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& ma
     for (int i = a.cta_begin[pair]; i < a.cta_begin[pair + 1]; ++i) {
         const Work w = load_work(a, i);
         const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        const bool prefetch = !kValues && w.ch.n * a.q_heads <= kPrefetchTiles * kPairRows;
         PageOf at[2];
         auto look_up = [&](long long key) {
             if (!by_box(maps, w, key)) return;
@@ -114,7 +131,14 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& ma
                         if (slot >= 0) y[k] = layer_groups + (int)(slot >> 3);
                     }
             }
-            if (t + 1 < w.tiles) look_up(key + kAttnKeys);
+            if (t + 1 < w.tiles) {
+                look_up(key + kAttnKeys);
+                if (prefetch && by_box(maps, w, key + kAttnKeys)) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (k < boxes) prefetch_rows(a, at[k], maps.box);
+                }
+            }
             const uint32_t empty = smem_addr(kValues ? &m->v_empty[ring.stage][part] : &m->k_empty[ring.stage]);
             if (!mbar_wait_cluster(empty, ring.phase ^ 1, &m->quit, a.status)) return;
             if (!box) {  // the copy warps' tile.  They do not follow the stages' uses, which a parity could not tell apart

@@ -219,7 +219,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     if (e == cudaSuccess && attention_takes_tiles(g))
         e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
     if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending && b->maps.box > 0) {
-        b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows};
+        b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows, kItemCostPairs};
         e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
     }
     if (e == cudaSuccess) e = cudaDeviceSynchronize();

@@ -104,12 +104,19 @@ struct ChunkPlan {
 int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyline_chunk_t* chunks, int32_t n,
                  int64_t max_tokens, int64_t free_pages, int64_t pop_base, ChunkPlan* out);
 
+// What an item costs beside its cache tiles: its queries, the output of 64 or 128 rows and, until the first scores are
+// there, an idle tensor core.  2 or 8 cache tiles (measured with 2, 4, 6 and 8: 64 drafts over grouped rows 72.5, 73, 74,
+// 74 us; by pairs a prompt chunk of 512 tokens of 128 heads 747, 741, 739, 737 us, ragged chunks 165, 164, 161, 159).
+constexpr int32_t kItemCost = 2;
+constexpr int32_t kItemCostPairs = 8;
+
 // What the split of the attention's work goes by.
 struct WorkShape {
     int32_t bands;  // key bands attention works on (1: MLA)
     int32_t group;  // query heads per band
     int32_t ctas;
     int32_t rows;   // query rows of a tile, at most kAttnRows, by pairs kPairRows (and ctas pairs)
+    int32_t item_cost = kItemCost;  // of an item's queries and output, in cache tiles
 };
 // Where the split is written: items[row tiles + ctas], cta_begin[ctas + 1], joins[ctas].
 struct Split {

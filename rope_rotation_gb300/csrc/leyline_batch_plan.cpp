@@ -101,17 +101,12 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
     return LEYLINE_OK;
 }
 
-// The split of the attention's work over the CTAs.  A row tile costs its key tiles plus a fixed
-// share for its queries and its output; the tiles form one list, which the CTAs take in
-// contiguous runs of equal cost, so a tile may end in one CTA and go on in the next.  A CTA never
-// starts or leaves less than kMinKeyTiles of a tile that has more.  split_by cuts by a given share
-// and returns the last CTA's cost.
-constexpr int64_t kTileCost = 2;
+// The split of the attention's work over the CTAs.  A row tile costs its key tiles plus item_cost;
+// the tiles form one list, which the CTAs take in contiguous runs of equal cost, so a tile may end
+// in one CTA and go on in the next.  A CTA never starts or leaves less than kMinKeyTiles of a tile
+// that has more.  split_by cuts by a given share and returns the last CTA's cost.
 constexpr int64_t kMinKeyTiles = 2;
 
-// Cycles of a cache tile in the two kernels of MLA rows (2 * kPairCycles: a pair holds two SMs).
-constexpr int64_t kTileCycles = 3400;
-constexpr int64_t kPairCycles = 1800;
 static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks, int64_t quota, Split* out)
 {
     int64_t used = 0;  // of the current CTA's quota
@@ -136,7 +131,7 @@ static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks,
                 while (done < tiles) {
                     const bool last_cta = cta + 1 == w.ctas;
                     const int64_t left = tiles - done;
-                    int64_t take = last_cta ? left : std::min(left, quota - used - kTileCost);
+                    int64_t take = last_cta ? left : std::min(left, quota - used - w.item_cost);
                     if (take < left && (take < kMinKeyTiles || left - take < kMinKeyTiles)) {
                         // too little room here, or too little left over: all of it or none
                         if (used > 0 && take < kMinKeyTiles) {
@@ -150,8 +145,8 @@ static int64_t split_by(const WorkShape& w, const std::vector<ChunkDev>& chunks,
                     it = AttnItem{(int32_t)k, band, (int32_t)r0, n_rows, (int32_t)(done * kAttnKeys),
                                   (int32_t)std::min(end, (done + take) * kAttnKeys), -1, 0};
                     done += take;
-                    used += take + kTileCost;
-                    if (used + kTileCost >= quota) next_cta();
+                    used += take + w.item_cost;
+                    if (used + w.item_cost >= quota) next_cta();
                 }
                 const int32_t parts = out->n_items - first_item;
                 if (parts > 1) {
@@ -179,23 +174,30 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
     // Cutting tiles adds pieces, and borders leave some of a CTA's share unused: the last CTA takes
     // what is left, so the share grows until that is no more than a share.
     const Split empty = *out;
-    int64_t quota = ceil_div(total + kTileCost * pieces, w.ctas) + 1;
+    int64_t quota = ceil_div(total + w.item_cost * pieces, w.ctas) + 1;
     while (split_by(w, chunks, quota, out) > quota) {
         *out = empty;
         quota += std::max<int64_t>(1, quota / 64);
     }
 }
 
-// Whether the work goes to pairs of CTAs: by the tiles that either kernel would take, times what a tile takes it.
+// Whether the work goes to pairs of CTAs: by an estimate of either kernel's cycles.  A cache tile of 64 rows takes a CTA
+// 3800 cycles and 10 for each query row, a pair 1900 for up to 128; an item costs a pair more at its ends, and the call
+// 4000 cycles more to start.  16 requests decode over 24000 rows: 16 heads 111 us by CTAs, 107 by pairs, 64 heads 124,
+// 113, 128 heads 206, 123; 64 over 4000 rows: 16 heads 78, 81, 64 heads 92, 90; one over 32768: 16 heads 18, 21, 128 heads
+// 28, 25; 300 over 130 rows: 64 heads 36, 40.
 bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks)
 {
-    int64_t single = 0, pair = 0;
+    constexpr int64_t kTile = 3800, kTileRow = 10, kTileItem = 8400, kPairTile = 1900, kPairItem = 12000, kPairStart = 4000;
+    const int64_t pairs = w.ctas / 2;
+    int64_t single = kTileItem * w.ctas, pair = kPairItem * pairs;  // as many items are cut
     for (const ChunkDev& c : chunks) {
-        const int64_t rows = (int64_t)c.n * w.group, tiles = ceil_div(c.start + c.n, kAttnKeys);
-        single += ceil_div(rows, kAttnRows) * tiles;
-        pair += ceil_div(rows, kPairRows) * tiles;
+        const int64_t rows = (int64_t)c.n * w.group, keys = ceil_div(c.start + c.n, kAttnKeys);
+        const int64_t tiles = ceil_div(rows, kAttnRows), pair_tiles = ceil_div(rows, kPairRows);
+        single += tiles * (keys * kTile + kTileItem) + rows * keys * kTileRow;
+        pair += pair_tiles * (keys * kPairTile + kPairItem);
     }
-    return single * kTileCycles > pair * 2 * kPairCycles;
+    return single * pairs > (pair + kPairStart * pairs) * w.ctas;
 }
 
 }  // namespace leyline

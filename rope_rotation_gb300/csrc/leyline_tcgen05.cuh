@@ -248,6 +248,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                  : "memory");
 }
 
+// Ask for `bytes` (a multiple of 16) at a 16-byte aligned address to be in L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Arrive on `bar` (counted among its expected arrivals) when this thread's earlier cp.async are done.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
 {
