@@ -16,31 +16,32 @@ __global__ void __launch_bounds__(kAnyThreads) attend_any_kernel(const __grid_co
 }
 
 // -------------------------------------------------------------------- join --
-// Partial results k of a row: out = sum w_k out_k / sum w_k with w_k = exp(lse_k - max),
-// lse = max + ln sum w_k.  A warp per query row and 128 value dimensions: its lanes form the weights of 32 parts at a
-// time, then read the parts eight loads at a time (a row split over 128 CTAs took 73 us with one dependent load after
-// another).  Where a plan splits tiles into many parts, kSplit = 4 warps share a row's: 12 -> 6 us for that row; with
-// two or three parts a row the other three would have nothing to do.  The parts are added in a fixed order, so
-// the result does not depend on which CTA finished first.
+// Partial results k of a row: out = sum w_k out_k with w_k = exp(lse_k - max) / sum of these, lse = max + ln of that sum.
+// A warp takes kSlices times 128 value dimensions of a query row: its lanes form the weights of 32 parts at a time, then
+// read the parts eight loads at a time (a row split over 128 CTAs took 73 us with one dependent load after another).
+// Bound by the latency of these steps: with 4 slices a warp and a row's 512 dimensions in one, a quarter as many warps
+// go through them (62 tiles of 128 rows in 2 or 3 parts: 26 -> 12 us).  Where a plan splits tiles into many parts, kSplit = 4
+// warps share a row's parts: 12 -> 6 us for that row; with two or three parts the other warps would have nothing to do.
+// The parts are added in a fixed order, so the result does not depend on which CTA finished first.
 constexpr int kJoinThreads = 128;
+constexpr int kJoinSlice = 128;
 
-template <int kSplit>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int slices, int rows)
+template <int kSplit, int kSlices>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int groups, int per_join)
 {
-    __shared__ float4 sum_s[kJoinThreads];
-    __shared__ float total_s[kJoinThreads / 32];
+    __shared__ float4 sum_s[kSlices][kJoinThreads];
     wait_for_previous_grid();
     // the next kernel is not let in early: its CTAs, one per SM, would crowd onto the SMs that are free first
-    constexpr int kUnits = kJoinThreads / 32 / kSplit;
+    constexpr int kUnits = kJoinThreads / 32 / kSplit;  // of a CTA: (row, group of slices)
+    constexpr int kAtOnce = 8 / kSlices;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = warp % kSplit;
-    const long long unit = blockIdx.x * (long long)kUnits + warp / kSplit;
-    const int slice = (int)(unit % slices);
-    const int j = (int)(unit / slices / rows), r = (int)(unit / slices % rows);
-    // (with kSplit > 1 a CTA has one unit, so it leaves as a whole)
-    if (j >= a.header->n_joins) return;
+    const int j = blockIdx.x / per_join, unit = (blockIdx.x - j * per_join) * kUnits + warp / kSplit;
+    const int r = unit / groups, first = (unit - r * groups) * kSlices * kJoinSlice + 4 * lane;
     const AttnJoin jn = a.joins[j];
-    if (r >= jn.rows) return;
+    // (with kSplit > 1 a CTA has one unit, so it leaves as a whole)
+    if (j >= a.header->n_joins || r >= jn.rows) return;
     const int pitch = a.header->pairs ? kPairRows : kAttnRows;
+    const ChunkDev ch = a.chunks[jn.chunk];
     const Geometry& g = a.g;
     const bool mla = g.rope_heads <= 1;
     const int group = a.q_heads / (mla ? 1 : g.rope_heads);
@@ -49,57 +50,71 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     float top = -INFINITY;
     for (int k = lane; k < jn.parts; k += 32) top = fmaxf(top, lse[(long long)k * pitch]);
     for (int m = 16; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const int d = 128 * slice + 4 * lane;
-    const bool on = d < vdim;
-    const float* part = a.part_out + ((long long)jn.part0 * pitch + r) * vdim + (on ? d : 0);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a part without rows: lse -inf, weight 0 (it wrote zeros)
+    auto weight = [&](int k) {
+        const float x = k < jn.parts ? lse[(long long)k * pitch] : -INFINITY;
+        return x == -INFINITY ? 0.f : exp2f((x - top) * kLog2e);
+    };
     float total = 0.f;
+    for (int k = lane; k < jn.parts; k += 32) total += weight(k);
+    for (int m = 16; m > 0; m /= 2) total += __shfl_xor_sync(0xffffffffu, total, m);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float* part = a.part_out + ((long long)jn.part0 * pitch + r) * vdim + first;
+    float4 o[kSlices];
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) o[s] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 32 * sub; k0 < jn.parts; k0 += 32 * kSplit) {
         const int n = min(32, jn.parts - k0);
-        const float x = lane < n ? lse[(long long)(k0 + lane) * pitch] : -INFINITY;
-        const float mine = x == -INFINITY ? 0.f : exp2f((x - top) * kLog2e);
-        total += mine;
-        for (int k = 0; k < n; k += 8) {
-            float4 v[8];
+        const float mine = weight(k0 + lane) * inv;
+        for (int k = 0; k < n; k += kAtOnce) {
+            float4 v[kAtOnce][kSlices];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[u] = k + u < n ? __ldcg(reinterpret_cast<const float4*>(part + (long long)(k0 + k + u) * pitch * vdim))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float w = __shfl_sync(0xffffffffu, mine, k + u);  // 0 for a part without rows, which wrote zeros
-                o.x = fmaf(w, v[u].x, o.x);
-                o.y = fmaf(w, v[u].y, o.y);
-                o.z = fmaf(w, v[u].z, o.z);
-                o.w = fmaf(w, v[u].w, o.w);
+                for (int s = 0; s < kSlices; ++s)
+                    v[u][s] = k + u < n && first + s * kJoinSlice < vdim
+                                  ? __ldcg(reinterpret_cast<const float4*>(part + (long long)(k0 + k + u) * pitch * vdim +
+                                                                           s * kJoinSlice))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const float w = __shfl_sync(0xffffffffu, mine, k + u);
+#pragma unroll
+                for (int s = 0; s < kSlices; ++s) {
+                    o[s].x = fmaf(w, v[u][s].x, o[s].x);
+                    o[s].y = fmaf(w, v[u][s].y, o[s].y);
+                    o[s].z = fmaf(w, v[u][s].z, o[s].z);
+                    o[s].w = fmaf(w, v[u][s].w, o[s].w);
+                }
             }
         }
     }
-    for (int m = 16; m > 0; m /= 2) total += __shfl_xor_sync(0xffffffffu, total, m);
     if (kSplit > 1) {
-        sum_s[threadIdx.x] = o;
-        if (lane == 0) total_s[warp] = total;
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) sum_s[s][threadIdx.x] = o[s];
         __syncthreads();
         if (sub != 0) return;
-        for (int k = 1; k < kSplit; ++k) {
-            const float4 v = sum_s[threadIdx.x + 32 * k];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-            total += total_s[warp + k];
-        }
+        for (int k = 1; k < kSplit; ++k)
+#pragma unroll
+            for (int s = 0; s < kSlices; ++s) {
+                const float4 v = sum_s[s][threadIdx.x + 32 * k];
+                o[s].x += v.x;
+                o[s].y += v.y;
+                o[s].z += v.z;
+                o[s].w += v.w;
+            }
     }
-    const float inv = total > 0.f ? 1.f / total : total;
-    const ChunkDev ch = a.chunks[jn.chunk];
-    const int row = jn.row0 + r;
-    const long long tok = ch.tok0 + row / group, head = jn.band * group + row % group;
-    if (on)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out.ptr) + tok * a.out.token_stride +
-                                  head * a.out.head_stride + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (slice == 0 && lane == 0 && a.lse)
-        a.lse[tok * a.q_heads + head] = total > 0.f ? top + log2f(total) * kLn2 : (total == 0.f ? -INFINITY : total);
+    const int row = jn.row0 + r, tok = row / group;
+    const long long t = ch.tok0 + tok, head = jn.band * group + row - tok * group;
+    __nv_bfloat16* to =
+        static_cast<__nv_bfloat16*>(a.out.ptr) + t * a.out.token_stride + head * a.out.head_stride + first;
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s)
+        if (first + s * kJoinSlice < vdim)
+            *reinterpret_cast<uint2*>(to + s * kJoinSlice) =
+                make_uint2(pack_bf16x2(o[s].x, o[s].y), pack_bf16x2(o[s].z, o[s].w));
+    if (first == 0 && a.lse)
+        a.lse[t * a.q_heads + head] = total > 0.f ? top + log2f(total) * kLn2 : (total == 0.f ? -INFINITY : total);
 }
 
 }  // namespace
@@ -121,11 +136,12 @@ int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* st
 int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream)
 {
     const int vdim = a.g.latent_dim / std::max(a.g.rope_heads, 1);
-    const int slices = (vdim + 127) / 128;
-    const long long units = (long long)joins * rows * slices;
+    const int slices = many_parts ? 1 : 4, groups = (vdim + slices * kJoinSlice - 1) / (slices * kJoinSlice);
+    const int units = kJoinThreads / 32 / (many_parts ? 4 : 1);
+    const int per_join = (rows * groups + units - 1) / units;
     cudaStream_t s = (cudaStream_t)stream;
-    return (int)(many_parts ? launch_dependent(join_kernel<4>, (int)units, kJoinThreads, s, a, slices, rows)
-                            : launch_dependent(join_kernel<1>, (int)((units + 3) / 4), kJoinThreads, s, a, slices, rows));
+    return (int)(many_parts ? launch_dependent(join_kernel<4, 1>, joins * per_join, kJoinThreads, s, a, groups, per_join)
+                            : launch_dependent(join_kernel<1, 4>, joins * per_join, kJoinThreads, s, a, groups, per_join));
 }
 
 }  // namespace leyline

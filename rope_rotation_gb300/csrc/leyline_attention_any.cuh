@@ -15,6 +15,24 @@ namespace {
 
 __device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
+// cos and sin of pending * theta_j, as a read of a lazy pool forms them (leyline_read.cu): in fp64, rounded once.  Below
+// kTurnSpan^2 by R(a) R(b) = R(a + b) from the pool's two turn tables, past it by sincos.
+__device__ __forceinline__ void pending_trig(int pend, const double* turn, int half, int j, bool bf16, float& c, float& s)
+{
+    const long long n = llabs((long long)pend);
+    double sd, cd;
+    if (n < (long long)kTurnSpan * kTurnSpan) {
+        const double2* tables = reinterpret_cast<const double2*>(turn + (half + 1) / 2 * 2) + (size_t)j * kTurnSpan;
+        const double2 x = tables[n % kTurnSpan], y = tables[(size_t)half * kTurnSpan + n / kTurnSpan];
+        cd = fma(y.x, x.x, -(y.y * x.y));
+        sd = copysign(1.0, (double)pend) * fma(y.y, x.x, y.x * x.y);
+    } else {
+        sincos((double)pend * turn[j], &sd, &cd);
+    }
+    c = bf16 ? __bfloat162float(__double2bfloat16(cd)) : (float)cd;
+    s = bf16 ? __bfloat162float(__double2bfloat16(sd)) : (float)sd;
+}
+
 // Slot of cache row `row` of a table row; -1 (with the status bit) when its page is bad.
 __device__ __forceinline__ long long row_slot(const int32_t* table_row, const Geometry& g, long long row,
                                               int32_t* status)

@@ -37,6 +37,36 @@ __global__ void gather_kernel(const uint4* kv, const int32_t* table_row, const G
 }
 
 // -------------------------------------------------------------------------
+// Lazy pools.  cos / sin of pending * theta_j, formed in fp64 and rounded once to the
+// rotation's arithmetic, as the host does for an eager splice.  A count below
+// kTurnSpan^2 in magnitude takes the angle-addition product of the pool's two turn
+// tables (R(a) R(b) = R(a + b): 2 loads and 6 fp64 operations); a larger one, fp64
+// sincos of the angle.
+__device__ __forceinline__ void pending_trig(int pend, const double* turn, int half, int j, bool bf16, float& c,
+                                             float& s)
+{
+    const long long a = pend < 0 ? -(long long)pend : (long long)pend;
+    double sd, cd;
+    if (a < (long long)kTurnSpan * kTurnSpan) {
+        const double2* lo = reinterpret_cast<const double2*>(turn + (half + 1) / 2 * 2);
+        const double2* hi = lo + (size_t)half * kTurnSpan;
+        const double2 l = lo[(size_t)j * kTurnSpan + (a % kTurnSpan)];
+        const double2 h = hi[(size_t)j * kTurnSpan + (a / kTurnSpan)];
+        cd = fma(h.x, l.x, -(h.y * l.y));
+        sd = fma(h.y, l.x, h.x * l.y);
+        if (pend < 0) sd = -sd;
+    } else {
+        sincos((double)pend * turn[j], &sd, &cd);
+    }
+    if (bf16) {
+        c = __bfloat162float(__double2bfloat16(cd));
+        s = __bfloat162float(__double2bfloat16(sd));
+    } else {
+        c = (float)cd;
+        s = (float)sd;
+    }
+}
+
 // The read kernels run one warp per row.  A warp forms the cos / sin of every pair
 // of a band once per pending count -- a lane per pair, into the warp's slice of
 // shared memory -- and keeps them while the count stays the same (after a splice a
