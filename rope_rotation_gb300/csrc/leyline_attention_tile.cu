@@ -17,8 +17,8 @@
 //              TMA instruction in 100 to 170 cycles, whatever its size, and a thread alone bound the kernel)
 //   warps 9-12 copy the queries (cp.async: any strides), the cache tiles that TMA does not take (block
 //              sizes that 8 does not divide; tiles that end inside, whose other rows are zeroed, since
-//              they meet weights of 0 in the product with V), and in a lazy pool turn the bands
-// In a lazy pool the band of each row is turned by its pending count on the way, in fp32, and goes
+//              they meet weights of 0 in the product with V)
+// In a lazy pool the load warps turn the band of each row by its pending count on the way, in fp32, and it goes
 // to shared memory as the sum of two bf16 values: the scores then carry the turn to 2^-17, not to the
 // 2^-9 of one bf16 rounding, which the other rows do not have either.
 //
@@ -73,7 +73,7 @@ struct Layout {
     int band, low;      // regions in a stage
     int stage, stage_bytes, stages;
     int p, misc;
-    int trig;           // lazy pools: cos, sin of the last pending count of each copy warp
+    int trig;           // lazy pools: cos, sin of the last pending count of each load warp
     int bytes;
 };
 
@@ -94,7 +94,7 @@ __host__ __device__ constexpr Layout make_layout(bool mla, bool lazy, bool whole
     l.p = l.stage + stages * l.stage_bytes;
     l.misc = l.p + l.rows * 128;
     l.trig = l.misc + (int)sizeof(Misc);
-    l.bytes = l.trig + (lazy ? kCopyWarps * 32 * keys * (int)sizeof(float2) : 0) + 1024;  // and room to align the start
+    l.bytes = l.trig + (lazy ? kLoadWarps * 32 * keys * (int)sizeof(float2) : 0) + 1024;  // and room to align the start
     return l;
 }
 
@@ -113,13 +113,13 @@ __device__ __forceinline__ int padded_rows(int rows) { return (rows + 15) & ~15;
 // -------------------------------------------------------------------- loads --
 // One lane of each load warp: the boxes of the 16 rows of PV's step `step`, the next tile's table entries in flight
 // meanwhile.
-template <bool kMla, bool kLazy, int kKeys>
+template <bool kMla, int kKeys>
 __device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& maps, const Layout& l, Misc* m, uint32_t smem,
                                            int step)
 {
     const bool wide = maps.box == 16;
     const int boxes = wide ? 1 : 2;  // of two groups of 8 rows, or one each
-    const bool bands = !kLazy && !maps.whole;
+    const bool bands = !maps.whole;
     const uint32_t bytes = (l.row_chunks + (bands ? kKeys : 0)) * (kRegionChunk / kSteps);
     const int layer_groups = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
     Ring ring;
@@ -169,12 +169,216 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& ma
     }
 }
 
-// ------------------------------------------------------------------- copies --
+// Place of 16 bytes `v` of row `row` of a tile in a region whose groups hold `chunks` chunks.
+__device__ __forceinline__ uint32_t place(uint32_t region, int chunks, int chunk, int row, int v)
+{
+    return region + ((row / 8) * chunks + chunk) * kAtomBytes + (row & 7) * 128 + ((v ^ (row & 7)) << 4);
+}
+
 __device__ __forceinline__ void store(uint32_t at, const uint4& y)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
 }
 
+// Lazy pools: the bands of a load warp's 16 rows of a tile, turned by their pending counts, to the stage as high and low
+// parts.  The 8 lanes of a row have 16 bytes of each of its chunks; a lane's rows are 16 step + lane / 8 + 4 r.
+template <int kKeys>
+struct Turner {
+    const AttnArgs& a;
+    const Layout& l;
+    float2* cs;  // cos, sin of `count`, this warp's
+    int lane, v, r0;
+    int count;
+    bool valid;
+
+    __device__ __forceinline__ void ensure(int c)
+    {
+        if (valid && c == count) return;
+        const bool bf16 = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
+        __syncwarp();
+        for (int j = lane; j < 32 * kKeys; j += 32) {
+            float co, si;
+            pending_trig(c, a.turn, 32 * kKeys, j, bf16, co, si);
+            cs[j] = make_float2(co, si);
+        }
+        __syncwarp();
+        count = c;
+        valid = true;
+    }
+
+    // Chunk c of the rows whose count is `count`; other: the partner lane's 16 bytes, where a band is one chunk.
+    template <bool kNaive, bool kHalfSplit>
+    __device__ __forceinline__ void turn_chunk(int c, const uint4 (&x)[4][kKeys], const uint4 (&other)[4],
+                                               const int (&pend)[4], uint32_t stage) const
+    {
+        float co[8], si[8];  // half-split: of 8 pairs, one value of each here, sin negative in first halves; else of 4
+        const bool first = kKeys == 1 ? v < 4 : c < kKeys / 2;
+        const int pair = kKeys == 1 ? 8 * (v & 3) : 64 * (c % (kKeys > 1 ? kKeys / 2 : 1)) + 8 * v;
+#pragma unroll
+        for (int k = 0; k < (kHalfSplit ? 8 : 4); ++k) {
+            const float2 t = cs[kHalfSplit ? pair + k : 32 * c + 4 * v + k];
+            co[k] = t.x;
+            si[k] = kHalfSplit && first ? -t.y : t.y;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t* xw = reinterpret_cast<const uint32_t*>(&x[r][c]);
+            // half-split: the other halves of this chunk's pairs
+            const uint32_t* ow = reinterpret_cast<const uint32_t*>(kKeys == 1 ? &other[r] : &x[r][(c + kKeys / 2) % kKeys]);
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float x0 = bf16_lo(xw[k]), x1 = bf16_hi(xw[k]);
+                float q0, q1;
+                if (kHalfSplit) {  // x' = x c - y s of the first half, y' = y c + x s of the second
+                    const float y0 = bf16_lo(ow[k]) * si[2 * k], y1 = bf16_hi(ow[k]) * si[2 * k + 1];
+                    q0 = kNaive ? round_bf16(x0 * co[2 * k]) + round_bf16(y0) : fmaf(x0, co[2 * k], y0);
+                    q1 = kNaive ? round_bf16(x1 * co[2 * k + 1]) + round_bf16(y1) : fmaf(x1, co[2 * k + 1], y1);
+                } else if (kNaive) {
+                    turn_bf16(x0, x1, co[k], si[k], q0, q1);
+                } else {
+                    turn_fp32(x0, x1, co[k], si[k], q0, q1);
+                }
+                hw[k] = pack_bf16x2(q0, q1);
+                // the naive arm's result is the rounded one
+                lw[k] = kNaive ? 0u : pack_bf16x2(q0 - bf16_lo(hw[k]), q1 - bf16_hi(hw[k]));
+            }
+            if (pend[r] == count) {
+                store(place(stage + l.band, kKeys, c, r0 + 4 * r, v), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+                store(place(stage + l.low, kKeys, c, r0 + 4 * r, v), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+            }
+        }
+    }
+
+    // x, pend: this lane's rows.  Mostly all rows of a warp share a count: then one pass, in which the four rows' chains
+    // run side by side (a row at a time took 1000 cycles each, by the warps that also copy the rows, and bound the
+    // kernel: 64 requests of 16 heads over 4000 rows LAZY_US); else a pass for each count.
+    __device__ __forceinline__ void rows(const uint4 (&x)[4][kKeys], const int (&pend)[4], uint32_t stage)
+    {
+        const bool naive = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
+        const bool half_split = a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
+        uint4 other[4];
+        if (kKeys == 1 && half_split) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) other[r] = shfl_xor_vec(x[r][0], 4);
+        }
+        unsigned left = 15;
+        for (;;) {
+            const unsigned lanes = __ballot_sync(0xffffffffu, left != 0);
+            if (lanes == 0) return;
+            int mine = pend[3];
+#pragma unroll
+            for (int r = 2; r >= 0; --r)
+                if (left >> r & 1) mine = pend[r];
+            const int c0 = __shfl_sync(0xffffffffu, mine, __ffs(lanes) - 1);
+            if (c0 == 0) {
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (pend[r] == 0) {
+                            store(place(stage + l.band, kKeys, c, r0 + 4 * r, v), x[r][c]);
+                            store(place(stage + l.low, kKeys, c, r0 + 4 * r, v), make_uint4(0, 0, 0, 0));
+                        }
+            } else {
+                ensure(c0);
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) {
+                    if (half_split) {
+                        if (naive) turn_chunk<true, true>(c, x, other, pend, stage);
+                        else turn_chunk<false, true>(c, x, other, pend, stage);
+                    } else {
+                        if (naive) turn_chunk<true, false>(c, x, other, pend, stage);
+                        else turn_chunk<false, false>(c, x, other, pend, stage);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (pend[r] == c0) left &= ~(1u << r);
+        }
+    }
+};
+
+// The load warps in a lazy pool: one lane issues the boxes of its 16 rows' values, then the whole warp turns their bands,
+// which were read while it waited for the stage.
+template <bool kMla, int kKeys>
+__device__ __forceinline__ void load_lazy(const AttnArgs& a, const TileMaps& maps, const Layout& l, Misc* m, uint32_t smem,
+                                          int step, float2* trig)
+{
+    const Geometry& g = a.g;
+    const int lane = threadIdx.x & 31, v = lane & 7, r0 = 16 * step + lane / 8;
+    const bool wide = maps.box == 16;
+    const int layer_groups = (int)((long long)a.layer * g.num_pages * g.block_size / 8);
+    Turner<kKeys> turner{a, l, trig, lane, v, r0, 0, false};
+    Ring ring;
+    for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i) {
+        const Work w = load_work(a, i);
+        const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        const int value_plane = kMla ? 0 : w.it.band * l.values, band_vec = kMla ? 0 : w.it.band * kKeys * 8;
+        // pages two tiles ahead, bands and counts one
+        PageOf next[4], box_next[2];
+        long long box_slot[2];
+        uint4 x[4][kKeys];
+        int pend[4];
+        auto look_up = [&](long long key) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) next[k] = page_of(a, maps, w, table_row, key + r0 + 4 * k);
+            if (!by_box(maps, w, key)) return;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) box_next[k] = page_of(a, maps, w, table_row, key + 16 * step + 8 * k);
+        };
+        auto read = [&](long long key) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const long long slot = slot_of(a, next[k]);
+                const uint4* band = a.kv + band_off(g, a.layer, max(slot, 0ll)) + band_vec + v;
+                pend[k] = slot >= 0 ? a.pending[slot] : 0;
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) x[k][c] = slot >= 0 ? ld_stream(band + 8 * c) : make_uint4(0, 0, 0, 0);
+            }
+            if (!by_box(maps, w, key)) return;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) box_slot[k] = slot_of(a, box_next[k]);
+        };
+        if (w.tiles > 0) {
+            look_up(w.it.key0);
+            read(w.it.key0);
+            if (w.tiles > 1) look_up(w.it.key0 + kAttnKeys);
+        }
+        for (int t = 0; t < w.tiles; ++t) {
+            const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            const uint32_t full = smem_addr(&m->full[ring.stage]);
+            const uint32_t stage = smem + l.stage + ring.stage * l.stage_bytes;
+            if (!warp_wait(smem_addr(&m->empty[ring.stage][step]), ring.phase ^ 1, &m->quit, a.status)) return;
+            if (elect_lane()) {
+                if (by_box(maps, w, key)) {
+                    mbar_expect_tx(full, l.row_chunks * (kRegionChunk / kSteps));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (wide && k == 1) break;
+                        const int y = box_slot[k] >= 0 ? layer_groups + (int)(box_slot[k] >> 3) : -2;
+                        tma_box4(stage + (2 * step + k) * l.row_chunks * kAtomBytes, &maps.rows, value_plane, y, full);
+                    }
+                } else {
+                    mbar_arrive(full);
+                }
+            }
+            __syncwarp();
+            turner.rows(x, pend, stage);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            if (t + 1 < w.tiles) {
+                read(key + kAttnKeys);
+                if (t + 2 < w.tiles) look_up(key + 2 * kAttnKeys);
+            }
+            ring.advance(l.stages);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- copies --
 template <bool kMla, bool kLazy, int kKeys>
 struct Copier {
     const AttnArgs& a;
@@ -182,92 +386,15 @@ struct Copier {
     const Layout& l;
     Misc* m;
     uint32_t smem;
-    float2* trig;    // this warp's
     int tid, v, r0;  // 16-byte chunk of a 128-byte row segment, first row
-    int trig_count;  // pending count whose cos / sin this warp's slice holds
-    bool trig_valid;
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, &m->quit, a.status); }
 
-    // This lane's 8 values of each chunk of a row's band, turned by the row's pending count, as hi + lo (all 32
-    // lanes; the 8 lanes of a row share `pend`).
-    __device__ __forceinline__ void turned(const uint4 (&x)[kKeys], int pend, uint4 (&hi)[kKeys], uint4 (&lo)[kKeys])
-    {
-        const bool bf16 = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
-        const bool half_split = a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
-        constexpr int kHalf = 32 * kKeys;  // pairs
-        const int lane = tid & 31;
-        unsigned todo = __ballot_sync(0xffffffffu, pend != 0);
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c) {
-            hi[c] = x[c];
-            lo[c] = make_uint4(0, 0, 0, 0);
-        }
-        if (todo == 0) return;
-        const uint4 other = kKeys == 1 ? shfl_xor_vec(x[0], 4) : x[0];
-        while (todo) {  // once per distinct count among the warp's rows
-            const int count = __shfl_sync(0xffffffffu, pend, __ffs(todo) - 1);
-            float2* cs = trig;
-            if (!trig_valid || trig_count != count) {
-                __syncwarp();
-                for (int j = lane; j < kHalf; j += 32) {
-                    float c, s;
-                    pending_trig(count, a.turn, kHalf, j, bf16, c, s);
-                    cs[j] = make_float2(c, s);
-                }
-                __syncwarp();
-                trig_valid = true;
-                trig_count = count;
-            }
-            if (pend == count) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) {
-                    const uint32_t* xw = reinterpret_cast<const uint32_t*>(&x[c]);
-                    // half-split: the other halves of this chunk's pairs
-                    const uint32_t* ow = reinterpret_cast<const uint32_t*>(kKeys == 1 ? &other : &x[(c + kKeys / 2) % kKeys]);
-                    const bool first = kKeys == 1 ? v < 4 : c < kKeys / 2;
-                    const int pair = kKeys == 1 ? 8 * (v & 3) : 64 * (c % (kKeys > 1 ? kKeys / 2 : 1)) + 8 * v;
-                    uint32_t *hw = reinterpret_cast<uint32_t*>(&hi[c]), *lw = reinterpret_cast<uint32_t*>(&lo[c]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float x0 = bf16_lo(xw[k]), x1 = bf16_hi(xw[k]);
-                        float q0, q1;
-                        if (half_split) {  // x' = x c - y s of the first half, y' = y c + x s of the second
-                            const float2 t0 = cs[pair + 2 * k], t1 = cs[pair + 2 * k + 1];
-                            const float sgn = first ? -1.f : 1.f;
-                            const float y0 = bf16_lo(ow[k]), y1 = bf16_hi(ow[k]);
-                            if (bf16) {
-                                q0 = round_bf16(x0 * t0.x) + sgn * round_bf16(y0 * t0.y);
-                                q1 = round_bf16(x1 * t1.x) + sgn * round_bf16(y1 * t1.y);
-                            } else {
-                                q0 = fmaf(x0, t0.x, sgn * (y0 * t0.y));
-                                q1 = fmaf(x1, t1.x, sgn * (y1 * t1.y));
-                            }
-                        } else {
-                            const float2 t = cs[32 * c + 4 * v + k];
-                            if (bf16) turn_bf16(x0, x1, t.x, t.y, q0, q1);
-                            else turn_fp32(x0, x1, t.x, t.y, q0, q1);
-                        }
-                        hw[k] = pack_bf16x2(q0, q1);
-                        // the naive arm's result is the rounded one
-                        lw[k] = bf16 ? 0u : pack_bf16x2(q0 - bf16_lo(hw[k]), q1 - bf16_hi(hw[k]));
-                    }
-                }
-            }
-            todo &= ~__ballot_sync(0xffffffffu, pend == count);
-        }
-    }
-
-    // This thread's 16 bytes of row `row` in a chunk of the queries, and in a region of a stage with `chunks` chunks a group.
+    // This thread's 16 bytes of row `row` in a chunk.
     __device__ __forceinline__ uint32_t q_place(int chunk, int row) const
     {
         return smem + chunk * l.q_chunk_bytes + row * 128 + ((v ^ (row & 7)) << 4);
     }
-    __device__ __forceinline__ uint32_t place(uint32_t region, int chunks, int chunk, int row) const
-    {
-        return region + ((row / 8) * chunks + chunk) * kAtomBytes + (row & 7) * 128 + ((v ^ (row & 7)) << 4);
-    }
-
     __device__ __forceinline__ void queries(const Work& w)
     {
         const int group = a.q_heads / (kMla ? 1 : a.g.rope_heads);
@@ -298,7 +425,6 @@ struct Copier {
         const int values = kMla ? 8 : l.values;
         Ring ring;
         uint32_t q_phase = 0;
-        trig_valid = false;
         for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i) {
             const Work w = load_work(a, i);
             if (w.tiles == 0) continue;
@@ -309,67 +435,41 @@ struct Copier {
             const int value_vec = kMla ? 0 : w.it.band * values * 8, band_vec = kMla ? 0 : w.it.band * kKeys * 8;
             PageOf next[4];  // of rows r0 + 16 k of the tile to come
             auto look_up = [&](long long key) {
-                if (by_box(maps, w, key) && !kLazy) return;
+                if (by_box(maps, w, key)) return;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) next[k] = page_of(a, maps, w, table_row, key + r0 + 16 * k);
             };
             look_up(w.it.key0);
             for (int t = 0; t < w.tiles; ++t) {
                 const long long key = w.it.key0 + (long long)t * kAttnKeys;
-                const bool box = by_box(maps, w, key);
                 const uint32_t full = smem_addr(&m->full[ring.stage]);
                 const uint32_t stage = smem + l.stage + ring.stage * l.stage_bytes;
-                if (box && !kLazy) {  // the load warp's tile: only these warps' arrivals
+                if (by_box(maps, w, key)) {  // the load warps' tile: only these warps' arrivals
                     look_up(key + kAttnKeys);
                     if (!wait(smem_addr(&m->empty[ring.stage][kSteps - 1]), ring.phase ^ 1)) return;
                     if (tid % 32 == 0) mbar_arrive_n(full, 32);
                     ring.advance(l.stages);
                     continue;
                 }
-                long long slot[4];  // < 0: not loaded
-                uint4 x[kLazy ? 4 : 1][kKeys];
-                int pend[4];
+                int slot[4];  // < 0: not loaded (a pool's rows that TMA can name are numbered in 32 bits)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    slot[k] = slot_of(a, next[k]);
-                    if (kLazy) {  // on the way while the values are copied
-                        const uint4* band = a.kv + band_off(g, a.layer, max(slot[k], 0ll)) + band_vec + v;
-                        pend[k] = slot[k] >= 0 ? a.pending[slot[k]] : 0;
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c)
-                            x[k][c] = slot[k] >= 0 ? ld_stream(band + 8 * c) : make_uint4(0, 0, 0, 0);
-                    }
-                }
+                for (int k = 0; k < 4; ++k) slot[k] = (int)slot_of(a, next[k]);
                 if (t + 1 < w.tiles) look_up(key + kAttnKeys);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {  // rows r0 + 16 k are freed by PV's step k
                     const int r = r0 + 16 * k;
                     if (!wait(smem_addr(&m->empty[ring.stage][k]), ring.phase ^ 1)) return;
-                    if (box) continue;
-                    const uint4* val = a.kv + lat_off(g, a.layer, max(slot[k], 0ll)) + value_vec + v;
+                    const uint4* val = a.kv + lat_off(g, a.layer, max(slot[k], 0)) + value_vec + v;
 #pragma unroll kMla ? 8 : 1
-                    for (int c = 0; c < values; ++c) cp_async16(place(stage, l.row_chunks, c, r), val + 8 * c, slot[k] >= 0);
-                    if (!kLazy) {
-                        const uint4* band = a.kv + band_off(g, a.layer, max(slot[k], 0ll)) + band_vec + v;
+                    for (int c = 0; c < values; ++c) cp_async16(place(stage, l.row_chunks, c, r, v), val + 8 * c, slot[k] >= 0);
+                    if (!kLazy) {  // (in a lazy pool the load warps bring the bands)
+                        const uint4* band = a.kv + band_off(g, a.layer, max(slot[k], 0)) + band_vec + v;
 #pragma unroll
                         for (int c = 0; c < kKeys; ++c)
-                            cp_async16(maps.whole ? place(stage, l.row_chunks, values + c, r) : place(stage + l.band, kKeys, c, r),
+                            cp_async16(maps.whole ? place(stage, l.row_chunks, values + c, r, v)
+                                                  : place(stage + l.band, kKeys, c, r, v),
                                        band + 8 * c, slot[k] >= 0);
                     }
-                }
-                if (kLazy) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint4 hi[kKeys], lo[kKeys];
-                        turned(x[kLazy ? k : 0], pend[k], hi, lo);
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c) {
-                            store(place(stage + l.band, kKeys, c, r0 + 16 * k), hi[c]);
-                            store(place(stage + l.low, kKeys, c, r0 + 16 * k), lo[c]);
-                        }
-                    }
-                    fence_async_smem();
-                    mbar_arrive(full);
                 }
                 cp_async_arrive(full);  // when the copies have landed
                 ring.advance(l.stages);
@@ -684,8 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            // the load warps and every copy thread (lazy pools: and again for the turned bands)
-            mbar_init(smem_addr(&m->full[s]), kLoadWarps + (kLazy ? 2 : 1) * kCopyThreads);
+            // the load warps (lazy pools: and again for the turned bands) and every copy thread
+            mbar_init(smem_addr(&m->full[s]), (kLazy ? 2 : 1) * kLoadWarps + kCopyThreads);
             for (int k = 0; k < kSteps; ++k) mbar_init(smem_addr(&m->empty[s][k]), 1);
         }
         mbar_init(smem_addr(&m->q_full), kCopyThreads);
@@ -718,12 +818,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         while (!mbar_try(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
         }
     } else if (warp < kLoadWarp + kLoadWarps) {
-        if (elect_lane()) load_tiles<kMla, kLazy, kKeys>(a, maps, l, m, smem, warp - kLoadWarp);
-        __syncwarp();
+        const int step = warp - kLoadWarp;
+        if (kLazy) {
+            float2* trig = reinterpret_cast<float2*>(raw + (smem - smem_addr(raw)) + l.trig) + step * 32 * kKeys;
+            load_lazy<kMla, kKeys>(a, maps, l, m, smem, step, trig);
+        } else {
+            if (elect_lane()) load_tiles<kMla, kKeys>(a, maps, l, m, smem, step);
+            __syncwarp();
+        }
     } else {
         const int tid = threadIdx.x - 32 * (kLoadWarp + kLoadWarps);
-        float2* trig = reinterpret_cast<float2*>(raw + (smem - smem_addr(raw)) + l.trig) + tid / 32 * 32 * kKeys;
-        Copier<kMla, kLazy, kKeys> c{a, maps, l, m, smem, trig, tid, tid % 8, tid / 8, 0, false};
+        Copier<kMla, kLazy, kKeys> c{a, maps, l, m, smem, tid, tid % 8, tid / 8};
         c.run();
         cp_async_wait_all();
     }
