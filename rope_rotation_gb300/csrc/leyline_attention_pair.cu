@@ -12,12 +12,17 @@
 // The reference maximum of a row is that of its item's first tile and stays: weights are exp2(x - m0), in bf16 and
 // fp32 as exact relative to their size as any.  A later score above m0 by more than 80 (as a power of 2) could leave
 // fp32's range in the sums; the item is then marked, as is one whose output is not finite, and computed
-// again at the end without the tensor cores (leyline_attention_any.cuh).  So O never has to be rescaled, which would take both CTAs to agree in the
-// middle of every tile.
+// again at the end without the tensor cores (leyline_attention_any.cuh).  So O never has to be rescaled, which would
+// take both CTAs to agree in the middle of every tile.
 //
 // Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
 // K and 7-10 V (TMA, one lane each: a thread issues a TMA instruction in 100 to 170 cycles, whatever its size, and a
 // thread alone bound the kernel), warps 11-14 copy the queries and the tiles that end inside.
+//
+// Bounds and measurements (GB300; cuBLAS bf16 at 1875 TFLOP/s).  The products take 864 + 512 cycles a tile, all of it
+// 1530, and an item's ends 13000.  A prompt chunk of 512 tokens of 128 heads over 8192 rows 737 us (1.54 PFLOP/s, 0.82 of
+// measured), ragged chunks of 61 tokens of 16 heads 148 us (1.2), 16 decodes of 128 heads over 24000 rows 120 us (4.9 TB/s,
+// 0.73 of measured copies; 1.2 PFLOP/s).
 #include "leyline_attention.cuh"
 
 namespace leyline {
