@@ -448,7 +448,8 @@ typedef struct {
 int leyline_batch_create(leyline_pool_t* pool, int32_t max_chunks, int32_t max_tokens, int32_t q_heads,
                          leyline_batch_t** out);
 
-/* Wait for the pool's enqueued work and free the batch. */
+/* Wait for the pool's enqueued work and free the batch.  Graphs that hold its calls
+ * cannot be replayed afterwards. */
 int leyline_batch_destroy(leyline_batch_t* batch);
 
 /* Plan a step: validate the chunks against seq_lens_host, take pages for rows past

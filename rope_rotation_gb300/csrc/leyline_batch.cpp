@@ -56,15 +56,15 @@ namespace {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The plan's device buffer: header, then chunks, items, per-CTA ranges and joins.
+// The plan's device buffer: header, chunks, per-CTA ranges and joins, and last the items, of which a plan copies its own.
 BatchLayout make_layout(int32_t max_chunks, int64_t max_tiles, int32_t ctas)
 {
     BatchLayout l;
     l.chunks = align_up(sizeof(BatchHeader), 16);
-    l.items = align_up(l.chunks + sizeof(ChunkDev) * (size_t)max_chunks, 16);
-    l.cta_begin = align_up(l.items + sizeof(AttnItem) * (size_t)(max_tiles + ctas), 16);
+    l.cta_begin = align_up(l.chunks + sizeof(ChunkDev) * (size_t)max_chunks, 16);
     l.joins = align_up(l.cta_begin + sizeof(int32_t) * (size_t)(ctas + 1), 16);
-    l.bytes = align_up(l.joins + sizeof(AttnJoin) * (size_t)ctas, 16);
+    l.items = align_up(l.joins + sizeof(AttnJoin) * (size_t)ctas, 16);
+    l.bytes = align_up(l.items + sizeof(AttnItem) * (size_t)(max_tiles + ctas), 16);
     return l;
 }
 
@@ -273,7 +273,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     a.staged = reinterpret_cast<const uint4*>(h);
     a.plan = reinterpret_cast<uint4*>(b->d_plan);
     a.runs = reinterpret_cast<const PlanRun*>(h + l.bytes);
-    a.plan_vecs = (int64_t)(l.bytes / 16);
+    a.plan_vecs = (int64_t)((l.items + sizeof(AttnItem) * (size_t)split.n_items) / 16);
     a.n_runs = (int32_t)cp.runs.size();
     a.max_blocks = bt->max_blocks;
     a.table = bt->table;

@@ -86,7 +86,7 @@ struct PlanRun {
 
 // Where the parts of the plan lie in the batch's device buffer (bytes).
 struct BatchLayout {
-    size_t chunks, items, cta_begin, joins, bytes;
+    size_t chunks, cta_begin, joins, items, bytes;
 };
 
 // Validated chunks of a plan and the pages they take.
@@ -200,6 +200,8 @@ struct AttnArgs {
     int32_t* status;
     Geometry g;
 };
+
+static_assert(sizeof(AttnItem) % 16 == 0, "plans are copied in 16-byte vectors");
 
 // Widest rows attention takes (leyline_batch_create checks them).
 constexpr int kAttnMaxValue = 1024;
