@@ -17,12 +17,13 @@
 //
 // Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
 // K and 7-10 V (TMA, one lane each: a thread issues a TMA instruction in 100 to 170 cycles, whatever its size, and a
-// thread alone bound the kernel), warps 11-14 copy the queries and the tiles that end inside.
+// thread alone bound the kernel; where 8 does not divide the block size they copy their rows, a warp each), warps
+// 11-14 copy the queries and the tiles that end inside.
 //
 // Bounds and measurements (GB300; cuBLAS bf16 at 1875 TFLOP/s).  The products take 864 + 512 cycles a tile, all of it
 // 1530, and an item's ends 13000.  A prompt chunk of 512 tokens of 128 heads over 8192 rows 737 us (1.54 PFLOP/s, 0.82 of
 // measured), ragged chunks of 61 tokens of 16 heads 148 us (1.2), 16 decodes of 128 heads over 24000 rows 120 us (4.9 TB/s,
-// 0.73 of measured copies; 1.2 PFLOP/s).
+// 0.73 of measured copies; 1.2 PFLOP/s).  One row a page, copied: 835, 198 and 143 us (by single CTAs 1426, 255 and 213).
 #include "leyline_attention.cuh"
 
 namespace leyline {
@@ -179,7 +180,81 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, const TileMaps& ma
     }
 }
 
-// Queries of this CTA's rows, and tiles that end inside: 16-byte copies, zeros for rows past the end.
+// Pools whose block size 8 does not divide: the same warps copy their 16 rows of every tile (zeros past the end), all lanes
+// 16 bytes at a time; pages are looked up two tiles ahead, and lines asked into L2 one ahead.
+template <bool kValues>
+__device__ __forceinline__ void copy_rows(const AttnArgs& a, const TileMaps& maps, Misc* m, uint32_t smem, uint32_t rank,
+                                          int part)
+{
+    const Geometry& g = a.g;
+    const int pair = blockIdx.x / 2, lane = threadIdx.x & 31, v = lane % 8, r0 = 16 * part + lane / 8;
+    const int first = kValues ? 0 : (int)rank * kHalfKeys;
+    const int chunks = maps.whole ? 9 : 8;
+    Ring ring;
+    for (int i = a.cta_begin[pair]; i < a.cta_begin[pair + 1]; ++i) {
+        const Work w = load_work(a, i);
+        const bool prefetch = !kValues && w.ch.n * a.q_heads <= kPrefetchTiles * kPairRows;
+        const int32_t* table_row = a.header->table + (long long)w.ch.req * a.header->max_blocks;
+        PageOf at[4], next[4];
+        auto look_up = [&](PageOf (&p)[4], long long key) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = page_of(a, maps, w, table_row, key + first + r0 + 4 * k);
+        };
+        look_up(at, w.it.key0);
+        look_up(next, w.it.key0 + kAttnKeys);
+        for (int t = 0; t < w.tiles; ++t) {
+            const long long key = w.it.key0 + (long long)t * kAttnKeys;
+            int slot[4];  // < 0: zeros
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                slot[k] = (int)slot_of(a, at[k]);
+                at[k] = next[k];
+            }
+            look_up(next, key + 2 * kAttnKeys);
+            if (!pair_warp_wait(smem_addr(kValues ? &m->v_empty[ring.stage][part] : &m->k_empty[ring.stage]), ring.phase ^ 1, m,
+                                a.status))
+                return;
+            const uint32_t dst = smem + (kValues ? kValueOff + ring.stage * kValueBytes : kKeyOff + ring.stage * kKeyBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + 4 * k;
+                const uint4* lat = a.kv + lat_off(g, a.layer, max(slot[k], 0)) + v;
+                const uint32_t in = (r & 7) * 128 + ((v ^ (r & 7)) << 4);
+                if (kValues) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        cp_async16(dst + (r / 8) * kValueGroup + c * kAtomBytes + in, lat + 8 * (4 * (c / 2) + 2 * (int)rank + c % 2),
+                                   slot[k] >= 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        cp_async16(dst + ((r / 8) * chunks + c) * kAtomBytes + in, lat + 8 * c, slot[k] >= 0);
+                    cp_async16(dst + (maps.whole ? ((r / 8) * 9 + 8) * kAtomBytes : kBandOff + (r / 8) * kAtomBytes) + in,
+                               a.kv + band_off(g, a.layer, max(slot[k], 0)) + v, slot[k] >= 0);
+                }
+            }
+            if (prefetch && t + 1 < w.tiles) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (at[k].page < 0 || at[k].page >= g.num_pages) continue;
+                    const int s = at[k].page * (int)g.block_size + at[k].off;
+                    prefetch_line(a.kv + lat_off(g, a.layer, s) + 8 * v);
+                    if (v == 0) prefetch_line(a.kv + band_off(g, a.layer, s));
+                }
+            }
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            // as many arrivals as the copy warps of both CTAs
+            if (lane < kCopyWarps / (kValues ? kSteps : kKeyWarps))
+                cluster_arrive_smem(cluster_addr(smem_addr(kValues ? &m->v_full[ring.stage] : &m->k_full[ring.stage]), 0));
+            ring.advance(kStages);
+        }
+    }
+}
+
+// Queries of this CTA's rows, and tiles that end inside (where TMA takes the others): 16-byte copies, zeros for rows past
+// the end.
 __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const TileMaps& maps, Misc* m, uint32_t smem, uint32_t rank)
 {
     const Geometry& g = a.g;
@@ -219,7 +294,7 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const TileMaps& ma
         const int stage = (ring_tiles + w.tiles - 1) % kStages;
         ring_tiles += w.tiles;
         const long long key = w.it.key0 + (long long)(w.tiles - 1) * kAttnKeys;
-        if (by_box(maps, w, key)) continue;
+        if (maps.box == 0 || by_box(maps, w, key)) continue;
         if (!pair_warp_wait(smem_addr(&m->tail_k[stage]), tail_phase >> stage & 1, m, a.status)) return;
         const uint32_t keys = smem + kKeyOff + stage * kKeyBytes, values = smem + kValueOff + stage * kValueBytes;
 #pragma unroll
@@ -533,10 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_pair_kernel(const __grid_c
             }
         }
     } else if (warp < kValueWarp) {
-        if (elect_lane()) load_tiles<false>(a, maps, m, smem, rank, warp - kKeyWarp);
+        if (maps.box == 0) copy_rows<false>(a, maps, m, smem, rank, warp - kKeyWarp);
+        else if (elect_lane()) load_tiles<false>(a, maps, m, smem, rank, warp - kKeyWarp);
         __syncwarp();
     } else if (warp < kCopyWarp) {
-        if (elect_lane()) load_tiles<true>(a, maps, m, smem, rank, warp - kValueWarp);
+        if (maps.box == 0) copy_rows<true>(a, maps, m, smem, rank, warp - kValueWarp);
+        else if (elect_lane()) load_tiles<true>(a, maps, m, smem, rank, warp - kValueWarp);
         __syncwarp();
     } else {
         copy_tiles(a, maps, m, smem, rank);
@@ -579,12 +656,13 @@ int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps)
     // values: 64 columns, 8 rows, planes of a half of the latent, halves, groups; a box takes two planes of both halves
     const cuuint64_t v_dims[5] = {64, 8, 4, 2, n}, v_strides[4] = {row, 128, 512, 8 * row};
     const cuuint32_t v_box[5] = {64, 8, 2, 2, groups};
-    if (encode(&maps->pair_keys, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, k_dims, k_strides, k_box, ones,
+    if (maps->box > 0 &&
+        (encode(&maps->pair_keys, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, k_dims, k_strides, k_box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
         encode(&maps->pair_values, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, v_dims, v_strides, v_box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS))
         return (int)cudaErrorInvalidValue;
     return (int)cudaFuncSetAttribute(attend_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }

@@ -218,7 +218,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g, p->kv, &b->maps);
     if (e == cudaSuccess && attention_takes_tiles(g))
         e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
-    if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending && b->maps.box > 0) {
+    if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending) {
         b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows, kItemCostPairs};
         e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
     }
@@ -258,7 +258,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     if (!cp.chunks.empty()) memcpy(h + l.chunks, cp.chunks.data(), sizeof(ChunkDev) * cp.chunks.size());
     Split split{reinterpret_cast<AttnItem*>(h + l.items), reinterpret_cast<int32_t*>(h + l.cta_begin),
                 reinterpret_cast<AttnJoin*>(h + l.joins)};
-    const bool pairs = b->pair_shape.ctas > 0 && pairs_are_faster(b->shape, cp.chunks);
+    const bool pairs = b->pair_shape.ctas > 0 && pairs_are_faster(b->shape, cp.chunks, b->maps.box == 0);
     split_work(pairs ? b->pair_shape : b->shape, cp.chunks, &split);
     BatchHeader hd{};
     hd.table = bt->table;

@@ -128,7 +128,7 @@ struct Split {
     int32_t n_parts = 0;
 };
 void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out);
-bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks);
+bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks, bool copied = false);
 
 struct HeadsView {
     void* ptr;
@@ -226,7 +226,7 @@ int launch_rotate(const RotateArgs& a, int64_t tokens, int sm_count, void* strea
 bool attention_takes_tiles(const Geometry& g);
 int attention_tile_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_tile(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
-// Attention by pairs of CTAs (leyline_attention_pair.cu), for MLA rows whose tiles come by TMA; after
+// Attention by pairs of CTAs (leyline_attention_pair.cu), for MLA rows of eager pools; after
 // attention_tile_prepare.
 int attention_pair_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, void* stream);

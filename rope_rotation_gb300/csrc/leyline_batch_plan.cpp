@@ -185,17 +185,19 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
 // 3800 cycles and 10 for each query row, a pair 1900 for up to 128; an item costs a pair more at its ends, and the call
 // 4000 cycles more to start.  16 requests decode over 24000 rows: 16 heads 111 us by CTAs, 107 by pairs, 64 heads 124,
 // 113, 128 heads 206, 123; 64 over 4000 rows: 16 heads 78, 81, 64 heads 92, 90; one over 32768: 16 heads 18, 21, 128 heads
-// 28, 25; 300 over 130 rows: 64 heads 36, 40.
-bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks)
+// 28, 25; 300 over 130 rows: 64 heads 36, 40.  Rows that are copied one by one (`copied`: block sizes that 8 does not
+// divide) take a pair 2450 a tile, a CTA no more than the others: 16 over 24000 rows, 64 heads 129, 140, 128 heads 213, 143.
+bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks, bool copied)
 {
-    constexpr int64_t kTile = 3800, kTileRow = 10, kTileItem = 8400, kPairTile = 1900, kPairItem = 12000, kPairStart = 4000;
+    constexpr int64_t kTile = 3800, kTileRow = 10, kTileItem = 8400, kPairItem = 12000, kPairStart = 4000;
+    const int64_t pair_tile = copied ? 2450 : 1900;
     const int64_t pairs = w.ctas / 2;
     int64_t single = kTileItem * w.ctas, pair = kPairItem * pairs;  // as many items are cut
     for (const ChunkDev& c : chunks) {
         const int64_t rows = (int64_t)c.n * w.group, keys = ceil_div(c.start + c.n, kAttnKeys);
         const int64_t tiles = ceil_div(rows, kAttnRows), pair_tiles = ceil_div(rows, kPairRows);
         single += tiles * (keys * kTile + kTileItem) + rows * keys * kTileRow;
-        pair += pair_tiles * (keys * kPairTile + kPairItem);
+        pair += pair_tiles * (keys * pair_tile + kPairItem);
     }
     return single * pairs > (pair + kPairStart * pairs) * w.ctas;
 }

@@ -248,6 +248,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                  : "memory");
 }
 
+// Ask for the 128-byte line at `p` to be in L2.
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
+
 // Ask for `bytes` (a multiple of 16) at a 16-byte aligned address to be in L2.
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
 {
