@@ -449,7 +449,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const int r = 32 * (warp & 1) + lane, half = warp >> 1;
-    const float scale2 = a.scale * kLog2e;
+    const float scale2 = a.scale * kLog2e, unit = scale2 > 0.f ? scale2 : 1.f;
     const int group = a.q_heads;
     int index = 0;
     uint32_t x_phase = 0;
@@ -460,7 +460,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
         const long long limit =
             r < rows ? (a.prefix ? w.ch.start : w.ch.start + (row0 + r) / group + 1) : 0;  // this row's: [0, limit)
         const long long open = a.prefix ? w.ch.start : w.ch.start + row0 / group + 1;      // every row attends below this
-        float top = -INFINITY, sum = 0.f;
+        float top = -INFINITY;
+        float2 sum = make_float2(0.f, 0.f);
         bool redo = false;
         for (int t = 0; t < w.tiles; ++t, ++index) {
             const long long key = w.it.key0 + (long long)t * kAttnKeys;
@@ -471,7 +472,11 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             tmem_wait_ld();
             float x[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * scale2;
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]);
+            if (scale2 <= 0.f) {  // (else the weights' exponents are formed in one step from the products)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] *= scale2;
+            }
             if (key + kAttnKeys > open || rows < kRows) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -480,6 +485,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             float most = x[0];
 #pragma unroll
             for (int k = 1; k < 32; ++k) most = fmaxf(most, x[k]);
+            most *= unit;
             if (t == 0) {
                 m->half[half][r] = most;
                 softmax_sync();
@@ -491,9 +497,10 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             uint32_t p[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const float e0 = exp2_approx(x[2 * k] - base), e1 = exp2_approx(x[2 * k + 1] - base);
-                sum += e0 + e1;
-                p[k] = pack_bf16x2(e0, e1);
+                float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(unit, unit), make_float2(-base, -base));
+                e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                sum = add2(sum, e);
+                p[k] = pack_bf16x2(e.x, e.y);
             }
             if (index > 1) mbar_wait_cluster(smem_addr(&m->pv_done[index & 1]), ((index - 2) >> 1) & 1, &m->quit, a.status);
             const uint32_t at = smem + kPOff + (index & 1) * kChunkBytes + r * 128;
@@ -509,7 +516,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
         }
         // the rows' sums, and 1 / l of both CTAs' rows in both
         softmax_sync();  // the maxima have been read
-        m->half[half][r] = sum;
+        m->half[half][r] = sum.x + sum.y;
         softmax_sync();
         if (half == 0) {
             const float l = m->half[0][r] + m->half[1][r];

@@ -650,7 +650,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t tmem_o = tmem + kTmemO + lanes;
-    const float scale2 = a.scale * kLog2e;
+    const float scale2 = a.scale * kLog2e, unit = scale2 > 0.f ? scale2 : 1.f;
     const int group = a.q_heads / (kMla ? 1 : a.g.rope_heads);
     const int vdim = kMla ? 512 : 64 * l.values;
     const int blocks = kMla ? 4 : (l.values + 1) / 2;
@@ -660,14 +660,15 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
         // this thread's two rows, their limits, running maxima (log2) and its part of their sums
         int row[2];
         long long limit[2];
-        float top[2], sum[2];
+        float top[2];
+        float2 sum[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             row[h] = 16 * warp + lane / 4 + 8 * h;
             const int tok = (w.it.row0 + min(row[h], w.it.rows - 1)) / group;
             limit[h] = row[h] < w.it.rows ? (a.prefix ? w.ch.start : w.ch.start + tok + 1) : 0;
             top[h] = -INFINITY;
-            sum[h] = 0.f;
+            sum[h] = make_float2(0.f, 0.f);
         }
         const long long open = a.prefix ? w.ch.start : w.ch.start + w.it.row0 / group + 1;  // every row attends below this
         const int n = padded_rows(w.it.rows);
@@ -682,7 +683,11 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                 tmem_ld_16x64(tmem + kTmemS + lanes + (index & 1) * 64, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * scale2;
+                for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]);
+                if (scale2 <= 0.f) {  // (else the weights' exponents are formed in one step from the products)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] *= scale2;
+                }
                 if (key + kAttnKeys > open || w.it.rows < n) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
@@ -692,8 +697,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) tile_top[(k >> 1) & 1] = fmaxf(tile_top[(k >> 1) & 1], x[k]);
-                tile_top[0] = quad_max(tile_top[0]);
-                tile_top[1] = quad_max(tile_top[1]);
+                tile_top[0] = quad_max(tile_top[0]) * unit;
+                tile_top[1] = quad_max(tile_top[1]) * unit;
             }
             const bool raise = any_of_softmax(tile_top[0] > top[0] + kRaise || tile_top[1] > top[1] + kRaise);
             float factor[2] = {1.f, 1.f};
@@ -703,7 +708,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                     const float old = top[h];
                     top[h] = fmaxf(old, tile_top[h]);
                     factor[h] = top[h] == -INFINITY ? 1.f : exp2f(old - top[h]);
-                    sum[h] *= factor[h];
+                    sum[h].x *= factor[h];
+                    sum[h].y *= factor[h];
                 }
             }
             // weights, their sum in fp32, and the weights rounded to bf16 for the product with V
@@ -713,9 +719,10 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const int h = k & 1;
-                    const float e0 = exp2_approx(x[2 * k] - base[h]), e1 = exp2_approx(x[2 * k + 1] - base[h]);
-                    sum[h] += e0 + e1;
-                    p[k] = pack_bf16x2(e0, e1);
+                    float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(unit, unit), make_float2(-base[h], -base[h]));
+                    e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    sum[h] = add2(sum[h], e);
+                    p[k] = pack_bf16x2(e.x, e.y);
                 }
             }
             // P and O are free when the product of the tile before has finished
@@ -745,7 +752,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
             if (lane == 0) mbar_arrive(smem_addr(&m->p_ready));
         }
         // the tile's result
-        float sums[2] = {quad_sum(sum[0]), quad_sum(sum[1])};
+        float sums[2] = {quad_sum(sum[0].x + sum[0].y), quad_sum(sum[1].x + sum[1].y)};
         if (lane % 4 == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
