@@ -438,7 +438,7 @@ typedef struct {
 
 /* Create a batch for plans of at most max_chunks chunks and max_tokens tokens, for
  * q_heads query heads (leyline_attention needs a multiple of rope_heads).  Allocates the plan's device
- * buffers (8 + 4 * rope_dim bytes per token), pinned staging for plans, and the
+ * buffers (8 + 4 * rope_dim bytes per token, 40 per 64 query rows), pinned staging for four plans, and the
  * attention workspace (partial outputs of row tiles whose rows are split over
  * several CTAs: some 40 MiB for MLA rows).  Synchronous.  The pool cannot be
  * destroyed while it has batches.

@@ -21,9 +21,9 @@
 // 11-14 copy the queries and the tiles that end inside.
 //
 // Bounds and measurements (GB300; cuBLAS bf16 at 1875 TFLOP/s).  The products take 864 + 512 cycles a tile, all of it
-// 1530, and an item's ends 13000.  A prompt chunk of 512 tokens of 128 heads over 8192 rows 737 us (1.54 PFLOP/s, 0.82 of
-// measured), ragged chunks of 61 tokens of 16 heads 148 us (1.2), 16 decodes of 128 heads over 24000 rows 120 us (4.9 TB/s,
-// 0.73 of measured copies; 1.2 PFLOP/s).  One row a page, copied: 835, 198 and 143 us (by single CTAs 1426, 255 and 213).
+// 1530, and an item's ends 13000.  A prompt chunk of 512 tokens of 128 heads over 8192 rows 718 us (1.58 PFLOP/s, 0.84 of
+// measured), ragged chunks of 61 tokens of 16 heads 147 us (1.2), 16 decodes of 128 heads over 24000 rows 117 us (5.1 TB/s,
+// 0.75 of measured copies; 1.2 PFLOP/s).  One row a page, copied: 817, 200 and 142 us (by single CTAs 1426, 255 and 213).
 #include "leyline_attention.cuh"
 
 namespace leyline {

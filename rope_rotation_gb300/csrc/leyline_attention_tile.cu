@@ -36,7 +36,7 @@
 // Bounds and measurements (GB300; HBM copies at 6782 GB/s).  MLA: shared memory carries 2500 cycles of operands a tile; a
 // tile takes 3400 from L2 and 3800 to 4400 from HBM, two of them in flight.  One decode of 16 heads over 32768 rows 18 us
 // (14 here, the rest the join), 64 over 4000 rows 78 us (4.8 TB/s).  Grouped: HBM; 4 drafted tokens of 16 requests, 32 heads on
-// 4 bands of 128, 72 us (4.9 TB/s, 0.72 of measured).  Lazy MLA rows one a page: 110 us for 64 requests over 4000 (3.4 TB/s),
+// 4 bands of 128, 70 us (5.0 TB/s, 0.74 of measured).  Lazy MLA rows one a page: 108 us for 64 requests over 4000 (3.4 TB/s),
 // by the copies of single rows and the turns; 16 rows a page 88.
 #include "leyline_attention.cuh"
 
