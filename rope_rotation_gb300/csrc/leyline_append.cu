@@ -6,7 +6,10 @@
 // R(p) applied to the position-free band.
 //
 // All three kernels are bound by memory (or, for a few tokens, by one launch): a row or a
-// band is read once, kept in registers while its norm's sum is formed, and written once.
+// band is read once, kept in registers while its norm's sum is formed, and written once.  Calls back to back: append of one
+// row 6 us and of 8192 MLA rows 7 (2.7 TB/s, in L2; 10 from a cold start), the host's time of a call; rotate of 4096 x 128
+// bands of 64 25 us (5.4 TB/s, 0.80 of measured copies).  A plan of 8192 tokens installs in 21 us, once a step, most of it
+// the fp64 sines.
 #include "leyline_batch.h"
 #include "leyline_device.cuh"
 
