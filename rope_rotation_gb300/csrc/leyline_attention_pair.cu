@@ -63,9 +63,9 @@ struct Misc {
     unsigned long long drained;
     uint32_t tmem;
     int quit;
-    float half[2][kRows];        // a row's maximum, then sum, over either half of a tile's columns
+    float half[2][kRows];        // a row's maximum over either half of a tile's columns; then the second half's two sums
     float redo;                  // not 0: some item is to be computed again
-    // 1 / l of both CTAs' rows, for items in turn: one CTA may be an item ahead of the other's last step
+    // 1 / sum of weights of both CTAs' rows, for items in turn: one CTA may be an item ahead of the other's last step
     alignas(16) float factor[2][2 * kRows];
 };
 static_assert(offsetof(Misc, factor) % 16 == 0 && kMiscOff % 16 == 0, "read in vectors");
@@ -461,7 +461,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             r < rows ? (a.prefix ? w.ch.start : w.ch.start + (row0 + r) / group + 1) : 0;  // this row's: [0, limit)
         const long long open = a.prefix ? w.ch.start : w.ch.start + row0 / group + 1;      // every row attends below this
         float top = -INFINITY;
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum = make_float2(0.f, 0.f), used = make_float2(0.f, 0.f);
         bool redo = false;
         for (int t = 0; t < w.tiles; ++t, ++index) {
             const long long key = w.it.key0 + (long long)t * kAttnKeys;
@@ -501,6 +501,8 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
                 e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                 sum = add2(sum, e);
                 p[k] = pack_bf16x2(e.x, e.y);
+                // the output is divided by the sum of the weights as the product has them (leyline_attention_tile.cu)
+                used = add2(used, make_float2(bf16_lo(p[k]), bf16_hi(p[k])));
             }
             if (index > 1) mbar_wait_cluster(smem_addr(&m->pv_done[index & 1]), ((index - 2) >> 1) & 1, &m->quit, a.status);
             const uint32_t at = smem + kPOff + (index & 1) * kChunkBytes + r * 128;
@@ -514,12 +516,15 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
             __syncwarp();
             if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->p_ready[index & 1]), 0));
         }
-        // the rows' sums, and 1 / l of both CTAs' rows in both
+        // the rows' sums, and 1 / sum of the used weights of both CTAs' rows in both
         softmax_sync();  // the maxima have been read
-        m->half[half][r] = sum.x + sum.y;
+        if (half == 1) {
+            m->half[0][r] = sum.x + sum.y;
+            m->half[1][r] = used.x + used.y;
+        }
         softmax_sync();
         if (half == 0) {
-            const float l = m->half[0][r] + m->half[1][r];
+            const float l = sum.x + sum.y + m->half[0][r], weights = used.x + used.y + m->half[1][r];
             if (r < rows) {
                 const float lse = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
                 if (w.it.part >= 0) {
@@ -529,7 +534,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, Misc* m, uint32_t
                     a.lse[(long long)(w.ch.tok0 + q / group) * a.q_heads + q % group] = lse;
                 }
             }
-            const float f = l == 0.f ? 0.f : 1.f / l;
+            const float f = weights == 0.f ? 0.f : 1.f / weights;
             const uint32_t to = smem_addr(&m->factor[x_phase][rank * kRows + r]);
             cluster_store(cluster_addr(to, 0), f);
             cluster_store(cluster_addr(to, 1), f);

@@ -64,7 +64,7 @@ struct Misc {
     uint32_t tmem;
     int quit;
     int redo;  // some item is to be computed again
-    alignas(16) float factor[kAttnRows];  // rescale, then 1 / l
+    alignas(16) float factor[kAttnRows];  // rescale, then 1 / sum of weights
 };
 static_assert(offsetof(Misc, factor) % 16 == 0 && sizeof(Misc) % 16 == 0, "read in vectors");
 
@@ -657,18 +657,19 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
     int index = 0;  // tiles before this one
     for (int i = a.cta_begin[blockIdx.x]; i < a.cta_begin[blockIdx.x + 1]; ++i) {
         const Work w = load_work(a, i);
-        // this thread's two rows, their limits, running maxima (log2) and its part of their sums
+        // this thread's two rows, their limits, running maxima (log2) and its part of their sums: of the weights, for lse,
+        // and of the weights as the product with V has them
         int row[2];
         long long limit[2];
         float top[2];
-        float2 sum[2];
+        float2 sum[2], used[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             row[h] = 16 * warp + lane / 4 + 8 * h;
             const int tok = (w.it.row0 + min(row[h], w.it.rows - 1)) / group;
             limit[h] = row[h] < w.it.rows ? (a.prefix ? w.ch.start : w.ch.start + tok + 1) : 0;
             top[h] = -INFINITY;
-            sum[h] = make_float2(0.f, 0.f);
+            sum[h] = used[h] = make_float2(0.f, 0.f);
         }
         const long long open = a.prefix ? w.ch.start : w.ch.start + w.it.row0 / group + 1;  // every row attends below this
         const int n = padded_rows(w.it.rows);
@@ -710,9 +711,14 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                     factor[h] = top[h] == -INFINITY ? 1.f : exp2f(old - top[h]);
                     sum[h].x *= factor[h];
                     sum[h].y *= factor[h];
+                    used[h].x *= factor[h];
+                    used[h].y *= factor[h];
                 }
             }
-            // weights, their sum in fp32, and the weights rounded to bf16 for the product with V
+            // Weights, and the weights rounded to bf16 for the product with V: a matrix instruction's operands have one type,
+            // and a second product for the low parts would double the work of O^T.  The output is divided by the sum of
+            // the rounded weights, so it is a mean of values whichever way they round: a row that attends to one row
+            // alone gets that row's value, where a sum of other weights than the product's left up to 2^-8 of it.
             uint32_t p[16];
             if (16 * warp < n) {
                 const float base[2] = {top[0] == -INFINITY ? 0.f : top[0], top[1] == -INFINITY ? 0.f : top[1]};
@@ -723,6 +729,7 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
                     e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                     sum[h] = add2(sum[h], e);
                     p[k] = pack_bf16x2(e.x, e.y);
+                    used[h] = add2(used[h], make_float2(bf16_lo(p[k]), bf16_hi(p[k])));
                 }
             }
             // P and O are free when the product of the tile before has finished
@@ -753,10 +760,11 @@ __device__ __forceinline__ void run_softmax(const AttnArgs& a, const Layout& l, 
         }
         // the tile's result
         float sums[2] = {quad_sum(sum[0].x + sum[0].y), quad_sum(sum[1].x + sum[1].y)};
+        float weights[2] = {quad_sum(used[0].x + used[0].y), quad_sum(used[1].x + used[1].y)};
         if (lane % 4 == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                m->factor[row[h]] = sums[h] == 0.f ? 0.f : 1.f / sums[h];
+                m->factor[row[h]] = weights[h] == 0.f ? 0.f : 1.f / weights[h];
                 if (row[h] >= w.it.rows) continue;
                 const float lse = sums[h] == 0.f ? -INFINITY : (top[h] + log2f(sums[h])) * kLn2;
                 if (w.it.part >= 0) {

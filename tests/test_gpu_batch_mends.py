@@ -1,0 +1,48 @@
+"""Batches of new tokens, cases that once went wrong: outputs whose weights are rounded, streams, captures, views that
+overlap, plans that no longer hold (see batch_harness for formulas and tolerances)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import rope_rotation_gb300
+    rope_rotation_gb300.build()
+
+
+import batch_harness as BH  # noqa: E402  (needs torch)
+
+LAZY, SPLIT = 2, 4
+
+
+@pytest.mark.parametrize("lat,rope,bands,heads,n,start,flags,B", [
+    (512, 64, 1, 128, 40, 1000, 0, 16), (512, 64, 1, 128, 40, 1000, SPLIT, 5), (512, 64, 1, 128, 1, 9000, 0, 16),
+    (512, 64, 1, 16, 1, 900, 0, 16), (512, 64, 1, 16, 3, 900, LAZY, 16), (512, 64, 1, 20, 30, 200, 0, 1),
+    (512, 128, 4, 32, 4, 1500, 0, 16), (512, 128, 4, 32, 4, 1500, LAZY, 1), (384, 64, 2, 8, 5, 300, 0, 16),
+    (512, 256, 2, 8, 5, 300, 0, 16), (40, 48, 1, 3, 5, 300, 0, 16)])
+@pytest.mark.parametrize("scale", [0.125, 1.0])
+def test_equal_values_come_back_as_they_are(lat, rope, bands, heads, n, start, flags, B, scale):
+    """Where all rows hold one value, its weighted mean is that value, whatever the weights: whichever way the weights are
+    rounded, their sum must be that of the rounded ones.  The sums' fp32 errors are under (end + 2) * 2^-23 < 2^-9.8 of the
+    value (end <= 9001; equal signs in a dimension), a bf16 half step is at least 2^-9 of it, so the output has its bits."""
+    cache = BH.make_cache([start], extra=n, layers=1, B=B, latent=lat, rope=rope, bands=bands, flags=flags)
+    b = cache.batch(1, n, heads)
+    chunks = [(0, start, n)]
+    b.plan(chunks)
+    rows = BH.bf16(start + n, cache.row, seed=1)
+    rows[:, :lat] = BH.bf16(1, lat, seed=2)
+    flat = torch.from_numpy(cache.slot_index(0, np.arange(start + n))).cuda()
+    cache.write_layer_rows(0, flat, rows)
+    ql = torch.zeros(n, heads, lat, dtype=torch.bfloat16, device="cuda") if bands == 1 else None
+    q = BH.bf16(n, heads, rope, seed=3)
+    out, lse = BH.check_attention(cache, b, 0, chunks, ql, q, scale, "equal values")
+    want = rows[0, :lat].view(bands, lat // bands).repeat_interleave(heads // bands, 0).expand(n, heads, lat // bands)
+    assert torch.equal(out, want), f"{int((out != want).sum())} of {out.numel()} values differ"
+    cache.check_status()
+    cache.close()
