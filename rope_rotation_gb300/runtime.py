@@ -9,6 +9,7 @@ nothing itself.
 """
 from __future__ import annotations
 
+import contextlib
 import weakref
 from typing import Sequence
 
@@ -123,9 +124,21 @@ class PagedCache:
         """dirs: a list of leyline.directive() or one leyline.directive_batch() array."""
         leyline.leyline_splice(self.pool, self.tables, dirs, stream)
 
+    def allocating(self, stream):
+        """The context in which a call on `stream` makes its outputs: torch hands out a block for the stream that is
+        current then, and may hand out one that another stream's kernels still use (None: the current stream)."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = self.torch.cuda.ExternalStream(stream, device=self.kv.device)
+        return self.torch.cuda.stream(stream)
+
     def gather(self, req: int, layer: int, t0: int, t1: int, out=None, stream=None):
+        """Rows [t0, t1) of a request in one layer.  An `out` made here belongs to `stream`, as if made with it
+        current: a caller who uses it on another stream orders the two, as for any tensor."""
         if out is None:
-            out = self.torch.empty((t1 - t0, self.row), dtype=self.torch.bfloat16, device=self.device)
+            with self.allocating(stream):
+                out = self.torch.empty((t1 - t0, self.row), dtype=self.torch.bfloat16, device=self.device)
         leyline.leyline_gather(self.pool, self.tables, req, layer, t0, t1, out, stream)
         return out
 
@@ -180,7 +193,7 @@ class Batch:
     plan() takes one chunk of new tokens per request, once a step; append(), rotate() and
     attention() then serve each layer, on tensors whose first axis is the plan's tokens, chunk after
     chunk.  The last three can be captured into a CUDA graph and replayed after each new plan,
-    on tensors with room for max_tokens.
+    on tensors with room for max_tokens.  Outputs that a call makes belong to the stream it runs on.
     """
 
     def __init__(self, cache: PagedCache, max_chunks: int, max_tokens: int, q_heads: int):
@@ -230,7 +243,8 @@ class Batch:
     def rotate(self, q, out=None, norm=None, eps: float = 1e-6, stream=None):
         """Norm and turn query bands [tokens][q_heads][rope_dim] into out (default: a new tensor; q itself is fine)."""
         if out is None:
-            out = self.cache.torch.empty_like(q)
+            with self.cache.allocating(stream):
+                out = self.cache.torch.empty_like(q)
         dim = self.cache.rope_dim
         leyline.leyline_rotate(self.handle, self._heads(q, "q", dim), self._heads(out, "out", dim),
                                self._weights(norm, "norm", dim), eps, self._stream(stream))
@@ -242,10 +256,12 @@ class Batch:
         their own (prefix: the rows before their chunk).  q_latent is None for rows of several bands."""
         torch = self.cache.torch
         if out is None:
-            out = torch.empty((q_rope.shape[0], self.q_heads, self.value_dim), dtype=torch.bfloat16,
-                              device=self.cache.kv.device)
+            with self.cache.allocating(stream):
+                out = torch.empty((q_rope.shape[0], self.q_heads, self.value_dim), dtype=torch.bfloat16,
+                                  device=self.cache.kv.device)
         if lse is None:
-            lse = torch.empty((q_rope.shape[0], self.q_heads), dtype=torch.float32, device=self.cache.kv.device)
+            with self.cache.allocating(stream):
+                lse = torch.empty((q_rope.shape[0], self.q_heads), dtype=torch.float32, device=self.cache.kv.device)
         elif (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < self.tokens
               or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
             raise ValueError(f"lse: expected contiguous fp32 [>= {self.tokens}][{self.q_heads}]")

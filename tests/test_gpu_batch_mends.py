@@ -46,3 +46,34 @@ def test_equal_values_come_back_as_they_are(lat, rope, bands, heads, n, start, f
     assert torch.equal(out, want), f"{int((out != want).sum())} of {out.numel()} values differ"
     cache.check_status()
     cache.close()
+
+
+def _stream_of(t):
+    """The stream that torch's allocator keeps a tensor's block for."""
+    at = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= at < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+@pytest.mark.parametrize("address", [False, True])
+def test_outputs_belong_to_the_stream_of_their_call(address):
+    """Made for the current stream, they could be blocks that its kernels still read, or be handed out again while the
+    call's stream writes them."""
+    cache = BH.make_cache([100], extra=8, layers=1)
+    b = cache.batch(1, 8, 16)
+    b.plan([(0, 100, 3)])
+    rows, ql, q = BH.bf16(3, 576), BH.bf16(3, 16, 512, seed=1), BH.bf16(3, 16, 64, seed=2)
+    b.append(0, rows)
+    want = (b.rotate(q), *b.attention(0, ql, q, 0.07), cache.gather(0, 0, 0, 103))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if address else side
+    got = (b.rotate(q, stream=s), *b.attention(0, ql, q, 0.07, stream=s), cache.gather(0, 0, 0, 103, stream=s))
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+        assert _stream_of(y) == side.cuda_stream and _stream_of(x) != side.cuda_stream
+    cache.check_status()
+    cache.close()
