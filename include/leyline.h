@@ -414,8 +414,9 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * and refuses a stream under capture.  leyline_append, leyline_rotate and
  * leyline_attention can be captured: they read the plan from the batch's device
  * memory, at addresses that do not change, so a graph of a step's layers can be
- * replayed after each new plan.  Their token tensors must then have room for the
- * tokens of every plan the graph is replayed with (at most max_tokens).  The
+ * replayed after each new plan.  Their token tensors must then have room for
+ * max_tokens tokens, whatever the plan at the time of the capture (views whose
+ * strides do not have it are refused).  The
  * library does not see replays: order them after the plan and before later work
  * on the pool (the same stream does), and do not replay two graphs of one batch
  * at once, since a batch has one workspace. */

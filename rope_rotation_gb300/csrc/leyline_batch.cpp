@@ -106,7 +106,10 @@ int check_norm(const void** w, int device, const char* what)
     return rc;
 }
 
-// Head axes written to must hold distinct places, for the plan's tokens.
+// The tokens a call's tensors hold: a captured call may be replayed with plans of up to max_tokens.
+int64_t room_of(const leyline_batch* b, bool captured) { return captured ? b->max_tokens : b->n_tokens; }
+
+// Head axes written to must hold distinct places, for `tokens` tokens.
 int check_written(const HeadsView& v, int64_t tokens, int64_t heads, int64_t dim, const char* what)
 {
     char msg[128];
@@ -405,7 +408,7 @@ int leyline_rotate(leyline_batch_t* b, const leyline_heads_t* q, const leyline_h
     if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
     rc = check_heads(q, p->device, "q", &a.q);
     if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
-    if (rc == LEYLINE_OK) rc = check_written(a.out, b->n_tokens, b->q_heads, p->g.rope_dim, "out");
+    if (rc == LEYLINE_OK) rc = check_written(a.out, room_of(b, captured), b->q_heads, p->g.rope_dim, "out");
     if (rc == LEYLINE_OK && q->ptr == out->ptr &&
         (q->token_stride != out->token_stride || q->head_stride != out->head_stride))
         rc = bad("q and out start at one address with different strides");
@@ -449,7 +452,7 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     rc = check_heads(q_rope, p->device, "q_rope", &a.q_rope);
     if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
     if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
-    if (rc == LEYLINE_OK) rc = check_written(a.out, b->n_tokens, b->q_heads, b->value_dim, "out");
+    if (rc == LEYLINE_OK) rc = check_written(a.out, room_of(b, captured), b->q_heads, b->value_dim, "out");
     // (an item may be computed again from its queries)
     if (rc == LEYLINE_OK && (a.out.ptr == a.q_rope.ptr || a.out.ptr == a.q_latent.ptr)) rc = bad("out must not lie over the queries");
     void* lse_alias = lse;

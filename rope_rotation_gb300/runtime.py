@@ -229,13 +229,22 @@ class Batch:
             raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({n},)")
         return t if t is None else self._device(t, what)
 
-    def _heads(self, t, what: str, dim: int) -> leyline.Heads:
-        return leyline.heads(self._device(t, what), what, self.tokens, self.q_heads, dim)
+    def _room(self, stream, *tensors) -> int:
+        """Tokens that the tensors of a call must have room for: the plan's, and under capture max_tokens, since the graph
+        may be replayed with any plan."""
+        if all(t is None or t.dim() > 0 and t.shape[0] >= self.max_tokens for t in tensors):
+            return self.tokens
+        with self.cache.allocating(stream):
+            return self.max_tokens if self.cache.torch.cuda.is_current_stream_capturing() else self.tokens
+
+    def _heads(self, t, what: str, tokens: int, dim: int) -> leyline.Heads:
+        return leyline.heads(self._device(t, what), what, tokens, self.q_heads, dim)
 
     def append(self, layer: int, rows, latent_norm=None, key_norm=None, eps: float = 1e-6, stream=None) -> None:
         """Write rows [tokens][row] of one layer, normed and turned by their positions."""
-        if rows.dim() != 2 or rows.shape[0] < self.tokens or rows.shape[1] != self.cache.row:
-            raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [>= {self.tokens}][{self.cache.row}]")
+        tokens = self._room(stream, rows)
+        if rows.dim() != 2 or rows.shape[0] < tokens or rows.shape[1] != self.cache.row:
+            raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [>= {tokens}][{self.cache.row}]")
         leyline.leyline_append(self.handle, layer, rows,
                                self._weights(latent_norm, "latent_norm", self.cache.latent_dim),
                                self._weights(key_norm, "key_norm", self.cache.rope_dim), eps, self._stream(stream))
@@ -245,8 +254,8 @@ class Batch:
         if out is None:
             with self.cache.allocating(stream):
                 out = self.cache.torch.empty_like(q)
-        dim = self.cache.rope_dim
-        leyline.leyline_rotate(self.handle, self._heads(q, "q", dim), self._heads(out, "out", dim),
+        dim, tokens = self.cache.rope_dim, self._room(stream, q, out)
+        leyline.leyline_rotate(self.handle, self._heads(q, "q", tokens, dim), self._heads(out, "out", tokens, dim),
                                self._weights(norm, "norm", dim), eps, self._stream(stream))
         return out
 
@@ -262,14 +271,16 @@ class Batch:
         if lse is None:
             with self.cache.allocating(stream):
                 lse = torch.empty((q_rope.shape[0], self.q_heads), dtype=torch.float32, device=self.cache.kv.device)
-        elif (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < self.tokens
-              or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
-            raise ValueError(f"lse: expected contiguous fp32 [>= {self.tokens}][{self.q_heads}]")
+        tokens = self._room(stream, q_latent, q_rope, out, lse)
+        if (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < tokens
+                or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
+            raise ValueError(f"lse: expected contiguous fp32 [>= {tokens}][{self.q_heads}]")
         if (q_latent is None) != (self.bands > 1):
             raise ValueError("q_latent goes with rows of one band (MLA), and only with those")
         leyline.leyline_attention(
-            self.handle, layer, None if q_latent is None else self._heads(q_latent, "q_latent", self.cache.latent_dim),
-            self._heads(q_rope, "q_rope", self.cache.rope_dim), self._heads(out, "out", self.value_dim),
+            self.handle, layer,
+            None if q_latent is None else self._heads(q_latent, "q_latent", tokens, self.cache.latent_dim),
+            self._heads(q_rope, "q_rope", tokens, self.cache.rope_dim), self._heads(out, "out", tokens, self.value_dim),
             self._device(lse, "lse"), scale, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0, self._stream(stream))
         return out, lse
 

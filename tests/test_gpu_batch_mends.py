@@ -77,3 +77,54 @@ def test_outputs_belong_to_the_stream_of_their_call(address):
         assert _stream_of(y) == side.cuda_stream and _stream_of(x) != side.cuda_stream
     cache.check_status()
     cache.close()
+
+
+def _refused_under_capture(call, error):
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    x = torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    with pytest.raises(error) as e:
+        with torch.cuda.graph(graph, stream=stream):
+            x += 1
+            call()
+    return e.value
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_capture_asks_for_room_for_every_plan(given):
+    """Captured calls go over the tokens of the plan that is current at a replay, up to max_tokens: tensors of the tokens of
+    the plan at the capture would be read and written out of range.  (Nothing is replayed here.)"""
+    from rope_rotation_gb300 import leyline
+    from rope_rotation_gb300.leyline import LeylineError
+    cache = BH.make_cache([100], extra=16, layers=1)
+    b = cache.batch(1, 8, 4)
+    b.plan([(0, 100, 2)])
+
+    def tensors(n):
+        return (BH.bf16(n, 576), BH.bf16(n, 4, 512), BH.bf16(n, 4, 64), torch.empty(n, 4, 512, dtype=torch.bfloat16, device="cuda"),
+                torch.empty(n, 4, device="cuda"))
+    rows, ql, q, out, lse = tensors(2)
+    big_rows, big_ql, big_q, big_out, big_lse = tensors(8)
+    flat = torch.empty(8 * 4 * 512, dtype=torch.bfloat16, device="cuda")
+    one = leyline.heads(flat.as_strided((2, 4, 512), (512, 2 * 512, 1)), "out", 2, 4, 512)  # heads outermost, 2 tokens each
+    turned = leyline.heads(flat.as_strided((2, 4, 64), (64, 2 * 64, 1)), "out", 2, 4, 64)
+    kw = lambda: {"stream": torch.cuda.current_stream()} if given else {}  # noqa: E731
+    for call in (
+            lambda: b.append(0, rows, **kw()), lambda: b.rotate(q, **kw()), lambda: b.rotate(big_q, out=q, **kw()),
+            lambda: b.attention(0, ql, big_q, 0.07, out=big_out, lse=big_lse, **kw()),
+            lambda: b.attention(0, big_ql, q, 0.07, out=big_out, lse=big_lse, **kw()),
+            lambda: b.attention(0, big_ql, big_q, 0.07, out=out, lse=big_lse, **kw()),
+            lambda: b.attention(0, big_ql, big_q, 0.07, out=big_out, lse=lse, **kw())):
+        _refused_under_capture(call, ValueError)
+    h = [leyline.heads(t, "q", 8, 4, d) for t, d in ((big_ql, 512), (big_q, 64))]
+    assert _refused_under_capture(lambda: leyline.leyline_rotate(b.handle, h[1], turned), LeylineError).code == -1
+    assert _refused_under_capture(lambda: leyline.leyline_attention(b.handle, 0, *h, one, None, 0.07), LeylineError).code == -1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):  # with the room it asks for
+        b.append(0, big_rows)
+        b.attention(0, big_ql, b.rotate(big_q), 0.07, out=big_out, lse=big_lse)
+    del graph
+    b.append(0, rows)  # and outside a capture the plan's tokens do
+    b.attention(0, ql, b.rotate(q), 0.07, out=out, lse=lse)
+    cache.check_status()
+    cache.close()
