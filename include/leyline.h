@@ -485,7 +485,7 @@ int leyline_append(leyline_batch_t* batch, int32_t layer, const void* rows, int6
 
 /* Turn the query bands q [tokens][q_heads][rope_dim] by their tokens' rotary
  * positions into out (same shape; may be q itself, but may not overlap it
- * otherwise), each first normed with `norm` (bf16 [rope_dim]) if it is not NULL, as
+ * otherwise: see leyline_attention), each first normed with `norm` (bf16 [rope_dim]) if it is not NULL, as
  * leyline_append norms keys; same arithmetic.  Enqueues one kernel.
  * Errors: INVALID_ARG, CUDA. */
 int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyline_heads_t* out, const void* norm,
@@ -507,8 +507,9 @@ int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyli
  * leyline_gather turns it but for the rounding: the scores take the turned band
  * to 2^-17 of its size (LEYLINE_ROTATE_BF16_NAIVE: as gathered).  lse (fp32 [tokens][q_heads], contiguous) may be NULL.
  * A token without rows (PREFIX, start 0) gets zeros and lse -inf.  Rows that a token
- * does not attend to do not reach its output, whatever they hold.  out may not
- * overlap the queries.
+ * does not attend to do not reach its output, whatever they hold.  out and lse may not
+ * overlap the queries, nor one another (INVALID_ARG).  Views that interleave without
+ * sharing a byte are fine if they have their token stride or their head stride in common.
  * Scores and sums are fp32; the weights exp(x - max) are rounded to bf16 for
  * the product with the values.  A row tile whose output is not finite, or whose scores
  * rise by more than 55 over those of the tile's first 64 rows, is computed again one

@@ -122,6 +122,11 @@ int check_written(const HeadsView& v, int64_t tokens, int64_t heads, int64_t dim
     return LEYLINE_OK;
 }
 
+Extent extent(const HeadsView& v, int64_t tokens, int64_t heads, int64_t dim)
+{
+    return Extent{reinterpret_cast<uintptr_t>(v.ptr), tokens, heads, 2 * v.token_stride, 2 * v.head_stride, 2 * dim};
+}
+
 // Common start of the calls of a step's layers.
 int enter(leyline_batch* b, cudaStream_t stream, bool* captured)
 {
@@ -412,6 +417,10 @@ int leyline_rotate(leyline_batch_t* b, const leyline_heads_t* q, const leyline_h
     if (rc == LEYLINE_OK && q->ptr == out->ptr &&
         (q->token_stride != out->token_stride || q->head_stride != out->head_stride))
         rc = bad("q and out start at one address with different strides");
+    const int64_t room = room_of(b, captured);
+    if (rc == LEYLINE_OK && q->ptr != out->ptr &&
+        overlap(extent(a.q, room, b->q_heads, p->g.rope_dim), extent(a.out, room, b->q_heads, p->g.rope_dim)))
+        rc = bad("out may be q itself, but not overlap it otherwise");
     if (rc == LEYLINE_OK) rc = check_norm(&norm, p->device, "norm");
     if (rc != LEYLINE_OK) return rc;
     a.norm = static_cast<const uint4*>(norm);
@@ -453,11 +462,16 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
     if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
     if (rc == LEYLINE_OK) rc = check_heads(out, p->device, "out", &a.out);
     if (rc == LEYLINE_OK) rc = check_written(a.out, room_of(b, captured), b->q_heads, b->value_dim, "out");
-    // (an item may be computed again from its queries)
-    if (rc == LEYLINE_OK && (a.out.ptr == a.q_rope.ptr || a.out.ptr == a.q_latent.ptr)) rc = bad("out must not lie over the queries");
     void* lse_alias = lse;
     if (rc == LEYLINE_OK && lse) rc = resolve_access(lse, p->device, "lse", &lse_alias, &host);
     if (rc != LEYLINE_OK) return rc;
+    // other CTAs read queries while one writes its outputs, and an item may be computed again from its queries
+    const int64_t room = room_of(b, captured);
+    const Extent to = extent(a.out, room, b->q_heads, b->value_dim), band = extent(a.q_rope, room, b->q_heads, g.rope_dim);
+    const Extent latent = extent(a.q_latent, mla ? room : 0, b->q_heads, g.latent_dim);
+    if (overlap(to, band) || overlap(to, latent)) return bad("out must not lie over the queries");
+    const Extent sums{reinterpret_cast<uintptr_t>(lse_alias), lse ? 1 : 0, 1, 0, 0, 4 * room * b->q_heads};
+    if (overlap(sums, band) || overlap(sums, latent) || overlap(sums, to)) return bad("lse must not lie over out or the queries");
     a.kv = static_cast<const uint4*>(p->kv);
     a.lse = static_cast<float*>(lse_alias);
     a.scale = scale;

@@ -136,6 +136,17 @@ struct HeadsView {
     int64_t head_stride;
 };
 
+// The memory of a view: `width` bytes at address + t * token_stride + h * head_stride (bytes, not negative).
+struct Extent {
+    uintptr_t address;
+    int64_t tokens, heads;
+    int64_t token_stride, head_stride;
+    int64_t width;
+};
+// Whether two views share a byte.  Views whose address ranges meet are told apart if they share their token stride or
+// their head stride (parts of one wider tensor do) and are not of very many pieces; else they count as overlapping.
+bool overlap(Extent a, Extent b);
+
 struct InstallArgs {
     const uint4* staged;   // pinned plan, copied to plan
     uint4* plan;

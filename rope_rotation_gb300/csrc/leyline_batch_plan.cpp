@@ -12,7 +12,54 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int bad(const char* msg) { return set_error(LEYLINE_ERR_INVALID_ARG, msg); }
 
+// Whether [a, a + wa) and [b + d * stride, ... + wb) meet for some d with -below <= d <= above.
+bool meet(int64_t a, int64_t wa, int64_t b, int64_t wb, int64_t stride, int64_t below, int64_t above)
+{
+    if (stride == 0) return a < b + wb && b < a + wa;
+    // a - wb < b + d * stride < a + wa
+    auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -ceil_div(-x, y); };
+    const int64_t lo = floor_div(a - wb - b, stride) + 1, hi = floor_div(a + wa - 1 - b, stride);
+    return std::max(lo, -below) <= std::min(hi, above);
+}
+
 }  // namespace
+
+bool overlap(Extent a, Extent b)
+{
+    if (a.tokens <= 0 || b.tokens <= 0 || a.heads <= 0 || b.heads <= 0) return false;
+    for (Extent* x : {&a, &b}) {  // the stride of an axis of one entry says nothing
+        if (x->heads == 1) x->head_stride = 0;
+        if (x->tokens == 1) x->token_stride = 0;
+    }
+    const int64_t shift = (int64_t)(b.address - a.address);
+    auto length = [](const Extent& x) { return (x.tokens - 1) * x.token_stride + (x.heads - 1) * x.head_stride + x.width; };
+    if (shift >= length(a) || -shift >= length(b)) return false;
+    // Along an axis whose stride they share (or that has one entry in one of them), `n` entries, only the distance of two
+    // entries matters; the other axis, `m` entries, is taken as one piece first, then entry by entry.
+    enum Answer { kNo, kYes, kUnknown };
+    constexpr int64_t kMostPairs = 1 << 16;
+    using Field = int64_t Extent::*;
+    auto along = [&](Field n, Field stride, Field m, Field other) {
+        if (a.*stride != b.*stride && a.*n > 1 && b.*n > 1) return kUnknown;
+        const int64_t s = a.*n > 1 ? a.*stride : b.*stride, below = a.*n - 1, above = b.*n - 1;
+        if (!meet(0, (a.*m - 1) * (a.*other) + a.width, shift, (b.*m - 1) * (b.*other) + b.width, s, below, above)) return kNo;
+        if (a.*other == b.*other || a.*m == 1 || b.*m == 1) {
+            if (a.*m + b.*m > kMostPairs) return kUnknown;
+            const int64_t o = a.*m > 1 ? a.*other : b.*other;
+            for (int64_t d = 1 - a.*m; d < b.*m; ++d)
+                if (meet(0, a.width, shift + d * o, b.width, s, below, above)) return kYes;
+            return kNo;
+        }
+        if (a.*m * (b.*m) > kMostPairs) return kUnknown;
+        for (int64_t i = 0; i < a.*m; ++i)
+            for (int64_t j = 0; j < b.*m; ++j)
+                if (meet(i * (a.*other), a.width, shift + j * (b.*other), b.width, s, below, above)) return kYes;
+        return kNo;
+    };
+    Answer x = along(&Extent::tokens, &Extent::token_stride, &Extent::heads, &Extent::head_stride);
+    if (x == kUnknown) x = along(&Extent::heads, &Extent::head_stride, &Extent::tokens, &Extent::token_stride);
+    return x != kNo;
+}
 
 int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyline_chunk_t* chunks, int32_t n,
                  int64_t max_tokens, int64_t free_pages, int64_t pop_base, ChunkPlan* out)

@@ -138,3 +138,43 @@ def test_a_capture_asks_for_room_for_every_plan(given):
     b.attention(0, ql, b.rotate(q), 0.07, out=out, lse=lse)
     cache.check_status()
     cache.close()
+
+
+def test_views_that_overlap_the_queries_are_refused():
+    """Outputs a head, a token or a part of a head off the queries, lse over them: other CTAs would read what one has
+    written.  Parts of one wider tensor that share no byte are taken, and give what tensors of their own do."""
+    from rope_rotation_gb300.leyline import LeylineError
+    cache = BH.make_cache([40], extra=16, layers=1)
+    b = cache.batch(1, 8, 4)
+    b.plan([(0, 40, 3)])
+    b.append(0, BH.bf16(3, 576, seed=4))
+    flat = BH.bf16(8 * 4 * 1100, seed=5)
+
+    def at(first, dim, token=4 * 512, head=512, dtype=torch.bfloat16):
+        return flat.as_strided((3, 4, dim), (token, head, 1), first)
+    ql, q = BH.bf16(3, 4, 512), BH.bf16(3, 4, 64, seed=1)
+    ql2 = at(0, 512)
+    for call in (
+            lambda: b.attention(0, ql2, q, 0.07, out=at(512, 512)), lambda: b.attention(0, ql2, q, 0.07, out=at(2048, 512)),
+            lambda: b.attention(0, ql2, q, 0.07, out=at(2048 * 3 - 8, 512)),
+            lambda: b.attention(0, ql, at(8, 64), 0.07, out=at(0, 512)),
+            lambda: b.attention(0, ql2, q, 0.07, lse=flat[8:32].view(torch.float32).view(3, 4)),
+            lambda: b.attention(0, ql, q, 0.07, out=at(0, 512), lse=flat[2048:2072].view(torch.float32).view(3, 4)),
+            lambda: b.rotate(at(0, 64), out=at(8, 64)), lambda: b.rotate(at(0, 64), out=at(512, 64)),
+            lambda: b.rotate(at(2048, 64), out=at(0, 64))):
+        before = flat.clone()
+        with pytest.raises(LeylineError) as e:
+            call()
+        assert e.value.code == -1
+        assert torch.equal(before.view(torch.int16), flat.view(torch.int16))
+    # a token's row as [head][latent 512 | band 64 | turned band 64 | output 512]
+    wide = torch.zeros(3, 4, 1152, dtype=torch.bfloat16, device="cuda")
+    wide[..., :512], wide[..., 512:576] = ql, q
+    turned = b.rotate(wide[..., 512:576], out=wide[..., 576:640])
+    out, lse = b.attention(0, wide[..., :512], turned, 0.07, out=wide[..., 640:])
+    want = b.attention(0, ql, b.rotate(q), 0.07)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(wide[..., :512], ql) and torch.equal(wide[..., 512:576], q)
+    b.rotate(at(0, 64), out=at(64, 64))
+    cache.check_status()
+    cache.close()
