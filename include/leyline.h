@@ -406,7 +406,10 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * from it on extend the request, and the plan takes their pages off the free
  * list, installs them in the table and advances the length.  The rows of a chunk
  * hold nothing defined from the plan on until every layer has been appended.  A plan
- * holds until a splice, a rollback or a freed page changes one of its requests.
+ * holds until a splice changes one of its requests, a rollback returns to a checkpoint
+ * made before it, or one of its pages is freed.  After the first two, calls that are not
+ * captured are refused (INVALID_ARG) until the next plan; replays and freed pages the
+ * library does not see.
  * rope_start is the rotary position of the chunk's first token: start, unless
  * EVICT directives left the request's survivors at other positions.
  *

@@ -45,6 +45,7 @@ struct leyline_batch {
     bool slot_used[kSlots] = {};
     int next_slot = 0;
     bool planned = false;
+    PlanMark mark;
     int32_t n_tokens = 0;
     int32_t n_joins = 0;
     bool pairs = false;  // the plan is for pairs
@@ -139,6 +140,8 @@ int enter(leyline_batch* b, cudaStream_t stream, bool* captured)
         return cuda_error(e, "querying the stream's capture status");
     }
     *captured = st != cudaStreamCaptureStatusNone;
+    if (!*captured && b->mark.stale && b->n_tokens > 0)
+        return bad("the batch's plan no longer holds: a splice or a rollback has changed one of its requests");
     b->pool->window_open = false;  // other work on the pool ends the window of overlapping splices
     // a captured call is ordered by its graph; an event of other work cannot enter the capture
     return *captured ? LEYLINE_OK : order_after_previous(b->pool, stream);
@@ -235,7 +238,12 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
         free_batch(b);
         return cuda_error(e, "creating the batch");
     }
-    ++p->batches;
+    try {
+        p->batches.push_back(&b->mark);
+    } catch (...) {
+        free_batch(b);
+        throw;
+    }
     *out = b;
     return LEYLINE_OK;
 }
@@ -255,6 +263,13 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     ChunkPlan cp;
     rc = check_chunks(p->g, *bt, chunks, n, b->max_tokens, p->q_tail - p->q_head, p->q_head, &cp);
     if (rc != LEYLINE_OK) return rc;
+
+    PlanMark mark;
+    mark.table = bt->table;
+    for (const ChunkDev& c : cp.chunks)
+        if (c.n > 0) mark.reqs.push_back(c.req);
+    std::sort(mark.reqs.begin(), mark.reqs.end());
+    mark.since_checkpoint = true;
 
     const int slot = b->next_slot;
     if (b->slot_used[slot]) {  // the install that read this staging slot may still be in flight
@@ -309,6 +324,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     p->q_head += cp.pages;
     if (cp.rewrites) p->ckpt_turned = true;
     b->planned = true;
+    std::swap(b->mark, mark);
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
@@ -337,7 +353,8 @@ int leyline_batch_destroy(leyline_batch_t* b)
     if (!b) return bad("null batch");
     DeviceGuard guard(b->pool->device);
     int rc = wait_pool(b->pool);
-    --b->pool->batches;
+    std::vector<PlanMark*>& live = b->pool->batches;
+    live.erase(std::find(live.begin(), live.end(), &b->mark));
     free_batch(b);
     return rc;
 }

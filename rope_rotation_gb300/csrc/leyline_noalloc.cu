@@ -200,6 +200,7 @@ extern "C" int leyline_splice_noalloc(leyline_pool_t* p, leyline_block_table_t* 
     if (plan.reindex && !p->d_pending) p->ckpt_turned = true;  // bands turned in place
 
     for (const ReqPlan& rp : plan.reqs) bt->seq_lens_host[rp.req] = rp.new_len;
+    outdate_plans(p, bt->table, plan);
     p->q_head += plan.total_pop;
     p->q_tail += plan.total_push;
     p->last_stats = plan.stats;

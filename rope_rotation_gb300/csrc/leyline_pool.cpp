@@ -272,7 +272,7 @@ int leyline_pool_create(const leyline_pool_desc_t* desc, void* kv_dev, leyline_p
 int leyline_pool_destroy(leyline_pool_t* p)
 {
     if (!p) return set_error(LEYLINE_ERR_INVALID_ARG, "null pool");
-    if (p->batches > 0) return set_error(LEYLINE_ERR_INVALID_ARG, "the pool still has batches: destroy them first");
+    if (!p->batches.empty()) return set_error(LEYLINE_ERR_INVALID_ARG, "the pool still has batches: destroy them first");
     DeviceGuard guard(p->device);
     if (p->has_work) cudaEventSynchronize(p->done);
     for (auto& ev : p->tev) {
@@ -568,6 +568,7 @@ int leyline_splice(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_d
     }
 
     for (const ReqPlan& rp : plan.reqs) bt->seq_lens_host[rp.req] = rp.new_len;
+    outdate_plans(p, bt->table, plan);
     p->q_head += plan.total_pop;
     p->q_tail += plan.total_push;
     p->last_stats = plan.stats;
@@ -732,6 +733,7 @@ int leyline_pool_checkpoint(leyline_pool_t* p, void* stream_v)
     p->ckpt_head = p->q_head;
     p->ckpt_tail = p->q_tail;
     p->ckpt_turned = false;
+    for (PlanMark* m : p->batches) m->since_checkpoint = false;
     return LEYLINE_OK;
 }
 
@@ -785,6 +787,7 @@ int leyline_pool_rollback(leyline_pool_t* p, int32_t flags, void* stream_v)
     p->q_head = p->ckpt_head;
     p->q_tail = p->ckpt_tail;
     p->ckpt_turned = false;
+    for (PlanMark* m : p->batches) m->stale |= m->since_checkpoint;  // its pages are free again
     return LEYLINE_OK;
 }
 

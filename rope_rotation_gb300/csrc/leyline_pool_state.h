@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <utility>
 #include <vector>
@@ -34,6 +35,14 @@ struct DeviceGuard {
     {
         if (prev >= 0) cudaSetDevice(prev);
     }
+};
+
+// The plan of a live batch, as later edits of the cache see it.
+struct PlanMark {
+    const int32_t* table = nullptr;
+    std::vector<int32_t> reqs;       // requests with new tokens, sorted
+    bool since_checkpoint = false;   // made after the pool's checkpoint
+    bool stale = false;              // an edit has changed one of its requests
 };
 }  // namespace leyline
 
@@ -101,7 +110,7 @@ struct leyline_pool {
     int64_t ckpt_head = 0;
     int64_t ckpt_tail = 0;
     bool ckpt_turned = false;  // stored rows were changed in place since the checkpoint
-    int batches = 0;           // live batches (leyline_batch_create)
+    std::vector<leyline::PlanMark*> batches;  // of live batches (leyline_batch_create)
 };
 
 namespace leyline {
@@ -115,4 +124,12 @@ int refuse_capture(cudaStream_t stream, const char* what);
 int order_after_previous(leyline_pool* p, cudaStream_t stream);
 // Record the pool's last enqueued work.
 int mark_done(leyline_pool* p, cudaStream_t stream);
+// A splice has rewritten the plan's requests of a table: batch plans made for their old rows no longer hold.
+inline void outdate_plans(leyline_pool* p, const int32_t* table, const Plan& splice)
+{
+    for (PlanMark* m : p->batches)
+        if (m->table == table)
+            for (const ReqPlan& r : splice.reqs)
+                if (std::binary_search(m->reqs.begin(), m->reqs.end(), r.req)) m->stale = true;
+}
 }  // namespace leyline

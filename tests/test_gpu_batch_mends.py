@@ -178,3 +178,66 @@ def test_views_that_overlap_the_queries_are_refused():
     b.rotate(at(0, 64), out=at(64, 64))
     cache.check_status()
     cache.close()
+
+
+@pytest.mark.parametrize("noalloc", [False, True])
+def test_plans_that_an_edit_has_outdated_are_refused(noalloc):
+    """After a splice of one of its requests a plan's slots may be another request's, after a rollback free ones."""
+    from rope_rotation_gb300 import leyline
+    from rope_rotation_gb300.leyline import LeylineError
+    cache = BH.make_cache([100, 80, 60], extra=64, layers=1, slack=50)
+    b, other = cache.batch(3, 16, 4), cache.batch(1, 16, 4)
+    rows, ql, q = BH.bf16(3, 576), BH.bf16(3, 4, 512), BH.bf16(3, 4, 64)
+
+    def splice(req):
+        dirs = [leyline.directive(req, 10, 30)]
+        if noalloc:
+            leyline.leyline_splice_noalloc(cache.pool, cache.tables, dirs)
+        else:
+            cache.splice(dirs)
+
+    def calls(batch=b):
+        batch.append(0, rows)
+        batch.rotate(q)
+        batch.attention(0, ql, q, 0.07)
+
+    def refused():
+        torch.cuda.synchronize()
+        before = cache.kv.clone()
+        for call in (lambda: b.append(0, rows), lambda: b.rotate(q), lambda: b.attention(0, ql, q, 0.07)):
+            with pytest.raises(LeylineError) as e:
+                call()
+            assert e.value.code == -1
+        assert torch.equal(before.view(torch.int16), cache.kv.view(torch.int16))
+    b.plan([(0, 100, 2), (2, 60, 1), (1, 80, 0)])
+    calls()
+    splice(1)  # no new tokens of this one
+    calls()
+    splice(2)
+    refused()
+    other.plan([(1, 60, 3)])  # another batch's plan does not make this one's good
+    calls(other)
+    refused()
+    b.plan([(2, 30, 3)])
+    calls()
+    table, lens = cache.table.clone(), cache.seq_lens_host.copy()
+    leyline.leyline_pool_checkpoint(cache.pool)
+    other.plan([(1, 63, 1)])
+    calls(other)
+    leyline.leyline_pool_rollback(cache.pool)
+    cache.table.copy_(table)
+    cache.seq_lens_dev.copy_(torch.from_numpy(lens).to(torch.int32))
+    cache.seq_lens_host[:] = lens
+    calls()  # made before the checkpoint
+    with pytest.raises(LeylineError):
+        other.append(0, rows)
+    b.plan([(0, 100, 1), (2, 10, 2)])
+    calls()
+    with pytest.raises(LeylineError):  # rows were written again
+        leyline.leyline_pool_rollback(cache.pool)
+    leyline.leyline_pool_rollback(cache.pool, leyline.LEYLINE_ROLLBACK_ACCEPT_TURNED)
+    refused()
+    b.plan([])
+    b.append(0, rows[:0])  # nothing to do
+    cache.check_status()
+    cache.close()
