@@ -446,7 +446,8 @@ typedef struct {
  * attention workspace (partial outputs of row tiles whose rows are split over
  * several CTAs: some 40 MiB for MLA rows).  Synchronous.  The pool cannot be
  * destroyed while it has batches.
- * Errors: INVALID_ARG (null argument, sizes out of range, or a pool whose rows
+ * Errors: INVALID_ARG (null argument, sizes out of range, max_tokens * q_heads /
+ * rope_heads not below 2^31 - 128, or a pool whose rows
  * leyline_attention does not take: latent_dim not a multiple of 8 * rope_heads,
  * zero or above 1024, rope_dim above 256), CUDA. */
 int leyline_batch_create(leyline_pool_t* pool, int32_t max_chunks, int32_t max_tokens, int32_t q_heads,

@@ -184,12 +184,8 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
 {
     const Geometry& g = p->g;
     const int32_t bands = std::max(g.rope_heads, 1);
-    if (max_chunks < 1 || max_chunks > (1 << 16)) return bad("max_chunks must be in [1, 65536]");
-    if (max_tokens < 1 || max_tokens > (1 << 22)) return bad("max_tokens must be in [1, 4194304]");
-    if (q_heads < 1 || q_heads > 1024) return bad("q_heads must be in [1, 1024]");
-    if (g.latent_dim < 8 || g.latent_dim > kAttnMaxValue || g.latent_dim % (8 * bands) != 0)
-        return bad("attention needs a latent_dim in [8, 1024], a multiple of 8 * rope_heads");
-    if (g.rope_dim > kAttnMaxRope) return bad("attention needs rope_dim <= 256");
+    const int checked = check_sizes(g, max_chunks, max_tokens, q_heads);
+    if (checked != LEYLINE_OK) return checked;
     DeviceGuard guard(p->device);
     if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
     leyline_batch* b = new leyline_batch();

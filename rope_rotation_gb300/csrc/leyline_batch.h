@@ -98,6 +98,8 @@ struct ChunkPlan {
     int64_t pages = 0;
     bool rewrites = false;  // rows that existed before are written again
 };
+// Validate a batch's sizes for a pool's rows.
+int check_sizes(const Geometry& g, int32_t max_chunks, int32_t max_tokens, int32_t q_heads);
 // Validate a plan's chunks against the table's lengths and lay out their runs; pop_base is the
 // ring position of the first page the plan takes.  Returns LEYLINE_OK or an error code (the
 // message is set); changes nothing but *out.

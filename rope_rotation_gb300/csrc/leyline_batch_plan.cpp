@@ -61,6 +61,21 @@ bool overlap(Extent a, Extent b)
     return x != kNo;
 }
 
+int check_sizes(const Geometry& g, int32_t max_chunks, int32_t max_tokens, int32_t q_heads)
+{
+    const int32_t bands = std::max(g.rope_heads, 1);
+    if (max_chunks < 1 || max_chunks > (1 << 16)) return bad("max_chunks must be in [1, 65536]");
+    if (max_tokens < 1 || max_tokens > (1 << 22)) return bad("max_tokens must be in [1, 4194304]");
+    if (q_heads < 1 || q_heads > 1024) return bad("q_heads must be in [1, 1024]");
+    if (g.latent_dim < 8 || g.latent_dim > kAttnMaxValue || g.latent_dim % (8 * bands) != 0)
+        return bad("attention needs a latent_dim in [8, 1024], a multiple of 8 * rope_heads");
+    if (g.rope_dim > kAttnMaxRope) return bad("attention needs rope_dim <= 256");
+    // the kernels count a chunk's query rows of a band in 32 bits
+    if (q_heads % bands == 0 && (int64_t)max_tokens * (q_heads / bands) > INT32_MAX - kPairRows)
+        return bad("max_tokens * q_heads / rope_heads must be below 2^31 - 128");
+    return LEYLINE_OK;
+}
+
 int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyline_chunk_t* chunks, int32_t n,
                  int64_t max_tokens, int64_t free_pages, int64_t pop_base, ChunkPlan* out)
 {
