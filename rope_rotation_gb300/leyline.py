@@ -426,8 +426,19 @@ def leyline_batch_plan(batch, tables: Tables, chunks, stream=None) -> None:
     _check(load().leyline_batch_plan(batch, ctypes.byref(tables.bt), a.ctypes.data, a.size, _stream_ptr(stream)))
 
 
+def _without_gradient(t, what: str):
+    """The operators of a batch have no backward pass: a tensor that would need one is refused."""
+    if t is not None and t.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            raise ValueError(f"{what}: requires a gradient, and the operators of a batch have none (detach it, or call "
+                             "under torch.no_grad())")
+    return t
+
+
 def heads(t, what: str, tokens: int, n_heads: int, dim: int) -> Heads:
     """A view of a bf16 tensor [>= tokens][n_heads][dim] whose last axis is contiguous."""
+    _without_gradient(t, what)
     if t.dtype != _bf16():
         raise ValueError(f"{what}: dtype {t.dtype}, expected torch.bfloat16")
     shape = t.shape
@@ -452,6 +463,8 @@ def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps
     """rows: bf16 [tokens][row] whose last axis is contiguous, on the pool's GPU or in pinned host
     memory; latent_norm, key_norm: contiguous bf16 weights or None."""
     import torch
+    for t, what in ((rows, "rows"), (latent_norm, "latent_norm"), (key_norm, "key_norm")):
+        _without_gradient(t, what)
     if rows.dtype != torch.bfloat16:
         raise ValueError(f"rows: dtype {rows.dtype}, expected torch.bfloat16")
     if rows.dim() != 2 or rows.stride(1) != 1:
@@ -465,6 +478,7 @@ def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps
 
 def leyline_rotate(batch, q: Heads, out: Heads, norm=None, eps: float = 1e-6, stream=None) -> None:
     """q, out: heads(); norm: contiguous bf16 weights or None."""
+    _without_gradient(norm, "norm")
     _check(load().leyline_rotate(batch, ctypes.byref(q), ctypes.byref(out),
                                  None if norm is None else _rows_ptr(norm, "norm"), eps, _stream_ptr(stream)))
 
@@ -472,6 +486,7 @@ def leyline_rotate(batch, q: Heads, out: Heads, norm=None, eps: float = 1e-6, st
 def leyline_attention(batch, layer: int, q_latent: Optional[Heads], q_rope: Heads, out: Heads, lse, scale: float,
                       flags: int = 0, stream=None) -> None:
     """q_latent (None for rows of several bands), q_rope, out: heads(); lse: contiguous fp32 or None."""
+    _without_gradient(lse, "lse")
     _check(load().leyline_attention(batch, layer, None if q_latent is None else ctypes.byref(q_latent),
                                     ctypes.byref(q_rope), ctypes.byref(out),
                                     None if lse is None else lse.data_ptr(), scale, flags, _stream_ptr(stream)))

@@ -194,6 +194,7 @@ class Batch:
     attention() then serve each layer, on tensors whose first axis is the plan's tokens, chunk after
     chunk.  The last three can be captured into a CUDA graph and replayed after each new plan,
     on tensors with room for max_tokens.  Outputs that a call makes belong to the stream it runs on.
+    There is no backward pass: tensors that require a gradient are refused outside torch.no_grad().
     """
 
     def __init__(self, cache: PagedCache, max_chunks: int, max_tokens: int, q_heads: int):

@@ -1,5 +1,5 @@
 """What a batch refuses, on the CPU and under the sanitizers: views of token tensors that overlap, fuzzed against the bytes
-they name, and sizes."""
+they name, sizes, and tensors that require a gradient."""
 import os
 import shutil
 import subprocess
@@ -41,3 +41,21 @@ def test_overlap_of_views_under_sanitizers(tmp_path):
 
 def test_sizes_of_a_batch(tmp_path):
     _run(_build(tmp_path, "batch_sizes_sanitize"))
+
+
+def test_tensors_that_require_a_gradient():
+    """There is no backward pass: the output would silently have no gradient.  No device is touched."""
+    torch = pytest.importorskip("torch")
+    from rope_rotation_gb300 import leyline as L
+    q = torch.zeros(4, 6, 64, dtype=torch.bfloat16, requires_grad=True)
+    rows, w = q.view(24, 64)[:4], torch.zeros(64, dtype=torch.bfloat16, requires_grad=True)
+    plain = L.heads(q.detach(), "q", 4, 6, 64)
+    for call in (lambda: L.heads(q, "q", 4, 6, 64), lambda: L.leyline_append(None, 0, rows),
+                 lambda: L.leyline_append(None, 0, rows.detach(), latent_norm=w),
+                 lambda: L.leyline_append(None, 0, rows.detach(), key_norm=w),
+                 lambda: L.leyline_rotate(None, plain, plain, norm=w),
+                 lambda: L.leyline_attention(None, 0, plain, plain, plain, torch.zeros(4, 6, requires_grad=True), 1.0)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():
+        assert L.heads(q, "q", 4, 6, 64).token_stride == 384
