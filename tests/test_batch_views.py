@@ -1,5 +1,5 @@
-"""What a batch refuses, on the CPU and under the sanitizers: views of token tensors that overlap, fuzzed against the bytes
-they name, sizes, and tensors that require a gradient."""
+"""The host side of a batch, on the CPU and under the sanitizers: views of token tensors that overlap, fuzzed against the
+bytes they name, sizes, the split of the attention's work, and tensors that require a gradient."""
 import os
 import shutil
 import subprocess
@@ -41,6 +41,12 @@ def test_overlap_of_views_under_sanitizers(tmp_path):
 
 def test_sizes_of_a_batch(tmp_path):
     _run(_build(tmp_path, "batch_sizes_sanitize"))
+
+
+def test_split_of_the_work_with_both_item_costs(tmp_path):
+    exe = _build(tmp_path, "batch_split_sanitize")
+    for seed in ("1", "2"):
+        _run(exe, "4000", seed)
 
 
 def test_tensors_that_require_a_gradient():
