@@ -63,8 +63,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Wait for the phase of `parity`.  False when the CTA has given up (*quit set here or elsewhere).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit, int32_t* status)
+// Wait for the phase of `parity`, up to `limit` ns.  False when the CTA has given up (*quit set here or elsewhere).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit, int32_t* status,
+                                          unsigned long long limit = kWaitLimit)
 {
     if (mbar_try(bar, parity)) return true;
     unsigned long long t0 = 0;
@@ -72,7 +73,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         if (spins % 64 != 0) continue;  // reading the clock is slow
         if (*quit) return false;
         if (t0 == 0) t0 = global_ns();
-        if (global_ns() - t0 > kWaitLimit) {
+        if (global_ns() - t0 > limit) {
             *quit = 1;
             raise_status(status, ST_TIMEOUT);
             return false;
@@ -165,7 +166,8 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 }
 
 // mbar_wait for barriers that the other CTA arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* quit, int32_t* status)
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* quit, int32_t* status,
+                                                  unsigned long long limit = kWaitLimit)
 {
     if (mbar_try_cluster(bar, parity)) return true;
     unsigned long long t0 = 0;
@@ -173,7 +175,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         if (spins % 64 != 0) continue;
         if (*quit) return false;
         if (t0 == 0) t0 = global_ns();
-        if (global_ns() - t0 > kWaitLimit) {
+        if (global_ns() - t0 > limit) {
             *quit = 1;
             raise_status(status, ST_TIMEOUT);
             return false;
