@@ -179,6 +179,18 @@ def current_stream_ptr(device: int) -> int:
     return _current_raw_stream(device)
 
 
+_captures = None
+
+
+def current_stream_captures() -> bool:
+    """Whether the current stream is being captured into a graph (torch.cuda.is_current_stream_capturing, looked up once)."""
+    global _captures
+    if _captures is None:
+        import torch
+        _captures = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+    return _captures()
+
+
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -426,19 +438,18 @@ def leyline_batch_plan(batch, tables: Tables, chunks, stream=None) -> None:
     _check(load().leyline_batch_plan(batch, ctypes.byref(tables.bt), a.ctypes.data, a.size, _stream_ptr(stream)))
 
 
-def _without_gradient(t, what: str):
+def _refuse_gradient(what: str) -> None:
     """The operators of a batch have no backward pass: a tensor that would need one is refused."""
-    if t is not None and t.requires_grad:
-        import torch
-        if torch.is_grad_enabled():
-            raise ValueError(f"{what}: requires a gradient, and the operators of a batch have none (detach it, or call "
-                             "under torch.no_grad())")
-    return t
+    import torch
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what}: requires a gradient, and the operators of a batch have none (detach it, or call "
+                         "under torch.no_grad())")
 
 
 def heads(t, what: str, tokens: int, n_heads: int, dim: int) -> Heads:
     """A view of a bf16 tensor [>= tokens][n_heads][dim] whose last axis is contiguous."""
-    _without_gradient(t, what)
+    if t.requires_grad:
+        _refuse_gradient(what)
     if t.dtype != _bf16():
         raise ValueError(f"{what}: dtype {t.dtype}, expected torch.bfloat16")
     shape = t.shape
@@ -463,8 +474,12 @@ def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps
     """rows: bf16 [tokens][row] whose last axis is contiguous, on the pool's GPU or in pinned host
     memory; latent_norm, key_norm: contiguous bf16 weights or None."""
     import torch
-    for t, what in ((rows, "rows"), (latent_norm, "latent_norm"), (key_norm, "key_norm")):
-        _without_gradient(t, what)
+    if rows.requires_grad:
+        _refuse_gradient("rows")
+    if latent_norm is not None and latent_norm.requires_grad:
+        _refuse_gradient("latent_norm")
+    if key_norm is not None and key_norm.requires_grad:
+        _refuse_gradient("key_norm")
     if rows.dtype != torch.bfloat16:
         raise ValueError(f"rows: dtype {rows.dtype}, expected torch.bfloat16")
     if rows.dim() != 2 or rows.stride(1) != 1:
@@ -478,7 +493,8 @@ def leyline_append(batch, layer: int, rows, latent_norm=None, key_norm=None, eps
 
 def leyline_rotate(batch, q: Heads, out: Heads, norm=None, eps: float = 1e-6, stream=None) -> None:
     """q, out: heads(); norm: contiguous bf16 weights or None."""
-    _without_gradient(norm, "norm")
+    if norm is not None and norm.requires_grad:
+        _refuse_gradient("norm")
     _check(load().leyline_rotate(batch, ctypes.byref(q), ctypes.byref(out),
                                  None if norm is None else _rows_ptr(norm, "norm"), eps, _stream_ptr(stream)))
 
@@ -486,7 +502,8 @@ def leyline_rotate(batch, q: Heads, out: Heads, norm=None, eps: float = 1e-6, st
 def leyline_attention(batch, layer: int, q_latent: Optional[Heads], q_rope: Heads, out: Heads, lse, scale: float,
                       flags: int = 0, stream=None) -> None:
     """q_latent (None for rows of several bands), q_rope, out: heads(); lse: contiguous fp32 or None."""
-    _without_gradient(lse, "lse")
+    if lse is not None and lse.requires_grad:
+        _refuse_gradient("lse")
     _check(load().leyline_attention(batch, layer, None if q_latent is None else ctypes.byref(q_latent),
                                     ctypes.byref(q_rope), ctypes.byref(out),
                                     None if lse is None else lse.data_ptr(), scale, flags, _stream_ptr(stream)))

@@ -230,20 +230,22 @@ class Batch:
             raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({n},)")
         return t if t is None else self._device(t, what)
 
-    def _room(self, stream, *tensors) -> int:
+    def _room(self, stream) -> int:
         """Tokens that the tensors of a call must have room for: the plan's, and under capture max_tokens, since the graph
         may be replayed with any plan."""
-        if all(t is None or t.dim() > 0 and t.shape[0] >= self.max_tokens for t in tensors):
+        if self.tokens == self.max_tokens:
             return self.tokens
+        if stream is None:
+            return self.max_tokens if leyline.current_stream_captures() else self.tokens
         with self.cache.allocating(stream):
-            return self.max_tokens if self.cache.torch.cuda.is_current_stream_capturing() else self.tokens
+            return self.max_tokens if leyline.current_stream_captures() else self.tokens
 
     def _heads(self, t, what: str, tokens: int, dim: int) -> leyline.Heads:
         return leyline.heads(self._device(t, what), what, tokens, self.q_heads, dim)
 
     def append(self, layer: int, rows, latent_norm=None, key_norm=None, eps: float = 1e-6, stream=None) -> None:
         """Write rows [tokens][row] of one layer, normed and turned by their positions."""
-        tokens = self._room(stream, rows)
+        tokens = self._room(stream)
         if rows.dim() != 2 or rows.shape[0] < tokens or rows.shape[1] != self.cache.row:
             raise ValueError(f"rows: shape {tuple(rows.shape)}, expected [>= {tokens}][{self.cache.row}]")
         leyline.leyline_append(self.handle, layer, rows,
@@ -255,7 +257,7 @@ class Batch:
         if out is None:
             with self.cache.allocating(stream):
                 out = self.cache.torch.empty_like(q)
-        dim, tokens = self.cache.rope_dim, self._room(stream, q, out)
+        dim, tokens = self.cache.rope_dim, self._room(stream)
         leyline.leyline_rotate(self.handle, self._heads(q, "q", tokens, dim), self._heads(out, "out", tokens, dim),
                                self._weights(norm, "norm", dim), eps, self._stream(stream))
         return out
@@ -272,7 +274,7 @@ class Batch:
         if lse is None:
             with self.cache.allocating(stream):
                 lse = torch.empty((q_rope.shape[0], self.q_heads), dtype=torch.float32, device=self.cache.kv.device)
-        tokens = self._room(stream, q_latent, q_rope, out, lse)
+        tokens = self._room(stream)
         if (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < tokens
                 or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
             raise ValueError(f"lse: expected contiguous fp32 [>= {tokens}][{self.q_heads}]")
