@@ -411,7 +411,9 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * captured are refused (INVALID_ARG) until the next plan; replays and freed pages the
  * library does not see.
  * rope_start is the rotary position of the chunk's first token: start, unless
- * EVICT directives left the request's survivors at other positions.
+ * EVICT directives left the request's survivors at other positions.  Frequencies are
+ * the pool's, rope_theta^(-2j/d): the turns of this library, a splice's like those of
+ * leyline_append and leyline_rotate, are not for a model that scales them otherwise.
  *
  * CUDA graphs.  leyline_batch_plan runs on the host for the lengths as they stand
  * and refuses a stream under capture.  leyline_append, leyline_rotate and
@@ -464,8 +466,9 @@ int leyline_batch_destroy(leyline_batch_t* batch);
  * seq_lens_host is updated at enqueue time.  Several chunks may name one request:
  * in the order given each starts at or below the length that the ones before it
  * leave, and their rows do not overlap.
- * Writing rows that existed at a leyline_pool_checkpoint counts as changing stored
- * rows in place: leyline_pool_rollback then asks for LEYLINE_ROLLBACK_ACCEPT_TURNED.
+ * Writing rows again (below the length that the request had before the plan) counts as
+ * changing stored rows in place: leyline_pool_rollback to a checkpoint made before then
+ * asks for LEYLINE_ROLLBACK_ACCEPT_TURNED.
  * Errors (nothing is enqueued or changed): INVALID_ARG (null argument, a bad chunk
  * field, more chunks or tokens than the batch holds, overlapping chunks, `stream`
  * under graph capture), CAPACITY (a length above max_blocks * block_size),
@@ -482,7 +485,7 @@ int leyline_batch_plan(leyline_batch_t* batch, leyline_block_table_t* bt, const 
  * position.  Everything is computed in fp32 and rounded once to bf16 (with
  * LEYLINE_ROTATE_BF16_NAIVE the turn rounds as a splice's does, after a norm that is
  * rounded to bf16); without norms the latent is copied bit for bit.  Enqueues one kernel; rows may lie in pinned
- * host memory.  Every row must be finite for a norm to be.
+ * host memory, but not in slots of the pool that the call writes.  Every row must be finite for a norm to be.
  * Errors: INVALID_ARG, CUDA. */
 int leyline_append(leyline_batch_t* batch, int32_t layer, const void* rows, int64_t row_stride,
                    const void* latent_norm, const void* key_norm, float eps, void* stream);
@@ -515,10 +518,12 @@ int leyline_rotate(leyline_batch_t* batch, const leyline_heads_t* q, const leyli
  * overlap the queries, nor one another (INVALID_ARG).  Views that interleave without
  * sharing a byte are fine if they have their token stride or their head stride in common.
  * Scores and sums are fp32; the weights exp(x - max) are rounded to bf16 for
- * the product with the values.  A row tile whose output is not finite, or whose scores
- * rise by more than 55 over those of the tile's first 64 rows, is computed again one
- * row at a time (a slow path).  Enqueues one kernel, and a second one that joins the
- * partial results of split row tiles.  Two calls on the same inputs and plan give
+ * the product with the values, and the output is divided by the sum of the rounded ones.
+ * A row tile whose output is not finite, or (MLA rows of eager pools) whose scores
+ * rise by more than 55 over those of the first 64 rows of its share, is computed again
+ * one row at a time, 20 to 200 times slower.  Enqueues one kernel, and a second one that
+ * joins the partial results of split row tiles; under capture both kinds of kernel and a
+ * join for any plan, some 3 to 70 us a call.  Two calls on the same inputs and plan give
  * the same bits.
  * Errors: INVALID_ARG, CUDA. */
 #define LEYLINE_ATTENTION_PREFIX 1

@@ -13,17 +13,20 @@
 // fp32 as exact relative to their size as any.  A later score above m0 by more than 80 (as a power of 2) could leave
 // fp32's range in the sums; the item is then marked, as is one whose output is not finite, and computed
 // again at the end without the tensor cores (leyline_attention_any.cuh).  So O never has to be rescaled, which would
-// take both CTAs to agree in the middle of every tile.
+// take both CTAs to agree in the middle of every tile.  Marked items are far slower: with all of them marked a prompt
+// chunk of 512 tokens of 128 heads over 8192 rows takes 143 ms instead of 0.73, 16 decodes of 128 heads over some 16000
+// rows 9.2 ms instead of 0.079; one request of the 16 alone takes as long, since its pairs finish last.
 //
 // Roles in each CTA: warps 0-3 softmax and output, warp 4 issues the products (in the first CTA alone), warps 5-6 load
 // K and 7-10 V (TMA, one lane each: a thread issues a TMA instruction in 100 to 170 cycles, whatever its size, and a
 // thread alone bound the kernel; where 8 does not divide the block size they copy their rows, a warp each), warps
 // 11-14 copy the queries and the tiles that end inside.
 //
-// Bounds and measurements (GB300; cuBLAS bf16 at 1875 TFLOP/s).  The products take 864 + 512 cycles a tile, all of it
-// 1530, and an item's ends 13000.  A prompt chunk of 512 tokens of 128 heads over 8192 rows 718 us (1.58 PFLOP/s, 0.84 of
-// measured), ragged chunks of 61 tokens of 16 heads 147 us (1.2), 16 decodes of 128 heads over 24000 rows 117 us (5.1 TB/s,
-// 0.75 of measured copies; 1.2 PFLOP/s).  One row a page, copied: 817, 200 and 142 us (by single CTAs 1426, 255 and 213).
+// Bounds and measurements (GB300; cuBLAS bf16 at 1875 TFLOP/s in a burst, 1674 under the power limit; calls back to back
+// over four inputs in turn).  The products take 864 + 512 cycles a tile, all of it 1530, and an item's ends 13000.  A prompt
+// chunk of 512 tokens of 128 heads over 8192 rows 780 us (1.45 PFLOP/s, 0.77 of the burst, 0.87 of the other; clocks at 1850
+// to 1940 MHz), ragged chunks of 61 tokens of 16 heads 147 us (1.2), 16 decodes of 128 heads over 24000 rows 118 us (5.0 TB/s,
+// 0.74 of measured copies; 1.2 PFLOP/s).  One row a page, copied: 867, 198 and 144 us.
 #include "leyline_attention.cuh"
 
 namespace leyline {
@@ -86,8 +89,10 @@ __device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, Mi
 // -------------------------------------------------------------------- loads --
 // The keys' loaders ask for the next tile's rows in L2 before they wait for a free stage: two tiles in shared memory are
 // too few bytes in flight for HBM's latency.  For chunks of few row tiles alone: the rows of a long chunk are in L2
-// already, and asking costs the loaders time (16 decodes of 128 heads, one tile each: 135 us without, 124 with; ragged
-// chunks of 8 tiles: 165, 163; a prompt chunk of 512 tiles: 747, 772).
+// already, and asking costs the loaders time.  Without and with, us: 16 decodes of 128 heads, one tile each, 135, 124; 8
+// requests over 8000 rows with 7, 12, 24 and 48 tiles each 120.5, 117; 170.5, 166.4; 313.2, 309.4; 617, 612; one over 8192
+// rows with 8, 16, 32, 64 and 128 tiles 32.5, 32.7; 42.6, 42.9; 65.0, 65.1; 112.4, 113.0; 205.1, 205.9; with 512 747, 772.
+// The border costs up to 2.5% between 9 and 48 tiles of several requests; past it one long chunk is what loses.
 constexpr int kPrefetchTiles = 8;
 
 // `n` rows at a page's row, whole.

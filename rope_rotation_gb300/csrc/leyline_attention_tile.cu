@@ -31,13 +31,14 @@
 // The maximum is only raised (and O rescaled) when a row's scores exceed it by 2^8: until then the
 // weights are at most 2^8, and sums and products are fp32.
 // An item whose output is not finite is computed again, without the tensor cores: there a weight of 0 keeps a masked
-// row's infinity or NaN out of the sum, in a matrix product it does not.
+// row's infinity or NaN out of the sum, in a matrix product it does not.  That is far slower: one NaN in an attended row of
+// one of 64 requests of 16 heads over 4000 rows 1.34 ms instead of 0.070, of one of 16 with grouped drafts 1.9 instead of 0.058.
 //
-// Bounds and measurements (GB300; HBM copies at 6782 GB/s).  MLA: shared memory carries 2500 cycles of operands a tile; a
-// tile takes 3400 from L2 and 3800 to 4400 from HBM, two of them in flight.  One decode of 16 heads over 32768 rows 18 us
-// (14 here, the rest the join), 64 over 4000 rows 78 us (4.8 TB/s).  Grouped: HBM; 4 drafted tokens of 16 requests, 32 heads on
-// 4 bands of 128, 70 us (5.0 TB/s, 0.74 of measured).  Lazy MLA rows one a page: 108 us for 64 requests over 4000 (3.4 TB/s),
-// by the copies of single rows and the turns; 16 rows a page 88.
+// Bounds and measurements (GB300; HBM copies at 6782 GB/s; calls back to back over four inputs in turn).  MLA: shared memory carries 2500 cycles of operands a tile; a
+// tile takes 3400 from L2 and 3800 to 4400 from HBM, two of them in flight.  One decode of 16 heads over 32768 rows 22 us
+// (18 with one input over and over, in L2: 14 here, the rest the join), 64 over 4000 rows 77 us (4.8 TB/s).  Grouped: HBM; 4
+// drafted tokens of 16 requests, 32 heads on 4 bands of 128, 73 us (4.8 TB/s, 0.71 of measured).  Lazy MLA rows one a page:
+// 112 us for 64 requests over 4000 (3.3 TB/s), by the copies of single rows and the turns; 16 rows a page 92.
 #include "leyline_attention.cuh"
 
 namespace leyline {
