@@ -129,8 +129,9 @@ class PagedCache:
         current then, and may hand out one that another stream's kernels still use (None: the current stream)."""
         if stream is None:
             return contextlib.nullcontext()
-        if isinstance(stream, int):
-            stream = self.torch.cuda.ExternalStream(stream, device=self.kv.device)
+        if not isinstance(stream, self.torch.cuda.Stream):  # an address, or another library's stream
+            address = stream if isinstance(stream, int) else stream.cuda_stream
+            stream = self.torch.cuda.ExternalStream(address, device=self.kv.device)
         return self.torch.cuda.stream(stream)
 
     def gather(self, req: int, layer: int, t0: int, t1: int, out=None, stream=None):

@@ -59,8 +59,15 @@ def _stream_of(t):
     raise AssertionError("no segment holds the tensor")
 
 
-@pytest.mark.parametrize("address", [False, True])
-def test_outputs_belong_to_the_stream_of_their_call(address):
+class _ForeignStream:
+    """Another library's stream: an object with the address."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("kind", ["torch", "address", "foreign"])
+def test_outputs_belong_to_the_stream_of_their_call(kind):
     """Made for the current stream, they could be blocks that its kernels still read, or be handed out again while the
     call's stream writes them."""
     cache = BH.make_cache([100], extra=8, layers=1)
@@ -71,7 +78,7 @@ def test_outputs_belong_to_the_stream_of_their_call(address):
     want = (b.rotate(q), *b.attention(0, ql, q, 0.07), cache.gather(0, 0, 0, 103))
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    s = side.cuda_stream if address else side
+    s = {"torch": side, "address": side.cuda_stream, "foreign": _ForeignStream(side)}[kind]
     got = (b.rotate(q, stream=s), *b.attention(0, ql, q, 0.07, stream=s), cache.gather(0, 0, 0, 103, stream=s))
     torch.cuda.synchronize()
     for x, y in zip(want, got):
