@@ -105,11 +105,11 @@ def draw(rng):
     keep = rng.choice([0.02, 0.25, 0.5, 0.5, 0.9, 0.99])
     ends = {"first": rng.choice([0, 1, 4, 37]), "last": rng.choice([0, 1, 64, 333])}
     if op == "select":
-        reqs, ctx = _log_int(rng, 1, 64), _log_int(rng, 16, 131072)
+        reqs, ctx = _log_int(rng, 1, 64), _log_int(rng, 100, 131072)
         while reqs * ctx > 2 ** 19:
             reqs = (reqs + 1) // 2
         return _select(None, reqs=reqs, ctx=ctx, keep=keep, **ends, **common)
-    reqs, ctx, layers = _log_int(rng, 1, 32), _log_int(rng, 16, 32768), _log_int(rng, 1, 27)
+    reqs, ctx, layers = _log_int(rng, 1, 32), _log_int(rng, 100, 32768), _log_int(rng, 1, 27)
     while reqs * ctx * layers > 2 ** 19:
         if reqs > 1:
             reqs = (reqs + 1) // 2
@@ -132,12 +132,11 @@ def _lengths(c):
 
 
 def _keeps(c):
-    """(request, rows kept, first rows kept, last rows kept) of each request."""
+    """(request, rows kept, first rows kept, last rows kept) of each request: the weights always have a say."""
     out = []
     for r, (total, _) in enumerate(_lengths(c)):
-        first = min(c["first"], total)
-        last = min(c["last"], total - first)
-        out.append((r, min(total, max(first + last, round(total * c["keep"]))), first, last))
+        first, last = min(c["first"], total // 8), min(c["last"], total // 8)
+        out.append((r, max(min(round(total * c["keep"]), total - 2), first + last + 2), first, last))
     return out
 
 
