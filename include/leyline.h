@@ -531,6 +531,82 @@ int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads
                       const leyline_heads_t* q_rope, const leyline_heads_t* out, float* lse, float scale,
                       int32_t flags, void* stream);
 
+/* ------------------------------------------- eviction by weight ----
+ *
+ * A request that may keep only so many rows loses those that its queries attend to least.  The
+ * pages name the compaction ("evict without resetting positions", the KV-streams page) and leave
+ * the choice of rows to a policy (section 2.3: signal-agnostic); here the policy is the attention
+ * weight that rows have been given:
+ *
+ *     leyline_attention(batch, layer, ..., lse, ...);                       in every layer, and then
+ *     leyline_attention_weights(batch, layer, ..., lse, &weights, ...);     adds up what it gave to each row
+ *     leyline_select_rows(pool, &bt, &weights, keeps, n, kept, ...);        now and then: the rows to keep
+ *     leyline_evict(pool, &bt, keeps, n, kept, ..., &weights, stream);      drops the others
+ *
+ * Lists of rows and weights stay on the device; a list may also come from another policy.  New
+ * rows after an eviction are encoded at the request's next position, not at their row:
+ * leyline_chunk_t.rope_start.
+ *
+ * The caller owns the weights: fp32, row s of request r at ptr[r * req_stride + s], 0 when a request
+ * starts.  One array may serve all layers (rows are dropped from all of them at once).
+ * leyline_evict moves the weights along and clears those behind the new length, so that appended
+ * rows start at 0; a splice or a rollback does not know them. */
+typedef struct {
+    float* ptr;          /* device memory of the pool's GPU, 4-byte aligned */
+    int64_t req_stride;  /* in elements, at least `rows` */
+    int64_t rows;        /* of a request, and */
+    int32_t num_reqs;    /* requests that the array holds */
+} leyline_row_weights_t;
+
+/* Add to the weights what the batch's queries gave to the rows they attend to in `layer`: for
+ * each request of the plan and each row s below the end of its last chunk,
+ *     w_s = decay * w_s + sum over its tokens that attend to s and all heads of
+ *           exp(scale * <query, key_s> - lse),
+ * with queries, scale and flags as leyline_attention takes them and lse ([tokens][q_heads],
+ * contiguous) as it returns it (or merged with that of other rows).  With decay 0 the old weights are not read.  A query
+ * row with lse -inf attends to nothing and adds nothing.  Rows behind, and those of requests that are not in the
+ * plan, are left as they were, and so is a row whose page is bad (status word).  The weights may not overlap
+ * the queries or lse.  Scores, exponentials and sums are fp32; two calls on the same inputs and
+ * plan give the same bits.  Can be captured, like leyline_attention, with weights that hold every
+ * request and row of the plan's block table; a replay whose plan is for another table, with more of them, leaves
+ * such a request's weights as they were (status word).
+ * Errors: INVALID_ARG, CUDA. */
+int leyline_attention_weights(leyline_batch_t* batch, int32_t layer, const leyline_heads_t* q_latent,
+                              const leyline_heads_t* q_rope, const float* lse, const leyline_row_weights_t* weights,
+                              float scale, float decay, int32_t flags, void* stream);
+
+/* What is kept of one request: n_keep of its rows, its first `first` and its last `last` among them. */
+typedef struct {
+    int32_t req;
+    int32_t n_keep;  /* 0 <= n_keep <= length */
+    int32_t first;   /* leyline_select_rows: first, last >= 0 and first + last <= n_keep; */
+    int32_t last;    /* leyline_evict does not look at them */
+} leyline_keep_t;
+
+/* The rows to keep of n distinct requests: those at both ends, and of the others the n_keep - first
+ * - last of greatest weight (equal weights: the lowest rows; -0 equals 0, a NaN is below everything).  The
+ * list of keeps[k] is kept[k * kept_stride ...], n_keep int32 rows in ascending order; what lies behind it is
+ * left as it was.  kept may not overlap the weights.  Enqueues one kernel for 32 requests.
+ * Errors: INVALID_ARG (also when `stream` is being captured: the lengths are those of
+ * seq_lens_host as it stands), CUDA. */
+int leyline_select_rows(leyline_pool_t* pool, const leyline_block_table_t* bt, const leyline_row_weights_t* weights,
+                        const leyline_keep_t* keeps, int32_t n, int32_t* kept, int64_t kept_stride, void* stream);
+
+/* Drop the rows of n distinct requests that are not in their lists (as leyline_select_rows lays them
+ * out): row kept[i] becomes row i in every layer.  Bands stay at the positions they were encoded at, as a
+ * LEYLINE_EVICT directive leaves them; pending turns and, if weights is not NULL, weights move along.
+ * With one row a page only table entries move, and the dropped rows' pages go back to the free list.  Otherwise rows
+ * move within the request's own pages, no free page is needed, and the pages behind the new length go back: stored
+ * rows are then written, and leyline_pool_rollback to a checkpoint made before asks for
+ * LEYLINE_ROLLBACK_ACCEPT_TURNED.  Entries with n_keep equal to the length change nothing.  seq_lens_host and the
+ * free-page count are updated at enqueue time; plans that name a request that lost rows no longer hold.
+ * A list must ascend strictly within [0, length).  If it does not the status word says so, and the
+ * request keeps its first n_keep rows instead.  Enqueues up to four kernels for 32 requests that lose rows.  The
+ * pool's staging buffer holds 8 bytes a kept row; the call waits for the pool's work when it has to grow.
+ * Errors (nothing is enqueued or changed): INVALID_ARG (also when `stream` is being captured).  CUDA. */
+int leyline_evict(leyline_pool_t* pool, leyline_block_table_t* bt, const leyline_keep_t* keeps, int32_t n,
+                  const int32_t* kept, int64_t kept_stride, const leyline_row_weights_t* weights, void* stream);
+
 /* ----------------------------------------------------------- checking ---- */
 
 /* Wait for the pool's enqueued work and read its device status word.  Returns

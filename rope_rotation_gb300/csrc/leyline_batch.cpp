@@ -50,6 +50,10 @@ struct leyline_batch {
     int32_t n_joins = 0;
     bool pairs = false;  // the plan is for pairs
     bool many_parts = false;  // it splits a tile into more than kFewParts
+    int32_t weigh_req = -1;   // its highest request, and the most rows one of them has weighed
+    int64_t weigh_rows = 0;
+    int32_t table_reqs = 0;   // of its block table
+    int64_t table_rows = 0;
 };
 
 namespace {
@@ -57,14 +61,15 @@ namespace {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The plan's device buffer: header, chunks, per-CTA ranges and joins, and last the items, of which a plan copies its own.
+// The plan's device buffer: header, chunks, per-CTA ranges, joins and requests, and last the items, of which a plan copies its own.
 BatchLayout make_layout(int32_t max_chunks, int64_t max_tiles, int32_t ctas)
 {
     BatchLayout l;
     l.chunks = align_up(sizeof(BatchHeader), 16);
     l.cta_begin = align_up(l.chunks + sizeof(ChunkDev) * (size_t)max_chunks, 16);
     l.joins = align_up(l.cta_begin + sizeof(int32_t) * (size_t)(ctas + 1), 16);
-    l.items = align_up(l.joins + sizeof(AttnJoin) * (size_t)ctas, 16);
+    l.weigh = align_up(l.joins + sizeof(AttnJoin) * (size_t)ctas, 16);
+    l.items = align_up(l.weigh + sizeof(WeighReq) * (size_t)max_chunks, 16);
     l.bytes = align_up(l.items + sizeof(AttnItem) * (size_t)(max_tiles + ctas), 16);
     return l;
 }
@@ -285,6 +290,12 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     hd.n_tokens = (int32_t)cp.tokens;
     hd.n_joins = split.n_joins;
     hd.pairs = pairs ? 1 : 0;
+    for (WeighReq& r : cp.weigh) {
+        r.begin = hd.weigh_work;
+        hd.weigh_work += r.end;
+    }
+    hd.weigh_reqs = (int32_t)cp.weigh.size();
+    if (!cp.weigh.empty()) memcpy(h + l.weigh, cp.weigh.data(), sizeof(WeighReq) * cp.weigh.size());
     memcpy(h, &hd, sizeof hd);
     if (!cp.runs.empty()) memcpy(h + l.bytes, cp.runs.data(), sizeof(PlanRun) * cp.runs.size());
 
@@ -324,6 +335,11 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
+    b->weigh_req = cp.weigh.empty() ? -1 : cp.weigh.back().req;
+    b->table_reqs = bt->num_reqs;
+    b->table_rows = (int64_t)bt->max_blocks * p->g.block_size;
+    b->weigh_rows = 0;
+    for (const WeighReq& r : cp.weigh) b->weigh_rows = std::max(b->weigh_rows, r.end);
     b->many_parts = false;
     for (int32_t j = 0; j < split.n_joins; ++j) b->many_parts |= split.joins[j].parts > kFewParts;
     return LEYLINE_OK;
@@ -517,6 +533,78 @@ int leyline_attention(leyline_batch_t* b, int32_t layer, const leyline_heads_t* 
         err = launch_join(a, joins, rows, captured || b->many_parts, stream);
         if (err != 0) return cuda_error((cudaError_t)err, "launching the join kernel");
     }
+    return leave(b, stream, captured);
+}
+
+int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_heads_t* q_latent,
+                              const leyline_heads_t* q_rope, const float* lse, const leyline_row_weights_t* weights,
+                              float scale, float decay, int32_t flags, void* stream_v)
+{
+    NvtxRange range("leyline_attention_weights");
+    clear_error();
+    if (!b || !weights) return bad("null argument");
+    leyline_pool* p = b->pool;
+    const Geometry& g = p->g;
+    const bool mla = g.rope_heads <= 1;
+    if (layer < 0 || layer >= g.num_layers) return bad("layer out of range");
+    if (!b->planned) return bad("the batch has no plan");
+    if (b->shape.group == 0) return bad("attention needs q_heads to be a multiple of rope_heads");
+    if ((flags & ~LEYLINE_ATTENTION_PREFIX) != 0) return bad("unknown flags");
+    if (!std::isfinite(scale)) return bad("scale must be finite");
+    if (!std::isfinite(decay) || decay < 0.f) return bad("decay must be finite and not negative");
+    if (!mla && q_latent) return bad("q_latent must be NULL for rows of several bands");
+    if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) != 0) return bad("lse must be a 4-byte aligned device pointer");
+    if (!weights->ptr || (reinterpret_cast<uintptr_t>(weights->ptr) & 3) != 0)
+        return bad("weights must be a 4-byte aligned device pointer");
+    if (weights->num_reqs < 0 || weights->rows < 0 || (weights->num_reqs > 1 && weights->req_stride < weights->rows))
+        return bad("weights: a request's stride is at least its rows");
+    cudaStream_t stream = (cudaStream_t)stream_v;
+    DeviceGuard guard(p->device);
+    if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
+    WeighArgs a{};
+    bool captured = false, host = false;
+    int rc = enter(b, stream, &captured);
+    if (rc != LEYLINE_OK) return rc;
+    if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
+    // (a replay's plan is checked on the device as well)
+    if (captured ? (b->table_reqs > weights->num_reqs || b->table_rows > weights->rows)
+                 : (b->weigh_req >= weights->num_reqs || b->weigh_rows > weights->rows))
+        return bad(captured ? "under capture weights need room for every request and row of the block table"
+                            : "weights do not hold every row of the plan's requests");
+    rc = check_heads(q_rope, p->device, "q_rope", &a.q_rope);
+    if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
+    void *lse_alias = nullptr, *weights_alias = nullptr;
+    if (rc == LEYLINE_OK) rc = resolve_access(lse, p->device, "lse", &lse_alias, &host);
+    if (rc == LEYLINE_OK) rc = resolve_access(weights->ptr, p->device, "weights", &weights_alias, &host);
+    if (rc != LEYLINE_OK) return rc;
+    // other CTAs read queries and lse while one writes weights
+    const int64_t room = room_of(b, captured);
+    const Extent to{reinterpret_cast<uintptr_t>(weights_alias), weights->num_reqs, 1, 4 * weights->req_stride, 0, 4 * weights->rows};
+    if (weights->rows > 0 &&
+        (overlap(to, extent(a.q_rope, room, b->q_heads, g.rope_dim)) ||
+         overlap(to, extent(a.q_latent, mla ? room : 0, b->q_heads, g.latent_dim)) ||
+         overlap(to, Extent{reinterpret_cast<uintptr_t>(lse_alias), 1, 1, 0, 0, 4 * room * b->q_heads})))
+        return bad("weights must not lie over the queries or lse");
+    a.kv = static_cast<const uint4*>(p->kv);
+    a.lse = static_cast<const float*>(lse_alias);
+    a.weights = static_cast<float*>(weights_alias);
+    a.req_stride = weights->req_stride;
+    a.rows = weights->rows;
+    a.num_reqs = weights->num_reqs;
+    a.scale = scale;
+    a.decay = decay;
+    a.layer = layer;
+    a.prefix = flags & LEYLINE_ATTENTION_PREFIX;
+    a.q_heads = b->q_heads;
+    a.header = reinterpret_cast<const BatchHeader*>(b->d_plan);
+    a.chunks = reinterpret_cast<const ChunkDev*>(b->d_plan + b->layout.chunks);
+    a.reqs = reinterpret_cast<const WeighReq*>(b->d_plan + b->layout.weigh);
+    a.pending = p->d_pending;
+    a.turn = p->d_theta_j;
+    a.status = p->d_status;
+    a.g = g;
+    int err = launch_weigh(a, p->sm_count, stream);
+    if (err != 0) return cuda_error((cudaError_t)err, "launching the weighing kernel");
     return leave(b, stream, captured);
 }
 

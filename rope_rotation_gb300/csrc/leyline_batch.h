@@ -33,7 +33,9 @@ struct BatchHeader {
     int32_t n_tokens;
     int32_t n_joins;
     int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
-    int32_t pad[2];
+    int32_t weigh_reqs;   // requests of the plan, one WeighReq each
+    int32_t pad;
+    int64_t weigh_work;   // their work, in rows
 };
 
 // One chunk, as attention sees it.
@@ -41,7 +43,7 @@ struct ChunkDev {
     int32_t req;
     int32_t n;       // tokens
     int32_t tok0;    // first token of the batch
-    int32_t pad;
+    int32_t next;    // the request's chunk with the next higher start, -1: none (and for a chunk without tokens)
     int64_t start;   // row of the first token
 };
 
@@ -71,6 +73,14 @@ struct AttnJoin {
     int32_t pad[2];
 };
 
+// The rows of one request that the plan's tokens give weight to.
+struct WeighReq {
+    int32_t req;
+    int32_t chunk;   // its chunk with the lowest start; the others follow by ChunkDev::next
+    int64_t end;     // rows [0, end)
+    int64_t begin;   // work of the requests before it
+};
+
 // A run of up to kPlanRun tokens of one chunk, as the plan's install kernel sees it.
 constexpr int kPlanRun = 32;
 struct PlanRun {
@@ -86,12 +96,13 @@ struct PlanRun {
 
 // Where the parts of the plan lie in the batch's device buffer (bytes).
 struct BatchLayout {
-    size_t chunks, cta_begin, joins, items, bytes;
+    size_t chunks, cta_begin, joins, weigh, items, bytes;
 };
 
 // Validated chunks of a plan and the pages they take.
 struct ChunkPlan {
     std::vector<ChunkDev> chunks;
+    std::vector<WeighReq> weigh;  // by request
     std::vector<PlanRun> runs;
     std::vector<std::pair<int32_t, int64_t>> new_len;  // (request, length) of extended requests
     int64_t tokens = 0;
@@ -214,6 +225,28 @@ struct AttnArgs {
     Geometry g;
 };
 
+struct WeighArgs {
+    const uint4* kv;
+    HeadsView q_latent, q_rope;  // q_latent.ptr nullptr for grouped rows
+    const float* lse;
+    float* weights;
+    int64_t req_stride;
+    int64_t rows;          // of a request, and requests, that the weights hold
+    int32_t num_reqs;
+    float scale;
+    float decay;
+    int32_t layer;
+    int32_t prefix;
+    int32_t q_heads;
+    const BatchHeader* header;
+    const ChunkDev* chunks;
+    const WeighReq* reqs;
+    const int32_t* pending;
+    const double* turn;
+    int32_t* status;
+    Geometry g;
+};
+
 static_assert(sizeof(AttnItem) % 16 == 0, "plans are copied in 16-byte vectors");
 
 // Widest rows attention takes (leyline_batch_create checks them).
@@ -247,6 +280,7 @@ int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, vo
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
+int launch_weigh(const WeighArgs& a, int sm_count, void* stream);
 // joins: of tiles of `rows` query rows; many_parts: some of them of more than kFewParts.
 constexpr int kFewParts = 16;
 int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream);

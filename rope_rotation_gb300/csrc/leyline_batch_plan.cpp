@@ -149,7 +149,7 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
     for (int32_t k = 0; k < n; ++k) {
         const leyline_chunk_t& c = chunks[k];
         Req& r = find(c.req);
-        out->chunks.push_back(ChunkDev{c.req, c.n, tok, 0, c.start});
+        out->chunks.push_back(ChunkDev{c.req, c.n, tok, -1, c.start});
         for (int32_t t = 0; t < c.n; t += kPlanRun) {
             r.last_run = (int64_t)out->runs.size();
             out->runs.push_back(PlanRun{c.req, std::min(kPlanRun, c.n - t), tok + t,
@@ -157,6 +157,15 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
                                         r.pop, -1});
         }
         tok += c.n;
+    }
+    before = -1;
+    for (int32_t k : order) {
+        const ChunkDev& c = out->chunks[k];
+        if (c.n == 0) continue;
+        if (before >= 0 && out->chunks[before].req == c.req) out->chunks[before].next = k;
+        else out->weigh.push_back(WeighReq{c.req, k, 0, 0});
+        out->weigh.back().end = c.start + c.n;
+        before = k;
     }
     for (const Req& r : reqs)
         if (r.last_run >= 0 && r.len != r.old_len) out->runs[r.last_run].new_len = r.len;

@@ -107,6 +107,21 @@ int mark_done(leyline_pool_t* p, cudaStream_t stream)
     return LEYLINE_OK;
 }
 
+int grow_stage(leyline_pool_t* p, size_t entries)
+{
+    if (entries <= p->d_stage_cap) return LEYLINE_OK;
+    int rc = wait_pool(p);
+    if (rc != LEYLINE_OK) return rc;
+    if (p->d_stage) cudaFree(p->d_stage);
+    p->d_stage = nullptr;
+    p->d_stage_cap = 0;
+    const size_t cap = std::max<size_t>(entries * 2, 1 << 14);
+    cudaError_t e = cudaMalloc(&p->d_stage, sizeof(int32_t) * cap);
+    if (e != cudaSuccess) return cuda_error(e, "allocating the staging buffer");
+    p->d_stage_cap = cap;
+    return LEYLINE_OK;
+}
+
 int resolve_access(const void* ptr, int device, const char* what, void** alias, bool* is_host)
 {
     char msg[256];
@@ -288,6 +303,7 @@ int leyline_pool_destroy(leyline_pool_t* p)
     if (p->d_status) cudaFree(p->d_status);
     if (p->d_queue) cudaFree(p->d_queue);
     if (p->d_stage) cudaFree(p->d_stage);
+    if (p->d_lists) cudaFree(p->d_lists);
     if (p->d_pending) cudaFree(p->d_pending);
     if (p->d_theta_j) cudaFree(p->d_theta_j);
     if (p->d_mat_slot) cudaFree(p->d_mat_slot);
@@ -442,17 +458,8 @@ int leyline_splice(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_d
 
     cudaError_t e;
     if (plan.reindex) {
-        if ((size_t)plan.total_stage > p->d_stage_cap) {
-            rc = wait_pool(p);
-            if (rc != LEYLINE_OK) return rc;
-            if (p->d_stage) cudaFree(p->d_stage);
-            p->d_stage = nullptr;
-            p->d_stage_cap = 0;
-            const size_t cap = std::max<size_t>((size_t)plan.total_stage * 2, 1 << 14);
-            e = cudaMalloc(&p->d_stage, sizeof(int32_t) * cap);
-            if (e != cudaSuccess) return cuda_error(e, "allocating the staging buffer");
-            p->d_stage_cap = cap;
-        }
+        rc = grow_stage(p, (size_t)plan.total_stage);
+        if (rc != LEYLINE_OK) return rc;
         a.stage = p->d_stage;
         a.total_prep = plan.total_prep;
         a.total_repl = plan.total_repl;

@@ -12,6 +12,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "leyline_evict.h"
 #include "leyline_internal.h"
 
 namespace leyline {
@@ -57,7 +58,8 @@ struct leyline_pool {
     int bulk_blocks_per_sm = 0;
     int reindex_blocks_per_sm = 1;
     int32_t move_kernel = 0;  // MoveKernel used by this pool
-    int32_t* d_stage = nullptr;  // re-index: staged table entries
+    int32_t* d_stage = nullptr;  // staged table entries of re-index calls, staged values of evictions
+    leyline::ListState* d_lists = nullptr;  // evictions: what the check of the lists found
     int32_t* d_pending = nullptr;  // lazy: pending turns per slot
     double* d_theta_j = nullptr;   // lazy: the readers' turn table (layout at kTurnSpan)
     size_t d_stage_cap = 0;      // entries
@@ -124,12 +126,16 @@ int refuse_capture(cudaStream_t stream, const char* what);
 int order_after_previous(leyline_pool* p, cudaStream_t stream);
 // Record the pool's last enqueued work.
 int mark_done(leyline_pool* p, cudaStream_t stream);
+// Room for `entries` values in the staging buffer (waits for the pool's work when it has to grow).
+int grow_stage(leyline_pool* p, size_t entries);
 // A splice has rewritten the plan's requests of a table: batch plans made for their old rows no longer hold.
-inline void outdate_plans(leyline_pool* p, const int32_t* table, const Plan& splice)
+inline void outdate_plans(leyline_pool* p, const int32_t* table, int32_t req)
 {
     for (PlanMark* m : p->batches)
-        if (m->table == table)
-            for (const ReqPlan& r : splice.reqs)
-                if (std::binary_search(m->reqs.begin(), m->reqs.end(), r.req)) m->stale = true;
+        if (m->table == table && std::binary_search(m->reqs.begin(), m->reqs.end(), req)) m->stale = true;
+}
+inline void outdate_plans(leyline_pool* p, const int32_t* table, const Plan& splice)
+{
+    for (const ReqPlan& r : splice.reqs) outdate_plans(p, table, r.req);
 }
 }  // namespace leyline

@@ -90,6 +90,11 @@ class Heads(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class RowWeights(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("req_stride", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("num_reqs", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _SIGNATURES = {
     "leyline_pool_create": (ctypes.c_int, [ctypes.POINTER(PoolDesc), _vp, ctypes.POINTER(_vp)]),
@@ -122,6 +127,14 @@ _SIGNATURES = {
     "leyline_rotate": (ctypes.c_int, [_vp, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _vp, ctypes.c_float, _vp]),
     "leyline_attention": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.POINTER(Heads), ctypes.POINTER(Heads),
                                          ctypes.POINTER(Heads), _vp, ctypes.c_float, ctypes.c_int32, _vp]),
+    "leyline_attention_weights": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _vp,
+                                                 ctypes.POINTER(RowWeights), ctypes.c_float, ctypes.c_float,
+                                                 ctypes.c_int32, _vp]),
+    # what is kept goes in as a plain address: the data of a KEEP_DTYPE array
+    "leyline_select_rows": (ctypes.c_int, [_vp, ctypes.POINTER(BlockTable), ctypes.POINTER(RowWeights), _vp,
+                                           ctypes.c_int32, _vp, ctypes.c_int64, _vp]),
+    "leyline_evict": (ctypes.c_int, [_vp, ctypes.POINTER(BlockTable), _vp, ctypes.c_int32, _vp, ctypes.c_int64,
+                                     ctypes.POINTER(RowWeights), _vp]),
     "leyline_sync_status": (ctypes.c_int, [_vp]),
     "leyline_kernel_timing_enable": (ctypes.c_int, [_vp, ctypes.c_int32]),
     "leyline_kernel_timing_read": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_double),
@@ -507,6 +520,84 @@ def leyline_attention(batch, layer: int, q_latent: Optional[Heads], q_rope: Head
     _check(load().leyline_attention(batch, layer, None if q_latent is None else ctypes.byref(q_latent),
                                     ctypes.byref(q_rope), ctypes.byref(out),
                                     None if lse is None else lse.data_ptr(), scale, flags, _stream_ptr(stream)))
+
+
+# -------------------------------------------------------------- eviction ----
+
+# leyline_keep_t as a numpy record: a structured array of it is a C array of entries.
+KEEP_DTYPE = np.dtype([("req", "<i4"), ("n_keep", "<i4"), ("first", "<i4"), ("last", "<i4")], align=True)
+
+
+def keep_batch(keeps) -> np.ndarray:
+    """keeps: (req, n_keep) or (req, n_keep, first, last) of each request (first, last: 0), or a KEEP_DTYPE
+    array, which is taken as it is."""
+    if isinstance(keeps, np.ndarray) and keeps.dtype == KEEP_DTYPE:
+        if keeps.ndim != 1 or not keeps.flags.c_contiguous:
+            raise ValueError("arrays of what is kept must be 1-D and contiguous")
+        return keeps
+    keeps = [tuple(k) for k in keeps]
+    if any(len(k) not in (2, 4) for k in keeps):
+        raise ValueError("an entry is (req, n_keep) or (req, n_keep, first, last)")
+    return np.array([k if len(k) == 4 else (*k, 0, 0) for k in keeps], dtype=KEEP_DTYPE)
+
+
+def row_weights(t, what: str = "weights") -> RowWeights:
+    """A view of an fp32 tensor [requests][rows] whose last axis is contiguous."""
+    import torch
+    if t.requires_grad:
+        _refuse_gradient(what)
+    if t.dtype != torch.float32:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected torch.float32")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected [requests][rows] with a contiguous last axis")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if stride < t.shape[1]:
+        raise ValueError(f"{what}: its requests' rows overlap")
+    return RowWeights(t.data_ptr(), stride, t.shape[1], t.shape[0])
+
+
+def _lists(kept, keeps: np.ndarray):
+    """(address, stride) of an int32 tensor [>= entries][>= n_keep] whose last axis is contiguous."""
+    import torch
+    if kept.dtype != torch.int32:
+        raise ValueError(f"kept: dtype {kept.dtype}, expected torch.int32")
+    longest = int(keeps["n_keep"].max()) if keeps.size else 0
+    if kept.dim() != 2 or kept.shape[0] < keeps.size or kept.shape[1] < longest:
+        raise ValueError(f"kept: shape {tuple(kept.shape)}, expected [>= {keeps.size}][>= {longest}]")
+    if kept.shape[1] > 1 and kept.stride(1) != 1:
+        raise ValueError("kept: the last axis must be contiguous")
+    if kept.shape[0] > 1 and kept.stride(0) < kept.shape[1]:
+        raise ValueError("kept: its lists overlap")
+    return kept.data_ptr(), kept.stride(0) if kept.shape[0] > 1 else kept.shape[1]
+
+
+def leyline_attention_weights(batch, layer: int, q_latent: Optional[Heads], q_rope: Heads, lse, weights, scale: float,
+                              decay: float = 1.0, flags: int = 0, stream=None) -> None:
+    """q_latent (None for rows of several bands), q_rope: heads(); lse: contiguous fp32; weights: as row_weights() takes them."""
+    if lse.requires_grad:
+        _refuse_gradient("lse")
+    w = row_weights(weights)
+    _check(load().leyline_attention_weights(batch, layer, None if q_latent is None else ctypes.byref(q_latent),
+                                            ctypes.byref(q_rope), lse.data_ptr(), ctypes.byref(w), scale, decay, flags,
+                                            _stream_ptr(stream)))
+
+
+def leyline_select_rows(pool, tables: Tables, weights, keeps, kept, stream=None) -> None:
+    """keeps: as keep_batch() takes them; kept: int32 [>= entries][>= n_keep], written."""
+    a = keep_batch(keeps)
+    w = row_weights(weights)
+    ptr, stride = _lists(kept, a)
+    _check(load().leyline_select_rows(pool, ctypes.byref(tables.bt), ctypes.byref(w), a.ctypes.data, a.size, ptr, stride,
+                                      _stream_ptr(stream)))
+
+
+def leyline_evict(pool, tables: Tables, keeps, kept, weights=None, stream=None) -> None:
+    """keeps, kept: as leyline_select_rows() takes and writes them; weights: moved along."""
+    a = keep_batch(keeps)
+    w = None if weights is None else row_weights(weights)
+    ptr, stride = _lists(kept, a)
+    _check(load().leyline_evict(pool, ctypes.byref(tables.bt), a.ctypes.data, a.size, ptr, stride,
+                                None if w is None else ctypes.byref(w), _stream_ptr(stream)))
 
 
 def leyline_sync_status(pool) -> None:

@@ -19,9 +19,11 @@ from . import leyline
 
 
 class _DeviceArray:
-    """int32 device memory owned by the pool, exposed through __cuda_array_interface__."""
+    """int32 device memory owned by the pool, exposed through __cuda_array_interface__.  A tensor over it keeps it, and
+    with it the cache whose end would free the memory."""
 
-    def __init__(self, addr: int, n: int, device: int):
+    def __init__(self, addr: int, n: int, device: int, owner):
+        self.owner = owner
         self.__cuda_array_interface__ = {"shape": (n,), "typestr": "<i4", "data": (addr, False), "version": 3}
         self.device = device
 
@@ -150,6 +152,34 @@ class PagedCache:
         """materialize several distinct requests in one launch per 64 of them."""
         leyline.leyline_materialize_requests(self.pool, self.tables, reqs, stream)
 
+    def _on_device(self, t, what: str):
+        if t.device != self.kv.device:
+            raise ValueError(f"{what}: on {t.device}, the cache is on {self.kv.device}")
+        return t
+
+    def select_rows(self, weights, keeps, out=None, stream=None):
+        """The rows that requests keep, by their weights [requests][rows] (Batch.attention_weights): of each entry
+        (req, n_keep) or (req, n_keep, first, last) of `keeps` the rows at its ends and those of greatest weight, in
+        ascending order in row k of `out` (default: a new int32 tensor, -1 behind each list)."""
+        a = leyline.keep_batch(keeps)
+        if out is None:
+            with self.allocating(stream):
+                out = self.torch.full((a.size, int(a["n_keep"].max()) if a.size else 0), -1, dtype=self.torch.int32,
+                                      device=self.kv.device)
+        leyline.leyline_select_rows(self.pool, self.tables, self._on_device(weights, "weights"), a,
+                                    self._on_device(out, "out"), self._stream(stream))
+        return out
+
+    def evict(self, keeps, kept, weights=None, stream=None) -> None:
+        """Drop the rows that the lists `kept` of select_rows(), or of another policy, do not name; weights move along."""
+        if weights is not None:
+            self._on_device(weights, "weights")
+        leyline.leyline_evict(self.pool, self.tables, keeps, self._on_device(kept, "kept"), weights, self._stream(stream))
+
+    def _stream(self, stream):
+        """The stream of a call: the one given, else the current one of the cache's device."""
+        return leyline.current_stream_ptr(self.kv.device.index) if stream is None else stream
+
     def batch(self, max_chunks: int, max_tokens: int, q_heads: int) -> "Batch":
         """A batch for steps of at most max_tokens new tokens in max_chunks chunks (see Batch)."""
         b = Batch(self, max_chunks, max_tokens, q_heads)
@@ -162,7 +192,7 @@ class PagedCache:
         if not addr:
             return None
         n = self.num_pages * self.block_size
-        holder = _DeviceArray(addr, n, self.device.index or 0)
+        holder = _DeviceArray(addr, n, self.device.index or 0, self)
         return self.torch.as_tensor(holder, device=self.device).view(self.num_pages, self.block_size)
 
     def free_pages(self) -> int:
@@ -287,6 +317,25 @@ class Batch:
             self._heads(q_rope, "q_rope", tokens, self.cache.rope_dim), self._heads(out, "out", tokens, self.value_dim),
             self._device(lse, "lse"), scale, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0, self._stream(stream))
         return out, lse
+
+    def attention_weights(self, layer: int, q_latent, q_rope, lse, scale: float, weights, decay: float = 1.0,
+                          prefix: bool = False, stream=None):
+        """Add to weights [requests][rows] (fp32) what the queries gave to each row they attend to, w = decay * w + sum of
+        exp(score - lse) over tokens and heads, with the lse that attention() returned for the same arguments."""
+        torch = self.cache.torch
+        tokens = self._room(stream)
+        if (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < tokens
+                or lse.shape[1] != self.q_heads or not lse.is_contiguous()):
+            raise ValueError(f"lse: expected contiguous fp32 [>= {tokens}][{self.q_heads}]")
+        if (q_latent is None) != (self.bands > 1):
+            raise ValueError("q_latent goes with rows of one band (MLA), and only with those")
+        leyline.leyline_attention_weights(
+            self.handle, layer,
+            None if q_latent is None else self._heads(q_latent, "q_latent", tokens, self.cache.latent_dim),
+            self._heads(q_rope, "q_rope", tokens, self.cache.rope_dim), self._device(lse, "lse"),
+            self._device(weights, "weights"), scale, decay, leyline.LEYLINE_ATTENTION_PREFIX if prefix else 0,
+            self._stream(stream))
+        return weights
 
     def close(self) -> None:
         if self.handle is not None:
