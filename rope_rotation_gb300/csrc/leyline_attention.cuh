@@ -199,5 +199,19 @@ EncodeTiled encode_tiled()
     return reinterpret_cast<EncodeTiled>(f);
 }
 
+// Map of `rows` rows of row_vecs 16-byte vectors at `base`: 64 columns, 8 rows of a group, planes of 64 columns, groups;
+// boxes of box_planes planes of box_groups groups.
+bool make_map(EncodeTiled encode, CUtensorMap* map, const uint4* base, int64_t rows, int row_vecs, int planes, int box_planes,
+              int box_groups)
+{
+    const cuuint64_t row = (cuuint64_t)row_vecs * 16;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)planes, (cuuint64_t)(rows / 8)};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)box_planes, (cuuint32_t)box_groups}, steps[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint4*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace leyline

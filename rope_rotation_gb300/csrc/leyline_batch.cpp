@@ -27,6 +27,8 @@ struct leyline_batch {
     int32_t value_dim = 0;
     WorkShape shape{};
     WorkShape pair_shape{};  // ctas 0: the pool's rows are not for pairs
+    WeighShape weigh_shape{};
+    WeighMaps weigh_maps{};
     int64_t max_tiles = 0;
     BatchLayout layout{};
     TileMaps maps{};
@@ -38,6 +40,7 @@ struct leyline_batch {
     float* d_part_out = nullptr;
     float* d_part_lse = nullptr;
     int32_t* d_redo = nullptr;
+    float* d_weigh_part = nullptr;
     // pinned staging, used in turn: the host rewrites a slot once the install that read it is done
     static constexpr int kSlots = 4;
     char* h_stage[kSlots] = {};
@@ -52,6 +55,7 @@ struct leyline_batch {
     bool many_parts = false;  // it splits a tile into more than kFewParts
     int32_t weigh_req = -1;   // its highest request, and the most rows one of them has weighed
     int64_t weigh_rows = 0;
+    int32_t weigh_tiles = 0;  // its header's
     int32_t table_reqs = 0;   // of its block table
     int64_t table_rows = 0;
 };
@@ -182,6 +186,7 @@ void free_batch(leyline_batch* b)
     if (b->d_part_out) cudaFree(b->d_part_out);
     if (b->d_part_lse) cudaFree(b->d_part_lse);
     if (b->d_redo) cudaFree(b->d_redo);
+    if (b->d_weigh_part) cudaFree(b->d_weigh_part);
     delete b;
 }
 
@@ -230,6 +235,11 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     if (e == cudaSuccess) e = (cudaError_t)attention_prepare(g, p->kv, &b->maps);
     if (e == cudaSuccess && attention_takes_tiles(g))
         e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
+    b->weigh_shape = WeighShape{attention_takes_tiles(g), bands, b->shape.group,
+                                ((bands == 1 ? g.latent_dim : 0) + g.rope_dim) / 64, p->sm_count};
+    if (e == cudaSuccess && b->weigh_shape.tiles) e = (cudaError_t)weigh_tile_prepare(g, p->kv, &b->weigh_maps);
+    if (e == cudaSuccess && b->weigh_shape.tiles)
+        e = cudaMalloc(&b->d_weigh_part, sizeof(float) * kWeighKeys * 2 * kWeighItems * (size_t)p->sm_count);
     if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending) {
         b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows, kItemCostPairs};
         e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
@@ -290,11 +300,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     hd.n_tokens = (int32_t)cp.tokens;
     hd.n_joins = split.n_joins;
     hd.pairs = pairs ? 1 : 0;
-    for (WeighReq& r : cp.weigh) {
-        r.begin = hd.weigh_work;
-        hd.weigh_work += r.end;
-    }
-    hd.weigh_reqs = (int32_t)cp.weigh.size();
+    weigh_work(b->weigh_shape, cp.chunks, &cp.weigh, &hd);
     if (!cp.weigh.empty()) memcpy(h + l.weigh, cp.weigh.data(), sizeof(WeighReq) * cp.weigh.size());
     memcpy(h, &hd, sizeof hd);
     if (!cp.runs.empty()) memcpy(h + l.bytes, cp.runs.data(), sizeof(PlanRun) * cp.runs.size());
@@ -336,6 +342,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_joins = split.n_joins;
     b->pairs = pairs;
     b->weigh_req = cp.weigh.empty() ? -1 : cp.weigh.back().req;
+    b->weigh_tiles = hd.weigh_tiles;
     b->table_reqs = bt->num_reqs;
     b->table_rows = (int64_t)bt->max_blocks * p->g.block_size;
     b->weigh_rows = 0;
@@ -603,7 +610,11 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.turn = p->d_theta_j;
     a.status = p->d_status;
     a.g = g;
-    int err = launch_weigh(a, p->sm_count, stream);
+    a.part = b->d_weigh_part;
+    // (a replay's plan may cut as many query tiles as any)
+    const int joins = captured ? kWeighItems * p->sm_count : b->weigh_tiles;
+    int err = b->weigh_shape.tiles ? launch_weigh_tile(a, b->weigh_maps, p->sm_count, joins, stream)
+                                   : launch_weigh(a, p->sm_count, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the weighing kernel");
     return leave(b, stream, captured);
 }

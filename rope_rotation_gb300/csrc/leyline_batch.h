@@ -34,9 +34,17 @@ struct BatchHeader {
     int32_t n_joins;
     int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
     int32_t weigh_reqs;   // requests of the plan, one WeighReq each
+    int32_t weigh_mode;   // WeighMode
+    int64_t weigh_work;   // their work, in its mode's unit
+    int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded, at most
+    int32_t weigh_seg;    // kKeysStay: query tiles of an item
+    int32_t weigh_tiles;  // kKeysStay: tiles of cache rows whose query tiles are cut into several items
     int32_t pad;
-    int64_t weigh_work;   // their work, in rows
 };
+
+// How the weights that queries give to rows are computed: by leyline_weigh.cu, a unit of work is a row; or by
+// leyline_weigh_tile.cu, a unit is 16 rows, or an item.
+enum WeighMode : int32_t { kAnyRows = 0, kQueriesStay = 1, kKeysStay = 2 };
 
 // One chunk, as attention sees it.
 struct ChunkDev {
@@ -79,6 +87,10 @@ struct WeighReq {
     int32_t chunk;   // its chunk with the lowest start; the others follow by ChunkDev::next
     int64_t end;     // rows [0, end)
     int64_t begin;   // work of the requests before it
+    int32_t units;   // kKeysStay: query tiles of all bands
+    int32_t segs;    // items they are cut into
+    int32_t part;    // place of its first item's sums, if they are cut
+    int32_t tile;    // tiles that are cut, of the requests before it
 };
 
 // A run of up to kPlanRun tokens of one chunk, as the plan's install kernel sees it.
@@ -142,6 +154,26 @@ struct Split {
 };
 void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out);
 bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks, bool copied = false);
+
+// The work of weighing rows (leyline_weigh_tile.cu).
+constexpr int kWeighKeys = 128;  // cache rows of a tile
+constexpr int kWeighCols = 128;  // query rows of a tile
+constexpr int kWeighSmem = 13 * kWeighKeys * 128;  // bytes of a CTA's operands: chunks of 64 columns, 128 bytes a row
+constexpr int kWeighStages = 4;  // chunks that pass, at least, where queries stay
+// Tokens of a query tile.
+constexpr int32_t weigh_tokens(int32_t group) { return group >= kWeighCols ? 1 : kWeighCols / group; }
+// Items of a CTA that query tiles are cut for, and the fewest of them in an item.
+constexpr int32_t kWeighItems = 8;
+constexpr int32_t kWeighMinSeg = 8;
+struct WeighShape {
+    bool tiles;        // leyline_weigh_tile.cu takes the rows
+    int32_t bands;
+    int32_t group;     // query heads of a band
+    int32_t q_chunks;  // 64-wide chunks of a query row of a band
+    int32_t ctas;
+};
+// Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * ctas items have sums of their own.
+void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
 
 struct HeadsView {
     void* ptr;
@@ -241,6 +273,7 @@ struct WeighArgs {
     const BatchHeader* header;
     const ChunkDev* chunks;
     const WeighReq* reqs;
+    float* part;           // [items][kWeighKeys]: sums of items of cut query tiles
     const int32_t* pending;
     const double* turn;
     int32_t* status;
@@ -280,7 +313,16 @@ int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, vo
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
+// Tensor maps of a pool's rows as TileMaps has them, in boxes of one plane: the latents (whole MLA rows: and their band),
+// and the bands.
+struct WeighMaps {
+    CUtensorMap rows, bands;
+    int box, shift, whole;  // as in TileMaps
+};
 int launch_weigh(const WeighArgs& a, int sm_count, void* stream);
+int weigh_tile_prepare(const Geometry& g, const void* kv, WeighMaps* maps);
+// joins: CTAs that add up the sums of cut query tiles, 0: the plan has none.
+int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int ctas, int joins, void* stream);
 // joins: of tiles of `rows` query rows; many_parts: some of them of more than kFewParts.
 constexpr int kFewParts = 16;
 int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream);

@@ -163,7 +163,7 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
         const ChunkDev& c = out->chunks[k];
         if (c.n == 0) continue;
         if (before >= 0 && out->chunks[before].req == c.req) out->chunks[before].next = k;
-        else out->weigh.push_back(WeighReq{c.req, k, 0, 0});
+        else out->weigh.push_back(WeighReq{c.req, k, 0, 0, 0, 0, 0, 0});
         out->weigh.back().end = c.start + c.n;
         before = k;
     }
@@ -249,6 +249,58 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
     while (split_by(w, chunks, quota, out) > quota) {
         *out = empty;
         quota += std::max<int64_t>(1, quota / 64);
+    }
+}
+
+void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header)
+{
+    header->weigh_reqs = (int32_t)reqs->size();
+    header->weigh_mode = kAnyRows;
+    header->weigh_work = 0;
+    header->weigh_cols = header->weigh_seg = header->weigh_tiles = 0;
+    int64_t most = 0;   // query rows of a request and band
+    int64_t units = 0;  // query tiles, of every tile of cache rows
+    bool single = true;
+    if (w.tiles && w.group > 0) {
+        const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
+        for (WeighReq& r : *reqs) {
+            int64_t n = 0;
+            for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) {
+                n += ceil_div(chunks[c].n, tokens) * blocks;
+                most = std::max(most, (int64_t)chunks[c].n * w.group);
+            }
+            single &= n == 1;
+            r.units = (int32_t)(n * w.bands);
+            units += n * w.bands * ceil_div(r.end, kWeighKeys);
+        }
+        const int64_t cols = ceil_div(most, 16) * 16, stay = cols * 128 * w.q_chunks * w.bands;
+        header->weigh_mode = kKeysStay;
+        if (single && stay + kWeighStages * kWeighKeys * 128 <= kWeighSmem) {
+            header->weigh_mode = kQueriesStay;
+            header->weigh_cols = (int32_t)cols;
+        } else {
+            header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.ctas));
+        }
+    }
+    int32_t parts = 0;
+    for (WeighReq& r : *reqs) {
+        r.begin = header->weigh_work;
+        r.segs = 1;
+        r.part = parts;
+        r.tile = header->weigh_tiles;
+        if (header->weigh_mode == kAnyRows) {
+            header->weigh_work += r.end;
+        } else if (header->weigh_mode == kQueriesStay) {
+            header->weigh_work += ceil_div(r.end, 16);
+        } else {
+            const int64_t tiles = ceil_div(r.end, kWeighKeys);
+            r.segs = (int32_t)ceil_div(r.units, header->weigh_seg);
+            header->weigh_work += tiles * r.segs;
+            if (r.segs > 1) {
+                parts += (int32_t)(tiles * r.segs);
+                header->weigh_tiles += (int32_t)tiles;
+            }
+        }
     }
 }
 
