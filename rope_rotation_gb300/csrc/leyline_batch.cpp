@@ -55,7 +55,7 @@ struct leyline_batch {
     bool many_parts = false;  // it splits a tile into more than kFewParts
     int32_t weigh_req = -1;   // its highest request, and the most rows one of them has weighed
     int64_t weigh_rows = 0;
-    int32_t weigh_tiles = 0;  // its header's
+    int32_t weigh_tiles = 0, weigh_mode = kAnyRows;  // its header's
     int32_t table_reqs = 0;   // of its block table
     int64_t table_rows = 0;
 };
@@ -343,6 +343,7 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->pairs = pairs;
     b->weigh_req = cp.weigh.empty() ? -1 : cp.weigh.back().req;
     b->weigh_tiles = hd.weigh_tiles;
+    b->weigh_mode = hd.weigh_mode;
     b->table_reqs = bt->num_reqs;
     b->table_rows = (int64_t)bt->max_blocks * p->g.block_size;
     b->weigh_rows = 0;
@@ -613,7 +614,8 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.part = b->d_weigh_part;
     // (a replay's plan may cut as many query tiles as any)
     const int joins = captured ? kWeighItems * p->sm_count : b->weigh_tiles;
-    int err = b->weigh_shape.tiles ? launch_weigh_tile(a, b->weigh_maps, p->sm_count, joins, stream)
+    int err = b->weigh_shape.tiles ? launch_weigh_tile(a, b->weigh_maps, captured || b->weigh_mode == kKeysStay ? room : 0, p->sm_count,
+                                                       joins, stream)
                                    : launch_weigh(a, p->sm_count, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the weighing kernel");
     return leave(b, stream, captured);

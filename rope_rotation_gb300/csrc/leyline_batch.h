@@ -321,8 +321,14 @@ struct WeighMaps {
 };
 int launch_weigh(const WeighArgs& a, int sm_count, void* stream);
 int weigh_tile_prepare(const Geometry& g, const void* kv, WeighMaps* maps);
-// joins: CTAs that add up the sums of cut query tiles, 0: the plan has none.
-int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int ctas, int joins, void* stream);
+// Tensor maps of a call's queries, in boxes of a query tile of 64 columns.
+struct QueryMaps {
+    CUtensorMap latent, band;
+    int usable;
+};
+// tokens: of the queries' tensors if some may pass (kKeysStay), else 0; joins: CTAs that add up the sums of cut query
+// tiles, 0: the plan has none.
+int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int64_t tokens, int ctas, int joins, void* stream);
 // joins: of tiles of `rows` query rows; many_parts: some of them of more than kFewParts.
 constexpr int kFewParts = 16;
 int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream);

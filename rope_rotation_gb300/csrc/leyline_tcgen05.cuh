@@ -99,6 +99,15 @@ __device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int z, i
         : "memory");
 }
 
+// A box of a three-dimensional tensor map from (x, y, z) on.
+__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // ------------------------------------------------------------ pairs of CTAs --
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -285,6 +294,11 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+
+// Groups of this thread's cp.async: all but the last `n` have landed after the wait.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 

@@ -174,6 +174,7 @@ struct Loader {
     static constexpr int kTurned = kLazy ? kKeys : 1;
     const WeighArgs& a;
     const WeighMaps& maps;
+    const QueryMaps& queries_map;
     const Shape& s;
     Misc* m;
     uint32_t smem;
@@ -185,6 +186,7 @@ struct Loader {
     // rows 16 warp + lane (lanes below 16) of the tile of keys at `slot_key` of request `slot_req`: -1 where there is none
     long long slot = -1;
     int slot_key = -1, slot_req = -1;
+    int landing = 0;  // chunks of copied rows that have been asked for and not been arrived for
     int count = 0;
     bool counted = false;
     uint4 x[4][kTurned];  // bands of rows lane / 8 + 4 k
@@ -318,7 +320,8 @@ struct Loader {
             const int b = c - s.latent;
             store_turned(b < s.keys ? b : b - s.keys, b >= s.keys, dst);
             fence_async_smem();
-            mbar_arrive(bar);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(bar, 32);
             return;
         }
         const bool in_rows = c < s.latent || maps.whole;
@@ -349,7 +352,23 @@ struct Loader {
                                           : a.kv + band_off(a.g, a.layer, from) + band * a.g.head_vecs + 8 * (c - s.latent) + v;
             cp_async16(dst + row * 128 + ((v ^ (row & 7)) << 4), p, at >= 0);
         }
-        cp_async_arrive(bar);
+        cp_async_commit();
+    }
+    // Whether key_chunk() leaves chunk c to be arrived for: an arrival of every lane when its copies land took
+    // 256 arrivals a chunk, and bound the kernel.
+    __device__ __forceinline__ bool copied(int c) const { return maps.box == 0 && !(kLazy && c >= s.latent); }
+
+    // Arrive for chunks that have landed: all but the last `kLeft` asked for, of which the next one goes to stage ring.stage.
+    template <int kLeft>
+    __device__ __forceinline__ void arrive_landed()
+    {
+        if (landing <= kLeft) return;
+        cp_async_wait<kLeft>();
+        __syncwarp();
+        for (; landing > kLeft; --landing) {
+            const int stage = ring.stage >= landing ? ring.stage - landing : ring.stage - landing + s.stages;
+            if (lane == 0) mbar_arrive_n(smem_addr(&m->full[stage]), 32);
+        }
     }
 
     // Query rows tid / 8 + 32 k of a unit, below `rows`: 16 bytes of chunk c each.
@@ -385,7 +404,10 @@ struct Loader {
 
     __device__ __forceinline__ void refuse() {}
     __device__ __forceinline__ void flush(const WeighReq&, const Tile&, int) {}
-    __device__ __forceinline__ void release() {}
+    __device__ __forceinline__ void release()
+    {
+        if (ok) arrive_landed<0>();
+    }
 
     __device__ __forceinline__ void queries(const WeighReq&, Unit u)
     {
@@ -406,6 +428,11 @@ struct Loader {
         look_up(r, t);
         read_bands(band);
         for (int c = 0; c < s.chunks; ++c) key_chunk(band, c, smem + c * kChunkBytes, smem_addr(&m->stay_full[c]));
+        if (maps.box > 0) return;
+        cp_async_wait<0>();
+        __syncwarp();
+        for (int c = lane; c < s.chunks; c += 32)
+            if (copied(c)) mbar_arrive_n(smem_addr(&m->stay_full[c]), 32);
     }
 
     __device__ __forceinline__ void unit(const WeighReq& r, const Tile& t, const Unit& u)
@@ -415,8 +442,35 @@ struct Loader {
             look_up(r, t);
             read_bands(u.band);
             for (int c = 0; c < s.chunks; ++c) {
+                // (a stage is not waited for while more chunks are still to be arrived for than leave one free)
+                if (copied(c)) arrive_landed<kWeighStages - 2>();
+                else arrive_landed<0>();
                 if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return;
                 key_chunk(u.band, c, smem + s.stay_bytes + ring.stage * kChunkBytes, smem_addr(&m->full[ring.stage]));
+                if (copied(c)) ++landing;
+                ring.advance(s.stages);
+            }
+            return;
+        }
+        if (queries_map.usable) {  // a box of a chunk is as many instructions' work as its rows'
+            const uint32_t bytes = s.heads * s.tokens * 128;
+            for (int c = 0; c < s.q_chunks; ++c) {
+                // Every warp waits for every stage and arrives for it, whichever asks for the box: one that left some out could
+                // run a lap ahead or fall one behind, where the parity that it waits for means another lap.
+                if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return;
+                if (lane == 0) {
+                    const uint32_t full = smem_addr(&m->full[ring.stage]);
+                    if (c % kLoadWarps == warp) {
+                        mbar_expect_tx(full, bytes);
+                        const bool latent = c < s.latent;
+                        tma_box3(smem + s.stay_bytes + ring.stage * kChunkBytes, latent ? &queries_map.latent : &queries_map.band,
+                                 64 * (latent ? c : c - s.latent), u.band * s.group + u.head0, u.ch.tok0 + u.tok, full);
+                        mbar_arrive_n(full, 31);
+                    } else {
+                        mbar_arrive_n(full, 32);
+                    }
+                }
+                __syncwarp();
                 ring.advance(s.stages);
             }
             return;
@@ -539,7 +593,7 @@ struct Summer {
         m->neg_lse[buf][c] = neg;
         m->limit[buf][c] = limit;
         // (and the columns are there for all warps)
-        const bool masked = any_of_softmax(c < n && limit < t.key0 + t.keys);
+        const bool masked = any_of_softmax(c < u.cols && limit < t.key0 + t.keys);
         mbar_wait(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * warp < t.keys) {
@@ -560,7 +614,7 @@ struct Summer {
                                      make_float2(scale2, scale2), make_float2(l.z, l.w));
                     e0 = make_float2(exp2_approx(e0.x), exp2_approx(e0.y));
                     e1 = make_float2(exp2_approx(e1.x), exp2_approx(e1.y));
-                    if (masked) {
+                    if (masked || c0 + 16 > u.cols) {  // (columns behind the last one hold anything)
                         const int4 to = *reinterpret_cast<const int4*>(&m->limit[buf][c0 + k]);
                         if (key >= to.x) e0.x = 0.f;
                         if (key >= to.y) e0.y = 0.f;
@@ -603,7 +657,8 @@ struct Summer {
 
 template <int kKeys>
 __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_constant__ WeighArgs a,
-                                                              const __grid_constant__ WeighMaps maps)
+                                                              const __grid_constant__ WeighMaps maps,
+                                                              const __grid_constant__ QueryMaps queries_map)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     const uint32_t smem = (smem_addr(raw) + 1023) & ~1023u;
@@ -648,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{a, maps, s, m, smem, trig, w, lane, (int)threadIdx.x - 32 * kLoadWarp};
+        Loader<kKeys> role{a, maps, queries_map, s, m, smem, trig, w, lane, (int)threadIdx.x - 32 * kLoadWarp};
         walk(a, s, role);
         cp_async_wait_all();
     }
@@ -683,7 +738,7 @@ __global__ void __launch_bounds__(kWeighKeys) join_weights_kernel(const __grid_c
     }
 }
 
-using Kernel = void (*)(WeighArgs, WeighMaps);
+using Kernel = void (*)(WeighArgs, WeighMaps, QueryMaps);
 
 Kernel kernel_of(const Geometry& g)
 {
@@ -714,9 +769,31 @@ int weigh_tile_prepare(const Geometry& g, const void* kv, WeighMaps* maps)
     return (int)cudaFuncSetAttribute(kernel_of(g), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 
-int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int ctas, int joins, void* stream)
+// Map of the queries `q` of `tokens` tokens, in boxes of 64 columns, `box_heads` heads and box_tokens tokens.  False: it
+// cannot be had (axes that stand still), and the queries are copied a row at a time.
+static bool query_map(CUtensorMap* map, const HeadsView& q, int dim, int heads, int64_t tokens, int box_heads, int box_tokens)
 {
-    cudaError_t e = launch_dependent_smem(kernel_of(a.g), ctas, kThreads, kSmemBytes, (cudaStream_t)stream, a, maps);
+    static const EncodeTiled encode = encode_tiled();
+    // the stride of an axis of one entry says nothing
+    const cuuint64_t head = heads > 1 ? 2 * (cuuint64_t)q.head_stride : 2 * (cuuint64_t)dim;
+    const cuuint64_t token = tokens > 1 ? 2 * (cuuint64_t)q.token_stride : head * heads;
+    if (!encode || head == 0 || token == 0) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens}, strides[2] = {head, token};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, steps[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.ptr, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int64_t tokens, int ctas, int joins, void* stream)
+{
+    QueryMaps queries{};
+    if (tokens > 0) {
+        const Geometry& g = a.g;
+        const int group = a.q_heads / std::max(g.rope_heads, 1), heads = std::min(group, kWeighCols), toks = weigh_tokens(group);
+        queries.usable = query_map(&queries.band, a.q_rope, g.rope_dim, a.q_heads, tokens, heads, toks) &&
+                         (g.rope_heads > 1 || query_map(&queries.latent, a.q_latent, g.latent_dim, a.q_heads, tokens, heads, toks));
+    }
+    cudaError_t e = launch_dependent_smem(kernel_of(a.g), ctas, kThreads, kSmemBytes, (cudaStream_t)stream, a, maps, queries);
     if (e == cudaSuccess && joins > 0) e = launch_dependent(join_weights_kernel, joins, kWeighKeys, (cudaStream_t)stream, a);
     return (int)e;
 }
