@@ -236,10 +236,11 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
     if (e == cudaSuccess && attention_takes_tiles(g))
         e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
     b->weigh_shape = WeighShape{attention_takes_tiles(g), bands, b->shape.group,
-                                ((bands == 1 ? g.latent_dim : 0) + g.rope_dim) / 64, p->sm_count};
+                                ((bands == 1 ? g.latent_dim : 0) + g.rope_dim) / 64, p->sm_count / 2};
     if (e == cudaSuccess && b->weigh_shape.tiles) e = (cudaError_t)weigh_tile_prepare(g, p->kv, &b->weigh_maps);
+    if (e == cudaSuccess && b->weigh_shape.tiles) e = (cudaError_t)weigh_pair_prepare(g);
     if (e == cudaSuccess && b->weigh_shape.tiles)
-        e = cudaMalloc(&b->d_weigh_part, sizeof(float) * kWeighKeys * 2 * kWeighItems * (size_t)p->sm_count);
+        e = cudaMalloc(&b->d_weigh_part, sizeof(float) * kPairKeys * 2 * kWeighItems * (size_t)b->weigh_shape.pairs);
     if (e == cudaSuccess && bands == 1 && attention_takes_tiles(g) && !p->d_pending) {
         b->pair_shape = WorkShape{1, b->shape.group, p->sm_count / 2, kPairRows, kItemCostPairs};
         e = (cudaError_t)attention_pair_prepare(g, p->kv, &b->maps);
@@ -612,11 +613,13 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.status = p->d_status;
     a.g = g;
     a.part = b->d_weigh_part;
-    // (a replay's plan may cut as many query tiles as any)
-    const int joins = captured ? kWeighItems * p->sm_count : b->weigh_tiles;
-    int err = b->weigh_shape.tiles ? launch_weigh_tile(a, b->weigh_maps, captured || b->weigh_mode == kKeysStay ? room : 0, p->sm_count,
-                                                       joins, stream)
-                                   : launch_weigh(a, p->sm_count, stream);
+    // a captured call may be replayed with plans for either kernel, and with plans that cut as many query tiles as any
+    int err = 0;
+    if (!b->weigh_shape.tiles) err = launch_weigh(a, p->sm_count, stream);
+    else if (captured || b->weigh_mode == kQueriesStay) err = launch_weigh_tile(a, b->weigh_maps, p->sm_count, stream);
+    if (err == 0 && b->weigh_shape.tiles && (captured || b->weigh_mode == kKeysStay))
+        err = launch_weigh_pair(a, b->weigh_maps, room, b->weigh_shape.pairs,
+                                captured ? kWeighItems * b->weigh_shape.pairs : b->weigh_tiles, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the weighing kernel");
     return leave(b, stream, captured);
 }

@@ -37,13 +37,13 @@ struct BatchHeader {
     int32_t weigh_mode;   // WeighMode
     int64_t weigh_work;   // their work, in its mode's unit
     int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded, at most
-    int32_t weigh_seg;    // kKeysStay: query tiles of an item
+    int32_t weigh_seg;    // kKeysStay: products of an item
     int32_t weigh_tiles;  // kKeysStay: tiles of cache rows whose query tiles are cut into several items
     int32_t pad;
 };
 
-// How the weights that queries give to rows are computed: by leyline_weigh.cu, a unit of work is a row; or by
-// leyline_weigh_tile.cu, a unit is 16 rows, or an item.
+// How the weights that queries give to rows are computed, and a unit of its work: by leyline_weigh.cu a row, by
+// leyline_weigh_tile.cu 16 rows, by leyline_weigh_pair.cu an item.
 enum WeighMode : int32_t { kAnyRows = 0, kQueriesStay = 1, kKeysStay = 2 };
 
 // One chunk, as attention sees it.
@@ -87,7 +87,7 @@ struct WeighReq {
     int32_t chunk;   // its chunk with the lowest start; the others follow by ChunkDev::next
     int64_t end;     // rows [0, end)
     int64_t begin;   // work of the requests before it
-    int32_t units;   // kKeysStay: query tiles of all bands
+    int32_t units;   // kKeysStay: products of a tile of cache rows, each of two query tiles, of all bands
     int32_t segs;    // items they are cut into
     int32_t part;    // place of its first item's sums, if they are cut
     int32_t tile;    // tiles that are cut, of the requests before it
@@ -155,24 +155,25 @@ struct Split {
 void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* out);
 bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks, bool copied = false);
 
-// The work of weighing rows (leyline_weigh_tile.cu).
-constexpr int kWeighKeys = 128;  // cache rows of a tile
+// The work of weighing rows on the tensor cores.
+constexpr int kWeighKeys = 128;  // cache rows of a CTA's tile
+constexpr int kPairKeys = 2 * kWeighKeys;  // of a pair's
 constexpr int kWeighCols = 128;  // query rows of a tile
 constexpr int kWeighSmem = 13 * kWeighKeys * 128;  // bytes of a CTA's operands: chunks of 64 columns, 128 bytes a row
 constexpr int kWeighStages = 4;  // chunks that pass, at least, where queries stay
 // Tokens of a query tile.
 constexpr int32_t weigh_tokens(int32_t group) { return group >= kWeighCols ? 1 : kWeighCols / group; }
-// Items of a CTA that query tiles are cut for, and the fewest of them in an item.
+// Items of a pair that query tiles are cut for, and the fewest products of an item.
 constexpr int32_t kWeighItems = 8;
-constexpr int32_t kWeighMinSeg = 8;
+constexpr int32_t kWeighMinSeg = 4;
 struct WeighShape {
-    bool tiles;        // leyline_weigh_tile.cu takes the rows
+    bool tiles;        // the tensor cores take the rows
     int32_t bands;
     int32_t group;     // query heads of a band
     int32_t q_chunks;  // 64-wide chunks of a query row of a band
-    int32_t ctas;
+    int32_t pairs;     // of CTAs
 };
-// Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * ctas items have sums of their own.
+// Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * pairs items have sums of their own.
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
 
 struct HeadsView {
@@ -273,7 +274,7 @@ struct WeighArgs {
     const BatchHeader* header;
     const ChunkDev* chunks;
     const WeighReq* reqs;
-    float* part;           // [items][kWeighKeys]: sums of items of cut query tiles
+    float* part;           // [items][kPairKeys]: sums of items of cut query tiles
     const int32_t* pending;
     const double* turn;
     int32_t* status;
@@ -326,9 +327,10 @@ struct QueryMaps {
     CUtensorMap latent, band;
     int usable;
 };
-// tokens: of the queries' tensors if some may pass (kKeysStay), else 0; joins: CTAs that add up the sums of cut query
-// tiles, 0: the plan has none.
-int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int64_t tokens, int ctas, int joins, void* stream);
+int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int ctas, void* stream);
+int weigh_pair_prepare(const Geometry& g);
+// tokens: of the queries' tensors; joins: CTAs that add up the sums of cut query tiles, 0: the plan has none.
+int launch_weigh_pair(const WeighArgs& a, const WeighMaps& maps, int64_t tokens, int pairs, int joins, void* stream);
 // joins: of tiles of `rows` query rows; many_parts: some of them of more than kFewParts.
 constexpr int kFewParts = 16;
 int launch_join(const AttnArgs& a, int joins, int rows, bool many_parts, void* stream);

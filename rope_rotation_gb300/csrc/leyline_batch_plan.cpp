@@ -259,19 +259,21 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
     header->weigh_work = 0;
     header->weigh_cols = header->weigh_seg = header->weigh_tiles = 0;
     int64_t most = 0;   // query rows of a request and band
-    int64_t units = 0;  // query tiles, of every tile of cache rows
+    int64_t units = 0;  // products of all tiles of cache rows
     bool single = true;
     if (w.tiles && w.group > 0) {
         const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
         for (WeighReq& r : *reqs) {
             int64_t n = 0;
             for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) {
-                n += ceil_div(chunks[c].n, tokens) * blocks;
+                const int64_t tiles = ceil_div(chunks[c].n, tokens) * blocks;
+                single &= tiles == 1 && chunks[c].next < 0;
+                n += ceil_div(tiles, 2);
                 most = std::max(most, (int64_t)chunks[c].n * w.group);
             }
             single &= n == 1;
             r.units = (int32_t)(n * w.bands);
-            units += n * w.bands * ceil_div(r.end, kWeighKeys);
+            units += n * w.bands * ceil_div(r.end, kPairKeys);
         }
         const int64_t cols = ceil_div(most, 16) * 16, stay = cols * 128 * w.q_chunks * w.bands;
         header->weigh_mode = kKeysStay;
@@ -279,7 +281,7 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
             header->weigh_mode = kQueriesStay;
             header->weigh_cols = (int32_t)cols;
         } else {
-            header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.ctas));
+            header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs));
         }
     }
     int32_t parts = 0;
@@ -293,7 +295,7 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
         } else if (header->weigh_mode == kQueriesStay) {
             header->weigh_work += ceil_div(r.end, 16);
         } else {
-            const int64_t tiles = ceil_div(r.end, kWeighKeys);
+            const int64_t tiles = ceil_div(r.end, kPairKeys);
             r.segs = (int32_t)ceil_div(r.units, header->weigh_seg);
             header->weigh_work += tiles * r.segs;
             if (r.segs > 1) {

@@ -99,15 +99,6 @@ __device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int z, i
         : "memory");
 }
 
-// A box of a three-dimensional tensor map from (x, y, z) on.
-__device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
 // ------------------------------------------------------------ pairs of CTAs --
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -200,6 +191,15 @@ __device__ __forceinline__ void pair_box4(uint32_t dst, const void* map, int z, 
         "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, "
         "%3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(0), "r"(z), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_box3(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 

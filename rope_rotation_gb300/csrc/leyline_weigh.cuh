@@ -1,0 +1,418 @@
+// leyline_weigh.cuh -- what the kernels that weigh rows on the tensor cores share (leyline_weigh_tile.cu,
+// leyline_weigh_pair.cu): how a tile's keys come to shared memory, and how a product's columns are summed.
+//
+// Both operands of S^T = K Q^T lie in shared memory as chunks of 64 columns, 128 bytes a row, swizzled: 16 KB for the 128
+// cache rows of a CTA.  A cache row is a TMEM lane, so a thread of the epilogue has a row of S^T and sums its columns in
+// registers: no reduction across threads, and a masked or bad row spoils no other.
+#pragma once
+
+#include "leyline_attention.cuh"
+
+namespace leyline {
+namespace {
+
+constexpr int kChunkBytes = kWeighKeys * 128;
+constexpr int kMaxChunks = 10;  // of a key: 8 of the latent, the band and its low part
+constexpr int kMaxStages = 12;
+
+// The kind of rows.
+struct Shape {
+    int bands, group;
+    int tokens, heads, blocks;  // query tile: tokens, heads of a token; tiles of a token's heads
+    int latent, keys, low;      // chunks of a key: of the latent, of the band, of the band's low part
+    int q_chunks, chunks;
+    int stay_bytes, stages;     // shared memory of what stays; chunks that pass
+};
+
+__device__ __forceinline__ Shape make_shape(const WeighArgs& a, bool lazy)
+{
+    Shape s;
+    const bool mla = a.g.rope_heads <= 1;
+    s.bands = mla ? 1 : a.g.rope_heads;
+    s.group = a.q_heads / s.bands;
+    s.tokens = weigh_tokens(s.group);
+    s.heads = min(s.group, kWeighCols);
+    s.blocks = (s.group + kWeighCols - 1) / kWeighCols;
+    s.latent = mla ? a.g.latent_vecs / 8 : 0;
+    s.keys = a.g.head_vecs / 8;
+    s.low = lazy ? s.keys : 0;
+    s.q_chunks = s.latent + s.keys;
+    s.chunks = s.q_chunks + s.low;
+    s.stay_bytes = s.stages = 0;
+    return s;
+}
+
+struct Tile {
+    int key0, keys;  // cache rows of the request
+};
+
+__device__ __forceinline__ int padded(int cols) { return (cols + 15) & ~15; }
+
+// The request whose work holds unit x.
+__device__ __forceinline__ WeighReq find_request(const WeighArgs& a, long long x)
+{
+    int lo = 0, hi = a.header->weigh_reqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.reqs[mid].begin <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return a.reqs[lo];
+}
+
+// (A replayed plan's table may have more requests or rows than the weights.)
+__device__ __forceinline__ bool weights_hold(const WeighArgs& a, const WeighReq& r)
+{
+    return r.req < a.num_reqs && r.end <= a.rows;
+}
+
+__device__ __forceinline__ void store_weight(const WeighArgs& a, const WeighReq& r, int key, float got)
+{
+    const int page = a.header->table[(long long)r.req * a.header->max_blocks + key / a.g.block_size];
+    if (page < 0 || page >= a.g.num_pages) return;  // (the loads have raised the status)
+    float* w = a.weights + r.req * a.req_stride + key;
+    *w = a.decay == 0.f ? got : fmaf(a.decay, *w, got);
+}
+
+// --------------------------------------------------------------------- keys --
+// The warps that bring a CTA's 128 cache rows, kRows of them each: boxes of 16 or 8 rows by TMA where 8 divides the block
+// size, else a row at a time.  In a lazy pool (kKeys > 0: the chunks of a band) they turn each row's band by its pending
+// count, in fp32, into the sum of two bf16 values, as leyline_attention_tile.cu does: the scores carry it to 2^-17.
+// kPair: of two CTAs whose chunks are counted in the first, whose warps alone arrive for boxes (an arrival from the other
+// CTA is slow), for all that are expected of both.
+template <int kWarps, int kKeys, bool kPair>
+struct KeyLoader {
+    static constexpr bool kLazy = kKeys > 0;
+    static constexpr int kTurned = kLazy ? kKeys : 1;
+    static constexpr int kRows = kWeighKeys / kWarps;  // 16 or 32
+    const WeighArgs& a;
+    const WeighMaps& maps;
+    const Shape& s;
+    float2* cs;  // lazy pools: cos, sin of `count`, this warp's
+    int warp, lane;
+    uint32_t rank;
+    // of row kRows * warp + lane of the tile at `slot_key` of request `slot_req`: -1 where there is none
+    long long slot = -1;
+    int slot_key = -1, slot_req = -1;
+    int ahead_page = -1, ahead_key = -1, ahead_req = -1;  // of the tile to come
+    int count = 0;
+    bool counted = false;
+    uint4 x[kRows / 4][kTurned];  // bands of rows lane / 8 + 4 k
+    int pend[kRows / 4];
+
+    __device__ __forceinline__ int page_of_row(const WeighReq& r, int key0, int keys) const
+    {
+        const int row = kRows * warp + lane;
+        if (lane >= kRows || row >= keys) return INT32_MIN;  // no such row
+        const unsigned u = (unsigned)(key0 + row), B = (unsigned)a.g.block_size;
+        return a.header->table[(long long)r.req * a.header->max_blocks + (maps.shift >= 0 ? u >> maps.shift : u / B)];
+    }
+    __device__ __forceinline__ long long slot_at(int page, int key0) const
+    {
+        if (page < 0 || page >= a.g.num_pages) return -1;
+        const unsigned u = (unsigned)(key0 + kRows * warp + lane), B = (unsigned)a.g.block_size;
+        return (long long)page * B + (u - (maps.shift >= 0 ? u >> maps.shift << maps.shift : u / B * B));
+    }
+    __device__ __forceinline__ void look_up(const WeighReq& r, const Tile& t)
+    {
+        if (slot_key == t.key0 && slot_req == r.req) return;
+        const int page = ahead_key == t.key0 && ahead_req == r.req ? ahead_page : page_of_row(r, t.key0, t.keys);
+        slot_key = t.key0;
+        slot_req = r.req;
+        slot = slot_at(page, t.key0);
+        if (slot < 0 && page != INT32_MIN) raise_status(a.status, ST_BAD_PAGE);
+    }
+    // The pages of a tile to come are read ...
+    __device__ __forceinline__ void ask_ahead(const WeighReq& r, int key0, int keys)
+    {
+        ahead_key = key0;
+        ahead_req = r.req;
+        ahead_page = page_of_row(r, key0, keys);
+    }
+    // ... and its rows asked into L2, whole: its chunks come one after another, 128 bytes of each row.
+    __device__ __forceinline__ void prefetch_ahead() const
+    {
+        const long long at = slot_at(ahead_page, ahead_key);
+        const bool pages = maps.box == 16 && maps.whole;
+        if (at < 0 || (pages && lane % 16 != 0)) return;
+        const int rows = pages ? 16 : 1;
+        if (s.latent > 0) prefetch_l2(a.kv + lat_off(a.g, a.layer, at), (uint32_t)(rows * 16 * (maps.whole ? a.g.row_vecs : a.g.latent_vecs)));
+        if (!maps.whole) prefetch_l2(a.kv + band_off(a.g, a.layer, at), (uint32_t)(16 * a.g.rope_vecs));
+    }
+
+    // The bands to turn, in registers.
+    __device__ __forceinline__ void read_bands(int band)
+    {
+        if constexpr (kLazy) {
+#pragma unroll
+            for (int k = 0; k < kRows / 4; ++k) {
+                const long long at = __shfl_sync(0xffffffffu, slot, lane / 8 + 4 * k);
+                const uint4* from = a.kv + band_off(a.g, a.layer, max(at, 0ll)) + band * a.g.head_vecs + lane % 8;
+                pend[k] = at >= 0 ? a.pending[at] : 0;
+#pragma unroll
+                for (int c = 0; c < kTurned; ++c) x[k][c] = at >= 0 ? ld_stream(from + 8 * c) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void ensure(int c)
+    {
+        if (counted && c == count) return;
+        const bool bf16 = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
+        __syncwarp();
+        for (int j = lane; j < 32 * kTurned; j += 32) {
+            float co, si;
+            pending_trig(c, a.turn, 32 * kTurned, j, bf16, co, si);
+            cs[j] = make_float2(co, si);
+        }
+        __syncwarp();
+        count = c;
+        counted = true;
+    }
+
+    // Chunk c of the turned bands, or what its rounding to bf16 leaves of it, to the chunk at `dst`: rows
+    // lane / 8 + 4 k, k0 <= k < k0 + 4.
+    template <int k0>
+    __device__ __forceinline__ void store_turned(int c, bool low, uint32_t dst)
+    {
+        const bool naive = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
+        const bool split = a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
+        const int v = lane % 8, half = kTurned / 2;
+        const bool first = kTurned == 1 ? v < 4 : c < half;
+        uint4 mine[4], other[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            mine[k] = x[k0 + k][0];
+#pragma unroll
+            for (int d = 1; d < kTurned; ++d)
+                if (d == c) mine[k] = x[k0 + k][d];
+            if (kTurned == 1) {
+                other[k] = shfl_xor_vec(mine[k], 4);
+            } else {
+                other[k] = x[k0 + k][0];
+#pragma unroll
+                for (int d = 1; d < kTurned; ++d)
+                    if (d == (first ? c + half : c - half)) other[k] = x[k0 + k][d];
+            }
+        }
+        // mostly all rows of a warp share a count; else a pass for each
+        unsigned left = 15;
+        for (;;) {
+            const unsigned lanes = __ballot_sync(0xffffffffu, left != 0);
+            if (lanes == 0) return;
+            int next = pend[k0 + 3];
+#pragma unroll
+            for (int k = 2; k >= 0; --k)
+                if (left >> k & 1) next = pend[k0 + k];
+            const int c0 = __shfl_sync(0xffffffffu, next, __ffs(lanes) - 1);
+            if (c0 != 0) ensure(c0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t* mw = reinterpret_cast<const uint32_t*>(&mine[k]);
+                const uint32_t* ow = reinterpret_cast<const uint32_t*>(&other[k]);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float q0 = bf16_lo(mw[e]), q1 = bf16_hi(mw[e]);
+                    if (c0 != 0) {
+                        const float x0 = q0, x1 = q1;
+                        if (split) {  // x' = x c - y s of the first half, y' = y c + x s of the second
+                            const int pair = kTurned == 1 ? 8 * (v & 3) : 64 * (first ? c : c - half) + 8 * v;
+                            const float2 t0 = cs[pair + 2 * e], t1 = cs[pair + 2 * e + 1];
+                            const float y0 = bf16_lo(ow[e]) * (first ? -t0.y : t0.y), y1 = bf16_hi(ow[e]) * (first ? -t1.y : t1.y);
+                            q0 = naive ? round_bf16(x0 * t0.x) + round_bf16(y0) : fmaf(x0, t0.x, y0);
+                            q1 = naive ? round_bf16(x1 * t1.x) + round_bf16(y1) : fmaf(x1, t1.x, y1);
+                        } else {
+                            const float2 t = cs[32 * c + 4 * v + e];
+                            if (naive) turn_bf16(x0, x1, t.x, t.y, q0, q1);
+                            else turn_fp32(x0, x1, t.x, t.y, q0, q1);
+                        }
+                    }
+                    w[e] = pack_bf16x2(q0, q1);
+                    // the naive arm's result is the rounded one
+                    if (low) w[e] = naive ? 0u : pack_bf16x2(q0 - bf16_lo(w[e]), q1 - bf16_hi(w[e]));
+                }
+                const int row = kRows * warp + lane / 8 + 4 * (k0 + k);
+                if (pend[k0 + k] == c0)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((v ^ (row & 7)) << 4)),
+                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                if (pend[k0 + k] == c0) left &= ~(1u << k);
+            }
+        }
+    }
+
+    // An arrival of this warp (its lane 0) for what it has written to shared memory.
+    __device__ __forceinline__ void arrive(uint32_t bar) const
+    {
+        if (kPair) cluster_arrive_smem(cluster_addr(bar, 0));
+        else mbar_arrive(bar);
+    }
+
+    // Whether key_chunk() leaves chunk c to be arrived for when its copies have landed: an arrival of every thread for its
+    // own, 256 a chunk, bound the kernel.
+    __device__ __forceinline__ bool copied(int c) const { return maps.box == 0 && !(kLazy && c >= s.latent); }
+
+    // This warp's rows of chunk c of the tile's keys to the chunk at `dst`; an arrival on `bar`.
+    __device__ __forceinline__ void key_chunk(int band, int c, uint32_t dst, uint32_t bar)
+    {
+        if (kLazy && c >= s.latent) {
+            const int b = c - s.latent;
+            store_turned<0>(b < s.keys ? b : b - s.keys, b >= s.keys, dst);
+            if constexpr (kRows == 32) store_turned<4>(b < s.keys ? b : b - s.keys, b >= s.keys, dst);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(bar);
+            return;
+        }
+        const bool in_rows = c < s.latent || maps.whole;
+        if (maps.box > 0) {
+            // the lane of a box's first row asks for it
+            const CUtensorMap* map = in_rows ? &maps.rows : &maps.bands;
+            const int plane = in_rows ? c : band * s.keys + (c - s.latent);
+            const int base = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
+            const uint32_t to = dst + (kRows * warp + lane) * 128;
+            if (kPair) {  // (a box before the first row arrives as zeros)
+                if (lane == 0 && rank == 0) {
+                    mbar_expect_tx(bar, 2 * kRows * 128);
+                    mbar_arrive(bar);
+                }
+                if (lane < kRows && lane % maps.box == 0)
+                    pair_box4(to, map, plane, slot >= 0 ? base + (int)(slot >> 3) : -2, cluster_addr(bar, 0));
+            } else {
+                const bool mine = lane % maps.box == 0 && slot >= 0;
+                const unsigned boxes = __ballot_sync(0xffffffffu, mine);
+                if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * maps.box * 128);
+                __syncwarp();
+                if (mine) tma_box4(to, map, plane, base + (int)(slot >> 3), bar);
+            }
+            __syncwarp();
+            return;
+        }
+        const int v = lane % 8;
+#pragma unroll
+        for (int k = 0; k < kRows / 4; ++k) {
+            const int r = lane / 8 + 4 * k, row = kRows * warp + r;
+            const long long at = __shfl_sync(0xffffffffu, slot, r), from = max(at, 0ll);
+            const uint4* p = c < s.latent ? a.kv + lat_off(a.g, a.layer, from) + 8 * c + v
+                                          : a.kv + band_off(a.g, a.layer, from) + band * a.g.head_vecs + 8 * (c - s.latent) + v;
+            cp_async16(dst + row * 128 + ((v ^ (row & 7)) << 4), p, at >= 0);
+        }
+        cp_async_commit();
+    }
+};
+
+// A query tile: tokens [tok, tok + toks) of a chunk, heads [head0, head0 + heads) of a band; column c is token c / heads.
+struct Unit {
+    ChunkDev ch;
+    int band, tok, toks, head0, heads, cols;
+};
+
+// 16 bytes of query row `row` (of which this thread has the 16 bytes v of each chunk) of chunks [c0, c1) of a unit, the
+// first of them to `dst` and the next ones `pitch` bytes on; zeros behind its last row.
+__device__ __forceinline__ void copy_query_row(const WeighArgs& a, const Shape& s, const Unit& u, int row, int v, int c0, int c1,
+                                               uint32_t dst, uint32_t pitch)
+{
+    const bool on = row < u.cols;
+    const int col = on ? row : 0, tok = u.cols > 0 ? col / u.heads : 0;
+    const long long t = u.cols > 0 ? u.ch.tok0 + u.tok + tok : 0, head = u.cols > 0 ? u.band * s.group + u.head0 + (col - tok * u.heads) : 0;
+    const uint4* latent = static_cast<const uint4*>(a.q_latent.ptr) + (t * a.q_latent.token_stride + head * a.q_latent.head_stride) / 8 + v;
+    const uint4* band = static_cast<const uint4*>(a.q_rope.ptr) + (t * a.q_rope.token_stride + head * a.q_rope.head_stride) / 8 + v;
+    const uint32_t to = dst + row * 128 + ((v ^ (row & 7)) << 4);
+    for (int c = c0; c < c1; ++c)
+        cp_async16(to + (c - c0) * pitch, c < s.latent ? latent + 8 * c : band + 8 * (c - s.latent), on);
+}
+
+// ----------------------------------------------------------------- products --
+// 64 columns of S^T, rows of 128 bytes in both operands.
+template <bool kPair>
+__device__ __forceinline__ void product(uint32_t d, uint32_t keys, uint32_t queries, uint32_t desc, bool more)
+{
+    const uint64_t k = smem_matrix(keys, 16, 1024), q = smem_matrix(queries, 16, 1024);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (kPair) pair_mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);
+        else mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);
+    }
+}
+
+// ----------------------------------------------------------------- epilogue --
+// Whether x holds in one of kWarps warps, which meet here (barrier 1).
+template <int kWarps>
+__device__ __forceinline__ bool any_of_warps(bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %1, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "n"(32 * kWarps), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// What a column of a unit is given: its lse, and the rows that it attends to, those below `limit` (none without an lse).
+struct Column {
+    float lse = INFINITY;
+    int limit = 0;
+
+    __device__ __forceinline__ float neg() const { return -lse * kLog2e; }
+    __device__ __forceinline__ int rows() const { return lse == -INFINITY ? 0 : limit; }
+};
+
+__device__ __forceinline__ Column column_of(const WeighArgs& a, const Shape& s, const Unit& u, int c)
+{
+    Column x;
+    if (c >= u.cols) return x;
+    const int tok = c / u.heads;
+    x.lse = a.lse[(long long)(u.ch.tok0 + u.tok + tok) * a.q_heads + u.band * s.group + u.head0 + (c - tok * u.heads)];
+    x.limit = (int)(a.prefix ? u.ch.start : u.ch.start + u.tok + tok + 1);
+    return x;
+}
+
+// sum over `n` columns (a multiple of 16) of exp2(x * scale2 + neg), of this thread's TMEM lane from `tmem` on; where
+// `masked`, of those alone whose limit lies above `key`, and of the columns below `cols` in any case (what lies behind
+// them may be anything).
+__device__ __forceinline__ float sum_columns(uint32_t tmem, int n, int cols, float scale2, const float* neg, const int* limit,
+                                             int key, bool masked)
+{
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    for (int c1 = 0; c1 < n; c1 += 32) {
+        uint32_t v[2][16];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            if (c1 + 16 * b < n) tmem_ld16(tmem + c1 + 16 * b, v[b]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int c0 = c1 + 16 * b;
+            if (c0 >= n) break;
+            const bool some = masked || c0 + 16 > cols;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(neg + c0 + k);
+                float2 e0 = fma2(make_float2(__uint_as_float(v[b][k]), __uint_as_float(v[b][k + 1])),
+                                 make_float2(scale2, scale2), make_float2(l.x, l.y));
+                float2 e1 = fma2(make_float2(__uint_as_float(v[b][k + 2]), __uint_as_float(v[b][k + 3])),
+                                 make_float2(scale2, scale2), make_float2(l.z, l.w));
+                e0 = make_float2(exp2_approx(e0.x), exp2_approx(e0.y));
+                e1 = make_float2(exp2_approx(e1.x), exp2_approx(e1.y));
+                if (some) {
+                    const int4 end = *reinterpret_cast<const int4*>(limit + c0 + k);
+                    if (key >= end.x) e0.x = 0.f;
+                    if (key >= end.y) e0.y = 0.f;
+                    if (key >= end.z) e1.x = 0.f;
+                    if (key >= end.w) e1.y = 0.f;
+                }
+                acc[0] = add2(acc[0], e0);
+                acc[1] = add2(acc[1], e1);
+            }
+        }
+    }
+    return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+}
+
+}  // namespace
+}  // namespace leyline

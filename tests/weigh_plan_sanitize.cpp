@@ -150,9 +150,9 @@ int main(int argc, char** argv)
         }
         int64_t at = 0, parts = 0, tiles_before = 0;
         for (const WeighReq& r : reqs) {
-            const int64_t tiles = ceil_div(r.end, kWeighKeys);
-            int64_t units = 0;
-            for (int32_t c = r.chunk; c >= 0; c = plan.chunks[c].next) units += ceil_div(plan.chunks[c].n, tokens) * blocks;
+            const int64_t tiles = ceil_div(r.end, kPairKeys);
+            int64_t units = 0;  // products of two query tiles
+            for (int32_t c = r.chunk; c >= 0; c = plan.chunks[c].next) units += ceil_div(ceil_div(plan.chunks[c].n, tokens) * blocks, 2);
             check(r.units == units * w.bands && r.begin == at, "units");
             check((int64_t)r.segs * h.weigh_seg >= r.units && (int64_t)(r.segs - 1) * h.weigh_seg < r.units, "segments cover them");
             at += tiles * r.segs;
@@ -173,7 +173,7 @@ int main(int argc, char** argv)
             for (int64_t i : {r.begin, r.begin + tiles * r.segs - 1}) check(&find(reqs, i) == &r, "an item's request is found");
         }
         check(at == h.weigh_work && tiles_before == h.weigh_tiles, "all of it");
-        check(parts <= 2 * (int64_t)kWeighItems * w.ctas, "sums fit their buffer");
+        check(parts <= 2 * (int64_t)kWeighItems * w.pairs, "sums fit their buffer");
     }
     std::printf("%ld plans by rows, %ld with queries that stay, %ld with keys that stay, %d failed checks\n", modes[0], modes[1],
                 modes[2], failures);
