@@ -63,7 +63,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         cmd = [cc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cu"):
             cmd += ["-Xptxas", "-v"] if verbose else []
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        for _ in range(6):  # the device compiler (CUDA 13.0, Arm hosts) crashes now and then on sound code
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode == 0 or "Segmentation fault" not in r.stdout + r.stderr:
+                break
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):

@@ -159,8 +159,9 @@ bool pairs_are_faster(const WorkShape& w, const std::vector<ChunkDev>& chunks, b
 constexpr int kWeighKeys = 128;  // cache rows of a CTA's tile
 constexpr int kPairKeys = 2 * kWeighKeys;  // of a pair's
 constexpr int kWeighCols = 128;  // query rows of a tile
-constexpr int kWeighSmem = 13 * kWeighKeys * 128;  // bytes of a CTA's operands: chunks of 64 columns, 128 bytes a row
-constexpr int kWeighStages = 4;  // chunks that pass, at least, where queries stay
+// Bytes of a CTA's operands: chunks of 64 columns, 128 bytes a row, and (where queries stay) 8 bytes for each of their rows.
+constexpr int kWeighSmem = 13 * kWeighKeys * 128 + 6144;
+constexpr int kWeighStages = 4;
 // Tokens of a query tile.
 constexpr int32_t weigh_tokens(int32_t group) { return group >= kWeighCols ? 1 : kWeighCols / group; }
 // Items of a pair that query tiles are cut for, and the fewest products of an item.
@@ -172,8 +173,14 @@ struct WeighShape {
     int32_t group;     // query heads of a band
     int32_t q_chunks;  // 64-wide chunks of a query row of a band
     int32_t pairs;     // of CTAs
+    int32_t stages = kWeighStages;  // chunks that pass, at least, where queries stay
 };
 // Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * pairs items have sums of their own.
+// Bytes of the queries that stay, and of what their rows are given.
+constexpr int64_t stay_bytes(int64_t bands, int64_t q_chunks, int64_t rows)
+{
+    return bands * q_chunks * rows * 128 + (bands * rows * 8 + 1023) / 1024 * 1024;
+}
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
 
 struct HeadsView {

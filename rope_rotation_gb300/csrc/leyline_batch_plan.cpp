@@ -275,9 +275,9 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
             r.units = (int32_t)(n * w.bands);
             units += n * w.bands * ceil_div(r.end, kPairKeys);
         }
-        const int64_t cols = ceil_div(most, 16) * 16, stay = cols * 128 * w.q_chunks * w.bands;
+        const int64_t cols = ceil_div(most, 16) * 16, stay = stay_bytes(w.bands, w.q_chunks, cols);
         header->weigh_mode = kKeysStay;
-        if (single && stay + kWeighStages * kWeighKeys * 128 <= kWeighSmem) {
+        if (single && stay + w.stages * kWeighKeys * 128 <= kWeighSmem) {
             header->weigh_mode = kQueriesStay;
             header->weigh_cols = (int32_t)cols;
         } else {

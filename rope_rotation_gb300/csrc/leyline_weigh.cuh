@@ -74,6 +74,73 @@ __device__ __forceinline__ void store_weight(const WeighArgs& a, const WeighReq&
     *w = a.decay == 0.f ? got : fmaf(a.decay, *w, got);
 }
 
+__device__ __forceinline__ uint4 load_smem(uint32_t at)
+{
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void store_smem(uint32_t at, const uint4& x)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
+// A turned value as bf16, and what its rounding leaves (nothing in the naive arm, whose result is the rounded one).
+__device__ __forceinline__ uint32_t split_value(bool naive, float q0, float q1, uint32_t& low)
+{
+    const uint32_t high = pack_bf16x2(q0, q1);
+    low = naive ? 0u : pack_bf16x2(q0 - bf16_lo(high), q1 - bf16_hi(high));
+    return high;
+}
+// Half-split pairs: 8 first halves (or second ones) `mine` turned with their others by t[0 .. 7].
+__device__ __forceinline__ uint4 turned_half(bool naive, const uint4& mine, const uint4& other, const float2* t, bool first, uint4& low)
+{
+    const uint32_t* mw = reinterpret_cast<const uint32_t*>(&mine);
+    const uint32_t* ow = reinterpret_cast<const uint32_t*>(&other);
+    uint4 high;
+    uint32_t* hw = reinterpret_cast<uint32_t*>(&high);
+    uint32_t* lw = reinterpret_cast<uint32_t*>(&low);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // x' = x c - y s of the first half, y' = y c + x s of the second
+        const float4 u = *reinterpret_cast<const float4*>(t + 2 * e);
+        const float a0 = bf16_lo(mw[e]), a1 = bf16_hi(mw[e]);
+        const float b0 = bf16_lo(ow[e]) * (first ? -u.y : u.y), b1 = bf16_hi(ow[e]) * (first ? -u.w : u.w);
+        const float q0 = naive ? round_bf16(a0 * u.x) + round_bf16(b0) : fmaf(a0, u.x, b0);
+        const float q1 = naive ? round_bf16(a1 * u.z) + round_bf16(b1) : fmaf(a1, u.z, b1);
+        hw[e] = split_value(naive, q0, q1, lw[e]);
+    }
+    return high;
+}
+// Interleaved pairs: 4 of them by t[0 .. 3].
+__device__ __forceinline__ uint4 turned_pairs(bool naive, const uint4& mine, const float2* t, uint4& low)
+{
+    const uint32_t* mw = reinterpret_cast<const uint32_t*>(&mine);
+    uint4 high;
+    uint32_t* hw = reinterpret_cast<uint32_t*>(&high);
+    uint32_t* lw = reinterpret_cast<uint32_t*>(&low);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float q0, q1;
+        if (naive) turn_bf16(bf16_lo(mw[e]), bf16_hi(mw[e]), t[e].x, t[e].y, q0, q1);
+        else turn_fp32(bf16_lo(mw[e]), bf16_hi(mw[e]), t[e].x, t[e].y, q0, q1);
+        hw[e] = split_value(naive, q0, q1, lw[e]);
+    }
+    return high;
+}
+
+// cos and sin of count * theta_j of `pairs` pairs to shared memory, by a warp.  Out of line: it is for a count that the warp
+// has not met before, and its sines would cost the loop around it registers.
+__device__ __noinline__ void trig_of(int count, const double* turn, int pairs, bool bf16, float2* cs)
+{
+    __syncwarp();
+    for (int j = threadIdx.x & 31; j < pairs; j += 32) {
+        float c, s;
+        pending_trig(count, turn, pairs, j, bf16, c, s);
+        cs[j] = make_float2(c, s);
+    }
+    __syncwarp();
+}
+
 // --------------------------------------------------------------------- keys --
 // The warps that bring a CTA's 128 cache rows, kRows of them each: boxes of 16 or 8 rows by TMA where 8 divides the block
 // size, else a row at a time.  In a lazy pool (kKeys > 0: the chunks of a band) they turn each row's band by its pending
@@ -94,11 +161,9 @@ struct KeyLoader {
     // of row kRows * warp + lane of the tile at `slot_key` of request `slot_req`: -1 where there is none
     long long slot = -1;
     int slot_key = -1, slot_req = -1;
-    int ahead_page = -1, ahead_key = -1, ahead_req = -1;  // of the tile to come
+    int next_page = -1, next_key = -1, next_req = -1;  // pages of the tile to come
     int count = 0;
     bool counted = false;
-    uint4 x[kRows / 4][kTurned];  // bands of rows lane / 8 + 4 k
-    int pend[kRows / 4];
 
     __device__ __forceinline__ int page_of_row(const WeighReq& r, int key0, int keys) const
     {
@@ -116,130 +181,114 @@ struct KeyLoader {
     __device__ __forceinline__ void look_up(const WeighReq& r, const Tile& t)
     {
         if (slot_key == t.key0 && slot_req == r.req) return;
-        const int page = ahead_key == t.key0 && ahead_req == r.req ? ahead_page : page_of_row(r, t.key0, t.keys);
+        const int page = next_key == t.key0 && next_req == r.req ? next_page : page_of_row(r, t.key0, t.keys);
         slot_key = t.key0;
         slot_req = r.req;
         slot = slot_at(page, t.key0);
         if (slot < 0 && page != INT32_MIN) raise_status(a.status, ST_BAD_PAGE);
     }
-    // The pages of a tile to come are read ...
-    __device__ __forceinline__ void ask_ahead(const WeighReq& r, int key0, int keys)
+    // The pages of the next tile of the rows below `end` are read while this one is loaded.  (Asking for its rows in L2 as
+    // well, whole, cost more than it gave: 16 decodes of 16 heads over some 24000 rows 107 -> 115 us.)
+    __device__ __forceinline__ void look_ahead(const WeighReq& r, const Tile& t, int end)
     {
-        ahead_key = key0;
-        ahead_req = r.req;
-        ahead_page = page_of_row(r, key0, keys);
+        const int key = t.key0 + kWeighKeys;
+        if (next_key == key && next_req == r.req) return;
+        next_page = page_of_row(r, key, end - key);
+        next_key = key;
+        next_req = r.req;
     }
-    // ... and its rows asked into L2, whole: its chunks come one after another, 128 bytes of each row.
-    __device__ __forceinline__ void prefetch_ahead() const
-    {
-        const long long at = slot_at(ahead_page, ahead_key);
-        const bool pages = maps.box == 16 && maps.whole;
-        if (at < 0 || (pages && lane % 16 != 0)) return;
-        const int rows = pages ? 16 : 1;
-        if (s.latent > 0) prefetch_l2(a.kv + lat_off(a.g, a.layer, at), (uint32_t)(rows * 16 * (maps.whole ? a.g.row_vecs : a.g.latent_vecs)));
-        if (!maps.whole) prefetch_l2(a.kv + band_off(a.g, a.layer, at), (uint32_t)(16 * a.g.rope_vecs));
-    }
-
-    // The bands to turn, in registers.
-    __device__ __forceinline__ void read_bands(int band)
-    {
-        if constexpr (kLazy) {
-#pragma unroll
-            for (int k = 0; k < kRows / 4; ++k) {
-                const long long at = __shfl_sync(0xffffffffu, slot, lane / 8 + 4 * k);
-                const uint4* from = a.kv + band_off(a.g, a.layer, max(at, 0ll)) + band * a.g.head_vecs + lane % 8;
-                pend[k] = at >= 0 ? a.pending[at] : 0;
-#pragma unroll
-                for (int c = 0; c < kTurned; ++c) x[k][c] = at >= 0 ? ld_stream(from + 8 * c) : make_uint4(0, 0, 0, 0);
-            }
-        }
-    }
-
     __device__ __forceinline__ void ensure(int c)
     {
         if (counted && c == count) return;
-        const bool bf16 = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
-        __syncwarp();
-        for (int j = lane; j < 32 * kTurned; j += 32) {
-            float co, si;
-            pending_trig(c, a.turn, 32 * kTurned, j, bf16, co, si);
-            cs[j] = make_float2(co, si);
-        }
-        __syncwarp();
+        trig_of(c, a.turn, 32 * kTurned, a.g.precision == LEYLINE_ROTATE_BF16_NAIVE, cs);
         count = c;
         counted = true;
     }
 
-    // Chunk c of the turned bands, or what its rounding to bf16 leaves of it, to the chunk at `dst`: rows
-    // lane / 8 + 4 k, k0 <= k < k0 + 4.
-    template <int k0>
-    __device__ __forceinline__ void store_turned(int c, bool low, uint32_t dst)
+    // Lazy pools: this warp's rows of a band are copied as they are to the chunks at high(c), and their counts to `counts`,
+    // one for each row of the warp ...
+    template <class At>
+    __device__ __forceinline__ void copy_bands(int band, const At& high, uint32_t counts) const
+    {
+        const int v = lane % 8;
+#pragma unroll
+        for (int k = 0; k < kRows / 4; ++k) {
+            const int r = lane / 8 + 4 * k, row = kRows * warp + r;
+            const long long at = __shfl_sync(0xffffffffu, slot, r);
+            const uint4* from = a.kv + band_off(a.g, a.layer, max(at, 0ll)) + band * a.g.head_vecs + v;
+#pragma unroll
+            for (int c = 0; c < kTurned; ++c) cp_async16(high(c) + row * 128 + ((v ^ (row & 7)) << 4), from + 8 * c, at >= 0);
+        }
+        if (lane < kRows) cp_async4(counts + 4 * lane, a.pending + max(slot, 0ll), slot >= 0);
+    }
+
+    // ... and once they have landed turned there, by a pair of rows at a time, lane / 8 + 4 k and 4 (k + 1); what their rounding
+    // to bf16 leaves goes to low(c).  (Held in registers from one tile to the next the bands spilled, and the spills waited
+    // for their loads: 16 decodes of 16 heads over some 24000 rows 256 us.)
+    template <bool kSplit, class High, class Low>
+    __device__ __forceinline__ void turn_as(const High& high, const Low& low, const int* counts)
     {
         const bool naive = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
-        const bool split = a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
-        const int v = lane % 8, half = kTurned / 2;
-        const bool first = kTurned == 1 ? v < 4 : c < half;
-        uint4 mine[4], other[4];
+        const int v = lane % 8;
+        constexpr int kHalf = kTurned / 2;
+        constexpr bool kTwo = kSplit && kTurned > 1;  // chunks c and c + kHalf hold the two halves of their pairs
+#pragma unroll 1
+        for (int k = 0; k < kRows / 4; k += 2) {
+            const int r0 = lane / 8 + 4 * k;
+            const int turns[2] = {counts[r0], counts[r0 + 4]};
+#pragma unroll 1
+            for (int c = 0; c < (kTwo ? kHalf : kTurned); ++c) {
+                uint4 x[2], y[2];  // y: the other halves of the pairs
+                uint32_t in[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mine[k] = x[k0 + k][0];
+                for (int i = 0; i < 2; ++i) {
+                    const int row = kRows * warp + r0 + 4 * i;
+                    in[i] = row * 128 + ((v ^ (row & 7)) << 4);
+                    x[i] = load_smem(high(c) + in[i]);
+                    if (kTwo) y[i] = load_smem(high(c + kHalf) + in[i]);
+                    else if (kSplit) y[i] = shfl_xor_vec(x[i], 4);
+                }
+                const bool first = kTwo || v < 4;  // x holds the first half of its pairs
+                // mostly all rows of a warp share a count; else a pass for each
+                bool left[2] = {true, true};
+                for (;;) {
+                    const unsigned lanes = __ballot_sync(0xffffffffu, left[0] || left[1]);
+                    if (lanes == 0) break;
+                    const int c0 = __shfl_sync(0xffffffffu, left[0] ? turns[0] : turns[1], __ffs(lanes) - 1);
+                    if (c0 != 0) ensure(c0);
+                    const float2* t = cs + (!kSplit ? 32 * c + 4 * v : kTwo ? 64 * c + 8 * v : 8 * (v & 3));
 #pragma unroll
-            for (int d = 1; d < kTurned; ++d)
-                if (d == c) mine[k] = x[k0 + k][d];
-            if (kTurned == 1) {
-                other[k] = shfl_xor_vec(mine[k], 4);
-            } else {
-                other[k] = x[k0 + k][0];
-#pragma unroll
-                for (int d = 1; d < kTurned; ++d)
-                    if (d == (first ? c + half : c - half)) other[k] = x[k0 + k][d];
-            }
-        }
-        // mostly all rows of a warp share a count; else a pass for each
-        unsigned left = 15;
-        for (;;) {
-            const unsigned lanes = __ballot_sync(0xffffffffu, left != 0);
-            if (lanes == 0) return;
-            int next = pend[k0 + 3];
-#pragma unroll
-            for (int k = 2; k >= 0; --k)
-                if (left >> k & 1) next = pend[k0 + k];
-            const int c0 = __shfl_sync(0xffffffffu, next, __ffs(lanes) - 1);
-            if (c0 != 0) ensure(c0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t* mw = reinterpret_cast<const uint32_t*>(&mine[k]);
-                const uint32_t* ow = reinterpret_cast<const uint32_t*>(&other[k]);
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float q0 = bf16_lo(mw[e]), q1 = bf16_hi(mw[e]);
-                    if (c0 != 0) {
-                        const float x0 = q0, x1 = q1;
-                        if (split) {  // x' = x c - y s of the first half, y' = y c + x s of the second
-                            const int pair = kTurned == 1 ? 8 * (v & 3) : 64 * (first ? c : c - half) + 8 * v;
-                            const float2 t0 = cs[pair + 2 * e], t1 = cs[pair + 2 * e + 1];
-                            const float y0 = bf16_lo(ow[e]) * (first ? -t0.y : t0.y), y1 = bf16_hi(ow[e]) * (first ? -t1.y : t1.y);
-                            q0 = naive ? round_bf16(x0 * t0.x) + round_bf16(y0) : fmaf(x0, t0.x, y0);
-                            q1 = naive ? round_bf16(x1 * t1.x) + round_bf16(y1) : fmaf(x1, t1.x, y1);
+                    for (int i = 0; i < 2; ++i) {
+                        if (!left[i] || turns[i] != c0) continue;
+                        left[i] = false;
+                        uint4 l, z, m;
+                        if (c0 == 0) {
+                            store_smem(low(c) + in[i], make_uint4(0, 0, 0, 0));
+                            if (kTwo) store_smem(low(c + kHalf) + in[i], make_uint4(0, 0, 0, 0));
+                        } else if (kTwo) {
+                            const uint4 h = turned_half(naive, x[i], y[i], t, true, l);
+                            z = turned_half(naive, y[i], x[i], t, false, m);
+                            store_smem(high(c) + in[i], h);
+                            store_smem(low(c) + in[i], l);
+                            store_smem(high(c + kHalf) + in[i], z);
+                            store_smem(low(c + kHalf) + in[i], m);
                         } else {
-                            const float2 t = cs[32 * c + 4 * v + e];
-                            if (naive) turn_bf16(x0, x1, t.x, t.y, q0, q1);
-                            else turn_fp32(x0, x1, t.x, t.y, q0, q1);
+                            const uint4 h = kSplit ? turned_half(naive, x[i], y[i], t, first, l) : turned_pairs(naive, x[i], t, l);
+                            store_smem(high(c) + in[i], h);
+                            store_smem(low(c) + in[i], l);
                         }
                     }
-                    w[e] = pack_bf16x2(q0, q1);
-                    // the naive arm's result is the rounded one
-                    if (low) w[e] = naive ? 0u : pack_bf16x2(q0 - bf16_lo(w[e]), q1 - bf16_hi(w[e]));
                 }
-                const int row = kRows * warp + lane / 8 + 4 * (k0 + k);
-                if (pend[k0 + k] == c0)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((v ^ (row & 7)) << 4)),
-                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                 : "memory");
-                if (pend[k0 + k] == c0) left &= ~(1u << k);
             }
         }
+    }
+    template <class High, class Low>
+    __device__ __forceinline__ void turn_bands(const High& high, const Low& low, const int* counts)
+    {
+        if (a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT) turn_as<true>(high, low, counts);
+        else turn_as<false>(high, low, counts);
+        fence_async_smem();  // (slow: once for all)
+        __syncwarp();
     }
 
     // An arrival of this warp (its lane 0) for what it has written to shared memory.
@@ -249,22 +298,13 @@ struct KeyLoader {
         else mbar_arrive(bar);
     }
 
-    // Whether key_chunk() leaves chunk c to be arrived for when its copies have landed: an arrival of every thread for its
+    // Whether key_chunk() leaves chunks to be arrived for when their copies have landed: an arrival of every thread for its
     // own, 256 a chunk, bound the kernel.
-    __device__ __forceinline__ bool copied(int c) const { return maps.box == 0 && !(kLazy && c >= s.latent); }
+    __device__ __forceinline__ bool copied() const { return maps.box == 0; }
 
-    // This warp's rows of chunk c of the tile's keys to the chunk at `dst`; an arrival on `bar`.
+    // This warp's rows of chunk c of the tile's keys as they are stored to the chunk at `dst`; an arrival on `bar`.
     __device__ __forceinline__ void key_chunk(int band, int c, uint32_t dst, uint32_t bar)
     {
-        if (kLazy && c >= s.latent) {
-            const int b = c - s.latent;
-            store_turned<0>(b < s.keys ? b : b - s.keys, b >= s.keys, dst);
-            if constexpr (kRows == 32) store_turned<4>(b < s.keys ? b : b - s.keys, b >= s.keys, dst);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(bar);
-            return;
-        }
         const bool in_rows = c < s.latent || maps.whole;
         if (maps.box > 0) {
             // the lane of a box's first row asks for it
@@ -298,7 +338,6 @@ struct KeyLoader {
                                           : a.kv + band_off(a.g, a.layer, from) + band * a.g.head_vecs + 8 * (c - s.latent) + v;
             cp_async16(dst + row * 128 + ((v ^ (row & 7)) << 4), p, at >= 0);
         }
-        cp_async_commit();
     }
 };
 

@@ -38,6 +38,7 @@ struct Misc {
     alignas(16) float neg[2][kCols];
     alignas(16) int limit[2][kCols];
     float half[kWeighKeys];  // sums over the second query tile's columns
+    int counts[kWeighKeys];
 };
 constexpr int kSmemBytes = kWeighSmem + (int)sizeof(Misc) + kLoadWarps * 128 * (int)sizeof(float2) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -145,6 +146,7 @@ struct Loader {
     KeyLoader<kLoadWarps, kKeys, true> keys;
     Misc* m;
     uint32_t smem;
+    int* counts;  // lazy pools: pending turns of this warp's rows
     bool copies;  // queries as well
     bool ok = true;
     Ring ring;
@@ -165,15 +167,19 @@ struct Loader {
         if (!wait(smem_addr(&m->stay_empty), stay_phase ^ 1)) return;
         stay_phase ^= 1;
         keys.look_up(r, t);
-        keys.read_bands(band);
-        for (int c = 0; c < s.chunks; ++c) keys.key_chunk(band, c, smem + c * kChunkBytes, smem_addr(&m->stay_full[c]));
-        if (keys.maps.box > 0) return;
-        cp_async_wait<0>();
-        fence_async_smem();
+        const int stored = kKeys > 0 ? s.latent : s.chunks;
+        auto high = [&](int c) { return smem + (s.latent + c) * kChunkBytes; };
+        auto low = [&](int c) { return high(c + s.low); };
+        if (kKeys > 0) keys.copy_bands(band, high, smem_addr(counts));
+        for (int c = 0; c < stored; ++c) keys.key_chunk(band, c, smem + c * kChunkBytes, smem_addr(&m->stay_full[c]));
+        if (kKeys == 0 && !keys.copied()) return;
+        cp_async_wait_all();
+        __syncwarp();
+        if (kKeys > 0) keys.turn_bands(high, low, counts);
+        else fence_async_smem();
         __syncwarp();
         if (keys.lane == 0)
-            for (int c = 0; c < s.chunks; ++c)
-                if (keys.copied(c)) keys.arrive(smem_addr(&m->stay_full[c]));
+            for (int c = keys.copied() ? 0 : stored; c < s.chunks; ++c) keys.arrive(smem_addr(&m->stay_full[c]));
     }
 
     __device__ __forceinline__ void unit(const WeighReq&, const Tile&, const Unit& u0, const Unit& u1)
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{{a, maps, s, trig, w, lane, rank}, m, smem, !queries.usable};
+        Loader<kKeys> role{{a, maps, s, trig, w, lane, rank}, m, smem, m->counts + 32 * w, !queries.usable};
         walk(a, s, rank, role);
         cp_async_wait_all();
     }

@@ -25,14 +25,15 @@ struct Misc {
     unsigned long long drained;
     uint32_t tmem;
     int quit;
-    alignas(16) float neg[2][kWeighCols];
-    alignas(16) int limit[2][kWeighCols];
+    int least[kSumWarps];
+    int counts[4][kWeighKeys];  // lazy pools: pending turns of the rows whose bands are in flight
 };
 constexpr int kSmemBytes = kWeighSmem + (int)sizeof(Misc) + kLoadWarps * 128 * (int)sizeof(float2) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
-// Every role walks the CTA's work in the same order: stay(r, u): the query tile u of every band is to stay; unit(r, t, u,
-// end): a product, of rows below `end`; flush(r, t): the tile's sums are complete; release(): the queries are no longer used.
+// Every role walks the CTA's work in the same order (the loaders by a loop of their own): stay(u): the query tile u of every
+// band is to stay; unit(t, u): a product; flush(r, t): the tile's sums are complete; release(): the queries are no longer
+// used.
 template <class Role>
 __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& role)
 {
@@ -47,11 +48,11 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& r
         }
         const ChunkDev ch = a.chunks[r.chunk];
         Unit u{ch, 0, 0, ch.n, 0, s.group, ch.n * s.group};
-        role.stay(r, u);
+        role.stay(u);
         const int end = (int)min((g_end - (long long)r.begin) * 16, (long long)r.end);
         for (int key0 = (int)(g - r.begin) * 16; key0 < end; key0 += kWeighKeys) {
             const Tile t{key0, min(kWeighKeys, end - key0)};
-            for (u.band = 0; u.band < s.bands; ++u.band) role.unit(r, t, u, end);
+            for (u.band = 0; u.band < s.bands; ++u.band) role.unit(t, u);
             role.flush(r, t);
         }
         role.release();
@@ -60,16 +61,27 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& r
 }
 
 // --------------------------------------------------------------------- loads --
+// What a warp has asked for by cp.async (rows that TMA does not take, the bands that are to be turned) and has not arrived
+// for: groups of copies, the oldest first.  They are waited for when the next ones are on their way.
+constexpr int kLanding = 3;
+constexpr int kTurnAfter = 4;  // chunks of the next unit are asked for before a unit's bands are turned
+
 template <int kKeys>
 struct Loader {
+    static constexpr int kTurned = kKeys;  // chunks of a band to turn; as many hold their low parts
     KeyLoader<kLoadWarps, kKeys, false> keys;
     Misc* m;
     uint32_t smem;
     int q_rows;
     bool ok = true;
     Ring ring;
+    int uses = 0;  // of stages so far
     uint32_t stay_phase = 0;
-    int landing = 0;  // chunks of copied rows that have been asked for and not been arrived for
+    // (In registers, a byte for each group: what lies in local memory comes from L2, next to all of shared memory.)
+    int landing = 0;
+    uint32_t kinds = 0, gaps = 0;  // 8 * first stage + (1 + buffer of counts: bands, 0: rows); stages to the next group's first
+    int oldest_use = 0, newest_use = 0;
+    int bands_read = 0;
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
     {
@@ -77,59 +89,117 @@ struct Loader {
         return ok;
     }
 
-    // Arrive for chunks that have landed: all but the last `kLeft` asked for, of which the next one goes to stage ring.stage.
-    template <int kLeft>
-    __device__ __forceinline__ void arrive_landed()
+    __device__ __forceinline__ uint32_t stage_at(int stage) const { return smem + keys.s.stay_bytes + stage * kChunkBytes; }
+    __device__ __forceinline__ int stage_after(int stage, int n) const
     {
-        if (landing <= kLeft) return;
-        cp_async_wait<kLeft>();
+        stage += n;
+        return stage >= keys.s.stages ? stage - keys.s.stages : stage;
+    }
+
+    // The oldest group: wait for its copies, turn them if they are bands, and arrive.
+    __device__ __forceinline__ void arrive_oldest()
+    {
+        if (landing == 1) cp_async_wait<0>();
+        else if (landing == 2) cp_async_wait<1>();
+        else cp_async_wait<2>();
         __syncwarp();
-        for (; landing > kLeft; --landing) {
-            const int stage = ring.stage >= landing ? ring.stage - landing : ring.stage - landing + keys.s.stages;
+        const int stage = (kinds & 255) / 8, buffer = (int)(kinds & 7) - 1;
+        if (buffer < 0) {
             if (keys.lane == 0) mbar_arrive(smem_addr(&m->full[stage]));
+        } else if constexpr (kKeys > 0) {
+            keys.turn_bands([&](int c) { return stage_at(stage_after(stage, c)); },
+                            [&](int c) { return stage_at(stage_after(stage, kTurned + c)); }, m->counts[buffer] + 16 * keys.warp);
+            if (keys.lane < 2 * kTurned) mbar_arrive(smem_addr(&m->full[stage_after(stage, keys.lane)]));
         }
+        --landing;
+        kinds >>= 8;
+        oldest_use += gaps & 255;
+        gaps >>= 8;
     }
-
-    __device__ __forceinline__ void refuse() {}
-    __device__ __forceinline__ void flush(const WeighReq&, const Tile&) {}
-    __device__ __forceinline__ void release()
+    __device__ __forceinline__ void land(int use, int what)
     {
-        if (ok) arrive_landed<0>();
+        cp_async_commit();
+        if (landing == 0) oldest_use = use;
+        else gaps |= (uint32_t)(use - newest_use) << (8 * (landing - 1));
+        newest_use = use;
+        kinds |= (uint32_t)what << (8 * landing);
+        ++landing;
     }
-
-    __device__ __forceinline__ void stay(const WeighReq&, Unit u)
+    __device__ __forceinline__ bool queries(Unit u)
     {
         const Shape& s = keys.s;
-        if (!wait(smem_addr(&m->stay_empty), stay_phase ^ 1)) return;
+        if (!wait(smem_addr(&m->stay_empty), stay_phase ^ 1)) return false;
         stay_phase ^= 1;
         const uint32_t pitch = q_rows * 128;
         const int tid = 32 * keys.warp + keys.lane;
         for (u.band = 0; u.band < s.bands; ++u.band)
             for (int row = tid / 8; row < q_rows; row += 4 * kLoadWarps)
                 copy_query_row(keys.a, s, u, row, tid % 8, 0, s.q_chunks, smem + u.band * s.q_chunks * pitch, pitch);
-        cp_async_wait_all();
+        cp_async_wait_all();  // (no groups are in flight between requests)
         __syncwarp();
         if (keys.lane == 0) mbar_arrive(smem_addr(&m->stay_full));
+        return true;
     }
 
-    __device__ __forceinline__ void unit(const WeighReq& r, const Tile& t, const Unit& u, int end)
+    // The rows [key0, end) of a request, in the order in which the other roles walk them: for each tile and band the chunks
+    // as they are stored, then the chunks of the turned band and of its low part.
+    __device__ __forceinline__ bool rows(const WeighReq& r, int key0, int end)
     {
-        if (!ok) return;
         const Shape& s = keys.s;
-        keys.look_up(r, t);
-        keys.read_bands(u.band);
-        const int next = t.key0 + kWeighKeys;
-        const bool ahead = u.band + 1 == s.bands && next < end;
-        if (ahead) keys.ask_ahead(r, next, min(kWeighKeys, end - next));
-        for (int c = 0; c < s.chunks; ++c) {
-            // (a stage is not waited for while more chunks are still to be arrived for than leave one free)
-            if (keys.copied(c)) arrive_landed<kWeighStages - 2>();
-            else arrive_landed<0>();
-            if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return;
-            keys.key_chunk(u.band, c, smem + s.stay_bytes + ring.stage * kChunkBytes, smem_addr(&m->full[ring.stage]));
-            if (keys.copied(c)) ++landing;
+        const int stored = kKeys > 0 ? s.latent : s.chunks, steps = stored + 2 * kTurned;
+        int step = 0, band = 0, first = 0, first_use = 0;
+        for (;;) {
+            // groups that are arrived for: all at the end, the oldest of kLanding and those whose stages are next, and
+            // bands when some chunks of the next unit have been asked for, by when they have landed
+            while (landing > 0 && (key0 >= end || landing == kLanding || uses - oldest_use >= s.stages ||
+                                   (kKeys > 0 && step == kTurnAfter && !keys.copied())))
+                arrive_oldest();
+            if (key0 >= end) return true;
+            if (step == 0 && band == 0) {
+                const Tile t{key0, min(kWeighKeys, end - key0)};
+                keys.look_up(r, t);
+                keys.look_ahead(r, t, end);
+            }
+            if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return false;
+            if (step < stored) {
+                keys.key_chunk(band, step, stage_at(ring.stage), smem_addr(&m->full[ring.stage]));
+                if (keys.copied()) land(uses, 8 * ring.stage);
+            }
+            if constexpr (kKeys > 0) {
+                if (step == stored) {
+                    first = ring.stage;
+                    first_use = uses;
+                }
+                if (step + 1 == steps) {
+                    const int buffer = bands_read++ & 3;
+                    keys.copy_bands(band, [&](int c) { return stage_at(stage_after(first, c)); },
+                                    smem_addr(m->counts[buffer] + 16 * keys.warp));
+                    land(first_use, 8 * first + 1 + buffer);
+                }
+            }
             ring.advance(s.stages);
-            if (c == 0 && ahead) keys.prefetch_ahead();
+            ++uses;
+            if (++step < steps) continue;
+            step = 0;
+            if (++band < s.bands) continue;
+            band = 0;
+            key0 += kWeighKeys;
+        }
+    }
+
+    __device__ __forceinline__ void run()
+    {
+        const WeighArgs& a = keys.a;
+        const long long work = a.header->weigh_work, g1 = work * (blockIdx.x + 1) / gridDim.x;
+        for (long long g = work * blockIdx.x / gridDim.x; g < g1;) {
+            const WeighReq r = find_request(a, g);
+            const long long g_end = min(g1, (long long)(r.begin + (r.end + 15) / 16));
+            if (weights_hold(a, r)) {
+                const ChunkDev ch = a.chunks[r.chunk];
+                if (!queries(Unit{ch, 0, 0, ch.n, 0, keys.s.group, ch.n * keys.s.group})) return;
+                if (!rows(r, (int)(g - r.begin) * 16, (int)min((g_end - (long long)r.begin) * 16, (long long)r.end))) return;
+            }
+            g = g_end;
         }
     }
 };
@@ -153,29 +223,29 @@ struct Issuer {
     }
     __device__ __forceinline__ void refuse() {}
     __device__ __forceinline__ void flush(const WeighReq&, const Tile&) {}
-    __device__ __forceinline__ void stay(const WeighReq&, const Unit&) { wait(smem_addr(&m->stay_full), stay_phase); }
+    __device__ __forceinline__ void stay(const Unit&) { wait(smem_addr(&m->stay_full), stay_phase); }
     __device__ __forceinline__ void release()
     {
         if (ok && elect_lane()) mma_commit(smem_addr(&m->stay_empty));
         __syncwarp();
         stay_phase ^= 1;
     }
-    __device__ __forceinline__ void unit(const WeighReq&, const Tile&, const Unit& u, int)
+    __device__ __forceinline__ void unit(const Tile&, const Unit& u)
     {
         const int buf = index & 1;
         if (!wait(smem_addr(&m->s_empty[buf]), ((index >> 1) & 1) ^ 1)) return;
         ++index;
         const uint32_t d = tmem + buf * kWeighCols, desc = mma_desc(kWeighKeys, padded(u.cols), false, false);
-        for (int c = 0; c < s.chunks; ++c) {
+        for (int step = 0; step < s.chunks; ++step) {
             if (!wait(smem_addr(&m->full[ring.stage]), ring.phase)) return;
             fence_async_smem();
             tcgen05_after_sync();
             if (elect_lane()) {
-                const int qc = c < s.q_chunks ? c : c - s.low;  // a band's low part meets the same queries
+                const int qc = step < s.q_chunks ? step : step - s.low;  // a band's low part meets the same queries
                 product<false>(d, smem + s.stay_bytes + ring.stage * kChunkBytes,
-                               smem + (u.band * s.q_chunks + qc) * q_rows * 128, desc, c > 0);
+                               smem + (u.band * s.q_chunks + qc) * q_rows * 128, desc, step > 0);
                 mma_commit(smem_addr(&m->empty[ring.stage]));
-                if (c + 1 == s.chunks) mma_commit(smem_addr(&m->s_full[buf]));
+                if (step + 1 == s.chunks) mma_commit(smem_addr(&m->s_full[buf]));
             }
             __syncwarp();
             ring.advance(s.stages);
@@ -184,43 +254,53 @@ struct Issuer {
 };
 
 // ---------------------------------------------------------------------- sums --
-// The warps meet at a named barrier, so when the CTA gives up they go through their units without waiting, and write
-// nothing; the status word says that the weights are not valid.
+// What the columns of all bands are given lies in shared memory while their queries stay.  The warps meet at a named barrier
+// then, so when the CTA gives up they go through their units without waiting, and write nothing; the status word says that
+// the weights are not valid.
 struct Summer {
     const WeighArgs& a;
     const Shape& s;
     Misc* m;
     uint32_t tmem;
+    float* neg;   // [bands][q_rows]
+    int* limit;
+    int q_rows;
     int warp, lane;
     int index = 0;
-    int at_tok = -1, at_band = -1;  // the query tile whose column this thread has
-    Column col;
+    int open = 0;  // rows below it are attended to by every column
     float sum = 0.f;
 
     __device__ __forceinline__ void refuse()
     {
         if (threadIdx.x == 0) raise_status(a.status, ST_BAD_ROW);
     }
-    __device__ __forceinline__ void stay(const WeighReq&, const Unit&) {}
+    __device__ __forceinline__ void stay(Unit u)
+    {
+        const int c = threadIdx.x;
+        any_of_warps<kSumWarps>(false);  // the columns before are no longer used
+        int least = INT32_MAX;
+        for (u.band = 0; u.band < s.bands; ++u.band) {
+            const Column col = column_of(a, s, u, c);
+            if (c >= q_rows) continue;
+            neg[u.band * q_rows + c] = col.neg();
+            limit[u.band * q_rows + c] = col.rows();
+            if (c < u.cols) least = min(least, col.rows());
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (lane == 0) m->least[warp] = least;
+        any_of_warps<kSumWarps>(false);
+        open = min(min(m->least[0], m->least[1]), min(m->least[2], m->least[3]));
+    }
     __device__ __forceinline__ void release() {}
 
-    __device__ __forceinline__ void unit(const WeighReq&, const Tile& t, const Unit& u, int)
+    __device__ __forceinline__ void unit(const Tile& t, const Unit& u)
     {
-        const int buf = index & 1, c = threadIdx.x, n = padded(u.cols);
-        if (u.ch.tok0 != at_tok || u.band != at_band) {
-            col = column_of(a, s, u, c);
-            at_tok = u.ch.tok0;
-            at_band = u.band;
-        }
-        m->neg[buf][c] = col.neg();
-        m->limit[buf][c] = col.rows();
-        // (and the columns are there for all warps)
-        const bool masked = any_of_warps<kSumWarps>(c < u.cols && col.rows() < t.key0 + t.keys);
+        const int buf = index & 1;
         mbar_wait(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * warp < t.keys)
-            sum += sum_columns(tmem + buf * kWeighCols + ((uint32_t)(32 * warp) << 16), n, u.cols, a.scale * kLog2e, m->neg[buf],
-                               m->limit[buf], t.key0 + 32 * warp + lane, masked);
+            sum += sum_columns(tmem + buf * kWeighCols + ((uint32_t)(32 * warp) << 16), padded(u.cols), u.cols, a.scale * kLog2e,
+                               neg + u.band * q_rows, limit + u.band * q_rows, t.key0 + 32 * warp + lane, t.key0 + t.keys > open);
         tcgen05_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&m->s_empty[buf]));
@@ -268,10 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     const uint32_t tmem = m->tmem;
     Shape s = make_shape(a, kKeys > 0);
     const int q_rows = a.header->weigh_cols;
-    s.stay_bytes = s.bands * s.q_chunks * q_rows * 128;
+    s.stay_bytes = (int)stay_bytes(s.bands, s.q_chunks, q_rows);
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / kChunkBytes);
     if (warp < kMmaWarp) {
-        Summer role{a, s, m, tmem, warp, lane};
+        float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * q_rows), q_rows, warp, lane};
         walk(a, s, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
@@ -287,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
         Loader<kKeys> role{{a, maps, s, trig, w, lane, 0}, m, smem, q_rows};
-        walk(a, s, role);
+        role.run();
         cp_async_wait_all();
     }
     __syncthreads();
