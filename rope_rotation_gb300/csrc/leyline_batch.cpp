@@ -237,8 +237,7 @@ int create_batch(leyline_pool_t* p, int32_t max_chunks, int32_t max_tokens, int3
         e = cudaMalloc(&b->d_redo, sizeof(int32_t) * 2 * (size_t)(b->max_tiles + b->shape.ctas));
     b->weigh_shape = WeighShape{attention_takes_tiles(g), bands, b->shape.group,
                                 ((bands == 1 ? g.latent_dim : 0) + g.rope_dim) / 64, p->sm_count / 2,
-                                // (the chunks of a band that is turned and of its low part pass together)
-                                p->d_pending ? std::max(kWeighStages, 2 * g.rope_dim / 64) : kWeighStages};
+                                g.rope_dim / 64, p->d_pending != nullptr};
     if (e == cudaSuccess && b->weigh_shape.tiles) e = (cudaError_t)weigh_tile_prepare(g, p->kv, &b->weigh_maps);
     if (e == cudaSuccess && b->weigh_shape.tiles) e = (cudaError_t)weigh_pair_prepare(g);
     if (e == cudaSuccess && b->weigh_shape.tiles)

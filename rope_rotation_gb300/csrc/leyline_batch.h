@@ -39,7 +39,7 @@ struct BatchHeader {
     int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded, at most
     int32_t weigh_seg;    // kKeysStay: products of an item
     int32_t weigh_tiles;  // kKeysStay: tiles of cache rows whose query tiles are cut into several items
-    int32_t pad;
+    int32_t weigh_box;    // kQueriesStay: index of weigh_planes
 };
 
 // How the weights that queries give to rows are computed, and a unit of its work: by leyline_weigh.cu a row, by
@@ -161,19 +161,29 @@ constexpr int kPairKeys = 2 * kWeighKeys;  // of a pair's
 constexpr int kWeighCols = 128;  // query rows of a tile
 // Bytes of a CTA's operands: chunks of 64 columns, 128 bytes a row, and (where queries stay) 8 bytes for each of their rows.
 constexpr int kWeighSmem = 13 * kWeighKeys * 128 + 6144;
-constexpr int kWeighStages = 4;
 // Tokens of a query tile.
 constexpr int32_t weigh_tokens(int32_t group) { return group >= kWeighCols ? 1 : kWeighCols / group; }
 // Items of a pair that query tiles are cut for, and the fewest products of an item.
 constexpr int32_t kWeighItems = 8;
 constexpr int32_t kWeighMinSeg = 4;
+// Planes of 64 columns that pass together where queries stay (one TMA box for 16 rows): as many as leave enough stages.
+constexpr int32_t weigh_planes(int32_t box, bool mla) { return box == 2 ? (mla ? 3 : 4) : box + 1; }
+constexpr int32_t kWeighBoxes = 3;
+// A turned band passes two of its chunks at a time, each with its low part (one, if it has no more).
+constexpr int32_t turned_planes(int32_t band_chunks) { return band_chunks == 1 ? 2 : 4; }
+constexpr int32_t weigh_stage_planes(int32_t box, bool mla, bool lazy, int32_t band_chunks)
+{
+    const int32_t p = weigh_planes(box, mla), t = lazy ? turned_planes(band_chunks) : 0;
+    return p > t ? p : t;
+}
 struct WeighShape {
     bool tiles;        // the tensor cores take the rows
     int32_t bands;
     int32_t group;     // query heads of a band
     int32_t q_chunks;  // 64-wide chunks of a query row of a band
     int32_t pairs;     // of CTAs
-    int32_t stages = kWeighStages;  // chunks that pass, at least, where queries stay
+    int32_t band_chunks = 1;
+    bool lazy = false;
 };
 // Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * pairs items have sums of their own.
 // Bytes of the queries that stay, and of what their rows are given.
@@ -321,10 +331,10 @@ int launch_attention_pair(const AttnArgs& a, const TileMaps& maps, int pairs, vo
 int attention_prepare(const Geometry& g, const void* kv, TileMaps* maps);
 // `ctas` is the number of CTAs the plan's work was split over.
 int launch_attention(const AttnArgs& a, const TileMaps& maps, int ctas, void* stream);
-// Tensor maps of a pool's rows as TileMaps has them, in boxes of one plane: the latents (whole MLA rows: and their band),
-// and the bands.
+// Tensor maps of a pool's rows as TileMaps has them, in boxes of weigh_planes: the latents (whole MLA rows: and their
+// band), and the bands.
 struct WeighMaps {
-    CUtensorMap rows, bands;
+    CUtensorMap rows[kWeighBoxes], bands[kWeighBoxes];
     int box, shift, whole;  // as in TileMaps
 };
 int launch_weigh(const WeighArgs& a, int sm_count, void* stream);

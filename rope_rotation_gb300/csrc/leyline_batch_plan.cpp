@@ -257,7 +257,7 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
     header->weigh_reqs = (int32_t)reqs->size();
     header->weigh_mode = kAnyRows;
     header->weigh_work = 0;
-    header->weigh_cols = header->weigh_seg = header->weigh_tiles = 0;
+    header->weigh_cols = header->weigh_seg = header->weigh_tiles = header->weigh_box = 0;
     int64_t most = 0;   // query rows of a request and band
     int64_t units = 0;  // products of all tiles of cache rows
     bool single = true;
@@ -277,10 +277,16 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
         }
         const int64_t cols = ceil_div(most, 16) * 16, stay = stay_bytes(w.bands, w.q_chunks, cols);
         header->weigh_mode = kKeysStay;
-        if (single && stay + w.stages * kWeighKeys * 128 <= kWeighSmem) {
+        // the widest boxes that leave three stages, else two of the next
+        for (int32_t box = kWeighBoxes - 1; single && box >= 0; --box) {
+            const int64_t stage = (int64_t)weigh_stage_planes(box, w.bands == 1, w.lazy, w.band_chunks) * kWeighKeys * 128;
+            if (stay + (box == kWeighBoxes - 1 ? 3 : 2) * stage > kWeighSmem) continue;
             header->weigh_mode = kQueriesStay;
             header->weigh_cols = (int32_t)cols;
-        } else {
+            header->weigh_box = box;
+            break;
+        }
+        if (header->weigh_mode == kKeysStay) {
             header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs));
         }
     }

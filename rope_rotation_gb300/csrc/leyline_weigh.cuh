@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kChunkBytes = kWeighKeys * 128;
 constexpr int kMaxChunks = 10;  // of a key: 8 of the latent, the band and its low part
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 13;
 
 // The kind of rows.
 struct Shape {
@@ -205,88 +205,86 @@ struct KeyLoader {
         counted = true;
     }
 
-    // Lazy pools: this warp's rows of a band are copied as they are to the chunks at high(c), and their counts to `counts`,
-    // one for each row of the warp ...
-    template <class At>
-    __device__ __forceinline__ void copy_bands(int band, const At& high, uint32_t counts) const
+    // Place of 16 bytes v of this warp's row r in a plane at `plane`, whose groups of 8 rows lie `pitch` bytes apart.
+    __device__ __forceinline__ uint32_t place(uint32_t plane, int pitch, int r, int v) const
+    {
+        return plane + (kRows * warp + r) / 8 * pitch + (r & 7) * 128 + ((v ^ (r & 7)) << 4);
+    }
+
+    // Lazy pools: this warp's rows of chunks c0 and, if there are two, c1 of a band are copied as they are to planes 0 and 1
+    // at `dst`, and their counts to `counts`, one for each row of the warp ...
+    __device__ __forceinline__ void copy_bands(int band, int c0, int c1, bool two, uint32_t dst, int pitch, uint32_t counts) const
     {
         const int v = lane % 8;
 #pragma unroll
         for (int k = 0; k < kRows / 4; ++k) {
-            const int r = lane / 8 + 4 * k, row = kRows * warp + r;
+            const int r = lane / 8 + 4 * k;
             const long long at = __shfl_sync(0xffffffffu, slot, r);
             const uint4* from = a.kv + band_off(a.g, a.layer, max(at, 0ll)) + band * a.g.head_vecs + v;
-#pragma unroll
-            for (int c = 0; c < kTurned; ++c) cp_async16(high(c) + row * 128 + ((v ^ (row & 7)) << 4), from + 8 * c, at >= 0);
+            cp_async16(place(dst, pitch, r, v), from + 8 * c0, at >= 0);
+            if (two) cp_async16(place(dst + kAtomBytes, pitch, r, v), from + 8 * c1, at >= 0);
         }
         if (lane < kRows) cp_async4(counts + 4 * lane, a.pending + max(slot, 0ll), slot >= 0);
     }
 
-    // ... and once they have landed turned there, by a pair of rows at a time, lane / 8 + 4 k and 4 (k + 1); what their rounding
-    // to bf16 leaves goes to low(c).  (Held in registers from one tile to the next the bands spilled, and the spills waited
+    // ... and once they have landed turned there; what their rounding to bf16 leaves goes to the planes behind them.  Half-split
+    // pairs: chunk c0 alone holds both halves of its pairs, or c0 and c1 the first and the second ones.  By pairs of rows,
+    // whose chains run side by side.  (Held in registers from one tile to the next the bands spilled, and the spills waited
     // for their loads: 16 decodes of 16 heads over some 24000 rows 256 us.)
-    template <bool kSplit, class High, class Low>
-    __device__ __forceinline__ void turn_as(const High& high, const Low& low, const int* counts)
+    template <bool kSplit, bool kTwo>
+    __device__ __forceinline__ void turn_as(int c0, int c1, uint32_t dst, int pitch, const int* counts)
     {
         const bool naive = a.g.precision == LEYLINE_ROTATE_BF16_NAIVE;
         const int v = lane % 8;
-        constexpr int kHalf = kTurned / 2;
-        constexpr bool kTwo = kSplit && kTurned > 1;  // chunks c and c + kHalf hold the two halves of their pairs
+        const uint32_t low = dst + (kTwo ? 2 : 1) * kAtomBytes;
+        const bool first = kTwo || v < 4;  // x holds the first half of its pairs
 #pragma unroll 1
         for (int k = 0; k < kRows / 4; k += 2) {
             const int r0 = lane / 8 + 4 * k;
             const int turns[2] = {counts[r0], counts[r0 + 4]};
-#pragma unroll 1
-            for (int c = 0; c < (kTwo ? kHalf : kTurned); ++c) {
-                uint4 x[2], y[2];  // y: the other halves of the pairs
-                uint32_t in[2];
+            uint4 x[2], y[2];  // y: the other halves of the pairs, or chunk c1
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[i] = load_smem(place(dst, pitch, r0 + 4 * i, v));
+                if (kTwo) y[i] = load_smem(place(dst + kAtomBytes, pitch, r0 + 4 * i, v));
+                else if (kSplit) y[i] = shfl_xor_vec(x[i], 4);
+            }
+            // mostly all rows of a warp share a count; else a pass for each
+            bool left[2] = {true, true};
+            for (;;) {
+                const unsigned lanes = __ballot_sync(0xffffffffu, left[0] || left[1]);
+                if (lanes == 0) break;
+                const int n = __shfl_sync(0xffffffffu, left[0] ? turns[0] : turns[1], __ffs(lanes) - 1);
+                if (n != 0) ensure(n);
+                const float2* t = cs + (!kSplit ? 32 * c0 + 4 * v : kTwo ? 64 * c0 + 8 * v : 8 * (v & 3));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int row = kRows * warp + r0 + 4 * i;
-                    in[i] = row * 128 + ((v ^ (row & 7)) << 4);
-                    x[i] = load_smem(high(c) + in[i]);
-                    if (kTwo) y[i] = load_smem(high(c + kHalf) + in[i]);
-                    else if (kSplit) y[i] = shfl_xor_vec(x[i], 4);
-                }
-                const bool first = kTwo || v < 4;  // x holds the first half of its pairs
-                // mostly all rows of a warp share a count; else a pass for each
-                bool left[2] = {true, true};
-                for (;;) {
-                    const unsigned lanes = __ballot_sync(0xffffffffu, left[0] || left[1]);
-                    if (lanes == 0) break;
-                    const int c0 = __shfl_sync(0xffffffffu, left[0] ? turns[0] : turns[1], __ffs(lanes) - 1);
-                    if (c0 != 0) ensure(c0);
-                    const float2* t = cs + (!kSplit ? 32 * c + 4 * v : kTwo ? 64 * c + 8 * v : 8 * (v & 3));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!left[i] || turns[i] != c0) continue;
-                        left[i] = false;
-                        uint4 l, z, m;
-                        if (c0 == 0) {
-                            store_smem(low(c) + in[i], make_uint4(0, 0, 0, 0));
-                            if (kTwo) store_smem(low(c + kHalf) + in[i], make_uint4(0, 0, 0, 0));
-                        } else if (kTwo) {
-                            const uint4 h = turned_half(naive, x[i], y[i], t, true, l);
-                            z = turned_half(naive, y[i], x[i], t, false, m);
-                            store_smem(high(c) + in[i], h);
-                            store_smem(low(c) + in[i], l);
-                            store_smem(high(c + kHalf) + in[i], z);
-                            store_smem(low(c + kHalf) + in[i], m);
-                        } else {
-                            const uint4 h = kSplit ? turned_half(naive, x[i], y[i], t, first, l) : turned_pairs(naive, x[i], t, l);
-                            store_smem(high(c) + in[i], h);
-                            store_smem(low(c) + in[i], l);
-                        }
+                    if (!left[i] || turns[i] != n) continue;
+                    left[i] = false;
+                    const uint32_t to = place(dst, pitch, r0 + 4 * i, v), to_low = place(low, pitch, r0 + 4 * i, v);
+                    uint4 l = make_uint4(0, 0, 0, 0), m = l;
+                    if (n != 0) {
+                        store_smem(to, kSplit ? turned_half(naive, x[i], y[i], t, first, l) : turned_pairs(naive, x[i], t, l));
+                        if (kTwo)
+                            store_smem(to + kAtomBytes, kSplit ? turned_half(naive, y[i], x[i], t, false, m)
+                                                               : turned_pairs(naive, y[i], t + 32 * (c1 - c0), m));
                     }
+                    store_smem(to_low, l);
+                    if (kTwo) store_smem(to_low + kAtomBytes, m);
                 }
             }
         }
     }
-    template <class High, class Low>
-    __device__ __forceinline__ void turn_bands(const High& high, const Low& low, const int* counts)
+    __device__ __forceinline__ void turn_bands(int c0, int c1, bool two, uint32_t dst, int pitch, const int* counts)
     {
-        if (a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT) turn_as<true>(high, low, counts);
-        else turn_as<false>(high, low, counts);
+        const bool split = a.g.pair_layout == LEYLINE_PAIRS_HALF_SPLIT;
+        if constexpr (kTurned == 1) {
+            if (split) turn_as<true, false>(c0, c1, dst, pitch, counts);
+            else turn_as<false, false>(c0, c1, dst, pitch, counts);
+        } else {
+            if (split) turn_as<true, true>(c0, c1, dst, pitch, counts);
+            else turn_as<false, true>(c0, c1, dst, pitch, counts);
+        }
         fence_async_smem();  // (slow: once for all)
         __syncwarp();
     }
@@ -298,47 +296,45 @@ struct KeyLoader {
         else mbar_arrive(bar);
     }
 
-    // Whether key_chunk() leaves chunks to be arrived for when their copies have landed: an arrival of every thread for its
-    // own, 256 a chunk, bound the kernel.
-    __device__ __forceinline__ bool copied() const { return maps.box == 0; }
-
-    // This warp's rows of chunk c of the tile's keys as they are stored to the chunk at `dst`; an arrival on `bar`.
-    __device__ __forceinline__ void key_chunk(int band, int c, uint32_t dst, uint32_t bar)
+    // This warp's rows of `n` planes from plane p on of the latents (whole MLA rows: and their band), or of the bands, to `dst`,
+    // by boxes of as many planes; an arrival on `bar`.
+    __device__ __forceinline__ void box_planes(bool in_rows, int box, int p, int n, uint32_t dst, uint32_t bar)
     {
-        const bool in_rows = c < s.latent || maps.whole;
-        if (maps.box > 0) {
-            // the lane of a box's first row asks for it
-            const CUtensorMap* map = in_rows ? &maps.rows : &maps.bands;
-            const int plane = in_rows ? c : band * s.keys + (c - s.latent);
-            const int base = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
-            const uint32_t to = dst + (kRows * warp + lane) * 128;
-            if (kPair) {  // (a box before the first row arrives as zeros)
-                if (lane == 0 && rank == 0) {
-                    mbar_expect_tx(bar, 2 * kRows * 128);
-                    mbar_arrive(bar);
-                }
-                if (lane < kRows && lane % maps.box == 0)
-                    pair_box4(to, map, plane, slot >= 0 ? base + (int)(slot >> 3) : -2, cluster_addr(bar, 0));
-            } else {
-                const bool mine = lane % maps.box == 0 && slot >= 0;
-                const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-                if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * maps.box * 128);
-                __syncwarp();
-                if (mine) tma_box4(to, map, plane, base + (int)(slot >> 3), bar);
+        // the lane of a box's first row asks for it
+        const CUtensorMap* map = in_rows ? &maps.rows[box] : &maps.bands[box];
+        const int base = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
+        const uint32_t to = dst + (kRows * warp + lane) * 128 * n;
+        if (kPair) {  // (a box before the first row arrives as zeros)
+            if (lane == 0 && rank == 0) {
+                mbar_expect_tx(bar, 2 * kRows * 128 * n);
+                mbar_arrive(bar);
             }
+            if (lane < kRows && lane % maps.box == 0)
+                pair_box4(to, map, p, slot >= 0 ? base + (int)(slot >> 3) : -2, cluster_addr(bar, 0));
+        } else {
+            const bool mine = lane < kRows && lane % maps.box == 0 && slot >= 0;
+            const unsigned boxes = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * maps.box * 128 * n);
             __syncwarp();
-            return;
+            if (mine) tma_box4(to, map, p, base + (int)(slot >> 3), bar);
         }
+        __syncwarp();
+    }
+    // The same planes, those below `end` of them, a row at a time: to be arrived for when they have landed (an arrival of
+    // every thread for its own, 256 a chunk, bound the kernel).
+    __device__ __forceinline__ void copy_planes(bool in_rows, int p, int n, int end, uint32_t dst)
+    {
         const int v = lane % 8;
 #pragma unroll
         for (int k = 0; k < kRows / 4; ++k) {
-            const int r = lane / 8 + 4 * k, row = kRows * warp + r;
+            const int r = lane / 8 + 4 * k;
             const long long at = __shfl_sync(0xffffffffu, slot, r), from = max(at, 0ll);
-            const uint4* p = c < s.latent ? a.kv + lat_off(a.g, a.layer, from) + 8 * c + v
-                                          : a.kv + band_off(a.g, a.layer, from) + band * a.g.head_vecs + 8 * (c - s.latent) + v;
-            cp_async16(dst + row * 128 + ((v ^ (row & 7)) << 4), p, at >= 0);
+            const uint4* row = (in_rows ? a.kv + lat_off(a.g, a.layer, from) : a.kv + band_off(a.g, a.layer, from)) + v;
+            for (int c = p; c < min(p + n, end); ++c)
+                cp_async16(place(dst + (c - p) * kAtomBytes, n * kAtomBytes, r, v), row + 8 * c, at >= 0);
         }
     }
+    __device__ __forceinline__ bool copied() const { return maps.box == 0; }
 };
 
 // A query tile: tokens [tok, tok + toks) of a chunk, heads [head0, head0 + heads) of a band; column c is token c / heads.
@@ -363,11 +359,11 @@ __device__ __forceinline__ void copy_query_row(const WeighArgs& a, const Shape& 
 }
 
 // ----------------------------------------------------------------- products --
-// 64 columns of S^T, rows of 128 bytes in both operands.
+// 64 columns of S^T, rows of 128 bytes in both operands; the keys' groups of 8 rows lie `pitch` bytes apart.
 template <bool kPair>
-__device__ __forceinline__ void product(uint32_t d, uint32_t keys, uint32_t queries, uint32_t desc, bool more)
+__device__ __forceinline__ void product(uint32_t d, uint32_t keys, int pitch, uint32_t queries, uint32_t desc, bool more)
 {
-    const uint64_t k = smem_matrix(keys, 16, 1024), q = smem_matrix(queries, 16, 1024);
+    const uint64_t k = smem_matrix(keys, 16, pitch), q = smem_matrix(queries, 16, 1024);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (kPair) pair_mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);

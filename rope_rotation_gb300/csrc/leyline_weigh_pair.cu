@@ -167,15 +167,27 @@ struct Loader {
         if (!wait(smem_addr(&m->stay_empty), stay_phase ^ 1)) return;
         stay_phase ^= 1;
         keys.look_up(r, t);
+        // the band's chunks lie behind the latent's, in the order in which they pass in leyline_weigh_tile.cu: two of them
+        // (one, if it has no more) and their low parts, groups of 8 rows of all of these together
         const int stored = kKeys > 0 ? s.latent : s.chunks;
-        auto high = [&](int c) { return smem + (s.latent + c) * kChunkBytes; };
-        auto low = [&](int c) { return high(c + s.low); };
-        if (kKeys > 0) keys.copy_bands(band, high, smem_addr(counts));
-        for (int c = 0; c < stored; ++c) keys.key_chunk(band, c, smem + c * kChunkBytes, smem_addr(&m->stay_full[c]));
+        constexpr bool kTwo = kKeys > 1;
+        constexpr int kPlanes = turned_planes(kKeys > 0 ? kKeys : 1), kPitch = kPlanes * kAtomBytes;
+        if (kKeys > 0)
+            for (int c = 0; c < (kTwo ? kKeys / 2 : 1); ++c)
+                keys.copy_bands(band, c, c + kKeys / 2, kTwo, smem + (s.latent + c * kPlanes) * kChunkBytes, kPitch, smem_addr(counts));
+        for (int c = 0; c < stored; ++c) {
+            const bool in_rows = c < s.latent || (kKeys == 0 && keys.maps.whole);
+            const int plane = in_rows ? c : band * s.keys + c - s.latent;
+            const uint32_t dst = smem + c * kChunkBytes;
+            if (keys.copied()) keys.copy_planes(in_rows, plane, 1, plane + 1, dst);
+            else keys.box_planes(in_rows, 0, plane, 1, dst, smem_addr(&m->stay_full[c]));
+        }
         if (kKeys == 0 && !keys.copied()) return;
         cp_async_wait_all();
         __syncwarp();
-        if (kKeys > 0) keys.turn_bands(high, low, counts);
+        if (kKeys > 0)
+            for (int c = 0; c < (kTwo ? kKeys / 2 : 1); ++c)
+                keys.turn_bands(c, c + kKeys / 2, kTwo, smem + (s.latent + c * kPlanes) * kChunkBytes, kPitch, counts);
         else fence_async_smem();
         __syncwarp();
         if (keys.lane == 0)
@@ -235,7 +247,10 @@ struct Issuer {
         const uint32_t d = tmem + buf * kCols, desc = mma_desc(2 * kWeighKeys, 2 * tile_cols(u, next), false, false);
         for (int c = 0; c < s.q_chunks; ++c) {
             const bool band = s.low > 0 && c >= s.latent;
-            if (!stay_ready) {
+            // chunks of a band: c = latent + b is plane b / half of the pair of chunks b % half
+            const int b = c - s.latent, half = max(s.low / 2, 1), planes = turned_planes(s.low);
+            const uint32_t turned = smem + (s.latent + b % half * planes) * kChunkBytes + b / half * kAtomBytes;
+            if (!stay_ready) {  // (a band's chunks and low parts become ready together)
                 if (!wait(smem_addr(&m->stay_full[c]), stay_phase)) return;
                 if (band && !wait(smem_addr(&m->stay_full[c + s.low]), stay_phase)) return;
             }
@@ -244,8 +259,12 @@ struct Issuer {
             tcgen05_after_sync();
             if (elect_lane()) {
                 const uint32_t at = smem + s.stay_bytes + ring.stage * kChunkBytes;
-                product<true>(d, smem + c * kChunkBytes, at, desc, c > 0);
-                if (band) product<true>(d, smem + (c + s.low) * kChunkBytes, at, desc, true);  // its low part
+                if (band) {
+                    product<true>(d, turned, planes * kAtomBytes, at, desc, c > 0);
+                    product<true>(d, turned + planes / 2 * kAtomBytes, planes * kAtomBytes, at, desc, true);  // its low part
+                } else {
+                    product<true>(d, smem + c * kChunkBytes, kAtomBytes, at, desc, c > 0);
+                }
                 pair_commit(smem_addr(&m->empty[ring.stage]));
                 if (c + 1 == s.q_chunks) pair_commit(smem_addr(&m->s_full[buf]));
             }

@@ -5,8 +5,9 @@
 //   S^T = K Q^T  [128 cache rows x up to 128 query rows],  w_s += sum over columns of exp2(S^T * scale * log2 e - lse * log2 e)
 //
 // lse is given, so tiles need no common maximum, and a row of the cache is read once.  The queries of all bands stay in
-// shared memory while the keys pass through a ring of chunks of 64 columns, as they come from HBM: the rest of shared
-// memory, 64 KB for 128 MLA query rows and 176 KB for 16.  The CTAs take equal shares of 16 rows, one CTA an SM.
+// shared memory while the keys pass through what is left of it, as they come from HBM, some planes of 64 columns at a time:
+// an SM takes about 110 cycles for a TMA box whatever its size, so boxes of one plane of 16 rows, 72 for a tile of MLA
+// rows, bound the kernel.  The CTAs take equal shares of 16 rows, one CTA an SM.
 //
 // Roles: warps 0-3 sum, warp 4 issues the products, warps 5-12 load, 16 rows of a chunk each.
 #include "leyline_weigh.cuh"
@@ -60,26 +61,61 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& r
     }
 }
 
+// How a tile's planes pass, a step a stage: those of the latents (whole MLA rows: and their band), then those of the bands
+// of all heads, `planes` at a time; in a lazy pool the bands turned, two of a band's chunks with their low parts.
+struct Steps {
+    int planes, stage_bytes;
+    int rows, bands;       // planes of either kind
+    int row_steps, steps;  // of a tile
+    int turned;            // planes of a turned step, 0: bands are not turned
+    int keys;              // chunks of a band
+
+    // Planes of step i, and the pitch of their groups of 8 rows.
+    __device__ __forceinline__ int count(int i) const
+    {
+        if (i < row_steps) return min(planes, rows - i * planes);
+        return turned > 0 ? turned : min(planes, bands - (i - row_steps) * planes);
+    }
+    __device__ __forceinline__ int pitch(int i) const { return (i >= row_steps && turned > 0 ? turned : planes) * kAtomBytes; }
+    // Turned steps of a band, and the first of the chunks of one.
+    __device__ __forceinline__ int band_steps() const { return keys > 1 ? keys / 2 : 1; }
+};
+
+__device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps& maps, const Shape& s)
+{
+    Steps t;
+    const bool mla = a.g.rope_heads <= 1;
+    t.planes = weigh_planes(a.header->weigh_box, mla);
+    t.stage_bytes = weigh_stage_planes(a.header->weigh_box, mla, s.low > 0, s.keys) * kChunkBytes;
+    t.keys = s.keys;
+    t.turned = s.low > 0 ? turned_planes(s.keys) : 0;
+    t.rows = s.latent + (maps.whole && s.low == 0 ? s.keys : 0);
+    t.bands = maps.whole && s.low == 0 ? 0 : s.bands * s.keys;
+    t.row_steps = (t.rows + t.planes - 1) / t.planes;
+    t.steps = t.row_steps + (t.turned > 0 ? s.bands * t.band_steps() : (t.bands + t.planes - 1) / t.planes);
+    return t;
+}
+
 // --------------------------------------------------------------------- loads --
 // What a warp has asked for by cp.async (rows that TMA does not take, the bands that are to be turned) and has not arrived
 // for: groups of copies, the oldest first.  They are waited for when the next ones are on their way.
 constexpr int kLanding = 3;
-constexpr int kTurnAfter = 4;  // chunks of the next unit are asked for before a unit's bands are turned
+constexpr int kTurnAfter = 2;  // steps of the next tile are asked for before a tile's bands are turned
 
 template <int kKeys>
 struct Loader {
-    static constexpr int kTurned = kKeys;  // chunks of a band to turn; as many hold their low parts
     KeyLoader<kLoadWarps, kKeys, false> keys;
+    const Steps& t;
     Misc* m;
     uint32_t smem;
-    int q_rows;
+    int q_rows, box;
     bool ok = true;
     Ring ring;
     int uses = 0;  // of stages so far
     uint32_t stay_phase = 0;
     // (In registers, a byte for each group: what lies in local memory comes from L2, next to all of shared memory.)
     int landing = 0;
-    uint32_t kinds = 0, gaps = 0;  // 8 * first stage + (1 + buffer of counts: bands, 0: rows); stages to the next group's first
+    uint32_t kinds = 0, gaps = 0;  // 16 * stage + (1 + 4 * first chunk + buffer of counts: bands, 0: rows); uses to the next one
     int oldest_use = 0, newest_use = 0;
     int bands_read = 0;
 
@@ -89,12 +125,7 @@ struct Loader {
         return ok;
     }
 
-    __device__ __forceinline__ uint32_t stage_at(int stage) const { return smem + keys.s.stay_bytes + stage * kChunkBytes; }
-    __device__ __forceinline__ int stage_after(int stage, int n) const
-    {
-        stage += n;
-        return stage >= keys.s.stages ? stage - keys.s.stages : stage;
-    }
+    __device__ __forceinline__ uint32_t stage_at(int stage) const { return smem + keys.s.stay_bytes + stage * t.stage_bytes; }
 
     // The oldest group: wait for its copies, turn them if they are bands, and arrive.
     __device__ __forceinline__ void arrive_oldest()
@@ -103,14 +134,14 @@ struct Loader {
         else if (landing == 2) cp_async_wait<1>();
         else cp_async_wait<2>();
         __syncwarp();
-        const int stage = (kinds & 255) / 8, buffer = (int)(kinds & 7) - 1;
-        if (buffer < 0) {
-            if (keys.lane == 0) mbar_arrive(smem_addr(&m->full[stage]));
-        } else if constexpr (kKeys > 0) {
-            keys.turn_bands([&](int c) { return stage_at(stage_after(stage, c)); },
-                            [&](int c) { return stage_at(stage_after(stage, kTurned + c)); }, m->counts[buffer] + 16 * keys.warp);
-            if (keys.lane < 2 * kTurned) mbar_arrive(smem_addr(&m->full[stage_after(stage, keys.lane)]));
+        const int stage = (kinds & 255) / 16, what = (int)(kinds & 15) - 1;
+        if constexpr (kKeys > 0) {
+            const int c = what / 4;
+            if (what >= 0)
+                keys.turn_bands(c, c + kKeys / 2, kKeys > 1, stage_at(stage), t.turned * kAtomBytes,
+                                m->counts[what % 4] + 16 * keys.warp);
         }
+        if (keys.lane == 0) mbar_arrive(smem_addr(&m->full[stage]));
         --landing;
         kinds >>= 8;
         oldest_use += gaps & 255;
@@ -141,48 +172,44 @@ struct Loader {
         return true;
     }
 
-    // The rows [key0, end) of a request, in the order in which the other roles walk them: for each tile and band the chunks
-    // as they are stored, then the chunks of the turned band and of its low part.
+    // The rows [key0, end) of a request, in the order in which the other roles walk them.
     __device__ __forceinline__ bool rows(const WeighReq& r, int key0, int end)
     {
         const Shape& s = keys.s;
-        const int stored = kKeys > 0 ? s.latent : s.chunks, steps = stored + 2 * kTurned;
-        int step = 0, band = 0, first = 0, first_use = 0;
+        int step = 0;
         for (;;) {
             // groups that are arrived for: all at the end, the oldest of kLanding and those whose stages are next, and
-            // bands when some chunks of the next unit have been asked for, by when they have landed
+            // bands when some steps of the next tile have been asked for, by when they have landed
             while (landing > 0 && (key0 >= end || landing == kLanding || uses - oldest_use >= s.stages ||
                                    (kKeys > 0 && step == kTurnAfter && !keys.copied())))
                 arrive_oldest();
             if (key0 >= end) return true;
-            if (step == 0 && band == 0) {
-                const Tile t{key0, min(kWeighKeys, end - key0)};
-                keys.look_up(r, t);
-                keys.look_ahead(r, t, end);
+            if (step == 0) {
+                const Tile tile{key0, min(kWeighKeys, end - key0)};
+                keys.look_up(r, tile);
+                keys.look_ahead(r, tile, end);
             }
             if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return false;
-            if (step < stored) {
-                keys.key_chunk(band, step, stage_at(ring.stage), smem_addr(&m->full[ring.stage]));
-                if (keys.copied()) land(uses, 8 * ring.stage);
-            }
-            if constexpr (kKeys > 0) {
-                if (step == stored) {
-                    first = ring.stage;
-                    first_use = uses;
-                }
-                if (step + 1 == steps) {
-                    const int buffer = bands_read++ & 3;
-                    keys.copy_bands(band, [&](int c) { return stage_at(stage_after(first, c)); },
-                                    smem_addr(m->counts[buffer] + 16 * keys.warp));
-                    land(first_use, 8 * first + 1 + buffer);
+            const uint32_t dst = stage_at(ring.stage);
+            const int band_step = step - t.row_steps;
+            if (kKeys > 0 && band_step >= 0) {
+                const int c = band_step % t.band_steps(), band = band_step / t.band_steps(), buffer = bands_read++ & 3;
+                keys.copy_bands(band, c, c + kKeys / 2, kKeys > 1, dst, t.turned * kAtomBytes, smem_addr(m->counts[buffer] + 16 * keys.warp));
+                land(uses, 16 * ring.stage + 1 + 4 * c + buffer);
+            } else {
+                const bool in_rows = band_step < 0;
+                const int p = (in_rows ? step : band_step) * t.planes;
+                if (keys.copied()) {
+                    keys.copy_planes(in_rows, p, t.planes, in_rows ? t.rows : t.bands, dst);
+                    land(uses, 16 * ring.stage);
+                } else {
+                    keys.box_planes(in_rows, box, p, t.planes, dst, smem_addr(&m->full[ring.stage]));
                 }
             }
             ring.advance(s.stages);
             ++uses;
-            if (++step < steps) continue;
+            if (++step < t.steps) continue;
             step = 0;
-            if (++band < s.bands) continue;
-            band = 0;
             key0 += kWeighKeys;
         }
     }
@@ -208,6 +235,7 @@ struct Loader {
 struct Issuer {
     const WeighArgs& a;
     const Shape& s;
+    const Steps& t;
     Misc* m;
     uint32_t smem, tmem;
     int q_rows;
@@ -215,6 +243,7 @@ struct Issuer {
     Ring ring;
     uint32_t stay_phase = 0;
     int index = 0;
+    int step = 0, plane = 0;  // of the tile: where the products have come to
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
     {
@@ -230,24 +259,43 @@ struct Issuer {
         __syncwarp();
         stay_phase ^= 1;
     }
+    // The query chunk of a plane of a step.
+    __device__ __forceinline__ int query_chunk(int at) const
+    {
+        if (step < t.row_steps) return step * t.planes + at;
+        const int i = step - t.row_steps;
+        if (t.turned == 0) return s.latent + (i * t.planes + at) % t.keys;
+        // planes of a turned step: the chunks c and c + keys / 2, then their low parts, which meet the same queries
+        return s.latent + i % t.band_steps() + (t.turned == 4 ? at % 2 * (t.keys / 2) : 0);
+    }
     __device__ __forceinline__ void unit(const Tile&, const Unit& u)
     {
         const int buf = index & 1;
         if (!wait(smem_addr(&m->s_empty[buf]), ((index >> 1) & 1) ^ 1)) return;
         ++index;
         const uint32_t d = tmem + buf * kWeighCols, desc = mma_desc(kWeighKeys, padded(u.cols), false, false);
-        for (int step = 0; step < s.chunks; ++step) {
-            if (!wait(smem_addr(&m->full[ring.stage]), ring.phase)) return;
-            fence_async_smem();
-            tcgen05_after_sync();
+        const uint32_t queries = smem + u.band * s.q_chunks * q_rows * 128;
+        for (int done = 0; done < s.chunks;) {
+            if (plane == 0) {
+                if (!wait(smem_addr(&m->full[ring.stage]), ring.phase)) return;
+                fence_async_smem();
+                tcgen05_after_sync();
+            }
+            const int count = t.count(step), n = min(count - plane, s.chunks - done);
             if (elect_lane()) {
-                const int qc = step < s.q_chunks ? step : step - s.low;  // a band's low part meets the same queries
-                product<false>(d, smem + s.stay_bytes + ring.stage * kChunkBytes,
-                               smem + (u.band * s.q_chunks + qc) * q_rows * 128, desc, step > 0);
-                mma_commit(smem_addr(&m->empty[ring.stage]));
-                if (step + 1 == s.chunks) mma_commit(smem_addr(&m->s_full[buf]));
+                const uint32_t at = smem + s.stay_bytes + ring.stage * t.stage_bytes;
+                for (int i = 0; i < n; ++i)
+                    product<false>(d, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc,
+                                   done + i > 0);
+                if (plane + n == count) mma_commit(smem_addr(&m->empty[ring.stage]));
+                if (done + n == s.chunks) mma_commit(smem_addr(&m->s_full[buf]));
             }
             __syncwarp();
+            done += n;
+            plane += n;
+            if (plane < count) continue;
+            plane = 0;
+            if (++step == t.steps) step = 0;
             ring.advance(s.stages);
         }
     }
@@ -349,14 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     Shape s = make_shape(a, kKeys > 0);
     const int q_rows = a.header->weigh_cols;
     s.stay_bytes = (int)stay_bytes(s.bands, s.q_chunks, q_rows);
-    s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / kChunkBytes);
+    const Steps t = make_steps(a, maps, s);
+    s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
         Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * q_rows), q_rows, warp, lane};
         walk(a, s, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
-        Issuer role{a, s, m, smem, tmem, q_rows};
+        Issuer role{a, s, t, m, smem, tmem, q_rows};
         walk(a, s, role);
         // nothing is in flight when TMEM is freed
         if (elect_lane()) mma_commit(smem_addr(&m->drained));
@@ -367,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{{a, maps, s, trig, w, lane, 0}, m, smem, q_rows};
+        Loader<kKeys> role{{a, maps, s, trig, w, lane, 0}, t, m, smem, q_rows, a.header->weigh_box};
         role.run();
         cp_async_wait_all();
     }
@@ -400,11 +449,13 @@ int weigh_tile_prepare(const Geometry& g, const void* kv, WeighMaps* maps)
     maps->shift = -1;
     for (int k = 0; k < 31; ++k)
         if (g.block_size == 1 << k) maps->shift = k;
-    const int groups = maps->box / 8;
-    if (maps->box &&
-        (!make_map(encode, &maps->rows, base, rows, g.lat_row_vecs, (g.latent_dim + (maps->whole ? g.rope_dim : 0)) / 64, 1, groups) ||
-         !make_map(encode, &maps->bands, base + g.rope_base_vecs, rows, g.rope_row_vecs, g.rope_vecs / 8, 1, groups)))
-        return (int)cudaErrorInvalidValue;
+    const bool mla = g.rope_heads <= 1;
+    for (int i = 0; maps->box > 0 && i < kWeighBoxes; ++i) {
+        const int groups = maps->box / 8, planes = weigh_planes(i, mla);
+        if (!make_map(encode, &maps->rows[i], base, rows, g.lat_row_vecs, (g.latent_dim + (maps->whole ? g.rope_dim : 0)) / 64, planes, groups) ||
+            !make_map(encode, &maps->bands[i], base + g.rope_base_vecs, rows, g.rope_row_vecs, g.rope_vecs / 8, planes, groups))
+            return (int)cudaErrorInvalidValue;
+    }
     return (int)cudaFuncSetAttribute(kernel_of(g), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 

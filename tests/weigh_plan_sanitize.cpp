@@ -116,7 +116,7 @@ int main(int argc, char** argv)
         const bool mla = chance(50);
         WeighShape w{chance(85), mla ? 1 : (int32_t)uniform(2, 9), (int32_t)(chance(30) ? uniform(1, 400) : uniform(1, 32)),
                      mla ? 9 : keys[uniform(0, 2)], (int32_t)uniform(1, 200),
-                     (int32_t)uniform(4, 8)};
+                     keys[uniform(0, 2)], chance(50)};
         BatchHeader h{};
         std::vector<WeighReq> reqs = plan.weigh;
         weigh_work(w, plan.chunks, &reqs, &h);
@@ -146,7 +146,8 @@ int main(int argc, char** argv)
                 check(x >= r.begin && x < r.begin + ceil_div(r.end, step), "its request is found");
             }
             if (h.weigh_mode == kQueriesStay)
-                check(stay_bytes(w.bands, w.q_chunks, h.weigh_cols) + w.stages * kWeighKeys * 128 <= kWeighSmem, "shared memory");
+                check(stay_bytes(w.bands, w.q_chunks, h.weigh_cols) + 2 * weigh_stage_planes(h.weigh_box, w.bands == 1, w.lazy, w.band_chunks) *
+                                                                              kWeighKeys * 128 <= kWeighSmem, "shared memory");
             continue;
         }
         int64_t at = 0, parts = 0, tiles_before = 0;
