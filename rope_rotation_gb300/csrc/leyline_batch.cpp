@@ -617,7 +617,7 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     // a captured call may be replayed with plans for either kernel, and with plans that cut as many query tiles as any
     int err = 0;
     if (!b->weigh_shape.tiles) err = launch_weigh(a, p->sm_count, stream);
-    else if (captured || b->weigh_mode == kQueriesStay) err = launch_weigh_tile(a, b->weigh_maps, p->sm_count, stream);
+    else if (captured || b->weigh_mode == kQueriesStay) err = launch_weigh_tile(a, b->weigh_maps, b->weigh_shape.pairs, stream);
     if (err == 0 && b->weigh_shape.tiles && (captured || b->weigh_mode == kKeysStay))
         err = launch_weigh_pair(a, b->weigh_maps, room, b->weigh_shape.pairs,
                                 captured ? kWeighItems * b->weigh_shape.pairs : b->weigh_tiles, stream);

@@ -36,14 +36,14 @@ struct BatchHeader {
     int32_t weigh_reqs;   // requests of the plan, one WeighReq each
     int32_t weigh_mode;   // WeighMode
     int64_t weigh_work;   // their work, in its mode's unit
-    int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded, at most
+    int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded to a multiple of 32, at most
     int32_t weigh_seg;    // kKeysStay: products of an item
     int32_t weigh_tiles;  // kKeysStay: tiles of cache rows whose query tiles are cut into several items
     int32_t weigh_box;    // kQueriesStay: index of weigh_planes
 };
 
 // How the weights that queries give to rows are computed, and a unit of its work: by leyline_weigh.cu a row, by
-// leyline_weigh_tile.cu 16 rows, by leyline_weigh_pair.cu an item.
+// leyline_weigh_tile.cu 32 rows, by leyline_weigh_pair.cu an item.
 enum WeighMode : int32_t { kAnyRows = 0, kQueriesStay = 1, kKeysStay = 2 };
 
 // One chunk, as attention sees it.
@@ -186,10 +186,10 @@ struct WeighShape {
     bool lazy = false;
 };
 // Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * pairs items have sums of their own.
-// Bytes of the queries that stay, and of what their rows are given.
+// Bytes of the queries that stay in a CTA, half of their rows, and of what all of them are given.
 constexpr int64_t stay_bytes(int64_t bands, int64_t q_chunks, int64_t rows)
 {
-    return bands * q_chunks * rows * 128 + (bands * rows * 8 + 1023) / 1024 * 1024;
+    return bands * q_chunks * rows / 2 * 128 + (bands * rows * 8 + 1023) / 1024 * 1024;
 }
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
 

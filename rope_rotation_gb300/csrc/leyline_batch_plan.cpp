@@ -275,7 +275,7 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
             r.units = (int32_t)(n * w.bands);
             units += n * w.bands * ceil_div(r.end, kPairKeys);
         }
-        const int64_t cols = ceil_div(most, 16) * 16, stay = stay_bytes(w.bands, w.q_chunks, cols);
+        const int64_t cols = ceil_div(most, 32) * 32, stay = stay_bytes(w.bands, w.q_chunks, cols);
         header->weigh_mode = kKeysStay;
         // the widest boxes that leave three stages, else two of the next
         for (int32_t box = kWeighBoxes - 1; single && box >= 0; --box) {
@@ -299,7 +299,7 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
         if (header->weigh_mode == kAnyRows) {
             header->weigh_work += r.end;
         } else if (header->weigh_mode == kQueriesStay) {
-            header->weigh_work += ceil_div(r.end, 16);
+            header->weigh_work += ceil_div(r.end, 32);
         } else {
             const int64_t tiles = ceil_div(r.end, kPairKeys);
             r.segs = (int32_t)ceil_div(r.units, header->weigh_seg);

@@ -145,9 +145,9 @@ __device__ __noinline__ void trig_of(int count, const double* turn, int pairs, b
 // The warps that bring a CTA's 128 cache rows, kRows of them each: boxes of 16 or 8 rows by TMA where 8 divides the block
 // size, else a row at a time.  In a lazy pool (kKeys > 0: the chunks of a band) they turn each row's band by its pending
 // count, in fp32, into the sum of two bf16 values, as leyline_attention_tile.cu does: the scores carry it to 2^-17.
-// kPair: of two CTAs whose chunks are counted in the first, whose warps alone arrive for boxes (an arrival from the other
+// The chunks of both CTAs of a pair are counted in the first, whose warps alone arrive for boxes (an arrival from the other
 // CTA is slow), for all that are expected of both.
-template <int kWarps, int kKeys, bool kPair>
+template <int kWarps, int kKeys>
 struct KeyLoader {
     static constexpr bool kLazy = kKeys > 0;
     static constexpr int kTurned = kLazy ? kKeys : 1;
@@ -187,16 +187,15 @@ struct KeyLoader {
         slot = slot_at(page, t.key0);
         if (slot < 0 && page != INT32_MIN) raise_status(a.status, ST_BAD_PAGE);
     }
-    // The pages of the next tile of the rows below `end` are read while this one is loaded.  (Asking for its rows in L2 as
-    // well, whole, cost more than it gave: 16 decodes of 16 heads over some 24000 rows 107 -> 115 us.)
-    __device__ __forceinline__ void look_ahead(const WeighReq& r, const Tile& t, int end)
+    // The pages of the next tile are read while this one is loaded.  (Asking for its rows in L2 as well, whole, cost more
+    // than it gave: 16 decodes of 16 heads over some 24000 rows 107 -> 115 us.)
+    __device__ __forceinline__ void look_ahead(const WeighReq& r, const Tile& t)
     {
-        const int key = t.key0 + kWeighKeys;
-        if (next_key == key && next_req == r.req) return;
-        next_page = page_of_row(r, key, end - key);
-        next_key = key;
+        next_page = page_of_row(r, t.key0, t.keys);
+        next_key = t.key0;
         next_req = r.req;
     }
+
     __device__ __forceinline__ void ensure(int c)
     {
         if (counted && c == count) return;
@@ -292,8 +291,7 @@ struct KeyLoader {
     // An arrival of this warp (its lane 0) for what it has written to shared memory.
     __device__ __forceinline__ void arrive(uint32_t bar) const
     {
-        if (kPair) cluster_arrive_smem(cluster_addr(bar, 0));
-        else mbar_arrive(bar);
+        cluster_arrive_smem(cluster_addr(bar, 0));
     }
 
     // This warp's rows of `n` planes from plane p on of the latents (whole MLA rows: and their band), or of the bands, to `dst`,
@@ -304,20 +302,13 @@ struct KeyLoader {
         const CUtensorMap* map = in_rows ? &maps.rows[box] : &maps.bands[box];
         const int base = (int)((long long)a.layer * a.g.num_pages * a.g.block_size / 8);
         const uint32_t to = dst + (kRows * warp + lane) * 128 * n;
-        if (kPair) {  // (a box before the first row arrives as zeros)
-            if (lane == 0 && rank == 0) {
-                mbar_expect_tx(bar, 2 * kRows * 128 * n);
-                mbar_arrive(bar);
-            }
-            if (lane < kRows && lane % maps.box == 0)
-                pair_box4(to, map, p, slot >= 0 ? base + (int)(slot >> 3) : -2, cluster_addr(bar, 0));
-        } else {
-            const bool mine = lane < kRows && lane % maps.box == 0 && slot >= 0;
-            const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-            if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * maps.box * 128 * n);
-            __syncwarp();
-            if (mine) tma_box4(to, map, p, base + (int)(slot >> 3), bar);
+        if (lane == 0 && rank == 0) {
+            mbar_expect_tx(bar, 2 * kRows * 128 * n);
+            mbar_arrive(bar);
         }
+        // (a box before the first row arrives as zeros)
+        if (lane < kRows && lane % maps.box == 0)
+            pair_box4(to, map, p, slot >= 0 ? base + (int)(slot >> 3) : -2, cluster_addr(bar, 0));
         __syncwarp();
     }
     // The same planes, those below `end` of them, a row at a time: to be arrived for when they have landed (an arrival of
@@ -343,13 +334,13 @@ struct Unit {
     int band, tok, toks, head0, heads, cols;
 };
 
-// 16 bytes of query row `row` (of which this thread has the 16 bytes v of each chunk) of chunks [c0, c1) of a unit, the
-// first of them to `dst` and the next ones `pitch` bytes on; zeros behind its last row.
-__device__ __forceinline__ void copy_query_row(const WeighArgs& a, const Shape& s, const Unit& u, int row, int v, int c0, int c1,
-                                               uint32_t dst, uint32_t pitch)
+// 16 bytes of query row `column` (of which this thread has the 16 bytes v of each chunk) of chunks [c0, c1) of a unit to row
+// `row`, of the first of them at `dst` and of the next ones `pitch` bytes on; zeros behind its last one.
+__device__ __forceinline__ void copy_query_row(const WeighArgs& a, const Shape& s, const Unit& u, int column, int row, int v, int c0,
+                                               int c1, uint32_t dst, uint32_t pitch)
 {
-    const bool on = row < u.cols;
-    const int col = on ? row : 0, tok = u.cols > 0 ? col / u.heads : 0;
+    const bool on = column < u.cols;
+    const int col = on ? column : 0, tok = u.cols > 0 ? col / u.heads : 0;
     const long long t = u.cols > 0 ? u.ch.tok0 + u.tok + tok : 0, head = u.cols > 0 ? u.band * s.group + u.head0 + (col - tok * u.heads) : 0;
     const uint4* latent = static_cast<const uint4*>(a.q_latent.ptr) + (t * a.q_latent.token_stride + head * a.q_latent.head_stride) / 8 + v;
     const uint4* band = static_cast<const uint4*>(a.q_rope.ptr) + (t * a.q_rope.token_stride + head * a.q_rope.head_stride) / 8 + v;
@@ -360,15 +351,11 @@ __device__ __forceinline__ void copy_query_row(const WeighArgs& a, const Shape& 
 
 // ----------------------------------------------------------------- products --
 // 64 columns of S^T, rows of 128 bytes in both operands; the keys' groups of 8 rows lie `pitch` bytes apart.
-template <bool kPair>
 __device__ __forceinline__ void product(uint32_t d, uint32_t keys, int pitch, uint32_t queries, uint32_t desc, bool more)
 {
     const uint64_t k = smem_matrix(keys, 16, pitch), q = smem_matrix(queries, 16, 1024);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (kPair) pair_mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);
-        else mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);
-    }
+    for (int e = 0; e < 4; ++e) pair_mma_bf16(d, k + (uint64_t)(2 * e), q + (uint64_t)(2 * e), desc, more || e > 0);
 }
 
 // ----------------------------------------------------------------- epilogue --
@@ -447,6 +434,27 @@ __device__ __forceinline__ float sum_columns(uint32_t tmem, int n, int cols, flo
         }
     }
     return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+}
+
+// Launch pairs of CTAs with programmatic stream serialization.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(KArgs...), int pairs, int threads, size_t smem, cudaStream_t stream, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

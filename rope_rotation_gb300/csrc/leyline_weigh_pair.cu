@@ -143,7 +143,7 @@ struct QueryLoader {
 
 template <int kKeys>
 struct Loader {
-    KeyLoader<kLoadWarps, kKeys, true> keys;
+    KeyLoader<kLoadWarps, kKeys> keys;
     Misc* m;
     uint32_t smem;
     int* counts;  // lazy pools: pending turns of this warp's rows
@@ -203,7 +203,7 @@ struct Loader {
         for (int c = 0; c < s.q_chunks; ++c) {
             if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return;
             for (int row = tid / 8; row < rows; row += 4 * kLoadWarps)
-                copy_query_row(keys.a, s, u, row, tid % 8, c, c + 1, smem + s.stay_bytes + ring.stage * kChunkBytes, 0);
+                copy_query_row(keys.a, s, u, row, row, tid % 8, c, c + 1, smem + s.stay_bytes + ring.stage * kChunkBytes, 0);
             cp_async_wait_all();
             fence_async_smem();
             __syncwarp();
@@ -260,10 +260,10 @@ struct Issuer {
             if (elect_lane()) {
                 const uint32_t at = smem + s.stay_bytes + ring.stage * kChunkBytes;
                 if (band) {
-                    product<true>(d, turned, planes * kAtomBytes, at, desc, c > 0);
-                    product<true>(d, turned + planes / 2 * kAtomBytes, planes * kAtomBytes, at, desc, true);  // its low part
+                    product(d, turned, planes * kAtomBytes, at, desc, c > 0);
+                    product(d, turned + planes / 2 * kAtomBytes, planes * kAtomBytes, at, desc, true);  // its low part
                 } else {
-                    product<true>(d, smem + c * kChunkBytes, kAtomBytes, at, desc, c > 0);
+                    product(d, smem + c * kChunkBytes, kAtomBytes, at, desc, c > 0);
                 }
                 pair_commit(smem_addr(&m->empty[ring.stage]));
                 if (c + 1 == s.q_chunks) pair_commit(smem_addr(&m->s_full[buf]));
@@ -482,21 +482,7 @@ int launch_weigh_pair(const WeighArgs& a, const WeighMaps& maps, int64_t tokens,
     QueryMaps queries{};
     queries.usable = query_map(&queries.band, a.q_rope, g.rope_dim, a.q_heads, tokens, heads, toks) &&
                      (g.rope_heads > 1 || query_map(&queries.latent, a.q_latent, g.latent_dim, a.q_heads, tokens, heads, toks));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(g), a, maps, queries);
+    cudaError_t e = launch_pairs(kernel_of(g), pairs, kThreads, kSmemBytes, (cudaStream_t)stream, a, maps, queries);
     if (e == cudaSuccess && joins > 0) e = launch_dependent(join_weights_kernel, joins, kPairKeys, (cudaStream_t)stream, a);
     return (int)e;
 }

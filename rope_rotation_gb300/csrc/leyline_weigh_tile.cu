@@ -2,14 +2,17 @@
 // every request's query rows of a band fit one tile of 128 (decoding): MLA rows and the grouped rows that attention takes
 // in tiles.
 //
-//   S^T = K Q^T  [128 cache rows x up to 128 query rows],  w_s += sum over columns of exp2(S^T * scale * log2 e - lse * log2 e)
+//   S^T = K Q^T  [256 cache rows x up to 128 query rows],  w_s += sum over columns of exp2(S^T * scale * log2 e - lse * log2 e)
 //
-// lse is given, so tiles need no common maximum, and a row of the cache is read once.  The queries of all bands stay in
-// shared memory while the keys pass through what is left of it, as they come from HBM, some planes of 64 columns at a time:
-// an SM takes about 110 cycles for a TMA box whatever its size, so boxes of one plane of 16 rows, 72 for a tile of MLA
-// rows, bound the kernel.  The CTAs take equal shares of 16 rows, one CTA an SM.
+// lse is given, so tiles need no common maximum, and a row of the cache is read once.  By pairs of CTAs (cta_group::2): each
+// has half of a tile's cache rows, of their S^T, and of the queries of all bands, which stay in shared memory while the keys
+// pass through what is left of it as they come from HBM, some planes of 64 columns at a time.  With all of 128 MLA query rows
+// in a CTA only 64 KB were left, too little in flight for HBM's latency; and an SM takes about 110 cycles for a TMA box
+// whatever its size, so boxes of one plane of 16 rows, 72 for 128 MLA rows, bound the kernel.  The pairs take equal shares
+// of 32 rows.
 //
-// Roles: warps 0-3 sum, warp 4 issues the products, warps 5-12 load, 16 rows of a chunk each.
+// Roles in each CTA: warps 0-3 sum, warp 4 issues the products (in the first CTA alone), warps 5-12 load, 16 rows of a plane
+// each.
 #include "leyline_weigh.cuh"
 
 namespace leyline {
@@ -19,10 +22,14 @@ constexpr int kSumWarps = 4, kMmaWarp = kSumWarps, kLoadWarp = kMmaWarp + 1, kLo
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr uint32_t kTmemCols = 256;  // two buffers of S^T
 
+// Barriers marked (first) are used in the first CTA alone; the others in both.
 struct Misc {
-    unsigned long long full[kMaxStages], empty[kMaxStages];
-    unsigned long long stay_full, stay_empty;
-    unsigned long long s_full[2], s_empty[2];
+    unsigned long long full[kMaxStages];  // (first)
+    unsigned long long empty[kMaxStages];
+    unsigned long long stay_full;         // (first)
+    unsigned long long stay_empty;
+    unsigned long long s_full[2];
+    unsigned long long s_empty[2];        // (first)
     unsigned long long drained;
     uint32_t tmem;
     int quit;
@@ -32,16 +39,29 @@ struct Misc {
 constexpr int kSmemBytes = kWeighSmem + (int)sizeof(Misc) + kLoadWarps * 128 * (int)sizeof(float2) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
-// Every role walks the CTA's work in the same order (the loaders by a loop of their own): stay(u): the query tile u of every
-// band is to stay; unit(t, u): a product; flush(r, t): the tile's sums are complete; release(): the queries are no longer
-// used.
-template <class Role>
-__device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& role)
+__device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, Misc* m, int32_t* status)
 {
-    const long long work = a.header->weigh_work, g1 = work * (blockIdx.x + 1) / gridDim.x;
-    for (long long g = work * blockIdx.x / gridDim.x; g < g1;) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, &m->quit, status));
+}
+
+// The share of a CTA in the rows [key0, end) of a pair, the first kPairKeys of them: half, in groups of 16.
+__device__ __forceinline__ Tile share_of(uint32_t rank, int key0, int end)
+{
+    const int keys = max(0, min(kPairKeys, end - key0)), half = min(keys, (keys + 31) / 32 * 16);
+    return rank == 0 ? Tile{key0, half} : Tile{key0 + half, keys - half};
+}
+
+// Every role of both CTAs walks the pair's work in the same order (the loaders by a loop of their own): stay(u): the query
+// tile u of every band is to stay; unit(t, u): a product, t of this CTA's rows, of which there may be none; flush(r, t): the
+// tile's sums are complete; release(): the queries are no longer used.
+template <class Role>
+__device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, uint32_t rank, Role& role)
+{
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const long long work = a.header->weigh_work, g1 = work * (pair + 1) / pairs;
+    for (long long g = work * pair / pairs; g < g1;) {
         const WeighReq r = find_request(a, g);
-        const long long g_end = min(g1, (long long)(r.begin + (r.end + 15) / 16));
+        const long long g_end = min(g1, (long long)(r.begin + (r.end + 31) / 32));
         if (!weights_hold(a, r)) {
             role.refuse();
             g = g_end;
@@ -50,9 +70,9 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, Role& r
         const ChunkDev ch = a.chunks[r.chunk];
         Unit u{ch, 0, 0, ch.n, 0, s.group, ch.n * s.group};
         role.stay(u);
-        const int end = (int)min((g_end - (long long)r.begin) * 16, (long long)r.end);
-        for (int key0 = (int)(g - r.begin) * 16; key0 < end; key0 += kWeighKeys) {
-            const Tile t{key0, min(kWeighKeys, end - key0)};
+        const int end = (int)min((g_end - (long long)r.begin) * 32, (long long)r.end);
+        for (int key0 = (int)(g - r.begin) * 32; key0 < end; key0 += kPairKeys) {
+            const Tile t = share_of(rank, key0, end);
             for (u.band = 0; u.band < s.bands; ++u.band) role.unit(t, u);
             role.flush(r, t);
         }
@@ -104,7 +124,7 @@ constexpr int kTurnAfter = 2;  // steps of the next tile are asked for before a 
 
 template <int kKeys>
 struct Loader {
-    KeyLoader<kLoadWarps, kKeys, false> keys;
+    KeyLoader<kLoadWarps, kKeys> keys;
     const Steps& t;
     Misc* m;
     uint32_t smem;
@@ -121,7 +141,7 @@ struct Loader {
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
     {
-        if (ok) ok = warp_wait(bar, parity, &m->quit, keys.a.status);
+        if (ok) ok = pair_warp_wait(bar, parity, m, keys.a.status);
         return ok;
     }
 
@@ -135,13 +155,14 @@ struct Loader {
         else cp_async_wait<2>();
         __syncwarp();
         const int stage = (kinds & 255) / 16, what = (int)(kinds & 15) - 1;
-        if constexpr (kKeys > 0) {
+        if (what < 0) {
+            fence_async_smem();
+            __syncwarp();
+        } else if constexpr (kKeys > 0) {
             const int c = what / 4;
-            if (what >= 0)
-                keys.turn_bands(c, c + kKeys / 2, kKeys > 1, stage_at(stage), t.turned * kAtomBytes,
-                                m->counts[what % 4] + 16 * keys.warp);
+            keys.turn_bands(c, c + kKeys / 2, kKeys > 1, stage_at(stage), t.turned * kAtomBytes, m->counts[what % 4] + 16 * keys.warp);
         }
-        if (keys.lane == 0) mbar_arrive(smem_addr(&m->full[stage]));
+        if (keys.lane == 0) keys.arrive(smem_addr(&m->full[stage]));
         --landing;
         kinds >>= 8;
         oldest_use += gaps & 255;
@@ -165,10 +186,12 @@ struct Loader {
         const int tid = 32 * keys.warp + keys.lane;
         for (u.band = 0; u.band < s.bands; ++u.band)
             for (int row = tid / 8; row < q_rows; row += 4 * kLoadWarps)
-                copy_query_row(keys.a, s, u, row, tid % 8, 0, s.q_chunks, smem + u.band * s.q_chunks * pitch, pitch);
+                copy_query_row(keys.a, s, u, (int)keys.rank * q_rows + row, row, tid % 8, 0, s.q_chunks,
+                               smem + u.band * s.q_chunks * pitch, pitch);
         cp_async_wait_all();  // (no groups are in flight between requests)
+        fence_async_smem();
         __syncwarp();
-        if (keys.lane == 0) mbar_arrive(smem_addr(&m->stay_full));
+        if (keys.lane == 0) keys.arrive(smem_addr(&m->stay_full));
         return true;
     }
 
@@ -185,9 +208,8 @@ struct Loader {
                 arrive_oldest();
             if (key0 >= end) return true;
             if (step == 0) {
-                const Tile tile{key0, min(kWeighKeys, end - key0)};
-                keys.look_up(r, tile);
-                keys.look_ahead(r, tile, end);
+                keys.look_up(r, share_of(keys.rank, key0, end));
+                keys.look_ahead(r, share_of(keys.rank, key0 + kPairKeys, end));
             }
             if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return false;
             const uint32_t dst = stage_at(ring.stage);
@@ -210,21 +232,22 @@ struct Loader {
             ++uses;
             if (++step < t.steps) continue;
             step = 0;
-            key0 += kWeighKeys;
+            key0 += kPairKeys;
         }
     }
 
     __device__ __forceinline__ void run()
     {
         const WeighArgs& a = keys.a;
-        const long long work = a.header->weigh_work, g1 = work * (blockIdx.x + 1) / gridDim.x;
-        for (long long g = work * blockIdx.x / gridDim.x; g < g1;) {
+        const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+        const long long work = a.header->weigh_work, g1 = work * (pair + 1) / pairs;
+        for (long long g = work * pair / pairs; g < g1;) {
             const WeighReq r = find_request(a, g);
-            const long long g_end = min(g1, (long long)(r.begin + (r.end + 15) / 16));
+            const long long g_end = min(g1, (long long)(r.begin + (r.end + 31) / 32));
             if (weights_hold(a, r)) {
                 const ChunkDev ch = a.chunks[r.chunk];
                 if (!queries(Unit{ch, 0, 0, ch.n, 0, keys.s.group, ch.n * keys.s.group})) return;
-                if (!rows(r, (int)(g - r.begin) * 16, (int)min((g_end - (long long)r.begin) * 16, (long long)r.end))) return;
+                if (!rows(r, (int)(g - r.begin) * 32, (int)min((g_end - (long long)r.begin) * 32, (long long)r.end))) return;
             }
             g = g_end;
         }
@@ -247,7 +270,7 @@ struct Issuer {
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
     {
-        if (ok) ok = warp_wait(bar, parity, &m->quit, a.status);
+        if (ok) ok = pair_warp_wait(bar, parity, m, a.status);
         return ok;
     }
     __device__ __forceinline__ void refuse() {}
@@ -255,7 +278,7 @@ struct Issuer {
     __device__ __forceinline__ void stay(const Unit&) { wait(smem_addr(&m->stay_full), stay_phase); }
     __device__ __forceinline__ void release()
     {
-        if (ok && elect_lane()) mma_commit(smem_addr(&m->stay_empty));
+        if (ok && elect_lane()) pair_commit(smem_addr(&m->stay_empty));
         __syncwarp();
         stay_phase ^= 1;
     }
@@ -273,7 +296,7 @@ struct Issuer {
         const int buf = index & 1;
         if (!wait(smem_addr(&m->s_empty[buf]), ((index >> 1) & 1) ^ 1)) return;
         ++index;
-        const uint32_t d = tmem + buf * kWeighCols, desc = mma_desc(kWeighKeys, padded(u.cols), false, false);
+        const uint32_t d = tmem + buf * kWeighCols, desc = mma_desc(kPairKeys, 2 * q_rows, false, false);
         const uint32_t queries = smem + u.band * s.q_chunks * q_rows * 128;
         for (int done = 0; done < s.chunks;) {
             if (plane == 0) {
@@ -285,10 +308,10 @@ struct Issuer {
             if (elect_lane()) {
                 const uint32_t at = smem + s.stay_bytes + ring.stage * t.stage_bytes;
                 for (int i = 0; i < n; ++i)
-                    product<false>(d, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc,
+                    product(d, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc,
                                    done + i > 0);
-                if (plane + n == count) mma_commit(smem_addr(&m->empty[ring.stage]));
-                if (done + n == s.chunks) mma_commit(smem_addr(&m->s_full[buf]));
+                if (plane + n == count) pair_commit(smem_addr(&m->empty[ring.stage]));
+                if (done + n == s.chunks) pair_commit(smem_addr(&m->s_full[buf]));
             }
             __syncwarp();
             done += n;
@@ -310,9 +333,10 @@ struct Summer {
     const Shape& s;
     Misc* m;
     uint32_t tmem;
-    float* neg;   // [bands][q_rows]
+    float* neg;   // [bands][cols]
     int* limit;
-    int q_rows;
+    int cols;
+    uint32_t rank;
     int warp, lane;
     int index = 0;
     int open = 0;  // rows below it are attended to by every column
@@ -320,7 +344,7 @@ struct Summer {
 
     __device__ __forceinline__ void refuse()
     {
-        if (threadIdx.x == 0) raise_status(a.status, ST_BAD_ROW);
+        if (threadIdx.x == 0 && rank == 0) raise_status(a.status, ST_BAD_ROW);
     }
     __device__ __forceinline__ void stay(Unit u)
     {
@@ -329,9 +353,9 @@ struct Summer {
         int least = INT32_MAX;
         for (u.band = 0; u.band < s.bands; ++u.band) {
             const Column col = column_of(a, s, u, c);
-            if (c >= q_rows) continue;
-            neg[u.band * q_rows + c] = col.neg();
-            limit[u.band * q_rows + c] = col.rows();
+            if (c >= cols) continue;
+            neg[u.band * cols + c] = col.neg();
+            limit[u.band * cols + c] = col.rows();
             if (c < u.cols) least = min(least, col.rows());
         }
         least = __reduce_min_sync(0xffffffffu, least);
@@ -344,14 +368,14 @@ struct Summer {
     __device__ __forceinline__ void unit(const Tile& t, const Unit& u)
     {
         const int buf = index & 1;
-        mbar_wait(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
+        mbar_wait_cluster(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * warp < t.keys)
             sum += sum_columns(tmem + buf * kWeighCols + ((uint32_t)(32 * warp) << 16), padded(u.cols), u.cols, a.scale * kLog2e,
-                               neg + u.band * q_rows, limit + u.band * q_rows, t.key0 + 32 * warp + lane, t.key0 + t.keys > open);
+                               neg + u.band * cols, limit + u.band * cols, t.key0 + 32 * warp + lane, t.key0 + t.keys > open);
         tcgen05_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&m->s_empty[buf]));
+        if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->s_empty[buf]), 0));
         ++index;
     }
 
@@ -372,59 +396,65 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     unsigned char* base = raw + (smem - smem_addr(raw));
     Misc* m = reinterpret_cast<Misc*>(base + kWeighSmem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     wait_for_previous_grid();
-    if (a.header->weigh_mode != kQueriesStay) return;  // the plan is for the other kernel
+    if (a.header->weigh_mode != kQueriesStay) return;  // the plan is for the other kernel (both CTAs see the same)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(smem_addr(&m->full[i]), kLoadWarps);
+            mbar_init(smem_addr(&m->full[i]), 2 * kLoadWarps);
             mbar_init(smem_addr(&m->empty[i]), 1);
         }
-        mbar_init(smem_addr(&m->stay_full), kLoadWarps);
+        mbar_init(smem_addr(&m->stay_full), 2 * kLoadWarps);
         mbar_init(smem_addr(&m->stay_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&m->s_full[i]), 1);
-            mbar_init(smem_addr(&m->s_empty[i]), kSumWarps);
+            mbar_init(smem_addr(&m->s_empty[i]), 2 * kSumWarps);
         }
         mbar_init(smem_addr(&m->drained), 1);
         m->quit = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&m->tmem), kTmemCols);
+    if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);
     tcgen05_before_sync();
     __syncthreads();
+    cluster_sync();
     tcgen05_after_sync();
     const uint32_t tmem = m->tmem;
     Shape s = make_shape(a, kKeys > 0);
-    const int q_rows = a.header->weigh_cols;
-    s.stay_bytes = (int)stay_bytes(s.bands, s.q_chunks, q_rows);
+    const int cols = a.header->weigh_cols, q_rows = cols / 2;
+    s.stay_bytes = (int)stay_bytes(s.bands, s.q_chunks, cols);
     const Steps t = make_steps(a, maps, s);
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
-        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * q_rows), q_rows, warp, lane};
-        walk(a, s, role);
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, rank, warp, lane};
+        walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
-        Issuer role{a, s, t, m, smem, tmem, q_rows};
-        walk(a, s, role);
-        // nothing is in flight when TMEM is freed
-        if (elect_lane()) mma_commit(smem_addr(&m->drained));
-        __syncwarp();
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
+        if (rank == 0) {
+            Issuer role{a, s, t, m, smem, tmem, q_rows};
+            walk(a, s, rank, role);
+            // nothing is in flight when TMEM is freed
+            if (elect_lane()) pair_commit(smem_addr(&m->drained));
+            __syncwarp();
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_cluster(smem_addr(&m->drained), 0) && global_ns() - t0 < kWaitLimit) {
+            }
         }
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{{a, maps, s, trig, w, lane, 0}, t, m, smem, q_rows, a.header->weigh_box};
+        Loader<kKeys> role{{a, maps, s, trig, w, lane, rank}, t, m, smem, q_rows, a.header->weigh_box};
         role.run();
         cp_async_wait_all();
     }
     __syncthreads();
     let_loads_land(&m->quit);
+    // neither CTA leaves while the other may still reach its shared memory, or a product its TMEM
+    cluster_sync();
     if (warp == kMmaWarp) {
         tcgen05_after_sync();
-        tmem_free(tmem, kTmemCols);
+        pair_tmem_free(tmem, kTmemCols);
     }
 }
 
@@ -459,9 +489,9 @@ int weigh_tile_prepare(const Geometry& g, const void* kv, WeighMaps* maps)
     return (int)cudaFuncSetAttribute(kernel_of(g), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 
-int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int ctas, void* stream)
+int launch_weigh_tile(const WeighArgs& a, const WeighMaps& maps, int pairs, void* stream)
 {
-    return (int)launch_dependent_smem(kernel_of(a.g), ctas, kThreads, kSmemBytes, (cudaStream_t)stream, a, maps);
+    return (int)launch_pairs(kernel_of(a.g), pairs, kThreads, kSmemBytes, (cudaStream_t)stream, a, maps);
 }
 
 }  // namespace leyline

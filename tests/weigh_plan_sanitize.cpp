@@ -129,7 +129,7 @@ int main(int argc, char** argv)
         const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
         check(tokens * std::min(w.group, kWeighCols) <= kWeighCols, "query tiles fit");
         if (h.weigh_mode != kKeysStay) {
-            const int64_t step = h.weigh_mode == kAnyRows ? 1 : 16;
+            const int64_t step = h.weigh_mode == kAnyRows ? 1 : 32;
             int64_t at = 0;
             for (const WeighReq& r : reqs) {
                 check(r.begin == at, "work in order");
