@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kSumWarps = 4, kMmaWarp = kSumWarps, kLoadWarp = kMmaWarp + 1, kLoadWarps = 8;
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
-constexpr uint32_t kTmemCols = 256;  // two buffers of S^T
+constexpr uint32_t kTmemCols = 512;
+constexpr int kBuffers = 8;  // of S^T, 4 where they have more than 64 columns
 
 // Barriers marked (first) are used in the first CTA alone; the others in both.
 struct Misc {
@@ -28,8 +29,8 @@ struct Misc {
     unsigned long long empty[kMaxStages];
     unsigned long long stay_full;         // (first)
     unsigned long long stay_empty;
-    unsigned long long s_full[2];
-    unsigned long long s_empty[2];        // (first)
+    unsigned long long s_full[kBuffers];
+    unsigned long long s_empty[kBuffers];  // (first)
     unsigned long long drained;
     uint32_t tmem;
     int quit;
@@ -115,6 +116,23 @@ __device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps&
     t.steps = t.row_steps + (t.turned > 0 ? s.bands * t.band_steps() : (t.bands + t.planes - 1) / t.planes);
     return t;
 }
+
+// The buffers of S^T, used in turn: with two of them grouped rows, whose bands have a product each, waited for their sums.
+struct Buffers {
+    int cols, count;
+    int at = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ explicit Buffers(int c) : cols(c), count(c > 64 ? 4 : kBuffers) {}
+    __device__ __forceinline__ uint32_t column() const { return at * cols; }
+    __device__ __forceinline__ void advance()
+    {
+        if (++at == count) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // --------------------------------------------------------------------- loads --
 // What a warp has asked for by cp.async (rows that TMA does not take, the bands that are to be turned) and has not arrived
@@ -262,10 +280,10 @@ struct Issuer {
     Misc* m;
     uint32_t smem, tmem;
     int q_rows;
+    Buffers buf;
     bool ok = true;
     Ring ring;
     uint32_t stay_phase = 0;
-    int index = 0;
     int step = 0, plane = 0;  // of the tile: where the products have come to
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity)
@@ -293,10 +311,10 @@ struct Issuer {
     }
     __device__ __forceinline__ void unit(const Tile&, const Unit& u)
     {
-        const int buf = index & 1;
-        if (!wait(smem_addr(&m->s_empty[buf]), ((index >> 1) & 1) ^ 1)) return;
-        ++index;
-        const uint32_t d = tmem + buf * kWeighCols, desc = mma_desc(kPairKeys, 2 * q_rows, false, false);
+        if (!wait(smem_addr(&m->s_empty[buf.at]), buf.phase ^ 1)) return;
+        const uint32_t d = tmem + buf.column(), full = smem_addr(&m->s_full[buf.at]);
+        buf.advance();
+        const uint32_t desc = mma_desc(kPairKeys, 2 * q_rows, false, false);
         const uint32_t queries = smem + u.band * s.q_chunks * q_rows * 128;
         for (int done = 0; done < s.chunks;) {
             if (plane == 0) {
@@ -311,7 +329,7 @@ struct Issuer {
                     product(d, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc,
                                    done + i > 0);
                 if (plane + n == count) pair_commit(smem_addr(&m->empty[ring.stage]));
-                if (done + n == s.chunks) pair_commit(smem_addr(&m->s_full[buf]));
+                if (done + n == s.chunks) pair_commit(full);
             }
             __syncwarp();
             done += n;
@@ -336,9 +354,9 @@ struct Summer {
     float* neg;   // [bands][cols]
     int* limit;
     int cols;
+    Buffers buf;
     uint32_t rank;
     int warp, lane;
-    int index = 0;
     int open = 0;  // rows below it are attended to by every column
     float sum = 0.f;
 
@@ -367,16 +385,15 @@ struct Summer {
 
     __device__ __forceinline__ void unit(const Tile& t, const Unit& u)
     {
-        const int buf = index & 1;
-        mbar_wait_cluster(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
+        mbar_wait_cluster(smem_addr(&m->s_full[buf.at]), buf.phase, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * warp < t.keys)
-            sum += sum_columns(tmem + buf * kWeighCols + ((uint32_t)(32 * warp) << 16), padded(u.cols), u.cols, a.scale * kLog2e,
+            sum += sum_columns(tmem + buf.column() + ((uint32_t)(32 * warp) << 16), padded(u.cols), u.cols, a.scale * kLog2e,
                                neg + u.band * cols, limit + u.band * cols, t.key0 + 32 * warp + lane, t.key0 + t.keys > open);
         tcgen05_before_sync();
         __syncwarp();
-        if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->s_empty[buf]), 0));
-        ++index;
+        if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->s_empty[buf.at]), 0));
+        buf.advance();
     }
 
     __device__ __forceinline__ void flush(const WeighReq& r, const Tile& t)
@@ -406,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
         }
         mbar_init(smem_addr(&m->stay_full), 2 * kLoadWarps);
         mbar_init(smem_addr(&m->stay_empty), 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBuffers; ++i) {
             mbar_init(smem_addr(&m->s_full[i]), 1);
             mbar_init(smem_addr(&m->s_empty[i]), 2 * kSumWarps);
         }
@@ -427,12 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
-        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, rank, warp, lane};
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, Buffers(cols),
+                    rank, warp, lane};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
         if (rank == 0) {
-            Issuer role{a, s, t, m, smem, tmem, q_rows};
+            Issuer role{a, s, t, m, smem, tmem, q_rows, Buffers(cols)};
             walk(a, s, rank, role);
             // nothing is in flight when TMEM is freed
             if (elect_lane()) pair_commit(smem_addr(&m->drained));
