@@ -155,20 +155,19 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     for (int32_t k = 0; k < n; ++k) {
         const int32_t len = (int32_t)bt->seq_lens_host[keeps[k].req];
         if (keeps[k].n_keep == len) continue;
-        EvictReq r{keeps[k].req, keeps[k].n_keep, 0, 0, len, k, 0, 0, p->q_tail + pages};
-        if (reqs.size() % kEvictReqs == 0) {
-            launch_stage = 0;
-        } else {
-            const EvictReq& b = reqs.back();
-            r.row_begin = b.row_begin + b.len;
-        }
-        r.stage = launch_stage;
-        launch_stage += r.n_keep;
-        most_stage = std::max(most_stage, launch_stage);
-        pages += ceil_div(len, g.block_size) - ceil_div(r.n_keep, g.block_size);
-        reqs.push_back(r);
+        reqs.push_back(EvictReq{keeps[k].req, keeps[k].n_keep, 0, 0, len, k, 0, 0, p->q_tail + pages});
+        pages += ceil_div(len, g.block_size) - ceil_div(keeps[k].n_keep, g.block_size);
     }
     if (reqs.empty()) return LEYLINE_OK;
+    // the longest first: a request's chains of rows take as long as its rows, whatever runs beside them
+    std::stable_sort(reqs.begin(), reqs.end(), [](const EvictReq& x, const EvictReq& y) { return x.n_keep > y.n_keep; });
+    for (size_t k = 0; k < reqs.size(); ++k) {
+        if (k % kEvictReqs == 0) launch_stage = 0;
+        else reqs[k].row_begin = reqs[k - 1].row_begin + reqs[k - 1].len;
+        reqs[k].stage = launch_stage;
+        launch_stage += reqs[k].n_keep;
+        most_stage = std::max(most_stage, launch_stage);
+    }
     if (p->q_tail - p->q_head + pages > g.num_pages)
         return bad("the requests hold more pages than the pool has free slots for: their tables were not filled from this pool");
     if (!p->d_lists) {

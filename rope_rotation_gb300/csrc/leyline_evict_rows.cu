@@ -121,20 +121,26 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
 
 // -------------------------------------------------------------------- move --
 constexpr int kChainThreads = 256;
-constexpr int kVecs = 8;         // 16-byte vectors of a thread in a batch
-constexpr int kBatchRows = 256;  // of a batch, at most
-// Batches whose slots are held: while a batch is written, slots of the next two are there, and a thread that is ahead
-// looks up those of the third.
-constexpr int kLists = 4;
+constexpr int kVecs = 8;                  // 16-byte vectors of a thread in a batch
+constexpr int kBatchRows = kChainThreads;  // of a batch, at most: a thread looks up one
+constexpr int kAhead = 2;                 // batches that are read before one is written
+constexpr int kDstLists = 8;
+static_assert(kAhead + 2 <= kDstLists, "slots are there from their look-up until they are written");
+
+struct ChainShared {
+    uint4 rows[kAhead][kVecs][kChainThreads];  // each thread's own vectors
+    long long src[2][kBatchRows], dst[kDstLists][kBatchRows];  // slots of a batch's rows, -1: none
+};
 
 // One chain: `slice` vectors of each row of one request in one layer, in batches of as many rows as the CTA's threads
-// hold.  The next batch is read before this one is written; the barrier between a batch's reads and its writes orders
-// them over the CTA.
+// hold.  Batches are read ahead (cp.async: a barrier waits for plain loads on their way): what a batch writes lies before
+// the sources of all later ones.  The barrier between a batch's reads and its writes orders them over the CTA.
 __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_constant__ EvictArgs a,
                                                                   const __grid_constant__ EvictSet set, int slices,
                                                                   int slice)
 {
-    __shared__ long long src_s[kLists][kBatchRows], dst_s[kLists][kBatchRows];
+    extern __shared__ __align__(16) unsigned char smem[];
+    ChainShared& sh = *reinterpret_cast<ChainShared*>(smem);
     wait_for_previous_grid();
     allow_next_grid();
     const Geometry& g = a.g;
@@ -143,66 +149,92 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
     const int layer = c / slices, first = (c - layer * slices) * slice;  // of the row's vectors
     const EvictReq& r = set.req[q];
     const ListState st = a.state[q];
-    const List kept = list_of(a, r, st);
-    const int width = min(slice, g.row_vecs - first);
+    const int32_t* kept = a.kept + (long long)r.list * a.kept_stride;  // (a bad list moves nothing)
+    const int32_t* table = a.table + (long long)r.req * a.max_blocks;
+    const int width = min(slice, g.row_vecs - first), B = g.block_size, tid = threadIdx.x;
     const int batch = min(kChainThreads * kVecs / width, kBatchRows);
-    const int todo = r.n_keep - st.hole;
-    const int batches = (todo + batch - 1) / batch;
-    const int B = g.block_size;
-    // slots of a batch's rows (-1: a bad page, the row is not moved)
-    auto look_up = [&](int b) {
-        if (b >= batches) return;
-        for (int i = threadIdx.x; i < batch; i += kChainThreads) {
-            const int row = st.hole + b * batch + i;
-            long long from = -1, to = -1;
-            if (row < r.n_keep) {
-                const int k = kept[row], fb = k / B, tb = row / B;
-                const int fp = page_at(a, r, fb), tp = page_at(a, r, tb);
-                if (fp >= 0 && tp >= 0) {
-                    from = (long long)fp * B + (k - fb * B);
-                    to = (long long)tp * B + (row - tb * B);
-                }
+    const int batches = (r.n_keep - st.hole + batch - 1) / batch;
+    // A thread looks up one row of each batch, each step a batch ahead of the next one: its place in the list, the pages of
+    // its source and of itself, their slots.
+    auto row_of = [&](int b) { return st.hole + b * batch + tid; };
+    auto has = [&](int b) { return tid < batch && row_of(b) < r.n_keep; };
+    auto ask_source = [&](int b) { return has(b) ? kept[row_of(b)] : 0; };
+    auto ask_pages = [&](int b, int k, int& from, int& to) {
+        if (!has(b)) return;
+        from = table[k / B];
+        to = table[row_of(b) / B];
+    };
+    auto settle = [&](int b, int k, int from_page, int to_page) {
+        if (tid >= batch) return;
+        long long from = -1, to = -1;
+        if (has(b)) {
+            if (from_page >= 0 && from_page < g.num_pages && to_page >= 0 && to_page < g.num_pages) {
+                from = (long long)from_page * B + k % B;
+                to = (long long)to_page * B + row_of(b) % B;
+            } else {
+                raise_status(a.status, ST_BAD_PAGE);
             }
-            src_s[b % kLists][i] = from;
-            dst_s[b % kLists][i] = to;
         }
+        sh.src[b & 1][tid] = from;
+        sh.dst[b % kDstLists][tid] = to;
     };
-    auto place = [&](long long slot, int v) -> uint4* {
-        return a.kv + (v < g.latent_vecs ? lat_off(g, layer, slot) + v : band_off(g, layer, slot) + (v - g.latent_vecs));
-    };
-    auto read = [&](int b, uint4 (&x)[kVecs]) {
-        if (b >= batches) return;
+    // A thread's vectors: of row `row[k]` of a batch the vector at `base[k]`, `pitch[k]` vectors from one slot to the next.
+    int row[kVecs], pitch[kVecs];
+    uint4* base[kVecs];
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int e = threadIdx.x + k * kChainThreads, i = e / width;
-            const long long from = i < batch ? src_s[b % kLists][i] : -1;
-            if (from >= 0) x[k] = ld_rw(place(from, first + e - i * width));
-        }
-    };
-    auto write = [&](int b, const uint4 (&x)[kVecs]) {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int e = threadIdx.x + k * kChainThreads, i = e / width;
-            const long long to = i < batch ? dst_s[b % kLists][i] : -1;
-            if (to >= 0) st_stream(place(to, first + e - i * width), x[k]);
-        }
-    };
-    uint4 even[kVecs], odd[kVecs];
-    look_up(0);
-    look_up(1);
-    __syncthreads();
-    read(0, even);
-    for (int b = 0; b < batches; b += 2) {
-        read(b + 1, odd);
-        look_up(b + 2);
-        __syncthreads();
-        write(b, even);
-        if (b + 1 == batches) break;
-        read(b + 2, even);
-        look_up(b + 3);
-        __syncthreads();
-        write(b + 1, odd);
+    for (int k = 0; k < kVecs; ++k) {
+        const int e = tid + k * kChainThreads, i = e / width, v = first + e - i * width;
+        const bool latent = v < g.latent_vecs;
+        row[k] = i < batch ? i : -1;
+        base[k] = a.kv + (latent ? lat_off(g, layer, 0) + v : band_off(g, layer, 0) + (v - g.latent_vecs));
+        pitch[k] = latent ? g.lat_row_vecs : g.rope_row_vecs;
     }
+    auto read = [&](int b) {
+        if (b < batches) {
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const long long from = row[k] >= 0 ? sh.src[b & 1][row[k]] : -1;
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(&sh.rows[b % kAhead][k][tid]);
+                if (from >= 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(base[k] + from * pitch[k]) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto write = [&](int b) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const long long to = row[k] >= 0 ? sh.dst[b % kDstLists][row[k]] : -1;
+            if (to >= 0) st_stream(base[k] + to * pitch[k], sh.rows[b % kAhead][k][tid]);
+        }
+    };
+    int from, to;
+    for (int b = 0; b < kAhead; ++b) {
+        const int k = ask_source(b);
+        ask_pages(b, k, from, to);
+        settle(b, k, from, to);
+        __syncthreads();
+        read(b);
+    }
+    {
+        const int k = ask_source(kAhead);
+        ask_pages(kAhead, k, from, to);
+        settle(kAhead, k, from, to);
+    }
+    int k1 = ask_source(kAhead + 1);
+    ask_pages(kAhead + 1, k1, from, to);
+    int k2 = ask_source(kAhead + 2);
+    for (int b = 0; b < batches; ++b) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncthreads();
+        write(b);
+        read(b + kAhead);
+        settle(b + kAhead + 1, k1, from, to);
+        k1 = k2;
+        ask_pages(b + kAhead + 2, k1, from, to);
+        k2 = ask_source(b + kAhead + 3);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ commit --
@@ -254,7 +286,10 @@ int launch_evict(const EvictArgs& a, const EvictSet& set, int sm_count, void* st
         e = launch_dependent(stage_kernel, grid_for(rows, kStageThreads, sm_count * 8), kStageThreads, s, a, set, rows);
     if (e == cudaSuccess && a.g.block_size > 1) {
         const int slice = 8, slices = (a.g.row_vecs + slice - 1) / slice;
-        e = launch_dependent(move_rows_kernel, set.n * a.g.num_layers * slices, kChainThreads, s, a, set, slices, slice);
+        e = cudaFuncSetAttribute(move_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainShared));
+        if (e == cudaSuccess)
+            e = launch_dependent_smem(move_rows_kernel, set.n * a.g.num_layers * slices, kChainThreads, sizeof(ChainShared), s, a,
+                                      set, slices, slice);
     }
     if (e == cudaSuccess)
         e = launch_dependent(commit_evict_kernel, grid_for(rows, kCommitThreads, sm_count * 16), kCommitThreads, s, a, set, rows);

@@ -4,13 +4,19 @@
 // up, and the rows at both ends: an ascending list.  Weights are compared as numbers: -0 equals 0, a NaN lies below
 // everything.
 //
-// Weights become 32-bit keys in their order.  The m-th greatest key is found digit by digit, from the top: a histogram
-// of the digit over the rows that share the digits found so far, and a sum over its bins from the greatest down.
+// Weights become 32-bit keys in their order.  The m-th greatest key is found by its digits, from the top: a histogram of the
+// digit over the rows that share the digits found so far, and a sum over its bins from the greatest down.  A cluster of CTAs
+// takes a request, each of them a run of its rows, which a thread holds in registers, 16 in a row; the histograms meet
+// through distributed shared memory, and the CTAs' counts of rows taken give each the place of its part of the list.
+#include <cooperative_groups.h>
+
 #include "leyline_device.cuh"
 #include "leyline_evict.h"
 
 namespace leyline {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // Keys in the order of the weights: 0 for a NaN, one key for both zeros.
 __device__ __forceinline__ uint32_t order_key(float w)
@@ -21,90 +27,199 @@ __device__ __forceinline__ uint32_t order_key(float w)
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kHeld = 16;  // rows of a thread
+constexpr int kSegment = kSelectThreads * kHeld;
+constexpr int kMostCtas = 8;  // of a cluster
+constexpr int kBins = 2048;
+// Shifts of the digits, of 11, 11 and 10 bits.
+__device__ __forceinline__ int shift_of(int digit) { return digit == 0 ? 21 : digit == 1 ? 10 : 0; }
 
-// Exclusive sum of x over the CTA's threads, and the total; scratch: 33 words.
-__device__ __forceinline__ int block_scan(int x, int* scratch, int& total)
+struct SelectShared {
+    alignas(16) uint32_t bins[3][kBins];
+    uint32_t scratch[33];
+    uint32_t found[2];
+    uint32_t taken[2];  // rows above the m-th greatest key, and of that key, of this CTA
+};
+
+// Inclusive sum of x over the CTA's threads; scratch[31] holds the total afterwards.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* scratch)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    int incl = x;
     for (int d = 1; d < 32; d *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
     }
     __syncthreads();  // scratch is free
-    if (lane == 31) scratch[warp] = incl;
+    if (lane == 31) scratch[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int s = lane < kSelectThreads / 32 ? scratch[lane] : 0;
+        uint32_t s = scratch[lane];
         for (int d = 1; d < 32; d *= 2) {
-            const int y = __shfl_up_sync(0xffffffffu, s, d);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
             if (lane >= d) s += y;
         }
         scratch[lane] = s;
     }
     __syncthreads();
-    total = scratch[kSelectThreads / 32 - 1];
-    return incl - x + (warp > 0 ? scratch[warp - 1] : 0);
+    return x + (warp > 0 ? scratch[warp - 1] : 0);
 }
 
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectArgs a,
                                                                 const __grid_constant__ EvictSet set)
 {
-    __shared__ int bins[256];
-    __shared__ int scratch[33];
-    __shared__ int found[2];
+    __shared__ SelectShared s;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ctas = cluster.num_blocks(), tid = threadIdx.x;
+    const EvictReq& r = set.req[blockIdx.x / ctas];
+    const float* w = a.weights + r.req * a.req_stride + r.first;
+    int32_t* kept = a.kept + (long long)r.list * a.kept_stride;
+    const int rows = r.len - r.last - r.first, m = r.n_keep - r.first - r.last;
+    // this CTA's rows [begin, end) of them, a thread's 16 (or as many as give every thread some) in a row
+    const int per = (rows + ctas - 1) / ctas, begin = min(rows, rank * per), end = min(rows, begin + per);
+    const int segments = (per + kSegment - 1) / kSegment;
+    const int held = segments > 1 ? kHeld : (per + kSelectThreads - 1) / kSelectThreads;
+    for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&s.bins[0][0])[i] = 0;
     wait_for_previous_grid();
     allow_next_grid();
-    const EvictReq r = set.req[blockIdx.x];
-    const float* w = a.weights + r.req * a.req_stride;
-    int32_t* kept = a.kept + (long long)r.list * a.kept_stride;
-    const int tid = threadIdx.x, end = r.len - r.last, m = r.n_keep - r.first - r.last;
+    uint32_t key[kHeld];
+    auto load = [&](int segment) {
+        const int at = begin + segment * kSegment + tid * held;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) key[k] = k < held && at + k < end ? order_key(w[at + k]) : 0;
+    };
+    auto count = [&](int segment) { return max(0, min(held, end - begin - segment * kSegment - tid * held)); };
+    load(0);
+    __syncthreads();
     uint32_t prefix = 0, mask = 0;
-    int want = m;  // rows still to be taken among those that share the prefix
-    for (int shift = 24; shift >= 0 && m > 0; shift -= 8) {
-        if (tid < 256) bins[tid] = 0;
-        __syncthreads();
-        for (int i = r.first + tid; i < end; i += kSelectThreads) {
-            const uint32_t k = order_key(w[i]);
-            if ((k & mask) == prefix) atomicAdd(&bins[k >> shift & 255], 1);
+    uint32_t want = m;  // rows still to be taken among those that share the prefix
+    for (int d = 0; d < 3 && m > 0; ++d) {
+        const int shift = shift_of(d);
+        const uint32_t bins_mask = d < 2 ? 2047u : 1023u;
+        for (int g = 0; g < segments; ++g) {
+            if (segments > 1) load(g);
+            const int n = count(g);
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                if (k >= held) break;
+                const bool on = k < n && (key[k] & mask) == prefix;
+                if (d == 0) {
+                    // the first digits of most weights are few: one count for the lanes that share a bin, where an atomic of
+                    // each of them took turns
+                    const uint32_t bin = on ? key[k] >> shift : kBins;
+                    const unsigned same = __match_any_sync(0xffffffffu, bin);
+                    if (on && (same & ((1u << (tid & 31)) - 1)) == 0) atomicAdd(&s.bins[0][bin], __popc(same));
+                } else if (on) {
+                    atomicAdd(&s.bins[d][key[k] >> shift & bins_mask], 1u);
+                }
+            }
+        }
+        cluster.sync();
+        // bins 2 tid and 2 tid + 1 from the greatest down, over all CTAs
+        const int bin = kBins - 2 - 2 * tid;
+        uint2 mine = make_uint2(0, 0);
+#pragma unroll
+        for (int c = 0; c < kMostCtas; ++c)
+            if (c < ctas) {
+                const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.bins[d][bin], c));
+                mine.x += x.x;
+                mine.y += x.y;
+            }
+        const uint32_t upto = block_scan(mine.x + mine.y, s.scratch), above = upto - mine.x - mine.y;
+        if (above < want && upto >= want) {
+            const bool upper = above + mine.y >= want;
+            s.found[0] = upper ? bin + 1 : bin;
+            s.found[1] = upper ? above : above + mine.y;
         }
         __syncthreads();
-        int total;
-        const int mine = tid < 256 ? bins[255 - tid] : 0;
-        const int above = block_scan(mine, scratch, total);
-        if (tid < 256 && above < want && above + mine >= want) {
-            found[0] = 255 - tid;
-            found[1] = above;
+        prefix |= s.found[0] << shift;
+        mask |= bins_mask << shift;
+        want -= s.found[1];
+    }
+    // `want` of the rows whose key is the m-th greatest, the lowest ones, and all above it
+    uint32_t above = 0, equal = 0;
+    for (int g = 0; g < segments && m > 0; ++g) {
+        if (segments > 1) load(g);
+        const int n = count(g);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            above += k < n && key[k] > prefix;
+            equal += k < n && key[k] == prefix;
         }
-        __syncthreads();
-        prefix |= (uint32_t)found[0] << shift;
-        mask |= 255u << shift;
-        want -= found[1];
-        __syncthreads();
     }
-    // `want` of the rows whose key is the m-th greatest, and all above it
-    for (int i = tid; i < r.first; i += kSelectThreads) kept[i] = i;
-    int taken = r.first, equal = 0;
-    for (int i0 = r.first; i0 < end && m > 0; i0 += kSelectThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < end ? order_key(w[i]) : 0;
-        const bool eq = i < end && k == prefix;
-        int n_eq, n_take;
-        const int before = block_scan(eq, scratch, n_eq);
-        const bool take = i < end && (k > prefix || (eq && equal + before < want));
-        const int at = block_scan(take, scratch, n_take);
-        if (take) kept[taken + at] = i;
-        taken += n_take;
-        equal += n_eq;
+    if (segments > 1) {  // (totals of the CTA; each segment's are found again below)
+        block_scan(above, s.scratch);
+        const uint32_t all = s.scratch[31];
+        block_scan(equal, s.scratch);
+        if (tid == 0) s.taken[0] = all, s.taken[1] = s.scratch[31];
+    } else {
+        const uint32_t both = block_scan(above << 16 | equal, s.scratch);  // (16384 rows of a CTA at most)
+        if (tid == 0) s.taken[0] = s.scratch[31] >> 16, s.taken[1] = s.scratch[31] & 0xffff;
+        above = (both >> 16) - above;
+        equal = (both & 0xffff) - equal;
     }
-    for (int i = tid; i < r.last; i += kSelectThreads) kept[r.n_keep - r.last + i] = end + i;
+    cluster.sync();
+    uint32_t above0 = 0, equal0 = 0;  // of the CTAs before
+    for (int c = 0; c < rank; ++c) {
+        above0 += *cluster.map_shared_rank(&s.taken[0], c);
+        equal0 += *cluster.map_shared_rank(&s.taken[1], c);
+    }
+    for (int g = 0; g < segments && m > 0; ++g) {
+        const int n = count(g);
+        if (segments > 1) {
+            load(g);
+            uint32_t x = 0, y = 0;
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                x += k < n && key[k] > prefix;
+                y += k < n && key[k] == prefix;
+            }
+            const uint32_t both = block_scan(x << 16 | y, s.scratch), all = s.scratch[31];
+            above = above0 + (both >> 16) - x;
+            equal = equal0 + (both & 0xffff) - y;
+            above0 += all >> 16;
+            equal0 += all & 0xffff;
+        } else {
+            above += above0;
+            equal += equal0;
+        }
+        const int at = r.first + begin + g * kSegment + tid * held;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            if (k >= n) break;
+            const bool is_above = key[k] > prefix, is_equal = key[k] == prefix;
+            if (is_above || (is_equal && equal < want)) kept[r.first + above + min(equal, want)] = at + k;
+            above += is_above;
+            equal += is_equal;
+        }
+    }
+    for (int i = rank * kSelectThreads + tid; i < r.first; i += ctas * kSelectThreads) kept[i] = i;
+    for (int i = rank * kSelectThreads + tid; i < r.last; i += ctas * kSelectThreads) kept[r.n_keep - r.last + i] = r.len - r.last + i;
+    cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 }  // namespace
 
 int launch_select(const SelectArgs& a, const EvictSet& set, void* stream)
 {
-    return (int)launch_dependent(select_kernel, set.n, kSelectThreads, (cudaStream_t)stream, a, set);
+    int longest = 0;
+    for (int k = 0; k < set.n; ++k) longest = std::max(longest, set.req[k].len);
+    // CTAs of a request: as few as leave a thread no more than 4 rows
+    int ctas = 1;
+    while (ctas < kMostCtas && longest > 4 * kSelectThreads * ctas) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(set.n * ctas));
+    cfg.blockDim = dim3((unsigned)kSelectThreads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return (int)cudaLaunchKernelEx(&cfg, select_kernel, a, set);
 }
 
 }  // namespace leyline
