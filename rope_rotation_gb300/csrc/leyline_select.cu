@@ -4,7 +4,7 @@
 // up, and the rows at both ends: an ascending list.  Weights are compared as numbers: -0 equals 0, a NaN lies below
 // everything.
 //
-// Weights become 32-bit keys in their order.  The m-th greatest key is found by its digits, from the top: a histogram of the
+// Weights become 32-bit keys in their order.  The m-th greatest key is found by its digits of 8 bits, from the top: a histogram of the
 // digit over the rows that share the digits found so far, and a sum over its bins from the greatest down.  A cluster of CTAs
 // takes a request, each of them a run of its rows, which a thread holds in registers, 16 in a row; the histograms meet
 // through distributed shared memory, and the CTAs' counts of rows taken give each the place of its part of the list.
@@ -30,14 +30,13 @@ constexpr int kSelectThreads = 1024;
 constexpr int kHeld = 16;  // rows of a thread
 constexpr int kSegment = kSelectThreads * kHeld;
 constexpr int kMostCtas = 8;  // of a cluster
-constexpr int kBins = 2048;
-// Shifts of the digits, of 11, 11 and 10 bits.
-__device__ __forceinline__ int shift_of(int digit) { return digit == 0 ? 21 : digit == 1 ? 10 : 0; }
+constexpr int kBins = 256;    // digits of 8 bits
+constexpr int kDigits = 4;
 
 struct SelectShared {
-    alignas(16) uint32_t bins[3][kBins];
+    alignas(16) uint32_t bins[kDigits][kBins];
     uint32_t scratch[33];
-    uint32_t found[2];
+    uint32_t found[3];  // digit, rows of greater ones, rows of this one
     uint32_t taken[2];  // rows above the m-th greatest key, and of that key, of this CTA
 };
 
@@ -78,7 +77,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     const int per = (rows + ctas - 1) / ctas, begin = min(rows, rank * per), end = min(rows, begin + per);
     const int segments = (per + kSegment - 1) / kSegment;
     const int held = segments > 1 ? kHeld : (per + kSelectThreads - 1) / kSelectThreads;
-    for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&s.bins[0][0])[i] = 0;
+    (&s.bins[0][0])[tid] = 0;
+    static_assert(kDigits * kBins == kSelectThreads, "a bin for each thread");
     wait_for_previous_grid();
     allow_next_grid();
     uint32_t key[kHeld];
@@ -92,9 +92,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     __syncthreads();
     uint32_t prefix = 0, mask = 0;
     uint32_t want = m;  // rows still to be taken among those that share the prefix
-    for (int d = 0; d < 3 && m > 0; ++d) {
-        const int shift = shift_of(d);
-        const uint32_t bins_mask = d < 2 ? 2047u : 1023u;
+    for (int d = 0; d < kDigits && m > 0; ++d) {
+        const int shift = 24 - 8 * d;
         for (int g = 0; g < segments; ++g) {
             if (segments > 1) load(g);
             const int n = count(g);
@@ -102,48 +101,67 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             for (int k = 0; k < kHeld; ++k) {
                 if (k >= held) break;
                 const bool on = k < n && (key[k] & mask) == prefix;
+                const uint32_t bin = on ? key[k] >> shift & 255u : kBins;
                 if (d == 0) {
                     // the first digits of most weights are few: one count for the lanes that share a bin, where an atomic of
                     // each of them took turns
-                    const uint32_t bin = on ? key[k] >> shift : kBins;
                     const unsigned same = __match_any_sync(0xffffffffu, bin);
                     if (on && (same & ((1u << (tid & 31)) - 1)) == 0) atomicAdd(&s.bins[0][bin], __popc(same));
                 } else if (on) {
-                    atomicAdd(&s.bins[d][key[k] >> shift & bins_mask], 1u);
+                    atomicAdd(&s.bins[d][bin], 1u);
                 }
             }
         }
-        cluster.sync();
-        // bins 2 tid and 2 tid + 1 from the greatest down, over all CTAs
-        const int bin = kBins - 2 - 2 * tid;
-        uint2 mine = make_uint2(0, 0);
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+        if (tid < 32) {  // 8 bins a lane from the greatest down, over all CTAs
+            const int first = kBins - 8 - 8 * tid;
+            uint32_t bin[8] = {};
 #pragma unroll
-        for (int c = 0; c < kMostCtas; ++c)
-            if (c < ctas) {
-                const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.bins[d][bin], c));
-                mine.x += x.x;
-                mine.y += x.y;
+            for (int c = 0; c < kMostCtas; ++c)
+                if (c < ctas) {
+                    const uint4* from = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.bins[d][first], c));
+                    const uint4 x = from[0], y = from[1];
+                    bin[0] += y.w, bin[1] += y.z, bin[2] += y.y, bin[3] += y.x;
+                    bin[4] += x.w, bin[5] += x.z, bin[6] += x.y, bin[7] += x.x;
+                }
+            uint32_t mine = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mine += bin[k];
+            uint32_t upto = mine;
+            for (int e = 1; e < 32; e *= 2) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, e);
+                if (tid >= e) upto += x;
             }
-        const uint32_t upto = block_scan(mine.x + mine.y, s.scratch), above = upto - mine.x - mine.y;
-        if (above < want && upto >= want) {
-            const bool upper = above + mine.y >= want;
-            s.found[0] = upper ? bin + 1 : bin;
-            s.found[1] = upper ? above : above + mine.y;
+            uint32_t before = upto - mine;
+            if (before < want && upto >= want) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (before < want && before + bin[k] >= want) {
+                        s.found[0] = first + 7 - k;
+                        s.found[1] = before;
+                        s.found[2] = bin[k];
+                    }
+                    before += bin[k];
+                }
+            }
         }
         __syncthreads();
         prefix |= s.found[0] << shift;
-        mask |= bins_mask << shift;
+        mask |= 255u << shift;
         want -= s.found[1];
+        if (s.found[2] == want) break;  // all rows of these digits are taken
+        __syncthreads();
     }
-    // `want` of the rows whose key is the m-th greatest, the lowest ones, and all above it
+    // `want` of the rows with the digits of the m-th greatest, the lowest ones, and all above them
     uint32_t above = 0, equal = 0;
     for (int g = 0; g < segments && m > 0; ++g) {
         if (segments > 1) load(g);
         const int n = count(g);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-            above += k < n && key[k] > prefix;
-            equal += k < n && key[k] == prefix;
+            above += k < n && (key[k] & mask) > prefix;
+            equal += k < n && (key[k] & mask) == prefix;
         }
     }
     if (segments > 1) {  // (totals of the CTA; each segment's are found again below)
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         above = (both >> 16) - above;
         equal = (both & 0xffff) - equal;
     }
-    cluster.sync();
+    if (ctas > 1) cluster.sync();
     uint32_t above0 = 0, equal0 = 0;  // of the CTAs before
     for (int c = 0; c < rank; ++c) {
         above0 += *cluster.map_shared_rank(&s.taken[0], c);
@@ -170,8 +188,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             uint32_t x = 0, y = 0;
 #pragma unroll
             for (int k = 0; k < kHeld; ++k) {
-                x += k < n && key[k] > prefix;
-                y += k < n && key[k] == prefix;
+                x += k < n && (key[k] & mask) > prefix;
+                y += k < n && (key[k] & mask) == prefix;
             }
             const uint32_t both = block_scan(x << 16 | y, s.scratch), all = s.scratch[31];
             above = above0 + (both >> 16) - x;
@@ -186,7 +204,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             if (k >= n) break;
-            const bool is_above = key[k] > prefix, is_equal = key[k] == prefix;
+            const bool is_above = (key[k] & mask) > prefix, is_equal = (key[k] & mask) == prefix;
             if (is_above || (is_equal && equal < want)) kept[r.first + above + min(equal, want)] = at + k;
             above += is_above;
             equal += is_equal;
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     }
     for (int i = rank * kSelectThreads + tid; i < r.first; i += ctas * kSelectThreads) kept[i] = i;
     for (int i = rank * kSelectThreads + tid; i < r.last; i += ctas * kSelectThreads) kept[r.n_keep - r.last + i] = r.len - r.last + i;
-    cluster.sync();  // no CTA leaves while another may read its counts
+    if (ctas > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 }  // namespace
