@@ -53,8 +53,8 @@ __device__ __forceinline__ Tile share_of(uint32_t rank, int key0, int end)
 }
 
 // Every role of both CTAs walks the pair's work in the same order (the loaders by a loop of their own): stay(u): the query
-// tile u of every band is to stay; unit(t, u): a product, t of this CTA's rows, of which there may be none; flush(r, t): the
-// tile's sums are complete; release(): the queries are no longer used.
+// tile u of every band is to stay; unit(t, u): a product, t of this CTA's rows, of which there may be none; tile(r, t), flush(r, t): the
+// tile's sums begin, and are complete; release(): the queries are no longer used.
 template <class Role>
 __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, uint32_t rank, Role& role)
 {
@@ -74,6 +74,7 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, uint32_
         const int end = (int)min((g_end - (long long)r.begin) * 32, (long long)r.end);
         for (int key0 = (int)(g - r.begin) * 32; key0 < end; key0 += kPairKeys) {
             const Tile t = share_of(rank, key0, end);
+            role.tile(r, t);
             for (u.band = 0; u.band < s.bands; ++u.band) role.unit(t, u);
             role.flush(r, t);
         }
@@ -138,6 +139,7 @@ struct Buffers {
 // What a warp has asked for by cp.async (rows that TMA does not take, the bands that are to be turned) and has not arrived
 // for: groups of copies, the oldest first.  They are waited for when the next ones are on their way.
 constexpr int kLanding = 3;
+constexpr int kQueries = 15;  // a group's kind: the queries
 constexpr int kTurnAfter = 2;  // steps of the next tile are asked for before a tile's bands are turned
 
 template <int kKeys>
@@ -153,7 +155,7 @@ struct Loader {
     uint32_t stay_phase = 0;
     // (In registers, a byte for each group: what lies in local memory comes from L2, next to all of shared memory.)
     int landing = 0;
-    uint32_t kinds = 0, gaps = 0;  // 16 * stage + (1 + 4 * first chunk + buffer of counts: bands, 0: rows); uses to the next one
+    uint32_t kinds = 0, gaps = 0;  // 16 * stage + (0: rows, 1 + 4 * first chunk + buffer of counts: bands), kQueries; uses to the next one
     int oldest_use = 0, newest_use = 0;
     int bands_read = 0;
 
@@ -173,14 +175,15 @@ struct Loader {
         else cp_async_wait<2>();
         __syncwarp();
         const int stage = (kinds & 255) / 16, what = (int)(kinds & 15) - 1;
-        if (what < 0) {
+        const bool queries = (kinds & 15) == kQueries;
+        if (what < 0 || queries) {
             fence_async_smem();
             __syncwarp();
         } else if constexpr (kKeys > 0) {
             const int c = what / 4;
             keys.turn_bands(c, c + kKeys / 2, kKeys > 1, stage_at(stage), t.turned * kAtomBytes, m->counts[what % 4] + 16 * keys.warp);
         }
-        if (keys.lane == 0) keys.arrive(smem_addr(&m->full[stage]));
+        if (keys.lane == 0) keys.arrive(smem_addr(queries ? &m->stay_full : &m->full[stage]));
         --landing;
         kinds >>= 8;
         oldest_use += gaps & 255;
@@ -206,10 +209,7 @@ struct Loader {
             for (int row = tid / 8; row < q_rows; row += 4 * kLoadWarps)
                 copy_query_row(keys.a, s, u, (int)keys.rank * q_rows + row, row, tid % 8, 0, s.q_chunks,
                                smem + u.band * s.q_chunks * pitch, pitch);
-        cp_async_wait_all();  // (no groups are in flight between requests)
-        fence_async_smem();
-        __syncwarp();
-        if (keys.lane == 0) keys.arrive(smem_addr(&m->stay_full));
+        land(uses, kQueries);  // (the keys are asked for meanwhile)
         return true;
     }
 
@@ -293,6 +293,7 @@ struct Issuer {
     }
     __device__ __forceinline__ void refuse() {}
     __device__ __forceinline__ void flush(const WeighReq&, const Tile&) {}
+    __device__ __forceinline__ void tile(const WeighReq&, const Tile&) {}
     __device__ __forceinline__ void stay(const Unit&) { wait(smem_addr(&m->stay_full), stay_phase); }
     __device__ __forceinline__ void release()
     {
@@ -359,6 +360,8 @@ struct Summer {
     int warp, lane;
     int open = 0;  // rows below it are attended to by every column
     float sum = 0.f;
+    int page = -1;  // of this thread's row of the tile, and its weight before
+    float before = 0.f;
 
     __device__ __forceinline__ void refuse()
     {
@@ -383,6 +386,14 @@ struct Summer {
     }
     __device__ __forceinline__ void release() {}
 
+    __device__ __forceinline__ void tile(const WeighReq& r, const Tile& t)
+    {
+        const int row = 32 * warp + lane;
+        page = -1;
+        if (row >= t.keys) return;
+        page = a.header->table[(long long)r.req * a.header->max_blocks + (t.key0 + row) / a.g.block_size];
+        before = a.decay == 0.f ? 0.f : a.weights[r.req * a.req_stride + t.key0 + row];
+    }
     __device__ __forceinline__ void unit(const Tile& t, const Unit& u)
     {
         mbar_wait_cluster(smem_addr(&m->s_full[buf.at]), buf.phase, &m->quit, a.status);
@@ -399,7 +410,9 @@ struct Summer {
     __device__ __forceinline__ void flush(const WeighReq& r, const Tile& t)
     {
         const int row = 32 * warp + lane;
-        if (row < t.keys && !*(volatile int*)&m->quit) store_weight(a, r, t.key0 + row, sum);
+        // (the loads have raised the status for a bad page)
+        if (row < t.keys && page >= 0 && page < a.g.num_pages && !*(volatile int*)&m->quit)
+            a.weights[r.req * a.req_stride + t.key0 + row] = a.decay == 0.f ? sum : fmaf(a.decay, before, sum);
         sum = 0.f;
     }
 };

@@ -543,32 +543,54 @@ def keep_batch(keeps) -> np.ndarray:
 
 def row_weights(t, what: str = "weights") -> RowWeights:
     """A view of an fp32 tensor [requests][rows] whose last axis is contiguous."""
-    import torch
     if t.requires_grad:
         _refuse_gradient(what)
-    if t.dtype != torch.float32:
+    if t.dtype != _fp32():
         raise ValueError(f"{what}: dtype {t.dtype}, expected torch.float32")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected [requests][rows] with a contiguous last axis")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if stride < t.shape[1]:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: expected [requests][rows]")
+    reqs, rows = shape
+    stride, inner = t.stride()
+    if inner != 1 and rows > 1:
+        raise ValueError(f"{what}: the last axis must be contiguous")
+    if reqs <= 1:  # the stride of an axis of one entry says nothing
+        stride = rows
+    elif stride < rows:
         raise ValueError(f"{what}: its requests' rows overlap")
-    return RowWeights(t.data_ptr(), stride, t.shape[1], t.shape[0])
+    return RowWeights(t.data_ptr(), stride, rows, reqs)
+
+
+def _fp32():
+    import torch
+    return torch.float32
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+def _address(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]  # (ndarray.ctypes makes an object for it)
 
 
 def _lists(kept, keeps: np.ndarray):
     """(address, stride) of an int32 tensor [>= entries][>= n_keep] whose last axis is contiguous."""
-    import torch
-    if kept.dtype != torch.int32:
+    if kept.dtype != _int32():
         raise ValueError(f"kept: dtype {kept.dtype}, expected torch.int32")
-    longest = int(keeps["n_keep"].max()) if keeps.size else 0
-    if kept.dim() != 2 or kept.shape[0] < keeps.size or kept.shape[1] < longest:
-        raise ValueError(f"kept: shape {tuple(kept.shape)}, expected [>= {keeps.size}][>= {longest}]")
-    if kept.shape[1] > 1 and kept.stride(1) != 1:
+    shape = kept.shape
+    longest = max(keeps["n_keep"].tolist(), default=0)
+    if len(shape) != 2 or shape[0] < keeps.size or shape[1] < longest:
+        raise ValueError(f"kept: shape {tuple(shape)}, expected [>= {keeps.size}][>= {longest}]")
+    stride, inner = kept.stride()
+    if inner != 1 and shape[1] > 1:
         raise ValueError("kept: the last axis must be contiguous")
-    if kept.shape[0] > 1 and kept.stride(0) < kept.shape[1]:
+    if shape[0] <= 1:
+        stride = shape[1]
+    elif stride < shape[1]:
         raise ValueError("kept: its lists overlap")
-    return kept.data_ptr(), kept.stride(0) if kept.shape[0] > 1 else kept.shape[1]
+    return kept.data_ptr(), stride
 
 
 def leyline_attention_weights(batch, layer: int, q_latent: Optional[Heads], q_rope: Heads, lse, weights, scale: float,
@@ -587,7 +609,7 @@ def leyline_select_rows(pool, tables: Tables, weights, keeps, kept, stream=None)
     a = keep_batch(keeps)
     w = row_weights(weights)
     ptr, stride = _lists(kept, a)
-    _check(load().leyline_select_rows(pool, ctypes.byref(tables.bt), ctypes.byref(w), a.ctypes.data, a.size, ptr, stride,
+    _check(load().leyline_select_rows(pool, ctypes.byref(tables.bt), ctypes.byref(w), _address(a), a.size, ptr, stride,
                                       _stream_ptr(stream)))
 
 
@@ -596,7 +618,7 @@ def leyline_evict(pool, tables: Tables, keeps, kept, weights=None, stream=None) 
     a = keep_batch(keeps)
     w = None if weights is None else row_weights(weights)
     ptr, stride = _lists(kept, a)
-    _check(load().leyline_evict(pool, ctypes.byref(tables.bt), a.ctypes.data, a.size, ptr, stride,
+    _check(load().leyline_evict(pool, ctypes.byref(tables.bt), _address(a), a.size, ptr, stride,
                                 None if w is None else ctypes.byref(w), _stream_ptr(stream)))
 
 
