@@ -128,17 +128,14 @@ __device__ __forceinline__ uint4 turned_pairs(bool naive, const uint4& mine, con
     return high;
 }
 
-// cos and sin of count * theta_j of `pairs` pairs to shared memory, by a warp.  Out of line: it is for a count that the warp
-// has not met before, and its sines would cost the loop around it registers.
-__device__ __noinline__ void trig_of(int count, const double* turn, int pairs, bool bf16, float2* cs)
+// cos and sin of count * theta_j of `pairs` pairs as a read of the pool forms them, rounded to bf16, by a warp.
+__device__ __noinline__ void naive_trig(int count, const double* turn, int pairs, float2* cs)
 {
-    __syncwarp();
     for (int j = threadIdx.x & 31; j < pairs; j += 32) {
         float c, s;
-        pending_trig(count, turn, pairs, j, bf16, c, s);
+        pending_trig(count, turn, pairs, j, true, c, s);
         cs[j] = make_float2(c, s);
     }
-    __syncwarp();
 }
 
 // --------------------------------------------------------------------- keys --
@@ -155,7 +152,8 @@ struct KeyLoader {
     const WeighArgs& a;
     const WeighMaps& maps;
     const Shape& s;
-    float2* cs;  // lazy pools: cos, sin of `count`, this warp's
+    float2* cs;           // lazy pools: cos, sin of `count`, this warp's
+    const double* turns;  // theta_j as a part of a whole turn
     int warp, lane;
     uint32_t rank;
     // of row kRows * warp + lane of the tile at `slot_key` of request `slot_req`: -1 where there is none
@@ -196,10 +194,26 @@ struct KeyLoader {
         next_req = r.req;
     }
 
+    // cos and sin of c * theta_j: the angle in turns in fp64, less its whole ones, then in fp32.  They are off by 2^-22 of the
+    // pair, where the scores carry a turned band to 2^-17.  (The product of the pool's two tables, in fp64, takes two loads
+    // from L2 for each pair, and every warp was held up by it wherever the count changed: 64 decodes of 16 heads over some
+    // 4000 rows, one a page, 163 us instead of 107.)
     __device__ __forceinline__ void ensure(int c)
     {
         if (counted && c == count) return;
-        trig_of(c, a.turn, 32 * kTurned, a.g.precision == LEYLINE_ROTATE_BF16_NAIVE, cs);
+        __syncwarp();
+        if (a.g.precision == LEYLINE_ROTATE_BF16_NAIVE) {
+            naive_trig(c, a.turn, 32 * kTurned, cs);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTurned; ++i) {
+                const double t = (double)c * turns[lane + 32 * i];
+                float si, co;
+                sincospif(2.f * (float)(t - rint(t)), &si, &co);
+                cs[lane + 32 * i] = make_float2(co, si);
+            }
+        }
+        __syncwarp();
         count = c;
         counted = true;
     }
@@ -359,6 +373,12 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t keys, int pitch, ui
 }
 
 // ----------------------------------------------------------------- epilogue --
+// Lazy pools: theta_j of a band's pairs as a part of a whole turn, to shared memory, by all threads.
+__device__ __forceinline__ void load_turns(const WeighArgs& a, int pairs, double* turns)
+{
+    for (int j = threadIdx.x; j < pairs; j += blockDim.x) turns[j] = a.turn[j] * 0.15915494309189533577;  // 1 / (2 pi)
+}
+
 // Whether x holds in one of kWarps warps, which meet here (barrier 1).
 template <int kWarps>
 __device__ __forceinline__ bool any_of_warps(bool x)

@@ -38,6 +38,7 @@ struct Misc {
     alignas(16) float neg[2][kCols];
     alignas(16) int limit[2][kCols];
     float half[kWeighKeys];  // sums over the second query tile's columns
+    double turns[128];
     int counts[kWeighKeys];
 };
 constexpr int kSmemBytes = kWeighSmem + (int)sizeof(Misc) + kLoadWarps * 128 * (int)sizeof(float2) + 1024;
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
         m->quit = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (kKeys > 0) load_turns(a, 32 * kKeys, m->turns);
     if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);
     tcgen05_before_sync();
     __syncthreads();
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{{a, maps, s, trig, w, lane, rank}, m, smem, m->counts + 32 * w, !queries.usable};
+        Loader<kKeys> role{{a, maps, s, trig, m->turns, w, lane, rank}, m, smem, m->counts + 32 * w, !queries.usable};
         walk(a, s, rank, role);
         cp_async_wait_all();
     }

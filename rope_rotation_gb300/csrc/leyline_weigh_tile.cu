@@ -35,6 +35,7 @@ struct Misc {
     uint32_t tmem;
     int quit;
     int least[kSumWarps];
+    double turns[128];
     int counts[4][kWeighKeys];  // lazy pools: pending turns of the rows whose bands are in flight
 };
 constexpr int kSmemBytes = kWeighSmem + (int)sizeof(Misc) + kLoadWarps * 128 * (int)sizeof(float2) + 1024;
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
         m->quit = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (kKeys > 0) load_turns(a, 32 * kKeys, m->turns);
     if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&m->tmem), kTmemCols);
     tcgen05_before_sync();
     __syncthreads();
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     } else {
         const int w = warp - kLoadWarp;
         float2* trig = reinterpret_cast<float2*>(base + kWeighSmem + sizeof(Misc)) + 128 * w;
-        Loader<kKeys> role{{a, maps, s, trig, w, lane, rank}, t, m, smem, q_rows, a.header->weigh_box};
+        Loader<kKeys> role{{a, maps, s, trig, m->turns, w, lane, rank}, t, m, smem, q_rows, a.header->weigh_box};
         role.run();
         cp_async_wait_all();
     }
