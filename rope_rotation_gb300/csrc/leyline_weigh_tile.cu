@@ -141,7 +141,6 @@ struct Buffers {
 // for: groups of copies, the oldest first.  They are waited for when the next ones are on their way.
 constexpr int kLanding = 3;
 constexpr int kQueries = 15;  // a group's kind: the queries
-constexpr int kTurnAfter = 2;  // steps of the next tile are asked for before a tile's bands are turned
 
 template <int kKeys>
 struct Loader {
@@ -175,7 +174,7 @@ struct Loader {
         else if (landing == 2) cp_async_wait<1>();
         else cp_async_wait<2>();
         __syncwarp();
-        const int stage = (kinds & 255) / 16, what = (int)(kinds & 15) - 1;
+        const int stage = (int)(kinds & 255) / 16, what = (int)(kinds & 15) - 1;
         const bool queries = (kinds & 15) == kQueries;
         if (what < 0 || queries) {
             fence_async_smem();
@@ -187,7 +186,7 @@ struct Loader {
         if (keys.lane == 0) keys.arrive(smem_addr(queries ? &m->stay_full : &m->full[stage]));
         --landing;
         kinds >>= 8;
-        oldest_use += gaps & 255;
+        oldest_use += (int)(gaps & 255);
         gaps >>= 8;
     }
     __device__ __forceinline__ void land(int use, int what)
@@ -218,19 +217,26 @@ struct Loader {
     __device__ __forceinline__ bool rows(const WeighReq& r, int key0, int end)
     {
         const Shape& s = keys.s;
+        const bool eager = !keys.copied() && t.row_steps > 0;
+        const int most = kKeys > 0 && keys.copied() ? 2 : kLanding;
         int step = 0;
         for (;;) {
-            // groups that are arrived for: all at the end, the oldest of kLanding and those whose stages are next, and
-            // bands when some steps of the next tile have been asked for, by when they have landed
-            while (landing > 0 && (key0 >= end || landing == kLanding || uses - oldest_use >= s.stages ||
-                                   (kKeys > 0 && step == kTurnAfter && !keys.copied())))
+            // Groups that are arrived for: all at the end, the oldest of `most` and those whose stages are next.  A product
+            // waits for a tile's turned bands, the last of its planes, so these go on as soon as they can: where TMA brings
+            // the other planes when the next tile's first are asked for (after two of them 128 us, after three 139, here 121:
+            // 16 decodes of 16 heads over some 24000 rows), else one group after another while the next stage is not free
+            // (64 decodes over some 4000 rows, one a page, 148 us without, here 129; rows that are not turned 84 without, 88
+            // with it).
+            const uint32_t empty = smem_addr(&m->empty[ring.stage]);
+            while (landing > 0 && (key0 >= end || landing == most || uses - oldest_use >= s.stages ||
+                                   (kKeys > 0 && (eager ? step == 1 : !__all_sync(0xffffffffu, mbar_test_cluster(empty, ring.phase ^ 1))))))
                 arrive_oldest();
             if (key0 >= end) return true;
             if (step == 0) {
                 keys.look_up(r, share_of(keys.rank, key0, end));
                 keys.look_ahead(r, share_of(keys.rank, key0 + kPairKeys, end));
             }
-            if (!wait(smem_addr(&m->empty[ring.stage]), ring.phase ^ 1)) return false;
+            if (!wait(empty, ring.phase ^ 1)) return false;
             const uint32_t dst = stage_at(ring.stage);
             const int band_step = step - t.row_steps;
             if (kKeys > 0 && band_step >= 0) {
