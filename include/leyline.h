@@ -274,7 +274,7 @@ int64_t leyline_free_page_count(const leyline_pool_t* pool);
  *     than were free at the checkpoint;
  *   - stored rope bands were turned in place since the checkpoint (a re-index
  *     splice of an eager pool, or leyline_materialize) or stored rows were written
- *     again (leyline_batch_plan), unless flags holds
+ *     again (leyline_batch_plan, leyline_evict), unless flags holds
  *     LEYLINE_ROLLBACK_ACCEPT_TURNED: the accounting is then restored but those
  *     bands stay turned and those rows as written (benchmark repeats, where the
  *     work and not the values matters).
@@ -601,7 +601,7 @@ int leyline_select_rows(leyline_pool_t* pool, const leyline_block_table_t* bt, c
  * LEYLINE_ROLLBACK_ACCEPT_TURNED.  Entries with n_keep equal to the length change nothing.  seq_lens_host and the
  * free-page count are updated at enqueue time; plans that name a request that lost rows no longer hold.
  * A list must ascend strictly within [0, length).  If it does not the status word says so, and the
- * request keeps its first n_keep rows instead.  Enqueues up to four kernels for 32 requests that lose rows.  The
+ * request keeps its first n_keep rows instead.  Enqueues up to three kernels for 32 requests that lose rows.  The
  * pool's staging buffer holds 8 bytes a kept row; the call waits for the pool's work when it has to grow.
  * Errors (nothing is enqueued or changed): INVALID_ARG (also when `stream` is being captured).  CUDA. */
 int leyline_evict(leyline_pool_t* pool, leyline_block_table_t* bt, const leyline_keep_t* keeps, int32_t n,

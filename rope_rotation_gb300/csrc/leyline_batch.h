@@ -12,6 +12,7 @@
 #include <utility>
 #include <vector>
 
+#include "leyline_evict.h"
 #include "leyline_internal.h"
 
 namespace leyline {

@@ -29,7 +29,7 @@ constexpr int kRowsPerWarp = 2;
 static_assert(kTileRows == (kMoveThreads / 32) * kRowsPerWarp, "tile shape");
 
 // device status bits (leyline_sync_status)
-enum : int32_t { ST_BAD_PAGE = 1, ST_BAD_BLOCK = 2, ST_BAD_FRESH = 4, ST_BAD_OLD = 8, ST_BAD_ROW = 64 };
+enum : int32_t { ST_BAD_PAGE = 1, ST_BAD_BLOCK = 2, ST_BAD_FRESH = 4, ST_BAD_OLD = 8 };
 
 __device__ __forceinline__ void raise_status(int32_t* status, int32_t bit) { atomicOr(status, bit); }
 

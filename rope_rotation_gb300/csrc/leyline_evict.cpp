@@ -126,7 +126,7 @@ int select_rows(leyline_pool_t* p, const leyline_block_table_t* bt, const leylin
         EvictSet set{};
         for (int32_t k = k0; k < std::min(n, k0 + kEvictReqs); ++k)
             set.req[set.n++] = EvictReq{keeps[k].req, keeps[k].n_keep, keeps[k].first, keeps[k].last,
-                                        (int32_t)bt->seq_lens_host[keeps[k].req], k, 0, 0, 0};
+                                        (int32_t)bt->seq_lens_host[keeps[k].req], k, 0, 0, 0, 0};
         int err = launch_select(a, set, stream);
         if (err != 0) return cuda_error((cudaError_t)err, "launching the selection kernel");
     }
@@ -155,7 +155,7 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     for (int32_t k = 0; k < n; ++k) {
         const int32_t len = (int32_t)bt->seq_lens_host[keeps[k].req];
         if (keeps[k].n_keep == len) continue;
-        reqs.push_back(EvictReq{keeps[k].req, keeps[k].n_keep, 0, 0, len, k, 0, 0, p->q_tail + pages});
+        reqs.push_back(EvictReq{keeps[k].req, keeps[k].n_keep, 0, 0, len, k, 0, 0, 0, p->q_tail + pages});
         pages += ceil_div(len, g.block_size) - ceil_div(keeps[k].n_keep, g.block_size);
     }
     if (reqs.empty()) return LEYLINE_OK;
@@ -163,7 +163,7 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     std::stable_sort(reqs.begin(), reqs.end(), [](const EvictReq& x, const EvictReq& y) { return x.n_keep > y.n_keep; });
     for (size_t k = 0; k < reqs.size(); ++k) {
         if (k % kEvictReqs == 0) launch_stage = 0;
-        else reqs[k].row_begin = reqs[k - 1].row_begin + reqs[k - 1].len;
+        else reqs[k].block_begin = reqs[k - 1].block_begin + (int32_t)ceil_div(reqs[k - 1].len, kStageRows);
         reqs[k].stage = launch_stage;
         launch_stage += reqs[k].n_keep;
         most_stage = std::max(most_stage, launch_stage);
@@ -171,7 +171,16 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     if (p->q_tail - p->q_head + pages > g.num_pages)
         return bad("the requests hold more pages than the pool has free slots for: their tables were not filled from this pool");
     if (!p->d_lists) {
-        cudaError_t e = cudaMalloc(&p->d_lists, sizeof(ListState) * kEvictReqs);
+        const std::vector<ListState> none(2 * kEvictReqs, ListState{0, INT32_MAX});
+        cudaError_t e = (cudaError_t)evict_prepare();
+        if (e == cudaSuccess) e = cudaMalloc(&p->d_lists, sizeof(ListState) * none.size());
+        if (e == cudaSuccess) {
+            e = cudaMemcpy(p->d_lists, none.data(), sizeof(ListState) * none.size(), cudaMemcpyHostToDevice);
+            if (e != cudaSuccess) {
+                cudaFree(p->d_lists);
+                p->d_lists = nullptr;
+            }
+        }
         if (e != cudaSuccess) return cuda_error(e, "allocating the lists' state");
     }
     const int64_t half = ceil_div(most_stage, 4) * 4;
@@ -188,7 +197,6 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     a.kept_stride = kept_stride;
     a.req_stride = w ? w->req_stride : 0;
     a.pending = p->d_pending;
-    a.state = p->d_lists;
     a.stage_i = p->d_stage;
     a.stage_w = reinterpret_cast<float*>(p->d_stage + half);
     a.status = p->d_status;
@@ -198,7 +206,10 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
         EvictSet set{};
         set.n = (int32_t)std::min<size_t>(kEvictReqs, reqs.size() - k0);
         std::copy(reqs.begin() + k0, reqs.begin() + k0 + set.n, set.req);
-        int err = launch_evict(a, set, p->sm_count, stream);
+        a.state = p->d_lists + p->lists_turn * kEvictReqs;
+        a.next_state = p->d_lists + (1 - p->lists_turn) * kEvictReqs;
+        p->lists_turn = 1 - p->lists_turn;
+        int err = launch_evict(a, set, stream);
         if (err != 0) return cuda_error((cudaError_t)err, "launching the eviction kernels");
     }
     rc = mark_done(p, stream);

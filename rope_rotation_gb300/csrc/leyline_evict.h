@@ -8,6 +8,10 @@
 
 namespace leyline {
 
+// Device status bit (leyline_sync_status), beside those of leyline_device.cuh: rows that a list must not name, or that the
+// weights do not hold.
+enum : int32_t { ST_BAD_ROW = 64 };
+
 // One request of a launch.
 struct EvictReq {
     int32_t req;      // table row
@@ -16,7 +20,8 @@ struct EvictReq {
     int32_t last;
     int32_t len;      // rows before the call
     int32_t list;     // row of the caller's array of lists
-    int64_t row_begin;   // evict: rows of the launch's requests before this one
+    int32_t block_begin; // evict: kStageRows-row blocks of the launch's requests before this one
+    int32_t pad;
     int64_t stage;       // evict: place of this request's kept rows in the staging arrays
     int64_t push;        // evict: ring position of the first page this request returns (mod q_cap)
 };
@@ -36,10 +41,13 @@ struct SelectArgs {
     int64_t kept_stride;
 };
 
-// What the check of a list found, in device memory, one for each request of a launch.
+constexpr int kStageRows = 256;
+
+// What the check of a list found, in device memory, one for each request of a launch.  Launches use two arrays of them in
+// turn: a launch's commit readies the other one.
 struct ListState {
     int32_t bad;   // not strictly ascending within [0, len): the first n_keep rows are kept instead
-    int32_t hole;  // first i with kept[i] != i (n_keep: none): rows before it stay where they are
+    int32_t hole;  // first i with kept[i] != i, or more than n_keep: rows before it stay where they are
 };
 
 struct EvictArgs {
@@ -54,6 +62,7 @@ struct EvictArgs {
     int64_t req_stride;
     int32_t* pending;      // lazy pools, else nullptr
     ListState* state;
+    ListState* next_state;
     // staged values of kept rows: weights, and pending turns or (one row a page) pages
     float* stage_w;
     int32_t* stage_i;
@@ -64,6 +73,7 @@ struct EvictArgs {
 
 // Each returns the cudaError_t of its launches as int.
 int launch_select(const SelectArgs& a, const EvictSet& set, void* stream);
-int launch_evict(const EvictArgs& a, const EvictSet& set, int sm_count, void* stream);
+int evict_prepare();  // before the first launch_evict
+int launch_evict(const EvictArgs& a, const EvictSet& set, void* stream);
 
 }  // namespace leyline

@@ -14,59 +14,7 @@
 namespace leyline {
 namespace {
 
-constexpr int kCheckThreads = 1024;
-
-// ------------------------------------------------------------------- check --
-// One CTA a request: whether its list ascends within [0, len), and the first row that moves.
-__global__ void __launch_bounds__(kCheckThreads) check_lists_kernel(const __grid_constant__ EvictArgs a,
-                                                                    const __grid_constant__ EvictSet set)
-{
-    __shared__ int hole;
-    wait_for_previous_grid();
-    allow_next_grid();
-    const EvictReq& r = set.req[blockIdx.x];
-    const int32_t* kept = a.kept + (long long)r.list * a.kept_stride;
-    if (threadIdx.x == 0) hole = r.n_keep;
-    __syncthreads();
-    bool bad = false;
-    int mine = r.n_keep;
-    for (int i = threadIdx.x; i < r.n_keep; i += kCheckThreads) {
-        const int k = kept[i];
-        bad |= k < 0 || k >= r.len || (i > 0 && kept[i - 1] >= k);
-        if (k != i) mine = min(mine, i);
-    }
-    if (mine < r.n_keep) atomicMin(&hole, mine);
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        a.state[blockIdx.x] = ListState{bad, bad ? r.n_keep : hole};
-        if (bad) raise_status(a.status, ST_BAD_ROW);
-    }
-}
-
 // ------------------------------------------------------------------- stage --
-struct List {
-    const int32_t* kept;
-    bool bad;
-    __device__ __forceinline__ int operator[](int i) const { return bad ? i : kept[i]; }
-};
-
-__device__ __forceinline__ List list_of(const EvictArgs& a, const EvictReq& r, const ListState& s)
-{
-    return List{a.kept + (long long)r.list * a.kept_stride, s.bad != 0};
-}
-
-// The request of row `row` of the launch's rows.
-__device__ __forceinline__ int req_of(const EvictSet& set, long long row)
-{
-    int lo = 0, hi = set.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (set.req[mid].row_begin <= row) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 __device__ __forceinline__ int page_at(const EvictArgs& a, const EvictReq& r, int blk)
 {
     const int page = a.table[(long long)r.req * a.max_blocks + blk];
@@ -75,48 +23,96 @@ __device__ __forceinline__ int page_at(const EvictArgs& a, const EvictReq& r, in
     return -1;
 }
 
-constexpr int kStageThreads = 256;
-
-// A thread for each row before the call: what moves of a kept row beside its rows goes to the staging arrays; with one
-// row a page, a dropped row's page goes back.
-__global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_constant__ EvictArgs a,
-                                                              const __grid_constant__ EvictSet set, long long rows)
+// The request of block `block` of kStageRows rows.
+__device__ __forceinline__ int req_of(const EvictSet& set, int block)
 {
+    int lo = 0, hi = set.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (set.req[mid].block_begin <= block) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The first of kept[0, n) that is not below `row`, by a warp: each step asks for 32 places at once.
+__device__ __forceinline__ int lower_bound(const int32_t* kept, int n, int row)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;  // what is below lo is below row, from hi on it is not
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && kept[at] < row);
+        const int count = below == 0 ? 0 : 32 - __clz(below);  // (of a list that does not ascend: any of them)
+        if (count == 0) return lo;
+        lo += (count - 1) * step + 1;
+        hi = min(hi, lo + step - 1);
+    }
+    return lo;
+}
+
+// A CTA for each kStageRows rows before the call.  The request's list is checked: whether it ascends within [0, len), and
+// where its first row is that moves.  What moves of a kept row beside its rows goes to the staging arrays, and with one row a
+// page a dropped row's page to the ring.  Nothing else is changed: after a bad list the commit does without all of it.
+__global__ void __launch_bounds__(kStageRows) stage_kernel(const __grid_constant__ EvictArgs a,
+                                                           const __grid_constant__ EvictSet set)
+{
+    __shared__ int mark[kStageRows], bounds[2], before[kStageRows / 32], hole;
     wait_for_previous_grid();
     allow_next_grid();
-    const int B = a.g.block_size;
-    for (long long x = blockIdx.x * (long long)kStageThreads + threadIdx.x; x < rows; x += (long long)gridDim.x * kStageThreads) {
-        const int q = req_of(set, x);
-        const EvictReq& r = set.req[q];
-        const List kept = list_of(a, r, a.state[q]);
-        const int row = (int)(x - r.row_begin);
-        if (B > 1) {
-            if (row >= r.n_keep) continue;
-            const int from = kept[row];
-            if (a.weights) a.stage_w[r.stage + row] = a.weights[r.req * a.req_stride + from];
-            if (a.pending) {
-                const int blk = from / B, page = page_at(a, r, blk);
-                a.stage_i[r.stage + row] = page < 0 ? 0 : a.pending[(long long)page * B + (from - blk * B)];
-            }
-            continue;
-        }
-        // kept rows before this one
-        int lo = 0, hi = r.n_keep;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (kept[mid] < row) lo = mid + 1;
-            else hi = mid;
-        }
-        const int page = a.table[(long long)r.req * a.max_blocks + row];
-        if (lo < r.n_keep && kept[lo] == row) {
-            a.stage_i[r.stage + lo] = page;
-            if (a.weights) a.stage_w[r.stage + lo] = a.weights[r.req * a.req_stride + row];
-            continue;
-        }
-        a.free_q[ring(r.push + (row - lo), a.q_cap)] = page;
-        if (page < 0 || page >= a.g.num_pages) raise_status(a.status, ST_BAD_PAGE);
-        else if (a.pending) a.pending[page] = 0;
+    const int q = req_of(set, blockIdx.x), tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    const EvictReq& r = set.req[q];
+    const int32_t* kept = a.kept + (long long)r.list * a.kept_stride;
+    const int row0 = (blockIdx.x - r.block_begin) * kStageRows, row = row0 + tid, B = a.g.block_size;
+    // this row's entry of the list
+    const int k = row < r.n_keep ? kept[row] : 0, last = row > 0 && row < r.n_keep ? kept[row - 1] : -1;
+    const bool bad = row < r.n_keep && (k < 0 || k >= r.len || last >= k);
+    if (tid == 0) hole = r.n_keep;
+    mark[tid] = -1;
+    if (B == 1 && warp < 2) {
+        const int bound = lower_bound(kept, r.n_keep, row0 + warp * kStageRows);
+        if (lane == 0) bounds[warp] = bound;
     }
+    __syncthreads();
+    if (row < r.n_keep && k != row) atomicMin(&hole, row);
+    if (B == 1) {
+        const int at = bounds[0] + tid;
+        if (at < bounds[1]) {
+            const int place = kept[at] - row0;
+            if (place >= 0 && place < kStageRows) mark[place] = at;
+        }
+    }
+    const bool any_bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        if (any_bad) atomicOr(&a.state[q].bad, 1);
+        if (hole < r.n_keep) atomicMin(&a.state[q].hole, hole);
+    }
+    if (B > 1) {
+        if (row >= r.n_keep || bad) return;
+        if (a.weights) a.stage_w[r.stage + row] = a.weights[r.req * a.req_stride + k];
+        if (a.pending) {
+            const int blk = k / B, page = page_at(a, r, blk);
+            a.stage_i[r.stage + row] = page < 0 ? 0 : a.pending[(long long)page * B + (k - blk * B)];
+        }
+        return;
+    }
+    const bool on = row < r.len;
+    const int at = on ? mark[tid] : -1;
+    const unsigned keeps = __ballot_sync(0xffffffffu, at >= 0);
+    if (lane == 0) before[warp] = __popc(keeps);
+    __syncthreads();
+    if (!on) return;
+    const int page = a.table[(long long)r.req * a.max_blocks + row];
+    if (page < 0 || page >= a.g.num_pages) raise_status(a.status, ST_BAD_PAGE);
+    if (at >= 0) {
+        a.stage_i[r.stage + at] = page;
+        if (a.weights) a.stage_w[r.stage + at] = a.weights[r.req * a.req_stride + row];
+        return;
+    }
+    int kept_before = bounds[0] + __popc(keeps & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) kept_before += before[w];
+    const int dropped = row - kept_before;  // (in range for a list that ascends)
+    if (dropped >= 0 && dropped < r.len - r.n_keep) a.free_q[ring(r.push + dropped, a.q_cap)] = page;
 }
 
 // -------------------------------------------------------------------- move --
@@ -148,7 +144,7 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
     const int q = blockIdx.x / per_req, c = blockIdx.x - q * per_req;
     const int layer = c / slices, first = (c - layer * slices) * slice;  // of the row's vectors
     const EvictReq& r = set.req[q];
-    const ListState st = a.state[q];
+    const ListState st{a.state[q].bad, a.state[q].bad ? r.n_keep : min(a.state[q].hole, r.n_keep)};
     const int32_t* kept = a.kept + (long long)r.list * a.kept_stride;  // (a bad list moves nothing)
     const int32_t* table = a.table + (long long)r.req * a.max_blocks;
     const int width = min(slice, g.row_vecs - first), B = g.block_size, tid = threadIdx.x;
@@ -238,61 +234,71 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ commit --
-__global__ void __launch_bounds__(kCommitThreads) commit_evict_kernel(const __grid_constant__ EvictArgs a,
-                                                                      const __grid_constant__ EvictSet set, long long rows)
+__global__ void __launch_bounds__(kStageRows) commit_evict_kernel(const __grid_constant__ EvictArgs a,
+                                                                  const __grid_constant__ EvictSet set)
 {
     wait_for_previous_grid();
     allow_next_grid();
-    const int B = a.g.block_size;
-    for (long long x = blockIdx.x * (long long)kCommitThreads + threadIdx.x; x < rows;
-         x += (long long)gridDim.x * kCommitThreads) {
-        const int q = req_of(set, x);
-        const EvictReq& r = set.req[q];
-        const int row = (int)(x - r.row_begin);
-        int32_t* table = a.table + (long long)r.req * a.max_blocks;
-        if (row == 0) a.seq_lens_dev[r.req] = r.n_keep;
-        if (a.weights) a.weights[r.req * a.req_stride + row] = row < r.n_keep ? a.stage_w[r.stage + row] : 0.f;
-        if (B == 1) {
-            table[row] = row < r.n_keep ? a.stage_i[r.stage + row] : -1;
-            continue;
+    if (blockIdx.x == 0 && threadIdx.x < kEvictReqs) a.next_state[threadIdx.x] = ListState{0, INT32_MAX};
+    const int q = req_of(set, blockIdx.x), B = a.g.block_size;
+    const EvictReq& r = set.req[q];
+    const int row = (blockIdx.x - r.block_begin) * kStageRows + threadIdx.x;
+    if (row >= r.len) return;
+    const bool bad = a.state[q].bad != 0;
+    int32_t* table = a.table + (long long)r.req * a.max_blocks;
+    if (row == 0) {
+        a.seq_lens_dev[r.req] = r.n_keep;
+        if (bad) raise_status(a.status, ST_BAD_ROW);
+    }
+    if (a.weights && (row >= r.n_keep || !bad))
+        a.weights[r.req * a.req_stride + row] = row < r.n_keep ? a.stage_w[r.stage + row] : 0.f;
+    if (B == 1) {
+        if (row >= r.n_keep) {  // of the pages that go back one each: those in the ring, or after a bad list the last ones
+            int32_t* back = a.free_q + ring(r.push + (row - r.n_keep), a.q_cap);
+            if (bad) *back = table[row];
+            const int page = *back;
+            if (a.pending && page >= 0 && page < a.g.num_pages) a.pending[page] = 0;
+            table[row] = -1;
+        } else if (!bad) {
+            table[row] = a.stage_i[r.stage + row];
         }
-        const int blk = row / B, keep_blocks = (r.n_keep + B - 1) / B;
-        if (row < r.n_keep && a.pending) {
-            const int page = page_at(a, r, blk);
-            if (page >= 0) a.pending[(long long)page * B + (row - blk * B)] = a.stage_i[r.stage + row];
-        }
-        // the first row of a block clears its dropped rows' turns, and gives its page back if all of them are
-        if (row != blk * B || (blk + 1) * (long long)B <= r.n_keep) continue;
+        return;
+    }
+    const int blk = row / B, keep_blocks = (r.n_keep + B - 1) / B;
+    if (row < r.n_keep && a.pending && !bad) {
         const int page = page_at(a, r, blk);
-        if (a.pending && page >= 0)
-            for (int i = max(r.n_keep - row, 0); i < min(B, r.len - row); ++i) a.pending[(long long)page * B + i] = 0;
-        if (blk >= keep_blocks) {
-            a.free_q[ring(r.push + (blk - keep_blocks), a.q_cap)] = page;
-            table[blk] = -1;
-        }
+        if (page >= 0) a.pending[(long long)page * B + (row - blk * B)] = a.stage_i[r.stage + row];
+    }
+    // the first row of a block clears its dropped rows' turns, and gives its page back if all of them are
+    if (row != blk * B || (blk + 1) * (long long)B <= r.n_keep) return;
+    const int page = page_at(a, r, blk);
+    if (a.pending && page >= 0)
+        for (int i = max(r.n_keep - row, 0); i < min(B, r.len - row); ++i) a.pending[(long long)page * B + i] = 0;
+    if (blk >= keep_blocks) {
+        a.free_q[ring(r.push + (blk - keep_blocks), a.q_cap)] = page;
+        table[blk] = -1;
     }
 }
 
 }  // namespace
 
-int launch_evict(const EvictArgs& a, const EvictSet& set, int sm_count, void* stream)
+int evict_prepare()
+{
+    return (int)cudaFuncSetAttribute(move_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainShared));
+}
+
+int launch_evict(const EvictArgs& a, const EvictSet& set, void* stream)
 {
     cudaStream_t s = (cudaStream_t)stream;
     const EvictReq& back = set.req[set.n - 1];
-    const long long rows = back.row_begin + back.len;
-    cudaError_t e = launch_dependent(check_lists_kernel, set.n, kCheckThreads, s, a, set);
-    if (e != cudaSuccess) return (int)e;
-    if (a.g.block_size == 1 || a.weights || a.pending)
-        e = launch_dependent(stage_kernel, grid_for(rows, kStageThreads, sm_count * 8), kStageThreads, s, a, set, rows);
+    const int blocks = back.block_begin + (back.len + kStageRows - 1) / kStageRows;
+    cudaError_t e = launch_dependent(stage_kernel, blocks, kStageRows, s, a, set);
     if (e == cudaSuccess && a.g.block_size > 1) {
         const int slice = 8, slices = (a.g.row_vecs + slice - 1) / slice;
-        e = cudaFuncSetAttribute(move_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainShared));
-        if (e == cudaSuccess)
-            e = launch_dependent_smem(move_rows_kernel, set.n * a.g.num_layers * slices, kChainThreads, sizeof(ChainShared), s, a,
-                                      set, slices, slice);
+        e = launch_dependent_smem(move_rows_kernel, set.n * a.g.num_layers * slices, kChainThreads, sizeof(ChainShared), s, a, set,
+                                  slices, slice);
     }
-    if (e == cudaSuccess)
-        e = launch_dependent(commit_evict_kernel, grid_for(rows, kCommitThreads, sm_count * 16), kCommitThreads, s, a, set, rows);
+    if (e == cudaSuccess) e = launch_dependent(commit_evict_kernel, blocks, kStageRows, s, a, set);
     return (int)e;
 }
 

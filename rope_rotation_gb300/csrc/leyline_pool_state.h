@@ -59,7 +59,8 @@ struct leyline_pool {
     int reindex_blocks_per_sm = 1;
     int32_t move_kernel = 0;  // MoveKernel used by this pool
     int32_t* d_stage = nullptr;  // staged table entries of re-index calls, staged values of evictions
-    leyline::ListState* d_lists = nullptr;  // evictions: what the check of the lists found
+    leyline::ListState* d_lists = nullptr;  // evictions: what the check of the lists found, two arrays used in turn
+    int lists_turn = 0;
     int32_t* d_pending = nullptr;  // lazy: pending turns per slot
     double* d_theta_j = nullptr;   // lazy: the readers' turn table (layout at kTurnSpan)
     size_t d_stage_cap = 0;      // entries

@@ -416,19 +416,34 @@ __device__ __forceinline__ Column column_of(const WeighArgs& a, const Shape& s, 
 
 // sum over `n` columns (a multiple of 16) of exp2(x * scale2 + neg), of this thread's TMEM lane from `tmem` on; where
 // `masked`, of those alone whose limit lies above `key`, and of the columns below `cols` in any case (what lies behind
-// them may be anything).
+// them may be anything).  x is the sum of kParts accumulators, `pitch` TMEM columns apart.
+template <int kParts = 1>
 __device__ __forceinline__ float sum_columns(uint32_t tmem, int n, int cols, float scale2, const float* neg, const int* limit,
-                                             int key, bool masked)
+                                             int key, bool masked, int pitch = 0)
 {
+    constexpr int kBlocks = kParts > 1 ? 1 : 2;  // of 16 columns at a time
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    for (int c1 = 0; c1 < n; c1 += 32) {
+    for (int c1 = 0; c1 < n; c1 += 16 * kBlocks) {
         uint32_t v[2][16];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-            if (c1 + 16 * b < n) tmem_ld16(tmem + c1 + 16 * b, v[b]);
+            if (kParts > 1 || c1 + 16 * b < n) tmem_ld16(tmem + c1 + (kParts > 1 ? b * pitch : 16 * b), v[b]);
         tmem_wait_ld();
+        auto add_to = [](uint32_t* x, const uint32_t* y) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) + __uint_as_float(y[k]));
+        };
+        if (kParts > 1) add_to(v[0], v[1]);
+        if (kParts > 2) {
+            uint32_t w[2][16];
+            tmem_ld16(tmem + c1 + 2 * pitch, w[0]);
+            if (kParts > 3) tmem_ld16(tmem + c1 + 3 * pitch, w[1]);
+            tmem_wait_ld();
+            if (kParts > 3) add_to(w[0], w[1]);
+            add_to(v[0], w[0]);
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
             const int c0 = c1 + 16 * b;
             if (c0 >= n) break;
             const bool some = masked || c0 + 16 > cols;

@@ -21,7 +21,7 @@ namespace {
 constexpr int kSumWarps = 4, kMmaWarp = kSumWarps, kLoadWarp = kMmaWarp + 1, kLoadWarps = 8;
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kBuffers = 8;  // of S^T, 4 where they have more than 64 columns
+constexpr int kBuffers = 8;  // of S^T, at most
 
 // Barriers marked (first) are used in the first CTA alone; the others in both.
 struct Misc {
@@ -120,13 +120,23 @@ __device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps&
 }
 
 // The buffers of S^T, used in turn: with two of them grouped rows, whose bands have a product each, waited for their sums.
+// A buffer is of several accumulators, each for a part of the key's chunks: the tensor cores cut each step's sum off toward
+// zero, so an accumulator's error grows with its steps and with what it has come to, and the 36 steps of an MLA key in one
+// took the weights of a decode 1.2e-6 off (relative, 2-norm), next to MMA_ERR in four of them, which cost no time
+// where HBM bounds the kernel.  A band alone, of at most 16 steps, has one.
 struct Buffers {
-    int cols, count;
+    int cols, chunks, parts, count;  // chunks: of a part
     int at = 0;
     uint32_t phase = 0;
 
-    __device__ __forceinline__ explicit Buffers(int c) : cols(c), count(c > 64 ? 4 : kBuffers) {}
-    __device__ __forceinline__ uint32_t column() const { return at * cols; }
+    __device__ __forceinline__ Buffers(int c, const Shape& s) : cols(c)
+    {
+        const int most = s.latent == 0 ? 1 : c > 64 ? 2 : 4;
+        chunks = (s.chunks + most - 1) / most;
+        parts = (s.chunks + chunks - 1) / chunks;
+        count = min(kBuffers, (int)kTmemCols / (c * parts));
+    }
+    __device__ __forceinline__ uint32_t column() const { return at * cols * parts; }
     __device__ __forceinline__ void advance()
     {
         if (++at == count) {
@@ -320,7 +330,9 @@ struct Issuer {
     __device__ __forceinline__ void unit(const Tile&, const Unit& u)
     {
         if (!wait(smem_addr(&m->s_empty[buf.at]), buf.phase ^ 1)) return;
-        const uint32_t d = tmem + buf.column(), full = smem_addr(&m->s_full[buf.at]);
+        uint32_t d = tmem + buf.column();  // the accumulator
+        int summed = 0;                    // its chunks so far
+        const uint32_t full = smem_addr(&m->s_full[buf.at]);
         buf.advance();
         const uint32_t desc = mma_desc(kPairKeys, 2 * q_rows, false, false);
         const uint32_t queries = smem + u.band * s.q_chunks * q_rows * 128;
@@ -333,13 +345,18 @@ struct Issuer {
             const int count = t.count(step), n = min(count - plane, s.chunks - done);
             if (elect_lane()) {
                 const uint32_t at = smem + s.stay_bytes + ring.stage * t.stage_bytes;
-                for (int i = 0; i < n; ++i)
-                    product(d, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc,
-                                   done + i > 0);
+                uint32_t to = d;
+                for (int i = 0, c = summed; i < n; ++i) {
+                    product(to, at + (plane + i) * kAtomBytes, t.pitch(step), queries + query_chunk(plane + i) * q_rows * 128, desc, c > 0);
+                    if (++c < buf.chunks) continue;
+                    c = 0;
+                    to += buf.cols;
+                }
                 if (plane + n == count) pair_commit(smem_addr(&m->empty[ring.stage]));
                 if (done + n == s.chunks) pair_commit(full);
             }
             __syncwarp();
+            for (summed += n; summed >= buf.chunks; summed -= buf.chunks) d += buf.cols;
             done += n;
             plane += n;
             if (plane < count) continue;
@@ -405,9 +422,17 @@ struct Summer {
     {
         mbar_wait_cluster(smem_addr(&m->s_full[buf.at]), buf.phase, &m->quit, a.status);
         tcgen05_after_sync();
-        if (32 * warp < t.keys)
-            sum += sum_columns(tmem + buf.column() + ((uint32_t)(32 * warp) << 16), padded(u.cols), u.cols, a.scale * kLog2e,
-                               neg + u.band * cols, limit + u.band * cols, t.key0 + 32 * warp + lane, t.key0 + t.keys > open);
+        if (32 * warp < t.keys) {
+            const uint32_t at = tmem + buf.column() + ((uint32_t)(32 * warp) << 16);
+            const int n = padded(u.cols), key = t.key0 + 32 * warp + lane;
+            const bool masked = t.key0 + t.keys > open;
+            const float scale2 = a.scale * kLog2e, *l = neg + u.band * cols;
+            const int* end = limit + u.band * cols;
+            sum += buf.parts == 4   ? sum_columns<4>(at, n, u.cols, scale2, l, end, key, masked, cols)
+                   : buf.parts == 3 ? sum_columns<3>(at, n, u.cols, scale2, l, end, key, masked, cols)
+                   : buf.parts == 2 ? sum_columns<2>(at, n, u.cols, scale2, l, end, key, masked, cols)
+                                    : sum_columns(at, n, u.cols, scale2, l, end, key, masked);
+        }
         tcgen05_before_sync();
         __syncwarp();
         if (lane == 0) cluster_arrive_smem(cluster_addr(smem_addr(&m->s_empty[buf.at]), 0));
@@ -465,13 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
-        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, Buffers(cols),
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, Buffers(cols, s),
                     rank, warp, lane};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
         if (rank == 0) {
-            Issuer role{a, s, t, m, smem, tmem, q_rows, Buffers(cols)};
+            Issuer role{a, s, t, m, smem, tmem, q_rows, Buffers(cols, s)};
             walk(a, s, rank, role);
             // nothing is in flight when TMEM is freed
             if (elect_lane()) pair_commit(smem_addr(&m->drained));

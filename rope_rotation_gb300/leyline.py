@@ -531,14 +531,16 @@ KEEP_DTYPE = np.dtype([("req", "<i4"), ("n_keep", "<i4"), ("first", "<i4"), ("la
 def keep_batch(keeps) -> np.ndarray:
     """keeps: (req, n_keep) or (req, n_keep, first, last) of each request (first, last: 0), or a KEEP_DTYPE
     array, which is taken as it is."""
-    if isinstance(keeps, np.ndarray) and keeps.dtype == KEEP_DTYPE:
+    if isinstance(keeps, np.ndarray) and (keeps.dtype is KEEP_DTYPE or keeps.dtype == KEEP_DTYPE):
         if keeps.ndim != 1 or not keeps.flags.c_contiguous:
             raise ValueError("arrays of what is kept must be 1-D and contiguous")
         return keeps
-    keeps = [tuple(k) for k in keeps]
-    if any(len(k) not in (2, 4) for k in keeps):
-        raise ValueError("an entry is (req, n_keep) or (req, n_keep, first, last)")
-    return np.array([k if len(k) == 4 else (*k, 0, 0) for k in keeps], dtype=KEEP_DTYPE)
+    flat = []
+    for k in keeps:
+        if len(k) not in (2, 4):
+            raise ValueError("an entry is (req, n_keep) or (req, n_keep, first, last)")
+        flat += k if len(k) == 4 else (*k, 0, 0)
+    return np.array(flat, dtype=np.int32).view(KEEP_DTYPE)
 
 
 def row_weights(t, what: str = "weights") -> RowWeights:

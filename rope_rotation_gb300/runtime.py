@@ -164,8 +164,8 @@ class PagedCache:
         a = leyline.keep_batch(keeps)
         if out is None:
             with self.allocating(stream):
-                out = self.torch.full((a.size, int(a["n_keep"].max()) if a.size else 0), -1, dtype=self.torch.int32,
-                                      device=self.kv.device)
+                longest = min(max(int(a["n_keep"].max()), 0), self.table.shape[1] * self.block_size) if a.size else 0
+                out = self.torch.full((a.size, longest), -1, dtype=self.torch.int32, device=self.kv.device)
         leyline.leyline_select_rows(self.pool, self.tables, self._on_device(weights, "weights"), a,
                                     self._on_device(out, "out"), self._stream(stream))
         return out

@@ -182,6 +182,25 @@ def test_weigh_many_query_rows(heads, tokens, length, kw):
     cache.close()
 
 
+@pytest.mark.parametrize("latent", [64, 128, 192, 256, 320, 448, 512])
+@pytest.mark.parametrize("rope,flags", [(64, 0), (128, 0), (64, LAZY), (128, LAZY)])
+def test_weigh_keys_of_few_columns(latent, rope, flags):
+    """Keys of 2 to 12 blocks of 64 columns, by 16 to 128 query rows."""
+    lens = [300, 31, 1]
+    cache = BH.make_cache(lens, seed=21, layers=1, latent=latent, rope=rope, flags=flags)
+    if cache.pending() is not None:
+        cache.pending().random_(-300, 300)
+    for heads in (16, 40, 72, 128):
+        b = cache.batch(3, 3, heads)
+        chunks = [(r, n - 1, 1) for r, n in enumerate(lens)]
+        b.plan(chunks)
+        ql, q = queries(cache, 3, heads, seed=22)
+        lse = 3 + torch.randn(3, heads, device="cuda")
+        check_weigh(cache, b, 0, chunks, ql, q, lse, 0.07, fresh_weights(cache, seed=1), 0.5, what=f"{latent} {rope} {heads}")
+        b.close()
+    cache.close()
+
+
 @pytest.mark.parametrize("kw", [{}, dict(B=1), dict(flags=LAZY), dict(rope=128, bands=4), dict(latent=64, rope=16)])
 def test_weigh_rows_that_hold_nothing(kw):
     """NaN and infinities in rows that no token attends to reach no other row's weight; a query row without an lse adds
@@ -295,6 +314,47 @@ def test_weigh_captured_and_replayed(kw):
             with torch.cuda.graph(torch.cuda.CUDAGraph()):
                 x += 1
                 b.attention_weights(0, ql, q, lse, 0.05, small)
+    b.close()
+    cache.close()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(rope=128, bands=4), dict(latent=64, rope=16)])
+@pytest.mark.parametrize("tokens", [1, 80])
+def test_weigh_replayed_for_another_table(kw, tokens):
+    """Weights that do not hold a replayed plan's requests or rows: those requests' are left as they were."""
+    from rope_rotation_gb300 import leyline
+    from rope_rotation_gb300.leyline import LeylineError
+    cache = BH.make_cache([400, 90], extra=200, seed=17, layers=1, **kw)
+    heads = 8 * cache.rope_heads
+    b = cache.batch(4, 300, heads)
+    ql, q = queries(cache, 300, heads, seed=10)
+    lse = 3 + torch.randn(300, heads, device="cuda")
+    rows = cache.table.shape[1] * cache.block_size
+    w = torch.rand(3, rows, device="cuda")  # the last row is not the weights'
+    view = w[:2]
+    b.plan([(0, 399, 1)])
+    b.attention_weights(0, ql, q, lse, 0.05, view)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.attention_weights(0, ql, q, lse, 0.05, view)
+    # of the same pool, with longer requests and more of them: their pages are those of the first table, again and again
+    blocks = cache.table.shape[1]
+    more = leyline.Tables(torch.cat([cache.table, cache.table[:1].expand(2, -1)]).repeat(1, 2).contiguous(),
+                          torch.zeros(4, dtype=torch.int32, device="cuda"), np.array([400, 90, 300, 300], dtype=np.int64))
+    more.table[:, blocks:] = cache.table[0, :1]
+    more.table[:, :blocks][more.table[:, :blocks] < 0] = cache.table[0, 0]
+    more.seq_lens_host[0] = rows + 50
+    chunks = [(0, rows + 50 - tokens, tokens), (2, 300 - tokens, tokens), (1, 90 - tokens, tokens)]
+    leyline.leyline_batch_plan(b.handle, more, leyline.chunk_batch(chunks), leyline.current_stream_ptr(0))
+    want = w.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    with pytest.raises(LeylineError) as e:
+        cache.check_status()
+    assert e.value.code == -8
+    assert torch.equal(w[[0, 2]], want[[0, 2]]) and torch.equal(w[1, 90:], want[1, 90:])
+    assert bool((w[1, :90] > want[1, :90]).any())
     b.close()
     cache.close()
 
@@ -732,6 +792,23 @@ def test_evict_refusals_and_bad_lists():
         assert len(ids) == 0
         full.close()
         cache.close()
+
+
+@pytest.mark.parametrize("B", [16, 1])
+def test_evict_after_bad_lists(B):
+    """What is found of a call's lists says nothing of the next ones', of fewer requests or of more."""
+    from rope_rotation_gb300.leyline import LeylineError
+    rng = np.random.default_rng(9)
+    lens = [60] * 40
+    cache = BH.make_cache(lens, seed=16, layers=1, B=B, latent=64, rope=16)
+    lists = torch.zeros(40, 50, dtype=torch.int32, device="cuda")  # none of them ascends
+    cache.evict([(r, 50) for r in range(40)], lists)
+    with pytest.raises(LeylineError):
+        cache.check_status()
+    for reqs, n in (([3], 45), (range(40), 40), ([7, 8], 30), (range(20), 25), ([5], 20), (range(40), 15)):
+        reqs = [int(r) for r in reqs if cache.seq_lens_host[r] >= n]
+        check_evict(cache, [(r, n) for r in reqs], [pick(rng, int(cache.seq_lens_host[r]), n) for r in reqs], what=f"{B} {n}")
+    cache.close()
 
 
 def test_evict_and_the_page_accounting():
