@@ -35,10 +35,19 @@ constexpr int kDigits = 4;
 
 struct SelectShared {
     alignas(16) uint32_t bins[kDigits][kBins];
+    alignas(16) uint32_t total[kBins];  // over the cluster
     uint32_t scratch[33];
     uint32_t found[3];  // digit, rows of greater ones, rows of this one
-    uint32_t taken[2];  // rows above the m-th greatest key, and of that key, of this CTA
+    uint2 taken;  // rows above the m-th greatest key, and of that key, of this CTA
 };
+
+// *p if `on`, else NaN.  Without a branch: behind one a load waited for the one before it to be used.
+__device__ __forceinline__ float load_if(bool on, const float* p)
+{
+    float x = __int_as_float(0x7fffffff);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}" : "+f"(x) : "l"(p), "r"((uint32_t)on) : "memory");
+    return x;
+}
 
 // Inclusive sum of x over the CTA's threads; scratch[31] holds the total afterwards.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* scratch)
@@ -84,8 +93,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     uint32_t key[kHeld];
     auto load = [&](int segment) {
         const int at = begin + segment * kSegment + tid * held;
+        float x[kHeld];
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) key[k] = k < held && at + k < end ? order_key(w[at + k]) : 0;
+        for (int k = 0; k < kHeld; ++k) x[k] = load_if(k < held && at + k < end, w + at + k);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) key[k] = order_key(x[k]);
     };
     auto count = [&](int segment) { return max(0, min(held, end - begin - segment * kSegment - tid * held)); };
     load(0);
@@ -112,19 +124,24 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
                 }
             }
         }
-        if (ctas > 1) cluster.sync();
-        else __syncthreads();
-        if (tid < 32) {  // 8 bins a lane from the greatest down, over all CTAs
-            const int first = kBins - 8 - 8 * tid;
-            uint32_t bin[8] = {};
+        const uint32_t* sums = s.bins[d];
+        if (ctas > 1) {
+            cluster.sync();
+            if (tid < kBins) {  // (a lane's 8 bins of each CTA in turn, by the warp below, took a round trip for each CTA)
+                uint32_t x[kMostCtas], all = 0;
 #pragma unroll
-            for (int c = 0; c < kMostCtas; ++c)
-                if (c < ctas) {
-                    const uint4* from = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.bins[d][first], c));
-                    const uint4 x = from[0], y = from[1];
-                    bin[0] += y.w, bin[1] += y.z, bin[2] += y.y, bin[3] += y.x;
-                    bin[4] += x.w, bin[5] += x.z, bin[6] += x.y, bin[7] += x.x;
-                }
+                for (int c = 0; c < kMostCtas; ++c) x[c] = *cluster.map_shared_rank(&s.bins[d][tid], c < ctas ? c : 0);
+#pragma unroll
+                for (int c = 0; c < kMostCtas; ++c) all += c < ctas ? x[c] : 0;
+                s.total[tid] = all;
+            }
+            sums = s.total;
+        }
+        __syncthreads();
+        if (tid < 32) {  // 8 bins a lane from the greatest down
+            const int first = kBins - 8 - 8 * tid;
+            const uint4 x = *reinterpret_cast<const uint4*>(sums + first), y = *reinterpret_cast<const uint4*>(sums + first + 4);
+            const uint32_t bin[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
             uint32_t mine = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) mine += bin[k];
@@ -168,18 +185,24 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         block_scan(above, s.scratch);
         const uint32_t all = s.scratch[31];
         block_scan(equal, s.scratch);
-        if (tid == 0) s.taken[0] = all, s.taken[1] = s.scratch[31];
+        if (tid == 0) s.taken = make_uint2(all, s.scratch[31]);
     } else {
         const uint32_t both = block_scan(above << 16 | equal, s.scratch);  // (16384 rows of a CTA at most)
-        if (tid == 0) s.taken[0] = s.scratch[31] >> 16, s.taken[1] = s.scratch[31] & 0xffff;
+        if (tid == 0) s.taken = make_uint2(s.scratch[31] >> 16, s.scratch[31] & 0xffff);
         above = (both >> 16) - above;
         equal = (both & 0xffff) - equal;
     }
-    if (ctas > 1) cluster.sync();
     uint32_t above0 = 0, equal0 = 0;  // of the CTAs before
-    for (int c = 0; c < rank; ++c) {
-        above0 += *cluster.map_shared_rank(&s.taken[0], c);
-        equal0 += *cluster.map_shared_rank(&s.taken[1], c);
+    if (ctas > 1) {
+        cluster.sync();
+        uint2 x[kMostCtas - 1];
+#pragma unroll
+        for (int c = 0; c < kMostCtas - 1; ++c) x[c] = *cluster.map_shared_rank(&s.taken, c < rank ? c : rank);
+#pragma unroll
+        for (int c = 0; c < kMostCtas - 1; ++c) {
+            above0 += c < rank ? x[c].x : 0;
+            equal0 += c < rank ? x[c].y : 0;
+        }
     }
     for (int g = 0; g < segments && m > 0; ++g) {
         const int n = count(g);

@@ -120,10 +120,10 @@ __device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps&
 }
 
 // The buffers of S^T, used in turn: with two of them grouped rows, whose bands have a product each, waited for their sums.
-// A buffer is of several accumulators, each for a part of the key's chunks: the tensor cores cut each step's sum off toward
-// zero, so an accumulator's error grows with its steps and with what it has come to, and the 36 steps of an MLA key in one
-// took the weights of a decode 1.2e-6 off (relative, 2-norm), next to MMA_ERR in four of them, which cost no time
-// where HBM bounds the kernel.  A band alone, of at most 16 steps, has one.
+// A buffer is of several accumulators, each for a part of the key's chunks: an accumulator's error grows with its steps and
+// with what it has come to (as that of sums cut off toward zero would), and the 36 steps of an MLA key in one took the weights
+// of one token 1.2e-6 off 64 bits (2-norm, relative), next to 4e-7 in three.  The time is the same: 16 decodes of 128
+// heads over some 24000 rows 104 us with one and with two.  A band alone, of at most 16 steps, has one.
 struct Buffers {
     int cols, chunks, parts, count;  // chunks: of a part
     int at = 0;

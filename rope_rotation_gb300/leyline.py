@@ -573,10 +573,6 @@ def _int32():
     return torch.int32
 
 
-def _address(a: np.ndarray) -> int:
-    return a.__array_interface__["data"][0]  # (ndarray.ctypes makes an object for it)
-
-
 def _lists(kept, keeps: np.ndarray):
     """(address, stride) of an int32 tensor [>= entries][>= n_keep] whose last axis is contiguous."""
     if kept.dtype != _int32():
@@ -611,7 +607,7 @@ def leyline_select_rows(pool, tables: Tables, weights, keeps, kept, stream=None)
     a = keep_batch(keeps)
     w = row_weights(weights)
     ptr, stride = _lists(kept, a)
-    _check(load().leyline_select_rows(pool, ctypes.byref(tables.bt), ctypes.byref(w), _address(a), a.size, ptr, stride,
+    _check(load().leyline_select_rows(pool, ctypes.byref(tables.bt), ctypes.byref(w), a.ctypes.data, a.size, ptr, stride,
                                       _stream_ptr(stream)))
 
 
@@ -620,7 +616,7 @@ def leyline_evict(pool, tables: Tables, keeps, kept, weights=None, stream=None) 
     a = keep_batch(keeps)
     w = None if weights is None else row_weights(weights)
     ptr, stride = _lists(kept, a)
-    _check(load().leyline_evict(pool, ctypes.byref(tables.bt), _address(a), a.size, ptr, stride,
+    _check(load().leyline_evict(pool, ctypes.byref(tables.bt), a.ctypes.data, a.size, ptr, stride,
                                 None if w is None else ctypes.byref(w), _stream_ptr(stream)))
 
 
