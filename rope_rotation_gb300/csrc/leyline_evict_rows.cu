@@ -8,12 +8,6 @@
 // pages, so that a full pool can be edited: kept[i] >= i, and a CTA that takes the rows in order may write row i once
 // it has read row kept[i], since every row it has still to read lies behind.  Such a chain of rows is kept to one CTA
 // for each (request, layer, slice of a row's columns), and the chains run side by side.
-//
-// What bounds it is HBM with pieces of 128 bytes: half of 32768 rows of 27 layers kept in 192 us for one request and 667 for
-// four, 90% of 16 requests of some 8000 rows of 4 layers, lazy, in 239 (0.78, 0.90 and 0.83 of the measured copy rate, with
-// the two small kernels around it).  With few layers it is a chain's latency, 1.4 us a batch of rows whatever its size: one
-// layer of the first 96 us.  Slices of 64 bytes then take 90 us, but 243 for 27 layers, and of 256 bytes 274.  One row a page,
-// 16 requests of some 24000 rows: 17 us, the latency of two kernels.
 #include "leyline_device.cuh"
 #include "leyline_evict.h"
 
@@ -126,24 +120,17 @@ constexpr int kChainThreads = 256;
 constexpr int kVecs = 8;                  // 16-byte vectors of a thread in a batch
 constexpr int kBatchRows = kChainThreads;  // of a batch, at most: a thread looks up one
 constexpr int kAhead = 2;                 // batches that are read before one is written
-constexpr int kDstLists = 4;
+constexpr int kDstLists = 8;
 static_assert(kAhead + 2 <= kDstLists, "slots are there from their look-up until they are written");
-// Batches by which a look-up's steps come before its rows are read, each with time for the loads of the one before to land
-// (kAhead, as the rows'): a row's place in the list, the pages of its source and of itself, their slots.
-constexpr int kSlotAhead = 1, kPageAhead = kSlotAhead + kAhead, kListAhead = kPageAhead + kAhead;
-constexpr int kLists = 8, kPages = 4;
-static_assert(kListAhead - kSlotAhead < kLists && kPageAhead - kSlotAhead < kPages, "what is looked up stays until it is used");
 
 struct ChainShared {
     uint4 rows[kAhead][kVecs][kChainThreads];  // each thread's own vectors
     long long src[2][kBatchRows], dst[kDstLists][kBatchRows];  // slots of a batch's rows, -1: none
-    int kept[kLists][kBatchRows], from[kPages][kBatchRows], to[kPages][kBatchRows];  // a thread looks up its own row
 };
 
 // One chain: `slice` vectors of each row of one request in one layer, in batches of as many rows as the CTA's threads
-// hold.  Batches are read ahead: what a batch writes lies before the sources of all later ones.  All loads are cp.async, since a
-// barrier waits for plain ones on their way (with the look-ups by plain loads 4 requests of 32768 rows in 27 layers, to half,
-// 731 us instead of 667).  The barrier between a batch's reads and its writes orders them over the CTA.
+// hold.  Batches are read ahead (cp.async: a barrier waits for plain loads on their way): what a batch writes lies before
+// the sources of all later ones.  The barrier between a batch's reads and its writes orders them over the CTA.
 __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_constant__ EvictArgs a,
                                                                   const __grid_constant__ EvictSet set, int slices,
                                                                   int slice)
@@ -163,25 +150,20 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
     const int width = min(slice, g.row_vecs - first), B = g.block_size, tid = threadIdx.x;
     const int batch = min(kChainThreads * kVecs / width, kBatchRows);
     const int batches = (r.n_keep - st.hole + batch - 1) / batch;
-    // a thread looks up one row of each batch
+    // A thread looks up one row of each batch, each step a batch ahead of the next one: its place in the list, the pages of
+    // its source and of itself, their slots.
     auto row_of = [&](int b) { return st.hole + b * batch + tid; };
     auto has = [&](int b) { return tid < batch && row_of(b) < r.n_keep; };
-    auto ask = [](int* to, const int32_t* from) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-    };
-    auto ask_source = [&](int b) {
-        if (has(b)) ask(&sh.kept[b % kLists][tid], kept + row_of(b));
-    };
-    auto ask_pages = [&](int b) {
+    auto ask_source = [&](int b) { return has(b) ? kept[row_of(b)] : 0; };
+    auto ask_pages = [&](int b, int k, int& from, int& to) {
         if (!has(b)) return;
-        ask(&sh.from[b % kPages][tid], table + sh.kept[b % kLists][tid] / B);
-        ask(&sh.to[b % kPages][tid], table + row_of(b) / B);
+        from = table[k / B];
+        to = table[row_of(b) / B];
     };
-    auto settle = [&](int b) {
+    auto settle = [&](int b, int k, int from_page, int to_page) {
         if (tid >= batch) return;
         long long from = -1, to = -1;
         if (has(b)) {
-            const int k = sh.kept[b % kLists][tid], from_page = sh.from[b % kPages][tid], to_page = sh.to[b % kPages][tid];
             if (from_page >= 0 && from_page < g.num_pages && to_page >= 0 && to_page < g.num_pages) {
                 from = (long long)from_page * B + k % B;
                 to = (long long)to_page * B + row_of(b) % B;
@@ -204,14 +186,16 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
         pitch[k] = latent ? g.lat_row_vecs : g.rope_row_vecs;
     }
     auto read = [&](int b) {
-        if (b >= batches) return;
+        if (b < batches) {
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const long long from = row[k] >= 0 ? sh.src[b & 1][row[k]] : -1;
-            const uint32_t to = (uint32_t)__cvta_generic_to_shared(&sh.rows[b % kAhead][k][tid]);
-            if (from >= 0)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(base[k] + from * pitch[k]) : "memory");
+            for (int k = 0; k < kVecs; ++k) {
+                const long long from = row[k] >= 0 ? sh.src[b & 1][row[k]] : -1;
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(&sh.rows[b % kAhead][k][tid]);
+                if (from >= 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(base[k] + from * pitch[k]) : "memory");
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto write = [&](int b) {
 #pragma unroll
@@ -220,34 +204,33 @@ __global__ void __launch_bounds__(kChainThreads) move_rows_kernel(const __grid_c
             if (to >= 0) st_stream(base[k] + to * pitch[k], sh.rows[b % kAhead][k][tid]);
         }
     };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    auto wait_all = [] { asm volatile("cp.async.wait_all;" ::: "memory"); };
-    for (int b = 0; b < kAhead + kListAhead; ++b) ask_source(b);
-    wait_all();
-    for (int b = 0; b < kAhead + kPageAhead; ++b)
-        if (b < kPages) ask_pages(b);
-    wait_all();
+    int from, to;
     for (int b = 0; b < kAhead; ++b) {
-        settle(b);
+        const int k = ask_source(b);
+        ask_pages(b, k, from, to);
+        settle(b, k, from, to);
         __syncthreads();
         read(b);
-        commit();
     }
-    static_assert(kAhead == 2 && kPages == 4, "the first batches' pages");
-    ask_pages(4);
-    wait_all();
-    settle(kAhead);
+    {
+        const int k = ask_source(kAhead);
+        ask_pages(kAhead, k, from, to);
+        settle(kAhead, k, from, to);
+    }
+    int k1 = ask_source(kAhead + 1);
+    ask_pages(kAhead + 1, k1, from, to);
+    int k2 = ask_source(kAhead + 2);
     for (int b = 0; b < batches; ++b) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         __syncthreads();
         write(b);
         read(b + kAhead);
-        settle(b + kAhead + kSlotAhead);
-        ask_pages(b + kAhead + kPageAhead);
-        ask_source(b + kAhead + kListAhead);
-        commit();
+        settle(b + kAhead + 1, k1, from, to);
+        k1 = k2;
+        ask_pages(b + kAhead + 2, k1, from, to);
+        k2 = ask_source(b + kAhead + 3);
     }
-    wait_all();
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ commit --
