@@ -6,7 +6,8 @@
 // lse -inf attends to nothing and adds nothing.
 //
 // A warp takes a cache row, whose key lies in its lanes' registers, and meets the query rows one after another, so the
-// sum has one order.
+// sum has one order.  The products on the CUDA cores bound it: one token each of 16 requests over 4000 rows takes 640 us with
+// 8 bands of 96 and 32 heads, 445 with 16 heads over latents of 448 and a band of 96 (and 22 on the tensor cores with 512 + 64).
 #include "leyline_attention_any.cuh"
 
 namespace leyline {

@@ -11,6 +11,12 @@
 // whatever its size, so boxes of one plane of 16 rows, 72 for 128 MLA rows, bound the kernel.  The pairs take equal shares
 // of 32 rows.
 //
+// What bounds it is HBM: 16 requests decode over some 24000 rows in 95 us with 16 heads, 97 with 64, 105 with 128 (0.88 to
+// 0.79 of the measured copy rate; the products 40 us of it); rows that are copied one by one (one a page) 110.  With few rows
+// it is the chain of waits of one tile, page, keys, products, sums: one request of 4096 rows 10 us, half of it the call's.
+// Grouped rows have a product and sums of 32 columns for each band of 256 rows, 16 requests of some 8000 rows 45 us, 0.56 of
+// the copy rate; lazy pools turn every band again, 64 decodes over some 4000 rows, one a page, 134 us.
+//
 // Roles in each CTA: warps 0-3 sum, warp 4 issues the products (in the first CTA alone), warps 5-12 load, 16 rows of a plane
 // each.
 #include "leyline_weigh.cuh"
