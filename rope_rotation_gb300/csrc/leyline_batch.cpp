@@ -55,7 +55,7 @@ struct leyline_batch {
     bool many_parts = false;  // it splits a tile into more than kFewParts
     int32_t weigh_req = -1;   // its highest request, and the most rows one of them has weighed
     int64_t weigh_rows = 0;
-    int32_t weigh_tiles = 0, weigh_mode = kAnyRows;  // its header's
+    int32_t weigh_tiles = 0, weigh_stay = 0, weigh_reqs = 0;  // its header's
     int32_t table_reqs = 0;   // of its block table
     int64_t table_rows = 0;
 };
@@ -343,13 +343,17 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     b->n_tokens = (int32_t)cp.tokens;
     b->n_joins = split.n_joins;
     b->pairs = pairs;
-    b->weigh_req = cp.weigh.empty() ? -1 : cp.weigh.back().req;
     b->weigh_tiles = hd.weigh_tiles;
-    b->weigh_mode = hd.weigh_mode;
+    b->weigh_stay = hd.weigh_stay;
+    b->weigh_reqs = hd.weigh_reqs;
     b->table_reqs = bt->num_reqs;
     b->table_rows = (int64_t)bt->max_blocks * p->g.block_size;
+    b->weigh_req = -1;
     b->weigh_rows = 0;
-    for (const WeighReq& r : cp.weigh) b->weigh_rows = std::max(b->weigh_rows, r.end);
+    for (const WeighReq& r : cp.weigh) {
+        b->weigh_req = std::max(b->weigh_req, r.req);
+        b->weigh_rows = std::max(b->weigh_rows, r.end);
+    }
     b->many_parts = false;
     for (int32_t j = 0; j < split.n_joins; ++j) b->many_parts |= split.joins[j].parts > kFewParts;
     return LEYLINE_OK;
@@ -614,11 +618,11 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.status = p->d_status;
     a.g = g;
     a.part = b->d_weigh_part;
-    // a captured call may be replayed with plans for either kernel, and with plans that cut as many query tiles as any
+    // a captured call may be replayed with plans for either kernel or both, and with plans that cut as many query tiles as any
     int err = 0;
     if (!b->weigh_shape.tiles) err = launch_weigh(a, p->sm_count, stream);
-    else if (captured || b->weigh_mode == kQueriesStay) err = launch_weigh_tile(a, b->weigh_maps, b->weigh_shape.pairs, stream);
-    if (err == 0 && b->weigh_shape.tiles && (captured || b->weigh_mode == kKeysStay))
+    else if (captured || b->weigh_stay > 0) err = launch_weigh_tile(a, b->weigh_maps, b->weigh_shape.pairs, stream);
+    if (err == 0 && b->weigh_shape.tiles && (captured || b->weigh_stay < b->weigh_reqs))
         err = launch_weigh_pair(a, b->weigh_maps, room, b->weigh_shape.pairs,
                                 captured ? kWeighItems * b->weigh_shape.pairs : b->weigh_tiles, stream);
     if (err != 0) return cuda_error((cudaError_t)err, "launching the weighing kernel");

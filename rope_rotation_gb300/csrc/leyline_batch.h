@@ -34,18 +34,18 @@ struct BatchHeader {
     int32_t n_tokens;
     int32_t n_joins;
     int32_t pairs;  // attention by pairs of CTAs (leyline_attention_pair.cu)
-    int32_t weigh_reqs;   // requests of the plan, one WeighReq each
-    int32_t weigh_mode;   // WeighMode
-    int64_t weigh_work;   // their work, in its mode's unit
-    int32_t weigh_cols;   // kQueriesStay: query rows of a band, padded to a multiple of 32, at most
-    int32_t weigh_seg;    // kKeysStay: products of an item
-    int32_t weigh_tiles;  // kKeysStay: tiles of cache rows whose query tiles are cut into several items
-    int32_t weigh_box;    // kQueriesStay: index of weigh_planes
+    // The weights that queries give to rows: one WeighReq for each request of the plan.  First those whose queries stay while
+    // keys pass (leyline_weigh_tile.cu, work in units of 32 rows), then the others: their keys stay while queries pass
+    // (leyline_weigh_pair.cu, items), or they are rows that the tensor cores do not take (leyline_weigh.cu, rows).
+    int32_t weigh_reqs;
+    int32_t weigh_stay;       // of them, those whose queries stay
+    int64_t weigh_stay_work;
+    int64_t weigh_work;       // of the others
+    int32_t weigh_cols;   // queries stay: query rows of a band, padded to a multiple of 32, at most
+    int32_t weigh_box;    // queries stay: index of weigh_planes
+    int32_t weigh_seg;    // keys stay: products of an item
+    int32_t weigh_tiles;  // keys stay: tiles of cache rows whose query tiles are cut into several items
 };
-
-// How the weights that queries give to rows are computed, and a unit of its work: by leyline_weigh.cu a row, by
-// leyline_weigh_tile.cu 32 rows, by leyline_weigh_pair.cu an item.
-enum WeighMode : int32_t { kAnyRows = 0, kQueriesStay = 1, kKeysStay = 2 };
 
 // One chunk, as attention sees it.
 struct ChunkDev {
@@ -87,8 +87,8 @@ struct WeighReq {
     int32_t req;
     int32_t chunk;   // its chunk with the lowest start; the others follow by ChunkDev::next
     int64_t end;     // rows [0, end)
-    int64_t begin;   // work of the requests before it
-    int32_t units;   // kKeysStay: products of a tile of cache rows, each of two query tiles, of all bands
+    int64_t begin;   // work of the requests of its kind before it
+    int32_t units;   // keys stay: products of a tile of cache rows, each of two query tiles, of all bands
     int32_t segs;    // items they are cut into
     int32_t part;    // place of its first item's sums, if they are cut
     int32_t tile;    // tiles that are cut, of the requests before it
@@ -167,6 +167,10 @@ constexpr int32_t weigh_tokens(int32_t group) { return group >= kWeighCols ? 1 :
 // Items of a pair that query tiles are cut for, and the fewest products of an item.
 constexpr int32_t kWeighItems = 8;
 constexpr int32_t kWeighMinSeg = 4;
+// Where queries of some requests stay and of others pass there are two kernels to launch: with as many tiles of the first for
+// each pair.  16 tokens of 16 heads over 8192 rows beside 12, 20 and 40 decodes over 4000 (192, 320 and 640 tiles for 76
+// pairs): 27, 39 and 65 us by one kernel, 33, 41 and 55 by two; 4 bands, 256 tokens and drafts of 4: 79, 100, 146 and 81, 88, 101.
+constexpr int32_t kWeighSplit = 4;
 // Planes of 64 columns that pass together where queries stay (one TMA box for 16 rows): as many as leave enough stages.
 constexpr int32_t weigh_planes(int32_t box, bool mla) { return box == 2 ? (mla ? 3 : 4) : box + 1; }
 constexpr int32_t kWeighBoxes = 3;
@@ -186,12 +190,13 @@ struct WeighShape {
     int32_t band_chunks = 1;
     bool lazy = false;
 };
-// Fills in the requests' work and the header's part of it; at most 2 * kWeighItems * pairs items have sums of their own.
 // Bytes of the queries that stay in a CTA, half of their rows, and of what all of them are given.
 constexpr int64_t stay_bytes(int64_t bands, int64_t q_chunks, int64_t rows)
 {
     return bands * q_chunks * rows / 2 * 128 + (bands * rows * 8 + 1023) / 1024 * 1024;
 }
+// Fills in the requests' work and the header's part of it, the requests whose queries stay first; at most 2 * kWeighItems *
+// pairs items have sums of their own.
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
 
 struct HeadsView {

@@ -255,59 +255,68 @@ void split_work(const WorkShape& w, const std::vector<ChunkDev>& chunks, Split* 
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header)
 {
     header->weigh_reqs = (int32_t)reqs->size();
-    header->weigh_mode = kAnyRows;
-    header->weigh_work = 0;
+    header->weigh_stay = 0;
+    header->weigh_stay_work = header->weigh_work = 0;
     header->weigh_cols = header->weigh_seg = header->weigh_tiles = header->weigh_box = 0;
-    int64_t most = 0;   // query rows of a request and band
-    int64_t units = 0;  // products of all tiles of cache rows
-    bool single = true;
-    if (w.tiles && w.group > 0) {
-        const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
+    if (!w.tiles || w.group <= 0) {
         for (WeighReq& r : *reqs) {
-            int64_t n = 0;
-            for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) {
-                const int64_t tiles = ceil_div(chunks[c].n, tokens) * blocks;
-                single &= tiles == 1 && chunks[c].next < 0;
-                n += ceil_div(tiles, 2);
-                most = std::max(most, (int64_t)chunks[c].n * w.group);
-            }
-            single &= n == 1;
-            r.units = (int32_t)(n * w.bands);
-            units += n * w.bands * ceil_div(r.end, kPairKeys);
+            r.begin = header->weigh_work;
+            header->weigh_work += r.end;
         }
-        const int64_t cols = ceil_div(most, 32) * 32, stay = stay_bytes(w.bands, w.q_chunks, cols);
-        header->weigh_mode = kKeysStay;
-        // the widest boxes that leave three stages, else two of the next
-        for (int32_t box = kWeighBoxes - 1; single && box >= 0; --box) {
-            const int64_t stage = (int64_t)weigh_stage_planes(box, w.bands == 1, w.lazy, w.band_chunks) * kWeighKeys * 128;
-            if (stay + (box == kWeighBoxes - 1 ? 3 : 2) * stage > kWeighSmem) continue;
-            header->weigh_mode = kQueriesStay;
-            header->weigh_cols = (int32_t)cols;
-            header->weigh_box = box;
-            break;
-        }
-        if (header->weigh_mode == kKeysStay) {
-            header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs));
-        }
+        return;
     }
-    int32_t parts = 0;
+    const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
+    int64_t most = 0;        // query rows of a request and band, where one tile takes them: their queries may stay
+    int64_t stay_tiles = 0;  // tiles of these requests' cache rows
+    auto may_stay = [&](const WeighReq& r) {
+        const ChunkDev& c = chunks[r.chunk];
+        return c.next < 0 && ceil_div(c.n, tokens) * blocks == 1;
+    };
     for (WeighReq& r : *reqs) {
-        r.begin = header->weigh_work;
+        int64_t n = 0;
+        for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) n += ceil_div(ceil_div(chunks[c].n, tokens) * blocks, 2);
+        r.units = (int32_t)(n * w.bands);
+        if (!may_stay(r)) continue;
+        ++header->weigh_stay;
+        most = std::max(most, (int64_t)chunks[r.chunk].n * w.group);
+        stay_tiles += ceil_div(r.end, kPairKeys);
+    }
+    if (header->weigh_stay < header->weigh_reqs && stay_tiles < kWeighSplit * w.pairs) header->weigh_stay = 0;
+    const int64_t cols = ceil_div(most, 32) * 32, stay = stay_bytes(w.bands, w.q_chunks, cols);
+    // the widest boxes that leave three stages, else two of the next
+    int32_t box = header->weigh_stay > 0 ? kWeighBoxes - 1 : -1;
+    for (; box >= 0; --box) {
+        const int64_t stage = (int64_t)weigh_stage_planes(box, w.bands == 1, w.lazy, w.band_chunks) * kWeighKeys * 128;
+        if (stay + (box == kWeighBoxes - 1 ? 3 : 2) * stage <= kWeighSmem) break;
+    }
+    if (box >= 0) {
+        header->weigh_cols = (int32_t)cols;
+        header->weigh_box = box;
+        if (header->weigh_stay < header->weigh_reqs) std::stable_partition(reqs->begin(), reqs->end(), may_stay);
+    } else {
+        header->weigh_stay = 0;
+    }
+    int64_t units = 0;  // products of all tiles of cache rows
+    for (size_t k = header->weigh_stay; k < reqs->size(); ++k) units += (*reqs)[k].units * ceil_div((*reqs)[k].end, kPairKeys);
+    header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs));
+    int32_t parts = 0;
+    for (size_t k = 0; k < reqs->size(); ++k) {
+        WeighReq& r = (*reqs)[k];
         r.segs = 1;
         r.part = parts;
         r.tile = header->weigh_tiles;
-        if (header->weigh_mode == kAnyRows) {
-            header->weigh_work += r.end;
-        } else if (header->weigh_mode == kQueriesStay) {
-            header->weigh_work += ceil_div(r.end, 32);
-        } else {
-            const int64_t tiles = ceil_div(r.end, kPairKeys);
-            r.segs = (int32_t)ceil_div(r.units, header->weigh_seg);
-            header->weigh_work += tiles * r.segs;
-            if (r.segs > 1) {
-                parts += (int32_t)(tiles * r.segs);
-                header->weigh_tiles += (int32_t)tiles;
-            }
+        if ((int32_t)k < header->weigh_stay) {
+            r.begin = header->weigh_stay_work;
+            header->weigh_stay_work += ceil_div(r.end, 32);
+            continue;
+        }
+        const int64_t tiles = ceil_div(r.end, kPairKeys);
+        r.begin = header->weigh_work;
+        r.segs = (int32_t)ceil_div(r.units, header->weigh_seg);
+        header->weigh_work += tiles * r.segs;
+        if (r.segs > 1) {
+            parts += (int32_t)(tiles * r.segs);
+            header->weigh_tiles += (int32_t)tiles;
         }
     }
 }

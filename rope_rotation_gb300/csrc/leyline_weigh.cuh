@@ -48,16 +48,16 @@ struct Tile {
 
 __device__ __forceinline__ int padded(int cols) { return (cols + 15) & ~15; }
 
-// The request whose work holds unit x.
-__device__ __forceinline__ WeighReq find_request(const WeighArgs& a, long long x)
+// The one of n requests whose work holds unit x.
+__device__ __forceinline__ WeighReq find_request(const WeighReq* reqs, int n, long long x)
 {
-    int lo = 0, hi = a.header->weigh_reqs - 1;
+    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a.reqs[mid].begin <= x) lo = mid;
+        if (reqs[mid].begin <= x) lo = mid;
         else hi = mid - 1;
     }
-    return a.reqs[lo];
+    return reqs[lo];
 }
 
 // (A replayed plan's table may have more requests or rows than the weights.)

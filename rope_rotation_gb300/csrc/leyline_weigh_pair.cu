@@ -1,5 +1,5 @@
-// leyline_weigh_pair.cu -- the weight that a batch's queries give to each cache row by pairs of CTAs (sm_103a), where some
-// request's query rows of a band do not fit one tile of 128: prompt chunks, drafts of many heads.
+// leyline_weigh_pair.cu -- the weight that a batch's queries give to each cache row by pairs of CTAs (sm_103a), for requests
+// whose query rows of a band do not fit one tile of 128: prompt chunks, drafts of many heads.
 //
 // As leyline_weigh_tile.cu, but the keys of 256 cache rows stay, 128 in each CTA, while query tiles pass, two at a time, one
 // through each CTA, in products that span both (cta_group::2):
@@ -62,7 +62,7 @@ __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, uint32_
     const long long work = a.header->weigh_work;
     const int seg = a.header->weigh_seg, pairs = gridDim.x / 2;
     for (long long i = blockIdx.x / 2; i < work; i += pairs) {
-        const WeighReq r = find_request(a, i);
+        const WeighReq r = find_request(a.reqs + a.header->weigh_stay, a.header->weigh_reqs - a.header->weigh_stay, i);
         if (!weights_hold(a, r)) {
             role.refuse();
             continue;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     wait_for_previous_grid();
-    if (a.header->weigh_mode != kKeysStay) return;  // the plan is for the other kernel (both CTAs see the same)
+    if (a.header->weigh_work == 0) return;  // no request of the plan is for this kernel (both CTAs see the same)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_addr(&m->full[i]), 2 * kLoadWarps);  // both CTAs' copying warps, or the asking lane for as many
@@ -435,15 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
 __global__ void __launch_bounds__(kPairKeys) join_weights_kernel(const __grid_constant__ WeighArgs a)
 {
     wait_for_previous_grid();
-    const int n = a.header->weigh_reqs;
+    const int n = a.header->weigh_reqs - a.header->weigh_stay;
+    const WeighReq* reqs = a.reqs + a.header->weigh_stay;
     for (int i = blockIdx.x; i < a.header->weigh_tiles; i += gridDim.x) {
         int lo = 0, hi = n - 1;  // the last request whose cut tiles begin at or before this one has it
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (a.reqs[mid].tile <= i) lo = mid;
+            if (reqs[mid].tile <= i) lo = mid;
             else hi = mid - 1;
         }
-        const WeighReq r = a.reqs[lo];
+        const WeighReq r = reqs[lo];
         const int tile = i - r.tile;
         const long long key = (long long)tile * kPairKeys + threadIdx.x;
         if (key >= r.end || !weights_hold(a, r)) continue;

@@ -1,5 +1,5 @@
-// leyline_weigh_tile.cu -- the weight that a batch's queries give to each cache row, on the tensor cores of sm_103a, where
-// every request's query rows of a band fit one tile of 128 (decoding): MLA rows and the grouped rows that attention takes
+// leyline_weigh_tile.cu -- the weight that a batch's queries give to each cache row, on the tensor cores of sm_103a, for
+// requests whose query rows of a band fit one tile of 128 (decoding): MLA rows and the grouped rows that attention takes
 // in tiles.
 //
 //   S^T = K Q^T  [256 cache rows x up to 128 query rows],  w_s += sum over columns of exp2(S^T * scale * log2 e - lse * log2 e)
@@ -66,9 +66,9 @@ template <class Role>
 __device__ __forceinline__ void walk(const WeighArgs& a, const Shape& s, uint32_t rank, Role& role)
 {
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-    const long long work = a.header->weigh_work, g1 = work * (pair + 1) / pairs;
+    const long long work = a.header->weigh_stay_work, g1 = work * (pair + 1) / pairs;
     for (long long g = work * pair / pairs; g < g1;) {
-        const WeighReq r = find_request(a, g);
+        const WeighReq r = find_request(a.reqs, a.header->weigh_stay, g);
         const long long g_end = min(g1, (long long)(r.begin + (r.end + 31) / 32));
         if (!weights_hold(a, r)) {
             role.refuse();
@@ -281,9 +281,9 @@ struct Loader {
     {
         const WeighArgs& a = keys.a;
         const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-        const long long work = a.header->weigh_work, g1 = work * (pair + 1) / pairs;
+        const long long work = a.header->weigh_stay_work, g1 = work * (pair + 1) / pairs;
         for (long long g = work * pair / pairs; g < g1;) {
-            const WeighReq r = find_request(a, g);
+            const WeighReq r = find_request(a.reqs, a.header->weigh_stay, g);
             const long long g_end = min(g1, (long long)(r.begin + (r.end + 31) / 32));
             if (weights_hold(a, r)) {
                 const ChunkDev ch = a.chunks[r.chunk];
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     wait_for_previous_grid();
-    if (a.header->weigh_mode != kQueriesStay) return;  // the plan is for the other kernel (both CTAs see the same)
+    if (a.header->weigh_stay == 0) return;  // no request of the plan is for this kernel (both CTAs see the same)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_addr(&m->full[i]), 2 * kLoadWarps);

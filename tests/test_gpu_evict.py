@@ -318,6 +318,43 @@ def test_weigh_captured_and_replayed(kw):
     cache.close()
 
 
+@pytest.mark.parametrize("kw,heads", [({}, 16), (dict(flags=LAZY, B=1), 16), (dict(rope=128, bands=4), 32), ({}, 128)])
+def test_weigh_steps_of_decodes_and_a_chunk(kw, heads):
+    """Plans whose requests go to two kernels: many decoded tokens beside chunks of a prompt."""
+    lens = [4200] * 20 + [700, 3, 1500]
+    cache = BH.make_cache(lens, seed=18, layers=1, **kw)
+    if cache.pending() is not None:
+        cache.pending().random_(-300, 300)
+    b = cache.batch(40, 600, heads)
+    scale = 0.06
+    w = fresh_weights(cache, seed=1)
+    graph = None
+    for chunks in ([(r, 4199 - r, 1) for r in range(20)] + [(20, 500, 200)],
+                   [(22, 0, 300), (20, 0, 0)] + [(r, 4199, 1) for r in (5, 3, 7)] + [(21, 2, 1)],
+                   [(20, 690, 10)] + [(r, 4100, 2) for r in reversed(range(20))] + [(22, 1499, 1), (20, 600, 3)]):
+        b.plan(chunks)
+        n = sum(c[2] for c in chunks)
+        b.append(0, BH.bf16(n, cache.row, seed=19))
+        ql, q = queries(cache, 600, heads, seed=20)
+        lse = 3 + torch.randn(600, heads, device="cuda")
+        check_weigh(cache, b, 0, chunks, ql, q, lse, scale, w, 0.5, what=f"{chunks[0]}")
+        if graph is None:
+            ql0, q0, lse0, w0 = ql, q, lse, torch.zeros_like(w)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                b.attention_weights(0, ql0, q0, lse0, scale, w0)
+        w0.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        cache.check_status()
+        one = torch.zeros_like(w)
+        b.attention_weights(0, ql0, q0, lse0, scale, one)
+        assert torch.equal(w0, one)  # a replay gives what a call does
+    b.close()
+    cache.close()
+
+
 @pytest.mark.parametrize("kw", [{}, dict(rope=128, bands=4), dict(latent=64, rope=16)])
 @pytest.mark.parametrize("tokens", [1, 80])
 def test_weigh_replayed_for_another_table(kw, tokens):

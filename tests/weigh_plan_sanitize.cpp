@@ -3,8 +3,9 @@
 //
 // Seeded random chunks and head layouts.  Of every plan it checks that
 //   - each request's chunks are linked in the order of their rows, and its rows end where the last one does;
-//   - the work, decoded as the kernels decode it, covers each row (kAnyRows, kQueriesStay), or each pair of a tile of
-//     cache rows and a query tile (kKeysStay), exactly once;
+//   - requests whose queries stay come first, each kind in the order of the requests;
+//   - the work, decoded as the kernels decode it, covers each row (queries that stay, rows of any shape), or each pair of a
+//     tile of cache rows and a query tile (keys that stay), exactly once;
 //   - what stays and what passes fit a CTA's shared memory;
 //   - the sums of cut query tiles have places of their own within their buffer, and the second kernel finds them.
 // Exit code 0: every check held.  Usage: weigh_plan_sanitize <iterations> <seed>
@@ -47,9 +48,9 @@ void check(bool ok, const char* what)
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The last request whose work begins at or before x, as the kernels look it up.
-const WeighReq& find(const std::vector<WeighReq>& reqs, int64_t x)
+const WeighReq& find(const WeighReq* reqs, int n, int64_t x)
 {
-    int lo = 0, hi = (int)reqs.size() - 1;
+    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (reqs[mid].begin <= x) lo = mid;
@@ -64,7 +65,7 @@ int main(int argc, char** argv)
 {
     const long iters = argc > 1 ? std::atol(argv[1]) : 2000;
     g_state = argc > 2 ? (uint64_t)std::atoll(argv[2]) : 1;
-    long modes[3] = {};
+    long modes[4] = {};
     for (iter = 0; iter < iters; ++iter) {
         Geometry g{};
         g.block_size = (int32_t)uniform(1, 40);
@@ -120,38 +121,47 @@ int main(int argc, char** argv)
         BatchHeader h{};
         std::vector<WeighReq> reqs = plan.weigh;
         weigh_work(w, plan.chunks, &reqs, &h);
-        ++modes[h.weigh_mode];
-        check(h.weigh_reqs == (int32_t)reqs.size() && (w.tiles || h.weigh_mode == kAnyRows), "header");
-        if (reqs.empty()) {
-            check(h.weigh_work == 0, "no work");
-            continue;
-        }
+        const int n = (int)reqs.size(), stay = h.weigh_stay;
+        ++modes[!w.tiles ? 0 : stay == n ? 1 : stay == 0 ? 2 : 3];
+        check(h.weigh_reqs == n && stay >= 0 && stay <= n && (w.tiles || stay == 0), "header");
         const int32_t tokens = weigh_tokens(w.group), blocks = (int32_t)ceil_div(w.group, kWeighCols);
         check(tokens * std::min(w.group, kWeighCols) <= kWeighCols, "query tiles fit");
-        if (h.weigh_mode != kKeysStay) {
-            const int64_t step = h.weigh_mode == kAnyRows ? 1 : 32;
-            int64_t at = 0;
-            for (const WeighReq& r : reqs) {
-                check(r.begin == at, "work in order");
-                at += ceil_div(r.end, step);
-                if (h.weigh_mode == kQueriesStay) {
-                    const ChunkDev& c = plan.chunks[r.chunk];
-                    check(c.next < 0 && c.n * w.group <= h.weigh_cols && h.weigh_cols <= kWeighCols, "one query tile");
-                }
-            }
-            check(at == h.weigh_work, "all of it");
-            for (int k = 0; k < 20; ++k) {
-                const int64_t x = uniform(0, at - 1);
-                const WeighReq& r = find(reqs, x);
-                check(x >= r.begin && x < r.begin + ceil_div(r.end, step), "its request is found");
-            }
-            if (h.weigh_mode == kQueriesStay)
-                check(stay_bytes(w.bands, w.q_chunks, h.weigh_cols) + 2 * weigh_stage_planes(h.weigh_box, w.bands == 1, w.lazy, w.band_chunks) *
-                                                                              kWeighKeys * 128 <= kWeighSmem, "shared memory");
-            continue;
+        std::set<int32_t> reqs_of;
+        for (int k = 0; k < n; ++k) {
+            check(k == 0 || k == stay || reqs[k].req > reqs[k - 1].req, "requests ascend within their kind");
+            reqs_of.insert(reqs[k].req);
         }
-        int64_t at = 0, parts = 0, tiles_before = 0;
-        for (const WeighReq& r : reqs) {
+        check(reqs_of == named, "every request is there");
+        // rows: of requests whose queries stay, or of all where the tensor cores do not take them
+        const int by_rows = w.tiles ? stay : n;
+        const int64_t step = w.tiles ? 32 : 1;
+        int64_t at = 0, stay_tiles = 0;
+        for (int k = 0; k < by_rows; ++k) {
+            const WeighReq& r = reqs[k];
+            check(r.begin == at, "work in order");
+            at += ceil_div(r.end, step);
+            stay_tiles += ceil_div(r.end, kPairKeys);
+            const ChunkDev& c = plan.chunks[r.chunk];
+            if (w.tiles) check(c.next < 0 && c.n * w.group <= h.weigh_cols && h.weigh_cols <= kWeighCols, "one query tile");
+        }
+        check(at == (w.tiles ? h.weigh_stay_work : h.weigh_work), "all of it");
+        for (int k = 0; k < 20 && at > 0; ++k) {
+            const int64_t x = uniform(0, at - 1);
+            const WeighReq& r = find(reqs.data(), by_rows, x);
+            check(x >= r.begin && x < r.begin + ceil_div(r.end, step), "its request is found");
+        }
+        if (stay > 0)
+            check(stay_bytes(w.bands, w.q_chunks, h.weigh_cols) + 2 * weigh_stage_planes(h.weigh_box, w.bands == 1, w.lazy, w.band_chunks) *
+                                                                          kWeighKeys * 128 <= kWeighSmem, "shared memory");
+        check(stay == 0 || stay == n || stay_tiles >= kWeighSplit * w.pairs, "two kernels where it is worth it");
+        if (!w.tiles) continue;
+        // items: of the others
+        const WeighReq* others = reqs.data() + stay;
+        const int m = n - stay;
+        int64_t parts = 0, tiles_before = 0;
+        at = 0;
+        for (int k = 0; k < m; ++k) {
+            const WeighReq& r = others[k];
             const int64_t tiles = ceil_div(r.end, kPairKeys);
             int64_t units = 0;  // products of two query tiles
             for (int32_t c = r.chunk; c >= 0; c = plan.chunks[c].next) units += ceil_div(ceil_div(plan.chunks[c].n, tokens) * blocks, 2);
@@ -162,22 +172,22 @@ int main(int argc, char** argv)
                 check(r.part == parts && r.tile == tiles_before, "places of cut query tiles");
                 parts += tiles * r.segs;
                 for (int64_t i : {tiles_before, tiles_before + tiles - 1}) {  // as the second kernel looks them up
-                    int lo = 0, hi = (int)reqs.size() - 1;
+                    int lo = 0, hi = m - 1;
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) >> 1;
-                        if (reqs[mid].tile <= i) lo = mid;
+                        if (others[mid].tile <= i) lo = mid;
                         else hi = mid - 1;
                     }
-                    check(&reqs[lo] == &r, "a cut tile's request is found");
+                    check(&others[lo] == &r, "a cut tile's request is found");
                 }
                 tiles_before += tiles;
             }
-            for (int64_t i : {r.begin, r.begin + tiles * r.segs - 1}) check(&find(reqs, i) == &r, "an item's request is found");
+            for (int64_t i : {r.begin, r.begin + tiles * r.segs - 1}) check(&find(others, m, i) == &r, "an item's request is found");
         }
         check(at == h.weigh_work && tiles_before == h.weigh_tiles, "all of it");
         check(parts <= 2 * (int64_t)kWeighItems * w.pairs, "sums fit their buffer");
     }
-    std::printf("%ld plans by rows, %ld with queries that stay, %ld with keys that stay, %d failed checks\n", modes[0], modes[1],
-                modes[2], failures);
-    return failures == 0 && modes[0] > 0 && modes[1] > 0 && modes[2] > 0 ? 0 : 1;
+    std::printf("%ld plans by rows, %ld with queries that stay, %ld with keys that stay, %ld of both, %d failed checks\n", modes[0],
+                modes[1], modes[2], modes[3], failures);
+    return failures == 0 && modes[0] > 0 && modes[1] > 0 && modes[2] > 0 && modes[3] > 0 ? 0 : 1;
 }
