@@ -406,8 +406,8 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * from it on extend the request, and the plan takes their pages off the free
  * list, installs them in the table and advances the length.  The rows of a chunk
  * hold nothing defined from the plan on until every layer has been appended.  A plan
- * holds until a splice changes one of its requests, a rollback returns to a checkpoint
- * made before it, or one of its pages is freed.  After the first two, calls that are not
+ * holds until a splice or an eviction changes one of its requests, a rollback returns to a
+ * checkpoint made before it, or one of its pages is freed.  After all but the last, calls that are not
  * captured are refused (INVALID_ARG) until the next plan; replays and freed pages the
  * library does not see.
  * rope_start is the rotary position of the chunk's first token: start, unless
@@ -416,8 +416,8 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * leyline_append and leyline_rotate, are not for a model that scales them otherwise.
  *
  * CUDA graphs.  leyline_batch_plan runs on the host for the lengths as they stand
- * and refuses a stream under capture.  leyline_append, leyline_rotate and
- * leyline_attention can be captured: they read the plan from the batch's device
+ * and refuses a stream under capture.  leyline_append, leyline_rotate,
+ * leyline_attention and leyline_attention_weights can be captured: they read the plan from the batch's device
  * memory, at addresses that do not change, so a graph of a step's layers can be
  * replayed after each new plan.  Their token tensors must then have room for
  * max_tokens tokens, whatever the plan at the time of the capture (views whose
@@ -446,7 +446,8 @@ typedef struct {
  * q_heads query heads (leyline_attention needs a multiple of rope_heads).  Allocates the plan's device
  * buffers (8 + 4 * rope_dim bytes per token, 40 per 64 query rows), pinned staging for four plans, and the
  * attention workspace (partial outputs of row tiles whose rows are split over
- * several CTAs: some 40 MiB for MLA rows).  Synchronous.  The pool cannot be
+ * several CTAs: some 40 MiB for MLA rows; for leyline_attention_weights 1.2 MiB of sums and
+ * 40 bytes per chunk).  Synchronous.  The pool cannot be
  * destroyed while it has batches.
  * Errors: INVALID_ARG (null argument, sizes out of range, max_tokens * q_heads /
  * rope_heads not below 2^31 - 128, or a pool whose rows
@@ -563,13 +564,16 @@ typedef struct {
  *     w_s = decay * w_s + sum over its tokens that attend to s and all heads of
  *           exp(scale * <query, key_s> - lse),
  * with queries, scale and flags as leyline_attention takes them and lse ([tokens][q_heads],
- * contiguous) as it returns it (or merged with that of other rows).  With decay 0 the old weights are not read.  A query
- * row with lse -inf attends to nothing and adds nothing.  Rows behind, and those of requests that are not in the
- * plan, are left as they were, and so is a row whose page is bad (status word).  The weights may not overlap
- * the queries or lse.  Scores, exponentials and sums are fp32; two calls on the same inputs and
- * plan give the same bits.  Can be captured, like leyline_attention, with weights that hold every
- * request and row of the plan's block table; a replay whose plan is for another table, with more of them, leaves
- * such a request's weights as they were (status word).
+ * contiguous) as it returns it (or merged with that of other rows, which then share the softmax).
+ * With decay 0 the old weights are not read.  A query row with lse -inf attends to nothing and adds
+ * nothing.  Rows behind, and those of requests that are not in the plan, are left as they were, and
+ * so is a row whose page is bad (status word).  The weights may not overlap the queries or lse.
+ * Scores, exponentials and sums are fp32; two calls on the same inputs and plan give the same bits.
+ * Enqueues a kernel for the requests whose query rows of a band fit one tile of 128, one for the
+ * others, and one that joins partial sums, as far as the plan has them; under capture all three.
+ * Can be captured, like leyline_attention, with weights that hold every request and row of the
+ * plan's block table; a replay whose plan is for another table, with more of them, leaves such a
+ * request's weights as they were (status word).
  * Errors: INVALID_ARG, CUDA. */
 int leyline_attention_weights(leyline_batch_t* batch, int32_t layer, const leyline_heads_t* q_latent,
                               const leyline_heads_t* q_rope, const float* lse, const leyline_row_weights_t* weights,

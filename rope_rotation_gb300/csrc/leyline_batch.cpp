@@ -150,7 +150,7 @@ int enter(leyline_batch* b, cudaStream_t stream, bool* captured)
     }
     *captured = st != cudaStreamCaptureStatusNone;
     if (!*captured && b->mark.stale && b->n_tokens > 0)
-        return bad("the batch's plan no longer holds: a splice or a rollback has changed one of its requests");
+        return bad("the batch's plan no longer holds: a splice, an eviction or a rollback has changed one of its requests");
     b->pool->window_open = false;  // other work on the pool ends the window of overlapping splices
     // a captured call is ordered by its graph; an event of other work cannot enter the capture
     return *captured ? LEYLINE_OK : order_after_previous(b->pool, stream);
