@@ -1,5 +1,5 @@
 // weigh_plan_sanitize.cpp -- a fuzz driver for the plan of weighing rows (weigh_work in leyline_batch_plan.cpp), built by
-// tests/test_batch_plan.py with AddressSanitizer and UndefinedBehaviorSanitizer.
+// tests/test_weigh_plan.py with AddressSanitizer and UndefinedBehaviorSanitizer.
 //
 // Seeded random chunks and head layouts.  Of every plan it checks that
 //   - each request's chunks are linked in the order of their rows, and its rows end where the last one does;
