@@ -197,7 +197,7 @@ struct KeyLoader {
     // cos and sin of c * theta_j: the angle in turns in fp64, less its whole ones, then in fp32.  They are off by 2^-22 of the
     // pair, where the scores carry a turned band to 2^-17.  (The product of the pool's two tables, in fp64, takes two loads
     // from L2 for each pair, and every warp was held up by it wherever the count changed: 64 decodes of 16 heads over some
-    // 4000 rows, one a page, 163 us instead of 107.)
+    // 4000 rows, one a page, 157 us instead of 129.)
     __device__ __forceinline__ void ensure(int c)
     {
         if (counted && c == count) return;
