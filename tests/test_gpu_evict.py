@@ -244,6 +244,42 @@ def test_weigh_rows_that_hold_nothing(kw):
     cache.close()
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("lat,rope,bands", [(512, 64, 1), (512, 128, 4), (512, 64, 8), (512, 256, 2), (72, 48, 1), (96, 96, 3)])
+def test_weigh_lazy_naive_pools(lat, rope, bands, layout):
+    """With the naive rounding a turned band is a bf16 value: a lazy pool's rows weigh what those of an eager pool do that
+    holds what a gather returns."""
+    lens = [1234, 77]
+    kw = dict(extra=8, precision=1, latent=lat, rope=rope, bands=bands, pair_layout=layout)
+    lazy, eager = BH.make_cache(lens, flags=LAZY, **kw), BH.make_cache(lens, **kw)
+    for r, n in enumerate(lens):
+        flat = torch.from_numpy(lazy.slot_index(r, np.arange(n))).cuda()
+        turns = torch.from_numpy(np.random.default_rng(r).integers(-9000, 9000, n // 10 + 1).astype(np.int32)).cuda()
+        lazy.pending().view(-1)[flat] = turns[torch.arange(n, device="cuda") // 10]
+        flat_e = torch.from_numpy(eager.slot_index(r, np.arange(n))).cuda()
+        for layer in range(2):
+            eager.write_layer_rows(layer, flat_e, lazy.gather(r, layer, 0, n))
+    heads = 8 * bands
+    b = lazy.batch(2, 120, heads)
+    for chunks in ([(0, 1233, 1), (1, 75, 2)], [(0, 1100, 110), (1, 70, 7)]):
+        tokens = sum(c[2] for c in chunks)
+        was = lazy.pending().clone()
+        b.plan(chunks)  # clears the counts of the chunks' rows, which are to be written: here they stay
+        torch.cuda.synchronize()
+        lazy.pending().copy_(was)
+        ql, q = queries(lazy, tokens, heads, seed=24)
+        lse = 3 + torch.randn(tokens, heads, device="cuda")
+        w = fresh_weights(lazy, seed=2)
+        want, tol, written = weights64(eager, 1, chunks, ql, q, lse, 0.07, w, 0.5)
+        b.attention_weights(1, ql, q, lse, 0.07, w, 0.5)
+        torch.cuda.synchronize()
+        lazy.check_status()
+        assert bool(((w.double() - want).abs()[written] <= tol[written]).all())
+    b.close()
+    lazy.close()
+    eager.close()
+
+
 def test_weigh_strided_tensors_and_same_bits():
     cache = BH.make_cache([900, 70], seed=6, layers=2)
     b = cache.batch(2, 40, 24)
