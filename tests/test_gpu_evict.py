@@ -244,6 +244,28 @@ def test_weigh_rows_that_hold_nothing(kw):
     cache.close()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(rope=128, bands=4), dict(latent=64, rope=16), dict(B=1, pair_layout=1)])
+def test_weigh_turns_of_any_count(kw):
+    """Counts up to the ends of their type.  Angles of 2^31 radians in fp64, here and in the formula, are off by 2^-21."""
+    cache = BH.make_cache([900, 300], seed=25, layers=1, flags=LAZY, **kw)
+    ends = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 26, -2 ** 26 - 1, 2 ** 20 + 1, 0, -1], dtype=torch.int32, device="cuda")
+    cache.pending().copy_(ends[torch.randint(0, 7, cache.pending().shape, device="cuda")])
+    heads = 16 * cache.rope_heads
+    b = cache.batch(2, 80, heads)
+    for chunks in ([(0, 899, 1), (1, 299, 1)], [(0, 840, 60)]):
+        was = cache.pending().clone()
+        b.plan(chunks)
+        torch.cuda.synchronize()
+        cache.pending().copy_(was)
+        tokens = sum(c[2] for c in chunks)
+        ql, q = queries(cache, tokens, heads, seed=26)
+        lse = 3 + torch.randn(tokens, heads, device="cuda")
+        check_weigh(cache, b, 0, chunks, ql, q, lse, 0.07, fresh_weights(cache, seed=1), what=f"{kw}",
+                    pair_layout=kw.get("pair_layout", 0))
+    b.close()
+    cache.close()
+
+
 @pytest.mark.parametrize("layout", [0, 1])
 @pytest.mark.parametrize("lat,rope,bands", [(512, 64, 1), (512, 128, 4), (512, 64, 8), (512, 256, 2), (72, 48, 1), (96, 96, 3)])
 def test_weigh_lazy_naive_pools(lat, rope, bands, layout):
@@ -865,6 +887,68 @@ def test_evict_refusals_and_bad_lists():
         assert len(ids) == 0
         full.close()
         cache.close()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(flags=LAZY), dict(B=1), dict(B=1, flags=LAZY | REINDEX), dict(flags=SPLIT, B=5)])
+def test_evict_among_other_work(kw):
+    """Splices that overlap, evictions, steps of a batch and selections in flight at once, on two streams: the same state as
+    of a pool that waits after every call."""
+    from rope_rotation_gb300 import leyline
+    rng = np.random.default_rng(10)
+    lens = [900, 700, 800, 600, 500, 40]
+    repl = BH.bf16(2, 7, 576, seed=31)
+    x, ql, q = BH.bf16(9, 576, seed=32), BH.bf16(9, 4, 512, seed=33), BH.bf16(9, 4, 64, seed=34)
+    wide = torch.zeros(6, 1000, dtype=torch.int32, device="cuda")
+    plans = []
+    for turn in range(3):
+        span, n = ((300, 200), (180, 150), (140, 100))[turn]
+        rows = {r: pick(rng, span, n) for r in (turn, 3, 4)}
+        for k, r in enumerate(rows):
+            wide[3 * (turn % 2) + k, 10:10 + len(rows[r])] = torch.tensor(rows[r], dtype=torch.int32)
+        plans.append(([(r, len(v)) for r, v in rows.items()], wide.clone()[3 * (turn % 2):3 * (turn % 2) + 3, 10:500]))
+    ends = []
+    for wait in (True, False):
+        cache = BH.make_cache(lens, extra=100, seed=30, slack=8000, **kw)
+        w = fresh_weights(cache, seed=35)
+        b = cache.batch(3, 9, 4)
+        out = []
+        torch.cuda.synchronize()
+        first, second = torch.cuda.Stream(), torch.cuda.Stream()
+
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+
+        for turn, (keeps, kept) in enumerate(plans):
+            with torch.cuda.stream(first):
+                for r in range(3):
+                    cache.splice([leyline.directive(r, 20 + turn, 60, repl)], first)
+                    done()
+            cache.evict(keeps, kept, weights=w, stream=second)
+            done()
+            first.wait_stream(second)  # (weights are the caller's to order)
+            with torch.cuda.stream(first):
+                n = [int(v) for v in cache.seq_lens_host]
+                b.plan([(3, n[3], 4), (turn, n[turn] - 2, 3), (5, n[5], 2)])
+                done()
+                for layer in range(2):
+                    b.append(layer, x)
+                    done()
+                _, lse = b.attention(1, ql, q, 0.05)
+                b.attention_weights(1, ql, q, lse, 0.05, w, 0.9)
+                done()
+                out.append(cache.select_rows(w, [(5, 30), (3, 100, 1, 2)]))
+            second.wait_stream(first)
+        torch.cuda.synchronize()
+        cache.check_status()
+        out += [cache.gather(r, layer, 0, int(cache.seq_lens_host[r])).view(torch.int16) for r in range(6) for layer in range(2)]
+        out += [w.view(torch.int32), cache.table.clone(), torch.tensor(free_ids(cache)), torch.from_numpy(cache.seq_lens_host.copy())]
+        ends.append([t.clone() for t in out])
+        torch.cuda.synchronize()
+        b.close()
+        cache.close()
+    for one, other in zip(*ends):
+        assert torch.equal(one, other)
 
 
 @pytest.mark.parametrize("B", [16, 1])
