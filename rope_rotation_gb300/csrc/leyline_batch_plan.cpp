@@ -158,6 +158,7 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
         }
         tok += c.n;
     }
+    out->weigh.reserve(order.size());
     before = -1;
     for (int32_t k : order) {
         const ChunkDev& c = out->chunks[k];
@@ -270,13 +271,16 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
     int64_t stay_tiles = 0;  // tiles of these requests' cache rows
     auto may_stay = [&](const WeighReq& r) {
         const ChunkDev& c = chunks[r.chunk];
-        return c.next < 0 && ceil_div(c.n, tokens) * blocks == 1;
+        return c.next < 0 && c.n <= tokens && blocks == 1;
     };
     for (WeighReq& r : *reqs) {
-        int64_t n = 0;
-        for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) n += ceil_div(ceil_div(chunks[c].n, tokens) * blocks, 2);
-        r.units = (int32_t)(n * w.bands);
-        if (!may_stay(r)) continue;
+        if (!may_stay(r)) {
+            int64_t n = 0;
+            for (int32_t c = r.chunk; c >= 0; c = chunks[c].next) n += ceil_div(ceil_div(chunks[c].n, tokens) * blocks, 2);
+            r.units = (int32_t)(n * w.bands);
+            continue;
+        }
+        r.units = w.bands;
         ++header->weigh_stay;
         most = std::max(most, (int64_t)chunks[r.chunk].n * w.group);
         stay_tiles += ceil_div(r.end, kPairKeys);
