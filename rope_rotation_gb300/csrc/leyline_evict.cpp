@@ -170,19 +170,6 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     }
     if (p->q_tail - p->q_head + pages > g.num_pages)
         return bad("the requests hold more pages than the pool has free slots for: their tables were not filled from this pool");
-    if (!p->d_lists) {
-        const std::vector<ListState> none(2 * kEvictReqs, ListState{0, INT32_MAX});
-        cudaError_t e = (cudaError_t)evict_prepare();
-        if (e == cudaSuccess) e = cudaMalloc(&p->d_lists, sizeof(ListState) * none.size());
-        if (e == cudaSuccess) {
-            e = cudaMemcpy(p->d_lists, none.data(), sizeof(ListState) * none.size(), cudaMemcpyHostToDevice);
-            if (e != cudaSuccess) {
-                cudaFree(p->d_lists);
-                p->d_lists = nullptr;
-            }
-        }
-        if (e != cudaSuccess) return cuda_error(e, "allocating the lists' state");
-    }
     const int64_t half = ceil_div(most_stage, 4) * 4;
     rc = grow_stage(p, (size_t)(2 * half));
     if (rc == LEYLINE_OK) rc = order_after_previous(p, stream);

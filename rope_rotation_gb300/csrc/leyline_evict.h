@@ -73,7 +73,7 @@ struct EvictArgs {
 
 // Each returns the cudaError_t of its launches as int.
 int launch_select(const SelectArgs& a, const EvictSet& set, void* stream);
-int evict_prepare();  // before the first launch_evict
+int evict_prepare();  // when a pool is created
 int launch_evict(const EvictArgs& a, const EvictSet& set, void* stream);
 
 }  // namespace leyline

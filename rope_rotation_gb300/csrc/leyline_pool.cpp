@@ -23,6 +23,7 @@
 #include <cstdlib>
 #include <cmath>
 #include <cstring>
+#include <iterator>
 #include <new>
 #include <string>
 #include <vector>
@@ -253,6 +254,14 @@ int leyline_pool_create(const leyline_pool_desc_t* desc, void* kv_dev, leyline_p
         }
     }
     if (e == cudaSuccess) e = (cudaError_t)launch_init_queue(p->d_queue, g.num_pages, nullptr);
+    // evictions: nothing found of any list yet.  Here and not in the first one, whose stream would not be ordered after the
+    // copy: one from pageable memory may not have arrived when cudaMemcpy returns.
+    ListState none[2 * kEvictReqs];
+    std::fill(std::begin(none), std::end(none), ListState{0, INT32_MAX});
+    if (e == cudaSuccess) e = (cudaError_t)evict_prepare();
+    if (e == cudaSuccess) e = cudaMalloc(&p->d_lists, sizeof none);
+    if (e == cudaSuccess)
+        e = cudaMemcpy(p->d_lists, none, sizeof none, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         int r = cuda_error(e, "creating the pool");

@@ -1,0 +1,275 @@
+// host_calls_fake.cpp -- the host side of the C ABI over a CUDA runtime of its own, built by tests/test_host_calls.py with
+// the sanitizers: what each call enqueues, and in which order.  No GPU is used and no kernel runs.
+//
+// The runtime here keeps device memory on the host.  As CUDA documents it, a copy from pageable memory to the device has
+// left the host's buffer when cudaMemcpy returns but may not have arrived, and a cudaMemset may not have run: both are work of
+// the legacy stream, which other streams made as non-blocking ones are not ordered after.  So such work has to be waited
+// for before a call returns or launches a kernel on another stream.
+// Exit code 0: every check of the named case held.  Usage: host_calls_fake <case>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <map>
+#include <string>
+#include <vector>
+
+#include "leyline_batch.h"
+#include "leyline_pool_state.h"
+
+using namespace leyline;
+
+namespace {
+
+std::map<uintptr_t, size_t> device_memory;
+bool legacy_pending = false;  // work of the legacy stream may still run
+int unordered = 0;            // kernels launched on another stream meanwhile
+int copies_in = 0, selects = 0, evictions = 0, weighings = 0;
+std::vector<ListState> seen_state;  // of the last eviction, both arrays
+
+int launched(void* stream)
+{
+    if (stream && legacy_pending) ++unordered;
+    return 0;
+}
+
+bool on_device(const void* p)
+{
+    auto at = device_memory.upper_bound((uintptr_t)p);
+    if (at == device_memory.begin()) return false;
+    --at;
+    return (uintptr_t)p < at->first + at->second;
+}
+
+int failures = 0;
+void check(bool ok, const char* what)
+{
+    if (ok) return;
+    std::fprintf(stderr, "failed: %s (last error: %s)\n", what, leyline_last_error());
+    ++failures;
+}
+
+}  // namespace
+
+extern "C" {
+
+cudaError_t cudaMalloc(void** p, size_t n)
+{
+    *p = std::aligned_alloc(256, (n + 255) / 256 * 256);
+    std::memset(*p, 0xab, n);
+    device_memory[(uintptr_t)*p] = n;
+    return cudaSuccess;
+}
+cudaError_t cudaFree(void* p)
+{
+    if (p) device_memory.erase((uintptr_t)p);
+    std::free(p);
+    return cudaSuccess;
+}
+cudaError_t cudaHostAlloc(void** p, size_t n, unsigned)
+{
+    *p = std::malloc(n);
+    return cudaSuccess;
+}
+cudaError_t cudaFreeHost(void* p)
+{
+    std::free(p);
+    return cudaSuccess;
+}
+cudaError_t cudaMemcpy(void* to, const void* from, size_t n, cudaMemcpyKind kind)
+{
+    std::memcpy(to, from, n);
+    legacy_pending = kind == cudaMemcpyHostToDevice;  // a copy to the host waits for the stream
+    copies_in += kind == cudaMemcpyHostToDevice;
+    return cudaSuccess;
+}
+cudaError_t cudaMemset(void* p, int v, size_t n)
+{
+    std::memset(p, v, n);
+    legacy_pending = true;
+    return cudaSuccess;
+}
+cudaError_t cudaMemcpyAsync(void* to, const void* from, size_t n, cudaMemcpyKind, cudaStream_t)
+{
+    std::memcpy(to, from, n);
+    return cudaSuccess;
+}
+cudaError_t cudaDeviceSynchronize()
+{
+    legacy_pending = false;
+    return cudaSuccess;
+}
+cudaError_t cudaStreamSynchronize(cudaStream_t s)
+{
+    if (!s) legacy_pending = false;
+    return cudaSuccess;
+}
+cudaError_t cudaPointerGetAttributes(cudaPointerAttributes* a, const void* p)
+{
+    *a = cudaPointerAttributes{};
+    a->type = on_device(p) ? cudaMemoryTypeDevice : cudaMemoryTypeUnregistered;
+    return cudaSuccess;
+}
+cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* st)
+{
+    *st = cudaStreamCaptureStatusNone;
+    return cudaSuccess;
+}
+cudaError_t cudaGetDevice(int* d)
+{
+    *d = 0;
+    return cudaSuccess;
+}
+cudaError_t cudaSetDevice(int) { return cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int)
+{
+    *v = 152;
+    return cudaSuccess;
+}
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+const char* cudaGetErrorString(cudaError_t) { return "an error"; }
+cudaError_t cudaEventCreate(cudaEvent_t* e)
+{
+    *e = nullptr;
+    return cudaSuccess;
+}
+cudaError_t cudaEventCreateWithFlags(cudaEvent_t* e, unsigned) { return cudaEventCreate(e); }
+cudaError_t cudaEventDestroy(cudaEvent_t) { return cudaSuccess; }
+cudaError_t cudaEventRecord(cudaEvent_t, cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaEventSynchronize(cudaEvent_t) { return cudaSuccess; }
+cudaError_t cudaStreamWaitEvent(cudaStream_t, cudaEvent_t, unsigned) { return cudaSuccess; }
+cudaError_t cudaEventElapsedTime(float* ms, cudaEvent_t, cudaEvent_t)
+{
+    *ms = 0.f;
+    return cudaSuccess;
+}
+
+}  // extern "C"
+
+namespace leyline {
+
+int launch_init_queue(int32_t* q, int64_t n, void* s)
+{
+    for (int64_t i = 0; i < n; ++i) q[i] = (int32_t)i;
+    if (!s) legacy_pending = true;
+    return launched(s);
+}
+int launch_clear_pending(int32_t*, const int32_t*, int64_t, int32_t, void* s)
+{
+    if (!s) legacy_pending = true;
+    return launched(s);
+}
+int launch_upload_plan(const void*, void*, size_t, void* s) { return launched(s); }
+int launch_splice(const SpliceArgs&, const ParamPlan*, int, void* s, cudaEvent_t, cudaEvent_t) { return launched(s); }
+int launch_gather(const void*, const int32_t*, const Geometry&, int32_t, int64_t, int64_t, void*, int32_t*, void* s) { return launched(s); }
+int launch_gather_lazy(const void*, const int32_t*, const Geometry&, int32_t, int64_t, int64_t, void*, const int32_t*, const double*,
+                       int32_t*, void* s)
+{
+    return launched(s);
+}
+int launch_materialize(void*, const int32_t*, int32_t, const MaterializeSet&, const Geometry&, int32_t*, const double*, int32_t*,
+                       const MaterializeScratch&, void* s)
+{
+    return launched(s);
+}
+int move_rotate_blocks_per_sm(int* n) { return *n = 1, 0; }
+int rotate_in_place_blocks_per_sm(int* n) { return *n = 1, 0; }
+int bulk_prepare(int32_t, int* n) { return *n = 1, 0; }
+int launch_install(const InstallArgs& a, void* s)
+{
+    for (int64_t i = 0; i < a.plan_vecs; ++i) a.plan[i] = a.staged[i];
+    return launched(s);
+}
+int launch_append(const AppendArgs&, int64_t, int, void* s) { return launched(s); }
+int launch_rotate(const RotateArgs&, int64_t, int, void* s) { return launched(s); }
+bool attention_takes_tiles(const Geometry&) { return false; }
+int attention_prepare(const Geometry&, const void*, TileMaps*) { return 0; }
+int attention_pair_prepare(const Geometry&, const void*, TileMaps*) { return 0; }
+int launch_attention(const AttnArgs&, const TileMaps&, int, void* s) { return launched(s); }
+int launch_attention_pair(const AttnArgs&, const TileMaps&, int, void* s) { return launched(s); }
+int launch_join(const AttnArgs&, int, int, bool, void* s) { return launched(s); }
+int weigh_tile_prepare(const Geometry&, const void*, WeighMaps*) { return 0; }
+int weigh_pair_prepare(const Geometry&) { return 0; }
+int launch_weigh(const WeighArgs&, int, void* s) { return ++weighings, launched(s); }
+int launch_weigh_tile(const WeighArgs&, const WeighMaps&, int, void* s) { return ++weighings, launched(s); }
+int launch_weigh_pair(const WeighArgs&, const WeighMaps&, int64_t, int, int, void* s) { return ++weighings, launched(s); }
+int launch_select(const SelectArgs&, const EvictSet&, void* s) { return ++selects, launched(s); }
+int evict_prepare() { return 0; }
+int launch_evict(const EvictArgs& a, const EvictSet&, void* s)
+{
+    ++evictions;
+    seen_state.assign(a.state, a.state + kEvictReqs);
+    seen_state.insert(seen_state.end(), a.next_state, a.next_state + kEvictReqs);
+    return launched(s);
+}
+
+}  // namespace leyline
+
+namespace {
+
+// A pool with two requests of 40 and 9 rows, or of `len0` and `len1`.
+struct Fixture {
+    leyline_pool_t* pool = nullptr;
+    void* kv = nullptr;
+    int32_t *table = nullptr, *lens_dev = nullptr, *kept = nullptr;
+    float* weights = nullptr;
+    int64_t lens[2];
+    leyline_block_table_t bt{};
+    leyline_row_weights_t w{};
+    void* stream = reinterpret_cast<void*>(0x1000);
+
+    Fixture(uint32_t flags = 0, int64_t len0 = 40, int64_t len1 = 9) : lens{len0, len1}
+    {
+        leyline_pool_desc_t d{};
+        d.num_layers = 1;
+        d.latent_dim = 512;
+        d.rope_dim = 64;
+        d.block_size = 4;
+        d.num_pages = 30;
+        d.rope_theta = 10000.0;
+        d.flags = flags;
+        cudaMalloc(&kv, 30 * 4 * 576 * 2);
+        check(leyline_pool_create(&d, kv, &pool) == LEYLINE_OK, "creating the pool");
+        check(!legacy_pending, "a pool's creation waits for its work");
+        cudaMalloc((void**)&table, 2 * 12 * 4);
+        cudaMalloc((void**)&lens_dev, 2 * 4);
+        cudaMalloc((void**)&kept, 2 * 40 * 4);
+        cudaMalloc((void**)&weights, 2 * 48 * 4);
+        std::vector<int32_t> pages(13);
+        check(leyline_alloc_pages(pool, 13, pages.data()) == LEYLINE_OK, "taking pages");
+        bt = leyline_block_table_t{table, lens_dev, lens, 2, 12};
+        w = leyline_row_weights_t{weights, 48, 48, 2};
+        legacy_pending = false;
+        copies_in = unordered = 0;
+    }
+    ~Fixture()
+    {
+        leyline_pool_destroy(pool);
+        for (void* p : {kv, (void*)table, (void*)lens_dev, (void*)kept, (void*)weights}) cudaFree(p);
+    }
+};
+
+void first_eviction()
+{
+    Fixture f;
+    const leyline_keep_t keep{0, 30, 0, 0};
+    check(leyline_evict(f.pool, &f.bt, &keep, 1, f.kept, 40, &f.w, f.stream) == LEYLINE_OK, "evicting");
+    check(evictions == 1 && f.lens[0] == 30, "the eviction is enqueued");
+    check(copies_in == 0, "the first eviction copies nothing by the legacy stream");
+    check(unordered == 0 && !legacy_pending, "no kernel runs beside work of the legacy stream");
+    for (const ListState& s : seen_state) check(s.bad == 0 && s.hole == INT_MAX, "the lists' states are ready");
+}
+
+}  // namespace
+
+int main(int argc, char** argv)
+{
+    const std::string name = argc > 1 ? argv[1] : "";
+    if (name == "first_eviction") first_eviction();
+    else check(false, "a case's name");
+    std::printf("%s: %d failed checks\n", name.c_str(), failures);
+    return failures == 0 ? 0 : 1;
+}
