@@ -374,11 +374,13 @@ int leyline_free_pages(leyline_pool_t* p, int32_t n, const int32_t* ids)
         if (e != cudaSuccess) return cuda_error(e, "writing the free-page ring");
         if (p->d_pending) {  // a free page carries no pending turn: clear the returned pages' counts
             e = (cudaError_t)launch_clear_pending(p->d_pending, p->d_queue + at, len, p->g.block_size, nullptr);
-            if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
             if (e != cudaSuccess) return cuda_error(e, "clearing pending turns of returned pages");
         }
         done += len;
     }
+    // a copy from pageable memory may still be on its way, and the streams of later calls need not wait for this one's
+    cudaError_t e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) return cuda_error(e, "returning pages");
     p->q_tail += n;
     return LEYLINE_OK;
 }

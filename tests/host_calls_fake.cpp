@@ -263,12 +263,23 @@ void first_eviction()
     for (const ListState& s : seen_state) check(s.bad == 0 && s.hole == INT_MAX, "the lists' states are ready");
 }
 
+void freed_pages()
+{
+    for (uint32_t flags : {0u, (uint32_t)LEYLINE_POOL_LAZY}) {
+        Fixture f(flags);
+        const int32_t ids[3] = {2, 0, 1};
+        check(leyline_free_pages(f.pool, 3, ids) == LEYLINE_OK, "returning pages");
+        check(!legacy_pending, "returned pages are in the free list when the call returns");
+    }
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
 {
     const std::string name = argc > 1 ? argv[1] : "";
     if (name == "first_eviction") first_eviction();
+    else if (name == "freed_pages") freed_pages();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;

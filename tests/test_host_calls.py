@@ -34,7 +34,7 @@ def run(exe, case):
     assert " 0 failed checks" in done.stdout
 
 
-CASES = ["first_eviction"]
+CASES = ["first_eviction", "freed_pages"]
 
 
 @pytest.mark.parametrize("case", CASES)
