@@ -712,7 +712,10 @@ int leyline_sync_status(leyline_pool_t* p)
     cudaError_t e = cudaMemcpy(&st, p->d_status, sizeof st, cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_error(e, "reading the status word");
     if (st != 0) {
-        cudaMemset(p->d_status, 0, sizeof(int32_t));
+        e = cudaMemset(p->d_status, 0, sizeof(int32_t));
+        // not beside the kernels of a later call, whose status it would take away
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+        if (e != cudaSuccess) return cuda_error(e, "clearing the status word");
         char msg[128];
         snprintf(msg, sizeof msg, "device check failed (status bits 0x%x)", st);
         return set_error(LEYLINE_ERR_DEVICE_CHECK, msg);

@@ -273,6 +273,15 @@ void freed_pages()
     }
 }
 
+void status_word()
+{
+    Fixture f;
+    *f.pool->d_status = 8;
+    check(leyline_sync_status(f.pool) == LEYLINE_ERR_DEVICE_CHECK, "the status is reported");
+    check(*f.pool->d_status == 0 && !legacy_pending, "the status word is clear when the call returns");
+    check(leyline_sync_status(f.pool) == LEYLINE_OK, "and stays so");
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
@@ -280,6 +289,7 @@ int main(int argc, char** argv)
     const std::string name = argc > 1 ? argv[1] : "";
     if (name == "first_eviction") first_eviction();
     else if (name == "freed_pages") freed_pages();
+    else if (name == "status_word") status_word();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;

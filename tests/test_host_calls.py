@@ -34,7 +34,7 @@ def run(exe, case):
     assert " 0 failed checks" in done.stdout
 
 
-CASES = ["first_eviction", "freed_pages"]
+CASES = ["first_eviction", "freed_pages", "status_word"]
 
 
 @pytest.mark.parametrize("case", CASES)
