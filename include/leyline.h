@@ -590,7 +590,8 @@ typedef struct {
 /* The rows to keep of n distinct requests: those at both ends, and of the others the n_keep - first
  * - last of greatest weight (equal weights: the lowest rows; -0 equals 0, a NaN is below everything).  The
  * list of keeps[k] is kept[k * kept_stride ...], n_keep int32 rows in ascending order; what lies behind it is
- * left as it was.  kept may not overlap the weights.  Enqueues one kernel for 32 requests.
+ * left as it was.  kept may not overlap the weights, and may be NULL where no entry keeps a row (as weights.ptr may where
+ * no request has one).  Enqueues one kernel for 32 requests.
  * Errors: INVALID_ARG (also when `stream` is being captured: the lengths are those of
  * seq_lens_host as it stands), CUDA. */
 int leyline_select_rows(leyline_pool_t* pool, const leyline_block_table_t* bt, const leyline_row_weights_t* weights,

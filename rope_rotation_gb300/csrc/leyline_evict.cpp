@@ -52,16 +52,29 @@ int check_keeps(const Geometry& g, const leyline_block_table_t& bt, const leylin
     return LEYLINE_OK;
 }
 
-// The rows' weights, for requests up to the longest of `keeps`.
+int64_t longest_list(const leyline_keep_t* keeps, int32_t n)
+{
+    int64_t longest = 0;
+    for (int32_t k = 0; k < n; ++k) longest = std::max<int64_t>(longest, keeps[k].n_keep);
+    return longest;
+}
+
+// The rows' weights, for requests up to the longest of `keeps`.  Requests without rows need no memory.
 int check_weights(const leyline_row_weights_t& w, const leyline_block_table_t& bt, const leyline_keep_t* keeps, int32_t n,
                   int device, float** alias)
 {
-    if (!w.ptr || (reinterpret_cast<uintptr_t>(w.ptr) & 3) != 0) return bad("weights must be a 4-byte aligned device pointer");
+    if ((reinterpret_cast<uintptr_t>(w.ptr) & 3) != 0) return bad("weights must be a 4-byte aligned device pointer");
     if (w.num_reqs < 0 || w.rows < 0 || (w.num_reqs > 1 && w.req_stride < w.rows))
         return bad("weights: a request's stride is at least its rows");
-    for (int32_t k = 0; k < n; ++k)
-        if (keeps[k].req >= w.num_reqs || bt.seq_lens_host[keeps[k].req] > w.rows)
-            return bad("weights do not hold every row of the requests");
+    bool rows = false;
+    for (int32_t k = 0; k < n; ++k) {
+        const int64_t len = bt.seq_lens_host[keeps[k].req];
+        if (keeps[k].req >= w.num_reqs || len > w.rows) return bad("weights do not hold every row of the requests");
+        rows |= len > 0;
+    }
+    *alias = nullptr;
+    if (!rows) return LEYLINE_OK;
+    if (!w.ptr) return bad("weights must be a 4-byte aligned device pointer");
     void* a;
     bool host;
     int rc = resolve_access(w.ptr, device, "weights", &a, &host);
@@ -69,10 +82,13 @@ int check_weights(const leyline_row_weights_t& w, const leyline_block_table_t& b
     return rc;
 }
 
-int check_lists(const int32_t* kept, int64_t kept_stride, int device, int32_t** alias)
+// Lists without rows need no memory.
+int check_lists(const int32_t* kept, int64_t kept_stride, int64_t longest, int device, int32_t** alias)
 {
-    if (!kept || (reinterpret_cast<uintptr_t>(kept) & 3) != 0) return bad("kept must be a 4-byte aligned device pointer");
     if (kept_stride < 0) return bad("kept_stride must not be negative");
+    *alias = nullptr;
+    if (longest == 0) return LEYLINE_OK;
+    if (!kept || (reinterpret_cast<uintptr_t>(kept) & 3) != 0) return bad("kept must be a 4-byte aligned device pointer");
     void* a;
     bool host;
     int rc = resolve_access(kept, device, "kept", &a, &host);
@@ -81,11 +97,9 @@ int check_lists(const int32_t* kept, int64_t kept_stride, int device, int32_t** 
 }
 
 // Whether the lists share a byte with the weights.
-bool lists_over_weights(const int32_t* kept, int64_t kept_stride, const leyline_keep_t* keeps, int32_t n, const float* w,
+bool lists_over_weights(const int32_t* kept, int64_t kept_stride, int64_t longest, int32_t n, const float* w,
                         const leyline_row_weights_t& view)
 {
-    int64_t longest = 0;
-    for (int32_t k = 0; k < n; ++k) longest = std::max<int64_t>(longest, keeps[k].n_keep);
     if (longest == 0 || view.rows == 0) return false;
     const Extent lists{reinterpret_cast<uintptr_t>(kept), n, 1, 4 * kept_stride, 0, 4 * longest};
     const Extent rows{reinterpret_cast<uintptr_t>(w), view.num_reqs, 1, 4 * view.req_stride, 0, 4 * view.rows};
@@ -111,11 +125,12 @@ int select_rows(leyline_pool_t* p, const leyline_block_table_t* bt, const leylin
     if (rc != LEYLINE_OK || n == 0) return rc;
     SelectArgs a{};
     float* weights = nullptr;
+    const int64_t longest = longest_list(keeps, n);
     rc = check_weights(*w, *bt, keeps, n, p->device, &weights);
-    if (rc == LEYLINE_OK) rc = check_lists(kept, kept_stride, p->device, &a.kept);
-    if (rc == LEYLINE_OK && lists_over_weights(a.kept, kept_stride, keeps, n, weights, *w))
+    if (rc == LEYLINE_OK) rc = check_lists(kept, kept_stride, longest, p->device, &a.kept);
+    if (rc == LEYLINE_OK && lists_over_weights(a.kept, kept_stride, longest, n, weights, *w))
         rc = bad("kept must not lie over the weights");
-    if (rc != LEYLINE_OK) return rc;
+    if (rc != LEYLINE_OK || longest == 0) return rc;
     a.weights = weights;
     a.req_stride = w->req_stride;
     a.kept_stride = kept_stride;
@@ -144,9 +159,10 @@ int evict(leyline_pool_t* p, leyline_block_table_t* bt, const leyline_keep_t* ke
     if (rc != LEYLINE_OK || n == 0) return rc;
     EvictArgs a{};
     int32_t* lists = nullptr;
-    rc = check_lists(kept, kept_stride, p->device, &lists);
+    const int64_t longest = longest_list(keeps, n);
+    rc = check_lists(kept, kept_stride, longest, p->device, &lists);
     if (rc == LEYLINE_OK && w) rc = check_weights(*w, *bt, keeps, n, p->device, &a.weights);
-    if (rc == LEYLINE_OK && w && lists_over_weights(lists, kept_stride, keeps, n, a.weights, *w))
+    if (rc == LEYLINE_OK && w && lists_over_weights(lists, kept_stride, longest, n, a.weights, *w))
         rc = bad("kept must not lie over the weights");
     if (rc != LEYLINE_OK) return rc;
 

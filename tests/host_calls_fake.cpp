@@ -282,6 +282,31 @@ void status_word()
     check(leyline_sync_status(f.pool) == LEYLINE_OK, "and stays so");
 }
 
+void empty_lists()
+{
+    Fixture f;
+    const leyline_keep_t none[2] = {{1, 0, 0, 0}, {0, 0, 0, 0}};
+    check(leyline_select_rows(f.pool, &f.bt, &f.w, none, 2, nullptr, 0, f.stream) == LEYLINE_OK, "lists of no rows have no memory");
+    check(selects == 0, "and nothing is enqueued for them");
+    const leyline_keep_t some{0, 1, 0, 0};
+    check(leyline_select_rows(f.pool, &f.bt, &f.w, &some, 1, nullptr, 40, f.stream) == LEYLINE_ERR_INVALID_ARG, "a list of one row has");
+    check(leyline_evict(f.pool, &f.bt, &some, 1, nullptr, 40, &f.w, f.stream) == LEYLINE_ERR_INVALID_ARG, "a list of one row has");
+    check(f.lens[0] == 40, "a refused call changes nothing");
+    const int64_t free_pages = leyline_free_page_count(f.pool);
+    check(leyline_evict(f.pool, &f.bt, none, 2, nullptr, 0, &f.w, f.stream) == LEYLINE_OK, "all rows of a request can be dropped");
+    check(evictions == 1 && f.lens[0] == 0 && f.lens[1] == 0, "and are");
+    check(leyline_free_page_count(f.pool) == free_pages + 13, "with their pages");
+    // requests without rows have no weights either
+    leyline_row_weights_t no_rows{nullptr, 0, 0, 2};
+    check(leyline_select_rows(f.pool, &f.bt, &no_rows, none, 2, nullptr, 0, f.stream) == LEYLINE_OK, "no weights of no rows");
+    check(leyline_evict(f.pool, &f.bt, none, 2, nullptr, 0, &no_rows, f.stream) == LEYLINE_OK, "no weights of no rows");
+    f.lens[0] = 5;
+    check(leyline_select_rows(f.pool, &f.bt, &no_rows, none, 2, nullptr, 0, f.stream) == LEYLINE_ERR_INVALID_ARG, "rows have weights");
+    no_rows = leyline_row_weights_t{nullptr, 48, 48, 2};
+    check(leyline_select_rows(f.pool, &f.bt, &no_rows, none, 2, nullptr, 0, f.stream) == LEYLINE_ERR_INVALID_ARG, "rows have weights");
+    check(leyline_evict(f.pool, &f.bt, none, 2, nullptr, 0, &no_rows, f.stream) == LEYLINE_ERR_INVALID_ARG, "rows have weights");
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
@@ -290,6 +315,7 @@ int main(int argc, char** argv)
     if (name == "first_eviction") first_eviction();
     else if (name == "freed_pages") freed_pages();
     else if (name == "status_word") status_word();
+    else if (name == "empty_lists") empty_lists();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;

@@ -54,3 +54,35 @@ def test_first_eviction_of_a_pool_leaves_the_legacy_stream_alone(B):
         assert torch.equal(BH.logical(cache, 0, 0, 100)[0], rows[torch.tensor(lists[0], device="cuda")])
         cache.close()
     assert running, f"the call waited for the legacy stream, {spent:.3f} s"
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(B=1), dict(flags=LAZY), dict(flags=LAZY, B=1)])
+def test_requests_that_keep_no_rows(kw):
+    """Selections and evictions of nothing, alone, together and among others, with lists as select_rows makes them."""
+    cache = BH.make_cache([50, 33, 0, 1], seed=3, layers=2, latent=64, rope=16, **kw)
+    pages = cache.free_pages()
+    if cache.pending() is not None:
+        for r in (0, 1, 3):
+            flat = torch.from_numpy(cache.slot_index(r, np.arange(int(cache.seq_lens_host[r])))).cuda()
+            cache.pending().view(-1)[flat] = 9
+    w = fresh_weights(cache, seed=1)
+    behind = w.clone()
+    kept = cache.select_rows(w, [(0, 0), (2, 0)])
+    assert tuple(kept.shape) == (2, 0)
+    cache.evict([(0, 0), (2, 0)], kept, weights=w)
+    torch.cuda.synchronize()
+    cache.check_status()
+    assert cache.seq_lens_host.tolist() == [0, 33, 0, 1] and cache.seq_lens_dev.tolist() == [0, 33, 0, 1]
+    assert cache.free_pages() == pages + -(-50 // cache.block_size) and bool((cache.table[0] == -1).all())
+    assert int((w[0, :50] != 0).sum()) == 0 and torch.equal(w[0, 50:], behind[0, 50:]) and torch.equal(w[1:], behind[1:])
+    kept = cache.select_rows(w, [(3, 0), (1, 7), (0, 0)])
+    check_evict(cache, [(3, 0), (1, 7), (0, 0)], [[], kept[1, :7].tolist(), []], weights=w)
+    cache.select_rows(w[:, :0], [(3, 0), (2, 0)])  # requests without rows have no weights
+    kept = cache.select_rows(w, [(1, 0)])
+    cache.evict([(1, 0)], kept)
+    torch.cuda.synchronize()
+    cache.check_status()
+    assert cache.free_pages() == cache.num_pages and int(cache.seq_lens_host.sum()) == 0
+    if cache.pending() is not None:
+        assert int(cache.pending().abs().sum()) == 0
+    cache.close()
