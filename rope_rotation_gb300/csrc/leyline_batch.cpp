@@ -567,9 +567,6 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     if (!std::isfinite(scale)) return bad("scale must be finite");
     if (!std::isfinite(decay) || decay < 0.f) return bad("decay must be finite and not negative");
     if (!mla && q_latent) return bad("q_latent must be NULL for rows of several bands");
-    if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) != 0) return bad("lse must be a 4-byte aligned device pointer");
-    if (!weights->ptr || (reinterpret_cast<uintptr_t>(weights->ptr) & 3) != 0)
-        return bad("weights must be a 4-byte aligned device pointer");
     if (weights->num_reqs < 0 || weights->rows < 0 || (weights->num_reqs > 1 && weights->req_stride < weights->rows))
         return bad("weights: a request's stride is at least its rows");
     cudaStream_t stream = (cudaStream_t)stream_v;
@@ -580,6 +577,9 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     int rc = enter(b, stream, &captured);
     if (rc != LEYLINE_OK) return rc;
     if (b->n_tokens == 0 && !captured) return LEYLINE_OK;
+    if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) != 0) return bad("lse must be a 4-byte aligned device pointer");
+    if (!weights->ptr || (reinterpret_cast<uintptr_t>(weights->ptr) & 3) != 0)
+        return bad("weights must be a 4-byte aligned device pointer");
     // (a replay's plan is checked on the device as well)
     if (captured ? (b->table_reqs > weights->num_reqs || b->table_rows > weights->rows)
                  : (b->weigh_req >= weights->num_reqs || b->weigh_rows > weights->rows))

@@ -307,6 +307,29 @@ void empty_lists()
     check(leyline_evict(f.pool, &f.bt, none, 2, nullptr, 0, &no_rows, f.stream) == LEYLINE_ERR_INVALID_ARG, "rows have weights");
 }
 
+void idle_step()
+{
+    Fixture f;
+    leyline_batch_t* b = nullptr;
+    check(leyline_batch_create(f.pool, 2, 8, 4, &b) == LEYLINE_OK, "creating the batch");
+    check(leyline_batch_plan(b, &f.bt, nullptr, 0, f.stream) == LEYLINE_OK, "a plan without tokens");
+    const leyline_heads_t empty{nullptr, 0, 0};
+    check(leyline_attention(b, 0, &empty, &empty, &empty, nullptr, 1.f, 0, f.stream) == LEYLINE_OK, "attention of no tokens");
+    check(leyline_attention_weights(b, 0, &empty, &empty, nullptr, &f.w, 1.f, 1.f, 0, f.stream) == LEYLINE_OK, "weights of no tokens");
+    const leyline_row_weights_t none{nullptr, 0, 0, 0};
+    check(leyline_attention_weights(b, 0, &empty, &empty, nullptr, &none, 1.f, 1.f, 0, f.stream) == LEYLINE_OK, "weights of no tokens");
+    check(weighings == 0, "nothing is enqueued");
+    const leyline_chunk_t chunk{0, 1, 39, 39};
+    check(leyline_batch_plan(b, &f.bt, &chunk, 1, f.stream) == LEYLINE_OK, "a plan of one token");
+    leyline_heads_t q{f.kv, 4 * 512, 512};
+    check(leyline_attention_weights(b, 0, &q, &q, nullptr, &f.w, 1.f, 1.f, 0, f.stream) == LEYLINE_ERR_INVALID_ARG, "a token has an lse");
+    leyline_row_weights_t null = f.w;
+    null.ptr = nullptr;
+    check(leyline_attention_weights(b, 0, &q, &q, (float*)f.table, &null, 1.f, 1.f, 0, f.stream) == LEYLINE_ERR_INVALID_ARG, "and weights");
+    check(leyline_attention_weights(b, 0, &q, &q, (float*)f.table, &f.w, 1.f, 1.f, 0, f.stream) == LEYLINE_OK && weighings == 1, "weighing it");
+    check(leyline_batch_destroy(b) == LEYLINE_OK, "destroying the batch");
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
@@ -316,6 +339,7 @@ int main(int argc, char** argv)
     else if (name == "freed_pages") freed_pages();
     else if (name == "status_word") status_word();
     else if (name == "empty_lists") empty_lists();
+    else if (name == "idle_step") idle_step();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;

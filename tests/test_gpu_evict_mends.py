@@ -86,3 +86,23 @@ def test_requests_that_keep_no_rows(kw):
     if cache.pending() is not None:
         assert int(cache.pending().abs().sum()) == 0
     cache.close()
+
+
+# ------------------------------------------------------------------- weigh --
+def test_a_step_without_tokens_takes_what_attention_returned():
+    cache = BH.make_cache([100], seed=4, layers=1)
+    b = cache.batch(2, 4, 8)
+    w = fresh_weights(cache)
+    want = w.clone()
+    for chunks in ([], [(0, 100, 0)]):
+        b.plan(chunks)
+        ql, q = queries(cache, 0, 8)
+        out, lse = b.attention(0, ql, q, 0.1)
+        assert tuple(lse.shape) == (0, 8)
+        b.attention_weights(0, ql, q, lse, 0.1, w)
+        b.attention_weights(0, ql, q, lse, 0.1, w[:0])
+    torch.cuda.synchronize()
+    cache.check_status()
+    assert torch.equal(w, want)
+    b.close()
+    cache.close()
