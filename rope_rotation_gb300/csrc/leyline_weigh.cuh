@@ -163,11 +163,12 @@ struct KeyLoader {
     int count = 0;
     bool counted = false;
 
+    // Whether this thread's row is one of a tile of `keys`.
+    __device__ __forceinline__ bool has_row(int keys) const { return lane < kRows && kRows * warp + lane < keys; }
     __device__ __forceinline__ int page_of_row(const WeighReq& r, int key0, int keys) const
     {
-        const int row = kRows * warp + lane;
-        if (lane >= kRows || row >= keys) return INT32_MIN;  // no such row
-        const unsigned u = (unsigned)(key0 + row), B = (unsigned)a.g.block_size;
+        if (!has_row(keys)) return -1;
+        const unsigned u = (unsigned)(key0 + kRows * warp + lane), B = (unsigned)a.g.block_size;
         return a.header->table[(long long)r.req * a.header->max_blocks + (maps.shift >= 0 ? u >> maps.shift : u / B)];
     }
     __device__ __forceinline__ long long slot_at(int page, int key0) const
@@ -183,7 +184,7 @@ struct KeyLoader {
         slot_key = t.key0;
         slot_req = r.req;
         slot = slot_at(page, t.key0);
-        if (slot < 0 && page != INT32_MIN) raise_status(a.status, ST_BAD_PAGE);
+        if (slot < 0 && has_row(t.keys)) raise_status(a.status, ST_BAD_PAGE);
     }
     // The pages of the next tile are read while this one is loaded.  (Asking for its rows in L2 as well, whole, cost more
     // than it gave: 16 decodes of 16 heads over some 24000 rows 107 -> 115 us.)

@@ -106,3 +106,38 @@ def test_a_step_without_tokens_takes_what_attention_returned():
     assert torch.equal(w, want)
     b.close()
     cache.close()
+
+
+PASSING = {  # more than 128 query rows a band, two chunks of one request, items that are cut and joined
+    "mla": (dict(), 20), "mla b1": (dict(B=1), 20), "mla lazy": (dict(flags=LAZY), 20), "mla split": (dict(flags=SPLIT), 7),
+    "mla lazy b1": (dict(flags=LAZY, B=1), 33), "mla 128 heads": (dict(), 128), "mla lazy 150 heads": (dict(flags=LAZY), 150),
+    "grouped": (dict(rope=128, bands=4), 16), "grouped lazy": (dict(rope=128, bands=2, flags=LAZY), 20),
+    "grouped 64 b1": (dict(rope=64, bands=2, B=1), 130), "grouped lazy 256": (dict(rope=256, bands=2, flags=LAZY), 12)}
+CHUNKS = [(0, 200, 40), (1, 100, 30), (0, 250, 20)]  # of requests of 300 and 200 rows
+
+
+@pytest.mark.parametrize("shape", ["mla", "mla lazy b1", "grouped", "grouped 64 b1"])
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_a_table_entry_of_any_value_is_reported(shape, tokens):
+    """The smallest number of all is a bad page like any other, where queries stay and where they pass."""
+    from rope_rotation_gb300.leyline import LeylineError
+    kw, per_band = PASSING[shape]
+    cache = BH.make_cache([300], seed=6, layers=1, **kw)
+    heads = min(per_band, 64) * cache.rope_heads
+    b = cache.batch(1, tokens, heads)
+    b.plan([(0, 300 - tokens, tokens)])
+    b.append(0, BH.bf16(tokens, cache.row))
+    ql, q = queries(cache, tokens, heads)
+    lse = torch.ones(tokens, heads, device="cuda")
+    w = fresh_weights(cache)
+    b.attention_weights(0, ql, q, lse, 0.1, w)
+    cache.check_status()
+    held = cache.table[0, 3].item()
+    cache.table[0, 3] = -2 ** 31
+    b.attention_weights(0, ql, q, lse, 0.1, w)
+    with pytest.raises(LeylineError) as e:
+        cache.check_status()
+    assert e.value.code == -8
+    cache.table[0, 3] = held
+    b.close()
+    cache.close()
