@@ -302,7 +302,9 @@ void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::v
     }
     int64_t units = 0;  // products of all tiles of cache rows
     for (size_t k = header->weigh_stay; k < reqs->size(); ++k) units += (*reqs)[k].units * ceil_div((*reqs)[k].end, kPairKeys);
-    header->weigh_seg = (int32_t)std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs));
+    // (no request has more than 2^31 - 1 products of a tile: a longer segment is all of them)
+    header->weigh_seg = (int32_t)std::min<int64_t>(
+        INT32_MAX, std::max<int64_t>(kWeighMinSeg, ceil_div(units, (int64_t)kWeighItems * w.pairs)));
     int32_t parts = 0;
     for (size_t k = 0; k < reqs->size(); ++k) {
         WeighReq& r = (*reqs)[k];
