@@ -279,9 +279,8 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
 
     PlanMark mark;
     mark.table = bt->table;
-    for (const ChunkDev& c : cp.chunks)
-        if (c.n > 0) mark.reqs.push_back(c.req);
-    std::sort(mark.reqs.begin(), mark.reqs.end());
+    mark.reqs.reserve(cp.weigh.size());
+    for (const WeighReq& r : cp.weigh) mark.reqs.push_back(r.req);
     mark.since_checkpoint = true;
 
     const int slot = b->next_slot;

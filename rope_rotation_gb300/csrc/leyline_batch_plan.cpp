@@ -83,9 +83,14 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
     const int64_t cap = (int64_t)bt.max_blocks * g.block_size;
     struct Req {
         int64_t old_len, len, pop, last_run;
+        int32_t req;
     };
-    std::vector<int32_t> order(n);
-    std::vector<int32_t> req_of;  // requests of the plan, sorted
+    auto before = [&](int32_t x, int32_t y) {
+        const leyline_chunk_t &a = chunks[x], &c = chunks[y];
+        return a.req != c.req ? a.req < c.req : a.start != c.start ? a.start < c.start : a.n < c.n;
+    };
+    std::vector<int32_t> order(n);  // of the chunks by their requests and rows
+    bool ordered = true;
     for (int32_t k = 0; k < n; ++k) {
         const leyline_chunk_t& c = chunks[k];
         order[k] = k;
@@ -96,22 +101,24 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
         }
         out->tokens += c.n;
         if (out->tokens > max_tokens) return bad("more tokens than the batch holds");
-        req_of.push_back(c.req);
+        ordered = ordered && (k == 0 || !before(k, k - 1));
     }
-    std::sort(req_of.begin(), req_of.end());
-    req_of.erase(std::unique(req_of.begin(), req_of.end()), req_of.end());
-    std::vector<Req> reqs(req_of.size());
-    auto find = [&](int32_t req) -> Req& {
-        return reqs[std::lower_bound(req_of.begin(), req_of.end(), req) - req_of.begin()];
-    };
-    for (size_t i = 0; i < reqs.size(); ++i) {
-        const int64_t len = bt.seq_lens_host[req_of[i]];
-        if (len < 0 || len > cap) return bad("seq_lens_host entry outside [0, max_blocks * block_size]");
-        reqs[i] = Req{len, len, -1, -1};
+    if (!ordered) std::sort(order.begin(), order.end(), before);
+    std::vector<Req> reqs;             // of the plan, ascending
+    std::vector<int32_t> req_of(n);    // of each chunk, in reqs
+    reqs.reserve(n);
+    for (int32_t k : order) {
+        const int32_t req = chunks[k].req;
+        if (reqs.empty() || reqs.back().req != req) {
+            const int64_t len = bt.seq_lens_host[req];
+            if (len < 0 || len > cap) return bad("seq_lens_host entry outside [0, max_blocks * block_size]");
+            reqs.push_back(Req{len, len, -1, -1, req});
+        }
+        req_of[k] = (int32_t)reqs.size() - 1;
     }
     for (int32_t k = 0; k < n; ++k) {
         const leyline_chunk_t& c = chunks[k];
-        Req& r = find(c.req);
+        Req& r = reqs[req_of[k]];
         if (c.start > r.len) {
             snprintf(msg, sizeof msg, "chunk %d: start %lld is past the request's length %lld", k, (long long)c.start,
                      (long long)r.len);
@@ -123,33 +130,42 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
         if (c.n > 0 && c.start < r.old_len) out->rewrites = true;
         r.len = std::max(r.len, c.start + c.n);
     }
-    // rows of one request's chunks may not overlap
-    std::sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
-        const leyline_chunk_t &a = chunks[x], &c = chunks[y];
-        return a.req != c.req ? a.req < c.req : a.start != c.start ? a.start < c.start : a.n < c.n;
-    });
-    int32_t before = -1;  // the last chunk with rows
+    // rows of one request's chunks may not overlap; they are linked in the order of their rows
+    out->chunks.assign(n, ChunkDev{0, 0, 0, -1, 0});
+    out->weigh.reserve(reqs.size());
+    int32_t last = -1;  // the last chunk with rows
     for (int32_t k : order) {
         const leyline_chunk_t& c = chunks[k];
         if (c.n == 0) continue;
-        if (before >= 0 && chunks[before].req == c.req && c.start < chunks[before].start + chunks[before].n) {
-            snprintf(msg, sizeof msg, "chunks %d and %d share rows of request %d", before, k, c.req);
+        const bool more = last >= 0 && chunks[last].req == c.req;
+        if (more && c.start < chunks[last].start + chunks[last].n) {
+            snprintf(msg, sizeof msg, "chunks %d and %d share rows of request %d", last, k, c.req);
             return bad(msg);
         }
-        before = k;
+        if (more) {
+            out->chunks[last].next = k;
+            out->weigh.back().end = c.start + c.n;
+        } else {
+            out->weigh.push_back(WeighReq{c.req, k, c.start + c.n, 0, 0, 0, 0, 0});
+        }
+        last = k;
     }
-    for (size_t i = 0; i < reqs.size(); ++i) {
-        Req& r = reqs[i];
+    for (Req& r : reqs) {
         r.pop = pop_base + out->pages;
         out->pages += ceil_div(r.len, g.block_size) - ceil_div(r.old_len, g.block_size);
-        if (r.len != r.old_len) out->new_len.emplace_back(req_of[i], r.len);
+        if (r.len != r.old_len) out->new_len.emplace_back(r.req, r.len);
     }
     if (out->pages > free_pages) return set_error(LEYLINE_ERR_NO_PAGES, "not enough free pages for the chunks' rows");
     int32_t tok = 0;
+    out->runs.reserve(n + out->tokens / kPlanRun);
     for (int32_t k = 0; k < n; ++k) {
         const leyline_chunk_t& c = chunks[k];
-        Req& r = find(c.req);
-        out->chunks.push_back(ChunkDev{c.req, c.n, tok, -1, c.start});
+        Req& r = reqs[req_of[k]];
+        ChunkDev& d = out->chunks[k];
+        d.req = c.req;
+        d.n = c.n;
+        d.tok0 = tok;
+        d.start = c.start;
         for (int32_t t = 0; t < c.n; t += kPlanRun) {
             r.last_run = (int64_t)out->runs.size();
             out->runs.push_back(PlanRun{c.req, std::min(kPlanRun, c.n - t), tok + t,
@@ -157,16 +173,6 @@ int check_chunks(const Geometry& g, const leyline_block_table_t& bt, const leyli
                                         r.pop, -1});
         }
         tok += c.n;
-    }
-    out->weigh.reserve(order.size());
-    before = -1;
-    for (int32_t k : order) {
-        const ChunkDev& c = out->chunks[k];
-        if (c.n == 0) continue;
-        if (before >= 0 && out->chunks[before].req == c.req) out->chunks[before].next = k;
-        else out->weigh.push_back(WeighReq{c.req, k, 0, 0, 0, 0, 0, 0});
-        out->weigh.back().end = c.start + c.n;
-        before = k;
     }
     for (const Req& r : reqs)
         if (r.last_run >= 0 && r.len != r.old_len) out->runs[r.last_run].new_len = r.len;
