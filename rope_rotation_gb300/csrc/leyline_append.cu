@@ -29,8 +29,10 @@ __global__ void __launch_bounds__(kInstallThreads) install_plan_kernel(const __g
     if ((int)blockIdx.x >= a.n_runs) {
         const long long ctas = gridDim.x - a.n_runs;
         for (long long i = (blockIdx.x - a.n_runs) * (long long)blockDim.x + threadIdx.x; i < a.plan_vecs;
-             i += ctas * blockDim.x)
-            a.plan[i] = a.staged[i];
+             i += ctas * blockDim.x) {
+            const long long at = i < a.gap_at ? i : i + a.gap;
+            a.plan[at] = a.staged[at];
+        }
         return;
     }
     const PlanRun r = a.runs[blockIdx.x];

@@ -65,7 +65,8 @@ namespace {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The plan's device buffer: header, chunks, per-CTA ranges, joins and requests, and last the items, of which a plan copies its own.
+// The plan's device buffer: header, chunks, per-CTA ranges, joins, and last the requests and the items, of which a plan copies
+// its own.
 BatchLayout make_layout(int32_t max_chunks, int64_t max_tiles, int32_t ctas)
 {
     BatchLayout l;
@@ -310,7 +311,10 @@ int plan_batch(leyline_batch_t* b, leyline_block_table_t* bt, const leyline_chun
     a.staged = reinterpret_cast<const uint4*>(h);
     a.plan = reinterpret_cast<uint4*>(b->d_plan);
     a.runs = reinterpret_cast<const PlanRun*>(h + l.bytes);
-    a.plan_vecs = (int64_t)((l.items + sizeof(AttnItem) * (size_t)split.n_items) / 16);
+    // of the requests' work and of the items those that the plan has
+    a.gap_at = (int64_t)(align_up(l.weigh + sizeof(WeighReq) * cp.weigh.size(), 16) / 16);
+    a.gap = (int64_t)(l.items / 16) - a.gap_at;
+    a.plan_vecs = (int64_t)((l.items + sizeof(AttnItem) * (size_t)split.n_items) / 16) - a.gap;
     a.n_runs = (int32_t)cp.runs.size();
     a.max_blocks = bt->max_blocks;
     a.table = bt->table;

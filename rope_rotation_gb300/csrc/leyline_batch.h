@@ -220,7 +220,8 @@ struct InstallArgs {
     const uint4* staged;   // pinned plan, copied to plan
     uint4* plan;
     const PlanRun* runs;   // pinned
-    int64_t plan_vecs;
+    int64_t plan_vecs;     // to copy, without
+    int64_t gap_at, gap;   // `gap` of them from vector gap_at on
     int32_t n_runs;
     int32_t max_blocks;
     int32_t* table;

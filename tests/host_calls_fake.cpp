@@ -27,6 +27,7 @@ namespace {
 std::map<uintptr_t, size_t> device_memory;
 bool legacy_pending = false;  // work of the legacy stream may still run
 int unordered = 0;            // kernels launched on another stream meanwhile
+int64_t copied_vecs = 0;      // of the last plan
 int copies_in = 0, selects = 0, evictions = 0, weighings = 0;
 std::vector<ListState> seen_state;  // of the last eviction, both arrays
 
@@ -180,7 +181,11 @@ int rotate_in_place_blocks_per_sm(int* n) { return *n = 1, 0; }
 int bulk_prepare(int32_t, int* n) { return *n = 1, 0; }
 int launch_install(const InstallArgs& a, void* s)
 {
-    for (int64_t i = 0; i < a.plan_vecs; ++i) a.plan[i] = a.staged[i];
+    for (int64_t i = 0; i < a.plan_vecs; ++i) {
+        const int64_t at = i < a.gap_at ? i : i + a.gap;
+        a.plan[at] = a.staged[at];
+    }
+    copied_vecs = a.plan_vecs;
     return launched(s);
 }
 int launch_append(const AppendArgs&, int64_t, int, void* s) { return launched(s); }
@@ -330,6 +335,21 @@ void idle_step()
     check(leyline_batch_destroy(b) == LEYLINE_OK, "destroying the batch");
 }
 
+void plan_copies()
+{
+    Fixture f;
+    const leyline_chunk_t chunks[2] = {{0, 1, 39, 39}, {1, 1, 8, 8}};
+    int64_t vecs[2];
+    for (int32_t room : {2, 4096}) {
+        leyline_batch_t* b = nullptr;
+        check(leyline_batch_create(f.pool, room, 8, 4, &b) == LEYLINE_OK, "creating the batch");
+        check(leyline_batch_plan(b, &f.bt, chunks, 2, f.stream) == LEYLINE_OK, "a plan of two tokens");
+        vecs[room > 2] = copied_vecs;
+        check(leyline_batch_destroy(b) == LEYLINE_OK, "destroying the batch");
+    }
+    check(16 * (vecs[1] - vecs[0]) <= (int64_t)sizeof(ChunkDev) * 4094 + 64, "a plan copies the work of its own requests");
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
@@ -340,6 +360,7 @@ int main(int argc, char** argv)
     else if (name == "status_word") status_word();
     else if (name == "empty_lists") empty_lists();
     else if (name == "idle_step") idle_step();
+    else if (name == "plan_copies") plan_copies();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;
