@@ -116,6 +116,102 @@ PASSING = {  # more than 128 query rows a band, two chunks of one request, items
 CHUNKS = [(0, 200, 40), (1, 100, 30), (0, 250, 20)]  # of requests of 300 and 200 rows
 
 
+def passing(shape):
+    kw, per_band = PASSING[shape]
+    cache = BH.make_cache([300, 200], seed=5, layers=1, **kw)
+    heads = per_band * cache.rope_heads
+    if cache.pending() is not None:
+        cache.pending().random_(-300, 300)
+    b = cache.batch(4, 90, heads)
+    b.plan(CHUNKS)
+    b.append(0, BH.bf16(90, cache.row, seed=8))
+    ql, q = queries(cache, 90, heads, seed=9)
+    lse = 2 + torch.rand(90, heads, device="cuda")
+    return cache, b, heads, ql, q, lse
+
+
+@pytest.mark.parametrize("shape", PASSING)
+def test_rows_that_hold_nothing_where_queries_pass(shape):
+    cache, b, heads, ql, q, lse = passing(shape)
+    for req, n in ((0, 270), (1, 130)):  # rows behind the chunks
+        flat = torch.from_numpy(cache.slot_index(req, np.arange(n, int(cache.seq_lens_host[req])))).cuda()
+        bad = torch.full((len(flat), cache.row), NAN, device="cuda", dtype=torch.bfloat16)
+        bad[::2] = INF
+        cache.write_layer_rows(0, flat, bad)
+    scale = 0.1
+    for what in ("some heads", "a token", "a chunk"):
+        holes = torch.zeros(90, heads, dtype=torch.bool, device="cuda")
+        if what == "some heads":
+            holes[::3, ::2] = True
+        elif what == "a token":
+            holes[[0, 39, 40, 89]] = True
+        else:
+            holes[40:70] = True
+        x = lse.clone()
+        x[holes] = -INF
+        no = q.clone()  # queries that attend to nothing may hold anything
+        no[holes] = NAN
+        nol = None if ql is None else torch.where(holes[..., None], torch.full_like(ql, INF), ql)
+        for decay, prefix in ((1.0, False), (0.0, True)):
+            w = fresh_weights(cache, seed=1)
+            if decay == 0.0:
+                w.fill_(NAN)
+            check_weigh(cache, b, 0, CHUNKS, nol, no, x, scale, w, decay, prefix, f"{shape} {what}")
+            assert bool(w[0, :270].isfinite().all()) and bool(w[1, :130].isfinite().all())
+        y = lse.clone()
+        y[holes] = INF  # so high that nothing is left
+        w1, w2 = fresh_weights(cache, seed=2), fresh_weights(cache, seed=2)
+        b.attention_weights(0, ql, q, y, scale, w1)
+        b.attention_weights(0, ql, q, x, scale, w2)
+        assert torch.equal(w1, w2), what
+    # attended rows that are not finite spoil their own weights alone
+    rows = np.array([17, 255, 256, 269])
+    flat = torch.from_numpy(cache.slot_index(0, rows)).cuda()
+    cache.write_layer_rows(0, flat, torch.full((4, cache.row), NAN, device="cuda", dtype=torch.bfloat16))
+    w3 = fresh_weights(cache, seed=2)
+    b.attention_weights(0, ql, q, x, scale, w3)
+    spoilt = torch.zeros_like(w3, dtype=torch.bool)
+    spoilt[0, torch.from_numpy(rows).cuda()] = True
+    assert bool(w3[spoilt].isnan().all()) and torch.equal(w3[~spoilt], w2[~spoilt])
+    torch.cuda.synchronize()
+    cache.check_status()
+    b.close()
+    cache.close()
+
+
+@pytest.mark.parametrize("shape", PASSING)
+def test_bad_pages_where_queries_pass(shape):
+    """In a full tile of 256 rows and in a partial one: the rows of the page keep their weights, all others get theirs."""
+    from rope_rotation_gb300.leyline import LeylineError
+    cache, b, heads, ql, q, lse = passing(shape)
+    B = cache.block_size
+    old = fresh_weights(cache, seed=4)
+    want = old.clone()
+    b.attention_weights(0, ql, q, lse, 0.1, want)
+    cache.check_status()
+    for row in (48, 258):
+        blk = row // B
+        held = cache.table[0, blk].item()
+        for page in (-1, cache.num_pages, 2 ** 31 - 1):
+            cache.table[0, blk] = page
+            got = old.clone()
+            b.attention_weights(0, ql, q, lse, 0.1, got)
+            with pytest.raises(LeylineError) as e:
+                cache.check_status()
+            assert e.value.code == -8
+            gone = torch.zeros_like(got, dtype=torch.bool)
+            gone[0, blk * B:(blk + 1) * B] = True
+            assert torch.equal(got[gone], old[gone]) and torch.equal(got[~gone], want[~gone])
+        cache.table[0, blk] = held
+    got = old.clone()
+    b.attention_weights(0, ql, q, lse, 0.1, got)
+    torch.cuda.synchronize()
+    cache.check_status()
+    assert torch.equal(got, want)
+    b.close()
+    cache.close()
+
+
 @pytest.mark.parametrize("shape", ["mla", "mla lazy b1", "grouped", "grouped 64 b1"])
 @pytest.mark.parametrize("tokens", [1, 40])
 def test_a_table_entry_of_any_value_is_reported(shape, tokens):
