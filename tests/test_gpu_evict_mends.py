@@ -237,3 +237,67 @@ def test_a_table_entry_of_any_value_is_reported(shape, tokens):
     cache.table[0, 3] = held
     b.close()
     cache.close()
+
+
+# ---------------------------------------------------------------- accuracy --
+NEAR = {
+    "mla": dict(), "mla b1": dict(B=1), "mla split": dict(flags=SPLIT), "mla lazy": dict(flags=LAZY),
+    "mla lazy b1 pairs": dict(flags=LAZY, B=1, pair_layout=1), "mla lazy split": dict(flags=LAZY | SPLIT, B=8),
+    "grouped 64": dict(rope=64, bands=4), "grouped 64 lazy": dict(rope=64, bands=4, flags=LAZY),
+    "grouped 128": dict(rope=128, bands=4), "grouped 128 lazy": dict(rope=128, bands=4, flags=LAZY),
+    "grouped 256": dict(rope=256, bands=2), "grouped 256 lazy pairs": dict(rope=256, bands=2, flags=LAZY, pair_layout=1),
+    "odd": dict(latent=72, rope=48), "odd bands lazy": dict(latent=96, rope=96, bands=3, flags=LAZY)}
+
+
+@pytest.mark.parametrize("shape", NEAR)
+@pytest.mark.parametrize("per_band", [1, 16, 40, 72, 128])
+def test_weights_are_near_those_of_64_bits(shape, per_band):
+    """In the 2-norm over a request's rows, within 2^-16: keys of 1 to 10 blocks of 64 columns by 1 to 128 query rows a band,
+    which stay, and by some more, which pass.
+
+    Inputs are N(0, 1) and scores of standard deviation 1, so the largest weights, which the norm goes by, have scores up to
+    5 and an lse of some 3.  An accumulator of the matrix unit that cuts its sum off at each of its up to 40 steps loses up to
+    2^-23 of it a step; it grows from 0 to the score, so 40 * 2^-23 * 5 / 2 = 1.2e-5 at most, every step cut by a whole bit.  The
+    exponent is rounded three times, 2^-24 of 8 each, 1.4e-6, the exponential and the sum add 2^-21.  A lazy band is the
+    sum of two bf16 values, off by 2^-18 of a pair at most and with both signs: over 64 products of the band alone 8 *
+    2^-18 / 8 = 3.8e-6 of a score's standard deviation, mostly averaged out over queries.  With one bf16 value instead it
+    would be 2e-3 (where queries stay), and 1e-4 over 130 queries."""
+    kw = NEAR[shape]
+    lens = [1500, 700, 130]
+    cache = BH.make_cache(lens, extra=0, seed=7, layers=1, **kw)
+    heads = per_band * cache.rope_heads
+    few = [(r, n - 1, 1) for r, n in enumerate(lens)]
+    many = -(-130 // per_band)  # tokens of more than 128 query rows a band
+    some = [(r, n - many, many) for r, n in enumerate(lens) if n > many]
+    turns = torch.randint(-4000, 300, cache.pending().shape, device="cuda", dtype=torch.int32) if cache.pending() is not None else None
+    for chunks in (few, some):
+        n = sum(c[2] for c in chunks)
+        b = cache.batch(3, n, heads)
+        b.plan(chunks)
+        if turns is not None:
+            torch.cuda.synchronize()
+            cache.pending().copy_(turns)
+        for band_alone in (False, True):
+            if cache.rope_heads > 1 and band_alone:
+                continue
+            ql, q = queries(cache, n, heads, seed=10)
+            d = cache.rope_dim
+            if ql is not None and band_alone:
+                ql.zero_()
+            elif ql is not None:
+                d += cache.latent_dim
+            scale = d ** -0.5
+            lse = 3 + torch.rand(n, heads, device="cuda")
+            w = torch.full((3, cache.table.shape[1] * cache.block_size), NAN, device="cuda")
+            want, tol, written = weights64(cache, 0, chunks, ql, q, lse, scale, w, 0.0, pair_layout=kw.get("pair_layout", 0))
+            b.attention_weights(0, ql, q, lse, scale, w, 0.0)
+            torch.cuda.synchronize()
+            cache.check_status()
+            for req, start, m in chunks:
+                on = written[req]
+                got, ref = w[req][on].double(), want[req][on]
+                off = float((got - ref).norm() / ref.norm())
+                assert off <= 2.0 ** -16, f"{shape} {per_band} {m} tokens, request {req}, band alone {band_alone}: {off}"
+                assert bool(((got - ref).abs() <= tol[req][on]).all())
+        b.close()
+    cache.close()
