@@ -13,8 +13,9 @@
 //
 // What bounds it is the tensor cores: 512 tokens of 128 heads over 8192 rows in 365 to 394 us, 0.80 to 0.86 of cuBLAS's rate
 // for what the causal mask leaves.  The exponentials, 128 a thread and product, take nearly as long as a product and run
-// beside the next one, in the other half of TMEM: a product has one accumulator, and its weights are 1.6e-6 off 64 bits at most
-// (2-norm, relative; see Buffers in leyline_weigh_tile.cu).  Two accumulators for products of half as many columns: 595 us.
+// beside the next one, in the other half of TMEM: a product has one accumulator, and its weights are 5e-7 off 64 bits at most
+// (2-norm, relative; 1.6e-6 if exponent_scale did not make up for what it cuts off).  Two accumulators for products of half as
+// many columns: 595 us.
 // 64 tokens of 16 heads over 32768 rows take 37 us, 20 of them at the tensor cores' rate: 128 items are two for some of the 76
 // pairs, and each waits for its keys.
 //
@@ -293,6 +294,7 @@ struct Summer {
     Misc* m;
     uint32_t tmem, rank;
     int warp, lane;
+    float scale2;   // of the exponents
     int index = 0;  // of the unit to be summed
     bool waiting = false, cut = false;
     int n = 0, cols = 0, key0 = 0, keys = 0;
@@ -331,7 +333,7 @@ struct Summer {
         mbar_wait_cluster(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * quarter < keys && cols > 0)
-            sum += sum_columns(tmem + buf * kCols + ((uint32_t)(32 * quarter) << 16) + from, padded(cols), cols, a.scale * kLog2e,
+            sum += sum_columns(tmem + buf * kCols + ((uint32_t)(32 * quarter) << 16) + from, padded(cols), cols, scale2,
                                m->neg[buf] + from, m->limit[buf] + from, key0 + 32 * quarter + lane, masked);
         tcgen05_before_sync();
         __syncwarp();
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
     s.stay_bytes = s.chunks * kChunkBytes;
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / kChunkBytes);
     if (warp < kMmaWarp) {
-        Summer role{a, s, m, tmem, rank, warp, lane};
+        Summer role{a, s, m, tmem, rank, warp, lane, exponent_scale(a.scale, 4 * s.chunks)};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {

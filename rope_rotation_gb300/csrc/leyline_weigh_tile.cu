@@ -127,9 +127,10 @@ __device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps&
 
 // The buffers of S^T, used in turn: with two of them grouped rows, whose bands have a product each, waited for their sums.
 // A buffer is of several accumulators, each for a part of the key's chunks: an accumulator's error grows with its steps and
-// with what it has come to (as that of sums cut off toward zero would), and the 36 steps of an MLA key in one took the weights
-// of one token 1.2e-6 off 64 bits (2-norm, relative), next to 4e-7 in three.  The time is the same: 16 decodes of 128
-// heads over some 24000 rows 104 us with one and with two.  A band alone, of at most 16 steps, has one.
+// with what it has come to, most of it a loss that exponent_scale makes up for.  Before that the 36 steps of an MLA key in one took
+// the weights of one token 1.2e-6 off 64 bits (2-norm, relative), next to 3 to 6e-7 in three; now three are 1.2e-7 off.  The time is
+// the same: 16 decodes of 128 heads over some 24000 rows 104 us with one and with two.  A band alone, of at most 16
+// steps, has one.
 struct Buffers {
     int cols, chunks, parts, count;  // chunks: of a part
     int at = 0;
@@ -388,6 +389,7 @@ struct Summer {
     Buffers buf;
     uint32_t rank;
     int warp, lane;
+    float scale2;  // of the exponents
     int open = 0;  // rows below it are attended to by every column
     float sum = 0.f;
     int page = -1;  // of this thread's row of the tile, and its weight before
@@ -432,7 +434,7 @@ struct Summer {
             const uint32_t at = tmem + buf.column() + ((uint32_t)(32 * warp) << 16);
             const int n = padded(u.cols), key = t.key0 + 32 * warp + lane;
             const bool masked = t.key0 + t.keys > open;
-            const float scale2 = a.scale * kLog2e, *l = neg + u.band * cols;
+            const float* l = neg + u.band * cols;
             const int* end = limit + u.band * cols;
             sum += buf.parts == 4   ? sum_columns<4>(at, n, u.cols, scale2, l, end, key, masked, cols)
                    : buf.parts == 3 ? sum_columns<3>(at, n, u.cols, scale2, l, end, key, masked, cols)
@@ -496,8 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
-        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, Buffers(cols, s),
-                    rank, warp, lane};
+        const Buffers buffers(cols, s);
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, buffers,
+                    rank, warp, lane, exponent_scale(a.scale, 4 * s.chunks / buffers.parts)};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {

@@ -301,3 +301,51 @@ def test_weights_are_near_those_of_64_bits(shape, per_band):
                 assert bool(((got - ref).abs() <= tol[req][on]).all())
         b.close()
     cache.close()
+
+
+@pytest.mark.parametrize("kw,per_band,tokens", [
+    (dict(), 20, 8), (dict(B=1), 128, 6), (dict(flags=LAZY), 20, 8), (dict(), 1, 1), (dict(), 16, 1), (dict(), 128, 1), (dict(B=1), 96, 1),
+    (dict(rope=256, bands=2), 20, 8), (dict(rope=256, bands=2), 8, 1), (dict(rope=128, bands=4), 20, 8), (dict(rope=64, bands=4), 3, 1)])
+def test_scores_are_not_biased(kw, per_band, tokens):
+    """The logarithm of a weight that one query alone gives is its score x.  Over rows with scores of many sizes and both signs,
+    |x| above an eighth of the largest, x is off by less than 2^-22 of itself in the mean.
+
+    An accumulator of the matrix unit cuts off half of its last bit a step on average, 0.72 * 2^-24 of what it holds; over n steps
+    that add up to x evenly (n + 1) / 2 times that at most, 8e-7 x for the 36 of an MLA key.  The kernels make up for 1.75e-8 (n - 1),
+    6.1e-7 x.  So x is 1.9e-7 too small at most, and if nothing were cut off in the first half of the steps 1.5e-7 too large.
+    2^-22 is 2.4e-7.  The factor's rounding adds 2^-25, and what differs from row to row averages out.  (One accumulator for MLA keys was
+    6.7e-7 too small, two 3.2e-7.)"""
+    n = 4096
+    cache = BH.make_cache([n], seed=1, layers=1, **kw)
+    heads, lat, d = per_band * cache.rope_heads, cache.latent_dim, cache.rope_dim
+    mla = cache.rope_heads == 1
+    b = cache.batch(1, tokens, heads)
+    b.plan([(0, n - tokens, tokens)])
+    g = torch.Generator(device="cuda").manual_seed(5)
+    width = d + (lat if mla else 0)
+    query = torch.randn(width, generator=g, device="cuda").bfloat16()
+    keys = (torch.linspace(-1.5, 1.5, n, device="cuda")[:, None] * query.float()
+            + 0.7 * torch.randn(n, width, generator=g, device="cuda")).bfloat16()
+    flat = torch.from_numpy(cache.slot_index(0, np.arange(n))).cuda()
+    rows = BH.bf16(n, cache.row, seed=2)
+    rows[:, 0 if mla else lat:(0 if mla else lat) + width] = keys
+    cache.write_layer_rows(0, flat, rows)
+    ql, q = queries(cache, tokens, heads, seed=3)
+    if mla:
+        ql[0, 0] = query[:lat]
+    q[0, 0] = query[-d:]
+    lse = torch.full((tokens, heads), INF, device="cuda")
+    lse[0, 0] = 0.0
+    scale = 2.0 ** -5  # exact
+    w = torch.zeros(1, cache.table.shape[1] * cache.block_size, device="cuda")
+    b.attention_weights(0, ql, q, lse, scale, w, 0.0)
+    torch.cuda.synchronize()
+    cache.check_status()
+    seen = n - tokens + 1
+    want = (keys.double() @ query.double())[:seen]
+    got = w[0, :seen].double().log() / scale
+    on = want.abs() > want.abs().max() / 8
+    off = float(((got - want) / want)[on].mean())
+    assert abs(off) < 2.0 ** -22, f"{kw} {per_band} {tokens}: {off}"
+    b.close()
+    cache.close()
