@@ -10,10 +10,10 @@
 // for each (request, layer, slice of a row's columns), and the chains run side by side.
 //
 // What bounds it is HBM with pieces of 128 bytes: half of 32768 rows of 27 layers kept in 176 us for one request and 686 for
-// four, 90% of 16 requests of some 8000 rows of 4 layers, lazy, in 237 (0.86, 0.88 and 0.84 of the measured copy rate, with
+// four, 90% of 16 requests of some 10000 rows of 4 layers, lazy, in 237 (0.86, 0.88 and 0.84 of the measured copy rate, with
 // the two small kernels around it).  With few layers it is a chain's latency, 1.4 us a batch of rows whatever its size: one
 // layer of the first 100 us.  Slices of 64 bytes then take 10% less, but 30% more in 27 layers, and so do 256 bytes.  One row
-// a page, 16 requests of some 24000 rows: 17 us, the latency of two kernels.
+// a page, 16 requests of some 30000 rows: 17 us, the latency of two kernels.
 #include "leyline_device.cuh"
 #include "leyline_evict.h"
 

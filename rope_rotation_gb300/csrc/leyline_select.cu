@@ -10,7 +10,7 @@
 // through distributed shared memory, and the CTAs' counts of rows taken give each the place of its part of the list.
 //
 // What bounds it is latency, the barriers of up to four digits and of the list: one request of 4096 rows 8 us, 16 of some
-// 24000 rows 23, 8 of 131072 rows 32, where a pass over the weights takes 0.6.  From 4 rows a thread on a request gets more
+// 30000 rows 23, 8 of 131072 rows 32, where a pass over the weights takes 0.6.  From 4 rows a thread on a request gets more
 // CTAs.
 #include <cooperative_groups.h>
 

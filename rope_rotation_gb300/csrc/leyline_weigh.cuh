@@ -187,7 +187,7 @@ struct KeyLoader {
         if (slot < 0 && has_row(t.keys)) raise_status(a.status, ST_BAD_PAGE);
     }
     // The pages of the next tile are read while this one is loaded.  (Asking for its rows in L2 as well, whole, cost more
-    // than it gave: 16 decodes of 16 heads over some 24000 rows 107 -> 115 us.)
+    // than it gave: 16 decodes of 16 heads over some 30000 rows 107 -> 115 us.)
     __device__ __forceinline__ void look_ahead(const WeighReq& r, const Tile& t)
     {
         next_page = page_of_row(r, t.key0, t.keys);
@@ -198,7 +198,7 @@ struct KeyLoader {
     // cos and sin of c * theta_j: the angle in turns in fp64, less its whole ones, then in fp32.  They are off by 2^-22 of the
     // pair, where the scores carry a turned band to 2^-17.  (The product of the pool's two tables, in fp64, takes two loads
     // from L2 for each pair, and every warp was held up by it wherever the count changed: 64 decodes of 16 heads over some
-    // 4000 rows, one a page, 157 us instead of 129.)
+    // 5000 rows, one a page, 157 us instead of 129.)
     __device__ __forceinline__ void ensure(int c)
     {
         if (counted && c == count) return;
@@ -244,7 +244,7 @@ struct KeyLoader {
     // ... and once they have landed turned there; what their rounding to bf16 leaves goes to the planes behind them.  Half-split
     // pairs: chunk c0 alone holds both halves of its pairs, or c0 and c1 the first and the second ones.  By pairs of rows,
     // whose chains run side by side.  (Held in registers from one tile to the next the bands spilled, and the spills waited
-    // for their loads: 16 decodes of 16 heads over some 24000 rows 256 us.)
+    // for their loads: 16 decodes of 16 heads over some 30000 rows 256 us.)
     template <bool kSplit, bool kTwo>
     __device__ __forceinline__ void turn_as(int c0, int c1, uint32_t dst, int pitch, const int* counts)
     {

@@ -11,13 +11,16 @@
 // request's query tiles are cut into segments a second kernel adds their sums up, in order.  Query tiles whose tokens all
 // lie before an item's cache rows are left out.
 //
-// What bounds it is the tensor cores: 512 tokens of 128 heads over 8192 rows in 365 to 394 us, 0.80 to 0.86 of cuBLAS's rate
+// What bounds it is the tensor cores: 512 tokens of 128 heads over 8192 rows in 365 us back to back, 397 a call whose queries
+// come from HBM, 0.80 to 0.86 of cuBLAS's rate
 // for what the causal mask leaves.  The exponentials, 128 a thread and product, take nearly as long as a product and run
 // beside the next one, in the other half of TMEM: a product has one accumulator, and its weights are 5e-7 off 64 bits at most
 // (2-norm, relative; 1.6e-6 if exponent_scale did not make up for what it cuts off).  Two accumulators for products of half as
 // many columns: 595 us.
 // 64 tokens of 16 heads over 32768 rows take 37 us, 20 of them at the tensor cores' rate: 128 items are two for some of the 76
-// pairs, and each waits for its keys.
+// pairs and one for others (the tensor cores 30 to 61% active, SM by SM), and each waits for its keys.
+// Narrow keys are bound by the sums: 512 tokens of 32 heads on 4 bands of 128 over 8192 rows take 89 us, 18 of them at the tensor
+// cores' rate and 28 at the exponentials'; a product of 8 steps is done long before the 128 columns a thread of the one before.
 //
 // Roles in each CTA: warps 0-3 sum the first query tile's columns, warps 4-7 the second's, warp 8 issues the products (in
 // the first CTA alone), warp 9 asks for the queries (TMA boxes, one lane), warps 10-13 bring the keys, 32 rows each, and

@@ -11,11 +11,15 @@
 // whatever its size, so boxes of one plane of 16 rows, 72 for 128 MLA rows, bound the kernel.  The pairs take equal shares
 // of 32 rows.
 //
-// What bounds it is HBM: 16 requests decode over some 24000 rows in 95 us with 16 heads, 97 with 64, 105 with 128 (0.88 to
+// What bounds it is HBM: 16 requests decode over some 30000 rows in 95 us with 16 heads, 97 with 64, 105 with 128 (0.88 to
 // 0.79 of the measured copy rate; the products 40 us of it); rows that are copied one by one (one a page) 110.  With few rows
 // it is the chain of waits of one tile, page, keys, products, sums: one request of 4096 rows 10 us, half of it the call's.
-// Grouped rows have a product and sums of 32 columns for each band of 256 rows, 16 requests of some 8000 rows 45 us, 0.56 of
-// the copy rate; lazy pools turn every band again, 64 decodes over some 4000 rows, one a page, 134 us.
+// Shares of few tiles are bound by their ends, the launch, the queries' and the first keys' arrival and the last tile's sums, some
+// 20 us: 16 grouped requests of some 10000 rows, 4 bands of 128, 8 tiles a pair, 45 us, 0.55 of the copy rate, DRAM 44% busy and
+// the exponentials' unit 6%; of 64000 rows 173 us (0.89), of 128000 327 (0.95), so more rows cost what a copy of them does.
+// Lazy pools turn every band again: 64 decodes over some 5000 rows, one a page, 129 us.  Of 100 us over 64 x 3800 rows 10 are the turns
+// (90 with counts of 0), and eager rows take 65: a tile's band comes by itself there, in a step of its own, and the warps that load wait
+// for it.
 //
 // Roles in each CTA: warps 0-3 sum, warp 4 issues the products (in the first CTA alone), warps 5-12 load, 16 rows of a plane
 // each.
@@ -129,7 +133,7 @@ __device__ __forceinline__ Steps make_steps(const WeighArgs& a, const WeighMaps&
 // A buffer is of several accumulators, each for a part of the key's chunks: an accumulator's error grows with its steps and
 // with what it has come to, most of it a loss that exponent_scale makes up for.  Before that the 36 steps of an MLA key in one took
 // the weights of one token 1.2e-6 off 64 bits (2-norm, relative), next to 3 to 6e-7 in three; now three are 1.2e-7 off.  The time is
-// the same: 16 decodes of 128 heads over some 24000 rows 104 us with one and with two.  A band alone, of at most 16
+// the same: 16 decodes of 128 heads over some 30000 rows 104 us with one and with two.  A band alone, of at most 16
 // steps, has one.
 struct Buffers {
     int cols, chunks, parts, count;  // chunks: of a part
@@ -241,8 +245,8 @@ struct Loader {
             // Groups that are arrived for: all at the end, the oldest of `most` and those whose stages are next.  A product
             // waits for a tile's turned bands, the last of its planes, so these go on as soon as they can: where TMA brings
             // the other planes when the next tile's first are asked for (after two of them 128 us, after three 139, here 121:
-            // 16 decodes of 16 heads over some 24000 rows), else one group after another while the next stage is not free
-            // (64 decodes over some 4000 rows, one a page, 148 us without, here 129; rows that are not turned 84 without, 88
+            // 16 decodes of 16 heads over some 30000 rows), else one group after another while the next stage is not free
+            // (64 decodes over some 5000 rows, one a page, 148 us without, here 129; rows that are not turned 84 without, 88
             // with it).
             const uint32_t empty = smem_addr(&m->empty[ring.stage]);
             while (landing > 0 && (key0 >= end || landing == most || uses - oldest_use >= s.stages ||

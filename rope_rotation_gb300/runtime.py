@@ -171,7 +171,8 @@ class PagedCache:
         return out
 
     def evict(self, keeps, kept, weights=None, stream=None) -> None:
-        """Drop the rows that the lists `kept` of select_rows(), or of another policy, do not name; weights move along."""
+        """Drop the rows that the lists `kept` of select_rows(), or of another policy, do not name; weights move along
+        (an array of weights for each layer: the others are the caller's to move, as all are after a splice)."""
         if weights is not None:
             self._on_device(weights, "weights")
         leyline.leyline_evict(self.pool, self.tables, keeps, self._on_device(kept, "kept"), weights, self._stream(stream))
@@ -221,9 +222,9 @@ class PagedCache:
 class Batch:
     """New tokens of a step: rows appended to the cache, queries turned, attention over the cache.
 
-    plan() takes one chunk of new tokens per request, once a step; append(), rotate() and
-    attention() then serve each layer, on tensors whose first axis is the plan's tokens, chunk after
-    chunk.  The last three can be captured into a CUDA graph and replayed after each new plan,
+    plan() takes chunks of new tokens, once a step; append(), rotate(), attention() and
+    attention_weights() then serve each layer, on tensors whose first axis is the plan's tokens, chunk after
+    chunk.  The last four can be captured into a CUDA graph and replayed after each new plan,
     on tensors with room for max_tokens.  Outputs that a call makes belong to the stream it runs on.
     There is no backward pass: tensors that require a gradient are refused outside torch.no_grad().
     """
@@ -321,7 +322,8 @@ class Batch:
     def attention_weights(self, layer: int, q_latent, q_rope, lse, scale: float, weights, decay: float = 1.0,
                           prefix: bool = False, stream=None):
         """Add to weights [requests][rows] (fp32) what the queries gave to each row they attend to, w = decay * w + sum of
-        exp(score - lse) over tokens and heads, with the lse that attention() returned for the same arguments."""
+        exp(score - lse) over tokens and heads, with the lse that attention() returned for the same arguments.  decay is of a
+        call: where one array serves all layers, give it in one layer of a step."""
         torch = self.cache.torch
         tokens = self._room(stream)
         if (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < tokens
