@@ -544,7 +544,8 @@ int leyline_attention(leyline_batch_t* batch, int32_t layer, const leyline_heads
  *     leyline_select_rows(pool, &bt, &weights, keeps, n, kept, ...);        now and then: the rows to keep
  *     leyline_evict(pool, &bt, keeps, n, kept, ..., &weights, stream);      drops the others
  *
- * Lists of rows and weights stay on the device; a list may also come from another policy.  New
+ * The three refuse requests of more than 2^31 - 2^16 rows (INVALID_ARG; a replayed weighing leaves their weights as they were,
+ * status word).  Lists of rows and weights stay on the device; a list may also come from another policy.  New
  * rows after an eviction are encoded at the request's next position, not at their row:
  * leyline_chunk_t.rope_start.
  *

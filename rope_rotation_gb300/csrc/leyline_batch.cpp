@@ -588,6 +588,7 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
                  : (b->weigh_req >= weights->num_reqs || b->weigh_rows > weights->rows))
         return bad(captured ? "under capture weights need room for every request and row of the block table"
                             : "weights do not hold every row of the plan's requests");
+    if (!captured && b->weigh_rows > kMostRows) return bad("a request of more than 2^31 - 2^16 rows");
     rc = check_heads(q_rope, p->device, "q_rope", &a.q_rope);
     if (rc == LEYLINE_OK && mla) rc = check_heads(q_latent, p->device, "q_latent", &a.q_latent);
     void *lse_alias = nullptr, *weights_alias = nullptr;
@@ -606,7 +607,7 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.lse = static_cast<const float*>(lse_alias);
     a.weights = static_cast<float*>(weights_alias);
     a.req_stride = weights->req_stride;
-    a.rows = weights->rows;
+    a.rows = std::min(weights->rows, kMostRows);
     a.num_reqs = weights->num_reqs;
     a.scale = scale;
     a.decay = decay;

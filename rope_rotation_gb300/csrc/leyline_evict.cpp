@@ -34,8 +34,9 @@ int check_keeps(const Geometry& g, const leyline_block_table_t& bt, const leylin
             return bad(msg);
         }
         const int64_t len = bt.seq_lens_host[e.req];
-        if (len < 0 || len > (int64_t)bt.max_blocks * g.block_size || len > INT32_MAX)
+        if (len < 0 || len > (int64_t)bt.max_blocks * g.block_size)
             return bad("seq_lens_host entry outside [0, max_blocks * block_size]");
+        if (len > kMostRows) return bad("a request of more than 2^31 - 2^16 rows");
         if (e.n_keep < 0 || e.n_keep > len) {
             snprintf(msg, sizeof msg, "entry %d: n_keep %d is not within the request's %lld rows", k, e.n_keep, (long long)len);
             return bad(msg);

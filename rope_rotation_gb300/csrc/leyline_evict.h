@@ -12,6 +12,10 @@ namespace leyline {
 // weights do not hold.
 enum : int32_t { ST_BAD_ROW = 64 };
 
+// Rows of a request that weighing, selecting and evicting take: their kernels count past its end in 32 bits (by 512 rows, 2^14
+// and some 2000).
+constexpr int64_t kMostRows = INT32_MAX - 65535;
+
 // One request of a launch.
 struct EvictReq {
     int32_t req;      // table row

@@ -28,6 +28,7 @@ std::map<uintptr_t, size_t> device_memory;
 bool legacy_pending = false;  // work of the legacy stream may still run
 int unordered = 0;            // kernels launched on another stream meanwhile
 int64_t copied_vecs = 0;      // of the last plan
+int64_t weighed_rows = 0;     // that the last weighing's kernels take of a request
 int copies_in = 0, selects = 0, evictions = 0, weighings = 0;
 std::vector<ListState> seen_state;  // of the last eviction, both arrays
 
@@ -198,7 +199,7 @@ int launch_attention_pair(const AttnArgs&, const TileMaps&, int, void* s) { retu
 int launch_join(const AttnArgs&, int, int, bool, void* s) { return launched(s); }
 int weigh_tile_prepare(const Geometry&, const void*, WeighMaps*) { return 0; }
 int weigh_pair_prepare(const Geometry&) { return 0; }
-int launch_weigh(const WeighArgs&, int, void* s) { return ++weighings, launched(s); }
+int launch_weigh(const WeighArgs& a, int, void* s) { return ++weighings, weighed_rows = a.rows, launched(s); }
 int launch_weigh_tile(const WeighArgs&, const WeighMaps&, int, void* s) { return ++weighings, launched(s); }
 int launch_weigh_pair(const WeighArgs&, const WeighMaps&, int64_t, int, int, void* s) { return ++weighings, launched(s); }
 int launch_select(const SelectArgs&, const EvictSet&, void* s) { return ++selects, launched(s); }
@@ -350,6 +351,40 @@ void plan_copies()
     check(16 * (vecs[1] - vecs[0]) <= (int64_t)sizeof(ChunkDev) * 4094 + 64, "a plan copies the work of its own requests");
 }
 
+void lengths()
+{
+    // rows are counted past a request's end in 32 bits: by 2^14 where they are selected, by 512 where they are weighed
+    const int64_t most = (int64_t)INT32_MAX - 65535;
+    Fixture f;
+    f.bt.max_blocks = 1 << 29;  // of 4 rows; nothing reads a table or weights here
+    float* weights = reinterpret_cast<float*>((uintptr_t)1 << 40);
+    device_memory[(uintptr_t)weights] = (size_t)1 << 34;
+    for (int64_t len : {most, most + 1, (int64_t)INT32_MAX - 64, (int64_t)INT32_MAX}) {
+        const bool taken = len <= most;
+        const int before = selects + evictions;
+        f.lens[0] = len;
+        f.w = leyline_row_weights_t{weights, INT32_MAX, INT32_MAX, 1};
+        const leyline_keep_t keep{0, 7, 1, 1};
+        check((leyline_select_rows(f.pool, &f.bt, &f.w, &keep, 1, f.kept, 40, f.stream) == LEYLINE_OK) == taken, "selecting");
+        if (!taken)
+            check(leyline_evict(f.pool, &f.bt, &keep, 1, f.kept, 40, &f.w, f.stream) == LEYLINE_ERR_INVALID_ARG, "evicting");
+        check(selects + evictions == before + taken && f.lens[0] == len, "nothing of a refused call is enqueued");
+    }
+    leyline_batch_t* b = nullptr;
+    check(leyline_batch_create(f.pool, 2, 8, 4, &b) == LEYLINE_OK, "creating the batch");
+    for (int64_t end : {most, most + 1, (int64_t)INT32_MAX - 64}) {
+        const int before = weighings;
+        f.lens[0] = end;
+        const leyline_chunk_t chunk{0, 1, end - 1, end - 1};
+        check(leyline_batch_plan(b, &f.bt, &chunk, 1, f.stream) == LEYLINE_OK, "a plan of the last row");
+        const leyline_heads_t q{f.kv, 4 * 512, 512};
+        const bool ok = leyline_attention_weights(b, 0, &q, &q, (float*)f.table, &f.w, 1.f, 1.f, 0, f.stream) == LEYLINE_OK;
+        check(ok == (end <= most) && weighings == before + ok, "weighing");
+        if (ok) check(weighed_rows <= most, "replayed plans of longer requests are left out");
+    }
+    check(leyline_batch_destroy(b) == LEYLINE_OK, "destroying the batch");
+}
+
 }  // namespace
 
 int main(int argc, char** argv)
@@ -361,6 +396,7 @@ int main(int argc, char** argv)
     else if (name == "empty_lists") empty_lists();
     else if (name == "idle_step") idle_step();
     else if (name == "plan_copies") plan_copies();
+    else if (name == "lengths") lengths();
     else check(false, "a case's name");
     std::printf("%s: %d failed checks\n", name.c_str(), failures);
     return failures == 0 ? 0 : 1;

@@ -34,7 +34,7 @@ def run(exe, case):
     assert " 0 failed checks" in done.stdout
 
 
-CASES = ["first_eviction", "freed_pages", "status_word", "empty_lists", "idle_step", "plan_copies"]
+CASES = ["first_eviction", "freed_pages", "status_word", "empty_lists", "idle_step", "plan_copies", "lengths"]
 
 
 @pytest.mark.parametrize("case", CASES)
