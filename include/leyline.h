@@ -410,8 +410,8 @@ int32_t* leyline_pending_ptr(leyline_pool_t* pool);
  * checkpoint made before it, or one of its pages is freed.  After all but the last, calls that are not
  * captured are refused (INVALID_ARG) until the next plan; replays and freed pages the
  * library does not see.
- * rope_start is the rotary position of the chunk's first token: start, unless
- * EVICT directives left the request's survivors at other positions.  Frequencies are
+ * rope_start is the rotary position of the chunk's first token: start, unless EVICT
+ * directives or leyline_evict left the request's survivors at other positions.  Frequencies are
  * the pool's, rope_theta^(-2j/d): the turns of this library, a splice's like those of
  * leyline_append and leyline_rotate, are not for a model that scales them otherwise.
  *

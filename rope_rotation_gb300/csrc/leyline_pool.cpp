@@ -773,8 +773,8 @@ int leyline_pool_rollback(leyline_pool_t* p, int32_t flags, void* stream_v)
                          "pages returned since the checkpoint have been taken again: their rows may be overwritten");
     if (p->ckpt_turned && !(flags & LEYLINE_ROLLBACK_ACCEPT_TURNED))
         return set_error(LEYLINE_ERR_INVALID_ARG,
-                         "stored rope bands were turned in place since the checkpoint (re-index splice of an eager "
-                         "pool, or materialize); a rollback would not undo that");
+                         "stored rows were changed in place since the checkpoint (re-index splice of an eager pool, "
+                         "materialize, a plan over existing rows, or an eviction); a rollback would not undo that");
     cudaStream_t stream = (cudaStream_t)stream_v;
     DeviceGuard guard(p->device);
     if (!guard.ok) return set_error(LEYLINE_ERR_CUDA, "cannot select the pool's device");
