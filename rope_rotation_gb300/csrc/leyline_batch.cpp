@@ -610,6 +610,15 @@ int leyline_attention_weights(leyline_batch_t* b, int32_t layer, const leyline_h
     a.rows = std::min(weights->rows, kMostRows);
     a.num_reqs = weights->num_reqs;
     a.scale = scale;
+    if (b->weigh_shape.tiles) {
+        const WeighShape& w = b->weigh_shape;
+        const int32_t key = w.q_chunks + (w.lazy ? w.band_chunks : 0);  // chunks, the band's low part with them
+        for (int32_t cols : {64, 128}) {
+            const int32_t parts = (int32_t)ceil_div(key, weigh_part(mla, key, cols));
+            a.scale2[cols > 64] = exponent_scale(scale, 4 * key / parts);
+        }
+        a.scale2[2] = exponent_scale(scale, 4 * key);
+    }
     a.decay = decay;
     a.layer = layer;
     a.prefix = flags & LEYLINE_ATTENTION_PREFIX;

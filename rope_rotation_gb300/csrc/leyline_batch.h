@@ -195,6 +195,26 @@ constexpr int64_t stay_bytes(int64_t bands, int64_t q_chunks, int64_t rows)
 {
     return bands * q_chunks * rows / 2 * 128 + (bands * rows * 8 + 1023) / 1024 * 1024;
 }
+// Chunks of a key that an accumulator adds up, where queries stay (see Buffers in leyline_weigh_tile.cu).
+constexpr int32_t weigh_part(bool mla, int32_t chunks, int32_t cols)
+{
+    const int32_t most = !mla ? 1 : cols > 64 ? 2 : 4;
+    return (chunks + most - 1) / most;
+}
+// scale * log2 e, with what a score has lost in an accumulator of `steps` steps of 16 columns made up for.  The matrix unit cuts
+// off what an accumulator has no bits for, toward zero (Fasi, Higham, Mikaitis and Pranesh, "Numerical behavior of NVIDIA tensor
+// cores", 2021): half of its last bit a step on average, 0.72 * 2^-24 of what it holds by then, and a sum that grows evenly to
+// x holds x / 2 on average: 2.1e-8 x a step.  Measured over scores of either sign and many sizes (means by size): 5.3 to 7.3e-7 x
+// for 36 steps, 2.4 to 2.9e-7 for 16, 1.5 to 2.1e-7 for 12, 1.1 to 1.3e-7 for 8.  1.75e-8 for each step but the first leaves 1.2e-7
+// x of it at most; of a query that equals the key, whose products all add up, 3e-7.  A sum that comes all at once in the
+// last steps loses next to nothing and is put off by as much.  Weights of a prompt's last window, 64 tokens of 16 heads over
+// 32768 rows, were 1.6e-6 off 64 bits without it (2-norm, relative) and are 5e-7 with it.
+// (On the host, in fp64 and rounded once: on the device it cost the loading warps registers, lazy decodes 129 -> 132 us.)
+inline float exponent_scale(float scale, int32_t steps)
+{
+    return (float)((double)scale * kLog2e * (1.0 + 1.75e-8 * (steps - 1)));
+}
+
 // Fills in the requests' work and the header's part of it, the requests whose queries stay first; at most 2 * kWeighItems *
 // pairs items have sums of their own.
 void weigh_work(const WeighShape& w, const std::vector<ChunkDev>& chunks, std::vector<WeighReq>* reqs, BatchHeader* header);
@@ -291,6 +311,7 @@ struct WeighArgs {
     int64_t rows;          // of a request, and requests, that the weights hold
     int32_t num_reqs;
     float scale;
+    float scale2[3];       // exponent_scale of it: queries stay, up to 64 columns and more; queries pass (tensor cores)
     float decay;
     int32_t layer;
     int32_t prefix;

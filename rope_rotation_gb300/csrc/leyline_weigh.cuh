@@ -374,19 +374,6 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t keys, int pitch, ui
 }
 
 // ----------------------------------------------------------------- epilogue --
-// scale * log2 e, with what a score has lost in an accumulator of `steps` steps of 16 columns made up for.  The matrix unit cuts
-// off what an accumulator has no bits for, toward zero (Fasi, Higham, Mikaitis and Pranesh, "Numerical behavior of NVIDIA tensor
-// cores", 2021): half of its last bit a step on average, 0.72 * 2^-24 of what it holds by then, and a sum that grows evenly to
-// x holds x / 2 on average: 2.1e-8 x a step.  Measured over scores of either sign and many sizes (means by size): 5.3 to 7.3e-7 x
-// for 36 steps, 2.4 to 2.9e-7 for 16, 1.5 to 2.1e-7 for 12, 1.1 to 1.3e-7 for 8.  1.75e-8 for each step but the first leaves 1.2e-7
-// x of it at most; of a query that equals the key, whose products all add up, 3e-7.  A sum that comes all at once in the
-// last steps loses next to nothing and is put off by as much.  Weights of a prompt's last window, 64 tokens of 16 heads over
-// 32768 rows, were 1.6e-6 off 64 bits without it (2-norm, relative) and are 5e-7 with it.
-__device__ __forceinline__ float exponent_scale(float scale, int steps)
-{
-    return (float)((double)scale * kLog2e * (1.0 + 1.75e-8 * (steps - 1)));  // (rounded once)
-}
-
 // Lazy pools: theta_j of a band's pairs as a part of a whole turn, to shared memory, by all threads.
 __device__ __forceinline__ void load_turns(const WeighArgs& a, int pairs, double* turns)
 {

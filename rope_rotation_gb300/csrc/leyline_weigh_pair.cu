@@ -297,7 +297,6 @@ struct Summer {
     Misc* m;
     uint32_t tmem, rank;
     int warp, lane;
-    float scale2;   // of the exponents
     int index = 0;  // of the unit to be summed
     bool waiting = false, cut = false;
     int n = 0, cols = 0, key0 = 0, keys = 0;
@@ -336,7 +335,7 @@ struct Summer {
         mbar_wait_cluster(smem_addr(&m->s_full[buf]), (index >> 1) & 1, &m->quit, a.status);
         tcgen05_after_sync();
         if (32 * quarter < keys && cols > 0)
-            sum += sum_columns(tmem + buf * kCols + ((uint32_t)(32 * quarter) << 16) + from, padded(cols), cols, scale2,
+            sum += sum_columns(tmem + buf * kCols + ((uint32_t)(32 * quarter) << 16) + from, padded(cols), cols, a.scale2[2],
                                m->neg[buf] + from, m->limit[buf] + from, key0 + 32 * quarter + lane, masked);
         tcgen05_before_sync();
         __syncwarp();
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_pair_kernel(const __grid_co
     s.stay_bytes = s.chunks * kChunkBytes;
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / kChunkBytes);
     if (warp < kMmaWarp) {
-        Summer role{a, s, m, tmem, rank, warp, lane, exponent_scale(a.scale, 4 * s.chunks)};
+        Summer role{a, s, m, tmem, rank, warp, lane};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {

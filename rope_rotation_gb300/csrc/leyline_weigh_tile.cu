@@ -142,8 +142,7 @@ struct Buffers {
 
     __device__ __forceinline__ Buffers(int c, const Shape& s) : cols(c)
     {
-        const int most = s.latent == 0 ? 1 : c > 64 ? 2 : 4;
-        chunks = (s.chunks + most - 1) / most;
+        chunks = weigh_part(s.latent > 0, s.chunks, c);
         parts = (s.chunks + chunks - 1) / chunks;
         count = min(kBuffers, (int)kTmemCols / (c * parts));
     }
@@ -393,7 +392,6 @@ struct Summer {
     Buffers buf;
     uint32_t rank;
     int warp, lane;
-    float scale2;  // of the exponents
     int open = 0;  // rows below it are attended to by every column
     float sum = 0.f;
     int page = -1;  // of this thread's row of the tile, and its weight before
@@ -438,7 +436,7 @@ struct Summer {
             const uint32_t at = tmem + buf.column() + ((uint32_t)(32 * warp) << 16);
             const int n = padded(u.cols), key = t.key0 + 32 * warp + lane;
             const bool masked = t.key0 + t.keys > open;
-            const float* l = neg + u.band * cols;
+            const float scale2 = cols > 64 ? a.scale2[1] : a.scale2[0], *l = neg + u.band * cols;
             const int* end = limit + u.band * cols;
             sum += buf.parts == 4   ? sum_columns<4>(at, n, u.cols, scale2, l, end, key, masked, cols)
                    : buf.parts == 3 ? sum_columns<3>(at, n, u.cols, scale2, l, end, key, masked, cols)
@@ -502,9 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tile_kernel(const __grid_co
     s.stages = min(kMaxStages, (kWeighSmem - s.stay_bytes) / t.stage_bytes);
     if (warp < kMmaWarp) {
         float* columns = reinterpret_cast<float*>(base + s.bands * s.q_chunks * q_rows * 128);
-        const Buffers buffers(cols, s);
-        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, buffers,
-                    rank, warp, lane, exponent_scale(a.scale, 4 * s.chunks / buffers.parts)};
+        Summer role{a, s, m, tmem, columns, reinterpret_cast<int*>(columns + s.bands * cols), cols, Buffers(cols, s),
+                    rank, warp, lane};
         walk(a, s, rank, role);
         tcgen05_before_sync();
     } else if (warp == kMmaWarp) {
