@@ -576,7 +576,7 @@ typedef struct {
  * steps of 64) the adding up cuts off instead of rounding; that is made up for as it is on average, which leaves a score x off
  * by some 1e-7 |x|, by 6e-7 |x| if its sum comes all at once.  Exponentials are approximations to 2^-22.  The turned band
  * of a lazy pool is the sum of two bf16 values there (2^-17 of its pair), turned by cos and sin to 2^-22.  Measured, the
- * weights of a request are within 7e-7 of 64 bits (2-norm, relative; 2.1e-6 for grouped rows of lazy pools).
+ * weights of a request are within 8e-7 of 64 bits (2-norm, relative; 2.1e-6 for grouped rows of lazy pools).
  * Enqueues a kernel for the requests whose query rows of a band fit one tile of 128, one for the
  * others, and one that joins partial sums, as far as the plan has them; under capture all three.
  * Can be captured, like leyline_attention, with weights that hold every request and row of the
